@@ -156,6 +156,8 @@ __global__ void __launch_bounds__(kThreads) gate_bwd_kernel(int H, int L, int D,
       if (e < D * DK) {
         const int d = e / DK, k = e % DK;
         float s = dwa[m];
+        // fully unrolled, the kMaxAcc copies of this loop take ptxas minutes
+#pragma unroll 8
         for (int t = 0; t < kTok; ++t) s = fmaf(xs[t * (D + 1) + d], dzs[t * DK + k], s);
         dwa[m] = s;
       }
