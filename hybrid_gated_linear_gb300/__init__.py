@@ -28,12 +28,25 @@ __all__ = [
     "lizard_feature_map_fwd", "lizard_feature_map_bwd", "lizard_feature_map_workspace_bytes",
     "lizard_attn_fwd_fmap", "lizard_selftest_wait_timeout", "lizard_gate_dims",
     "lizard_gate_fwd", "lizard_gate_bwd", "lizard_gate_workspace_bytes", "lizard_gla_std_fwd",
-    "lizard_gla_std_workspace_bytes", "LIZARD_F32", "LIZARD_BF16", "EXPORTED_SYMBOLS",
+    "lizard_gla_std_workspace_bytes",
+    "lizard_rope_spec", "lizard_rope", "lizard_rope_dims", "lizard_rope_table", "lizard_rope_fwd",
+    "lizard_rope_bwd", "LIZARD_ROPE_HALF", "LIZARD_ROPE_INTERLEAVED", "LIZARD_ROPE_PLAIN",
+    "LIZARD_ROPE_LINEAR", "LIZARD_ROPE_PARTS", "lizard_strides", "lizard_cache", "lizard_cache_io",
+    "lizard_cache_workspace_bytes", "lizard_cache_write", "lizard_cache_read",
+    "lizard_cache_attn_dims", "lizard_cache_attn_workspace_bytes", "lizard_cache_attn",
+    "LIZARD_KV_E4M3", "LIZARD_KV_I8", "LIZARD_F32", "LIZARD_BF16", "EXPORTED_SYMBOLS",
 ]
 
 LIZARD_F32 = 0
 LIZARD_BF16 = 1
 LIZARD_NOALLOC_MAX_SEQUENCES = 16384
+LIZARD_ROPE_HALF = 0
+LIZARD_ROPE_INTERLEAVED = 1
+LIZARD_ROPE_PLAIN = 0
+LIZARD_ROPE_LINEAR = 1
+LIZARD_ROPE_PARTS = 2
+LIZARD_KV_E4M3 = 0
+LIZARD_KV_I8 = 1
 
 EXPORTED_SYMBOLS = (
     "lizard_attn_fwd", "lizard_attn_bwd", "lizard_decode_step", "lizard_chunk_cumsum",
@@ -45,6 +58,9 @@ EXPORTED_SYMBOLS = (
     "lizard_feature_map_bwd", "lizard_feature_map_workspace_bytes", "lizard_attn_fwd_fmap",
     "lizard_selftest_wait_timeout", "lizard_gate_fwd", "lizard_gate_bwd",
     "lizard_gate_workspace_bytes", "lizard_gla_std_fwd", "lizard_gla_std_workspace_bytes",
+    "lizard_rope_table", "lizard_rope_fwd", "lizard_rope_bwd", "lizard_cache_workspace_bytes",
+    "lizard_cache_write", "lizard_cache_read", "lizard_cache_attn_workspace_bytes",
+    "lizard_cache_attn",
 )
 
 STATUS_NAMES = {0: "LIZARD_OK", 1: "LIZARD_ERR_INVALID_ARG", 2: "LIZARD_ERR_UNSUPPORTED",
@@ -80,6 +96,71 @@ class lizard_gate_dims(ctypes.Structure):
 class lizard_fmap_dims(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int32), ("H", ctypes.c_int32), ("L", ctypes.c_int32),
                 ("D", ctypes.c_int32), ("F", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class lizard_strides(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int64), ("h", ctypes.c_int64), ("t", ctypes.c_int64)]
+
+
+class lizard_rope_spec(ctypes.Structure):
+    _fields_ = [("rot", ctypes.c_int32), ("scaling", ctypes.c_int32), ("base", ctypes.c_double),
+                ("factor", ctypes.c_double), ("low", ctypes.c_double), ("high", ctypes.c_double),
+                ("original", ctypes.c_int64)]
+
+
+class lizard_rope(ctypes.Structure):
+    """A rotary table on the device; keeps its tensor alive."""
+    _fields_ = [("turns", ctypes.c_void_p), ("rot", ctypes.c_int32), ("layout", ctypes.c_int32),
+                ("attn_factor", ctypes.c_float)]
+
+    def __init__(self, turns, rot: int, layout: int, attn_factor: float = 1.0):
+        if turns.element_size() != 8 or turns.numel() != rot // 2 or not turns.is_contiguous():
+            raise ValueError("turns must be the rot/2 words of lizard_rope_table")
+        super().__init__(turns.data_ptr(), rot, layout, attn_factor)
+        self._keep = turns
+
+
+class lizard_rope_dims(ctypes.Structure):
+    _fields_ = [("N", ctypes.c_int32), ("H", ctypes.c_int32), ("Hk", ctypes.c_int32),
+                ("T", ctypes.c_int32), ("d", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class lizard_cache(ctypes.Structure):
+    """The pools and the page table of an 8-bit cache; keeps their tensors alive.
+    k_codes, v_codes [pages,Hk,page_tokens,d] of one byte per element, k_scale, v_scale
+    [pages,Hk] fp32, table [N,max_pages] int32, all contiguous on one device."""
+    _fields_ = [("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("table", ctypes.c_void_p), ("N", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("pages", ctypes.c_int32), ("Hk", ctypes.c_int32), ("page_tokens", ctypes.c_int32),
+                ("d", ctypes.c_int32), ("format", ctypes.c_int32)]
+
+    def __init__(self, k_codes, v_codes, k_scale, v_scale, table, format: int):
+        import torch
+        pages, hk, page_tokens, d = k_codes.shape
+        if v_codes.shape != k_codes.shape or k_codes.element_size() != 1 or v_codes.element_size() != 1:
+            raise ValueError("k_codes and v_codes must be [pages, Hk, page_tokens, d] bytes")
+        for s in (k_scale, v_scale):
+            if tuple(s.shape) != (pages, hk) or s.dtype != torch.float32:
+                raise ValueError("k_scale and v_scale must be [pages, Hk] float32")
+        if table.dim() != 2 or table.dtype != torch.int32:
+            raise ValueError("table must be [N, max_pages] int32")
+        keep = (k_codes, v_codes, k_scale, v_scale, table)
+        if not all(t.is_contiguous() and t.device == table.device for t in keep):
+            raise ValueError("the cache's tensors must be contiguous and on one device")
+        super().__init__(*(t.data_ptr() for t in keep), table.shape[0], table.shape[1], pages, hk,
+                         page_tokens, d, format)
+        self._keep = keep
+
+
+class lizard_cache_io(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class lizard_cache_attn_dims(ctypes.Structure):
+    _fields_ = [("H", ctypes.c_int32), ("T", ctypes.c_int32), ("M", ctypes.c_int32),
+                ("W", ctypes.c_int32), ("dtype", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("alpha", ctypes.c_float)]
 
 
 _lock = threading.Lock()
@@ -134,6 +215,14 @@ def library():
                 "lizard_gate_bwd": (I32, [GDP, P, P, P, P, P, P, SZ, P]),
                 "lizard_gla_std_workspace_bytes": (SZ, [DP]),
                 "lizard_gla_std_fwd": (I32, [DP] + [P] * 8 + [SZ, P]),
+                "lizard_rope_table": (I32, [P, P]),
+                "lizard_rope_fwd": (I32, [P] * 12),
+                "lizard_rope_bwd": (I32, [P] * 12),
+                "lizard_cache_workspace_bytes": (SZ, []),
+                "lizard_cache_write": (I32, [P] * 10 + [SZ, P]),
+                "lizard_cache_read": (I32, [P] * 9 + [SZ, P]),
+                "lizard_cache_attn_workspace_bytes": (SZ, [P, P]),
+                "lizard_cache_attn": (I32, [P] * 15 + [SZ, P]),
             }
             for name, (res, args) in sig.items():
                 fn = getattr(lib, name)
@@ -397,3 +486,115 @@ def lizard_attn_fwd_fmap(dims: lizard_dims, x_q, x_k, w_q, w_k, v, log_gamma, q,
         _ptr(q), _ptr(k), _ptr(meta_k), _ptr(meta_v), int(W), float(alpha), _ptr(y), _ptr(h0),
         _ptr(h_final), _ptr(workspace), _ws_bytes(workspace), _stream(stream))
     _check(st, "lizard_attn_fwd_fmap")
+
+
+# ------------------------------------------------------------------------------------
+# rotary positions, the 8-bit paged cache and the attention over it
+# ------------------------------------------------------------------------------------
+def _rows(t, shape, dtype: int):
+    """Pointer and strides (None when contiguous) of a [N,H,T,d] device tensor."""
+    if t is None:
+        return None, None
+    if t.shape != shape or _dtype_code(t) != dtype or not t.is_cuda:
+        raise ValueError(f"expected a device tensor of shape {shape} and element type {dtype}, "
+                         f"got {tuple(t.shape)} {t.dtype} on {t.device}")
+    if t.is_contiguous():
+        return t.data_ptr(), None
+    s = t.stride()
+    if s[3] != 1:
+        raise ValueError("the channels of a row must be contiguous")
+    return t.data_ptr(), ctypes.byref(lizard_strides(s[0], s[1], s[2]))
+
+
+def _ints(t, shape, size: int):
+    """Pointer of a contiguous device tensor of integers of `size` bytes (None -> NULL)."""
+    if t is None:
+        return None
+    if (t.shape != shape or t.element_size() != size or t.is_floating_point() or not t.is_cuda
+            or not t.is_contiguous()):
+        raise ValueError(f"expected a contiguous int{8 * size} device tensor of shape {shape}, got "
+                         f"{tuple(t.shape)} {t.dtype} on {t.device}")
+    return t.data_ptr()
+
+
+def _ref(x):
+    return None if x is None else ctypes.byref(x)
+
+
+def lizard_rope_table(spec: lizard_rope_spec):
+    """The rotary table of ``spec`` as an int64 CPU tensor of rot/2 words (64-bit fixed-point
+    turns per token); move it to the device and pass it to :class:`lizard_rope`."""
+    import torch
+    table = torch.zeros(max(spec.rot // 2, 1), dtype=torch.int64)
+    _check(library().lizard_rope_table(ctypes.byref(spec), table.data_ptr()), "lizard_rope_table")
+    return table
+
+
+def _rope_call(name, dims, rope, a_q, a_k, positions, b_q, b_k, stream):
+    sq = (dims.N, dims.H, dims.T, dims.d)
+    sk = (dims.N, dims.Hk, dims.T, dims.d)
+    aq, bq = _rows(a_q, sq, dims.dtype), _rows(b_q, sq, dims.dtype)
+    ak, bk = _rows(a_k, sk, dims.dtype), _rows(b_k, sk, dims.dtype)
+    st = getattr(library(), name)(_ref(dims), _ref(rope), *aq, *ak,
+                                  _ints(positions, (dims.N, dims.T), 8), *bq, *bk, _stream(stream))
+    _check(st, name)
+
+
+def lizard_rope_fwd(dims: lizard_rope_dims, rope: lizard_rope, x_q, x_k, positions, y_q, y_k,
+                    stream=None):
+    """Rotates queries [N,H,T,d] and keys [N,Hk,T,d] (or None) into y_q, y_k (which may be
+    the inputs); the tensors may be strided."""
+    _rope_call("lizard_rope_fwd", dims, rope, x_q, x_k, positions, y_q, y_k, stream)
+
+
+def lizard_rope_bwd(dims: lizard_rope_dims, rope: lizard_rope, dy_q, dy_k, positions, dx_q, dx_k,
+                    stream=None):
+    """Gradients of lizard_rope_fwd's inputs from those of its outputs."""
+    _rope_call("lizard_rope_bwd", dims, rope, dy_q, dy_k, positions, dx_q, dx_k, stream)
+
+
+def lizard_cache_workspace_bytes() -> int:
+    return library().lizard_cache_workspace_bytes()
+
+
+def lizard_cache_write(cache: lizard_cache, io: lizard_cache_io, k, v, rope, pos, count, workspace,
+                       stream=None):
+    """Quantises tokens k, v [N,Hk,T,d] (may be strided) into positions pos[n] + j, j < count[n]
+    (None: T) of the cache, the keys rotated first if ``rope`` is given."""
+    shape = (cache.N, cache.Hk, io.T, cache.d)
+    st = library().lizard_cache_write(
+        _ref(cache), _ref(io), *_rows(k, shape, io.dtype), *_rows(v, shape, io.dtype), _ref(rope),
+        _ints(pos, (cache.N,), 8), _ints(count, (cache.N,), 4), _ptr(workspace),
+        _ws_bytes(workspace), _stream(stream))
+    _check(st, "lizard_cache_write")
+
+
+def lizard_cache_read(cache: lizard_cache, io: lizard_cache_io, pos, count, k, v, workspace,
+                      stream=None):
+    """Values of positions pos[n] + j, j < count[n] (None: T) into k, v [N,Hk,T,d]; other rows 0."""
+    shape = (cache.N, cache.Hk, io.T, cache.d)
+    st = library().lizard_cache_read(
+        _ref(cache), _ref(io), _ints(pos, (cache.N,), 8), _ints(count, (cache.N,), 4),
+        *_rows(k, shape, io.dtype), *_rows(v, shape, io.dtype), _ptr(workspace),
+        _ws_bytes(workspace), _stream(stream))
+    _check(st, "lizard_cache_read")
+
+
+def lizard_cache_attn_workspace_bytes(cache: lizard_cache, dims: lizard_cache_attn_dims) -> int:
+    return library().lizard_cache_attn_workspace_bytes(_ref(cache), _ref(dims))
+
+
+def lizard_cache_attn(cache: lizard_cache, dims: lizard_cache_attn_dims, q, rope, pos, count, first,
+                      meta_k, meta_v, y_add, y, workspace, stream=None):
+    """y = y_add + alpha * attention of q [N,H,T,d] over the cache and the meta tokens
+    (meta_k, meta_v [H,M,d]); q, y_add and y may be strided, y_add may be None or y."""
+    shape = (cache.N, dims.H, dims.T, cache.d)
+    for m in (meta_k, meta_v):
+        if m is not None and (m.shape != (dims.H, dims.M, cache.d) or _dtype_code(m) != dims.dtype):
+            raise ValueError("meta_k and meta_v must be [H, M, d] in the call's element type")
+    st = library().lizard_cache_attn(
+        _ref(cache), _ref(dims), *_rows(q, shape, dims.dtype), _ref(rope), _ints(pos, (cache.N,), 8),
+        _ints(count, (cache.N,), 4), _ints(first, (cache.N,), 8), _ptr(meta_k), _ptr(meta_v),
+        *_rows(y_add, shape, dims.dtype), *_rows(y, shape, dims.dtype), _ptr(workspace),
+        _ws_bytes(workspace), _stream(stream))
+    _check(st, "lizard_cache_attn")

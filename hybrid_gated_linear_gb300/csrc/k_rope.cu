@@ -1,0 +1,157 @@
+// k_rope.cu -- rotary positions of queries and keys in one launch, forward and adjoint.
+//
+// Pair i < rot/2 of every head of a token at position p is turned by p theta_i (include/
+// lizard.h states the layouts and scalings); the adjoint turns by -p theta_i, so both are
+// this kernel with the sign of the sine changed.  Two loads and two stores of a row per
+// head and a handful of FMAs per pair: memory bound, so each thread computes the cosines
+// and sines of its VP pairs once, in registers, and walks over the heads of its token with
+// 16-byte accesses.
+#include "kv_cache.cuh"
+
+namespace lz {
+namespace {
+
+constexpr int kThreads = 256;
+
+// VP consecutive elements (16 bytes when VP > 1).
+template <typename T, int VP>
+__device__ __forceinline__ void load_v(const T* p, float (&x)[VP]) {
+  if (VP == 1) {
+    x[0] = ld_f(p);
+  } else {
+#pragma unroll
+    for (int i = 0; i < VP; i += 4) {
+      const float4 v = ld4(p + i);
+      x[i] = v.x, x[i + 1] = v.y, x[i + 2] = v.z, x[i + 3] = v.w;
+    }
+  }
+}
+template <>
+__device__ __forceinline__ void load_v<bf16, 8>(const bf16* p, float (&x)[8]) {
+  const uint4 u = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+template <typename T, int VP>
+__device__ __forceinline__ void store_v(T* p, const float (&x)[VP]) {
+  if (VP == 1) {
+    *p = cvt_out<T>(x[0]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < VP; i += 4) st4(p + i, make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]));
+  }
+}
+template <>
+__device__ __forceinline__ void store_v<bf16, 8>(bf16* p, const float (&x)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&b);
+  }
+  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// One thread per (token, unit of 2 VP channels, group of `hpt` heads).  Units below
+// rot / (2 VP) are rotated (VP pairs); the others are copied.  VP = 16 bytes' worth of
+// elements where both halves of a unit are aligned, else 1.
+template <typename T, int VP>
+__global__ void __launch_bounds__(kThreads) rope_kernel(RopeCall a, int units, int hpt,
+                                                        int groups) {
+  const int64_t idx = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  const int64_t total = (int64_t)a.N * a.T * units * groups;
+  if (idx >= total) return;
+  const int u = (int)(idx % units);
+  const int64_t r = idx / units;
+  const int64_t nt = r % ((int64_t)a.N * a.T);
+  const int g = (int)(r / ((int64_t)a.N * a.T));
+  const int n = (int)(nt / a.T), t = (int)(nt % a.T);
+  const bool turned = u < a.rope.rot / (2 * VP);
+  const bool half = a.rope.layout == LIZARD_ROPE_HALF;
+  // channels of the unit's two vectors
+  const int c0 = turned && half ? u * VP : u * 2 * VP;
+  const int c1 = turned && half ? c0 + a.rope.rot / 2 : c0 + VP;
+  float co[VP], si[VP];
+  if (turned) {
+    const int64_t p = a.positions ? a.positions[nt] : t;
+#pragma unroll
+    for (int i = 0; i < VP; ++i) {
+      rope_angle(a.rope.turns[u * VP + i], p, a.rope.factor, co[i], si[i]);
+      si[i] *= a.sign;
+    }
+  }
+  const int h1 = min(a.H + a.Hk, (g + 1) * hpt);
+#pragma unroll 2
+  for (int h = g * hpt; h < h1; ++h) {
+    const bool q = h < a.H;
+    const int hh = q ? h : h - a.H;
+    const Strides& sx = q ? a.sxq : a.sxk;
+    const Strides& sy = q ? a.syq : a.syk;
+    const T* x = static_cast<const T*>(q ? a.xq : a.xk) + n * sx.n + hh * sx.h + t * sx.t;
+    T* y = static_cast<T*>(q ? a.yq : a.yk) + n * sy.n + hh * sy.h + t * sy.t;
+    float v[VP], w[VP];
+    load_v<T, VP>(x + c0, v);
+    load_v<T, VP>(x + c1, w);
+    if (turned && half) {
+#pragma unroll
+      for (int i = 0; i < VP; ++i) {
+        const float p = v[i], s = w[i];
+        v[i] = p * co[i] - s * si[i];
+        w[i] = s * co[i] + p * si[i];
+      }
+    } else if (turned) {
+      // neighbours are pairs: pairs 0..VP/2-1 lie in v, the others in w
+#pragma unroll
+      for (int i = 0; i < VP; ++i) {
+        if (VP == 1) {
+          const float p = v[0], s = w[0];
+          v[0] = p * co[0] - s * si[0];
+          w[0] = s * co[0] + p * si[0];
+        } else {
+          float* e = i < VP / 2 ? &v[2 * i] : &w[2 * i - VP];
+          const float p = e[0], s = e[VP > 1 ? 1 : 0];
+          e[0] = p * co[i] - s * si[i];
+          e[VP > 1 ? 1 : 0] = s * co[i] + p * si[i];
+        }
+      }
+    }
+    store_v<T, VP>(y + c0, v);
+    store_v<T, VP>(y + c1, w);
+  }
+}
+
+template <typename T, int VP>
+cudaError_t launch(const RopeCall& a, cudaStream_t s, int* launches) {
+  const int units = a.d / (2 * VP), heads = a.H + a.Hk;
+  const int64_t lanes = (int64_t)a.N * a.T * units;
+  const int64_t want = (int64_t)ctas_per_wave(4) * kThreads;
+  int64_t hpt = lanes * heads / want;
+  hpt = hpt < 1 ? 1 : hpt > heads ? heads : hpt;
+  const int groups = (int)((heads + hpt - 1) / hpt);
+  const int64_t blocks = (lanes * groups + kThreads - 1) / kThreads;
+  if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
+  trace_begin("rope", s);
+  rope_kernel<T, VP><<<(unsigned)blocks, kThreads, 0, s>>>(a, units, (int)hpt, groups);
+  trace_end(s);
+  ++*launches;
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_typed(const RopeCall& a, cudaStream_t s, int* launches) {
+  constexpr int V = 16 / sizeof(T);
+  return a.rope.rot % (2 * V) == 0 && a.d % (2 * V) == 0 ? launch<T, V>(a, s, launches)
+                                                         : launch<T, 1>(a, s, launches);
+}
+
+}  // namespace
+
+cudaError_t launch_rope(const RopeCall& a, lizard_dtype dt, cudaStream_t s, int* launches) {
+  return dt == LIZARD_F32 ? launch_typed<float>(a, s, launches) : launch_typed<bf16>(a, s, launches);
+}
+
+}  // namespace lz

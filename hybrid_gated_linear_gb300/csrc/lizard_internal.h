@@ -289,4 +289,65 @@ cudaError_t launch_ring_fill(int N, int H, int L, int W, int dk, int dv, lizard_
                              const void* k, const void* v, void* kr, void* vr, int64_t* pos,
                              cudaStream_t s, int* launches);
 
+// The cache, rotary table and row strides of the 8-bit cache calls after validation.
+struct CacheArgs {
+  unsigned char *k, *v;
+  float *ks, *vs;
+  const int32_t* table;
+  int N, max_pages, pages, Hk, P, log_p, d;
+  int fmt;  // lizard_kv_format
+};
+struct RopeArgs {
+  const uint64_t* turns;  // null: no rotation
+  int rot, layout;
+  float factor;
+};
+struct Strides {
+  int64_t n, h, t;
+};
+
+struct RopeCall {
+  int N, H, Hk, T, d;
+  RopeArgs rope;
+  float sign;  // of the sine: 1 forward, -1 backward
+  const void *xq, *xk;
+  void *yq, *yk;
+  Strides sxq, sxk, syq, syk;
+  const int64_t* positions;
+};
+cudaError_t launch_rope(const RopeCall& a, lizard_dtype dt, cudaStream_t s, int* launches);
+
+struct CacheIo {
+  CacheArgs c;
+  int T;
+  void *k, *v;  // inputs of a write, outputs of a read
+  Strides sk, sv;
+  RopeArgs rope;
+  const int64_t* pos;
+  const int32_t* count;
+  unsigned* status;
+};
+cudaError_t launch_cache_write(const CacheIo& a, lizard_dtype dt, cudaStream_t s, int* launches);
+cudaError_t launch_cache_read(const CacheIo& a, lizard_dtype dt, cudaStream_t s, int* launches);
+
+struct CacheAttn {
+  CacheArgs c;
+  int H, T, M, W;
+  float scale, alpha;
+  const void* q;
+  Strides sq;
+  RopeArgs rope;
+  const int64_t* pos;
+  const int32_t* count;
+  const int64_t* first;
+  const void *mk, *mv, *add;
+  Strides sadd;
+  void* y;
+  Strides sy;
+  unsigned* status;
+  unsigned char* ws;  // workspace after the header
+};
+size_t cache_attn_workspace(int N, int Hk, int H, int T, int d);
+cudaError_t launch_cache_attn(const CacheAttn& a, lizard_dtype dt, cudaStream_t s, int* launches);
+
 }  // namespace lz

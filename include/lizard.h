@@ -389,6 +389,185 @@ lizard_status lizard_gla_std_fwd(const lizard_dims* dims, const void* phi_q, con
 lizard_status lizard_selftest_wait_timeout(void* workspace, size_t workspace_bytes,
                                            int64_t wait_cycles, void* stream);
 
+/*
+ * Rotary positions, an 8-bit paged key/value cache and the attention over it: the softmax
+ * side of a hybrid model, next to the gated branch.  "Lizard" (arXiv 2507.09025) replaces
+ * softmax layers of a pretrained model by the operator above; the layers a hybrid keeps,
+ * the teacher it is distilled from, and anchor windows too long for a ring in the element
+ * type need positions, a cache that holds fewer bytes, grouped heads, and several new
+ * tokens at once (a chunk of a prompt, drafted tokens).
+ *
+ * Rows.  x [N,H,T,d] tensors of these calls may be strided: the element (n,h,t,c) is at
+ * n * s.n + h * s.h + t * s.t + c elements; NULL strides mean contiguous.  Strides are
+ * multiples of 16 bytes (0 repeats a row of an input); an output's elements must be
+ * distinct.  d is 64 or 128 for the cache calls.
+ */
+typedef struct lizard_strides { int64_t n, h, t; } lizard_strides; /* elements */
+
+/*
+ * Rotary positions.  Channel pair i < rot/2 of a head at position p is turned by p theta_i:
+ *   (a, b) -> f (a cos - b sin, b cos + a sin),   theta_i = base^(-2i/rot) before scaling,
+ * with (a, b) = channels (i, i + rot/2) (HALF) or (2i, 2i+1) (INTERLEAVED); the channels
+ * from rot on are copied.  f = attn_factor (> 0; 1 for none).  Scaling for long contexts:
+ * LINEAR divides every theta_i by factor; PARTS keeps the theta_i that turn more than
+ * `high` times over `original` tokens, divides those that turn fewer than `low` times, and
+ * mixes linearly between ("YaRN", arXiv 2309.00071, section 3.2).
+ * lizard_rope_table (host) writes theta_i / (2 pi) as 64-bit fixed-point turns per token:
+ * p * turns mod 2^64 is then the exact angle of any position, however far, and its upper
+ * bits are all the kernels convert to floating point.  `table` holds rot/2 words; the
+ * caller copies it to the device once and passes it as lizard_rope.turns.
+ */
+typedef enum lizard_rope_layout {
+    LIZARD_ROPE_HALF = 0,
+    LIZARD_ROPE_INTERLEAVED = 1
+} lizard_rope_layout;
+typedef enum lizard_rope_scaling {
+    LIZARD_ROPE_PLAIN = 0,
+    LIZARD_ROPE_LINEAR = 1,
+    LIZARD_ROPE_PARTS = 2
+} lizard_rope_scaling;
+
+typedef struct lizard_rope_spec {
+    int32_t rot;          /* rotated channels, even, 2..512 */
+    int32_t scaling;      /* lizard_rope_scaling */
+    double base;          /* > 1 */
+    double factor;        /* >= 1; LINEAR and PARTS */
+    double low, high;     /* 0 <= low < high; PARTS */
+    int64_t original;     /* >= 1; PARTS */
+} lizard_rope_spec;
+
+typedef struct lizard_rope {
+    const uint64_t* turns;  /* device, rot/2 words of lizard_rope_table */
+    int32_t rot;            /* even, 2..d */
+    int32_t layout;         /* lizard_rope_layout */
+    float attn_factor;      /* > 0 */
+} lizard_rope;
+
+typedef struct lizard_rope_dims {
+    int32_t N, H, Hk, T;  /* sequences, query heads, key heads (0: no keys), tokens (0: no-op) */
+    int32_t d;            /* channels per head, a multiple of 8, 8..512 */
+    lizard_dtype dtype;
+} lizard_rope_dims;
+
+lizard_status lizard_rope_table(const lizard_rope_spec* spec, uint64_t* table);
+
+/*
+ * y_q = rotate(x_q) [N,H,T,d], y_k = rotate(x_k) [N,Hk,T,d] (x_k, y_k NULL when Hk = 0), in
+ * one launch; positions [N,T] int64 (any value) or NULL for 0..T-1.  An output may be its
+ * own input (same pointer and strides).  The backward turns the gradients the other way
+ * (the adjoint: f times the rotation by -p theta_i).
+ */
+lizard_status lizard_rope_fwd(const lizard_rope_dims* dims, const lizard_rope* rope,
+                              const void* x_q, const lizard_strides* s_xq, const void* x_k,
+                              const lizard_strides* s_xk, const int64_t* positions, void* y_q,
+                              const lizard_strides* s_yq, void* y_k, const lizard_strides* s_yk,
+                              void* stream);
+lizard_status lizard_rope_bwd(const lizard_rope_dims* dims, const lizard_rope* rope,
+                              const void* dy_q, const lizard_strides* s_dyq, const void* dy_k,
+                              const lizard_strides* s_dyk, const int64_t* positions, void* dx_q,
+                              const lizard_strides* s_dxq, void* dx_k,
+                              const lizard_strides* s_dxk, void* stream);
+
+/*
+ * Paged 8-bit cache.  Keys and values are pools of pages; one page holds page_tokens tokens
+ * of every key head:
+ *   k_codes, v_codes [pages][Hk][page_tokens][d] bytes,  k_scale, v_scale [pages][Hk] fp32,
+ *   value = code * scale,  code = e4m3 (max 448) or a signed byte in -127..127.
+ * A scale is a power of two, 2^ceil(log2(amax / max code)) (2^-126 at least): multiplying by
+ * it and rescaling codes to a larger one are exact but for the rounding to the format.
+ * Inside a page, the 16-byte chunk c of token row r is stored at place c ^ (r mod 8) of its
+ * row (d = 128) or c ^ (r/2 mod 4) (d = 64): the order in which a tile copied linearly to
+ * shared memory is read without bank conflicts.
+ * Token t of sequence n lies in page table[n][(t / page_tokens) mod max_pages], row
+ * t mod page_tokens.  A table that covers the whole context never wraps; a window needs
+ * only the pages that overlap it, reused as a ring.
+ */
+typedef enum lizard_kv_format { LIZARD_KV_E4M3 = 0, LIZARD_KV_I8 = 1 } lizard_kv_format;
+
+typedef struct lizard_cache {
+    void *k_codes, *v_codes;
+    float *k_scale, *v_scale;
+    const int32_t* table;  /* [N][max_pages], page numbers in 0..pages-1 */
+    int32_t N, max_pages;
+    int32_t pages, Hk;
+    int32_t page_tokens;   /* 16, 32, 64 or 128 */
+    int32_t d;             /* 64 or 128 */
+    lizard_kv_format format;
+} lizard_cache;
+
+typedef struct lizard_cache_io {
+    int32_t T;             /* tokens per sequence at most, >= 0 (0 is a no-op) */
+    lizard_dtype dtype;    /* of k and v */
+} lizard_cache_io;
+
+/*
+ * Write: tokens j < count[n] of k, v [N,Hk,T,d] T go to positions pos[n] + j (count NULL:
+ * all T), the keys rotated on the way if `rope` is given (in fp32, unrounded).  pos [N]
+ * int64, count [N] int32.  A page whose first row is written starts afresh; a page that
+ * already holds earlier tokens keeps the larger of its scale and the new tokens' one, its
+ * codes rounded again when the scale grows; rows after the last written token are dead.
+ * The same page must not be written for two sequences in one call.  NaN is stored as 0 and
+ * an infinity as the largest code, and both set LIZARD_ERR_DEVICE_CHECK; so does a sequence
+ * whose tokens span more than max_pages pages, a negative position, a count outside 0..T or
+ * a page number outside the pool: nothing is written for such a sequence (page).
+ *
+ * Read: positions pos[n] + j, j < count[n], of the cache as values k, v [N,Hk,T,d] T, zeros
+ * for the other rows (and for rows of a sequence or page that fails the checks above).
+ *
+ * Workspace: lizard_cache_workspace_bytes() bytes, zero before the first call; only the
+ * status word is used, so calls ordered on one stream may share it.
+ */
+size_t lizard_cache_workspace_bytes(void);
+lizard_status lizard_cache_write(const lizard_cache* cache, const lizard_cache_io* io,
+                                 const void* k, const lizard_strides* s_k, const void* v,
+                                 const lizard_strides* s_v, const lizard_rope* rope,
+                                 const int64_t* pos, const int32_t* count, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+lizard_status lizard_cache_read(const lizard_cache* cache, const lizard_cache_io* io,
+                                const int64_t* pos, const int32_t* count, void* k,
+                                const lizard_strides* s_k, void* v, const lizard_strides* s_v,
+                                void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Attention over the cache, merged with another branch's output:
+ *   y = y_add + alpha * softmax(scale [q . meta_k ; q' . k_t]) [meta_v ; v_t]
+ * Query j < count[n] of sequence n sits at position p = pos[n] + j (its own key and value
+ * already written) and sees the tokens t <= p with t >= first[n] (NULL: 0) and, for W > 0,
+ * t > p - W, and all M meta tokens of its head.  q' is q rotated at p if `rope` is given;
+ * meta tokens carry no position and meet q itself.  Query head h reads key head
+ * h / (H / Hk).  A query that sees nothing gets y_add (0 without it); rows j >= count[n]
+ * are written as 0.
+ *   q, y, y_add [N,H,T,d] T (y_add NULL, or y itself, or apart from it); meta_k, meta_v
+ *   [H,M,d] T contiguous; pos, first [N] int64, count [N] int32.
+ * A sequence that fails the checks of lizard_cache_write (for the pages its queries see)
+ * sees no cached token, a page number outside the pool is skipped, and both set
+ * LIZARD_ERR_DEVICE_CHECK.  Every sum and the softmax are in fp32; bf16 calls round the
+ * query and the unnormalised probabilities to 11 bits for the tensor cores, fp32 calls
+ * carry them in two such parts.  Run-to-run identical.
+ * Workspace: lizard_cache_attn_workspace_bytes, zero before the first call; each call
+ * leaves it zero but for the status word and scratch.  Calls that may run at the same time
+ * need their own.
+ */
+typedef struct lizard_cache_attn_dims {
+    int32_t H;             /* query heads, a multiple of the cache's Hk */
+    int32_t T;             /* new tokens per sequence, >= 0 (0 is a no-op) */
+    int32_t M;             /* meta tokens per head, 0..16 */
+    int32_t W;             /* window (tokens including self), 0: none */
+    lizard_dtype dtype;    /* of q, meta_k, meta_v, y_add, y */
+    float scale;           /* <= 0 selects 1/sqrt(d) */
+    float alpha;
+} lizard_cache_attn_dims;
+
+size_t lizard_cache_attn_workspace_bytes(const lizard_cache* cache,
+                                         const lizard_cache_attn_dims* dims);
+lizard_status lizard_cache_attn(const lizard_cache* cache, const lizard_cache_attn_dims* dims,
+                                const void* q, const lizard_strides* s_q,
+                                const lizard_rope* rope, const int64_t* pos,
+                                const int32_t* count, const int64_t* first, const void* meta_k,
+                                const void* meta_v, const void* y_add,
+                                const lizard_strides* s_add, void* y, const lizard_strides* s_y,
+                                void* workspace, size_t workspace_bytes, void* stream);
+
 /* Static description of a status code. */
 const char* lizard_status_string(lizard_status status);
 
