@@ -1,138 +1,691 @@
-// k_cache_attn.cu -- attention over the 8-bit paged cache, merged with another branch.
+// k_cache_attn.cu -- attention over the 8-bit paged cache for one to a few new tokens per
+// sequence (decode, verification of drafts), merged with another branch.
 //
-// One warp per (sequence, query head, new token): each lane holds D/32 channels of the
-// query, the logits of the visible tokens come one at a time, and a running maximum m and
-// sum l rescale the accumulated output (o <- o e^{m-m'} + e^{z-m'} v), so the cache is read
-// once.  Meta tokens meet the query before its rotation.
+// For each (sequence n, key head) the rows are its G = H / Hk query heads times the new
+// tokens.  With z the logits in units of log 2, softmax is one pass over the cache:
+//   m' = max(m, z),  l' = l 2^(m-m') + sum 2^(z-m'),  o' = o 2^(m-m') + sum 2^(z-m') v.
+// The value scales are powers of two 2^e per page, so the weights the tensor cores see are
+// 2^(z+e-mo) with a maximum mo of their own: they stay in (0, 1], whatever the pages' scales.
+//
+// What bounds it: the cache is read once, 2 D bytes per token and head, and everything else
+// is small; the floor is those bytes at the measured copy rate.  So the work is cut evenly
+// over the bytes, not over the sequences: all 32-token units of all (sequence, head) pairs
+// form one list, every CTA takes an equal contiguous share of it, and pairs that end up in
+// several CTAs are joined by the last of them to finish (fixed order: results do not depend
+// on timing).  Inside a CTA every warp owns units of its own, with no CTA-wide barrier in
+// the loop: one lane copies the keys, then the values of the next unit with bulk copies
+// (pages are contiguous and stored in the order the reads want) while the warp computes.
+// The products run on mma.sync: 16 rows fill its M, where the 128 rows of a tcgen05 tile
+// would be an eighth full, and the tensor time is a third of the copy time.
+#include <algorithm>
+
 #include "kv_cache.cuh"
+#include "tc_sm100.cuh"
 
 namespace lz {
 namespace {
 
-constexpr int kWarps = 8;
+using tc::mbar_try_wait;
 
-template <int D, int F>
-__device__ __forceinline__ void load_codes(const unsigned char* row, int r, int lane, float (&x)[D / 32]) {
-  constexpr int E = D / 32;
-  const int e = lane * E;
-  const unsigned char* p = row + chunk_place<D>(r, e / 16) * 16 + e % 16;
-  const uint32_t w = E == 4 ? *reinterpret_cast<const uint32_t*>(p) : *reinterpret_cast<const uint16_t*>(p);
-  const float4 v = codes_to_float<F>(w);
-  x[0] = v.x, x[1] = v.y;
-  if (E == 4) x[E - 2] = v.z, x[E - 1] = v.w;
+constexpr int kThreads = 256;
+constexpr int kUnit = 32;  // tokens per unit of work
+constexpr int kMaxM = 16;
+constexpr int kMaxCtas = 512;  // CTAs of a launch at most (sizes the scratch)
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-template <typename T, int D, int F>
-__global__ void __launch_bounds__(kWarps * 32) attn_kernel(CacheAttn a) {
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31;
-  const int64_t row = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (row >= (int64_t)a.c.N * a.H * a.T) return;
-  const int t = (int)(row % a.T), h = (int)(row / a.T % a.H), n = (int)(row / a.T / a.H);
-  const int hk = h / (a.H / a.c.Hk);
-  T* y = static_cast<T*>(a.y) + n * a.sy.n + h * a.sy.h + t * a.sy.t;
-  const int cnt = a.count ? a.count[n] : a.T;
-  const int64_t p0 = a.pos[n], p = p0 + t;
-  const int64_t first = a.first ? a.first[n] : 0;
-  const bool known = cnt >= 0 && cnt <= a.T && p0 >= 0;
-  if (!known && lane == 0) raise_status(a.status, kDevCheck);
-  if (t >= cnt || cnt > a.T) {
-#pragma unroll
-    for (int i = 0; i < E; ++i) y[lane * E + i] = cvt_out<T>(0.f);
-    return;
-  }
-  // the pages all of this sequence's queries see have to fit the table
-  int64_t lo0 = a.W > 0 ? p0 - a.W + 1 : 0;
-  lo0 = max(lo0, max(first, (int64_t)0));
-  const bool seen = known && lo0 <= p0 + cnt - 1;
-  const bool fits = seen && span_ok(a.c, lo0, p0 + cnt - 1);
-  if (seen && !fits && lane == 0) raise_status(a.status, kDevCheck);
-  const int64_t lo = max(lo0, a.W > 0 ? p - a.W + 1 : (int64_t)0);
+__device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// What rounding (lo, hi) to halves lost, again as halves.
+__device__ __forceinline__ uint32_t half2_rest(float lo, float hi, uint32_t r) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&r));
+  return half2_bits(lo - f.x, hi - f.y);
+}
 
-  const T* qp = static_cast<const T*>(a.q) + n * a.sq.n + h * a.sq.h + t * a.sq.t;
-  float q[E], o[E], m = -INFINITY, l = 0.f;
+// What the rows of one (sequence, block of rows) see.  `m` counts them: sequence m / RB,
+// rows RR * (m % RB) and on (row = token * G + head in group).
+struct Segment {
+  int64_t base;  // first unit's first token (a multiple of kUnit)
+  int64_t p0;    // position of token 0
+  int64_t first; // first visible token, >= 0
+  int lo, hi;    // visible tokens of the block relative to base; hi < lo: none
+  int units;     // >= 1
+  int cnt;       // tokens with a query
+};
+
+__device__ __forceinline__ Segment segment_of(const CacheAttn& a, int m, int RB, int RR, int G) {
+  const int n = m / RB, r0 = (m - n * RB) * RR;
+  Segment s;
+  s.p0 = a.pos[n];
+  s.cnt = a.count ? a.count[n] : a.T;
+  s.first = a.first ? max((int64_t)0, a.first[n]) : 0;
+  const bool known = s.cnt >= 0 && s.cnt <= a.T && s.p0 >= 0;
+  if (!known) raise_status(a.status, kDevCheck);
+  s.cnt = known ? s.cnt : 0;
+  s.base = 0, s.lo = 0, s.hi = -1, s.units = 1;
+  if (r0 < s.cnt * G) {
+    // what the whole sequence sees has to fit its table
+    const int64_t all_lo = max(s.first, a.W > 0 ? s.p0 - a.W + 1 : (int64_t)0), all_hi = s.p0 + s.cnt - 1;
+    if (all_lo <= all_hi) {
+      if (!span_ok(a.c, all_lo, all_hi)) {
+        raise_status(a.status, kDevCheck);
+      } else {
+        const int t0 = r0 / G, t1 = (min(r0 + RR, s.cnt * G) - 1) / G;
+        const int64_t lo = max(s.first, a.W > 0 ? s.p0 + t0 - a.W + 1 : (int64_t)0), hi = s.p0 + t1;
+        if (lo <= hi) {
+          s.base = lo & ~(int64_t)(kUnit - 1);
+          s.lo = (int)(lo - s.base);
+          s.hi = (int)(hi - s.base);
+          s.units = s.hi / kUnit + 1;
+        }
+      }
+    }
+  }
+  return s;
+}
+
+// One merged set of rows: maxima, sum and output of a row (unnormalised).
+struct RowStat {
+  float m, mo, l;
+};
+
+template <typename T, int D, int F, int RG>
+struct Shape {
+  static constexpr int NS = sizeof(T) == 4 ? 2 : 1;  // parts of a query and of a probability
+  static constexpr int TG = 8 / RG;                  // warps that share out a piece's units
+  static constexpr int S = RG;                       // stages per unit group
+  static constexpr int RR = 16 * RG;                 // rows
+  static constexpr int kHalf = kUnit * D;            // bytes of the keys of a unit
+  // dynamic shared memory: the unit buffers, which the merge of the warps' outputs reuses
+  // (8 warps x 16 rows x D floats, the same size), then the queries
+  static constexpr int kBuf = TG * S * 2 * kHalf;
+  static_assert(kBuf == 8 * 16 * D * 4, "the merge fills the unit buffers");
+  static constexpr int kSmem = kBuf + RR * D * 2 * NS;
+  // two CTAs per SM where their shared memory allows it
+  static constexpr int kPerSm = kSmem + RR * kMaxM * 4 + 4096 <= 113 * 1024 ? 2 : 1;
+  static constexpr int kPartial = RR * (D + 4);      // floats of a partial result
+};
+
+template <typename T, int D, int F, int RG>
+__global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG>::kPerSm) split_kernel(CacheAttn a, int RB, int min_units) {
+  using Sh = Shape<T, D, F, RG>;
+  constexpr int NS = Sh::NS, TG = Sh::TG, S = Sh::S, RR = Sh::RR, KS = D / 16, NT = D / 8;
+  extern __shared__ __align__(128) unsigned char smem[];
+  unsigned char* s_q = smem + Sh::kBuf;
+  __shared__ __align__(8) uint64_t s_bar[4][TG * S];  // keys full, values full, keys free, values free
+  __shared__ float s_rs[RR];                          // log2 e * scale * the query's power of two
+  __shared__ float s_zm[RR * kMaxM];                  // logits of the meta tokens
+  __shared__ RowStat s_st[8][16];
+  __shared__ int64_t s_sum[8];
+  __shared__ int64_t s_start;
+  __shared__ int s_m, s_abort, s_last;
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = lane >> 2, t4 = lane & 3;
+  const int rg = warp % RG, tg = warp / RG;
+  const int G = a.H / a.c.Hk, Hk = a.c.Hk, M2 = a.c.N * RB;
+
+  if (tid == 0) {
+    for (int i = 0; i < TG * S; ++i) {
+      tc::mbar_init(&s_bar[0][i], 1);
+      tc::mbar_init(&s_bar[1][i], 1);
+      tc::mbar_init(&s_bar[2][i], RG);
+      tc::mbar_init(&s_bar[3][i], RG);
+    }
+    s_abort = 0;
+    tc::fence_mbar_init();
+  }
+  pdl_wait();
+
+  // this CTA's share [f0, f1) of the list of units (sequence-major, then head, then token)
+  int64_t mine = 0;
+  for (int m = tid; m < M2; m += kThreads) mine += segment_of(a, m, RB, RR, G).units;
 #pragma unroll
-  for (int i = 0; i < E; ++i) q[i] = ld_f(qp + lane * E + i), o[i] = 0.f;
-  auto add = [&](float z, const float (&v)[E], float s) {
-    const float mn = fmaxf(m, z);
-    const float f = expf(m - mn), w = expf(z - mn);
-    l = l * f + w;
+  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+  if (lane == 0) s_sum[warp] = mine;
+  __syncthreads();
+  int64_t total = 0;
 #pragma unroll
-    for (int i = 0; i < E; ++i) o[i] = fmaf(w * s, v[i], o[i] * f);
-    m = mn;
+  for (int w = 0; w < 8; ++w) total += s_sum[w];
+  total *= Hk;
+  int64_t share = (total + gridDim.x - 1) / gridDim.x;
+  if (share < min_units) share = min_units;
+  int64_t f = blockIdx.x * share;
+  const int64_t f1 = min(total, f + share);
+  if (f >= total) return;
+  {  // the segment f lies in
+    int64_t before = 0;
+    for (int m0 = 0; m0 < M2; m0 += kThreads) {
+      const int m = m0 + tid;
+      const int64_t u = m < M2 ? (int64_t)segment_of(a, m, RB, RR, G).units * Hk : 0;
+      int64_t c = u;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, c, o);
+        if (lane >= o) c += x;
+      }
+      __syncthreads();
+      if (lane == 31) s_sum[warp] = c;
+      __syncthreads();
+      for (int w = 0; w < warp; ++w) c += s_sum[w];
+      c += before;
+      if (f < c && f >= c - u) s_m = m, s_start = c - u;
+      for (int w = 0; w < 8; ++w) before += s_sum[w];
+      if (f < before) break;
+    }
+    __syncthreads();
+  }
+  int m = s_m;
+  int64_t seg0 = s_start;  // list index of segment m's first unit (head 0)
+
+  uint32_t used = 0;  // units this warp's group has consumed, over all pieces
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const long long c0 = clock64();
+    while (true) {
+#pragma unroll 1
+      for (int k = 0; k < 32; ++k)
+        if (mbar_try_wait(bar, parity)) return true;
+      if (*(volatile int*)&s_abort) return false;
+      if (clock64() - c0 > 2000000000ll) {
+        *(volatile int*)&s_abort = 1;
+        return false;
+      }
+    }
   };
-  for (int j = 0; j < a.M; ++j) {
-    const T* k = static_cast<const T*>(a.mk) + ((size_t)h * a.M + j) * D + lane * E;
-    const T* v = static_cast<const T*>(a.mv) + ((size_t)h * a.M + j) * D + lane * E;
-    float z = 0.f, x[E];
+
+  while (f < f1) {
+    const Segment sg = segment_of(a, m, RB, RR, G);
+    const int n = m / RB, r0 = (m - n * RB) * RR;
+    const int hk = (int)((f - seg0) / sg.units);
+    const int64_t head0 = seg0 + (int64_t)hk * sg.units;  // list index of this head's first unit
+    const int ua = (int)(f - head0), ub = (int)min((int64_t)sg.units, f1 - head0);
+    const int nu = ub - ua > tg ? (ub - ua - tg + TG - 1) / TG : 0;  // units of this group
+
+    // ---- pages and scales of the group's units, 32 units at a time in the lanes' registers
+    // (two 16-token blocks per unit; -1: nothing to see there)
+    int id0 = -1, id1 = -1, nid0 = -1, nid1 = -1;
+    float ks0 = 0.f, ks1 = 0.f, nks0 = 0.f, nks1 = 0.f;
+    int ve0 = 0, ve1 = 0, nve0 = 0, nve1 = 0;
+    auto load_meta = [&](int batch) {
+      const int j = batch * 32 + lane;
+      nid0 = nid1 = -1;
+      if (j < nu) {
+        const int tok = (ua + tg + j * TG) * kUnit;
+        const bool in0 = tok + 15 >= sg.lo && tok <= sg.hi, in1 = tok + 31 >= sg.lo && tok + 16 <= sg.hi;
+        const uint32_t pg = (uint32_t)((sg.base + tok) >> a.c.log_p);
+        if (in0 || (in1 && a.c.P > 16)) {
+          nid0 = pool_page(a.c, n, pg);
+          if (nid0 < 0) raise_status(a.status, kDevCheck);
+        }
+        if (a.c.P > 16) {
+          nid1 = in1 ? nid0 : -1;
+          if (!in0) nid0 = -1;
+        } else if (in1) {
+          nid1 = pool_page(a.c, n, pg + 1);
+          if (nid1 < 0) raise_status(a.status, kDevCheck);
+        }
+        if (nid0 >= 0) {
+          const size_t ph = (size_t)nid0 * Hk + hk;
+          nks0 = a.c.ks[ph];
+          nve0 = (int)(__float_as_uint(a.c.vs[ph]) >> 23) - 127;
+        }
+        if (nid1 >= 0) {
+          const size_t ph = (size_t)nid1 * Hk + hk;
+          nks1 = a.c.ks[ph];
+          nve1 = (int)(__float_as_uint(a.c.vs[ph]) >> 23) - 127;
+        }
+      }
+    };
+    // Copies the keys (x = 0) or values (x = 1) of the group's unit j into its stage.
+    auto copy = [&](int x, int j, int i0, int i1) {
+      const uint32_t u = used + j;  // running number of the unit
+      const int st = tg * S + u % S;
+      unsigned char* dst = smem + (size_t)st * 2 * Sh::kHalf + x * Sh::kHalf;
+      const unsigned char* pool = x ? a.c.v : a.c.k;
+      const int tok = (ua + tg + j * TG) * kUnit;
+      const int row = (int)((sg.base + tok) & (a.c.P - 1));
+      uint64_t* bar = &s_bar[x][st];
+      const uint32_t half = Sh::kHalf / 2;
+      tc::mbar_arrive_expect_tx(bar, (i0 >= 0 ? half : 0) + (i1 >= 0 ? half : 0));
+      if (i0 >= 0)
+        tc::bulk_load(dst, pool + (((size_t)i0 * Hk + hk) * a.c.P + row) * D, i0 == i1 && a.c.P > 16 ? 2 * half : half,
+                      bar);
+      if (i1 >= 0 && !(i0 == i1 && a.c.P > 16))
+        tc::bulk_load(dst + half, pool + (((size_t)i1 * Hk + hk) * a.c.P + ((row + 16) & (a.c.P - 1))) * D, half,
+                      bar);
+    };
+    // page ids of unit j (in the current or the next batch); all lanes take part
+    auto ids_of = [&](int j, int now, int& i0, int& i1) {
+      const bool next = (j >> 5) != (now >> 5);
+      i0 = __shfl_sync(0xffffffffu, next ? nid0 : id0, j & 31);
+      i1 = __shfl_sync(0xffffffffu, next ? nid1 : id1, j & 31);
+    };
+    load_meta(0);
+    id0 = nid0, id1 = nid1, ks0 = nks0, ks1 = nks1, ve0 = nve0, ve1 = nve1;
+    load_meta(1);
+    if (rg == 0)
+      for (int j = 0; j < S && j < nu; ++j) {
+        int i0, i1;
+        ids_of(j, 0, i0, i1);
+        if (lane == 0) copy(0, j, i0, i1), copy(1, j, i0, i1);
+        __syncwarp();
+      }
+
+    // ---- queries: rotated, scaled to a power of two near 2^13, in the order the MMAs read
+    constexpr int LPR = D / 4, RPI = 32 / LPR;  // lanes per row, rows per iteration of a warp
+    const int rows = min(RR, sg.cnt * G - r0);  // rows with a query (may be <= 0)
+    for (int rb = warp * RPI; rb < RR; rb += 8 * RPI) {
+      const int r = rb + lane / LPR, d0 = (lane % LPR) * 4;
+      float x[4] = {0.f, 0.f, 0.f, 0.f};
+      const bool have = r < rows;
+      const T* qp = nullptr;
+      if (have) {
+        const int tt = (r0 + r) / G, h = hk * G + (r0 + r) % G;
+        qp = static_cast<const T*>(a.q) + n * a.sq.n + h * a.sq.h + tt * a.sq.t;
+        const float4 v = ld4(qp + d0);
+        x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+      }
+      if (ua == 0)  // the piece with the first unit adds the meta tokens
+        for (int j = 0; j < a.M; ++j) {
+          float z = 0.f;
+          if (have) {
+            const int h = hk * G + (r0 + r) % G;
+            const float4 k = ld4(static_cast<const T*>(a.mk) + ((size_t)h * a.M + j) * D + d0);
+            z = x[0] * k.x + x[1] * k.y + x[2] * k.z + x[3] * k.w;
+          }
 #pragma unroll
-    for (int i = 0; i < E; ++i) z = fmaf(q[i], ld_f(k + i), z), x[i] = ld_f(v + i);
-    add(warp_sum(z) * a.scale, x, 1.f);
-  }
-  if (a.rope.turns) {
+          for (int o = LPR / 2; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+          if (lane % LPR == 0) s_zm[r * kMaxM + j] = z * (a.scale * kLog2e);
+        }
+      if (have && a.rope.turns && d0 < a.rope.rot) {
+        const int64_t p = sg.p0 + (r0 + r) / G;
+        const int hr = a.rope.rot / 2;
+        float y[4];
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-      const int e = lane * E + i, hr = a.rope.rot / 2;
-      if (e < a.rope.rot) {
-        const bool half = a.rope.layout == LIZARD_ROPE_HALF;
-        const bool low = half ? e < hr : e % 2 == 0;
-        const int pair = half ? (low ? e : e - hr) : e / 2;
-        const float other = ld_f(qp + (half ? (low ? e + hr : e - hr) : e ^ 1));
-        float co, si;
-        rope_angle(a.rope.turns[pair], p, a.rope.factor, co, si);
-        q[i] = low ? q[i] * co - other * si : q[i] * co + other * si;
+        for (int i = 0; i < 4; ++i) {
+          const int e = d0 + i;
+          y[i] = x[i];
+          if (e < a.rope.rot) {
+            const bool half = a.rope.layout == LIZARD_ROPE_HALF;
+            const bool low = half ? e < hr : (e & 1) == 0;
+            const float o = half ? ld_f(qp + (low ? e + hr : e - hr)) : x[i ^ 1];
+            float co, si;
+            rope_angle(a.rope.turns[half ? (low ? e : e - hr) : e >> 1], p, a.rope.factor, co, si);
+            y[i] = low ? x[i] * co - o * si : x[i] * co + o * si;
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = y[i];
+      }
+      float mx = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
+#pragma unroll
+      for (int o = LPR / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      // x = 2^e x', |x'| < 2^14: halves keep 11 bits down to 2^-28 of the row's largest
+      int e = (int)(__float_as_uint(mx) >> 23) - 127 - 13;
+      e = max(-126, min(e, 113));
+      const float inv = exp2_int(-e);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i] *= inv;
+      if (lane % LPR == 0) s_rs[r] = a.scale * kLog2e * exp2_int(e);
+      // element d = (D/4) t + 4 s + i of row r feeds lane (r%8) t, step s, register 2 (i/2) + r/8%2
+      const int t = d0 / (D / 4), s = (d0 % (D / 4)) / 4;
+      uint32_t* dst = reinterpret_cast<uint32_t*>(s_q) +
+                      ((size_t)((r >> 4) * NS * KS + s) * 32 + (r & 7) * 4 + t) * 4 + ((r >> 3) & 1);
+      const uint32_t w0 = half2_bits(x[0], x[1]), w1 = half2_bits(x[2], x[3]);
+      dst[0] = w0, dst[2] = w1;
+      if (NS == 2) {
+        dst[KS * 128] = half2_rest(x[0], x[1], w0);
+        dst[KS * 128 + 2] = half2_rest(x[2], x[3], w1);
       }
     }
-  }
-  if (fits) {
-    for (int64_t pg = lo >> a.c.log_p; pg <= p >> a.c.log_p; ++pg) {
-      const int id = pool_page(a.c, n, (uint32_t)pg);
-      if (id < 0) {
-        if (lane == 0) raise_status(a.status, kDevCheck);
-        continue;
-      }
-      const size_t ph = (size_t)id * a.c.Hk + hk;
-      const unsigned char *kp = a.c.k + ph * a.c.P * D, *vp = a.c.v + ph * a.c.P * D;
-      const float ks = a.c.ks[ph] * a.scale, vs = a.c.vs[ph];
-      const int64_t t0 = pg << a.c.log_p;
-      const int r0 = (int)max((int64_t)0, lo - t0), r1 = (int)min((int64_t)a.c.P - 1, p - t0);
-      for (int r = r0; r <= r1; ++r) {
-        float k[E], v[E], z = 0.f;
-        load_codes<D, F>(kp + (size_t)r * D, r, lane, k);
-        load_codes<D, F>(vp + (size_t)r * D, r, lane, v);
+    __syncthreads();
+
+    // ---- this warp's rows g and g + 8
+    float o[NT][4], mrow[2] = {-INFINITY, -INFINITY}, mo[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
-        for (int i = 0; i < E; ++i) z = fmaf(q[i], k[i], z);
-        add(warp_sum(z) * ks, v, vs);
+    for (int i = 0; i < NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    int lo_r[2], hi_r[2];
+    float rs[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = rg * 16 + g + 8 * i, tt = (r0 + r) / G;
+      rs[i] = s_rs[r];
+      hi_r[i] = r < rows ? (int)(sg.p0 + tt - sg.base) : -1;
+      const int64_t lo = max(sg.first, a.W > 0 ? sg.p0 + tt - a.W + 1 : (int64_t)0);
+      lo_r[i] = (int)max((int64_t)0, min(lo - sg.base, (int64_t)0x7fffffff));
+      if (sg.hi < sg.lo) hi_r[i] = -1;
+    }
+    // tokens every row of the block sees
+    const int tl = rows > 0 ? (r0 + rows - 1) / G : 0;
+    const int all_lo = (int)max((int64_t)0, max(sg.first, a.W > 0 ? sg.p0 + tl - a.W + 1 : (int64_t)0) - sg.base);
+    const int all_hi = rows > 0 ? (int)(sg.p0 + r0 / G - sg.base) : -1;
+    const uint4* qf = reinterpret_cast<const uint4*>(s_q) + (size_t)rg * NS * KS * 32 + lane;
+
+    for (int j = 0; j < nu; ++j) {
+      if ((j & 31) == 0 && j > 0) {
+        id0 = nid0, id1 = nid1, ks0 = nks0, ks1 = nks1, ve0 = nve0, ve1 = nve1;
+        load_meta((j >> 5) + 1);
+      }
+      const uint32_t u = used + j;
+      const int st = tg * S + u % S;
+      const uint32_t parity = (u / S) & 1;
+      const unsigned char* kb = smem + (size_t)st * 2 * Sh::kHalf;
+      const unsigned char* vb = kb + Sh::kHalf;
+      const int tok = (ua + tg + j * TG) * kUnit;
+      const float kk[2] = {__shfl_sync(0xffffffffu, ks0, j & 31), __shfl_sync(0xffffffffu, ks1, j & 31)};
+      const int ve[2] = {__shfl_sync(0xffffffffu, ve0, j & 31), __shfl_sync(0xffffffffu, ve1, j & 31)};
+      const bool ok0 = __shfl_sync(0xffffffffu, id0, j & 31) >= 0, ok1 = __shfl_sync(0xffffffffu, id1, j & 31) >= 0;
+
+      // logits: lane (g, t4) holds channels (D/4) t4 .. of token 8 i + g
+      if (!wait(&s_bar[0][st], parity)) break;
+      float z[4][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        z[i][0] = z[i][1] = z[i][2] = z[i][3] = 0.f;
+        const int r = 8 * i + g;
+        uint32_t w[KS];
+#pragma unroll
+        for (int h = 0; h < KS / 4; ++h) {
+          const uint4 v = *reinterpret_cast<const uint4*>(kb + r * D + 16 * chunk_place<D>(r, KS / 4 * t4 + h));
+          w[4 * h] = v.x, w[4 * h + 1] = v.y, w[4 * h + 2] = v.z, w[4 * h + 3] = v.w;
+        }
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+          uint32_t b0, b1;
+          codes_to_half<F>(w[s], b0, b1);
+#pragma unroll
+          for (int p = 0; p < NS; ++p) {
+            const uint4 q = qf[(p * KS + s) * 32];
+            const uint32_t qa[4] = {q.x, q.y, q.z, q.w};
+            mma16816(z[i], qa, b0, b1);
+          }
+        }
+      }
+      // the keys' stage is free: the next unit that uses it
+      auto refill = [&](int x) {
+        // with one warp per group its own reads are done; else the unit before this one,
+        // which the other warps have most likely left, is replaced
+        const int back = RG > 1 ? 1 : 0;
+        if (RG > 1) {
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&s_bar[2 + x][st]);
+        }
+        if (rg == 0 && j - back + S < nu && j >= back) {
+          int i0, i1;
+          ids_of(j - back + S, j, i0, i1);
+          if (RG > 1) {
+            const uint32_t v = u - 1;
+            if (!wait(&s_bar[2 + x][tg * S + v % S], (v / S) & 1)) return;
+          }
+          __syncwarp();
+          if (lane == 0) copy(x, j - back + S, i0, i1);
+          __syncwarp();
+        }
+      };
+      refill(0);
+
+      // scale and mask; column 8 i + 2 t4 + e
+      float sm[2][2] = {{-INFINITY, -INFINITY}, {-INFINITY, -INFINITY}};  // [row][block] maxima
+      const bool whole = ok0 && ok1 && tok >= all_lo && tok + kUnit - 1 <= all_hi;
+      const float f0[2] = {rs[0] * kk[0], rs[0] * kk[1]}, f8[2] = {rs[1] * kk[0], rs[1] * kk[1]};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float v = z[i][e] * (e < 2 ? f0[i >> 1] : f8[i >> 1]) * kCodeUnit<F>;
+          if (!whole) {
+            const int c = tok + 8 * i + 2 * t4 + (e & 1);
+            const bool see = (i < 2 ? ok0 : ok1) && c >= lo_r[e >> 1] && c <= hi_r[e >> 1];
+            v = see ? v : -INFINITY;
+          }
+          z[i][e] = v;
+          sm[e >> 1][i >> 1] = fmaxf(sm[e >> 1][i >> 1], v);
+        }
+      float mn[2], mon[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          sm[i][b] = fmaxf(sm[i][b], __shfl_xor_sync(0xffffffffu, sm[i][b], 1));
+          sm[i][b] = fmaxf(sm[i][b], __shfl_xor_sync(0xffffffffu, sm[i][b], 2));
+        }
+        mn[i] = fmaxf(mrow[i], fmaxf(sm[i][0], sm[i][1]));
+        mon[i] = fmaxf(mo[i], fmaxf(sm[i][0] + (float)ve[0], sm[i][1] + (float)ve[1]));
+      }
+      const bool grew = mn[0] > mrow[0] || mn[1] > mrow[1] || mon[0] > mo[0] || mon[1] > mo[1];
+      if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          // -inf - -inf: nothing seen so far, and nothing to rescale
+          const float fl = mn[i] > mrow[i] ? exp2f(mrow[i] - mn[i]) : 1.f;
+          const float fo = mon[i] > mo[i] ? exp2f(mo[i] - mon[i]) : 1.f;
+          l[i] *= fl;
+          mrow[i] = mn[i], mo[i] = mon[i];
+#pragma unroll
+          for (int k = 0; k < NT; ++k) o[k][2 * i] *= fo, o[k][2 * i + 1] *= fo;
+        }
+      }
+      uint32_t pw[NS][2][4];
+      {
+        const float ml[2] = {mrow[0] == -INFINITY ? 0.f : mrow[0], mrow[1] == -INFINITY ? 0.f : mrow[1]};
+        float sh[2][2];  // 2^(z + ve - mo)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int b = 0; b < 2; ++b) sh[i][b] = mo[i] == -INFINITY ? 0.f : mo[i] - (float)ve[b];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float p[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            l[e >> 1] += tc::ex2_approx(z[i][e] - ml[e >> 1]);
+            p[e] = tc::ex2_approx(z[i][e] - sh[e >> 1][i >> 1]);
+          }
+          const uint32_t w0 = half2_bits(p[0], p[1]), w1 = half2_bits(p[2], p[3]);
+          pw[0][i >> 1][(i & 1) * 2] = w0, pw[0][i >> 1][(i & 1) * 2 + 1] = w1;
+          if (NS == 2) {
+            pw[NS - 1][i >> 1][(i & 1) * 2] = half2_rest(p[0], p[1], w0);
+            pw[NS - 1][i >> 1][(i & 1) * 2 + 1] = half2_rest(p[2], p[3], w1);
+          }
+        }
+      }
+
+      // output: lane (g, t4) holds channels (D/8) g .. of tokens 2 t4, 2 t4 + 1 (+ 8)
+      if (!wait(&s_bar[1][st], parity)) break;
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        constexpr int WV = D / 32;  // words of a lane's channels
+        uint32_t w[4][WV];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int r = 16 * b + 2 * t4 + (k & 1) + 8 * (k >> 1);
+          if (D == 128) {
+            const uint4 v = *reinterpret_cast<const uint4*>(vb + r * D + 16 * chunk_place<D>(r, g));
+            w[k][0] = v.x, w[k][1] = v.y, w[k][WV - 2] = v.z, w[k][WV - 1] = v.w;
+          } else {
+            const uint2 v = *reinterpret_cast<const uint2*>(vb + r * D + 16 * chunk_place<D>(r, g >> 1) + 8 * (g & 1));
+            w[k][0] = v.x, w[k][1] = v.y;
+          }
+        }
+#pragma unroll
+        for (int q = 0; q < WV; ++q) {
+          uint32_t b0[4], b1[4];
+          codes_to_half<F>(__byte_perm(w[0][q], w[1][q], 0x5140), b0[0], b0[1]);
+          codes_to_half<F>(__byte_perm(w[0][q], w[1][q], 0x7362), b0[2], b0[3]);
+          codes_to_half<F>(__byte_perm(w[2][q], w[3][q], 0x5140), b1[0], b1[1]);
+          codes_to_half<F>(__byte_perm(w[2][q], w[3][q], 0x7362), b1[2], b1[3]);
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int p = 0; p < NS; ++p) mma16816(o[4 * q + c], pw[p][b], b0[c], b1[c]);
+        }
+      }
+      refill(1);
+    }
+
+    // ---- join the groups' results; then this piece is a partial or the whole
+    used += nu;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+      if (t4 == 0) s_st[warp][g + 8 * i] = RowStat{mrow[i], mo[i], l[i]};
+    }
+    __syncthreads();  // every unit buffer has been read
+    if (*(volatile int*)&s_abort) break;
+    float* s_o = reinterpret_cast<float*>(smem);
+    constexpr int V4 = D / 4, ROWSTEP = kThreads / V4;
+    // o[k][2 i + e] is channel (D/8) (2 t4 + e) + k of row g + 8 i
+    const bool whole_seg = ua == 0 && ub == sg.units;
+    const int seg = m * Hk + hk;
+    float* part = reinterpret_cast<float*>(a.ws + (((size_t)M2 * Hk * sizeof(unsigned) + 255) & ~(size_t)255));
+    auto slot = [&](int64_t cta, bool starts) { return part + (size_t)(2 * cta + (starts ? 1 : 0)) * Sh::kPartial; };
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int k = 0; k < NT; k += 4)
+          *reinterpret_cast<float4*>(s_o + ((size_t)warp * 16 + g + 8 * i) * D + NT * (2 * t4 + e) + k) =
+              make_float4(o[k][2 * i + e] * kCodeUnit<F>, o[k + 1][2 * i + e] * kCodeUnit<F>,
+                          o[k + 2][2 * i + e] * kCodeUnit<F>, o[k + 3][2 * i + e] * kCodeUnit<F>);
+    __syncthreads();
+    auto finish = [&](int r, int d0, RowStat s, float4 v) {
+      // row r's 4 channels, normalised and merged
+      if (r0 + r >= a.T * G) return;
+      const int tt = (r0 + r) / G, h = hk * G + (r0 + r) % G;
+      T* y = static_cast<T*>(a.y) + n * a.sy.n + h * a.sy.h + tt * a.sy.t + d0;
+      if (tt >= sg.cnt) {
+        st4(y, make_float4(0.f, 0.f, 0.f, 0.f));
+        return;
+      }
+      const float f = s.l > 0.f ? a.alpha / s.l * exp2f(s.mo - s.m) : 0.f;
+      v.x *= f, v.y *= f, v.z *= f, v.w *= f;
+      if (a.add) {
+        const float4 w = ld4(static_cast<const T*>(a.add) + n * a.sadd.n + h * a.sadd.h + tt * a.sadd.t + d0);
+        v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
+      }
+      st4(y, v);
+    };
+    auto join = [](RowStat& s, float4& v, RowStat b, float4 w) {
+      const float mm = fmaxf(s.m, b.m), mo2 = fmaxf(s.mo, b.mo);
+      const float fa = s.m == mm ? 1.f : exp2f(s.m - mm), fb = b.m == mm ? 1.f : exp2f(b.m - mm);
+      const float ga = s.mo == mo2 ? 1.f : exp2f(s.mo - mo2), gb = b.mo == mo2 ? 1.f : exp2f(b.mo - mo2);
+      s.l = s.l * fa + b.l * fb;
+      v.x = v.x * ga + w.x * gb, v.y = v.y * ga + w.y * gb;
+      v.z = v.z * ga + w.z * gb, v.w = v.w * ga + w.w * gb;
+      s.m = mm, s.mo = mo2;
+    };
+    const int d0 = (tid % V4) * 4;
+    for (int r = tid / V4; r < RR; r += ROWSTEP) {
+      RowStat s{-INFINITY, -INFINITY, 0.f};
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int q = 0; q < TG; ++q) {
+        const int w = q * RG + r / 16;
+        join(s, v, s_st[w][r % 16], *reinterpret_cast<const float4*>(s_o + ((size_t)w * 16 + r % 16) * D + d0));
+      }
+      if (ua == 0 && r < rows) {
+        const int h = hk * G + (r0 + r) % G;
+        for (int j = 0; j < a.M; ++j) {
+          const float z = s_zm[r * kMaxM + j];
+          join(s, v, RowStat{z, z, 1.f}, ld4(static_cast<const T*>(a.mv) + ((size_t)h * a.M + j) * D + d0));
+        }
+      }
+      if (whole_seg) {
+        finish(r, d0, s, v);
+      } else {
+        float* p = slot(blockIdx.x, ua == 0);
+        *reinterpret_cast<float4*>(p + (size_t)r * D + d0) = v;
+        if (d0 == 0)
+          *reinterpret_cast<float4*>(p + (size_t)RR * D + 4 * r) = make_float4(s.m, s.mo, s.l, 0.f);
       }
     }
+    if (!whole_seg) {
+      const int64_t c0 = head0 / share, c1 = (head0 + sg.units - 1) / share;
+      __threadfence();
+      __syncthreads();
+      if (tid == 0) s_last = atomicAdd(reinterpret_cast<unsigned*>(a.ws) + seg, 1u) == (unsigned)(c1 - c0);
+      __syncthreads();
+      if (s_last) {
+        __threadfence();
+        for (int r = tid / V4; r < RR; r += ROWSTEP) {
+          RowStat s{-INFINITY, -INFINITY, 0.f};
+          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int64_t c = c0; c <= c1; ++c) {
+            const float* p = slot(c, c * share <= head0);
+            const float4 b = __ldcg(reinterpret_cast<const float4*>(p + (size_t)RR * D + 4 * r));
+            join(s, v, RowStat{b.x, b.y, b.z}, __ldcg(reinterpret_cast<const float4*>(p + (size_t)r * D + d0)));
+          }
+          finish(r, d0, s, v);
+        }
+        if (tid == 0) reinterpret_cast<unsigned*>(a.ws)[seg] = 0u;
+      }
+    }
+    f = head0 + ub;
+    if (hk == Hk - 1 && ub == sg.units) seg0 += (int64_t)sg.units * Hk, ++m;
+    // the buffers were written with ordinary stores: order them before the next copies
+    tc::fence_proxy_async_smem();
+    __syncthreads();
   }
-  const float f = l > 0.f ? a.alpha / l : 0.f;
-  const T* add_p = a.add ? static_cast<const T*>(a.add) + n * a.sadd.n + h * a.sadd.h + t * a.sadd.t : nullptr;
-#pragma unroll
-  for (int i = 0; i < E; ++i) {
-    const int e = lane * E + i;
-    y[e] = cvt_out<T>(o[i] * f + (add_p ? ld_f(add_p + e) : 0.f));
+  if (*(volatile int*)&s_abort) {
+    if (tid == 0) raise_status(a.status, kDevTimeout);
+    // a wait gave up after a second; copies that other groups issued just before they saw
+    // the flag land well within a millisecond
+    const long long c0 = clock64();
+    while (clock64() - c0 < 4000000ll) {
+    }
   }
+  pdl_trigger();
 }
 
-template <typename T, int D, int F>
-cudaError_t launch(const CacheAttn& a, cudaStream_t s, int* launches) {
-  const int64_t rows = (int64_t)a.c.N * a.H * a.T;
+template <typename T, int D, int F, int RG>
+cudaError_t launch_split(const CacheAttn& a, cudaStream_t s, int* launches) {
+  using Sh = Shape<T, D, F, RG>;
+  const int rows = a.H / a.c.Hk * a.T, RB = (rows + Sh::RR - 1) / Sh::RR;
+  auto* kernel = split_kernel<T, D, F, RG>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem);
+  if (e != cudaSuccess) return e;
   trace_begin("cache_attn", s);
-  attn_kernel<T, D, F><<<(unsigned)((rows + kWarps - 1) / kWarps), kWarps * 32, 0, s>>>(a);
+  e = launch_pdl(kernel, dim3(std::min(ctas_per_wave(Sh::kPerSm), kMaxCtas)), dim3(kThreads), Sh::kSmem, s, a, RB, (int)Sh::TG);
   trace_end(s);
   ++*launches;
-  return cudaGetLastError();
+  return e;
+}
+
+template <typename T, int D, int F>
+cudaError_t by_rows(const CacheAttn& a, cudaStream_t s, int* launches) {
+  const int rows = a.H / a.c.Hk * a.T;
+  return rows <= 16   ? launch_split<T, D, F, 1>(a, s, launches)
+         : rows <= 32 ? launch_split<T, D, F, 2>(a, s, launches)
+         : rows <= 64 ? launch_split<T, D, F, 4>(a, s, launches)
+                      : launch_split<T, D, F, 8>(a, s, launches);
 }
 
 template <typename T, int D>
 cudaError_t by_format(const CacheAttn& a, cudaStream_t s, int* launches) {
-  return a.c.fmt == LIZARD_KV_E4M3 ? launch<T, D, 0>(a, s, launches) : launch<T, D, 1>(a, s, launches);
+  return a.c.fmt == LIZARD_KV_E4M3 ? by_rows<T, D, 0>(a, s, launches) : by_rows<T, D, 1>(a, s, launches);
 }
 
 }  // namespace
 
-size_t cache_attn_workspace(int, int, int, int, int) { return 0; }
+size_t cache_attn_workspace(int N, int Hk, int H, int T, int d) {
+  const int rows = H / Hk * T, RR = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+  const int RB = rows > 0 ? (rows + RR - 1) / RR : 1;
+  // a counter per (sequence, rows, head), then two partial results per CTA (kMaxCtas: an
+  // upper bound, so that the size does not depend on the device)
+  return align_up((size_t)N * RB * Hk * sizeof(unsigned), 256) + (size_t)2 * kMaxCtas * RR * (d + 4) * sizeof(float);
+}
 
 cudaError_t launch_cache_attn(const CacheAttn& a, lizard_dtype dt, cudaStream_t s, int* launches) {
   if (dt == LIZARD_F32)
