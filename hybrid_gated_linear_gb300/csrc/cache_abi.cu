@@ -122,7 +122,9 @@ lizard_status cache_ok(const lizard_cache* c, lz::CacheArgs* out) {
   const int P = c->page_tokens;
   if ((c->d != 64 && c->d != 128) || (P != 16 && P != 32 && P != 64 && P != 128))
     return LIZARD_ERR_UNSUPPORTED;
-  if ((__int128)c->pages * c->Hk * P * c->d > kMaxExtent || (int64_t)c->max_pages * P > (1ll << 30)) return LIZARD_ERR_INVALID_ARG;
+  if ((__int128)c->pages * c->Hk * P * c->d > kMaxExtent || 
+      (__int128)c->pages * c->Hk * P >= (1ll << 35) || (int64_t)c->max_pages * P > (1ll << 30))
+    return LIZARD_ERR_INVALID_ARG;
   *out = lz::CacheArgs{static_cast<unsigned char*>(c->k_codes), static_cast<unsigned char*>(c->v_codes),
                        c->k_scale, c->v_scale, c->table, c->N, c->max_pages, c->pages, c->Hk, P,
                        P == 16 ? 4 : P == 32 ? 5 : P == 64 ? 6 : 7, c->d, (int)c->format};

@@ -29,6 +29,10 @@ using tc::mbar_try_wait;
 
 constexpr int kThreads = 256;
 constexpr int kUnit = 32;  // tokens per unit of work
+// Starting a (sequence, head) costs a CTA about as much as this many units: the list of work
+// holds that many empty entries in front of every segment, so that CTAs with many short
+// segments get fewer units.
+constexpr int kSegCost = 12;
 constexpr int kMaxM = 16;
 constexpr int kMaxCtas = 512;  // CTAs of a launch at most (sizes the scratch)
 constexpr float kLog2e = 1.4426950408889634f;
@@ -93,6 +97,24 @@ __device__ __forceinline__ Segment segment_of(const CacheAttn& a, int m, int RB,
   return s;
 }
 
+// What a CTA works on between two merges: units ua .. ub-1 of one segment and key head.  Kept
+// in shared memory, with the position in the list: none of it is worth a register in the loop.
+struct Piece {
+  Segment s;
+  int64_t f, seg0;      // list indices: of the next piece, of segment m's first entry (head 0)
+  int64_t head0;        // of this head's first unit
+  int m, n, r0, hk, ua, ub, seg, rows;
+};
+
+// Where a unit's two 16-token blocks are (in blocks of 16 rows from the pool's start), their
+// key scales, the value scales' exponent bits (byte 0 and 1), and in bits 16 and 17 whether
+// there is anything to see.
+struct UnitMeta {
+  int at0, at1;
+  float ks0, ks1;
+  int info;
+};
+
 // One merged set of rows: maxima, sum and output of a row (unnormalised).
 struct RowStat {
   float m, mo, l;
@@ -111,7 +133,7 @@ struct Shape {
   static_assert(kBuf == 8 * 16 * D * 4, "the merge fills the unit buffers");
   static constexpr int kSmem = kBuf + RR * D * 2 * NS;
   // two CTAs per SM where their shared memory allows it
-  static constexpr int kPerSm = kSmem + RR * kMaxM * 4 + 4096 <= 113 * 1024 ? 2 : 1;
+  static constexpr int kPerSm = kSmem + RR * kMaxM * 4 + TG * 1280 + 2048 <= 113 * 1024 ? 2 : 1;
   static constexpr int kPartial = RR * (D + 4);      // floats of a partial result
 };
 
@@ -125,9 +147,10 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG>::kPerSm) split_ke
   __shared__ float s_rs[RR];                          // log2 e * scale * the query's power of two
   __shared__ float s_zm[RR * kMaxM];                  // logits of the meta tokens
   __shared__ RowStat s_st[8][16];
+  __shared__ UnitMeta s_meta[TG][2][32];  // of each group, two batches of 32 units
   __shared__ int64_t s_sum[8];
-  __shared__ int64_t s_start;
-  __shared__ int s_m, s_abort, s_last;
+  __shared__ Piece s_p;
+  __shared__ int s_abort, s_last;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t4 = lane & 3;
@@ -148,7 +171,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG>::kPerSm) split_ke
 
   // this CTA's share [f0, f1) of the list of units (sequence-major, then head, then token)
   int64_t mine = 0;
-  for (int m = tid; m < M2; m += kThreads) mine += segment_of(a, m, RB, RR, G).units;
+  for (int m = tid; m < M2; m += kThreads) mine += segment_of(a, m, RB, RR, G).units + kSegCost;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
   if (lane == 0) s_sum[warp] = mine;
@@ -159,14 +182,14 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG>::kPerSm) split_ke
   total *= Hk;
   int64_t share = (total + gridDim.x - 1) / gridDim.x;
   if (share < min_units) share = min_units;
-  int64_t f = blockIdx.x * share;
+  const int64_t f = blockIdx.x * share;
   const int64_t f1 = min(total, f + share);
   if (f >= total) return;
   {  // the segment f lies in
     int64_t before = 0;
     for (int m0 = 0; m0 < M2; m0 += kThreads) {
       const int m = m0 + tid;
-      const int64_t u = m < M2 ? (int64_t)segment_of(a, m, RB, RR, G).units * Hk : 0;
+      const int64_t u = m < M2 ? (int64_t)(segment_of(a, m, RB, RR, G).units + kSegCost) * Hk : 0;
       int64_t c = u;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -178,15 +201,12 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG>::kPerSm) split_ke
       __syncthreads();
       for (int w = 0; w < warp; ++w) c += s_sum[w];
       c += before;
-      if (f < c && f >= c - u) s_m = m, s_start = c - u;
+      if (f < c && f >= c - u) s_p.m = m, s_p.seg0 = c - u, s_p.f = f;
       for (int w = 0; w < 8; ++w) before += s_sum[w];
       if (f < before) break;
     }
     __syncthreads();
   }
-  int m = s_m;
-  int64_t seg0 = s_start;  // list index of segment m's first unit (head 0)
-
   uint32_t used = 0;  // units this warp's group has consumed, over all pieces
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     if (mbar_try_wait(bar, parity)) return true;
@@ -203,87 +223,95 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG>::kPerSm) split_ke
     }
   };
 
-  while (f < f1) {
-    const Segment sg = segment_of(a, m, RB, RR, G);
-    const int n = m / RB, r0 = (m - n * RB) * RR;
-    const int hk = (int)((f - seg0) / sg.units);
-    const int64_t head0 = seg0 + (int64_t)hk * sg.units;  // list index of this head's first unit
-    const int ua = (int)(f - head0), ub = (int)min((int64_t)sg.units, f1 - head0);
-    const int nu = ub - ua > tg ? (ub - ua - tg + TG - 1) / TG : 0;  // units of this group
+  while (true) {
+    if (tid == 0) {
+      Piece& p = s_p;
+      p.ub = 0;
+      if (p.f < f1) {
+        p.s = segment_of(a, p.m, RB, RR, G);
+        p.n = p.m / RB;
+        p.r0 = (p.m - p.n * RB) * RR;
+        const int entries = p.s.units + kSegCost;
+        p.hk = (int)((p.f - p.seg0) / entries);
+        const int64_t next = p.seg0 + (int64_t)(p.hk + 1) * entries;
+        p.head0 = next - p.s.units;
+        p.ua = (int)max((int64_t)0, p.f - p.head0);
+        // not positive: the share ends before this head's first unit
+        p.ub = (int)max((int64_t)0, min((int64_t)p.s.units, f1 - p.head0));
+        p.seg = p.m * Hk + p.hk;
+        p.rows = max(0, min(RR, p.s.cnt * G - p.r0));
+        p.f = next;
+        if (p.hk == Hk - 1) p.seg0 = next, ++p.m;
+      }
+    }
+    __syncthreads();
+    if (s_p.ub == 0) break;
+    const int n = s_p.n, hk = s_p.hk, ua = s_p.ua;
+    const int nu = s_p.ub - ua > tg ? (s_p.ub - ua - tg + TG - 1) / TG : 0;  // units of this group
 
-    // ---- pages and scales of the group's units, 32 units at a time in the lanes' registers
-    // (two 16-token blocks per unit; -1: nothing to see there)
-    int id0 = -1, id1 = -1, nid0 = -1, nid1 = -1;
-    float ks0 = 0.f, ks1 = 0.f, nks0 = 0.f, nks1 = 0.f;
-    int ve0 = 0, ve1 = 0, nve0 = 0, nve1 = 0;
+    // ---- pages and scales of the group's units, 32 units at a time
     auto load_meta = [&](int batch) {
       const int j = batch * 32 + lane;
-      nid0 = nid1 = -1;
+      UnitMeta u{0, 0, 0.f, 0.f, 0};
       if (j < nu) {
-        const int tok = (ua + tg + j * TG) * kUnit;
-        const bool in0 = tok + 15 >= sg.lo && tok <= sg.hi, in1 = tok + 31 >= sg.lo && tok + 16 <= sg.hi;
-        const uint32_t pg = (uint32_t)((sg.base + tok) >> a.c.log_p);
-        if (in0 || (in1 && a.c.P > 16)) {
-          nid0 = pool_page(a.c, n, pg);
-          if (nid0 < 0) raise_status(a.status, kDevCheck);
+        const int tok = (ua + tg + j * TG) * kUnit, lo = s_p.s.lo, hi = s_p.s.hi;
+        const bool in0 = tok + 15 >= lo && tok <= hi, in1 = tok + 31 >= lo && tok + 16 <= hi;
+        const uint32_t pg = (uint32_t)((s_p.s.base + tok) >> a.c.log_p);
+        const int row = (int)((s_p.s.base + tok) & (a.c.P - 1));
+        const bool small = a.c.P == 16;
+        int i0 = -1, i1 = -1;
+        if (in0 || (in1 && !small)) {
+          i0 = pool_page(a.c, n, pg);
+          if (i0 < 0) raise_status(a.status, kDevCheck);
         }
-        if (a.c.P > 16) {
-          nid1 = in1 ? nid0 : -1;
-          if (!in0) nid0 = -1;
-        } else if (in1) {
-          nid1 = pool_page(a.c, n, pg + 1);
-          if (nid1 < 0) raise_status(a.status, kDevCheck);
+        i1 = i0;
+        if (small && in1) {
+          i1 = pool_page(a.c, n, pg + 1);
+          if (i1 < 0) raise_status(a.status, kDevCheck);
         }
-        if (nid0 >= 0) {
-          const size_t ph = (size_t)nid0 * Hk + hk;
-          nks0 = a.c.ks[ph];
-          nve0 = (int)(__float_as_uint(a.c.vs[ph]) >> 23) - 127;
+        if (in0 && i0 >= 0) {
+          const size_t ph = (size_t)i0 * Hk + hk;
+          u.at0 = (int)((ph * a.c.P + row) >> 4);
+          u.ks0 = a.c.ks[ph];
+          u.info |= 1 << 16 | __float_as_uint(a.c.vs[ph]) >> 23;
         }
-        if (nid1 >= 0) {
-          const size_t ph = (size_t)nid1 * Hk + hk;
-          nks1 = a.c.ks[ph];
-          nve1 = (int)(__float_as_uint(a.c.vs[ph]) >> 23) - 127;
+        if (in1 && i1 >= 0) {
+          const size_t ph = (size_t)i1 * Hk + hk;
+          u.at1 = (int)((ph * a.c.P + ((row + 16) & (a.c.P - 1))) >> 4);
+          u.ks1 = a.c.ks[ph];
+          u.info |= 1 << 17 | (__float_as_uint(a.c.vs[ph]) >> 23) << 8;
         }
       }
+      s_meta[tg][batch & 1][lane] = u;
+      __syncwarp();
     };
     // Copies the keys (x = 0) or values (x = 1) of the group's unit j into its stage.
-    auto copy = [&](int x, int j, int i0, int i1) {
-      const uint32_t u = used + j;  // running number of the unit
-      const int st = tg * S + u % S;
-      unsigned char* dst = smem + (size_t)st * 2 * Sh::kHalf + x * Sh::kHalf;
-      const unsigned char* pool = x ? a.c.v : a.c.k;
-      const int tok = (ua + tg + j * TG) * kUnit;
-      const int row = (int)((sg.base + tok) & (a.c.P - 1));
-      uint64_t* bar = &s_bar[x][st];
-      const uint32_t half = Sh::kHalf / 2;
-      tc::mbar_arrive_expect_tx(bar, (i0 >= 0 ? half : 0) + (i1 >= 0 ? half : 0));
-      if (i0 >= 0)
-        tc::bulk_load(dst, pool + (((size_t)i0 * Hk + hk) * a.c.P + row) * D, i0 == i1 && a.c.P > 16 ? 2 * half : half,
-                      bar);
-      if (i1 >= 0 && !(i0 == i1 && a.c.P > 16))
-        tc::bulk_load(dst + half, pool + (((size_t)i1 * Hk + hk) * a.c.P + ((row + 16) & (a.c.P - 1))) * D, half,
-                      bar);
-    };
-    // page ids of unit j (in the current or the next batch); all lanes take part
-    auto ids_of = [&](int j, int now, int& i0, int& i1) {
-      const bool next = (j >> 5) != (now >> 5);
-      i0 = __shfl_sync(0xffffffffu, next ? nid0 : id0, j & 31);
-      i1 = __shfl_sync(0xffffffffu, next ? nid1 : id1, j & 31);
-    };
-    load_meta(0);
-    id0 = nid0, id1 = nid1, ks0 = nks0, ks1 = nks1, ve0 = nve0, ve1 = nve1;
-    load_meta(1);
-    if (rg == 0)
-      for (int j = 0; j < S && j < nu; ++j) {
-        int i0, i1;
-        ids_of(j, 0, i0, i1);
-        if (lane == 0) copy(0, j, i0, i1), copy(1, j, i0, i1);
-        __syncwarp();
+    auto copy = [&](int x, int j) {
+      if (lane == 0) {
+        const UnitMeta& u = s_meta[tg][(j >> 5) & 1][j & 31];
+        const int st = tg * S + (used + j) % S, in = u.info >> 16;
+        unsigned char* dst = smem + (size_t)st * 2 * Sh::kHalf + x * Sh::kHalf;
+        const unsigned char* pool = x ? a.c.v : a.c.k;
+        uint64_t* bar = &s_bar[x][st];
+        constexpr uint32_t half = Sh::kHalf / 2;
+        tc::mbar_arrive_expect_tx(bar, half * __popc(in));
+        if (in == 3 && u.at1 == u.at0 + 1) {
+          tc::bulk_load(dst, pool + (size_t)u.at0 * half, 2 * half, bar);
+        } else {
+          if (in & 1) tc::bulk_load(dst, pool + (size_t)u.at0 * half, half, bar);
+          if (in & 2) tc::bulk_load(dst + half, pool + (size_t)u.at1 * half, half, bar);
+        }
       }
+      __syncwarp();
+    };
+    if (rg == 0) {
+      load_meta(0);
+      for (int j = 0; j < S && j < nu; ++j) copy(0, j), copy(1, j);
+    }
 
     // ---- queries: rotated, scaled to a power of two near 2^13, in the order the MMAs read
     constexpr int LPR = D / 4, RPI = 32 / LPR;  // lanes per row, rows per iteration of a warp
-    const int rows = min(RR, sg.cnt * G - r0);  // rows with a query (may be <= 0)
+    const int rows = s_p.rows, r0 = s_p.r0;  // rows with a query
     for (int rb = warp * RPI; rb < RR; rb += 8 * RPI) {
       const int r = rb + lane / LPR, d0 = (lane % LPR) * 4;
       float x[4] = {0.f, 0.f, 0.f, 0.f};
@@ -308,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG>::kPerSm) split_ke
           if (lane % LPR == 0) s_zm[r * kMaxM + j] = z * (a.scale * kLog2e);
         }
       if (have && a.rope.turns && d0 < a.rope.rot) {
-        const int64_t p = sg.p0 + (r0 + r) / G;
+        const int64_t p = s_p.s.p0 + (r0 + r) / G;
         const int hr = a.rope.rot / 2;
         float y[4];
 #pragma unroll
@@ -356,58 +384,67 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG>::kPerSm) split_ke
     for (int i = 0; i < NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
     int lo_r[2], hi_r[2];
     float rs[2];
+    // first token a query at position p sees, relative to the segment's base
+    auto sees_from = [&](int64_t p) {
+      const int64_t lo = max(s_p.s.first, a.W > 0 ? p - a.W + 1 : (int64_t)0) - s_p.s.base;
+      return (int)max((int64_t)0, min(lo, (int64_t)0x7fffffff));
+    };
+    const bool any = s_p.s.hi >= s_p.s.lo;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int r = rg * 16 + g + 8 * i, tt = (r0 + r) / G;
+      const int r = rg * 16 + g + 8 * i;
+      const int64_t p = s_p.s.p0 + (r0 + r) / G;
       rs[i] = s_rs[r];
-      hi_r[i] = r < rows ? (int)(sg.p0 + tt - sg.base) : -1;
-      const int64_t lo = max(sg.first, a.W > 0 ? sg.p0 + tt - a.W + 1 : (int64_t)0);
-      lo_r[i] = (int)max((int64_t)0, min(lo - sg.base, (int64_t)0x7fffffff));
-      if (sg.hi < sg.lo) hi_r[i] = -1;
+      hi_r[i] = any && r < rows ? (int)(p - s_p.s.base) : -1;
+      lo_r[i] = sees_from(p);
     }
     // tokens every row of the block sees
-    const int tl = rows > 0 ? (r0 + rows - 1) / G : 0;
-    const int all_lo = (int)max((int64_t)0, max(sg.first, a.W > 0 ? sg.p0 + tl - a.W + 1 : (int64_t)0) - sg.base);
-    const int all_hi = rows > 0 ? (int)(sg.p0 + r0 / G - sg.base) : -1;
+    const int all_lo = rows > 0 ? sees_from(s_p.s.p0 + (r0 + rows - 1) / G) : 0;
+    const int all_hi = any && rows > 0 ? (int)(s_p.s.p0 + r0 / G - s_p.s.base) : -1;
     const uint4* qf = reinterpret_cast<const uint4*>(s_q) + (size_t)rg * NS * KS * 32 + lane;
 
     for (int j = 0; j < nu; ++j) {
-      if ((j & 31) == 0 && j > 0) {
-        id0 = nid0, id1 = nid1, ks0 = nks0, ks1 = nks1, ve0 = nve0, ve1 = nve1;
-        load_meta((j >> 5) + 1);
-      }
+      // the next batch replaces the last one, which no warp of the group (at most S - 1 units
+      // behind) still reads half a batch later
+      if (rg == 0 && (j & 31) == 16 && (j | 31) + 1 < nu) load_meta((j >> 5) + 1);
       const uint32_t u = used + j;
       const int st = tg * S + u % S;
       const uint32_t parity = (u / S) & 1;
       const unsigned char* kb = smem + (size_t)st * 2 * Sh::kHalf;
       const unsigned char* vb = kb + Sh::kHalf;
       const int tok = (ua + tg + j * TG) * kUnit;
-      const float kk[2] = {__shfl_sync(0xffffffffu, ks0, j & 31), __shfl_sync(0xffffffffu, ks1, j & 31)};
-      const int ve[2] = {__shfl_sync(0xffffffffu, ve0, j & 31), __shfl_sync(0xffffffffu, ve1, j & 31)};
-      const bool ok0 = __shfl_sync(0xffffffffu, id0, j & 31) >= 0, ok1 = __shfl_sync(0xffffffffu, id1, j & 31) >= 0;
-
       // logits: lane (g, t4) holds channels (D/4) t4 .. of token 8 i + g
       if (!wait(&s_bar[0][st], parity)) break;
+      const UnitMeta& um = s_meta[tg][(j >> 5) & 1][j & 31];
+      const float kk[2] = {um.ks0, um.ks1};
+      const int in = um.info;
+      const bool ok0 = in >> 16 & 1, ok1 = in >> 17 & 1;
+      const float ve[2] = {(float)((in & 0xff) - 127), (float)((in >> 8 & 0xff) - 127)};
       float z[4][4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        z[i][0] = z[i][1] = z[i][2] = z[i][3] = 0.f;
-        const int r = 8 * i + g;
-        uint32_t w[KS];
+      for (int i = 0; i < 4; i += 2) {  // two tiles of 8 tokens share the reads of the queries
+        uint32_t w[2][KS];
 #pragma unroll
-        for (int h = 0; h < KS / 4; ++h) {
-          const uint4 v = *reinterpret_cast<const uint4*>(kb + r * D + 16 * chunk_place<D>(r, KS / 4 * t4 + h));
-          w[4 * h] = v.x, w[4 * h + 1] = v.y, w[4 * h + 2] = v.z, w[4 * h + 3] = v.w;
+        for (int k = 0; k < 2; ++k) {
+          z[i + k][0] = z[i + k][1] = z[i + k][2] = z[i + k][3] = 0.f;
+          const int r = 8 * (i + k) + g;
+#pragma unroll
+          for (int h = 0; h < KS / 4; ++h) {
+            const uint4 v = *reinterpret_cast<const uint4*>(kb + r * D + 16 * chunk_place<D>(r, KS / 4 * t4 + h));
+            w[k][4 * h] = v.x, w[k][4 * h + 1] = v.y, w[k][4 * h + 2] = v.z, w[k][4 * h + 3] = v.w;
+          }
         }
 #pragma unroll
         for (int s = 0; s < KS; ++s) {
-          uint32_t b0, b1;
-          codes_to_half<F>(w[s], b0, b1);
+          uint32_t b[2][2];
+          codes_to_half<F>(w[0][s], b[0][0], b[0][1]);
+          codes_to_half<F>(w[1][s], b[1][0], b[1][1]);
 #pragma unroll
           for (int p = 0; p < NS; ++p) {
             const uint4 q = qf[(p * KS + s) * 32];
             const uint32_t qa[4] = {q.x, q.y, q.z, q.w};
-            mma16816(z[i], qa, b0, b1);
+            mma16816(z[i], qa, b[0][0], b[0][1]);
+            mma16816(z[i + 1], qa, b[1][0], b[1][1]);
           }
         }
       }
@@ -421,15 +458,12 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG>::kPerSm) split_ke
           if (lane == 0) tc::mbar_arrive(&s_bar[2 + x][st]);
         }
         if (rg == 0 && j - back + S < nu && j >= back) {
-          int i0, i1;
-          ids_of(j - back + S, j, i0, i1);
           if (RG > 1) {
             const uint32_t v = u - 1;
             if (!wait(&s_bar[2 + x][tg * S + v % S], (v / S) & 1)) return;
           }
           __syncwarp();
-          if (lane == 0) copy(x, j - back + S, i0, i1);
-          __syncwarp();
+          copy(x, j - back + S);
         }
       };
       refill(0);
@@ -442,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG>::kPerSm) split_ke
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          float v = z[i][e] * (e < 2 ? f0[i >> 1] : f8[i >> 1]) * kCodeUnit<F>;
+          float v = z[i][e] * (e < 2 ? f0[i >> 1] : f8[i >> 1]);
           if (!whole) {
             const int c = tok + 8 * i + 2 * t4 + (e & 1);
             const bool see = (i < 2 ? ok0 : ok1) && c >= lo_r[e >> 1] && c <= hi_r[e >> 1];
@@ -460,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG>::kPerSm) split_ke
           sm[i][b] = fmaxf(sm[i][b], __shfl_xor_sync(0xffffffffu, sm[i][b], 2));
         }
         mn[i] = fmaxf(mrow[i], fmaxf(sm[i][0], sm[i][1]));
-        mon[i] = fmaxf(mo[i], fmaxf(sm[i][0] + (float)ve[0], sm[i][1] + (float)ve[1]));
+        mon[i] = fmaxf(mo[i], fmaxf(sm[i][0] + ve[0], sm[i][1] + ve[1]));
       }
       const bool grew = mn[0] > mrow[0] || mn[1] > mrow[1] || mon[0] > mo[0] || mon[1] > mo[1];
       if (__any_sync(0xffffffffu, grew)) {
@@ -482,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG>::kPerSm) split_ke
 #pragma unroll
         for (int i = 0; i < 2; ++i)
 #pragma unroll
-          for (int b = 0; b < 2; ++b) sh[i][b] = mo[i] == -INFINITY ? 0.f : mo[i] - (float)ve[b];
+          for (int b = 0; b < 2; ++b) sh[i][b] = mo[i] == -INFINITY ? 0.f : mo[i] - ve[b];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           float p[4];
@@ -517,6 +551,16 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG>::kPerSm) split_ke
             w[k][0] = v.x, w[k][1] = v.y;
           }
         }
+        if (!whole) {  // what no token was written to may be NaN: 0 times it has to be 0
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int c = tok + 16 * b + 2 * t4 + (k & 1) + 8 * (k >> 1);
+            if (!((b ? ok1 : ok0) && c >= s_p.s.lo && c <= s_p.s.hi)) {
+#pragma unroll
+              for (int q = 0; q < WV; ++q) w[k][q] = 0;
+            }
+          }
+        }
 #pragma unroll
         for (int q = 0; q < WV; ++q) {
           uint32_t b0[4], b1[4];
@@ -546,8 +590,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG>::kPerSm) split_ke
     float* s_o = reinterpret_cast<float*>(smem);
     constexpr int V4 = D / 4, ROWSTEP = kThreads / V4;
     // o[k][2 i + e] is channel (D/8) (2 t4 + e) + k of row g + 8 i
-    const bool whole_seg = ua == 0 && ub == sg.units;
-    const int seg = m * Hk + hk;
+    const bool whole_seg = ua == 0 && s_p.ub == s_p.s.units;
     float* part = reinterpret_cast<float*>(a.ws + (((size_t)M2 * Hk * sizeof(unsigned) + 255) & ~(size_t)255));
     auto slot = [&](int64_t cta, bool starts) { return part + (size_t)(2 * cta + (starts ? 1 : 0)) * Sh::kPartial; };
 #pragma unroll
@@ -557,25 +600,18 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG>::kPerSm) split_ke
 #pragma unroll
         for (int k = 0; k < NT; k += 4)
           *reinterpret_cast<float4*>(s_o + ((size_t)warp * 16 + g + 8 * i) * D + NT * (2 * t4 + e) + k) =
-              make_float4(o[k][2 * i + e] * kCodeUnit<F>, o[k + 1][2 * i + e] * kCodeUnit<F>,
-                          o[k + 2][2 * i + e] * kCodeUnit<F>, o[k + 3][2 * i + e] * kCodeUnit<F>);
+              make_float4(o[k][2 * i + e], o[k + 1][2 * i + e], o[k + 2][2 * i + e], o[k + 3][2 * i + e]);
     __syncthreads();
-    auto finish = [&](int r, int d0, RowStat s, float4 v) {
+    auto finish = [&](int r, RowStat s, float4 v, int d0) {
       // row r's 4 channels, normalised and merged
-      if (r0 + r >= a.T * G) return;
       const int tt = (r0 + r) / G, h = hk * G + (r0 + r) % G;
-      T* y = static_cast<T*>(a.y) + n * a.sy.n + h * a.sy.h + tt * a.sy.t + d0;
-      if (tt >= sg.cnt) {
-        st4(y, make_float4(0.f, 0.f, 0.f, 0.f));
-        return;
-      }
       const float f = s.l > 0.f ? a.alpha / s.l * exp2f(s.mo - s.m) : 0.f;
       v.x *= f, v.y *= f, v.z *= f, v.w *= f;
       if (a.add) {
         const float4 w = ld4(static_cast<const T*>(a.add) + n * a.sadd.n + h * a.sadd.h + tt * a.sadd.t + d0);
         v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
       }
-      st4(y, v);
+      st4(static_cast<T*>(a.y) + n * a.sy.n + h * a.sy.h + tt * a.sy.t + d0, v);
     };
     auto join = [](RowStat& s, float4& v, RowStat b, float4 w) {
       const float mm = fmaxf(s.m, b.m), mo2 = fmaxf(s.mo, b.mo);
@@ -587,7 +623,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG>::kPerSm) split_ke
       s.m = mm, s.mo = mo2;
     };
     const int d0 = (tid % V4) * 4;
-    for (int r = tid / V4; r < RR; r += ROWSTEP) {
+    for (int r = tid / V4; r < rows; r += ROWSTEP) {
       RowStat s{-INFINITY, -INFINITY, 0.f};
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
@@ -595,7 +631,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG>::kPerSm) split_ke
         const int w = q * RG + r / 16;
         join(s, v, s_st[w][r % 16], *reinterpret_cast<const float4*>(s_o + ((size_t)w * 16 + r % 16) * D + d0));
       }
-      if (ua == 0 && r < rows) {
+      if (ua == 0) {
         const int h = hk * G + (r0 + r) % G;
         for (int j = 0; j < a.M; ++j) {
           const float z = s_zm[r * kMaxM + j];
@@ -603,7 +639,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG>::kPerSm) split_ke
         }
       }
       if (whole_seg) {
-        finish(r, d0, s, v);
+        finish(r, s, v, d0);
       } else {
         float* p = slot(blockIdx.x, ua == 0);
         *reinterpret_cast<float4*>(p + (size_t)r * D + d0) = v;
@@ -611,29 +647,33 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG>::kPerSm) split_ke
           *reinterpret_cast<float4*>(p + (size_t)RR * D + 4 * r) = make_float4(s.m, s.mo, s.l, 0.f);
       }
     }
+    if (ua == 0)  // queries beyond the sequence's count
+      for (int r = rows + tid / V4; r < RR && r0 + r < a.T * G; r += ROWSTEP) {
+        const int tt = (r0 + r) / G, h = hk * G + (r0 + r) % G;
+        st4(static_cast<T*>(a.y) + n * a.sy.n + h * a.sy.h + tt * a.sy.t + d0, make_float4(0.f, 0.f, 0.f, 0.f));
+      }
     if (!whole_seg) {
-      const int64_t c0 = head0 / share, c1 = (head0 + sg.units - 1) / share;
+      const int64_t c0 = s_p.head0 / share, c1 = (s_p.head0 + s_p.s.units - 1) / share;
       __threadfence();
       __syncthreads();
-      if (tid == 0) s_last = atomicAdd(reinterpret_cast<unsigned*>(a.ws) + seg, 1u) == (unsigned)(c1 - c0);
+      if (tid == 0) s_last = atomicAdd(reinterpret_cast<unsigned*>(a.ws) + s_p.seg, 1u) == (unsigned)(c1 - c0);
       __syncthreads();
       if (s_last) {
         __threadfence();
-        for (int r = tid / V4; r < RR; r += ROWSTEP) {
+        for (int r = tid / V4; r < rows; r += ROWSTEP) {
           RowStat s{-INFINITY, -INFINITY, 0.f};
           float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
           for (int64_t c = c0; c <= c1; ++c) {
-            const float* p = slot(c, c * share <= head0);
+            const float* p = slot(c, c * share <= s_p.head0);
             const float4 b = __ldcg(reinterpret_cast<const float4*>(p + (size_t)RR * D + 4 * r));
             join(s, v, RowStat{b.x, b.y, b.z}, __ldcg(reinterpret_cast<const float4*>(p + (size_t)r * D + d0)));
           }
-          finish(r, d0, s, v);
+          finish(r, s, v, d0);
         }
-        if (tid == 0) reinterpret_cast<unsigned*>(a.ws)[seg] = 0u;
+        if (tid == 0) reinterpret_cast<unsigned*>(a.ws)[s_p.seg] = 0u;
       }
     }
-    f = head0 + ub;
-    if (hk == Hk - 1 && ub == sg.units) seg0 += (int64_t)sg.units * Hk, ++m;
     // the buffers were written with ordinary stores: order them before the next copies
     tc::fence_proxy_async_smem();
     __syncthreads();
@@ -657,7 +697,7 @@ cudaError_t launch_split(const CacheAttn& a, cudaStream_t s, int* launches) {
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem);
   if (e != cudaSuccess) return e;
   trace_begin("cache_attn", s);
-  e = launch_pdl(kernel, dim3(std::min(ctas_per_wave(Sh::kPerSm), kMaxCtas)), dim3(kThreads), Sh::kSmem, s, a, RB, (int)Sh::TG);
+  e = launch_pdl(kernel, dim3(std::min(ctas_per_wave(Sh::kPerSm), kMaxCtas)), dim3(kThreads), Sh::kSmem, s, a, RB, (int)Sh::TG + kSegCost);
   trace_end(s);
   ++*launches;
   return e;

@@ -17,14 +17,14 @@ __device__ __forceinline__ int chunk_place(int r, int c) {
   return D == 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3);
 }
 
-// 2^-8 x of the four e4m3 codes of a word as two half2: sign, exponent and mantissa move to
-// the binary16 fields, whose bias is 8 larger.  Exact for every finite code, subnormals
-// included; the two NaN codes come out as +-1.875 (bytes never written are masked by the
-// callers, and need no care for being NaN).
+// The four e4m3 codes of a word as two half2 (exact; the two NaN codes, which only bytes never
+// written can hold, come out as NaN).  One conversion per pair at the rate of the integer
+// pipe; moving the fields with shifts and masks takes four operations per pair.
 __device__ __forceinline__ void e4m3x4_to_half(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  const uint32_t a = __byte_perm(w, 0, 0x1404), b = __byte_perm(w, 0, 0x3424);
-  lo = (a & 0x80008000u) | ((a >> 1) & 0x3f803f80u);
-  hi = (b & 0x80008000u) | ((b >> 1) & 0x3f803f80u);
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
 }
 
 // The four signed bytes of a word as two half2: 1024 + 128 + x is exact in binary16 with x's
@@ -39,15 +39,12 @@ __device__ __forceinline__ void i8x4_to_half(uint32_t w, uint32_t& lo, uint32_t&
   hi = *reinterpret_cast<const uint32_t*>(&y);
 }
 
-// Codes as halves: F = 0 e4m3 (times 2^-8, see kCodeUnit), 1 signed bytes.
+// Codes as halves: F = 0 e4m3, 1 signed bytes.
 template <int F>
 __device__ __forceinline__ void codes_to_half(uint32_t w, uint32_t& lo, uint32_t& hi) {
   if (F == 0) e4m3x4_to_half(w, lo, hi);
   else i8x4_to_half(w, lo, hi);
 }
-// What one unit of a converted code stands for, in units of the page's scale.
-template <int F> constexpr float kCodeUnit = F == 0 ? 256.f : 1.f;
-
 // Four codes as floats, in units of the scale.
 template <int F>
 __device__ __forceinline__ float4 codes_to_float(uint32_t w) {
@@ -55,8 +52,7 @@ __device__ __forceinline__ float4 codes_to_float(uint32_t w) {
   codes_to_half<F>(w, lo, hi);
   const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo));
   const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-  constexpr float u = kCodeUnit<F>;
-  return make_float4(a.x * u, a.y * u, b.x * u, b.y * u);
+  return make_float4(a.x, a.y, b.x, b.y);
 }
 
 // Four values (already divided by the scale) to codes, ties to even, saturating.
