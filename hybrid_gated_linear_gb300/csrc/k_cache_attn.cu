@@ -28,13 +28,14 @@ namespace {
 using tc::mbar_try_wait;
 
 constexpr int kThreads = 256;
-constexpr int kUnit = 32;  // tokens per unit of work
-// Starting a (sequence, head) costs a CTA about as much as this many units: the list of work
-// holds that many empty entries in front of every segment, so that CTAs with many short
-// segments get fewer units.
-constexpr int kSegCost = 12;
+constexpr int kUnit = 32;   // tokens per unit of work
+constexpr int kBatch = 16;  // units whose pages and scales are looked up at a time
 constexpr int kMaxM = 16;
-constexpr int kMaxCtas = 512;  // CTAs of a launch at most (sizes the scratch)
+constexpr int kMaxCtas = 304;  // CTAs of a launch at most (sizes the scratch): two per SM
+// From this many (sequence, head) pairs on, each warp works alone: starting and ending a
+// segment then stalls one warp of sixteen instead of a CTA's eight.  Below, a pair would be
+// spread over so many warps that joining their results costs more.
+constexpr int64_t kSoloSegments = 64;
 constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -106,13 +107,12 @@ struct Piece {
   int m, n, r0, hk, ua, ub, seg, rows;
 };
 
-// Where a unit's two 16-token blocks are (in blocks of 16 rows from the pool's start), their
-// key scales, the value scales' exponent bits (byte 0 and 1), and in bits 16 and 17 whether
-// there is anything to see.
+// Where a unit's two 16-token blocks are (in blocks of 16 rows from the pool's start) and, one
+// byte each, the exponent bits of their key scales and of their value scales; a key scale of
+// 0 (no valid scale is) marks a block with nothing to see.
 struct UnitMeta {
   int at0, at1;
-  float ks0, ks1;
-  int info;
+  uint32_t exps;  // key 0, key 1, value 0, value 1
 };
 
 // One merged set of rows: maxima, sum and output of a row (unnormalised).
@@ -120,45 +120,64 @@ struct RowStat {
   float m, mo, l;
 };
 
-template <typename T, int D, int F, int RG>
+// Solo: every warp works through a share of its own, without the others of its CTA.
+template <typename T, int D, int F, int RG, bool Solo>
 struct Shape {
+  static_assert(!Solo || RG == 1, "a warp has 16 rows");
   static constexpr int NS = sizeof(T) == 4 ? 2 : 1;  // parts of a query and of a probability
-  static constexpr int TG = 8 / RG;                  // warps that share out a piece's units
+  static constexpr int TG = Solo ? 1 : 8 / RG;       // groups that share out a piece's units
+  static constexpr int NG = 8 / RG;                  // groups of a CTA
   static constexpr int S = RG;                       // stages per unit group
-  static constexpr int RR = 16 * RG;                 // rows
+  static constexpr int RR = 16 * RG;                 // rows of a team
+  static constexpr int NT = Solo ? 8 : 1;            // teams of a CTA
   static constexpr int kHalf = kUnit * D;            // bytes of the keys of a unit
   // dynamic shared memory: the unit buffers, which the merge of the warps' outputs reuses
   // (8 warps x 16 rows x D floats, the same size), then the queries
-  static constexpr int kBuf = TG * S * 2 * kHalf;
+  static constexpr int kBuf = NG * S * 2 * kHalf;
   static_assert(kBuf == 8 * 16 * D * 4, "the merge fills the unit buffers");
-  static constexpr int kSmem = kBuf + RR * D * 2 * NS;
+  static constexpr int kSmem = kBuf + NT * RR * D * 2 * NS;
   // two CTAs per SM where their shared memory allows it
-  static constexpr int kPerSm = kSmem + RR * kMaxM * 4 + TG * 1280 + 2048 <= 113 * 1024 ? 2 : 1;
-  static constexpr int kPartial = RR * (D + 4);      // floats of a partial result
+  static constexpr int kPerSm =
+      kSmem + NT * RR * (kMaxM + 1) * 4 + NG * 2 * kBatch * (int)sizeof(UnitMeta) + 2560 <= 113 * 1024 ? 2 : 1;
+  // Starting a segment costs a team about as much as this many units: the list of work holds
+  // that many empty entries in front of every segment, so that teams with many short segments
+  // get fewer units.
+  static constexpr int kSegCost = Solo ? 3 : 12;
+  static constexpr int kMinShare = TG + kSegCost;
 };
 
-template <typename T, int D, int F, int RG>
-__global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG>::kPerSm) split_kernel(CacheAttn a, int RB, int min_units) {
-  using Sh = Shape<T, D, F, RG>;
-  constexpr int NS = Sh::NS, TG = Sh::TG, S = Sh::S, RR = Sh::RR, KS = D / 16, NT = D / 8;
+template <typename T, int D, int F, int RG, bool Solo>
+__global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG, Solo>::kPerSm)
+    split_kernel(CacheAttn a, int RB, int prow) {
+  using Sh = Shape<T, D, F, RG, Solo>;
+  constexpr int NS = Sh::NS, TG = Sh::TG, S = Sh::S, RR = Sh::RR, KS = D / 16, NT = D / 8, NG = Sh::NG;
+  constexpr int kSegCost = Sh::kSegCost, kTeams = Sh::NT, kTeam = Solo ? 32 : kThreads;
   extern __shared__ __align__(128) unsigned char smem[];
-  unsigned char* s_q = smem + Sh::kBuf;
-  __shared__ __align__(8) uint64_t s_bar[4][TG * S];  // keys full, values full, keys free, values free
-  __shared__ float s_rs[RR];                          // log2 e * scale * the query's power of two
-  __shared__ float s_zm[RR * kMaxM];                  // logits of the meta tokens
+  __shared__ __align__(8) uint64_t s_bar[4][NG * S];  // keys full, values full, keys free, values free
+  __shared__ float s_rs_all[kTeams][RR];              // log2 e * scale * the query's power of two
+  __shared__ float s_zm_all[kTeams][RR * kMaxM];      // logits of the meta tokens
   __shared__ RowStat s_st[8][16];
-  __shared__ UnitMeta s_meta[TG][2][32];  // of each group, two batches of 32 units
+  __shared__ UnitMeta s_meta[NG][2][kBatch];  // of each group, two batches
   __shared__ int64_t s_sum[8];
-  __shared__ Piece s_p;
+  __shared__ Piece s_pieces[kTeams];
   __shared__ int s_abort, s_last;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t4 = lane & 3;
-  const int rg = warp % RG, tg = warp / RG;
+  const int rg = warp % RG, group = warp / RG, tg = Solo ? 0 : group;
+  // the team (the CTA, or this warp): its threads, its memory, its barrier
+  const int team = Solo ? warp : 0, tt_id = Solo ? lane : tid;
+  unsigned char* s_q = smem + Sh::kBuf + (size_t)team * RR * D * 2 * NS;
+  float *s_rs = s_rs_all[team], *s_zm = s_zm_all[team];
+  Piece& s_p = s_pieces[team];
+  auto team_sync = [] {
+    if (Solo) __syncwarp();
+    else __syncthreads();
+  };
   const int G = a.H / a.c.Hk, Hk = a.c.Hk, M2 = a.c.N * RB;
 
   if (tid == 0) {
-    for (int i = 0; i < TG * S; ++i) {
+    for (int i = 0; i < NG * S; ++i) {
       tc::mbar_init(&s_bar[0][i], 1);
       tc::mbar_init(&s_bar[1][i], 1);
       tc::mbar_init(&s_bar[2][i], RG);
@@ -169,7 +188,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG>::kPerSm) split_ke
   }
   pdl_wait();
 
-  // this CTA's share [f0, f1) of the list of units (sequence-major, then head, then token)
+  // this team's share [f, f1) of the list of units (sequence-major, then head, then token)
   int64_t mine = 0;
   for (int m = tid; m < M2; m += kThreads) mine += segment_of(a, m, RB, RR, G).units + kSegCost;
 #pragma unroll
@@ -180,12 +199,15 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG>::kPerSm) split_ke
 #pragma unroll
   for (int w = 0; w < 8; ++w) total += s_sum[w];
   total *= Hk;
-  int64_t share = (total + gridDim.x - 1) / gridDim.x;
-  if (share < min_units) share = min_units;
-  const int64_t f = blockIdx.x * share;
-  const int64_t f1 = min(total, f + share);
-  if (f >= total) return;
-  {  // the segment f lies in
+  const int workers = gridDim.x * kTeams;
+  int64_t share = (total + workers - 1) / workers;
+  if (share < Sh::kMinShare) share = Sh::kMinShare;
+  const int64_t worker = (int64_t)blockIdx.x * kTeams + team;
+  const int64_t f1 = min(total, (worker + 1) * share);
+  const int64_t cta_f = (int64_t)blockIdx.x * kTeams * share;  // the first team's share
+  if (cta_f >= total) return;
+  {  // the segments that the teams' shares start in
+    if (tid < kTeams) s_pieces[tid].f = total;
     int64_t before = 0;
     for (int m0 = 0; m0 < M2; m0 += kThreads) {
       const int m = m0 + tid;
@@ -201,9 +223,12 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG>::kPerSm) split_ke
       __syncthreads();
       for (int w = 0; w < warp; ++w) c += s_sum[w];
       c += before;
-      if (f < c && f >= c - u) s_p.m = m, s_p.seg0 = c - u, s_p.f = f;
+      for (int w = 0; w < kTeams; ++w) {
+        const int64_t f = cta_f + w * share;
+        if (f < c && f >= c - u) s_pieces[w].m = m, s_pieces[w].seg0 = c - u, s_pieces[w].f = f;
+      }
       for (int w = 0; w < 8; ++w) before += s_sum[w];
-      if (f < before) break;
+      if (cta_f + (kTeams - 1) * share < before) break;
     }
     __syncthreads();
   }
@@ -224,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG>::kPerSm) split_ke
   };
 
   while (true) {
-    if (tid == 0) {
+    if (tt_id == 0) {
       Piece& p = s_p;
       p.ub = 0;
       if (p.f < f1) {
@@ -244,16 +269,16 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG>::kPerSm) split_ke
         if (p.hk == Hk - 1) p.seg0 = next, ++p.m;
       }
     }
-    __syncthreads();
+    team_sync();
     if (s_p.ub == 0) break;
     const int n = s_p.n, hk = s_p.hk, ua = s_p.ua;
     const int nu = s_p.ub - ua > tg ? (s_p.ub - ua - tg + TG - 1) / TG : 0;  // units of this group
 
-    // ---- pages and scales of the group's units, 32 units at a time
+    // ---- pages and scales of the group's units, a batch at a time
     auto load_meta = [&](int batch) {
-      const int j = batch * 32 + lane;
-      UnitMeta u{0, 0, 0.f, 0.f, 0};
-      if (j < nu) {
+      const int j = batch * kBatch + lane;
+      UnitMeta u{0, 0, 0};
+      if (lane < kBatch && j < nu) {
         const int tok = (ua + tg + j * TG) * kUnit, lo = s_p.s.lo, hi = s_p.s.hi;
         const bool in0 = tok + 15 >= lo && tok <= hi, in1 = tok + 31 >= lo && tok + 16 <= hi;
         const uint32_t pg = (uint32_t)((s_p.s.base + tok) >> a.c.log_p);
@@ -272,34 +297,33 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG>::kPerSm) split_ke
         if (in0 && i0 >= 0) {
           const size_t ph = (size_t)i0 * Hk + hk;
           u.at0 = (int)((ph * a.c.P + row) >> 4);
-          u.ks0 = a.c.ks[ph];
-          u.info |= 1 << 16 | __float_as_uint(a.c.vs[ph]) >> 23;
+          u.exps |= (__float_as_uint(a.c.ks[ph]) >> 23 & 0xff) | (__float_as_uint(a.c.vs[ph]) >> 23 & 0xff) << 16;
         }
         if (in1 && i1 >= 0) {
           const size_t ph = (size_t)i1 * Hk + hk;
           u.at1 = (int)((ph * a.c.P + ((row + 16) & (a.c.P - 1))) >> 4);
-          u.ks1 = a.c.ks[ph];
-          u.info |= 1 << 17 | (__float_as_uint(a.c.vs[ph]) >> 23) << 8;
+          u.exps |= (__float_as_uint(a.c.ks[ph]) >> 23 & 0xff) << 8 | (__float_as_uint(a.c.vs[ph]) >> 23 & 0xff) << 24;
         }
       }
-      s_meta[tg][batch & 1][lane] = u;
+      if (lane < kBatch) s_meta[group][batch & 1][lane] = u;
       __syncwarp();
     };
     // Copies the keys (x = 0) or values (x = 1) of the group's unit j into its stage.
     auto copy = [&](int x, int j) {
       if (lane == 0) {
-        const UnitMeta& u = s_meta[tg][(j >> 5) & 1][j & 31];
-        const int st = tg * S + (used + j) % S, in = u.info >> 16;
+        const UnitMeta& u = s_meta[group][(j / kBatch) & 1][j % kBatch];
+        const int st = group * S + (used + j) % S;
+        const bool in0 = u.exps & 0xff, in1 = u.exps & 0xff00;
         unsigned char* dst = smem + (size_t)st * 2 * Sh::kHalf + x * Sh::kHalf;
         const unsigned char* pool = x ? a.c.v : a.c.k;
         uint64_t* bar = &s_bar[x][st];
         constexpr uint32_t half = Sh::kHalf / 2;
-        tc::mbar_arrive_expect_tx(bar, half * __popc(in));
-        if (in == 3 && u.at1 == u.at0 + 1) {
+        tc::mbar_arrive_expect_tx(bar, half * ((in0 ? 1 : 0) + (in1 ? 1 : 0)));
+        if (in0 && in1 && u.at1 == u.at0 + 1) {
           tc::bulk_load(dst, pool + (size_t)u.at0 * half, 2 * half, bar);
         } else {
-          if (in & 1) tc::bulk_load(dst, pool + (size_t)u.at0 * half, half, bar);
-          if (in & 2) tc::bulk_load(dst + half, pool + (size_t)u.at1 * half, half, bar);
+          if (in0) tc::bulk_load(dst, pool + (size_t)u.at0 * half, half, bar);
+          if (in1) tc::bulk_load(dst + half, pool + (size_t)u.at1 * half, half, bar);
         }
       }
       __syncwarp();
@@ -312,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG>::kPerSm) split_ke
     // ---- queries: rotated, scaled to a power of two near 2^13, in the order the MMAs read
     constexpr int LPR = D / 4, RPI = 32 / LPR;  // lanes per row, rows per iteration of a warp
     const int rows = s_p.rows, r0 = s_p.r0;  // rows with a query
-    for (int rb = warp * RPI; rb < RR; rb += 8 * RPI) {
+    for (int rb = (Solo ? 0 : warp) * RPI; rb < RR; rb += (Solo ? 1 : 8) * RPI) {
       const int r = rb + lane / LPR, d0 = (lane % LPR) * 4;
       float x[4] = {0.f, 0.f, 0.f, 0.f};
       const bool have = r < rows;
@@ -376,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG>::kPerSm) split_ke
         dst[KS * 128 + 2] = half2_rest(x[2], x[3], w1);
       }
     }
-    __syncthreads();
+    team_sync();
 
     // ---- this warp's rows g and g + 8
     float o[NT][4], mrow[2] = {-INFINITY, -INFINITY}, mo[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
@@ -406,20 +430,20 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG>::kPerSm) split_ke
     for (int j = 0; j < nu; ++j) {
       // the next batch replaces the last one, which no warp of the group (at most S - 1 units
       // behind) still reads half a batch later
-      if (rg == 0 && (j & 31) == 16 && (j | 31) + 1 < nu) load_meta((j >> 5) + 1);
+      if (rg == 0 && j % kBatch == kBatch / 2 && (j | (kBatch - 1)) + 1 < nu) load_meta(j / kBatch + 1);
       const uint32_t u = used + j;
-      const int st = tg * S + u % S;
+      const int st = group * S + u % S;
       const uint32_t parity = (u / S) & 1;
       const unsigned char* kb = smem + (size_t)st * 2 * Sh::kHalf;
       const unsigned char* vb = kb + Sh::kHalf;
       const int tok = (ua + tg + j * TG) * kUnit;
       // logits: lane (g, t4) holds channels (D/4) t4 .. of token 8 i + g
       if (!wait(&s_bar[0][st], parity)) break;
-      const UnitMeta& um = s_meta[tg][(j >> 5) & 1][j & 31];
-      const float kk[2] = {um.ks0, um.ks1};
-      const int in = um.info;
-      const bool ok0 = in >> 16 & 1, ok1 = in >> 17 & 1;
-      const float ve[2] = {(float)((in & 0xff) - 127), (float)((in >> 8 & 0xff) - 127)};
+      const UnitMeta& um = s_meta[group][(j / kBatch) & 1][j % kBatch];
+      const uint32_t ex = um.exps;
+      const float kk[2] = {__uint_as_float((ex & 0xff) << 23), __uint_as_float((ex >> 8 & 0xff) << 23)};
+      const bool ok0 = ex & 0xff, ok1 = ex & 0xff00;
+      const float ve[2] = {(float)((int)(ex >> 16 & 0xff) - 127), (float)((int)(ex >> 24) - 127)};
       float z[4][4];
 #pragma unroll
       for (int i = 0; i < 4; i += 2) {  // two tiles of 8 tokens share the reads of the queries
@@ -460,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG>::kPerSm) split_ke
         if (rg == 0 && j - back + S < nu && j >= back) {
           if (RG > 1) {
             const uint32_t v = u - 1;
-            if (!wait(&s_bar[2 + x][tg * S + v % S], (v / S) & 1)) return;
+            if (!wait(&s_bar[2 + x][group * S + v % S], (v / S) & 1)) return;
           }
           __syncwarp();
           copy(x, j - back + S);
@@ -585,14 +609,14 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG>::kPerSm) split_ke
       l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
       if (t4 == 0) s_st[warp][g + 8 * i] = RowStat{mrow[i], mo[i], l[i]};
     }
-    __syncthreads();  // every unit buffer has been read
+    team_sync();  // every unit buffer has been read
     if (*(volatile int*)&s_abort) break;
     float* s_o = reinterpret_cast<float*>(smem);
-    constexpr int V4 = D / 4, ROWSTEP = kThreads / V4;
+    constexpr int V4 = D / 4, ROWSTEP = kTeam / V4;
     // o[k][2 i + e] is channel (D/8) (2 t4 + e) + k of row g + 8 i
     const bool whole_seg = ua == 0 && s_p.ub == s_p.s.units;
     float* part = reinterpret_cast<float*>(a.ws + (((size_t)M2 * Hk * sizeof(unsigned) + 255) & ~(size_t)255));
-    auto slot = [&](int64_t cta, bool starts) { return part + (size_t)(2 * cta + (starts ? 1 : 0)) * Sh::kPartial; };
+    auto slot = [&](int64_t w, bool starts) { return part + (size_t)(2 * w + (starts ? 1 : 0)) * prow * (D + 4); };
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -601,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG>::kPerSm) split_ke
         for (int k = 0; k < NT; k += 4)
           *reinterpret_cast<float4*>(s_o + ((size_t)warp * 16 + g + 8 * i) * D + NT * (2 * t4 + e) + k) =
               make_float4(o[k][2 * i + e], o[k + 1][2 * i + e], o[k + 2][2 * i + e], o[k + 3][2 * i + e]);
-    __syncthreads();
+    team_sync();
     auto finish = [&](int r, RowStat s, float4 v, int d0) {
       // row r's 4 channels, normalised and merged
       const int tt = (r0 + r) / G, h = hk * G + (r0 + r) % G;
@@ -622,13 +646,13 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG>::kPerSm) split_ke
       v.z = v.z * ga + w.z * gb, v.w = v.w * ga + w.w * gb;
       s.m = mm, s.mo = mo2;
     };
-    const int d0 = (tid % V4) * 4;
-    for (int r = tid / V4; r < rows; r += ROWSTEP) {
+    const int d0 = (tt_id % V4) * 4;
+    for (int r = tt_id / V4; r < rows; r += ROWSTEP) {
       RowStat s{-INFINITY, -INFINITY, 0.f};
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int q = 0; q < TG; ++q) {
-        const int w = q * RG + r / 16;
+        const int w = Solo ? warp : q * RG + r / 16;
         join(s, v, s_st[w][r % 16], *reinterpret_cast<const float4*>(s_o + ((size_t)w * 16 + r % 16) * D + d0));
       }
       if (ua == 0) {
@@ -641,42 +665,79 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG>::kPerSm) split_ke
       if (whole_seg) {
         finish(r, s, v, d0);
       } else {
-        float* p = slot(blockIdx.x, ua == 0);
+        float* p = slot(worker, ua == 0);
         *reinterpret_cast<float4*>(p + (size_t)r * D + d0) = v;
         if (d0 == 0)
-          *reinterpret_cast<float4*>(p + (size_t)RR * D + 4 * r) = make_float4(s.m, s.mo, s.l, 0.f);
+          *reinterpret_cast<float4*>(p + (size_t)prow * D + 4 * r) = make_float4(s.m, s.mo, s.l, 0.f);
       }
     }
     if (ua == 0)  // queries beyond the sequence's count
-      for (int r = rows + tid / V4; r < RR && r0 + r < a.T * G; r += ROWSTEP) {
+      for (int r = rows + tt_id / V4; r < RR && r0 + r < a.T * G; r += ROWSTEP) {
         const int tt = (r0 + r) / G, h = hk * G + (r0 + r) % G;
         st4(static_cast<T*>(a.y) + n * a.sy.n + h * a.sy.h + tt * a.sy.t + d0, make_float4(0.f, 0.f, 0.f, 0.f));
       }
     if (!whole_seg) {
       const int64_t c0 = s_p.head0 / share, c1 = (s_p.head0 + s_p.s.units - 1) / share;
       __threadfence();
-      __syncthreads();
-      if (tid == 0) s_last = atomicAdd(reinterpret_cast<unsigned*>(a.ws) + s_p.seg, 1u) == (unsigned)(c1 - c0);
-      __syncthreads();
-      if (s_last) {
+      team_sync();
+      int last = 0;
+      if (tt_id == 0)
+        last = atomicAdd(reinterpret_cast<unsigned*>(a.ws) + s_p.seg, 1u) == (unsigned)(c1 - c0);
+      if (Solo) {
+        last = __shfl_sync(0xffffffffu, last, 0);
+      } else {
+        if (tid == 0) s_last = last;
+        __syncthreads();
+        last = s_last;
+      }
+      if (last) {
+        // the V4 lanes of a row read the statistics of V4 partials at a time, turn them into
+        // weights, and then add the outputs with independent loads
         __threadfence();
-        for (int r = tid / V4; r < rows; r += ROWSTEP) {
+        const int k = tt_id % V4;
+        for (int rb = 0; rb < rows; rb += ROWSTEP) {
+          const int r = rb + tt_id / V4;
           RowStat s{-INFINITY, -INFINITY, 0.f};
           float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-          for (int64_t c = c0; c <= c1; ++c) {
-            const float* p = slot(c, c * share <= s_p.head0);
-            const float4 b = __ldcg(reinterpret_cast<const float4*>(p + (size_t)RR * D + 4 * r));
-            join(s, v, RowStat{b.x, b.y, b.z}, __ldcg(reinterpret_cast<const float4*>(p + (size_t)r * D + d0)));
+          for (int64_t cb = c0; cb <= c1; cb += V4) {
+            float4 b = make_float4(-INFINITY, -INFINITY, 0.f, 0.f);
+            if (r < rows && cb + k <= c1)
+              b = __ldcg(reinterpret_cast<const float4*>(slot(cb + k, (cb + k) * share <= s_p.head0) +
+                                                         (size_t)prow * D + 4 * r));
+            float mm = b.x, mw = b.y;
+#pragma unroll
+            for (int o = V4 / 2; o > 0; o >>= 1) {
+              mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
+              mw = fmaxf(mw, __shfl_xor_sync(0xffffffffu, mw, o));
+            }
+            mm = fmaxf(mm, s.m), mw = fmaxf(mw, s.mo);
+            const float fs = s.m == mm ? 1.f : exp2f(s.m - mm), fv = s.mo == mw ? 1.f : exp2f(s.mo - mw);
+            float ls = b.x == -INFINITY ? 0.f : b.z * exp2f(b.x - mm);
+            const float wk = b.y == -INFINITY ? 0.f : exp2f(b.y - mw);
+#pragma unroll
+            for (int o = V4 / 2; o > 0; o >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o);
+            s = RowStat{mm, mw, s.l * fs + ls};
+            v.x *= fv, v.y *= fv, v.z *= fv, v.w *= fv;
+            const int cn = (int)min((int64_t)V4, c1 - cb + 1);
+#pragma unroll 8
+            for (int i = 0; i < cn; ++i) {
+              const float w = __shfl_sync(0xffffffffu, wk, i, V4);
+              if (r < rows) {
+                const float4 x = __ldcg(reinterpret_cast<const float4*>(
+                    slot(cb + i, i == 0 && cb * share <= s_p.head0) + (size_t)r * D + d0));
+                v.x = fmaf(w, x.x, v.x), v.y = fmaf(w, x.y, v.y);
+                v.z = fmaf(w, x.z, v.z), v.w = fmaf(w, x.w, v.w);
+              }
+            }
           }
-          finish(r, s, v, d0);
+          if (r < rows) finish(r, s, v, d0);
         }
-        if (tid == 0) reinterpret_cast<unsigned*>(a.ws)[s_p.seg] = 0u;
+        if (tt_id == 0) reinterpret_cast<unsigned*>(a.ws)[s_p.seg] = 0u;
       }
     }
     // the buffers were written with ordinary stores: order them before the next copies
     tc::fence_proxy_async_smem();
-    __syncthreads();
+    team_sync();
   }
   if (*(volatile int*)&s_abort) {
     if (tid == 0) raise_status(a.status, kDevTimeout);
@@ -689,27 +750,35 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG>::kPerSm) split_ke
   pdl_trigger();
 }
 
-template <typename T, int D, int F, int RG>
+template <typename T, int D, int F, int RG, bool Solo>
 cudaError_t launch_split(const CacheAttn& a, cudaStream_t s, int* launches) {
-  using Sh = Shape<T, D, F, RG>;
+  using Sh = Shape<T, D, F, RG, Solo>;
   const int rows = a.H / a.c.Hk * a.T, RB = (rows + Sh::RR - 1) / Sh::RR;
-  auto* kernel = split_kernel<T, D, F, RG>;
+  auto* kernel = split_kernel<T, D, F, RG, Solo>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem);
   if (e != cudaSuccess) return e;
   trace_begin("cache_attn", s);
-  e = launch_pdl(kernel, dim3(std::min(ctas_per_wave(Sh::kPerSm), kMaxCtas)), dim3(kThreads), Sh::kSmem, s, a, RB, (int)Sh::TG + kSegCost);
+  e = launch_pdl(kernel, dim3(std::min(ctas_per_wave(Sh::kPerSm), kMaxCtas)), dim3(kThreads), Sh::kSmem, s, a, RB,
+                 std::min(rows, Sh::RR));
   trace_end(s);
   ++*launches;
   return e;
 }
 
+// Rows of a team, and whether the teams are single warps.
+int team_rows(int rows) { return rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
+bool solo_warps(int N, int Hk, int rows) { return rows <= 16 && (int64_t)N * Hk >= kSoloSegments; }
+
 template <typename T, int D, int F>
 cudaError_t by_rows(const CacheAttn& a, cudaStream_t s, int* launches) {
   const int rows = a.H / a.c.Hk * a.T;
-  return rows <= 16   ? launch_split<T, D, F, 1>(a, s, launches)
-         : rows <= 32 ? launch_split<T, D, F, 2>(a, s, launches)
-         : rows <= 64 ? launch_split<T, D, F, 4>(a, s, launches)
-                      : launch_split<T, D, F, 8>(a, s, launches);
+  if (solo_warps(a.c.N, a.c.Hk, rows)) return launch_split<T, D, F, 1, true>(a, s, launches);
+  switch (team_rows(rows)) {
+    case 16: return launch_split<T, D, F, 1, false>(a, s, launches);
+    case 32: return launch_split<T, D, F, 2, false>(a, s, launches);
+    case 64: return launch_split<T, D, F, 4, false>(a, s, launches);
+  }
+  return launch_split<T, D, F, 8, false>(a, s, launches);
 }
 
 template <typename T, int D>
@@ -720,11 +789,11 @@ cudaError_t by_format(const CacheAttn& a, cudaStream_t s, int* launches) {
 }  // namespace
 
 size_t cache_attn_workspace(int N, int Hk, int H, int T, int d) {
-  const int rows = H / Hk * T, RR = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
-  const int RB = rows > 0 ? (rows + RR - 1) / RR : 1;
-  // a counter per (sequence, rows, head), then two partial results per CTA (kMaxCtas: an
-  // upper bound, so that the size does not depend on the device)
-  return align_up((size_t)N * RB * Hk * sizeof(unsigned), 256) + (size_t)2 * kMaxCtas * RR * (d + 4) * sizeof(float);
+  const int rows = H / Hk * T, RR = team_rows(rows), RB = rows > 0 ? (rows + RR - 1) / RR : 1;
+  const int teams = kMaxCtas * (solo_warps(N, Hk, rows) ? 8 : 1);
+  // a counter per (sequence, rows, head), then two partial results per team
+  return align_up((size_t)N * RB * Hk * sizeof(unsigned), 256) +
+         (size_t)2 * teams * std::min(rows, RR) * (d + 4) * sizeof(float);
 }
 
 cudaError_t launch_cache_attn(const CacheAttn& a, lizard_dtype dt, cudaStream_t s, int* launches) {
