@@ -35,7 +35,7 @@ constexpr int kMaxCtas = 304;  // CTAs of a launch at most (sizes the scratch): 
 // From this many (sequence, head) pairs on, each warp works alone: starting and ending a
 // segment then stalls one warp of sixteen instead of a CTA's eight.  Below, a pair would be
 // spread over so many warps that joining their results costs more.
-constexpr int64_t kSoloSegments = 64;
+constexpr int64_t kSoloSegments = 128;
 constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -103,8 +103,8 @@ __device__ __forceinline__ Segment segment_of(const CacheAttn& a, int m, int RB,
 struct Piece {
   Segment s;
   int64_t f, seg0;      // list indices: of the next piece, of segment m's first entry (head 0)
-  int64_t head0;        // of this head's first unit
   int m, n, r0, hk, ua, ub, seg, rows;
+  int c0, c1;           // the teams that share the segment and head
 };
 
 // Where a unit's two 16-token blocks are (in blocks of 16 rows from the pool's start) and, one
@@ -143,7 +143,7 @@ struct Shape {
   // that many empty entries in front of every segment, so that teams with many short segments
   // get fewer units.
   static constexpr int kSegCost = Solo ? 3 : 12;
-  static constexpr int kMinShare = TG + kSegCost;
+  static constexpr int kMinUnits = 4 * TG;  // of a piece, where a segment has them
 };
 
 template <typename T, int D, int F, int RG, bool Solo>
@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG, Solo>::kPerSm)
     if (Solo) __syncwarp();
     else __syncthreads();
   };
-  const int G = a.H / a.c.Hk, Hk = a.c.Hk, M2 = a.c.N * RB;
+  const int G = a.H / a.c.Hk, Hk = a.c.Hk;
 
   if (tid == 0) {
     for (int i = 0; i < NG * S; ++i) {
@@ -188,31 +188,43 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG, Solo>::kPerSm)
   }
   pdl_wait();
 
-  // this team's share [f, f1) of the list of units (sequence-major, then head, then token)
-  int64_t mine = 0;
-  for (int m = tid; m < M2; m += kThreads) mine += segment_of(a, m, RB, RR, G).units + kSegCost;
+  // How the units are shared out.  With few segments for the teams there are, every segment is
+  // cut into ceil(units / U) equal pieces, U such that the pieces are at most as many as the
+  // teams; else the list of all units (sequence-major, then head, then token, kSegCost empty
+  // entries in front of each segment) is cut into equal shares, whatever segments they cross.
+  const int M2 = a.c.N * RB;
+  const int workers = gridDim.x * kTeams, worker = blockIdx.x * kTeams + team;
+  const bool pieces = (int64_t)M2 * Hk * 8 <= workers;
+  int64_t U = 0, share = 1, f1, total;
+  {
+    const int mine = tid < M2 ? segment_of(a, tid, RB, RR, G).units : 0;
+    int64_t c = mine;
+    for (int m = tid + kThreads; m < M2; m += kThreads) c += segment_of(a, m, RB, RR, G).units;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
-  if (lane == 0) s_sum[warp] = mine;
-  __syncthreads();
-  int64_t total = 0;
+    for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
+    if (lane == 0) s_sum[warp] = c;
+    if (tid < kTeams) s_pieces[tid].m = -1;
+    __syncthreads();
+    int64_t units = 0;
 #pragma unroll
-  for (int w = 0; w < 8; ++w) total += s_sum[w];
-  total *= Hk;
-  const int workers = gridDim.x * kTeams;
-  int64_t share = (total + workers - 1) / workers;
-  if (share < Sh::kMinShare) share = Sh::kMinShare;
-  const int64_t worker = (int64_t)blockIdx.x * kTeams + team;
-  const int64_t f1 = min(total, (worker + 1) * share);
-  const int64_t cta_f = (int64_t)blockIdx.x * kTeams * share;  // the first team's share
-  if (cta_f >= total) return;
-  {  // the segments that the teams' shares start in
-    if (tid < kTeams) s_pieces[tid].f = total;
+    for (int w = 0; w < 8; ++w) units += s_sum[w];
+    units *= Hk;
+    if (pieces) {
+      U = max((units + workers - M2 * Hk - 1) / (workers - M2 * Hk), (int64_t)Sh::kMinUnits);
+    } else {
+      total = units + (int64_t)M2 * Hk * kSegCost;
+      share = max((total + workers - 1) / workers, (int64_t)(Sh::kMinUnits + kSegCost));
+    }
+    const int64_t cta_f = (int64_t)blockIdx.x * kTeams * share;  // where the first team starts
     int64_t before = 0;
     for (int m0 = 0; m0 < M2; m0 += kThreads) {
       const int m = m0 + tid;
-      const int64_t u = m < M2 ? (int64_t)(segment_of(a, m, RB, RR, G).units + kSegCost) * Hk : 0;
-      int64_t c = u;
+      int64_t u = 0;
+      if (m < M2) {
+        const int n_u = m0 == 0 ? mine : segment_of(a, m, RB, RR, G).units;
+        u = (pieces ? (n_u + U - 1) / U : (int64_t)n_u + kSegCost) * Hk;
+      }
+      c = u;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int64_t x = __shfl_up_sync(0xffffffffu, c, o);
@@ -231,6 +243,8 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG, Solo>::kPerSm)
       if (cta_f + (kTeams - 1) * share < before) break;
     }
     __syncthreads();
+    f1 = (worker + 1) * share;
+    if (!pieces) f1 = min(f1, total);
   }
   uint32_t used = 0;  // units this warp's group has consumed, over all pieces
   auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -252,21 +266,33 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG, Solo>::kPerSm)
     if (tt_id == 0) {
       Piece& p = s_p;
       p.ub = 0;
-      if (p.f < f1) {
+      if (p.m >= 0 && p.f < f1) {
         p.s = segment_of(a, p.m, RB, RR, G);
         p.n = p.m / RB;
         p.r0 = (p.m - p.n * RB) * RR;
-        const int entries = p.s.units + kSegCost;
-        p.hk = (int)((p.f - p.seg0) / entries);
-        const int64_t next = p.seg0 + (int64_t)(p.hk + 1) * entries;
-        p.head0 = next - p.s.units;
-        p.ua = (int)max((int64_t)0, p.f - p.head0);
-        // not positive: the share ends before this head's first unit
-        p.ub = (int)max((int64_t)0, min((int64_t)p.s.units, f1 - p.head0));
-        p.seg = p.m * Hk + p.hk;
         p.rows = max(0, min(RR, p.s.cnt * G - p.r0));
-        p.f = next;
-        if (p.hk == Hk - 1) p.seg0 = next, ++p.m;
+        if (pieces) {
+          const int k = (int)((p.s.units + U - 1) / U), i = (int)(p.f - p.seg0);
+          p.hk = i / k;
+          p.ua = (int)((int64_t)p.s.units * (i - p.hk * k) / k);
+          p.ub = (int)((int64_t)p.s.units * (i - p.hk * k + 1) / k);
+          p.c0 = (int)p.seg0 + p.hk * k;
+          p.c1 = p.c0 + k - 1;
+          p.f = f1;
+        } else {
+          const int entries = p.s.units + kSegCost;
+          p.hk = (int)((p.f - p.seg0) / entries);
+          const int64_t next = p.seg0 + (int64_t)(p.hk + 1) * entries;
+          const int64_t head0 = next - p.s.units;  // this head's first unit
+          p.ua = (int)max((int64_t)0, p.f - head0);
+          // 0: the share ends before this head's first unit
+          p.ub = (int)max((int64_t)0, min((int64_t)p.s.units, f1 - head0));
+          p.c0 = (int)(head0 / share);
+          p.c1 = (int)((next - 1) / share);
+          p.f = next;
+        }
+        p.seg = p.m * Hk + p.hk;
+        if (p.hk == Hk - 1) p.seg0 = p.f, ++p.m;
       }
     }
     team_sync();
@@ -335,69 +361,108 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG, Solo>::kPerSm)
 
     // ---- queries: rotated, scaled to a power of two near 2^13, in the order the MMAs read
     constexpr int LPR = D / 4, RPI = 32 / LPR;  // lanes per row, rows per iteration of a warp
+    constexpr int WARPS = Solo ? 1 : 8;
     const int rows = s_p.rows, r0 = s_p.r0;  // rows with a query
-    for (int rb = (Solo ? 0 : warp) * RPI; rb < RR; rb += (Solo ? 1 : 8) * RPI) {
-      const int r = rb + lane / LPR, d0 = (lane % LPR) * 4;
-      float x[4] = {0.f, 0.f, 0.f, 0.f};
-      const bool have = r < rows;
-      const T* qp = nullptr;
-      if (have) {
-        const int tt = (r0 + r) / G, h = hk * G + (r0 + r) % G;
-        qp = static_cast<const T*>(a.q) + n * a.sq.n + h * a.sq.h + tt * a.sq.t;
-        const float4 v = ld4(qp + d0);
-        x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+    for (int i = tt_id; i < RR * D * NS / 8; i += kTeam) reinterpret_cast<uint4*>(s_q)[i] = make_uint4(0, 0, 0, 0);
+    for (int i = tt_id; i < RR; i += kTeam) s_rs[i] = 0.f;
+    team_sync();
+    const int d0q = (lane % LPR) * 4;
+    for (int rb = (Solo ? 0 : warp) * RPI; rb < rows; rb += 4 * WARPS * RPI) {
+      float x[4][4], y[4][4];
+      bool have[4];
+      // four rows at a time, so that their loads are in flight together
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int r = rb + k * WARPS * RPI + lane / LPR;
+        have[k] = r < rows;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f), o = v;
+        if (have[k]) {
+          const int tt = (r0 + r) / G, h = hk * G + (r0 + r) % G;
+          const T* qp = static_cast<const T*>(a.q) + n * a.sq.n + h * a.sq.h + tt * a.sq.t;
+          v = ld4(qp + d0q);
+          const int hr = a.rope.rot / 2;
+          if (a.rope.turns && a.rope.layout == LIZARD_ROPE_HALF && d0q < a.rope.rot) {
+            // the pairs' other channels
+            auto other = [&](int e) { return e < a.rope.rot ? ld_f(qp + (e < hr ? e + hr : e - hr)) : 0.f; };
+            if (hr % 4 == 0) o = ld4(qp + (d0q < hr ? d0q + hr : d0q - hr));
+            else o = make_float4(other(d0q), other(d0q + 1), other(d0q + 2), other(d0q + 3));
+          } else {
+            o = make_float4(v.y, v.x, v.w, v.z);
+          }
+        }
+        x[k][0] = v.x, x[k][1] = v.y, x[k][2] = v.z, x[k][3] = v.w;
+        y[k][0] = o.x, y[k][1] = o.y, y[k][2] = o.z, y[k][3] = o.w;
       }
       if (ua == 0)  // the piece with the first unit adds the meta tokens
         for (int j = 0; j < a.M; ++j) {
-          float z = 0.f;
-          if (have) {
-            const int h = hk * G + (r0 + r) % G;
-            const float4 k = ld4(static_cast<const T*>(a.mk) + ((size_t)h * a.M + j) * D + d0);
-            z = x[0] * k.x + x[1] * k.y + x[2] * k.z + x[3] * k.w;
+          float z[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int h = hk * G + (r0 + rb + k * WARPS * RPI + lane / LPR) % G;
+            const float4 v = have[k] ? ld4(static_cast<const T*>(a.mk) + ((size_t)h * a.M + j) * D + d0q)
+                                     : make_float4(0.f, 0.f, 0.f, 0.f);
+            z[k] = x[k][0] * v.x + x[k][1] * v.y + x[k][2] * v.z + x[k][3] * v.w;
           }
 #pragma unroll
-          for (int o = LPR / 2; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-          if (lane % LPR == 0) s_zm[r * kMaxM + j] = z * (a.scale * kLog2e);
-        }
-      if (have && a.rope.turns && d0 < a.rope.rot) {
-        const int64_t p = s_p.s.p0 + (r0 + r) / G;
-        const int hr = a.rope.rot / 2;
-        float y[4];
+          for (int k = 0; k < 4; ++k) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int e = d0 + i;
-          y[i] = x[i];
-          if (e < a.rope.rot) {
-            const bool half = a.rope.layout == LIZARD_ROPE_HALF;
-            const bool low = half ? e < hr : (e & 1) == 0;
-            const float o = half ? ld_f(qp + (low ? e + hr : e - hr)) : x[i ^ 1];
-            float co, si;
-            rope_angle(a.rope.turns[half ? (low ? e : e - hr) : e >> 1], p, a.rope.factor, co, si);
-            y[i] = low ? x[i] * co - o * si : x[i] * co + o * si;
+            for (int o = LPR / 2; o > 0; o >>= 1) z[k] += __shfl_xor_sync(0xffffffffu, z[k], o);
+            if (lane % LPR == 0 && have[k])
+              s_zm[(rb + k * WARPS * RPI + lane / LPR) * kMaxM + j] = z[k] * (a.scale * kLog2e);
           }
         }
+      float co[4], si[4];
+      int angle_of = -1;  // token whose angles co, si hold: the heads of a token share them
+#pragma unroll 1
+      for (int k = 0; k < 4; ++k) {
+        const int r = rb + k * WARPS * RPI + lane / LPR;
+        if (rb + k * WARPS * RPI >= rows) break;
+        float v[4];
+        // the arrays are indexed by constants only
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[i] = y[i];
-      }
-      float mx = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
+        for (int i = 0; i < 4; ++i) v[i] = k == 0 ? x[0][i] : k == 1 ? x[1][i] : k == 2 ? x[2][i] : x[3][i];
+        if (a.rope.turns && r < rows && d0q < a.rope.rot) {
+          const int tt = (r0 + r) / G, hr = a.rope.rot / 2;
+          const bool half = a.rope.layout == LIZARD_ROPE_HALF;
+          if (tt != angle_of) {
+            angle_of = tt;
 #pragma unroll
-      for (int o = LPR / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-      // x = 2^e x', |x'| < 2^14: halves keep 11 bits down to 2^-28 of the row's largest
-      int e = (int)(__float_as_uint(mx) >> 23) - 127 - 13;
-      e = max(-126, min(e, 113));
-      const float inv = exp2_int(-e);
+            for (int i = 0; i < 4; ++i) {
+              const int e = d0q + i;
+              co[i] = 1.f, si[i] = 0.f;
+              if (e < a.rope.rot) {
+                const bool low = half ? e < hr : (e & 1) == 0;
+                rope_angle(a.rope.turns[half ? (low ? e : e - hr) : e >> 1], s_p.s.p0 + tt, a.rope.factor, co[i], si[i]);
+                if (low) si[i] = -si[i];
+              }
+            }
+          }
 #pragma unroll
-      for (int i = 0; i < 4; ++i) x[i] *= inv;
-      if (lane % LPR == 0) s_rs[r] = a.scale * kLog2e * exp2_int(e);
-      // element d = (D/4) t + 4 s + i of row r feeds lane (r%8) t, step s, register 2 (i/2) + r/8%2
-      const int t = d0 / (D / 4), s = (d0 % (D / 4)) / 4;
-      uint32_t* dst = reinterpret_cast<uint32_t*>(s_q) +
-                      ((size_t)((r >> 4) * NS * KS + s) * 32 + (r & 7) * 4 + t) * 4 + ((r >> 3) & 1);
-      const uint32_t w0 = half2_bits(x[0], x[1]), w1 = half2_bits(x[2], x[3]);
-      dst[0] = w0, dst[2] = w1;
-      if (NS == 2) {
-        dst[KS * 128] = half2_rest(x[0], x[1], w0);
-        dst[KS * 128 + 2] = half2_rest(x[2], x[3], w1);
+          for (int i = 0; i < 4; ++i) {
+            const float o = k == 0 ? y[0][i] : k == 1 ? y[1][i] : k == 2 ? y[2][i] : y[3][i];
+            v[i] = v[i] * co[i] + o * si[i];
+          }
+        }
+        float mx = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
+#pragma unroll
+        for (int o = LPR / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        // v = 2^e v', |v'| < 2^14: halves keep 11 bits down to 2^-28 of the row's largest
+        int e = (int)(__float_as_uint(mx) >> 23) - 127 - 13;
+        e = max(-126, min(e, 113));
+        const float inv = exp2_int(-e);
+        if (r < rows) {
+          if (lane % LPR == 0) s_rs[r] = a.scale * kLog2e * exp2_int(e);
+          // element d = (D/4) t + 4 s + i of row r feeds lane (r%8) t, step s, register 2 (i/2) + r/8%2
+          const int t = d0q / (D / 4), s = (d0q % (D / 4)) / 4;
+          uint32_t* dst = reinterpret_cast<uint32_t*>(s_q) +
+                          ((size_t)((r >> 4) * NS * KS + s) * 32 + (r & 7) * 4 + t) * 4 + ((r >> 3) & 1);
+          const uint32_t w0 = half2_bits(v[0] * inv, v[1] * inv), w1 = half2_bits(v[2] * inv, v[3] * inv);
+          dst[0] = w0, dst[2] = w1;
+          if (NS == 2) {
+            dst[KS * 128] = half2_rest(v[0] * inv, v[1] * inv, w0);
+            dst[KS * 128 + 2] = half2_rest(v[2] * inv, v[3] * inv, w1);
+          }
+        }
       }
     }
     team_sync();
@@ -616,7 +681,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG, Solo>::kPerSm)
     // o[k][2 i + e] is channel (D/8) (2 t4 + e) + k of row g + 8 i
     const bool whole_seg = ua == 0 && s_p.ub == s_p.s.units;
     float* part = reinterpret_cast<float*>(a.ws + (((size_t)M2 * Hk * sizeof(unsigned) + 255) & ~(size_t)255));
-    auto slot = [&](int64_t w, bool starts) { return part + (size_t)(2 * w + (starts ? 1 : 0)) * prow * (D + 4); };
+    auto slot = [&](int w, bool starts) { return part + (size_t)(2 * w + (starts ? 1 : 0)) * prow * (D + 4); };
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -677,7 +742,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG, Solo>::kPerSm)
         st4(static_cast<T*>(a.y) + n * a.sy.n + h * a.sy.h + tt * a.sy.t + d0, make_float4(0.f, 0.f, 0.f, 0.f));
       }
     if (!whole_seg) {
-      const int64_t c0 = s_p.head0 / share, c1 = (s_p.head0 + s_p.s.units - 1) / share;
+      const int c0 = s_p.c0, c1 = s_p.c1;
       __threadfence();
       team_sync();
       int last = 0;
@@ -692,45 +757,67 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG, Solo>::kPerSm)
       }
       if (last) {
         // the V4 lanes of a row read the statistics of V4 partials at a time, turn them into
-        // weights, and then add the outputs with independent loads
+        // weights, and then add the outputs, four rows and four partials in flight
         __threadfence();
         const int k = tt_id % V4;
-        for (int rb = 0; rb < rows; rb += ROWSTEP) {
-          const int r = rb + tt_id / V4;
-          RowStat s{-INFINITY, -INFINITY, 0.f};
-          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-          for (int64_t cb = c0; cb <= c1; cb += V4) {
-            float4 b = make_float4(-INFINITY, -INFINITY, 0.f, 0.f);
-            if (r < rows && cb + k <= c1)
-              b = __ldcg(reinterpret_cast<const float4*>(slot(cb + k, (cb + k) * share <= s_p.head0) +
-                                                         (size_t)prow * D + 4 * r));
-            float mm = b.x, mw = b.y;
+        constexpr int RW = 4;
+        for (int rb = tt_id / V4; rb - tt_id / V4 < rows; rb += RW * ROWSTEP) {
+          RowStat s[RW];
+          float4 v[RW];
 #pragma unroll
-            for (int o = V4 / 2; o > 0; o >>= 1) {
-              mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
-              mw = fmaxf(mw, __shfl_xor_sync(0xffffffffu, mw, o));
+          for (int q = 0; q < RW; ++q) s[q] = RowStat{-INFINITY, -INFINITY, 0.f}, v[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int cb = c0; cb <= c1; cb += V4) {
+            float wk[RW];
+            float4 b[RW];
+#pragma unroll
+            for (int q = 0; q < RW; ++q) {
+              b[q] = make_float4(-INFINITY, -INFINITY, 0.f, 0.f);
+              if (rb + q * ROWSTEP < rows && cb + k <= c1)
+                b[q] = __ldcg(reinterpret_cast<const float4*>(slot(cb + k, cb + k == c0) + (size_t)prow * D +
+                                                              4 * (rb + q * ROWSTEP)));
             }
-            mm = fmaxf(mm, s.m), mw = fmaxf(mw, s.mo);
-            const float fs = s.m == mm ? 1.f : exp2f(s.m - mm), fv = s.mo == mw ? 1.f : exp2f(s.mo - mw);
-            float ls = b.x == -INFINITY ? 0.f : b.z * exp2f(b.x - mm);
-            const float wk = b.y == -INFINITY ? 0.f : exp2f(b.y - mw);
 #pragma unroll
-            for (int o = V4 / 2; o > 0; o >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o);
-            s = RowStat{mm, mw, s.l * fs + ls};
-            v.x *= fv, v.y *= fv, v.z *= fv, v.w *= fv;
-            const int cn = (int)min((int64_t)V4, c1 - cb + 1);
-#pragma unroll 8
-            for (int i = 0; i < cn; ++i) {
-              const float w = __shfl_sync(0xffffffffu, wk, i, V4);
-              if (r < rows) {
-                const float4 x = __ldcg(reinterpret_cast<const float4*>(
-                    slot(cb + i, i == 0 && cb * share <= s_p.head0) + (size_t)r * D + d0));
-                v.x = fmaf(w, x.x, v.x), v.y = fmaf(w, x.y, v.y);
-                v.z = fmaf(w, x.z, v.z), v.w = fmaf(w, x.w, v.w);
+            for (int q = 0; q < RW; ++q) {
+              float mm = b[q].x, mw = b[q].y;
+#pragma unroll
+              for (int o = V4 / 2; o > 0; o >>= 1) {
+                mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
+                mw = fmaxf(mw, __shfl_xor_sync(0xffffffffu, mw, o));
               }
+              mm = fmaxf(mm, s[q].m), mw = fmaxf(mw, s[q].mo);
+              const float fs = s[q].m == mm ? 1.f : exp2f(s[q].m - mm), fv = s[q].mo == mw ? 1.f : exp2f(s[q].mo - mw);
+              float ls = b[q].x == -INFINITY ? 0.f : b[q].z * exp2f(b[q].x - mm);
+              wk[q] = b[q].y == -INFINITY ? 0.f : exp2f(b[q].y - mw);
+#pragma unroll
+              for (int o = V4 / 2; o > 0; o >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o);
+              s[q] = RowStat{mm, mw, s[q].l * fs + ls};
+              v[q].x *= fv, v[q].y *= fv, v[q].z *= fv, v[q].w *= fv;
+            }
+            const int cn = min(V4, c1 - cb + 1);
+            for (int i = 0; i < cn; i += 4) {
+              float4 x[RW][4];
+#pragma unroll
+              for (int q = 0; q < RW; ++q)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  x[q][e] = make_float4(0.f, 0.f, 0.f, 0.f);
+                  if (rb + q * ROWSTEP < rows && i + e < cn)
+                    x[q][e] = __ldcg(reinterpret_cast<const float4*>(slot(cb + i + e, cb + i + e == c0) +
+                                                                     (size_t)(rb + q * ROWSTEP) * D + d0));
+                }
+#pragma unroll
+              for (int q = 0; q < RW; ++q)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const float w = __shfl_sync(0xffffffffu, wk[q], (i + e) & (V4 - 1), V4);
+                  v[q].x = fmaf(w, x[q][e].x, v[q].x), v[q].y = fmaf(w, x[q][e].y, v[q].y);
+                  v[q].z = fmaf(w, x[q][e].z, v[q].z), v[q].w = fmaf(w, x[q][e].w, v[q].w);
+                }
             }
           }
-          if (r < rows) finish(r, s, v, d0);
+#pragma unroll
+          for (int q = 0; q < RW; ++q)
+            if (rb + q * ROWSTEP < rows) finish(rb + q * ROWSTEP, s[q], v[q], d0);
         }
         if (tt_id == 0) reinterpret_cast<unsigned*>(a.ws)[s_p.seg] = 0u;
       }
