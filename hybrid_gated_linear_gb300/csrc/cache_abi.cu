@@ -293,7 +293,7 @@ lizard_status lizard_cache_read(const lizard_cache* cache, const lizard_cache_io
 size_t lizard_cache_attn_workspace_bytes(const lizard_cache* cache, const lizard_cache_attn_dims* dims) {
   lz::CacheArgs c;
   if (cache_ok(cache, &c) != LIZARD_OK || !attn_dims_ok(c, dims)) return 0;
-  return lz::kWsHeader + lz::cache_attn_workspace(c.N, c.Hk, dims->H, dims->T, c.d);
+  return lz::kWsHeader + lz::cache_attn_workspace(c.N, c.Hk, dims->H, dims->T, c.d, dims->dtype);
 }
 
 lizard_status lizard_cache_attn(const lizard_cache* cache, const lizard_cache_attn_dims* dims, const void* q,

@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG, Solo>::kPerSm)
     if (!pieces) f1 = min(f1, total);
   }
   uint32_t used = 0;  // units this warp's group has consumed, over all pieces
-  auto wait = [&](uint64_t* bar, uint32_t parity) {
+  auto wait_lane = [&](uint64_t* bar, uint32_t parity) {
     if (mbar_try_wait(bar, parity)) return true;
     const long long c0 = clock64();
     while (true) {
@@ -260,6 +260,11 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG, Solo>::kPerSm)
         return false;
       }
     }
+  };
+  // one answer for the warp: what follows a wait is executed by all its lanes together
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    const bool ok = wait_lane(bar, parity);
+    return __all_sync(0xffffffffu, ok) != 0;
   };
 
   while (true) {
@@ -875,7 +880,8 @@ cudaError_t by_format(const CacheAttn& a, cudaStream_t s, int* launches) {
 
 }  // namespace
 
-size_t cache_attn_workspace(int N, int Hk, int H, int T, int d) {
+size_t cache_attn_workspace(int N, int Hk, int H, int T, int d, lizard_dtype dt) {
+  if (cache_attn_tc_used(H, Hk, T, dt)) return cache_attn_tc_workspace(N, Hk, H, T, d);
   const int rows = H / Hk * T, RR = team_rows(rows), RB = rows > 0 ? (rows + RR - 1) / RR : 1;
   const int teams = kMaxCtas * (solo_warps(N, Hk, rows) ? 8 : 1);
   // a counter per (sequence, rows, head), then two partial results per team
@@ -884,6 +890,7 @@ size_t cache_attn_workspace(int N, int Hk, int H, int T, int d) {
 }
 
 cudaError_t launch_cache_attn(const CacheAttn& a, lizard_dtype dt, cudaStream_t s, int* launches) {
+  if (cache_attn_tc_used(a.H, a.c.Hk, a.T, dt)) return launch_cache_attn_tc(a, s, launches);
   if (dt == LIZARD_F32)
     return a.c.d == 64 ? by_format<float, 64>(a, s, launches) : by_format<float, 128>(a, s, launches);
   return a.c.d == 64 ? by_format<bf16, 64>(a, s, launches) : by_format<bf16, 128>(a, s, launches);

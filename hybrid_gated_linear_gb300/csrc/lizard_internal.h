@@ -347,7 +347,11 @@ struct CacheAttn {
   unsigned* status;
   unsigned char* ws;  // workspace after the header
 };
-size_t cache_attn_workspace(int N, int Hk, int H, int T, int d);
+size_t cache_attn_workspace(int N, int Hk, int H, int T, int d, lizard_dtype dt);
+// The tcgen05 path for many rows (query heads of a key head times new tokens).
+bool cache_attn_tc_used(int H, int Hk, int T, lizard_dtype dt);
+size_t cache_attn_tc_workspace(int N, int Hk, int H, int T, int d);
+cudaError_t launch_cache_attn_tc(const CacheAttn& a, cudaStream_t s, int* launches);
 cudaError_t launch_cache_attn(const CacheAttn& a, lizard_dtype dt, cudaStream_t s, int* launches);
 
 }  // namespace lz
