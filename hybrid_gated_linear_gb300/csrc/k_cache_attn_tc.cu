@@ -33,6 +33,7 @@ constexpr int kBlock = 128;      // tokens per block
 constexpr int kThreads = 416;    // warps 0-7 rows, 8-11 codes, 12 MMA
 constexpr int kMaxM = 16;
 constexpr float kLazy = 8.f;     // P <= 2^8 fits binary16 with room for its sums
+constexpr float kFar = 60.f;      // see weights()
 constexpr float kLog2e = 1.4426950408889634f;
 
 // Barriers: operand tiles full and free (two stages each), per row tile scores ready, weights
@@ -76,6 +77,101 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
 __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Two fp32 multiply-adds or additions in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "add.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
+// A row's largest logit in each 16-token part of a block.  Checked: some token of the block
+// may be hidden from the row, or a whole part unseen.
+template <bool Checked>
+__device__ __forceinline__ void part_maxima(uint32_t ts, const float2* sc, float rs, int tok, int lo_r, int hi_r,
+                                            float (&mb)[8]) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t u[2][32];
+    tmem_ld32(ts + 64 * h, u[0]);
+    tmem_ld32(ts + 64 * h + 32, u[1]);
+    tmem_ld_wait();
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      float x = -INFINITY, y = -INFINITY;
+#pragma unroll
+      for (int e = 0; e < 16; e += 2) {
+        float s0 = __uint_as_float(u[b >> 1][(b & 1) * 16 + e]), s1 = __uint_as_float(u[b >> 1][(b & 1) * 16 + e + 1]);
+        if (Checked) {
+          const int c = tok + 64 * h + 16 * b + e;
+          s0 = c >= lo_r && c <= hi_r ? s0 : -INFINITY;
+          s1 = c + 1 >= lo_r && c + 1 <= hi_r ? s1 : -INFINITY;
+        }
+        x = fmaxf(x, s0), y = fmaxf(y, s1);
+      }
+      const float k = sc[4 * h + b].x;
+      mb[4 * h + b] = !Checked || k > 0.f ? fmaxf(x, y) * (rs * k) : -INFINITY;
+    }
+  }
+}
+
+// Replaces a row's scores of a block by its weights 2^(z + e - mo) as binary16 and returns
+// their sum in units of 2^m.  Checked additionally covers parts whose values are so much
+// smaller than the others' that their weights would vanish before their share of the sum
+// does: the sum then takes exponentials of its own.
+template <bool Checked>
+__device__ __forceinline__ float weights(uint32_t ts, const float2* sc, float rs, int tok, int lo_r, int hi_r, float m,
+                                         float mo) {
+  float l = 0.f;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t u[2][32], pk[16];
+    tmem_ld32(ts + 64 * h, u[0]);
+    tmem_ld32(ts + 64 * h + 32, u[1]);
+    tmem_ld_wait();
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      const float2 f = sc[4 * h + b];
+      const float k = rs * f.x, sh = f.y - mo;
+      float2 sum = make_float2(0.f, 0.f);
+      float own = 0.f;
+      const bool far = Checked && mo - f.y - m > kFar;
+#pragma unroll
+      for (int e = 0; e < 16; e += 2) {
+        const float2 x = make_float2(__uint_as_float(u[b >> 1][(b & 1) * 16 + e]),
+                                     __uint_as_float(u[b >> 1][(b & 1) * 16 + e + 1]));
+        float2 w;
+        if (Checked) {
+          const int c = tok + 64 * h + 16 * b + e;
+          const float z0 = f.x > 0.f && c >= lo_r && c <= hi_r ? x.x * k : -INFINITY;
+          const float z1 = f.x > 0.f && c + 1 >= lo_r && c + 1 <= hi_r ? x.y * k : -INFINITY;
+          if (far) own += ex2_approx(z0 - m) + ex2_approx(z1 - m);
+          w = make_float2(ex2_approx(z0 + sh), ex2_approx(z1 + sh));
+        } else {
+          const float2 z = fma2(x, make_float2(k, k), make_float2(sh, sh));
+          w = make_float2(ex2_approx(z.x), ex2_approx(z.y));
+        }
+        sum = add2(sum, w);
+        pk[(b & 1) * 8 + e / 2] = half2_bits(w.x, w.y);
+      }
+      l += far ? own : (sum.x + sum.y) * ex2_approx(mo - f.y - m);
+      if (Checked) __syncwarp();
+      if (b & 1) tmem_st16(ts + 32 * h + 16 * (b >> 1), pk);
+    }
+  }
+  return l;
 }
 
 // What this CTA's rows see; token numbers relative to base.
@@ -377,35 +473,14 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(CacheAttn a, int ti
       if (!(ok = wait_all(SC + (i & 3), (i >> 2) & 1) && wait_all(SF + t, i & 1))) break;
       tc_fence_after();
       const float2* sc = s_scale[i & 3];
-      const bool edge = tok < all_lo || tok + kBlock - 1 > all_hi;
-      // maxima of the block's parts
+      bool checked = tok < all_lo || tok + kBlock - 1 > all_hi;
+#pragma unroll
+      for (int b = 0; b < 8; ++b) checked |= sc[b].x == 0.f;
       float mb[8], mn = m, mon = mo;
+      if (checked) part_maxima<true>(ts, sc, rs, tok, lo_r, hi_r, mb);
+      else part_maxima<false>(ts, sc, rs, tok, lo_r, hi_r, mb);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t u[2][32];
-        tmem_ld32(ts + 64 * h, u[0]);
-        tmem_ld32(ts + 64 * h + 32, u[1]);
-        tmem_ld_wait();
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          float x = -INFINITY, y = -INFINITY;
-#pragma unroll
-          for (int e = 0; e < 16; e += 2) {
-            float s0 = __uint_as_float(u[b >> 1][(b & 1) * 16 + e]), s1 = __uint_as_float(u[b >> 1][(b & 1) * 16 + e + 1]);
-            if (edge) {
-              const int c = tok + 64 * h + 16 * b + e;
-              s0 = c >= lo_r && c <= hi_r ? s0 : -INFINITY;
-              s1 = c + 1 >= lo_r && c + 1 <= hi_r ? s1 : -INFINITY;
-            }
-            x = fmaxf(x, s0), y = fmaxf(y, s1);
-          }
-          const float2 f = sc[4 * h + b];
-          const float z = f.x > 0.f ? fmaxf(x, y) * (rs * f.x) : -INFINITY;
-          mb[4 * h + b] = z;
-          mn = fmaxf(mn, z);
-          mon = fmaxf(mon, z + f.y);
-        }
-      }
+      for (int b = 0; b < 8; ++b) mn = fmaxf(mn, mb[b]), mon = fmaxf(mon, mb[b] + sc[b].y);
       // the sum's scale follows m exactly, the output's only in steps
       if (mn > m) l *= exp2f(m - mn), m = mn;
       const bool jump = mon > mo + kLazy;
@@ -428,40 +503,11 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(CacheAttn a, int ti
         }
       }
       const float ml = m == -INFINITY ? 0.f : m, mol = mo == -INFINITY ? 0.f : mo;
+      bool far = false;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t u[2][32], pk[16];
-        tmem_ld32(ts + 64 * h, u[0]);
-        tmem_ld32(ts + 64 * h + 32, u[1]);
-        tmem_ld_wait();
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          const float2 f = sc[4 * h + b];
-          const float k = rs * f.x, sh = f.y - mol;
-          float s0 = 0.f, s1 = 0.f;
-          // a part whose values are so much smaller that its weights would vanish before
-          // their share of the sum does: the sum takes exponentials of its own
-          const bool far = mol - f.y - ml > 60.f;
-#pragma unroll
-          for (int e = 0; e < 16; e += 2) {
-            float z0 = __uint_as_float(u[b >> 1][(b & 1) * 16 + e]) * k;
-            float z1 = __uint_as_float(u[b >> 1][(b & 1) * 16 + e + 1]) * k;
-            if (edge) {
-              const int c = tok + 64 * h + 16 * b + e;
-              z0 = c >= lo_r && c <= hi_r ? z0 : -INFINITY;
-              z1 = c + 1 >= lo_r && c + 1 <= hi_r ? z1 : -INFINITY;
-            }
-            if (f.x == 0.f) z0 = z1 = -INFINITY;
-            const float w0 = ex2_approx(z0 + sh), w1 = ex2_approx(z1 + sh);
-            if (far) l += ex2_approx(z0 - ml) + ex2_approx(z1 - ml);
-            s0 += w0, s1 += w1;
-            pk[(b & 1) * 8 + e / 2] = half2_bits(w0, w1);
-          }
-          if (!far) l += (s0 + s1) * ex2_approx(mol - f.y - ml);
-          __syncwarp();
-          if (b & 1) tmem_st16(ts + 32 * h + 16 * (b >> 1), pk);
-        }
-      }
+      for (int b = 0; b < 8; ++b) far |= mol - sc[b].y - ml > kFar;
+      if (__any_sync(0xffffffffu, checked || far)) l += weights<true>(ts, sc, rs, tok, lo_r, hi_r, ml, mol);
+      else l += weights<false>(ts, sc, rs, tok, lo_r, hi_r, ml, mol);
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
