@@ -4,7 +4,7 @@
 // Rows are the G = H / Hk query heads times the new tokens of a (sequence, key head), row =
 // token * G + head.  One CTA takes 256 rows (two tiles of 128, the M of an MMA) and walks
 // over the visible cache in blocks of 128 tokens:
-//   4 warps   turn a block's codes into binary16 tiles (each code is exact in 11 bits); the
+//   3 warps   turn a block's codes into binary16 tiles (each code is exact in 11 bits); the
 //             copy from global memory runs one block ahead in registers
 //   1 thread  issues S = Q K^T (operands in shared memory) and O += P V (P in tensor memory)
 //   2 x 4 warps, one thread per row: running maxima and sum, P = 2^(z + e - mo) as binary16
@@ -30,7 +30,10 @@ using namespace tc;
 
 constexpr int kRows = 256;       // rows per CTA
 constexpr int kBlock = 128;      // tokens per block
-constexpr int kThreads = 416;    // warps 0-7 rows, 8-11 codes, 12 MMA
+constexpr int kCodeWarps = 3;
+constexpr int kMmaWarp = 8 + kCodeWarps;
+// warps 0-7 rows, 8-10 codes, 11 MMA: twelve warps may have 168 registers per thread
+constexpr int kThreads = 32 * (kMmaWarp + 1);
 constexpr int kMaxM = 16;
 constexpr float kLazy = 8.f;     // P <= 2^8 fits binary16 with room for its sums
 constexpr float kFar = 60.f;      // see weights()
@@ -97,32 +100,44 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   return d;
 }
 
+// Waits for the row's TMEM loads; the registers are named so that no use moves in front.
+__device__ __forceinline__ void tmem_ld_wait32(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
+                 "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29])
+               :
+               : "memory");
+  asm volatile("" : "+r"(r[30]), "+r"(r[31]));
+}
+
 // A row's largest logit in each 16-token part of a block.  Checked: some token of the block
 // may be hidden from the row, or a whole part unseen.
 template <bool Checked>
-__device__ __forceinline__ void part_maxima(uint32_t ts, const float2* sc, float rs, int tok, int lo_r, int hi_r,
+__device__ __forceinline__ void part_maxima(uint32_t ts, const float2 (&sc)[8], float rs, int tok, int lo_r, int hi_r,
                                             float (&mb)[8]) {
+  uint32_t u[2][32];
+  tmem_ld32(ts, u[0]);
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    uint32_t u[2][32];
-    tmem_ld32(ts + 64 * h, u[0]);
-    tmem_ld32(ts + 64 * h + 32, u[1]);
-    tmem_ld_wait();
+  for (int q = 0; q < 4; ++q) {
+    tmem_ld_wait32(u[q & 1]);
+    if (q < 3) tmem_ld32(ts + 32 * (q + 1), u[(q + 1) & 1]);
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
+    for (int b = 0; b < 2; ++b) {
       float x = -INFINITY, y = -INFINITY;
 #pragma unroll
       for (int e = 0; e < 16; e += 2) {
-        float s0 = __uint_as_float(u[b >> 1][(b & 1) * 16 + e]), s1 = __uint_as_float(u[b >> 1][(b & 1) * 16 + e + 1]);
+        float s0 = __uint_as_float(u[q & 1][b * 16 + e]), s1 = __uint_as_float(u[q & 1][b * 16 + e + 1]);
         if (Checked) {
-          const int c = tok + 64 * h + 16 * b + e;
+          const int c = tok + 32 * q + 16 * b + e;
           s0 = c >= lo_r && c <= hi_r ? s0 : -INFINITY;
           s1 = c + 1 >= lo_r && c + 1 <= hi_r ? s1 : -INFINITY;
         }
         x = fmaxf(x, s0), y = fmaxf(y, s1);
       }
-      const float k = sc[4 * h + b].x;
-      mb[4 * h + b] = !Checked || k > 0.f ? fmaxf(x, y) * (rs * k) : -INFINITY;
+      const float k = sc[2 * q + b].x;
+      mb[2 * q + b] = !Checked || k > 0.f ? fmaxf(x, y) * (rs * k) : -INFINITY;
     }
   }
 }
@@ -132,29 +147,29 @@ __device__ __forceinline__ void part_maxima(uint32_t ts, const float2* sc, float
 // smaller than the others' that their weights would vanish before their share of the sum
 // does: the sum then takes exponentials of its own.
 template <bool Checked>
-__device__ __forceinline__ float weights(uint32_t ts, const float2* sc, float rs, int tok, int lo_r, int hi_r, float m,
-                                         float mo) {
+__device__ __forceinline__ float weights(uint32_t ts, const float2 (&sc)[8], float rs, int tok, int lo_r, int hi_r,
+                                         float m, float mo) {
   float l = 0.f;
+  uint32_t u[2][32];
+  tmem_ld32(ts, u[0]);
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    uint32_t u[2][32], pk[16];
-    tmem_ld32(ts + 64 * h, u[0]);
-    tmem_ld32(ts + 64 * h + 32, u[1]);
-    tmem_ld_wait();
+  for (int q = 0; q < 4; ++q) {
+    uint32_t pk[16];
+    tmem_ld_wait32(u[q & 1]);
+    if (q < 3) tmem_ld32(ts + 32 * (q + 1), u[(q + 1) & 1]);
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      const float2 f = sc[4 * h + b];
+    for (int b = 0; b < 2; ++b) {
+      const float2 f = sc[2 * q + b];
       const float k = rs * f.x, sh = f.y - mo;
       float2 sum = make_float2(0.f, 0.f);
       float own = 0.f;
       const bool far = Checked && mo - f.y - m > kFar;
 #pragma unroll
       for (int e = 0; e < 16; e += 2) {
-        const float2 x = make_float2(__uint_as_float(u[b >> 1][(b & 1) * 16 + e]),
-                                     __uint_as_float(u[b >> 1][(b & 1) * 16 + e + 1]));
+        const float2 x = make_float2(__uint_as_float(u[q & 1][b * 16 + e]), __uint_as_float(u[q & 1][b * 16 + e + 1]));
         float2 w;
         if (Checked) {
-          const int c = tok + 64 * h + 16 * b + e;
+          const int c = tok + 32 * q + 16 * b + e;
           const float z0 = f.x > 0.f && c >= lo_r && c <= hi_r ? x.x * k : -INFINITY;
           const float z1 = f.x > 0.f && c + 1 >= lo_r && c + 1 <= hi_r ? x.y * k : -INFINITY;
           if (far) own += ex2_approx(z0 - m) + ex2_approx(z1 - m);
@@ -164,12 +179,13 @@ __device__ __forceinline__ float weights(uint32_t ts, const float2* sc, float rs
           w = make_float2(ex2_approx(z.x), ex2_approx(z.y));
         }
         sum = add2(sum, w);
-        pk[(b & 1) * 8 + e / 2] = half2_bits(w.x, w.y);
+        pk[b * 8 + e / 2] = half2_bits(w.x, w.y);
       }
       l += far ? own : (sum.x + sum.y) * ex2_approx(mo - f.y - m);
-      if (Checked) __syncwarp();
-      if (b & 1) tmem_st16(ts + 32 * h + 16 * (b >> 1), pk);
     }
+    if (Checked) __syncwarp();
+    // columns 16 q .. of the weights lie below the scores read so far and those in flight
+    tmem_st16(ts + 16 * q, pk);
   }
   return l;
 }
@@ -188,7 +204,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(CacheAttn a, int ti
   unsigned char* sm = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   __shared__ Ctl<NB> s_ctl;
   __shared__ float s_rs[kRows];
-  __shared__ float2 s_scale[4][8];  // of a block's 16-token parts: key scale (0: unseen), log2 of the value scale
+  __shared__ __align__(16) float2 s_scale[4][8];  // of a block's 16-token parts: key scale (0: unseen), log2 of the value scale
   __shared__ View s_v;
   __shared__ int s_last;
   Ctl<NB>* ctl = &s_ctl;
@@ -199,13 +215,13 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(CacheAttn a, int ti
   const int nh = unit % (a.c.N * Hk), tile = tiles - 1 - unit / (a.c.N * Hk);
   const int n = nh / Hk, hk = nh % Hk;
 
-  if (warp == 12) {
+  if (warp == kMmaWarp) {
     tmem_alloc(&ctl->tmem, 512);
     tmem_relinquish();
   }
   if (tid == 0) {
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&ctl->bar[KF + i], 4), mbar_init(&ctl->bar[VF + i], 4);
+      mbar_init(&ctl->bar[KF + i], kCodeWarps), mbar_init(&ctl->bar[VF + i], kCodeWarps);
       mbar_init(&ctl->bar[KE + i], 1), mbar_init(&ctl->bar[VE + i], 1);
       mbar_init(&ctl->bar[SF + i], 1), mbar_init(&ctl->bar[PF + i], 4), mbar_init(&ctl->bar[OD + i], 1);
     }
@@ -327,16 +343,26 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(CacheAttn a, int ti
   };
   bool done_ok = true;
   float l = 0.f, m = -INFINITY, mo = -INFINITY;
-  if (warp == 12) {
+  if (warp == kMmaWarp) {
     // ------------------------------------------------------------------ MMA issuer
     if (lane == 0) {
+      // descriptors differ in their address field (16-byte units) only: one addition per MMA,
+      // since this thread's instructions are what the tensor cores wait for
       const uint32_t sb = smem_u32(sm);
+      const uint64_t dq = desc_k(sb + Sm::Q, kBlock, 0), dk = desc_k(sb + Sm::K, kBlock, 0);
+      const uint64_t dv = desc_mn(sb + Sm::V, kBlock, 0);
+      constexpr uint32_t kTile16 = Sm::kTile / 16;
       const uint32_t id_s = idesc_f16(128, kBlock, false), id_o = idesc_f16(128, D, true);
       bool ok = true;
       auto scores = [&](int t, int i) {
-        for (int j = 0; j < D / 16; ++j)
-          mma_bf16(tmem + t * kBlock, desc_k(sb + Sm::Q + t * Sm::kTile, kBlock, j),
-                   desc_k(sb + Sm::K + (i & 1) * Sm::kTile, kBlock, j), id_s, j > 0);
+        const uint64_t qa = dq + t * kTile16, kb = dk + (i & 1) * kTile16;
+        const uint32_t ts = tmem + t * kBlock;
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) {
+          constexpr uint32_t kCol = kBlock * 128 / 16;  // next 64 channels
+          const uint32_t off = (j >> 2) * kCol + (j & 3) * 2;
+          mma_bf16(ts, qa + off, kb + off, id_s, j > 0);
+        }
         mma_commit(&ctl->bar[SF + t]);
         if (t == 1) mma_commit(&ctl->bar[KE + (i & 1)]);
       };
@@ -350,9 +376,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(CacheAttn a, int ti
         for (int t = 0; ok && t < 2; ++t) {
           if (!(ok = wait_bar(ctl, PF + t, i & 1))) break;
           tc_fence_after();
-          for (int j = 0; j < kBlock / 16; ++j)
-            mma_f16_ts(tmem + 256 + t * D, tmem + t * kBlock + 8 * j, desc_mn(sb + Sm::V + (i & 1) * Sm::kTile, kBlock, j),
-                       id_o, i > 0 || j > 0);
+          const uint64_t vb = dv + (i & 1) * kTile16;
+          const uint32_t to = tmem + 256 + t * D, ts = tmem + t * kBlock;
+#pragma unroll
+          for (int j = 0; j < kBlock / 16; ++j) mma_f16_ts(to, ts + 8 * j, vb + j * 128, id_o, j > 0 || i > 0);
           mma_commit(&ctl->bar[OD + t]);
           if (t == 1) mma_commit(&ctl->bar[VE + (i & 1)]);
           if (i + 1 < nblk) {
@@ -368,87 +395,102 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(CacheAttn a, int ti
     }
   } else if (warp >= 8) {
     // ------------------------------------------------------------------ codes -> binary16
-    constexpr int CPR = D / 16, RPW = 32 / CPR, IT = kBlock / (4 * RPW);  // chunks per row, rows per warp, steps
-    const int w = warp - 8, pl = lane % CPR;
+    // Warp w takes the 16-token parts w, w + 3, w + 6 of a block: IT steps of 32 chunks each.
+    constexpr int IT = D / 32, RPS = 16 / IT, NP = (8 + kCodeWarps - 1) / kCodeWarps;
+    const int w = warp - 8;
+    // Eight lanes that store together hold half rows (64 channels) of two rows: their stores
+    // fall into different banks.  A step adds 4 (8) rows.
+    const int row = D == 128 ? 2 * (lane >> 4) + ((lane >> 2) & 1) : lane >> 2;
+    const int chunk = D == 128 ? 4 * ((lane >> 3) & 1) + (lane & 3) : lane & 3;
     const int lo = s_v.lo, hi = s_v.hi;
     const int64_t base = s_v.base;
-    // this lane's 16-token part of a block: its page and scales
-    int id = -1, nid = -1;
+    // Four blocks are looked up at a time, the next four while these are converted: lane
+    // 8 b + p has part p of block b, where it is (in parts of 16 rows) and its scales.
+    int at = -1, nat = -1;
     float2 sc = make_float2(0.f, 0.f), nsc = sc;
     auto look = [&](int i) {
-      nid = -1;
+      i += lane >> 3;
+      nat = -1;
       nsc = make_float2(0.f, 0.f);
-      if (lane < 8 && i < nblk) {
-        const int tok = (s_v.b0 + i) * kBlock + lane * 16;
-        if (tok + 15 >= lo && tok <= hi) {
-          nid = pool_page(a.c, n, (uint32_t)((base + tok) >> a.c.log_p));
-          if (nid < 0) {
-            raise_status(a.status, kDevCheck);
-          } else {
-            const size_t ph = (size_t)nid * Hk + hk;
-            nsc = make_float2(a.c.ks[ph], (float)((int)(__float_as_uint(a.c.vs[ph]) >> 23 & 0xff) - 127));
-          }
+      const int tok = (s_v.b0 + i) * kBlock + (lane & 7) * 16;
+      if (i < nblk && tok + 15 >= lo && tok <= hi) {
+        const int id = pool_page(a.c, n, (uint32_t)((base + tok) >> a.c.log_p));
+        if (id < 0) {
+          raise_status(a.status, kDevCheck);
+        } else {
+          const size_t ph = (size_t)id * Hk + hk;
+          nat = (int)((ph * a.c.P + (int)((base + tok) & (a.c.P - 1))) >> 4);
+          nsc = make_float2(a.c.ks[ph], (float)((int)(__float_as_uint(a.c.vs[ph]) >> 23 & 0xff) - 127));
         }
       }
     };
-    auto load = [&](const unsigned char* pool, int i, int idl, uint4 (&u)[IT]) {
+    auto load = [&](const unsigned char* pool, int i, uint4 (&u)[NP][IT]) {
+      const int tok = (s_v.b0 + i) * kBlock;
+      // parts that end beyond what is seen hold bytes that were never written
+      const bool inner = tok >= lo && tok + kBlock - 1 <= hi;
 #pragma unroll
-      for (int k = 0; k < IT; ++k) {
-        const int r = k * 4 * RPW + w * RPW + lane / CPR;
-        const int tok = (s_v.b0 + i) * kBlock + r;
-        const int page = __shfl_sync(0xffffffffu, idl, (k * 4 * RPW + w * RPW) >> 4);
-        u[k] = make_uint4(0, 0, 0, 0);
-        if (i < nblk && page >= 0 && tok >= lo && tok <= hi)
-          u[k] = __ldg(reinterpret_cast<const uint4*>(
-              pool + (((size_t)page * Hk + hk) * a.c.P + (int)((base + tok) & (a.c.P - 1))) * D + pl * 16));
+      for (int q = 0; q < NP; ++q) {
+        const int p = w + q * kCodeWarps;
+        // past the batch in `at`, block i is the first of the next one
+        const int part = __shfl_sync(0xffffffffu, (i & 3) ? at : nat, (i & 3) * 8 + (p & 7));
+        const unsigned char* src = pool + (size_t)part * (16 * D);
+#pragma unroll
+        for (int k = 0; k < IT; ++k) {
+          const int r = row + k * RPS, tk = tok + 16 * p + r;
+          u[q][k] = make_uint4(0, 0, 0, 0);
+          if (p < 8 && i < nblk && part >= 0 && (inner || (tk >= lo && tk <= hi)))
+            u[q][k] = *reinterpret_cast<const uint4*>(src + r * D + 16 * chunk_place<D>(r, chunk));
+        }
       }
     };
-    auto convert = [&](unsigned char* tile, const uint4 (&u)[IT]) {
+    auto convert = [&](unsigned char* tile, const uint4 (&u)[NP][IT]) {
 #pragma unroll
-      for (int k = 0; k < IT; ++k) {
-        const int r = k * 4 * RPW + w * RPW + lane / CPR;
-        const int c = chunk_place<D>(r, pl);  // the chunk stored at this place (its own inverse)
-        uint32_t h[8];
-        const uint32_t x[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
+      for (int q = 0; q < NP; ++q) {
+        const int p = w + q * kCodeWarps;
+        if (p >= 8) break;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) codes_to_half<F>(x[e], h[2 * e], h[2 * e + 1]);
-        const uint4 a0 = make_uint4(h[0], h[1], h[2], h[3]), a1 = make_uint4(h[4], h[5], h[6], h[7]);
-        // lanes of the upper 64 channels store their halves in the other order: no conflicts
-        const bool sw = c >= 4;
-        *reinterpret_cast<uint4*>(tile + sw128_offset(r, 16 * c + (sw ? 8 : 0), kBlock)) = sw ? a1 : a0;
-        *reinterpret_cast<uint4*>(tile + sw128_offset(r, 16 * c + (sw ? 0 : 8), kBlock)) = sw ? a0 : a1;
+        for (int k = 0; k < IT; ++k) {
+          const int r = row + k * RPS;
+          uint32_t h[8];
+          const uint32_t x[4] = {u[q][k].x, u[q][k].y, u[q][k].z, u[q][k].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) codes_to_half<F>(x[e], h[2 * e], h[2 * e + 1]);
+          unsigned char* t = tile + p * 16 * 128;
+          *reinterpret_cast<uint4*>(t + sw128_offset(r, 16 * chunk, kBlock)) = make_uint4(h[0], h[1], h[2], h[3]);
+          *reinterpret_cast<uint4*>(t + sw128_offset(r, 16 * chunk + 8, kBlock)) = make_uint4(h[4], h[5], h[6], h[7]);
+        }
       }
       fence_proxy_async_smem();
     };
-    uint4 ku[IT], vu[IT];
+    uint4 ku[NP][IT], vu[NP][IT];
     look(0);
-    id = nid, sc = nsc;
-    load(a.c.k, 0, id, ku);
-    load(a.c.v, 0, id, vu);
-    look(1);
+    load(a.c.k, 0, ku);
+    load(a.c.v, 0, vu);
     bool ok = true;
     for (int i = 0; i < nblk; ++i) {
       const int st = i & 1;
       const uint32_t free_par = ((i >> 1) & 1) ^ 1;
+      if ((i & 3) == 0) {
+        at = nat, sc = nsc;
+        look(i + 4);
+      }
       if (i >= 2 && !(ok = wait_all(KE + st, free_par))) break;
       // Block i - 4's scales are no longer read: the keys' stage is free, so the scores of block
       // i - 2 are done, which were issued after every row had finished block i - 3.
       if (w == 0) {
-        if (lane < 8) s_scale[i & 3][lane] = sc;
+        if (lane >> 3 == (i & 3)) s_scale[i & 3][lane & 7] = sc;
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl->bar[SC + (i & 3)]);
       }
       convert(sm + Sm::K + st * Sm::kTile, ku);
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->bar[KF + st]);
-      id = nid, sc = nsc;
-      load(a.c.k, i + 1, id, ku);
+      load(a.c.k, i + 1, ku);
       if (i >= 2 && !(ok = wait_all(VE + st, free_par))) break;
       convert(sm + Sm::V + st * Sm::kTile, vu);
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->bar[VF + st]);
-      load(a.c.v, i + 1, id, vu);
-      look(i + 2);
+      load(a.c.v, i + 1, vu);
     }
     if (!ok) ctl->abort = 1;
   } else {
@@ -472,7 +514,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(CacheAttn a, int ti
       const int tok = (s_v.b0 + i) * kBlock;
       if (!(ok = wait_all(SC + (i & 3), (i >> 2) & 1) && wait_all(SF + t, i & 1))) break;
       tc_fence_after();
-      const float2* sc = s_scale[i & 3];
+      float2 sc[8];
+#pragma unroll
+      for (int b = 0; b < 8; b += 2) {
+        const float4 x = *reinterpret_cast<const float4*>(&s_scale[i & 3][b]);
+        sc[b] = make_float2(x.x, x.y), sc[b + 1] = make_float2(x.z, x.w);
+      }
       bool checked = tok < all_lo || tok + kBlock - 1 > all_hi;
 #pragma unroll
       for (int b = 0; b < 8; ++b) checked |= sc[b].x == 0.f;
@@ -604,7 +651,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(CacheAttn a, int ti
   }
   tc_fence_before();
   cta_sync();
-  if (warp == 12) {
+  if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
