@@ -375,28 +375,36 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG, Solo>::kPerSm)
     for (int rb = (Solo ? 0 : warp) * RPI; rb < rows; rb += 4 * WARPS * RPI) {
       float x[4][4], y[4][4];
       bool have[4];
-      // four rows at a time, so that their loads are in flight together
+      {
+        // four rows at a time, dead ones reading the last live one: no branch keeps the loads
+        // from being in flight together
+        Raw4<T> xr[4], yr[4];
+        const T* qp[4];
+        const bool half = a.rope.turns && a.rope.layout == LIZARD_ROPE_HALF && d0q < a.rope.rot;
+        const int hr = a.rope.rot / 2;
+        const int other = half && hr % 4 == 0 ? (d0q < hr ? d0q + hr : d0q - hr) : d0q;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int r = rb + k * WARPS * RPI + lane / LPR;
-        have[k] = r < rows;
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f), o = v;
-        if (have[k]) {
-          const int tt = (r0 + r) / G, h = hk * G + (r0 + r) % G;
-          const T* qp = static_cast<const T*>(a.q) + n * a.sq.n + h * a.sq.h + tt * a.sq.t;
-          v = ld4(qp + d0q);
-          const int hr = a.rope.rot / 2;
-          if (a.rope.turns && a.rope.layout == LIZARD_ROPE_HALF && d0q < a.rope.rot) {
-            // the pairs' other channels
-            auto other = [&](int e) { return e < a.rope.rot ? ld_f(qp + (e < hr ? e + hr : e - hr)) : 0.f; };
-            if (hr % 4 == 0) o = ld4(qp + (d0q < hr ? d0q + hr : d0q - hr));
-            else o = make_float4(other(d0q), other(d0q + 1), other(d0q + 2), other(d0q + 3));
-          } else {
+        for (int k = 0; k < 4; ++k) {
+          const int r = rb + k * WARPS * RPI + lane / LPR, rr = r0 + min(r, rows - 1);
+          const int tt = rr / G, h = hk * G + rr - tt * G;
+          have[k] = r < rows;
+          qp[k] = static_cast<const T*>(a.q) + n * a.sq.n + h * a.sq.h + tt * a.sq.t;
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) xr[k] = raw4(qp[k] + d0q), yr[k] = raw4(qp[k] + other);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float4 v = xr[k].value();
+          float4 o = yr[k].value();
+          if (half && hr % 4 != 0) {
+            auto at = [&](int e) { return e < a.rope.rot ? ld_f(qp[k] + (e < hr ? e + hr : e - hr)) : 0.f; };
+            o = make_float4(at(d0q), at(d0q + 1), at(d0q + 2), at(d0q + 3));
+          } else if (!half) {
             o = make_float4(v.y, v.x, v.w, v.z);
           }
+          x[k][0] = v.x, x[k][1] = v.y, x[k][2] = v.z, x[k][3] = v.w;
+          y[k][0] = o.x, y[k][1] = o.y, y[k][2] = o.z, y[k][3] = o.w;
         }
-        x[k][0] = v.x, x[k][1] = v.y, x[k][2] = v.z, x[k][3] = v.w;
-        y[k][0] = o.x, y[k][1] = o.y, y[k][2] = o.z, y[k][3] = o.w;
       }
       if (ua == 0)  // the piece with the first unit adds the meta tokens
         for (int j = 0; j < a.M; ++j) {
@@ -404,8 +412,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG, Solo>::kPerSm)
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const int h = hk * G + (r0 + rb + k * WARPS * RPI + lane / LPR) % G;
-            const float4 v = have[k] ? ld4(static_cast<const T*>(a.mk) + ((size_t)h * a.M + j) * D + d0q)
-                                     : make_float4(0.f, 0.f, 0.f, 0.f);
+            const float4 v = ld4(static_cast<const T*>(a.mk) + ((size_t)h * a.M + j) * D + d0q);
             z[k] = x[k][0] * v.x + x[k][1] * v.y + x[k][2] * v.z + x[k][3] * v.w;
           }
 #pragma unroll

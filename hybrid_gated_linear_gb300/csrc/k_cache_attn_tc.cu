@@ -16,8 +16,9 @@
 //
 // What bounds it: 4 D multiply-adds per row and token on the tensor cores against one
 // exponential (32 per clock and SM) and a handful of fp32 operations per row and token; the
-// cache's bytes are few.  When there are fewer CTAs than SMs, each CTA's cache range is cut
-// into pieces, joined by the last CTA to finish (fixed order).
+// cache's bytes are few.  One CTA per SM takes an equal share of the list of all blocks of
+// all (sequence, rows, head), whatever their lengths; where a share ends inside one, its parts
+// are joined by the last CTA to finish (fixed order: results do not depend on timing).
 #include <algorithm>
 
 #include "kv_cache.cuh"
@@ -35,6 +36,9 @@ constexpr int kMmaWarp = 8 + kCodeWarps;
 // warps 0-7 rows, 8-10 codes, 11 MMA: twelve warps may have 168 registers per thread
 constexpr int kThreads = 32 * (kMmaWarp + 1);
 constexpr int kMaxM = 16;
+// Starting rows costs a CTA about as much as kCost blocks; pieces shorter than kMinBlocks are
+// not worth joining.
+constexpr int kCost = 2, kMinBlocks = 4;
 constexpr float kLazy = 8.f;     // P <= 2^8 fits binary16 with room for its sums
 constexpr float kFar = 60.f;      // see weights()
 constexpr float kLog2e = 1.4426950408889634f;
@@ -190,31 +194,387 @@ __device__ __forceinline__ float weights(uint32_t ts, const float2 (&sc)[8], flo
   return l;
 }
 
-// What this CTA's rows see; token numbers relative to base.
+// What the rows of one (sequence, 256 rows) see; token numbers relative to base.  m counts
+// them: sequence m / tiles, rows 256 (m % tiles) and on.
 struct View {
   int64_t base, p0, first;
-  int lo, hi, cnt, rows, r0;
-  int b0, b1;  // its blocks
+  int lo, hi;    // hi < lo: nothing
+  int cnt, rows, r0;
+  int units;     // blocks, at least one
 };
 
+__device__ __forceinline__ View view_of(const CacheAttn& a, int m, int tiles, int G) {
+  View v;
+  const int n = m / tiles;
+  v.p0 = a.pos[n];
+  v.cnt = a.count ? a.count[n] : a.T;
+  v.first = a.first ? max((int64_t)0, a.first[n]) : 0;
+  const bool known = v.cnt >= 0 && v.cnt <= a.T && v.p0 >= 0;
+  if (!known) raise_status(a.status, kDevCheck);
+  v.cnt = known ? v.cnt : 0;
+  v.r0 = (m - n * tiles) * kRows;
+  v.rows = max(0, min(kRows, v.cnt * G - v.r0));
+  v.base = 0, v.lo = 0, v.hi = -1, v.units = 1;
+  const int64_t all_lo = max(v.first, a.W > 0 ? v.p0 - a.W + 1 : (int64_t)0), all_hi = v.p0 + v.cnt - 1;
+  if (v.rows > 0 && all_lo <= all_hi) {
+    if (!span_ok(a.c, all_lo, all_hi)) {
+      raise_status(a.status, kDevCheck);
+    } else {
+      const int64_t lo = max(v.first, a.W > 0 ? v.p0 + v.r0 / G - a.W + 1 : (int64_t)0);
+      const int64_t hi = v.p0 + (v.r0 + v.rows - 1) / G;
+      if (lo <= hi) {
+        v.base = lo & ~(int64_t)(kBlock - 1);
+        v.lo = (int)(lo - v.base);
+        v.hi = (int)(hi - v.base);
+        v.units = v.hi / kBlock + 1;
+      }
+    }
+  }
+  return v;
+}
+
+// What the CTA works on: blocks ua .. ub-1 of one view and head, and where it is in the list.
+struct Piece {
+  View v;
+  int64_t f, seg0;  // list indices: of the next piece, of view m's first entry (head 0)
+  int m, n, hk, ua, ub, seg;
+  int c0, c1;       // the CTAs that share it
+};
+
+// The queries of a piece, rotated and scaled to a power of two near 2^13, as swizzled tiles; rs
+// gets log2 e * scale * the power of two.  All warps.  Kept short on purpose: code that runs
+// once per piece costs its instruction fetches.  Scratch: the rows' places, then the (cos, sin)
+// pairs of the piece's tokens, in the key and value tiles.
+template <int D>
+__device__ __noinline__ void stage_queries(const CacheAttn& a, const Piece& s_p, unsigned char* tiles,
+                                           float* s_rs, int64_t* s_off, int* s_tok, float2* s_cs) {
+  constexpr int LPR = D / 4, RPI = 32 / LPR, WARPS = kThreads / 32;  // lanes per row, rows per step of a warp
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // every field once: through the references each use would be a load
+  const RopeArgs rope = a.rope;
+  const int G = a.H / a.c.Hk, rows = s_p.v.rows, r0 = s_p.v.r0, pairs = rope.rot / 2;
+  const bf16* q0 = static_cast<const bf16*>(a.q) + s_p.n * a.sq.n;
+  const float scale = a.scale * kLog2e;
+  const int t0 = r0 / G;
+  if (tid < kRows) {
+    // rows beyond the call's point at the piece's first, which exists
+    const int rr = r0 + tid < a.T * G ? r0 + tid : r0;
+    const int tt = rr / G, h = s_p.hk * G + rr - tt * G;
+    s_off[tid] = h * a.sq.h + tt * a.sq.t;
+    s_tok[tid] = tt - t0;
+  }
+  if (rope.turns && rows > 0) {
+    const int64_t p0 = s_p.v.p0 + t0;
+    const int n = ((r0 + rows - 1) / G - t0 + 1) * pairs;
+#pragma unroll 2
+    for (int e = tid; e < n; e += kThreads) {
+      const int t = e / pairs;
+      float2 f;
+      rope_angle(rope.turns[e - t * pairs], p0 + t, rope.factor, f.x, f.y);
+      s_cs[e] = f;
+    }
+  }
+  cta_sync();
+  const int d0 = (lane % LPR) * 4;
+  const bool half = rope.layout == LIZARD_ROPE_HALF, turn = rope.turns && d0 < rope.rot;
+  // where the pairs' other channels are, if they lie together
+  const int other = turn && half && pairs % 4 == 0 ? (d0 < pairs ? d0 + pairs : d0 - pairs) : d0;
+  constexpr int RW = 4;
+#pragma unroll 1
+  for (int rb = warp * RPI; rb < kRows; rb += RW * WARPS * RPI) {
+    // dead rows read row 0 (the loads stay free of branches, so all of them are in flight)
+    Raw4<bf16> x[RW], y[RW];
+#pragma unroll
+    for (int k = 0; k < RW; ++k) {
+      const int r = rb + k * WARPS * RPI + lane / LPR;
+      const bf16* qp = q0 + s_off[r < rows ? r : 0];
+      x[k] = raw4(qp + d0);
+      y[k] = raw4(qp + other);
+    }
+#pragma unroll
+    for (int k = 0; k < RW; ++k) {
+      const int r = rb + k * WARPS * RPI + lane / LPR;
+      const float4 xf = x[k].value(), yf = y[k].value();
+      float v[4] = {xf.x, xf.y, xf.z, xf.w}, o[4] = {yf.x, yf.y, yf.z, yf.w};
+      if (r >= rows) v[0] = v[1] = v[2] = v[3] = 0.f;
+      if (turn && half && pairs % 4 != 0) {  // the pairs' other channels, one by one
+        const bf16* qp = q0 + s_off[r < rows ? r : 0];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int e = d0 + i;
+          o[i] = e < rope.rot ? ld_f(qp + (e < pairs ? e + pairs : e - pairs)) : 0.f;
+        }
+      } else if (!half) {
+        o[0] = xf.y, o[1] = xf.x, o[2] = xf.w, o[3] = xf.z;
+      }
+      if (turn && r < rows) {
+        const float2* cs = s_cs + s_tok[r] * pairs;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int e = d0 + i;
+          if (e < rope.rot) {
+            const bool low = half ? e < pairs : (e & 1) == 0;
+            const float2 f = cs[half ? (low ? e : e - pairs) : e >> 1];
+            v[i] = v[i] * f.x + (low ? -o[i] : o[i]) * f.y;
+          }
+        }
+      }
+      float mx = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
+#pragma unroll
+      for (int o = LPR / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      const int e = max(-126, min((int)(__float_as_uint(mx) >> 23) - 127 - 13, 113));
+      const float inv = exp2_int(-e);
+      if (r < kRows) {
+        if (lane % LPR == 0) s_rs[r] = r < rows ? scale * exp2_int(e) : 1.f;
+        *reinterpret_cast<uint2*>(tiles + (r >> 7) * (kBlock * D * 2) + sw128_offset(r & 127, d0, kBlock)) =
+            make_uint2(half2_bits(v[0] * inv, v[1] * inv), half2_bits(v[2] * inv, v[3] * inv));
+      }
+    }
+  }
+  fence_proxy_async_smem();
+}
+
+// Where CTA c's partial result is: with the first block of its rows, or continuing them.
+template <int D>
+__device__ __forceinline__ size_t partial_at(int c, bool starts) {
+  return (size_t)(2 * c + (starts ? 1 : 0)) * kRows * (D + 4);
+}
+
+// What the output functions read, copied once.
+struct Out {
+  const bf16 *q, *mk, *mv, *add;  // q, add, y at the piece's sequence
+  bf16* y;
+  int64_t qh, qt, ah, at, yh, yt;
+  float scale, alpha;
+  int G, M, TG, hk, r0, rows;
+};
+__device__ __forceinline__ Out out_of(const CacheAttn& a, const Piece& p) {
+  Out o;
+  o.q = static_cast<const bf16*>(a.q) + p.n * a.sq.n;
+  o.mk = static_cast<const bf16*>(a.mk), o.mv = static_cast<const bf16*>(a.mv);
+  o.add = a.add ? static_cast<const bf16*>(a.add) + p.n * a.sadd.n : nullptr;
+  o.y = static_cast<bf16*>(a.y) + p.n * a.sy.n;
+  o.qh = a.sq.h, o.qt = a.sq.t, o.ah = a.sadd.h, o.at = a.sadd.t, o.yh = a.sy.h, o.yt = a.sy.t;
+  o.scale = a.scale * kLog2e, o.alpha = a.alpha;
+  o.G = a.H / a.c.Hk, o.M = a.M, o.TG = a.T * o.G, o.hk = p.hk, o.r0 = p.v.r0, o.rows = p.v.rows;
+  return o;
+}
+
+// Logits of the meta tokens of a row in units of log 2; they join its statistics.
+template <int D>
+__device__ __forceinline__ void with_meta(const Out& a, const bf16* q, int head, float (&zm)[kMaxM], float& m,
+                                          float& l) {
+  float top = m;
+#pragma unroll
+  for (int j = 0; j < kMaxM; ++j) {
+    zm[j] = -INFINITY;
+    if (j < a.M) {
+      const bf16* k = a.mk + ((size_t)head * a.M + j) * D;
+      float z = 0.f;
+#pragma unroll 4
+      for (int d = 0; d < D; d += 4) {
+        const float4 x = ld4(q + d), w = ld4(k + d);
+        z += x.x * w.x + x.y * w.y + x.z * w.z + x.w * w.w;
+      }
+      zm[j] = z * a.scale;
+      top = fmaxf(top, zm[j]);
+    }
+  }
+  l = m == -INFINITY ? 0.f : l * exp2f(m - top);
+#pragma unroll
+  for (int j = 0; j < kMaxM; ++j)
+    if (j < a.M) l += exp2f(zm[j] - top);
+  m = top;
+}
+
+// Four channels of a row: o in units of 2^mo, normalised by (m, l), with the meta tokens' values
+// and the other branch's output.
+template <int D>
+__device__ __forceinline__ float4 merged(const Out& a, float4 o, int head, int d, const float (&zm)[kMaxM],
+                                         const bf16* add, float m, float mo, float l) {
+  const float f = l > 0.f && mo != -INFINITY ? a.alpha / l * exp2f(mo - m) : 0.f;
+  float4 v = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+  if (a.M > 0) {
+    const float fm = l > 0.f ? a.alpha / l : 0.f;
+#pragma unroll
+    for (int j = 0; j < kMaxM; ++j)
+      if (j < a.M) {
+        const float w = exp2f(zm[j] - m) * fm;
+        const float4 x = ld4(a.mv + ((size_t)head * a.M + j) * D + d);
+        v.x = fmaf(w, x.x, v.x), v.y = fmaf(w, x.y, v.y), v.z = fmaf(w, x.z, v.z), v.w = fmaf(w, x.w, v.w);
+      }
+  }
+  if (add) {
+    const float4 x = ld4(add + d);
+    v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
+  }
+  return v;
+}
+
+// A finished piece's rows, one thread per row (the first 256 threads): `to` is the thread's
+// accumulator.
+template <int D>
+__device__ __noinline__ void write_rows(const CacheAttn& args, const Piece& p, uint32_t to, float m, float mo, float l) {
+  const Out a = out_of(args, p);
+  const int r = threadIdx.x, tt = (a.r0 + r) / a.G, head = a.hk * a.G + (a.r0 + r) % a.G;
+  const bool live = r < a.rows, in_call = a.r0 + r < a.TG;
+  bf16* y = a.y + head * a.yh + tt * a.yt;
+  const bf16* add = a.add ? a.add + head * a.ah + tt * a.at : nullptr;
+  float zm[kMaxM];
+  if (live && a.M > 0) with_meta<D>(a, a.q + head * a.qh + tt * a.qt, head, zm, m, l);
+#pragma unroll 1
+  for (int c = 0; c < D; c += 16) {
+    uint32_t u[16];
+    __syncwarp();
+    tmem_ld16(to + c, u);
+    tmem_ld_wait();
+    uint32_t w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (live) {
+#pragma unroll
+      for (int e = 0; e < 16; e += 4) {
+        const float4 o = merged<D>(a, make_float4(__uint_as_float(u[e]), __uint_as_float(u[e + 1]),
+                                                  __uint_as_float(u[e + 2]), __uint_as_float(u[e + 3])),
+                                   head, c + e, zm, add, m, mo, l);
+        w[e / 2] = pack_bf16x2(o.x, o.y), w[e / 2 + 1] = pack_bf16x2(o.z, o.w);
+      }
+    }
+    if (in_call) {
+      *reinterpret_cast<uint4*>(y + c) = make_uint4(w[0], w[1], w[2], w[3]);
+      *reinterpret_cast<uint4*>(y + c + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+  }
+}
+
+template <int D>
+__device__ __noinline__ void write_partial(float* mine, uint32_t to, float m, float mo, float l) {
+  const int r = threadIdx.x;
+  *reinterpret_cast<float4*>(mine + (size_t)kRows * D + 4 * r) = make_float4(m, mo, l, 0.f);
+#pragma unroll 1
+  for (int c = 0; c < D; c += 32) {
+    uint32_t u[32];
+    tmem_ld32(to + c, u);
+    tmem_ld_wait();
+#pragma unroll
+    for (int e = 0; e < 32; e += 4)
+      *reinterpret_cast<uint4*>(mine + (size_t)r * D + c + e) = make_uint4(u[e], u[e + 1], u[e + 2], u[e + 3]);
+  }
+}
+
+// The parts of CTAs c0 .. c1 joined.  First one thread per row merges the statistics (and the
+// meta tokens'), then D / 4 lanes per row add the outputs, each part with its weight.  Scratch:
+// per row the output maximum and the factor of the sum, then the meta tokens' weights.
+template <int D>
+__device__ __noinline__ void join_rows(const CacheAttn& args, const Piece& p, const float* part, float2* s_fin,
+                                       float* s_meta) {
+  constexpr int V4 = D / 4, STEP = kThreads / V4, RW = 4;
+  const Out a = out_of(args, p);
+  const int c0 = p.c0, c1 = p.c1, tid = threadIdx.x;
+  if (tid < a.rows) {
+    float m = -INFINITY, mo = -INFINITY, l = 0.f;
+#pragma unroll 4
+    for (int c = c0; c <= c1; ++c) {
+      const float4 x = __ldcg(reinterpret_cast<const float4*>(part + partial_at<D>(c, c == c0) + (size_t)kRows * D + 4 * tid));
+      const float mm = fmaxf(m, x.x);
+      if (x.x != -INFINITY) l = (m == -INFINITY ? 0.f : l * exp2f(m - mm)) + x.z * exp2f(x.x - mm);
+      m = mm, mo = fmaxf(mo, x.y);
+    }
+    float zm[kMaxM];
+    if (a.M > 0) {
+      const int tt = (a.r0 + tid) / a.G, head = a.hk * a.G + (a.r0 + tid) % a.G;
+      with_meta<D>(a, a.q + head * a.qh + tt * a.qt, head, zm, m, l);
+      const float f = l > 0.f ? a.alpha / l : 0.f;
+#pragma unroll
+      for (int j = 0; j < kMaxM; ++j)
+        if (j < a.M) s_meta[tid * kMaxM + j] = exp2f(zm[j] - m) * f;
+    }
+    s_fin[tid] = make_float2(mo, l > 0.f && mo != -INFINITY ? a.alpha / l * exp2f(mo - m) : 0.f);
+  }
+  __syncthreads();
+  const int k = tid % V4, d = 4 * k;
+  // every lane of a warp takes every step: the shuffles need them
+#pragma unroll 1
+  for (int rb = 0; rb < kRows && a.r0 + rb < a.TG; rb += RW * STEP) {
+    const int rl = rb + tid / V4;
+    float4 v[RW];
+#pragma unroll
+    for (int q = 0; q < RW; ++q) v[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+    for (int cb = c0; cb <= c1; cb += V4) {
+      float wk[RW];  // of part cb + k
+#pragma unroll
+      for (int q = 0; q < RW; ++q) {
+        const int r = rl + q * STEP;
+        wk[q] = 0.f;
+        if (r < a.rows && cb + k <= c1) {
+          const float mo = __ldcg(part + partial_at<D>(cb + k, cb + k == c0) + (size_t)kRows * D + 4 * r + 1);
+          if (mo != -INFINITY) wk[q] = exp2f(mo - s_fin[r].x);
+        }
+      }
+      const int cn = min(V4, c1 - cb + 1);
+#pragma unroll 1
+      for (int i = 0; i < cn; i += 2) {
+        float4 o[RW][2];
+#pragma unroll
+        for (int q = 0; q < RW; ++q)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            o[q][e] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (rl + q * STEP < a.rows && i + e < cn)
+              o[q][e] = __ldcg(reinterpret_cast<const float4*>(part + partial_at<D>(cb + i + e, cb + i + e == c0) +
+                                                               (size_t)(rl + q * STEP) * D + d));
+          }
+#pragma unroll
+        for (int q = 0; q < RW; ++q)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float w = __shfl_sync(0xffffffffu, wk[q], (i + e) & (V4 - 1), V4);
+            v[q].x = fmaf(w, o[q][e].x, v[q].x), v[q].y = fmaf(w, o[q][e].y, v[q].y);
+            v[q].z = fmaf(w, o[q][e].z, v[q].z), v[q].w = fmaf(w, o[q][e].w, v[q].w);
+          }
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < RW; ++q) {
+      const int r = rl + q * STEP;
+      if (r < kRows && a.r0 + r < a.TG) {
+        const int tt = (a.r0 + r) / a.G, head = a.hk * a.G + (a.r0 + r) - tt * a.G;
+        if (r < a.rows) {
+          const float f = s_fin[r].y;
+          v[q].x *= f, v[q].y *= f, v[q].z *= f, v[q].w *= f;
+          for (int j = 0; j < a.M; ++j) {
+            const float w = s_meta[r * kMaxM + j];
+            const float4 x = ld4(a.mv + ((size_t)head * a.M + j) * D + d);
+            v[q].x = fmaf(w, x.x, v[q].x), v[q].y = fmaf(w, x.y, v[q].y);
+            v[q].z = fmaf(w, x.z, v[q].z), v[q].w = fmaf(w, x.w, v[q].w);
+          }
+          if (a.add) {
+            const float4 x = ld4(a.add + head * a.ah + tt * a.at + d);
+            v[q].x += x.x, v[q].y += x.y, v[q].z += x.z, v[q].w += x.w;
+          }
+        }
+        st4(a.y + head * a.yh + tt * a.yt + d, v[q]);
+      }
+    }
+    __syncwarp();
+  }
+}
+
 template <int D, int F>
-__global__ void __launch_bounds__(kThreads, 1) prompt_kernel(CacheAttn a, int tiles, int splits) {
+__global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_constant__ CacheAttn a, int tiles) {
   using Sm = Smem<D>;
   extern __shared__ unsigned char smem_raw[];
   unsigned char* sm = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   __shared__ Ctl<NB> s_ctl;
   __shared__ float s_rs[kRows];
+  __shared__ int64_t s_off[kRows];
+  __shared__ int s_tok[kRows];
   __shared__ __align__(16) float2 s_scale[4][8];  // of a block's 16-token parts: key scale (0: unseen), log2 of the value scale
-  __shared__ View s_v;
+  __shared__ int64_t s_sum[kThreads / 32];
+  __shared__ Piece s_p;
   __shared__ int s_last;
   Ctl<NB>* ctl = &s_ctl;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int G = a.H / a.c.Hk, Hk = a.c.Hk;
-  // the tiles with the most to see first
-  const int split = blockIdx.x % splits, unit = blockIdx.x / splits;
-  const int nh = unit % (a.c.N * Hk), tile = tiles - 1 - unit / (a.c.N * Hk);
-  const int n = nh / Hk, hk = nh % Hk;
-
   if (warp == kMmaWarp) {
     tmem_alloc(&ctl->tmem, 512);
     tmem_relinquish();
@@ -231,116 +591,85 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(CacheAttn a, int ti
     fence_mbar_init();
   }
   pdl_wait();
-  if (tid == 0) {
-    View v;
-    v.p0 = a.pos[n];
-    v.cnt = a.count ? a.count[n] : a.T;
-    v.first = a.first ? max((int64_t)0, a.first[n]) : 0;
-    const bool known = v.cnt >= 0 && v.cnt <= a.T && v.p0 >= 0;
-    if (!known) raise_status(a.status, kDevCheck);
-    v.cnt = known ? v.cnt : 0;
-    v.r0 = tile * kRows;
-    v.rows = max(0, min(kRows, v.cnt * G - v.r0));
-    v.base = 0, v.lo = 0, v.hi = -1;
-    const int64_t all_lo = max(v.first, a.W > 0 ? v.p0 - a.W + 1 : (int64_t)0), all_hi = v.p0 + v.cnt - 1;
-    if (v.rows > 0 && all_lo <= all_hi) {
-      if (!span_ok(a.c, all_lo, all_hi)) {
-        raise_status(a.status, kDevCheck);
-      } else {
-        const int64_t lo = max(v.first, a.W > 0 ? v.p0 + v.r0 / G - a.W + 1 : (int64_t)0);
-        const int64_t hi = v.p0 + (v.r0 + v.rows - 1) / G;
-        if (lo <= hi) {
-          v.base = lo & ~(int64_t)(kBlock - 1);
-          v.lo = (int)(lo - v.base);
-          v.hi = (int)(hi - v.base);
-        }
+  // this CTA's share [f, f1) of the list: kCost empty entries, then the blocks, of each view
+  // and head (sequence-major, then rows, then head)
+  const int M2 = a.c.N * tiles;
+  int64_t share, f1;
+  {
+    const int mine = tid < M2 ? view_of(a, tid, tiles, G).units + kCost : 0;
+    int64_t c = mine;
+    for (int m = tid + kThreads; m < M2; m += kThreads) c += view_of(a, m, tiles, G).units + kCost;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
+    if (lane == 0) s_sum[warp] = c;
+    __syncthreads();
+    int64_t total = 0;
+    for (int w = 0; w < kThreads / 32; ++w) total += s_sum[w];
+    total *= Hk;
+    share = max((total + gridDim.x - 1) / gridDim.x, (int64_t)(kMinBlocks + kCost));
+    const int64_t f = blockIdx.x * share;
+    f1 = min(total, f + share);
+    int64_t before = 0;
+    for (int m0 = 0; f < total && m0 < M2; m0 += kThreads) {
+      const int m = m0 + tid;
+      const int64_t u = (int64_t)Hk * (m0 == 0 ? mine : m < M2 ? view_of(a, m, tiles, G).units + kCost : 0);
+      c = u;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, c, o);
+        if (lane >= o) c += x;
       }
+      __syncthreads();
+      if (lane == 31) s_sum[warp] = c;
+      __syncthreads();
+      for (int w = 0; w < warp; ++w) c += s_sum[w];
+      c += before;
+      if (f < c && f >= c - u) s_p.m = m, s_p.seg0 = c - u, s_p.f = f;
+      for (int w = 0; w < kThreads / 32; ++w) before += s_sum[w];
+      if (f < before) break;
     }
-    const int nb = v.hi < v.lo ? 0 : v.hi / kBlock + 1;
-    v.b0 = (int)((int64_t)nb * split / splits);
-    v.b1 = (int)((int64_t)nb * (split + 1) / splits);
-    s_v = v;
-  }
-  cta_sync();
-  const int rows = s_v.rows, r0 = s_v.r0, nblk = s_v.b1 - s_v.b0;
-
-  // ---- queries: rotated, scaled to a power of two near 2^13, as swizzled tiles
-  if (warp < 8) {
-    constexpr int LPR = D / 4, RPI = 32 / LPR;  // lanes per row, rows per step of a warp
-    const int d0 = (lane % LPR) * 4, hr = a.rope.rot / 2;
-    const bool half = a.rope.layout == LIZARD_ROPE_HALF;
-    float co[4], si[4];
-    int angle_of = -1;  // token whose angles co, si hold
-    for (int k0 = 0; k0 < 32; k0 += 4 * RPI) {
-      float x[4][4], y[4][4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int r = warp * 32 + k0 + k * RPI + lane / LPR;
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f), o = v;
-        if (r < rows) {
-          const int tt = (r0 + r) / G, h = hk * G + (r0 + r) % G;
-          const bf16* qp = static_cast<const bf16*>(a.q) + n * a.sq.n + h * a.sq.h + tt * a.sq.t;
-          v = ld4(qp + d0);
-          if (a.rope.turns && half && d0 < a.rope.rot) {
-            auto other = [&](int e) { return e < a.rope.rot ? ld_f(qp + (e < hr ? e + hr : e - hr)) : 0.f; };
-            if (hr % 4 == 0) o = ld4(qp + (d0 < hr ? d0 + hr : d0 - hr));
-            else o = make_float4(other(d0), other(d0 + 1), other(d0 + 2), other(d0 + 3));
-          } else {
-            o = make_float4(v.y, v.x, v.w, v.z);
-          }
-        }
-        x[k][0] = v.x, x[k][1] = v.y, x[k][2] = v.z, x[k][3] = v.w;
-        y[k][0] = o.x, y[k][1] = o.y, y[k][2] = o.z, y[k][3] = o.w;
-      }
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int r = warp * 32 + k0 + k * RPI + lane / LPR;
-        float v[4] = {x[k][0], x[k][1], x[k][2], x[k][3]};
-        if (a.rope.turns && r < rows && d0 < a.rope.rot) {
-          const int tt = (r0 + r) / G;
-          if (tt != angle_of) {
-            angle_of = tt;
-#pragma unroll 1
-            for (int i = 0; i < 4; ++i) {
-              const int e = d0 + i;
-              float c = 1.f, s = 0.f;
-              if (e < a.rope.rot) {
-                const bool low = half ? e < hr : (e & 1) == 0;
-                rope_angle(a.rope.turns[half ? (low ? e : e - hr) : e >> 1], s_v.p0 + tt, a.rope.factor, c, s);
-                if (low) s = -s;
-              }
-              if (i == 0) co[0] = c, si[0] = s;
-              else if (i == 1) co[1] = c, si[1] = s;
-              else if (i == 2) co[2] = c, si[2] = s;
-              else co[3] = c, si[3] = s;
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] = v[i] * co[i] + y[k][i] * si[i];
-        }
-        float mx = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
-#pragma unroll
-        for (int o = LPR / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        int e = (int)(__float_as_uint(mx) >> 23) - 127 - 13;
-        e = max(-126, min(e, 113));
-        const float inv = exp2_int(-e);
-        if (lane % LPR == 0) s_rs[r] = r < rows ? a.scale * kLog2e * exp2_int(e) : 1.f;
-        *reinterpret_cast<uint2*>(sm + Sm::Q + (r >> 7) * Sm::kTile + sw128_offset(r & 127, d0, kBlock)) =
-            make_uint2(half2_bits(v[0] * inv, v[1] * inv), half2_bits(v[2] * inv, v[3] * inv));
-      }
-    }
-    fence_proxy_async_smem();
+    if (f >= total && tid == 0) s_p.f = f1;
   }
   tc_fence_before();
   cta_sync();
   tc_fence_after();
   const uint32_t tmem = ctl->tmem;
-
   // one answer for the warp: what follows a wait is executed by all its lanes together
   auto wait_all = [&](int b, uint32_t parity) {
     const bool o = wait_bar(ctl, b, parity);
     return __all_sync(0xffffffffu, o) != 0;
   };
+  int it = 0;  // blocks done in earlier pieces: stages and phases go on from there
+
+  while (true) {
+  if (tid == 0) {
+    Piece& p = s_p;
+    p.ub = 0;
+    if (p.f < f1) {
+      p.v = view_of(a, p.m, tiles, G);
+      p.n = p.m / tiles;
+      const int entries = p.v.units + kCost;
+      p.hk = (int)((p.f - p.seg0) / entries);
+      const int64_t next = p.seg0 + (int64_t)(p.hk + 1) * entries, head0 = next - p.v.units;
+      p.ua = (int)max((int64_t)0, p.f - head0);
+      // 0: the share ends before this head's first block
+      p.ub = (int)max((int64_t)0, min((int64_t)p.v.units, f1 - head0));
+      p.seg = p.m * Hk + p.hk;
+      p.c0 = (int)(head0 / share);
+      p.c1 = (int)((next - 1) / share);
+      p.f = next;
+      if (p.hk == Hk - 1) p.seg0 = next, ++p.m;
+    }
+  }
+  cta_sync();
+  if (s_p.ub == 0) break;
+  const View& s_v = s_p.v;
+  const int n = s_p.n, hk = s_p.hk, b0 = s_p.ua, nblk = s_p.ub - s_p.ua;
+  const int rows = s_v.rows, r0 = s_v.r0;
+
+  stage_queries<D>(a, s_p, sm + Sm::Q, s_rs, s_off, s_tok, reinterpret_cast<float2*>(sm + Sm::K));
+  cta_sync();
+
   bool done_ok = true;
   float l = 0.f, m = -INFINITY, mo = -INFINITY;
   if (warp == kMmaWarp) {
@@ -355,7 +684,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(CacheAttn a, int ti
       const uint32_t id_s = idesc_f16(128, kBlock, false), id_o = idesc_f16(128, D, true);
       bool ok = true;
       auto scores = [&](int t, int i) {
-        const uint64_t qa = dq + t * kTile16, kb = dk + (i & 1) * kTile16;
+        const uint64_t qa = dq + t * kTile16, kb = dk + (i & 1) * kTile16;  // i counts over all pieces
         const uint32_t ts = tmem + t * kBlock;
 #pragma unroll
         for (int j = 0; j < D / 16; ++j) {
@@ -366,11 +695,12 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(CacheAttn a, int ti
         mma_commit(&ctl->bar[SF + t]);
         if (t == 1) mma_commit(&ctl->bar[KE + (i & 1)]);
       };
-      if (nblk > 0 && (ok = wait_bar(ctl, KF, 0))) {
+      const int end = it + nblk;
+      if ((ok = wait_bar(ctl, KF + (it & 1), (it >> 1) & 1))) {
         tc_fence_after();
-        scores(0, 0), scores(1, 0);
+        scores(0, it), scores(1, it);
       }
-      for (int i = 0; ok && i < nblk; ++i) {
+      for (int i = it; ok && i < end; ++i) {
         const uint32_t par = (i >> 1) & 1;
         ok = wait_bar(ctl, VF + (i & 1), par);
         for (int t = 0; ok && t < 2; ++t) {
@@ -379,10 +709,10 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(CacheAttn a, int ti
           const uint64_t vb = dv + (i & 1) * kTile16;
           const uint32_t to = tmem + 256 + t * D, ts = tmem + t * kBlock;
 #pragma unroll
-          for (int j = 0; j < kBlock / 16; ++j) mma_f16_ts(to, ts + 8 * j, vb + j * 128, id_o, j > 0 || i > 0);
+          for (int j = 0; j < kBlock / 16; ++j) mma_f16_ts(to, ts + 8 * j, vb + j * 128, id_o, j > 0 || i > it);
           mma_commit(&ctl->bar[OD + t]);
           if (t == 1) mma_commit(&ctl->bar[VE + (i & 1)]);
-          if (i + 1 < nblk) {
+          if (i + 1 < end) {
             if (t == 0 && !(ok = wait_bar(ctl, KF + ((i + 1) & 1), ((i + 1) >> 1) & 1))) break;
             tc_fence_after();
             scores(t, i + 1);
@@ -390,8 +720,6 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(CacheAttn a, int ti
         }
       }
       if (!ok) ctl->abort = 1;
-      mma_commit(&ctl->bar[DONE]);
-      drain_bar(ctl, DONE, 1, globaltimer_ns());
     }
   } else if (warp >= 8) {
     // ------------------------------------------------------------------ codes -> binary16
@@ -407,12 +735,13 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(CacheAttn a, int ti
     // Four blocks are looked up at a time, the next four while these are converted: lane
     // 8 b + p has part p of block b, where it is (in parts of 16 rows) and its scales.
     int at = -1, nat = -1;
+    uint32_t full = 0, nfull = 0;  // the lanes whose part exists
     float2 sc = make_float2(0.f, 0.f), nsc = sc;
     auto look = [&](int i) {
       i += lane >> 3;
       nat = -1;
       nsc = make_float2(0.f, 0.f);
-      const int tok = (s_v.b0 + i) * kBlock + (lane & 7) * 16;
+      const int tok = (b0 + i) * kBlock + (lane & 7) * 16;
       if (i < nblk && tok + 15 >= lo && tok <= hi) {
         const int id = pool_page(a.c, n, (uint32_t)((base + tok) >> a.c.log_p));
         if (id < 0) {
@@ -423,11 +752,26 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(CacheAttn a, int ti
           nsc = make_float2(a.c.ks[ph], (float)((int)(__float_as_uint(a.c.vs[ph]) >> 23 & 0xff) - 127));
         }
       }
+      nfull = __ballot_sync(0xffffffffu, nat >= 0);
     };
     auto load = [&](const unsigned char* pool, int i, uint4 (&u)[NP][IT]) {
-      const int tok = (s_v.b0 + i) * kBlock;
+      const int tok = (b0 + i) * kBlock;
+      if (i < nblk && tok >= lo && tok + kBlock - 1 <= hi &&
+          (((i & 3) ? full : nfull) >> ((i & 3) * 8) & 0xff) == 0xff) {
+#pragma unroll
+        for (int q = 0; q < NP; ++q) {
+          const int p = w + q * kCodeWarps;
+          const int part = __shfl_sync(0xffffffffu, (i & 3) ? at : nat, (i & 3) * 8 + (p & 7));
+          const unsigned char* src = pool + (size_t)part * (16 * D) + row * D;
+          if (p < 8) {
+#pragma unroll
+            for (int k = 0; k < IT; ++k)
+              u[q][k] = *reinterpret_cast<const uint4*>(src + k * RPS * D + 16 * chunk_place<D>(row + k * RPS, chunk));
+          }
+        }
+        return;
+      }
       // parts that end beyond what is seen hold bytes that were never written
-      const bool inner = tok >= lo && tok + kBlock - 1 <= hi;
 #pragma unroll
       for (int q = 0; q < NP; ++q) {
         const int p = w + q * kCodeWarps;
@@ -438,7 +782,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(CacheAttn a, int ti
         for (int k = 0; k < IT; ++k) {
           const int r = row + k * RPS, tk = tok + 16 * p + r;
           u[q][k] = make_uint4(0, 0, 0, 0);
-          if (p < 8 && i < nblk && part >= 0 && (inner || (tk >= lo && tk <= hi)))
+          if (p < 8 && i < nblk && part >= 0 && tk >= lo && tk <= hi)
             u[q][k] = *reinterpret_cast<const uint4*>(src + r * D + 16 * chunk_place<D>(r, chunk));
         }
       }
@@ -468,25 +812,25 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(CacheAttn a, int ti
     load(a.c.v, 0, vu);
     bool ok = true;
     for (int i = 0; i < nblk; ++i) {
-      const int st = i & 1;
-      const uint32_t free_par = ((i >> 1) & 1) ^ 1;
+      const int gi = it + i, st = gi & 1;  // gi counts over all pieces
+      const uint32_t free_par = ((gi >> 1) & 1) ^ 1;
       if ((i & 3) == 0) {
-        at = nat, sc = nsc;
+        at = nat, sc = nsc, full = nfull;
         look(i + 4);
       }
-      if (i >= 2 && !(ok = wait_all(KE + st, free_par))) break;
+      if (gi >= 2 && !(ok = wait_all(KE + st, free_par))) break;
       // Block i - 4's scales are no longer read: the keys' stage is free, so the scores of block
       // i - 2 are done, which were issued after every row had finished block i - 3.
       if (w == 0) {
-        if (lane >> 3 == (i & 3)) s_scale[i & 3][lane & 7] = sc;
+        if (lane >> 3 == (i & 3)) s_scale[gi & 3][lane & 7] = sc;
         __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl->bar[SC + (i & 3)]);
+        if (lane == 0) mbar_arrive(&ctl->bar[SC + (gi & 3)]);
       }
       convert(sm + Sm::K + st * Sm::kTile, ku);
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->bar[KF + st]);
       load(a.c.k, i + 1, ku);
-      if (i >= 2 && !(ok = wait_all(VE + st, free_par))) break;
+      if (gi >= 2 && !(ok = wait_all(VE + st, free_par))) break;
       convert(sm + Sm::V + st * Sm::kTile, vu);
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->bar[VF + st]);
@@ -511,13 +855,14 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(CacheAttn a, int ti
     const int all_hi = last >= 128 * t ? (int)(s_v.p0 + (r0 + 128 * t) / G - s_v.base) : 0x7fffffff;
     bool ok = true;
     for (int i = 0; i < nblk; ++i) {
-      const int tok = (s_v.b0 + i) * kBlock;
-      if (!(ok = wait_all(SC + (i & 3), (i >> 2) & 1) && wait_all(SF + t, i & 1))) break;
+      const int tok = (b0 + i) * kBlock;
+      const int gi = it + i;  // counts over all pieces
+      if (!(ok = wait_all(SC + (gi & 3), (gi >> 2) & 1) && wait_all(SF + t, gi & 1))) break;
       tc_fence_after();
       float2 sc[8];
 #pragma unroll
       for (int b = 0; b < 8; b += 2) {
-        const float4 x = *reinterpret_cast<const float4*>(&s_scale[i & 3][b]);
+        const float4 x = *reinterpret_cast<const float4*>(&s_scale[gi & 3][b]);
         sc[b] = make_float2(x.x, x.y), sc[b + 1] = make_float2(x.z, x.w);
       }
       bool checked = tok < all_lo || tok + kBlock - 1 > all_hi;
@@ -535,7 +880,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(CacheAttn a, int ti
         const float f = mon > mo ? exp2f(mo - mon) : 1.f;
         mo = fmaxf(mo, mon);
         if (i > 0) {
-          if (!(ok = wait_all(OD + t, (i - 1) & 1))) break;
+          if (!(ok = wait_all(OD + t, (gi - 1) & 1))) break;
           tc_fence_after();
 #pragma unroll 1
           for (int c = 0; c < D; c += 32) {
@@ -560,94 +905,46 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(CacheAttn a, int ti
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->bar[PF + t]);
     }
-    if (ok && nblk > 0 && (ok = wait_all(OD + t, (nblk - 1) & 1))) tc_fence_after();
+    if (ok && (ok = wait_all(OD + t, (it + nblk - 1) & 1))) tc_fence_after();
     if (!ok) ctl->abort = 1;
     done_ok = ok;
   }
 
   // ---- output
-  const bool alone = splits == 1;
-  float* part = reinterpret_cast<float*>(a.ws + (((size_t)tiles * a.c.N * Hk * sizeof(unsigned) + 255) & ~(size_t)255));
-  const int r = tid;  // row of the CTA (the first 256 threads)
-  const int tt = (r0 + r) / G, head = hk * G + (r0 + r) % G;
-  const bool in_call = tid < kRows && r0 + r < a.T * G;
-  bf16* y = static_cast<bf16*>(a.y) + n * a.sy.n + head * a.sy.h + tt * a.sy.t;
-  const bf16* add = a.add ? static_cast<const bf16*>(a.add) + n * a.sadd.n + head * a.sadd.h + tt * a.sadd.t : nullptr;
-  // The meta tokens join a row's statistics; their logits stay for the values' weights.
-  float zm[kMaxM];
-  auto with_meta = [&](float& m_, float& l_) {
-    const bf16* qp = static_cast<const bf16*>(a.q) + n * a.sq.n + head * a.sq.h + tt * a.sq.t;
-    float top = m_;
-#pragma unroll
-    for (int j = 0; j < kMaxM; ++j) {
-      zm[j] = -INFINITY;
-      if (j < a.M) {
-        const bf16* k = static_cast<const bf16*>(a.mk) + ((size_t)head * a.M + j) * D;
-        float z = 0.f;
-#pragma unroll 1
-        for (int d = 0; d < D; d += 4) {
-          const float4 x = ld4(qp + d), w = ld4(k + d);
-          z += x.x * w.x + x.y * w.y + x.z * w.z + x.w * w.w;
-        }
-        zm[j] = z * a.scale * kLog2e;
-        top = fmaxf(top, zm[j]);
-      }
+  const bool alone = s_p.ua == 0 && s_p.ub == s_v.units;
+  float* part = reinterpret_cast<float*>(a.ws + (((size_t)M2 * Hk * sizeof(unsigned) + 255) & ~(size_t)255));
+  auto slot = [&](int c) { return part + partial_at<D>(c, c == s_p.c0); };
+  if (warp < 8 && __all_sync(0xffffffffu, done_ok && !*(volatile int*)&ctl->abort)) {
+    const uint32_t to = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 256 + (warp >> 2) * D;
+    if (alone) write_rows<D>(a, s_p, to, m, mo, l);
+    else write_partial<D>(slot(blockIdx.x), to, m, mo, l);
+  }
+  it += nblk;
+  tc_fence_before();
+  cta_sync();
+  tc_fence_after();
+  if (*(volatile int*)&ctl->abort) break;
+  if (!alone) {
+    __threadfence();
+    __syncthreads();
+    unsigned* counter = reinterpret_cast<unsigned*>(a.ws) + s_p.seg;
+    const int c0 = s_p.c0, c1 = s_p.c1;
+    if (tid == 0) s_last = atomicAdd(counter, 1u) == (unsigned)(c1 - c0);
+    __syncthreads();
+    if (s_last) {
+      __threadfence();
+      join_rows<D>(a, s_p, part, reinterpret_cast<float2*>(sm + Sm::K), reinterpret_cast<float*>(sm + Sm::V));
+      if (tid == 0) *counter = 0u;
     }
-    l_ = m_ == -INFINITY ? 0.f : l_ * exp2f(m_ - top);
-#pragma unroll
-    for (int j = 0; j < kMaxM; ++j)
-      if (j < a.M) l_ += exp2f(zm[j] - top);
-    m_ = top;
-  };
-  // Four channels of a row: o in units of 2^mo_, to be normalised by (m_, l_).
-  auto finish = [&](float4 o, int d, float m_, float mo_, float l_) {
-    const float f = l_ > 0.f && mo_ != -INFINITY ? a.alpha / l_ * exp2f(mo_ - m_) : 0.f;
-    float4 v = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
-    if (f == 0.f) v = make_float4(0.f, 0.f, 0.f, 0.f);  // o may hold nothing
-    if (a.M > 0) {
-      const float fm = l_ > 0.f ? a.alpha / l_ : 0.f;
-#pragma unroll
-      for (int j = 0; j < kMaxM; ++j)
-        if (j < a.M) {
-          const float w = exp2f(zm[j] - m_) * fm;
-          const float4 x = ld4(static_cast<const bf16*>(a.mv) + ((size_t)head * a.M + j) * D + d);
-          v.x = fmaf(w, x.x, v.x), v.y = fmaf(w, x.y, v.y), v.z = fmaf(w, x.z, v.z), v.w = fmaf(w, x.w, v.w);
-        }
+  }
+  cta_sync();  // before s_p and the queries' tiles are written again
+  }
+  if (warp == kMmaWarp) {
+    if (lane == 0) {
+      mma_commit(&ctl->bar[DONE]);
+      drain_bar(ctl, DONE, 1, globaltimer_ns());
     }
-    if (add) {
-      const float4 x = ld4(add + d);
-      v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
-    }
-    return v;
-  };
-  const bool live = tid < kRows && r < rows && done_ok;
-  if (warp < 8 && __all_sync(0xffffffffu, !*(volatile int*)&ctl->abort)) {
-    const int t = warp >> 2;
-    const uint32_t to = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 256 + t * D;
-    float m_ = m, l_ = l;
-    if (alone && a.M > 0 && live) with_meta(m_, l_);
-    float* mine = part + (size_t)blockIdx.x * kRows * (D + 4);
-    if (!alone) *reinterpret_cast<float4*>(mine + (size_t)kRows * D + 4 * r) = make_float4(m, mo, l, 0.f);
-#pragma unroll 1
-    for (int c = 0; c < D; c += 16) {
-      uint32_t u[16];
-      __syncwarp();
-      if (nblk > 0) {
-        tmem_ld16(to + c, u);
-        tmem_ld_wait();
-      } else {
-#pragma unroll
-        for (int e = 0; e < 16; ++e) u[e] = 0;
-      }
-#pragma unroll
-      for (int e = 0; e < 16; e += 4) {
-        float4 o = make_float4(__uint_as_float(u[e]), __uint_as_float(u[e + 1]), __uint_as_float(u[e + 2]),
-                               __uint_as_float(u[e + 3]));
-        if (!alone) *reinterpret_cast<float4*>(mine + (size_t)r * D + c + e) = o;
-        else if (live) st4(y + c + e, finish(o, c + e, m_, mo, l_));
-        else if (in_call) st4(y + c + e, make_float4(0.f, 0.f, 0.f, 0.f));
-      }
-    }
+    __syncwarp();
   }
   tc_fence_before();
   cta_sync();
@@ -655,65 +952,20 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(CacheAttn a, int ti
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
-  if (*(volatile int*)&ctl->abort) {
-    if (tid == 0) raise_status(a.status, kDevTimeout);
-  } else if (!alone) {
-    __threadfence();
-    __syncthreads();
-    unsigned* counter = reinterpret_cast<unsigned*>(a.ws) + unit;
-    if (tid == 0) s_last = atomicAdd(counter, 1u) == (unsigned)(splits - 1);
-    __syncthreads();
-    if (s_last && tid < kRows) {
-      __threadfence();
-      const float* p0 = part + (size_t)unit * splits * kRows * (D + 4);
-      const size_t step = (size_t)kRows * (D + 4);
-      float m_ = -INFINITY, mo_ = -INFINITY, l_ = 0.f;
-      for (int s = 0; s < splits; ++s) {
-        const float4 x = __ldcg(reinterpret_cast<const float4*>(p0 + s * step + (size_t)kRows * D + 4 * r));
-        m_ = fmaxf(m_, x.x), mo_ = fmaxf(mo_, x.y);
-      }
-      for (int s = 0; s < splits; ++s) {
-        const float4 x = __ldcg(reinterpret_cast<const float4*>(p0 + s * step + (size_t)kRows * D + 4 * r));
-        if (x.x != -INFINITY) l_ += x.z * exp2f(x.x - m_);
-      }
-      if (r < rows && a.M > 0) with_meta(m_, l_);
-      if (in_call)
-#pragma unroll 1
-        for (int d = 0; d < D; d += 4) {
-          float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (r < rows) {
-            for (int s = 0; s < splits; ++s) {
-              const float mos = __ldcg(p0 + s * step + (size_t)kRows * D + 4 * r + 1);
-              if (mos == -INFINITY) continue;
-              const float w = exp2f(mos - mo_);
-              const float4 x = __ldcg(reinterpret_cast<const float4*>(p0 + s * step + (size_t)r * D + d));
-              o.x = fmaf(w, x.x, o.x), o.y = fmaf(w, x.y, o.y), o.z = fmaf(w, x.z, o.z), o.w = fmaf(w, x.w, o.w);
-            }
-            o = finish(o, d, m_, mo_, l_);
-          }
-          st4(y + d, o);
-        }
-      if (tid == 0) *counter = 0u;
-    }
-  }
+  if (*(volatile int*)&ctl->abort && tid == 0) raise_status(a.status, kDevTimeout);
   pdl_trigger();
 }
 
-// CTAs of one wave; pieces a CTA's range is cut into when there are fewer CTAs than that.
-constexpr int kWave = 152;
-int split_count(int ctas) { return std::max(1, std::min(64, kWave / ctas)); }
+constexpr int kMaxCtas = 152;  // one per SM; sizes the scratch
 
 template <int D, int F>
 cudaError_t launch(const CacheAttn& a, cudaStream_t s, int* launches) {
   const int tiles = (a.H / a.c.Hk * a.T + kRows - 1) / kRows;
-  const int64_t ctas = (int64_t)tiles * a.c.N * a.c.Hk;
-  const int splits = ctas < kWave ? split_count((int)ctas) : 1;
-  if (ctas * splits > 0x7fffffffll) return cudaErrorInvalidValue;
   constexpr int smem = Smem<D>::kBytes + 1024;
   cudaError_t e = cudaFuncSetAttribute(prompt_kernel<D, F>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   trace_begin("cache_attn_prompt", s);
-  e = launch_pdl(prompt_kernel<D, F>, dim3((unsigned)(ctas * splits)), dim3(kThreads), smem, s, a, tiles, splits);
+  e = launch_pdl(prompt_kernel<D, F>, dim3(std::min(ctas_per_wave(1), kMaxCtas)), dim3(kThreads), smem, s, a, tiles);
   trace_end(s);
   ++*launches;
   return e;
@@ -725,10 +977,9 @@ bool cache_attn_tc_used(int H, int Hk, int T, lizard_dtype dt) { return dt == LI
 
 size_t cache_attn_tc_workspace(int N, int Hk, int H, int T, int d) {
   const int tiles = (H / Hk * T + kRows - 1) / kRows;
-  const int64_t ctas = (int64_t)tiles * N * Hk;
-  const int splits = ctas < kWave ? split_count((int)ctas) : 1;
-  const size_t counters = align_up((size_t)ctas * sizeof(unsigned), 256);
-  return splits > 1 ? counters + (size_t)ctas * splits * kRows * (d + 4) * sizeof(float) : counters;
+  // a counter per (sequence, rows, head), then two partial results per CTA
+  return align_up((size_t)tiles * N * Hk * sizeof(unsigned), 256) +
+         (size_t)2 * kMaxCtas * kRows * (d + 4) * sizeof(float);
 }
 
 cudaError_t launch_cache_attn_tc(const CacheAttn& a, cudaStream_t s, int* launches) {

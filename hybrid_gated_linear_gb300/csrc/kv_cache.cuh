@@ -82,6 +82,23 @@ __device__ __forceinline__ int scale_exponent(float amax) {
 
 __device__ __forceinline__ float exp2_int(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
 
+// Four consecutive elements as loaded, and as floats: loads in one loop, conversions (the
+// first uses, which wait) in the next.
+template <typename T> struct Raw4;
+template <> struct alignas(16) Raw4<float> {
+  float4 v;
+  __device__ __forceinline__ float4 value() const { return v; }
+};
+template <> struct alignas(8) Raw4<bf16> {
+  uint2 v;
+  __device__ __forceinline__ float4 value() const {
+    return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xffff0000u), __uint_as_float(v.y << 16),
+                       __uint_as_float(v.y & 0xffff0000u));
+  }
+};
+template <typename T>
+__device__ __forceinline__ Raw4<T> raw4(const T* p) { return *reinterpret_cast<const Raw4<T>*>(p); }
+
 // cos and sin of position p of a pair (times the factor): p * turns wraps to the exact
 // fraction of a turn; its upper 32 bits, as a signed count of half turns / 2^31, are rounded
 // once to fp32 (an angle error of pi 2^-25 at most).
