@@ -4,8 +4,9 @@
 // Rows are the G = H / Hk query heads times the new tokens of a (sequence, key head), row =
 // token * G + head.  One CTA takes 256 rows (two tiles of 128, the M of an MMA) and walks
 // over the visible cache in blocks of 128 tokens:
-//   3 warps   turn a block's codes into binary16 tiles (each code is exact in 11 bits); the
-//             copy from global memory runs one block ahead in registers
+//   3 warps   turn a block's codes into binary16 tiles (each code is exact in 11 bits); bulk
+//             copies bring the codes into shared memory one block ahead (loads into registers
+//             kept these warps waiting: 1.31 ms against 1.0 for 2 x 2048 tokens at 16384)
 //   1 thread  issues S = Q K^T (operands in shared memory) and O += P V (P in tensor memory)
 //   2 x 4 warps, one thread per row: running maxima and sum, P = 2^(z + e - mo) as binary16
 //             over the columns S was read from
@@ -44,8 +45,9 @@ constexpr float kFar = 60.f;      // see weights()
 constexpr float kLog2e = 1.4426950408889634f;
 
 // Barriers: operand tiles full and free (two stages each), per row tile scores ready, weights
-// written and output updated, scales of a block written (a ring of four).
-enum { KF = 0, VF = 2, KE = 4, VE = 6, SF = 8, PF = 10, OD = 12, SC = 14, DONE = 18, NB = 19 };
+// written and output updated, scales of a block written (a ring of four); then the codes of
+// keys and values in shared memory (RF, RF + 1) and read (RE, RE + 1).
+enum { KF = 0, VF = 2, KE = 4, VE = 6, SF = 8, PF = 10, OD = 12, SC = 14, RF = 18, RE = 20, DONE = 22, NB = 23 };
 
 template <int D>
 struct Smem {
@@ -53,7 +55,9 @@ struct Smem {
   static constexpr int Q = 0;                     // two tiles of 128 rows
   static constexpr int K = Q + 2 * kTile;         // two stages
   static constexpr int V = K + 2 * kTile;
-  static constexpr int kBytes = V + 2 * kTile;    // 192 KiB at D = 128
+  static constexpr int kRaw = kBlock * D;         // a block's codes
+  static constexpr int R = V + 2 * kTile;         // of the keys, then of the values
+  static constexpr int kBytes = R + 2 * kRaw;     // 224 KiB at D = 128
 };
 
 __device__ __forceinline__ uint32_t idesc_f16(int M, int N, bool b_mn_major) {
@@ -566,8 +570,6 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   unsigned char* sm = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   __shared__ Ctl<NB> s_ctl;
   __shared__ float s_rs[kRows];
-  __shared__ int64_t s_off[kRows];
-  __shared__ int s_tok[kRows];
   __shared__ __align__(16) float2 s_scale[4][8];  // of a block's 16-token parts: key scale (0: unseen), log2 of the value scale
   __shared__ int64_t s_sum[kThreads / 32];
   __shared__ Piece s_p;
@@ -586,6 +588,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       mbar_init(&ctl->bar[SF + i], 1), mbar_init(&ctl->bar[PF + i], 4), mbar_init(&ctl->bar[OD + i], 1);
     }
     for (int i = 0; i < 4; ++i) mbar_init(&ctl->bar[SC + i], 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&ctl->bar[RF + i], 1), mbar_init(&ctl->bar[RE + i], kCodeWarps);
     mbar_init(&ctl->bar[DONE], 1);
     ctl->abort = 0;
     fence_mbar_init();
@@ -667,7 +670,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   const int n = s_p.n, hk = s_p.hk, b0 = s_p.ua, nblk = s_p.ub - s_p.ua;
   const int rows = s_v.rows, r0 = s_v.r0;
 
-  stage_queries<D>(a, s_p, sm + Sm::Q, s_rs, s_off, s_tok, reinterpret_cast<float2*>(sm + Sm::K));
+  stage_queries<D>(a, s_p, sm + Sm::Q, s_rs, reinterpret_cast<int64_t*>(sm + Sm::R),
+                   reinterpret_cast<int*>(sm + Sm::R) + 2 * kRows, reinterpret_cast<float2*>(sm + Sm::K));
   cta_sync();
 
   bool done_ok = true;
@@ -724,79 +728,78 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   } else if (warp >= 8) {
     // ------------------------------------------------------------------ codes -> binary16
     // Warp w takes the 16-token parts w, w + 3, w + 6 of a block: IT steps of 32 chunks each.
-    constexpr int IT = D / 32, RPS = 16 / IT, NP = (8 + kCodeWarps - 1) / kCodeWarps;
+    constexpr int IT = D / 32, NP = (8 + kCodeWarps - 1) / kCodeWarps;
     const int w = warp - 8;
-    // Eight lanes that store together hold half rows (64 channels) of two rows: their stores
-    // fall into different banks.  A step adds 4 (8) rows.
-    const int row = D == 128 ? 2 * (lane >> 4) + ((lane >> 2) & 1) : lane >> 2;
+    // Eight lanes that access together hold four chunks each of two rows.  At D = 128 the rows
+    // are r and r ^ 5: the codes they read lie in different halves of the banks (chunk c of row r
+    // is at place c ^ (r & 7)), and so do the binary16 chunks they store, 2 c ^ (r & 7).
     const int chunk = D == 128 ? 4 * ((lane >> 3) & 1) + (lane & 3) : lane & 3;
+    const int row = D == 128 ? ((lane >> 4) & 1) ^ ((lane & 4) ? 5 : 0) : lane >> 2;
+    auto row_of = [&](int k) { return D == 128 ? 8 * (k >> 1) + (row ^ (2 * (k & 1))) : 8 * k + row; };
     const int lo = s_v.lo, hi = s_v.hi;
     const int64_t base = s_v.base;
-    // Four blocks are looked up at a time, the next four while these are converted: lane
-    // 8 b + p has part p of block b, where it is (in parts of 16 rows) and its scales.
-    int at = -1, nat = -1;
+    // Four blocks are looked up at a time: lane 8 b + p has part p of block b.  The page numbers
+    // of the batch after next are on their way while the next batch's scales are.
+    int at = -1, nat = -1;  // where the part is (in parts of 16 rows; -1: unseen)
     uint32_t full = 0, nfull = 0;  // the lanes whose part exists
     float2 sc = make_float2(0.f, 0.f), nsc = sc;
+    int id = -1;
+    auto token = [&](int i) { return (b0 + i + (lane >> 3)) * kBlock + (lane & 7) * 16; };
     auto look = [&](int i) {
-      i += lane >> 3;
+      id = -2;  // nothing to see
+      const int tok = token(i);
+      if (i + (lane >> 3) < nblk && tok + 15 >= lo && tok <= hi)
+        id = a.c.table[(size_t)n * a.c.max_pages + (uint32_t)((base + tok) >> a.c.log_p) % (uint32_t)a.c.max_pages];
+    };
+    auto find = [&](int i) {
       nat = -1;
       nsc = make_float2(0.f, 0.f);
-      const int tok = (b0 + i) * kBlock + (lane & 7) * 16;
-      if (i < nblk && tok + 15 >= lo && tok <= hi) {
-        const int id = pool_page(a.c, n, (uint32_t)((base + tok) >> a.c.log_p));
-        if (id < 0) {
-          raise_status(a.status, kDevCheck);
-        } else {
-          const size_t ph = (size_t)id * Hk + hk;
-          nat = (int)((ph * a.c.P + (int)((base + tok) & (a.c.P - 1))) >> 4);
-          nsc = make_float2(a.c.ks[ph], (float)((int)(__float_as_uint(a.c.vs[ph]) >> 23 & 0xff) - 127));
-        }
+      if ((unsigned)id < (unsigned)a.c.pages) {
+        const size_t ph = (size_t)id * Hk + hk;
+        nat = (int)((ph * a.c.P + (int)((base + token(i)) & (a.c.P - 1))) >> 4);
+        nsc = make_float2(a.c.ks[ph], a.c.vs[ph]);
+      } else if (id != -2) {
+        raise_status(a.status, kDevCheck);
       }
       nfull = __ballot_sync(0xffffffffu, nat >= 0);
     };
-    auto load = [&](const unsigned char* pool, int i, uint4 (&u)[NP][IT]) {
-      const int tok = (b0 + i) * kBlock;
-      if (i < nblk && tok >= lo && tok + kBlock - 1 <= hi &&
-          (((i & 3) ? full : nfull) >> ((i & 3) * 8) & 0xff) == 0xff) {
-#pragma unroll
-        for (int q = 0; q < NP; ++q) {
-          const int p = w + q * kCodeWarps;
-          const int part = __shfl_sync(0xffffffffu, (i & 3) ? at : nat, (i & 3) * 8 + (p & 7));
-          const unsigned char* src = pool + (size_t)part * (16 * D) + row * D;
-          if (p < 8) {
-#pragma unroll
-            for (int k = 0; k < IT; ++k)
-              u[q][k] = *reinterpret_cast<const uint4*>(src + k * RPS * D + 16 * chunk_place<D>(row + k * RPS, chunk));
-          }
-        }
-        return;
-      }
-      // parts that end beyond what is seen hold bytes that were never written
-#pragma unroll
-      for (int q = 0; q < NP; ++q) {
-        const int p = w + q * kCodeWarps;
-        // past the batch in `at`, block i is the first of the next one
-        const int part = __shfl_sync(0xffffffffu, (i & 3) ? at : nat, (i & 3) * 8 + (p & 7));
-        const unsigned char* src = pool + (size_t)part * (16 * D);
-#pragma unroll
-        for (int k = 0; k < IT; ++k) {
-          const int r = row + k * RPS, tk = tok + 16 * p + r;
-          u[q][k] = make_uint4(0, 0, 0, 0);
-          if (p < 8 && i < nblk && part >= 0 && tk >= lo && tk <= hi)
-            u[q][k] = *reinterpret_cast<const uint4*>(src + r * D + 16 * chunk_place<D>(r, chunk));
-        }
-      }
+    // Copies block i's codes (x = 0 keys, 1 values); past the batch in `at`, it is the next one's.
+    auto copy = [&](int x, int i) {
+      const uint32_t mask = ((i & 3) ? full : nfull) >> ((i & 3) * 8) & 0xff;
+      const int part = __shfl_sync(0xffffffffu, (i & 3) ? at : nat, (i & 3) * 8 + (lane & 7));
+      if (lane == 0) mbar_arrive_expect_tx(&ctl->bar[RF + x], __popc(mask) * 16 * D);
+      __syncwarp();
+      if (lane < 8 && part >= 0)
+        bulk_load(sm + Sm::R + x * Sm::kRaw + lane * 16 * D, (x ? a.c.v : a.c.k) + (size_t)part * (16 * D), 16 * D,
+                  &ctl->bar[RF + x]);
     };
-    auto convert = [&](unsigned char* tile, const uint4 (&u)[NP][IT]) {
+    auto convert = [&](const unsigned char* raw, unsigned char* tile, int i) {
+      const int tok = (b0 + i) * kBlock;
+      const uint32_t mask = full >> ((i & 3) * 8) & 0xff;
+      // parts that end beyond what is seen hold bytes that were never written
+      const bool whole = mask == 0xff && tok >= lo && tok + kBlock - 1 <= hi;
 #pragma unroll
       for (int q = 0; q < NP; ++q) {
         const int p = w + q * kCodeWarps;
         if (p >= 8) break;
+        uint4 u[IT];
 #pragma unroll
         for (int k = 0; k < IT; ++k) {
-          const int r = row + k * RPS;
+          const int r = row_of(k);
+          u[k] = *reinterpret_cast<const uint4*>(raw + (p * 16 + r) * D + 16 * chunk_place<D>(r, chunk));
+        }
+        if (!whole) {
+#pragma unroll
+          for (int k = 0; k < IT; ++k) {
+            const int tk = tok + 16 * p + row_of(k);
+            if (!(mask >> p & 1) || tk < lo || tk > hi) u[k] = make_uint4(0, 0, 0, 0);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < IT; ++k) {
+          const int r = row_of(k);
           uint32_t h[8];
-          const uint32_t x[4] = {u[q][k].x, u[q][k].y, u[q][k].z, u[q][k].w};
+          const uint32_t x[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) codes_to_half<F>(x[e], h[2 * e], h[2 * e + 1]);
           unsigned char* t = tile + p * 16 * 128;
@@ -806,35 +809,42 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       }
       fence_proxy_async_smem();
     };
-    uint4 ku[NP][IT], vu[NP][IT];
     look(0);
-    load(a.c.k, 0, ku);
-    load(a.c.v, 0, vu);
+    find(0);
+    look(4);
+    if (w < 2) copy(w, 0);
     bool ok = true;
     for (int i = 0; i < nblk; ++i) {
       const int gi = it + i, st = gi & 1;  // gi counts over all pieces
       const uint32_t free_par = ((gi >> 1) & 1) ^ 1;
       if ((i & 3) == 0) {
         at = nat, sc = nsc, full = nfull;
-        look(i + 4);
+        find(i + 4);
+        look(i + 8);
       }
-      if (gi >= 2 && !(ok = wait_all(KE + st, free_par))) break;
-      // Block i - 4's scales are no longer read: the keys' stage is free, so the scores of block
-      // i - 2 are done, which were issued after every row had finished block i - 3.
-      if (w == 0) {
-        if (lane >> 3 == (i & 3)) s_scale[gi & 3][lane & 7] = sc;
+      // Keys, then values.  Warp x copies the next block's once all three have read this one's.
+#pragma unroll 1
+      for (int x = 0; x < 2; ++x) {
+        if (gi >= 2 && !(ok = wait_all((x ? VE : KE) + st, free_par))) break;
+        if (x == 0 && w == 0) {
+          // Block i - 4's scales are no longer read: the keys' stage is free, so the scores of
+          // block i - 2 are done, which were issued after every row had finished block i - 3.
+          if (lane >> 3 == (i & 3))
+            s_scale[gi & 3][lane & 7] =
+                make_float2(sc.x, at >= 0 ? (float)((int)(__float_as_uint(sc.y) >> 23 & 0xff) - 127) : 0.f);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ctl->bar[SC + (gi & 3)]);
+        }
+        if (!(ok = wait_all(RF + x, gi & 1))) break;
+        convert(sm + Sm::R + x * Sm::kRaw, sm + (x ? Sm::V : Sm::K) + st * Sm::kTile, i);
         __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl->bar[SC + (gi & 3)]);
+        if (lane == 0) mbar_arrive(&ctl->bar[(x ? VF : KF) + st]), mbar_arrive(&ctl->bar[RE + x]);
+        if (w == x && i + 1 < nblk) {
+          if (!(ok = wait_all(RE + x, gi & 1))) break;
+          copy(x, i + 1);
+        }
       }
-      convert(sm + Sm::K + st * Sm::kTile, ku);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl->bar[KF + st]);
-      load(a.c.k, i + 1, ku);
-      if (gi >= 2 && !(ok = wait_all(VE + st, free_par))) break;
-      convert(sm + Sm::V + st * Sm::kTile, vu);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl->bar[VF + st]);
-      load(a.c.v, i + 1, vu);
+      if (!ok) break;
     }
     if (!ok) ctl->abort = 1;
   } else {
@@ -952,7 +962,14 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
-  if (*(volatile int*)&ctl->abort && tid == 0) raise_status(a.status, kDevTimeout);
+  if (*(volatile int*)&ctl->abort) {
+    if (tid == 0) raise_status(a.status, kDevTimeout);
+    // a wait gave up after a second; copies issued just before the others saw that land well
+    // within a millisecond
+    const long long c0 = clock64();
+    while (clock64() - c0 < 4000000ll) {
+    }
+  }
   pdl_trigger();
 }
 
