@@ -246,7 +246,8 @@ def _ptr(t):
 def _stream(stream):
     if stream is None:
         import torch
-        stream = torch.cuda.current_stream()
+        # the current stream's handle, without the Stream object around it
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     handle = getattr(stream, "cuda_stream", stream)
     return ctypes.c_void_p(int(handle))
 
@@ -495,7 +496,7 @@ def _rows(t, shape, dtype: int):
     """Pointer and strides (None when contiguous) of a [N,H,T,d] device tensor."""
     if t is None:
         return None, None
-    if t.shape != shape or _dtype_code(t) != dtype or not t.is_cuda:
+    if t.shape != shape or not t.is_cuda or _dtype_code(t) != dtype:
         raise ValueError(f"expected a device tensor of shape {shape} and element type {dtype}, "
                          f"got {tuple(t.shape)} {t.dtype} on {t.device}")
     if t.is_contiguous():

@@ -13,70 +13,102 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// 16 consecutive elements of a row.
-__device__ __forceinline__ void load16(const float* p, float (&x)[16]) {
+// 16 consecutive elements of a row as loaded, and as floats: loads in one loop, conversions
+// (the first uses, which wait) in the next.
+template <typename T> struct Raw16 {
+  uint4 v[sizeof(T)];
+  __device__ __forceinline__ void load(const T* p) {
 #pragma unroll
-  for (int i = 0; i < 16; i += 4) {
-    const float4 v = ld4(p + i);
-    x[i] = v.x, x[i + 1] = v.y, x[i + 2] = v.z, x[i + 3] = v.w;
+    for (int i = 0; i < (int)sizeof(T); ++i) v[i] = reinterpret_cast<const uint4*>(p)[i];
   }
-}
-__device__ __forceinline__ void load16(const bf16* p, float (&x)[16]) {
-  const uint4 u0 = *reinterpret_cast<const uint4*>(p), u1 = *reinterpret_cast<const uint4*>(p + 8);
-  const uint32_t w[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
+  __device__ __forceinline__ void value(float (&x)[16]) const {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    for (int i = 0; i < (int)sizeof(T); ++i) {
+      const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (sizeof(T) == 4) {
+          x[4 * i + j] = __uint_as_float(w[j]);
+        } else {
+          x[(8 * i + 2 * j) & 15] = __uint_as_float(w[j] << 16);
+          x[(8 * i + 2 * j + 1) & 15] = __uint_as_float(w[j] & 0xffff0000u);
+        }
+      }
+    }
+  }
+};
+
+// Cosines and sines of a row's pairs in shared memory, four floats of padding every 32: lanes
+// that read the pairs of different chunks with 16-byte accesses hit different banks.
+__device__ __forceinline__ int pair_at(int i) { return i + 4 * (i >> 5); }
+__host__ __device__ __forceinline__ int row_floats(int pairs) { return (pairs + 4 * ((pairs - 1) >> 5) + 3) & ~3; }
+
+// Half layout with pairs that do not come in whole chunks; kept out of line for its registers.
+template <typename T>
+__device__ __noinline__ void rotate_odd(int rot, const T* row, int c, const float* co, const float* si, float* x) {
+  const int hr = rot / 2;
+  for (int i = 0; i < 16 && c + i < rot; ++i) {
+    const int e = c + i;
+    const bool low = e < hr;
+    const int q = pair_at(low ? e : e - hr);
+    const float other = ld_f(row + (low ? e + hr : e - hr));
+    x[i] = low ? x[i] * co[q] - other * si[q] : x[i] * co[q] + other * si[q];
   }
 }
 
-// Rotates channels c..c+15 (already in x) of a row; cs holds the row's (cos, sin) pairs.
+// Rotates channels c..c+15 (already in x, the pairs' other channels in o where they form a
+// chunk too) of a row; co and si hold the row's cosines and sines.
 template <typename T>
-__device__ __forceinline__ void rotate16(const RopeArgs& r, const T* row, int c, const float2* cs,
-                                         float (&x)[16]) {
+__device__ __forceinline__ void rotate16(const RopeArgs& r, const T* row, int c, const float* co, const float* si,
+                                         const float (&o)[16], float (&x)[16]) {
   if (c >= r.rot) return;
+  const int hr = r.rot / 2;
   if (r.layout == LIZARD_ROPE_INTERLEAVED) {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       if (c + 2 * i < r.rot) {
-        const float2 f = cs[c / 2 + i];
-        const float a = x[2 * i], b = x[2 * i + 1];
-        x[2 * i] = a * f.x - b * f.y;
-        x[2 * i + 1] = b * f.x + a * f.y;
+        const int q = pair_at(c / 2 + i);
+        const float f = co[q], g = si[q], a = x[2 * i], b = x[2 * i + 1];
+        x[2 * i] = a * f - b * g;
+        x[2 * i + 1] = b * f + a * g;
       }
-    return;
-  }
-  const int hr = r.rot / 2;
-  float o[16];
-  if (hr % 16 == 0) {  // the pairs' other channels are a chunk too
-    load16(row + (c < hr ? c + hr : c - hr), o);
+  } else if (hr % 16 == 0) {
+    const float sign = c < hr ? -1.f : 1.f;
+    const int q = pair_at(c < hr ? c : c - hr);
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+      const float4 f = *reinterpret_cast<const float4*>(co + q + i), g = *reinterpret_cast<const float4*>(si + q + i);
+      x[i] = x[i] * f.x + sign * o[i] * g.x;
+      x[i + 1] = x[i + 1] * f.y + sign * o[i + 1] * g.y;
+      x[i + 2] = x[i + 2] * f.z + sign * o[i + 2] * g.z;
+      x[i + 3] = x[i + 3] * f.w + sign * o[i + 3] * g.w;
+    }
   } else {
+    float y[16];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int e = c + i;
-      o[i] = e < r.rot ? ld_f(row + (e < hr ? e + hr : e - hr)) : 0.f;
-    }
-  }
+    for (int i = 0; i < 16; ++i) y[i] = x[i];
+    rotate_odd(r.rot, row, c, co, si, y);
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int e = c + i;
-    if (e < r.rot) {
-      const bool low = e < hr;
-      const float2 f = cs[low ? e : e - hr];
-      x[i] = low ? x[i] * f.x - o[i] * f.y : x[i] * f.x + o[i] * f.y;
-    }
+    for (int i = 0; i < 16; ++i) x[i] = y[i];
   }
 }
 
-template <typename T, int D, int F, int CH>
-__global__ void __launch_bounds__(kThreads) write_kernel(CacheIo a) {
+// Heads that a CTA takes one after the other where there are CTAs enough: the next head's loads
+// are in flight while this one's maximum is found and its codes are stored, and rotated keys
+// share their angles.
+constexpr int kHeads = 4;
+
+// TH threads hold CH 16-channel chunks each of the new rows of a page.  One warp where they
+// suffice (a decode step), so that many heads share an SM.
+template <typename T, int D, int F, int CH, int TH>
+__global__ void __launch_bounds__(TH, TH == 256 ? 2 : 1) write_kernel(CacheIo a, int per) {
   constexpr int C = D / 16;
-  extern __shared__ float2 s_cs[];  // (cos, sin) of every new row's pairs
-  __shared__ float s_max[kThreads / 32];
-  const int n = blockIdx.z, hk = blockIdx.y >> 1;
+  extern __shared__ __align__(16) float s_cs[];  // cosines, then sines, of every new row's pairs
+  __shared__ float s_max[TH / 32];
+  pdl_wait();
+  const int n = blockIdx.z, tid = threadIdx.x;
   const bool values = blockIdx.y & 1;
-  const int tid = threadIdx.x;
+  const int h0 = (int)(blockIdx.y >> 1) * per, h1 = min(h0 + per, a.c.Hk);
   const int64_t p0 = a.pos[n];
   const int cnt = a.count ? a.count[n] : a.T;
   if (cnt == 0) return;
@@ -96,78 +128,104 @@ __global__ void __launch_bounds__(kThreads) write_kernel(CacheIo a) {
   const int r0 = t0 < p0 ? (int)(p0 - t0) : 0;
   const int r1 = (int)min((int64_t)a.c.P, p0 + cnt - t0);
   const Strides st = values ? a.sv : a.sk;
-  const T* src = static_cast<const T*>(values ? a.v : a.k) + n * st.n + hk * st.h;
-  unsigned char* dst = (values ? a.c.v : a.c.k) + ((size_t)id * a.c.Hk + hk) * a.c.P * D;
-  float* scale = (values ? a.c.vs : a.c.ks) + (size_t)id * a.c.Hk + hk;
   const bool turn = !values && a.rope.turns;
-  const int pairs = a.rope.rot / 2;
+  const int pairs = a.rope.rot / 2, rf = row_floats(pairs);
+  float* s_si = s_cs + (size_t)min(a.T, a.c.P) * rf;
   if (turn) {
-    for (int e = tid; e < (r1 - r0) * pairs; e += kThreads) {
-      const int r = e / pairs, i = e - r * pairs;
-      float2 f;
-      rope_angle(a.rope.turns[i], t0 + r0 + r, a.rope.factor, f.x, f.y);
-      s_cs[e] = f;
+    for (int e = tid; e < (r1 - r0) * pairs; e += TH) {
+      const int r = e / pairs, i = e - r * pairs, q = r * rf + pair_at(i);
+      rope_angle(a.rope.turns[i], t0 + r0 + r, a.rope.factor, s_cs[q], s_si[q]);
     }
     __syncthreads();
   }
+  const bool chunked = turn && a.rope.layout == LIZARD_ROPE_HALF && pairs % 16 == 0;
 
-  float x[CH][16];
-  float amax = 0.f;
-  bool odd = false;
+  const T* in = static_cast<const T*>(values ? a.v : a.k) + n * st.n;
+  Raw16<T> raw[CH], other[CH];
+  float had = 0.f;
+  auto load = [&](int hk) {
 #pragma unroll
-  for (int i = 0; i < CH; ++i) {
-    const int e = tid + i * kThreads, r = e / C, c = e % C * 16;
-    if (r < r0 || r >= r1) continue;
-    const T* row = src + (t0 + r - p0) * st.t;
-    load16(row + c, x[i]);
-    if (turn) rotate16(a.rope, row, c, s_cs + (r - r0) * pairs, x[i]);
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      const float m = fabsf(x[i][j]);
-      const bool fin = m <= 3.402823466e38f;
-      odd |= !fin;
-      if (isnan(x[i][j])) x[i][j] = 0.f;
-      amax = fmaxf(amax, fin ? m : 0.f);
+    for (int i = 0; i < CH; ++i) {
+      const int e = tid + i * TH, r = r0 + e / C, c = e % C * 16;
+      if (r < r1) {
+        const T* row = in + hk * st.h + (t0 + r - p0) * st.t;
+        raw[i].load(row + c);
+        if (chunked && c < a.rope.rot) other[i].load(row + (c < pairs ? c + pairs : c - pairs));
+      }
     }
-  }
-  if (odd) raise_status(a.status, kDevCheck);
-  amax = warp_max(amax);
-  if ((tid & 31) == 0) s_max[tid >> 5] = amax;
-  const float had = r0 > 0 ? *scale : 0.f;
-  __syncthreads();
+    if (r0 > 0) had = ((values ? a.c.vs : a.c.ks) + (size_t)id * a.c.Hk)[hk];
+  };
+  load(h0);
+#pragma unroll 1
+  for (int hk = h0; hk < h1; ++hk) {
+    const T* src = in + hk * st.h;
+    unsigned char* dst = (values ? a.c.v : a.c.k) + ((size_t)id * a.c.Hk + hk) * a.c.P * D;
+    float* scale = (values ? a.c.vs : a.c.ks) + (size_t)id * a.c.Hk + hk;
+    float x[CH][16];
+    float amax = 0.f;
+    bool odd = false;
 #pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) amax = fmaxf(amax, s_max[w]);
-  const float need = exp2_int(scale_exponent<F>(amax));
-  const bool kept = had > 0.f && had <= 3.402823466e38f;
-  const float now = kept ? fmaxf(had, need) : need;
-  const float inv = 1.f / now;  // a power of two: exact
-  const bool grew = kept && now != had;
+    for (int i = 0; i < CH; ++i) {
+      const int e = tid + i * TH, r = r0 + e / C, c = e % C * 16;
+      if (r >= r1) continue;
+      raw[i].value(x[i]);
+      if (turn) {
+        float o[16];
+        if (chunked) other[i].value(o);
+        const float* co = s_cs + (size_t)(r - r0) * rf;
+        rotate16(a.rope, src + (t0 + r - p0) * st.t, c, co, s_si + (co - s_cs), o, x[i]);
+      }
 #pragma unroll
-  for (int i = 0; i < CH; ++i) {
-    const int e = tid + i * kThreads, r = e / C, c = e % C;
-    uint4* at = reinterpret_cast<uint4*>(dst + (size_t)r * D + 16 * chunk_place<D>(r, c));
-    if (r >= r0 && r < r1) {
+      for (int j = 0; j < 16; ++j) {
+        const float m = fabsf(x[i][j]);
+        const bool fin = m <= 3.402823466e38f;
+        odd |= !fin;
+        if (isnan(x[i][j])) x[i][j] = 0.f;
+        amax = fmaxf(amax, fin ? m : 0.f);
+      }
+    }
+    if (odd) raise_status(a.status, kDevCheck);
+    const float was = had;
+    if (hk + 1 < h1) load(hk + 1);
+    amax = warp_max(amax);
+    if ((tid & 31) == 0) s_max[tid >> 5] = amax;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < TH / 32; ++w) amax = fmaxf(amax, s_max[w]);
+    const float need = exp2_int(scale_exponent<F>(amax));
+    const bool kept = was > 0.f && was <= 3.402823466e38f;
+    const float now = kept ? fmaxf(was, need) : need;
+    const float inv = 1.f / now;  // a power of two: exact
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const int e = tid + i * TH, r = r0 + e / C, c = e % C;
+      if (r >= r1) continue;
       uint32_t w[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         w[j] = float_to_codes<F>(x[i][4 * j] * inv, x[i][4 * j + 1] * inv, x[i][4 * j + 2] * inv,
                                  x[i][4 * j + 3] * inv);
-      *at = make_uint4(w[0], w[1], w[2], w[3]);
-    } else if (r < r0 && grew) {
-      const float f = had * inv;
-      const uint4 old = *at;
-      const uint32_t o[4] = {old.x, old.y, old.z, old.w};
-      uint32_t w[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float4 v = codes_to_float<F>(o[j]);
-        w[j] = float_to_codes<F>(v.x * f, v.y * f, v.z * f, v.w * f);
-      }
-      *at = make_uint4(w[0], w[1], w[2], w[3]);
+      *reinterpret_cast<uint4*>(dst + (size_t)r * D + 16 * chunk_place<D>(r, c)) = make_uint4(w[0], w[1], w[2], w[3]);
     }
+    if (kept && now != was) {  // the scale grew: earlier tokens are rounded again
+      const float f = was * inv;
+#pragma unroll 1
+      for (int e = tid; e < r0 * C; e += TH) {
+        uint4* at = reinterpret_cast<uint4*>(dst + (size_t)e * 16);
+        const uint4 old = *at;
+        const uint32_t o[4] = {old.x, old.y, old.z, old.w};
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float4 v = codes_to_float<F>(o[j]);
+          w[j] = float_to_codes<F>(v.x * f, v.y * f, v.z * f, v.w * f);
+        }
+        *at = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+    __syncthreads();  // every thread has read the old scale and the maxima
+    if (tid == 0) *scale = now;
   }
-  // every thread has read the old scale before the barrier above
-  if (tid == 0) *scale = now;
 }
 
 __device__ __forceinline__ void store16(float* p, const float (&x)[16]) {
@@ -189,6 +247,7 @@ __device__ __forceinline__ void store16(bf16* p, const float (&x)[16]) {
 template <typename T, int D, int F>
 __global__ void __launch_bounds__(kThreads) read_kernel(CacheIo a) {
   constexpr int C = D / 16;
+  pdl_wait();
   const int n = blockIdx.z, hk = blockIdx.y >> 1;
   const bool values = blockIdx.y & 1;
   const int64_t e = (int64_t)blockIdx.x * kThreads + threadIdx.x;
@@ -226,26 +285,30 @@ __global__ void __launch_bounds__(kThreads) read_kernel(CacheIo a) {
   store16(dst + 16 * c, x);
 }
 
-template <typename T, int D, int F, int CH>
-cudaError_t launch_write_ch(const CacheIo& a, cudaStream_t s, int* launches) {
-  const dim3 grid((a.T + a.c.P - 2) / a.c.P + 1, 2 * a.c.Hk, a.c.N);
-  const size_t smem = (size_t)min(a.T, a.c.P) * (a.rope.rot / 2) * sizeof(float2);
-  cudaError_t e = cudaFuncSetAttribute(write_kernel<T, D, F, CH>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, 128 * (D / 2) * 8);
+template <typename T, int D, int F, int CH, int TH>
+cudaError_t launch_write_as(const CacheIo& a, cudaStream_t s, int* launches) {
+  const int J = (a.T + a.c.P - 2) / a.c.P + 1;
+  const int per = (int64_t)J * a.c.Hk * a.c.N * 2 / kHeads >= ctas_per_wave(4) ? kHeads : 1;
+  const dim3 grid(J, 2 * ((a.c.Hk + per - 1) / per), a.c.N);
+  const size_t smem = a.rope.turns ? (size_t)min(a.T, a.c.P) * row_floats(a.rope.rot / 2) * 2 * sizeof(float) : 0;
+  cudaError_t e = cudaSuccess;
+  if (smem > 48 * 1024)
+    e = cudaFuncSetAttribute(write_kernel<T, D, F, CH, TH>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   trace_begin("cache_write", s);
-  write_kernel<T, D, F, CH><<<grid, kThreads, smem, s>>>(a);
+  e = launch_pdl(write_kernel<T, D, F, CH, TH>, grid, dim3(TH), smem, s, a, per);
   trace_end(s);
   ++*launches;
-  return cudaGetLastError();
+  return e;
 }
 
 template <typename T, int D, int F>
 cudaError_t launch_write(const CacheIo& a, cudaStream_t s, int* launches) {
-  const int ch = a.c.P * (D / 16) / kThreads;  // 16-code chunks per thread
-  return ch >= 4   ? launch_write_ch<T, D, F, 4>(a, s, launches)
-         : ch == 2 ? launch_write_ch<T, D, F, 2>(a, s, launches)
-                   : launch_write_ch<T, D, F, 1>(a, s, launches);
+  const int chunks = min(a.T, a.c.P) * (D / 16);  // of the new rows of a page, at most
+  return chunks <= 32    ? launch_write_as<T, D, F, 1, 32>(a, s, launches)
+         : chunks <= 256 ? launch_write_as<T, D, F, 1, 256>(a, s, launches)
+         : chunks <= 512 ? launch_write_as<T, D, F, 2, 256>(a, s, launches)
+                         : launch_write_as<T, D, F, 2, 512>(a, s, launches);
 }
 
 template <typename T, int D, int F>
@@ -253,10 +316,10 @@ cudaError_t launch_read(const CacheIo& a, cudaStream_t s, int* launches) {
   const int64_t chunks = (int64_t)a.T * (D / 16);
   const dim3 grid((unsigned)((chunks + kThreads - 1) / kThreads), 2 * a.c.Hk, a.c.N);
   trace_begin("cache_read", s);
-  read_kernel<T, D, F><<<grid, kThreads, 0, s>>>(a);
+  const cudaError_t e = launch_pdl(read_kernel<T, D, F>, grid, dim3(kThreads), 0, s, a);
   trace_end(s);
   ++*launches;
-  return cudaGetLastError();
+  return e;
 }
 
 template <typename T, int D>

@@ -62,6 +62,7 @@ __device__ __forceinline__ void store_v<bf16, 8>(bf16* p, const float (&x)[8]) {
 template <typename T, int VP>
 __global__ void __launch_bounds__(kThreads) rope_kernel(RopeCall a, int units, int hpt,
                                                         int groups) {
+  pdl_wait();
   const int64_t idx = (int64_t)blockIdx.x * kThreads + threadIdx.x;
   const int64_t total = (int64_t)a.N * a.T * units * groups;
   if (idx >= total) return;
@@ -135,10 +136,11 @@ cudaError_t launch(const RopeCall& a, cudaStream_t s, int* launches) {
   const int64_t blocks = (lanes * groups + kThreads - 1) / kThreads;
   if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
   trace_begin("rope", s);
-  rope_kernel<T, VP><<<(unsigned)blocks, kThreads, 0, s>>>(a, units, (int)hpt, groups);
+  const cudaError_t e = launch_pdl(rope_kernel<T, VP>, dim3((unsigned)blocks), dim3(kThreads), 0, s, a, units,
+                                   (int)hpt, groups);
   trace_end(s);
   ++*launches;
-  return cudaGetLastError();
+  return e;
 }
 
 template <typename T>
