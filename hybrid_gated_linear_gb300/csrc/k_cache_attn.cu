@@ -35,7 +35,7 @@ constexpr int kMaxCtas = 304;  // CTAs of a launch at most (sizes the scratch): 
 // From this many (sequence, head) pairs on, each warp works alone: starting and ending a
 // segment then stalls one warp of sixteen instead of a CTA's eight.  Below, a pair would be
 // spread over so many warps that joining their results costs more.
-constexpr int64_t kSoloSegments = 128;
+constexpr int64_t kSoloSegments = 256;
 constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -114,6 +114,14 @@ struct UnitMeta {
   int at0, at1;
   uint32_t exps;  // key 0, key 1, value 0, value 1
 };
+
+// Adds 1 to a counter and returns what it was: the writes of this thread's team, ordered before
+// by its barrier, become visible with it, and those of the teams that counted before are seen.
+__device__ __forceinline__ unsigned count_up(unsigned* p) {
+  unsigned v;
+  asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
 
 // One merged set of rows: maxima, sum and output of a row (unnormalised).
 struct RowStat {
@@ -694,14 +702,21 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG, Solo>::kPerSm)
     const bool whole_seg = ua == 0 && s_p.ub == s_p.s.units;
     float* part = reinterpret_cast<float*>(a.ws + (((size_t)M2 * Hk * sizeof(unsigned) + 255) & ~(size_t)255));
     auto slot = [&](int w, bool starts) { return part + (size_t)(2 * w + (starts ? 1 : 0)) * prow * (D + 4); };
+    // Four channels f of row r of warp w: lanes g, t4 write them together, so their places in a
+    // row are spread by both.
+    auto merge_at = [&](int w, int r, int f) {
+      const int t = f / (D / 16);  // the writer's t4
+      return reinterpret_cast<float4*>(s_o) + ((size_t)w * 16 + r) * (D / 4) + (f ^ (((r & 7) ^ (t << 1)) & 7));
+    };
 #pragma unroll
     for (int i = 0; i < 2; ++i)
+      if (rg * 16 + g + 8 * i < rows)
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
+        for (int e = 0; e < 2; ++e)
 #pragma unroll
-        for (int k = 0; k < NT; k += 4)
-          *reinterpret_cast<float4*>(s_o + ((size_t)warp * 16 + g + 8 * i) * D + NT * (2 * t4 + e) + k) =
-              make_float4(o[k][2 * i + e], o[k + 1][2 * i + e], o[k + 2][2 * i + e], o[k + 3][2 * i + e]);
+          for (int k = 0; k < NT; k += 4)
+            *merge_at(warp, g + 8 * i, (NT * (2 * t4 + e) + k) / 4) =
+                make_float4(o[k][2 * i + e], o[k + 1][2 * i + e], o[k + 2][2 * i + e], o[k + 3][2 * i + e]);
     team_sync();
     auto finish = [&](int r, RowStat s, float4 v, int d0) {
       // row r's 4 channels, normalised and merged
@@ -730,7 +745,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG, Solo>::kPerSm)
 #pragma unroll
       for (int q = 0; q < TG; ++q) {
         const int w = Solo ? warp : q * RG + r / 16;
-        join(s, v, s_st[w][r % 16], *reinterpret_cast<const float4*>(s_o + ((size_t)w * 16 + r % 16) * D + d0));
+        join(s, v, s_st[w][r % 16], *merge_at(w, r % 16, d0 / 4));
       }
       if (ua == 0) {
         const int h = hk * G + (r0 + r) % G;
@@ -755,11 +770,9 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG, Solo>::kPerSm)
       }
     if (!whole_seg) {
       const int c0 = s_p.c0, c1 = s_p.c1;
-      __threadfence();
       team_sync();
       int last = 0;
-      if (tt_id == 0)
-        last = atomicAdd(reinterpret_cast<unsigned*>(a.ws) + s_p.seg, 1u) == (unsigned)(c1 - c0);
+      if (tt_id == 0) last = count_up(reinterpret_cast<unsigned*>(a.ws) + s_p.seg) == (unsigned)(c1 - c0);
       if (Solo) {
         last = __shfl_sync(0xffffffffu, last, 0);
       } else {
@@ -769,11 +782,67 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG, Solo>::kPerSm)
       }
       if (last) {
         // the V4 lanes of a row read the statistics of V4 partials at a time, turn them into
-        // weights, and then add the outputs, four rows and four partials in flight
-        __threadfence();
+        // weights, and then add the outputs with many loads in flight
         const int k = tt_id % V4;
-        constexpr int RW = 4;
-        for (int rb = tt_id / V4; rb - tt_id / V4 < rows; rb += RW * ROWSTEP) {
+        constexpr int RW = 4, GROUPS = ROWSTEP;
+        int rp = 1;
+        while (rp < rows && rp < GROUPS) rp <<= 1;
+        if (!Solo && rp < GROUPS) {
+          // fewer rows than groups of lanes: GROUPS / rp groups share out a row's partials
+          const int grp = tt_id / V4, r = grp % rp, sub = grp / rp, PS = GROUPS / rp, np = c1 - c0 + 1;
+          RowStat s{-INFINITY, -INFINITY, 0.f};
+          for (int cb = c0; cb <= c1; cb += V4) {
+            float4 b = make_float4(-INFINITY, -INFINITY, 0.f, 0.f);
+            if (r < rows && cb + k <= c1)
+              b = __ldcg(reinterpret_cast<const float4*>(slot(cb + k, cb + k == c0) + (size_t)prow * D + 4 * r));
+            float mm = b.x, mw = b.y;
+#pragma unroll
+            for (int o = V4 / 2; o > 0; o >>= 1) {
+              mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
+              mw = fmaxf(mw, __shfl_xor_sync(0xffffffffu, mw, o));
+            }
+            mm = fmaxf(mm, s.m), mw = fmaxf(mw, s.mo);
+            float ls = b.x == -INFINITY ? 0.f : b.z * exp2f(b.x - mm);
+#pragma unroll
+            for (int o = V4 / 2; o > 0; o >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o);
+            s = RowStat{mm, mw, (s.m == mm ? s.l : s.l * exp2f(s.m - mm)) + ls};
+          }
+          float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+          const int ca = c0 + np * sub / PS, cz = c0 + np * (sub + 1) / PS;
+          for (int cb = ca; __any_sync(0xffffffffu, cb < cz); cb += V4) {
+            float wk = 0.f;
+            if (r < rows && cb + k < cz) {
+              const float mo_k = __ldcg(slot(cb + k, cb + k == c0) + (size_t)prow * D + 4 * r + 1);
+              if (mo_k != -INFINITY) wk = exp2f(mo_k - s.mo);
+            }
+            const int cn = min(V4, cz - cb);
+            for (int i = 0; __any_sync(0xffffffffu, i < cn); i += 8) {
+              float4 x[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                x[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (r < rows && i + e < cn)
+                  x[e] = __ldcg(reinterpret_cast<const float4*>(slot(cb + i + e, cb + i + e == c0) + (size_t)r * D + d0));
+              }
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const float w = __shfl_sync(0xffffffffu, wk, (i + e) & (V4 - 1), V4);
+                v.x = fmaf(w, x[e].x, v.x), v.y = fmaf(w, x[e].y, v.y);
+                v.z = fmaf(w, x[e].z, v.z), v.w = fmaf(w, x[e].w, v.w);
+              }
+            }
+          }
+          float4* s_v = reinterpret_cast<float4*>(s_o);
+          s_v[tt_id] = v;
+          team_sync();
+          if (sub == 0 && r < rows) {
+            for (int q = 1; q < PS; ++q) {
+              const float4 w = s_v[(q * rp + r) * V4 + k];
+              v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
+            }
+            finish(r, s, v, d0);
+          }
+        } else for (int rb = tt_id / V4; rb - tt_id / V4 < rows; rb += RW * ROWSTEP) {
           RowStat s[RW];
           float4 v[RW];
 #pragma unroll
