@@ -775,6 +775,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG, Solo>::kPerSm)
       if (tt_id == 0) last = count_up(reinterpret_cast<unsigned*>(a.ws) + s_p.seg) == (unsigned)(c1 - c0);
       if (Solo) {
         last = __shfl_sync(0xffffffffu, last, 0);
+        __syncwarp();
       } else {
         if (tid == 0) s_last = last;
         __syncthreads();
