@@ -947,7 +947,9 @@ cudaError_t by_rows(const CacheAttn& a, cudaStream_t s, int* launches) {
     case 32: return launch_split<T, D, F, 2, false>(a, s, launches);
     case 64: return launch_split<T, D, F, 4, false>(a, s, launches);
   }
-  return launch_split<T, D, F, 8, false>(a, s, launches);
+  // more rows in bf16 run on tcgen05 (cache_attn_tc_used)
+  if constexpr (sizeof(T) == 4) return launch_split<T, D, F, 8, false>(a, s, launches);
+  return cudaErrorInvalidValue;
 }
 
 template <typename T, int D>

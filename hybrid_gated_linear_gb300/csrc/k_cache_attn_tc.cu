@@ -283,18 +283,26 @@ __device__ __noinline__ void stage_queries(const CacheAttn& a, const Piece& s_p,
   const bool half = rope.layout == LIZARD_ROPE_HALF, turn = rope.turns && d0 < rope.rot;
   // where the pairs' other channels are, if they lie together
   const int other = turn && half && pairs % 4 == 0 ? (d0 < pairs ? d0 + pairs : d0 - pairs) : d0;
-  constexpr int RW = 4;
-#pragma unroll 1
-  for (int rb = warp * RPI; rb < kRows; rb += RW * WARPS * RPI) {
-    // dead rows read row 0 (the loads stay free of branches, so all of them are in flight)
-    Raw4<bf16> x[RW], y[RW];
+  constexpr int RW = 4, RSTEP = RW * WARPS * RPI;
+  // dead rows read row 0 (the loads stay free of branches, so all of them are in flight), and
+  // the next rows' loads run ahead of this step's work
+  Raw4<bf16> nx[RW], ny[RW];
+  auto fetch = [&](int rb) {
 #pragma unroll
     for (int k = 0; k < RW; ++k) {
       const int r = rb + k * WARPS * RPI + lane / LPR;
       const bf16* qp = q0 + s_off[r < rows ? r : 0];
-      x[k] = raw4(qp + d0);
-      y[k] = raw4(qp + other);
+      nx[k] = raw4(qp + d0);
+      ny[k] = raw4(qp + other);
     }
+  };
+  fetch(warp * RPI);
+#pragma unroll 1
+  for (int rb = warp * RPI; rb < kRows; rb += RSTEP) {
+    Raw4<bf16> x[RW], y[RW];
+#pragma unroll
+    for (int k = 0; k < RW; ++k) x[k] = nx[k], y[k] = ny[k];
+    if (rb + RSTEP < kRows) fetch(rb + RSTEP);
 #pragma unroll
     for (int k = 0; k < RW; ++k) {
       const int r = rb + k * WARPS * RPI + lane / LPR;
@@ -311,7 +319,14 @@ __device__ __noinline__ void stage_queries(const CacheAttn& a, const Piece& s_p,
       } else if (!half) {
         o[0] = xf.y, o[1] = xf.x, o[2] = xf.w, o[3] = xf.z;
       }
-      if (turn && r < rows) {
+      if (turn && half && pairs % 4 == 0) {
+        const float s = d0 < pairs ? -1.f : 1.f;
+        const float4* cs = reinterpret_cast<const float4*>(s_cs + s_tok[r < rows ? r : 0] * pairs +
+                                                           (d0 < pairs ? d0 : d0 - pairs));
+        const float4 f = cs[0], g = cs[1];
+        v[0] = v[0] * f.x + s * o[0] * f.y, v[1] = v[1] * f.z + s * o[1] * f.w;
+        v[2] = v[2] * g.x + s * o[2] * g.y, v[3] = v[3] * g.z + s * o[3] * g.w;
+      } else if (turn && r < rows) {
         const float2* cs = s_cs + s_tok[r] * pairs;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -469,7 +484,8 @@ __device__ __noinline__ void write_partial(float* mine, uint32_t to, float m, fl
 // per row the output maximum and the factor of the sum, then the meta tokens' weights.
 template <int D>
 __device__ __noinline__ void join_rows(const CacheAttn& args, const Piece& p, const float* part, float2* s_fin,
-                                       float* s_meta) {
+                                       float* s_meta, float* s_w) {
+  constexpr int kKept = 32;  // parts whose weights fit the scratch
   constexpr int V4 = D / 4, STEP = kThreads / V4, RW = 4;
   const Out a = out_of(args, p);
   const int c0 = p.c0, c1 = p.c1, tid = threadIdx.x;
@@ -491,6 +507,12 @@ __device__ __noinline__ void join_rows(const CacheAttn& args, const Piece& p, co
       for (int j = 0; j < kMaxM; ++j)
         if (j < a.M) s_meta[tid * kMaxM + j] = exp2f(zm[j] - m) * f;
     }
+    if (c1 - c0 < kKept)
+#pragma unroll 4
+      for (int c = c0; c <= c1; ++c) {
+        const float x = __ldcg(part + partial_at<D>(c, c == c0) + (size_t)kRows * D + 4 * tid + 1);
+        s_w[(c - c0) * kRows + tid] = x == -INFINITY ? 0.f : exp2f(x - mo);
+      }
     s_fin[tid] = make_float2(mo, l > 0.f && mo != -INFINITY ? a.alpha / l * exp2f(mo - m) : 0.f);
   }
   __syncthreads();
@@ -509,7 +531,9 @@ __device__ __noinline__ void join_rows(const CacheAttn& args, const Piece& p, co
       for (int q = 0; q < RW; ++q) {
         const int r = rl + q * STEP;
         wk[q] = 0.f;
-        if (r < a.rows && cb + k <= c1) {
+        if (c1 - c0 < kKept) {
+          if (r < a.rows && cb + k <= c1) wk[q] = s_w[(cb + k - c0) * kRows + r];
+        } else if (r < a.rows && cb + k <= c1) {
           const float mo = __ldcg(part + partial_at<D>(cb + k, cb + k == c0) + (size_t)kRows * D + 4 * r + 1);
           if (mo != -INFINITY) wk[q] = exp2f(mo - s_fin[r].x);
         }
@@ -943,7 +967,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     __syncthreads();
     if (s_last) {
       __threadfence();
-      join_rows<D>(a, s_p, part, reinterpret_cast<float2*>(sm + Sm::K), reinterpret_cast<float*>(sm + Sm::V));
+      join_rows<D>(a, s_p, part, reinterpret_cast<float2*>(sm + Sm::K), reinterpret_cast<float*>(sm + Sm::V),
+                   reinterpret_cast<float*>(sm + Sm::Q));
       if (tid == 0) *counter = 0u;
     }
   }
@@ -990,7 +1015,10 @@ cudaError_t launch(const CacheAttn& a, cudaStream_t s, int* launches) {
 
 }  // namespace
 
-bool cache_attn_tc_used(int H, int Hk, int T, lizard_dtype dt) { return dt == LIZARD_BF16 && H / Hk * T > 128; }
+// Us for H = 32, Hk = 8, d = 128 here and in k_cache_attn.cu: 64 rows 130 against 121 (eight
+// sequences of 8192 tokens), 128 rows 137 against 221 there and 151 against 268 (one of 65536),
+// but 73 against 55 at 1000 tokens, where neither fills the GPU.
+bool cache_attn_tc_used(int H, int Hk, int T, lizard_dtype dt) { return dt == LIZARD_BF16 && H / Hk * T > 64; }
 
 size_t cache_attn_tc_workspace(int N, int Hk, int H, int T, int d) {
   const int tiles = (H / Hk * T + kRows - 1) / kRows;
