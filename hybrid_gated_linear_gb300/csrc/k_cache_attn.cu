@@ -7,6 +7,9 @@
 // The value scales are powers of two 2^e per page, so the weights the tensor cores see are
 // 2^(z+e-mo) with a maximum mo of their own: they stay in (0, 1], whatever the pages' scales.
 //
+// l's maximum m moves with every unit, mo (and with it the rescaling of o) only by more than
+// 2^kLazy at a time.
+//
 // What bounds it: the cache is read once, 2 D bytes per token and head, and everything else
 // is small; the floor is those bytes at the measured copy rate.  So the work is cut evenly
 // over the bytes, not over the sequences: all 32-token units of all (sequence, head) pairs
@@ -36,6 +39,8 @@ constexpr int kMaxCtas = 304;  // CTAs of a launch at most (sizes the scratch): 
 // segment then stalls one warp of sixteen instead of a CTA's eight.  Below, a pair would be
 // spread over so many warps that joining their results costs more.
 constexpr int64_t kSoloSegments = 256;
+constexpr float kLazy = 8.f;  // outputs are rescaled when their maximum has grown by 2^8: weights fit binary16
+constexpr float kFar = 60.f;  // see where it is used
 constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -510,6 +515,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG, Solo>::kPerSm)
     // tokens every row of the block sees
     const int all_lo = rows > 0 ? sees_from(s_p.s.p0 + (r0 + rows - 1) / G) : 0;
     const int all_hi = any && rows > 0 ? (int)(s_p.s.p0 + r0 / G - s_p.s.base) : -1;
+    const bool high = rows - rg * 16 > 8;
     const uint4* qf = reinterpret_cast<const uint4*>(s_q) + (size_t)rg * NS * KS * 32 + lane;
 
     for (int j = 0; j < nu; ++j) {
@@ -526,8 +532,10 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG, Solo>::kPerSm)
       if (!wait(&s_bar[0][st], parity)) break;
       const UnitMeta& um = s_meta[group][(j / kBatch) & 1][j % kBatch];
       const uint32_t ex = um.exps;
-      const float kk[2] = {__uint_as_float((ex & 0xff) << 23), __uint_as_float((ex >> 8 & 0xff) << 23)};
       const bool ok0 = ex & 0xff, ok1 = ex & 0xff00;
+      // an unseen block's products become -inf: any positive factor will do
+      const float kk[2] = {ok0 ? __uint_as_float((ex & 0xff) << 23) : 1.f,
+                           ok1 ? __uint_as_float((ex >> 8 & 0xff) << 23) : 1.f};
       const float ve[2] = {(float)((int)(ex >> 16 & 0xff) - 127), (float)((int)(ex >> 24) - 127)};
       float z[4][4];
 #pragma unroll
@@ -577,69 +585,86 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG, Solo>::kPerSm)
       };
       refill(0);
 
-      // scale and mask; column 8 i + 2 t4 + e
-      float sm[2][2] = {{-INFINITY, -INFINITY}, {-INFINITY, -INFINITY}};  // [row][block] maxima
+      // Row half h (rows g, g + 8) and 16-token block b: z holds raw products, to be multiplied
+      // by f = rs kk.  The upper half is skipped where there are eight rows or fewer.
       const bool whole = ok0 && ok1 && tok >= all_lo && tok + kUnit - 1 <= all_hi;
-      const float f0[2] = {rs[0] * kk[0], rs[0] * kk[1]}, f8[2] = {rs[1] * kk[0], rs[1] * kk[1]};
+      if (!whole) {  // column 8 i + 2 t4 + e
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float v = z[i][e] * (e < 2 ? f0[i >> 1] : f8[i >> 1]);
-          if (!whole) {
-            const int c = tok + 8 * i + 2 * t4 + (e & 1);
-            const bool see = (i < 2 ? ok0 : ok1) && c >= lo_r[e >> 1] && c <= hi_r[e >> 1];
-            v = see ? v : -INFINITY;
-          }
-          z[i][e] = v;
-          sm[e >> 1][i >> 1] = fmaxf(sm[e >> 1][i >> 1], v);
-        }
-      float mn[2], mon[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          sm[i][b] = fmaxf(sm[i][b], __shfl_xor_sync(0xffffffffu, sm[i][b], 1));
-          sm[i][b] = fmaxf(sm[i][b], __shfl_xor_sync(0xffffffffu, sm[i][b], 2));
-        }
-        mn[i] = fmaxf(mrow[i], fmaxf(sm[i][0], sm[i][1]));
-        mon[i] = fmaxf(mo[i], fmaxf(sm[i][0] + ve[0], sm[i][1] + ve[1]));
-      }
-      const bool grew = mn[0] > mrow[0] || mn[1] > mrow[1] || mon[0] > mo[0] || mon[1] > mo[1];
-      if (__any_sync(0xffffffffu, grew)) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          // -inf - -inf: nothing seen so far, and nothing to rescale
-          const float fl = mn[i] > mrow[i] ? exp2f(mrow[i] - mn[i]) : 1.f;
-          const float fo = mon[i] > mo[i] ? exp2f(mo[i] - mon[i]) : 1.f;
-          l[i] *= fl;
-          mrow[i] = mn[i], mo[i] = mon[i];
-#pragma unroll
-          for (int k = 0; k < NT; ++k) o[k][2 * i] *= fo, o[k][2 * i + 1] *= fo;
-        }
-      }
-      uint32_t pw[NS][2][4];
-      {
-        const float ml[2] = {mrow[0] == -INFINITY ? 0.f : mrow[0], mrow[1] == -INFINITY ? 0.f : mrow[1]};
-        float sh[2][2];  // 2^(z + ve - mo)
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int b = 0; b < 2; ++b) sh[i][b] = mo[i] == -INFINITY ? 0.f : mo[i] - ve[b];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float p[4];
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            l[e >> 1] += tc::ex2_approx(z[i][e] - ml[e >> 1]);
-            p[e] = tc::ex2_approx(z[i][e] - sh[e >> 1][i >> 1]);
+            const int c = tok + 8 * i + 2 * t4 + (e & 1);
+            const bool see = (i < 2 ? ok0 : ok1) && c >= lo_r[e >> 1] && c <= hi_r[e >> 1];
+            z[i][e] = see ? z[i][e] : -INFINITY;
           }
-          const uint32_t w0 = half2_bits(p[0], p[1]), w1 = half2_bits(p[2], p[3]);
-          pw[0][i >> 1][(i & 1) * 2] = w0, pw[0][i >> 1][(i & 1) * 2 + 1] = w1;
-          if (NS == 2) {
-            pw[NS - 1][i >> 1][(i & 1) * 2] = half2_rest(p[0], p[1], w0);
-            pw[NS - 1][i >> 1][(i & 1) * 2 + 1] = half2_rest(p[2], p[3], w1);
+      }
+      float mon[2];
+      bool jump = false;
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (h == 0 || high) {
+          float mn = mrow[h];
+          mon[h] = mo[h];
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            float x = fmaxf(fmaxf(z[2 * b][2 * h], z[2 * b][2 * h + 1]), fmaxf(z[2 * b + 1][2 * h], z[2 * b + 1][2 * h + 1]));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+            x *= rs[h] * kk[b];
+            mn = fmaxf(mn, x);
+            mon[h] = fmaxf(mon[h], x + ve[b]);
           }
+          // the sum's scale follows its maximum exactly, the output's only in steps
+          if (mn > mrow[h]) l[h] *= tc::ex2_approx(mrow[h] - mn), mrow[h] = mn;
+          jump |= mon[h] > mo[h] + kLazy;
+        }
+      if (__any_sync(0xffffffffu, jump)) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          if (h == 0 || high) {
+            const float f = mon[h] > mo[h] ? exp2f(mo[h] - mon[h]) : 1.f;
+            mo[h] = fmaxf(mo[h], mon[h]);
+#pragma unroll
+            for (int k = 0; k < NT; ++k) o[k][2 * h] *= f, o[k][2 * h + 1] *= f;
+          }
+      }
+      uint32_t pw[NS][2][4];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (h == 0 || high) {
+          const float ml = mrow[h] == -INFINITY ? 0.f : mrow[h], mol = mo[h] == -INFINITY ? 0.f : mo[h];
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            const float f = rs[h] * kk[b], sh = mol - ve[b];
+            float sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float x = z[2 * b + i][2 * h], y = z[2 * b + i][2 * h + 1];
+              const float p = tc::ex2_approx(fmaf(x, f, -sh)), q = tc::ex2_approx(fmaf(y, f, -sh));
+              sum += p + q;
+              const uint32_t w = half2_bits(p, q);
+              pw[0][b][2 * i + h] = w;
+              if (NS == 2) pw[NS - 1][b][2 * i + h] = half2_rest(p, q, w);
+            }
+            // The weights' sum in units of 2^m.  Where a block's values are so much smaller than
+            // the others' that its weights vanish before their share of the sum does, the sum
+            // takes exponentials of its own.
+            if (__any_sync(0xffffffffu, sh - ml > kFar)) {
+              sum = 0.f;
+#pragma unroll
+              for (int i = 0; i < 2; ++i)
+                sum += tc::ex2_approx(fmaf(z[2 * b + i][2 * h], f, -ml)) +
+                       tc::ex2_approx(fmaf(z[2 * b + i][2 * h + 1], f, -ml));
+              l[h] += sum;
+            } else {
+              l[h] += sum * tc::ex2_approx(sh - ml);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int p = 0; p < NS; ++p)
+#pragma unroll
+            for (int b = 0; b < 2; ++b) pw[p][b][h] = pw[p][b][2 + h] = 0;
         }
       }
 
