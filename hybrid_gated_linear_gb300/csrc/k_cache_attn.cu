@@ -110,6 +110,7 @@ struct Piece {
   int64_t f, seg0;      // list indices: of the next piece, of segment m's first entry (head 0)
   int m, n, r0, hk, ua, ub, seg, rows;
   int c0, c1;           // the teams that share the segment and head
+  int all_lo, all_hi;   // tokens that every row sees, relative to the segment's base
 };
 
 // Where a unit's two 16-token blocks are (in blocks of 16 rows from the pool's start) and, one
@@ -310,6 +311,10 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG, Solo>::kPerSm)
           p.f = next;
         }
         p.seg = p.m * Hk + p.hk;
+        const int64_t last = p.s.p0 + (p.r0 + max(p.rows, 1) - 1) / G;
+        p.all_lo = (int)min(max((int64_t)0, max(p.s.first, a.W > 0 ? last - a.W + 1 : (int64_t)0) - p.s.base),
+                            (int64_t)0x7fffffff);
+        p.all_hi = p.s.hi >= p.s.lo && p.rows > 0 ? (int)(p.s.p0 + p.r0 / G - p.s.base) : -1;
         if (p.hk == Hk - 1) p.seg0 = p.f, ++p.m;
       }
     }
@@ -496,25 +501,11 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG, Solo>::kPerSm)
     float o[NT][4], mrow[2] = {-INFINITY, -INFINITY}, mo[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-    int lo_r[2], hi_r[2];
-    float rs[2];
     // first token a query at position p sees, relative to the segment's base
     auto sees_from = [&](int64_t p) {
       const int64_t lo = max(s_p.s.first, a.W > 0 ? p - a.W + 1 : (int64_t)0) - s_p.s.base;
       return (int)max((int64_t)0, min(lo, (int64_t)0x7fffffff));
     };
-    const bool any = s_p.s.hi >= s_p.s.lo;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = rg * 16 + g + 8 * i;
-      const int64_t p = s_p.s.p0 + (r0 + r) / G;
-      rs[i] = s_rs[r];
-      hi_r[i] = any && r < rows ? (int)(p - s_p.s.base) : -1;
-      lo_r[i] = sees_from(p);
-    }
-    // tokens every row of the block sees
-    const int all_lo = rows > 0 ? sees_from(s_p.s.p0 + (r0 + rows - 1) / G) : 0;
-    const int all_hi = any && rows > 0 ? (int)(s_p.s.p0 + r0 / G - s_p.s.base) : -1;
     const bool high = rows - rg * 16 > 8;
     const uint4* qf = reinterpret_cast<const uint4*>(s_q) + (size_t)rg * NS * KS * 32 + lane;
 
@@ -587,8 +578,17 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG, Solo>::kPerSm)
 
       // Row half h (rows g, g + 8) and 16-token block b: z holds raw products, to be multiplied
       // by f = rs kk.  The upper half is skipped where there are eight rows or fewer.
-      const bool whole = ok0 && ok1 && tok >= all_lo && tok + kUnit - 1 <= all_hi;
-      if (!whole) {  // column 8 i + 2 t4 + e
+      const bool whole = ok0 && ok1 && tok >= s_p.all_lo && tok + kUnit - 1 <= s_p.all_hi;
+      const float rs[2] = {s_rs[rg * 16 + g], s_rs[rg * 16 + g + 8]};
+      if (!whole) {  // column 8 i + 2 t4 + e; at the ends only, so the limits are found here
+        int lo_r[2], hi_r[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int r = rg * 16 + g + 8 * i;
+          const int64_t p = s_p.s.p0 + (s_p.r0 + r) / G;
+          hi_r[i] = s_p.s.hi >= s_p.s.lo && r < s_p.rows ? (int)(p - s_p.s.base) : -1;
+          lo_r[i] = sees_from(p);
+        }
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
