@@ -320,36 +320,36 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG, Solo>::kPerSm)
     }
     team_sync();
     if (s_p.ub == 0) break;
-    const int n = s_p.n, hk = s_p.hk, ua = s_p.ua;
-    const int nu = s_p.ub - ua > tg ? (s_p.ub - ua - tg + TG - 1) / TG : 0;  // units of this group
+    // s_p is read again wherever it is needed: its fields are worth no register in the loop
+    const int nu = s_p.ub - s_p.ua > tg ? (s_p.ub - s_p.ua - tg + TG - 1) / TG : 0;  // units of this group
 
     // ---- pages and scales of the group's units, a batch at a time
     auto load_meta = [&](int batch) {
       const int j = batch * kBatch + lane;
       UnitMeta u{0, 0, 0};
       if (lane < kBatch && j < nu) {
-        const int tok = (ua + tg + j * TG) * kUnit, lo = s_p.s.lo, hi = s_p.s.hi;
+        const int tok = (s_p.ua + tg + j * TG) * kUnit, lo = s_p.s.lo, hi = s_p.s.hi;
         const bool in0 = tok + 15 >= lo && tok <= hi, in1 = tok + 31 >= lo && tok + 16 <= hi;
         const uint32_t pg = (uint32_t)((s_p.s.base + tok) >> a.c.log_p);
         const int row = (int)((s_p.s.base + tok) & (a.c.P - 1));
         const bool small = a.c.P == 16;
         int i0 = -1, i1 = -1;
         if (in0 || (in1 && !small)) {
-          i0 = pool_page(a.c, n, pg);
+          i0 = pool_page(a.c, s_p.n, pg);
           if (i0 < 0) raise_status(a.status, kDevCheck);
         }
         i1 = i0;
         if (small && in1) {
-          i1 = pool_page(a.c, n, pg + 1);
+          i1 = pool_page(a.c, s_p.n, pg + 1);
           if (i1 < 0) raise_status(a.status, kDevCheck);
         }
         if (in0 && i0 >= 0) {
-          const size_t ph = (size_t)i0 * Hk + hk;
+          const size_t ph = (size_t)i0 * Hk + s_p.hk;
           u.at0 = (int)((ph * a.c.P + row) >> 4);
           u.exps |= (__float_as_uint(a.c.ks[ph]) >> 23 & 0xff) | (__float_as_uint(a.c.vs[ph]) >> 23 & 0xff) << 16;
         }
         if (in1 && i1 >= 0) {
-          const size_t ph = (size_t)i1 * Hk + hk;
+          const size_t ph = (size_t)i1 * Hk + s_p.hk;
           u.at1 = (int)((ph * a.c.P + ((row + 16) & (a.c.P - 1))) >> 4);
           u.exps |= (__float_as_uint(a.c.ks[ph]) >> 23 & 0xff) << 8 | (__float_as_uint(a.c.vs[ph]) >> 23 & 0xff) << 24;
         }
@@ -385,12 +385,11 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG, Solo>::kPerSm)
     // ---- queries: rotated, scaled to a power of two near 2^13, in the order the MMAs read
     constexpr int LPR = D / 4, RPI = 32 / LPR;  // lanes per row, rows per iteration of a warp
     constexpr int WARPS = Solo ? 1 : 8;
-    const int rows = s_p.rows, r0 = s_p.r0;  // rows with a query
     for (int i = tt_id; i < RR * D * NS / 8; i += kTeam) reinterpret_cast<uint4*>(s_q)[i] = make_uint4(0, 0, 0, 0);
     for (int i = tt_id; i < RR; i += kTeam) s_rs[i] = 0.f;
     team_sync();
     const int d0q = (lane % LPR) * 4;
-    for (int rb = (Solo ? 0 : warp) * RPI; rb < rows; rb += 4 * WARPS * RPI) {
+    for (int rb = (Solo ? 0 : warp) * RPI; rb < s_p.rows; rb += 4 * WARPS * RPI) {
       float x[4][4], y[4][4];
       bool have[4];
       {
@@ -403,10 +402,10 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG, Solo>::kPerSm)
         const int other = half && hr % 4 == 0 ? (d0q < hr ? d0q + hr : d0q - hr) : d0q;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const int r = rb + k * WARPS * RPI + lane / LPR, rr = r0 + min(r, rows - 1);
-          const int tt = rr / G, h = hk * G + rr - tt * G;
-          have[k] = r < rows;
-          qp[k] = static_cast<const T*>(a.q) + n * a.sq.n + h * a.sq.h + tt * a.sq.t;
+          const int r = rb + k * WARPS * RPI + lane / LPR, rr = s_p.r0 + min(r, s_p.rows - 1);
+          const int tt = rr / G, h = s_p.hk * G + rr - tt * G;
+          have[k] = r < s_p.rows;
+          qp[k] = static_cast<const T*>(a.q) + s_p.n * a.sq.n + h * a.sq.h + tt * a.sq.t;
         }
 #pragma unroll
         for (int k = 0; k < 4; ++k) xr[k] = raw4(qp[k] + d0q), yr[k] = raw4(qp[k] + other);
@@ -424,12 +423,12 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG, Solo>::kPerSm)
           y[k][0] = o.x, y[k][1] = o.y, y[k][2] = o.z, y[k][3] = o.w;
         }
       }
-      if (ua == 0)  // the piece with the first unit adds the meta tokens
+      if (s_p.ua == 0)  // the piece with the first unit adds the meta tokens
         for (int j = 0; j < a.M; ++j) {
           float z[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const int h = hk * G + (r0 + rb + k * WARPS * RPI + lane / LPR) % G;
+            const int h = s_p.hk * G + (s_p.r0 + rb + k * WARPS * RPI + lane / LPR) % G;
             const float4 v = ld4(static_cast<const T*>(a.mk) + ((size_t)h * a.M + j) * D + d0q);
             z[k] = x[k][0] * v.x + x[k][1] * v.y + x[k][2] * v.z + x[k][3] * v.w;
           }
@@ -446,13 +445,13 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG, Solo>::kPerSm)
 #pragma unroll 1
       for (int k = 0; k < 4; ++k) {
         const int r = rb + k * WARPS * RPI + lane / LPR;
-        if (rb + k * WARPS * RPI >= rows) break;
+        if (rb + k * WARPS * RPI >= s_p.rows) break;
         float v[4];
         // the arrays are indexed by constants only
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = k == 0 ? x[0][i] : k == 1 ? x[1][i] : k == 2 ? x[2][i] : x[3][i];
-        if (a.rope.turns && r < rows && d0q < a.rope.rot) {
-          const int tt = (r0 + r) / G, hr = a.rope.rot / 2;
+        if (a.rope.turns && r < s_p.rows && d0q < a.rope.rot) {
+          const int tt = (s_p.r0 + r) / G, hr = a.rope.rot / 2;
           const bool half = a.rope.layout == LIZARD_ROPE_HALF;
           if (tt != angle_of) {
             angle_of = tt;
@@ -480,7 +479,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG, Solo>::kPerSm)
         int e = (int)(__float_as_uint(mx) >> 23) - 127 - 13;
         e = max(-126, min(e, 113));
         const float inv = exp2_int(-e);
-        if (r < rows) {
+        if (r < s_p.rows) {
           if (lane % LPR == 0) s_rs[r] = a.scale * kLog2e * exp2_int(e);
           // element d = (D/4) t + 4 s + i of row r feeds lane (r%8) t, step s, register 2 (i/2) + r/8%2
           const int t = d0q / (D / 4), s = (d0q % (D / 4)) / 4;
@@ -506,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG, Solo>::kPerSm)
       const int64_t lo = max(s_p.s.first, a.W > 0 ? p - a.W + 1 : (int64_t)0) - s_p.s.base;
       return (int)max((int64_t)0, min(lo, (int64_t)0x7fffffff));
     };
-    const bool high = rows - rg * 16 > 8;
+    const bool high = s_p.rows - rg * 16 > 8;
     const uint4* qf = reinterpret_cast<const uint4*>(s_q) + (size_t)rg * NS * KS * 32 + lane;
 
     for (int j = 0; j < nu; ++j) {
@@ -518,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG, Solo>::kPerSm)
       const uint32_t parity = (u / S) & 1;
       const unsigned char* kb = smem + (size_t)st * 2 * Sh::kHalf;
       const unsigned char* vb = kb + Sh::kHalf;
-      const int tok = (ua + tg + j * TG) * kUnit;
+      const int tok = (s_p.ua + tg + j * TG) * kUnit;
       // logits: lane (g, t4) holds channels (D/4) t4 .. of token 8 i + g
       if (!wait(&s_bar[0][st], parity)) break;
       const UnitMeta& um = s_meta[group][(j / kBatch) & 1][j % kBatch];
@@ -724,7 +723,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG, Solo>::kPerSm)
     float* s_o = reinterpret_cast<float*>(smem);
     constexpr int V4 = D / 4, ROWSTEP = kTeam / V4;
     // o[k][2 i + e] is channel (D/8) (2 t4 + e) + k of row g + 8 i
-    const bool whole_seg = ua == 0 && s_p.ub == s_p.s.units;
+    const bool whole_seg = s_p.ua == 0 && s_p.ub == s_p.s.units;
     float* part = reinterpret_cast<float*>(a.ws + (((size_t)M2 * Hk * sizeof(unsigned) + 255) & ~(size_t)255));
     auto slot = [&](int w, bool starts) { return part + (size_t)(2 * w + (starts ? 1 : 0)) * prow * (D + 4); };
     // Four channels f of row r of warp w: lanes g, t4 write them together, so their places in a
@@ -735,7 +734,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG, Solo>::kPerSm)
     };
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-      if (rg * 16 + g + 8 * i < rows)
+      if (rg * 16 + g + 8 * i < s_p.rows)
 #pragma unroll
         for (int e = 0; e < 2; ++e)
 #pragma unroll
@@ -745,14 +744,14 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG, Solo>::kPerSm)
     team_sync();
     auto finish = [&](int r, RowStat s, float4 v, int d0) {
       // row r's 4 channels, normalised and merged
-      const int tt = (r0 + r) / G, h = hk * G + (r0 + r) % G;
+      const int tt = (s_p.r0 + r) / G, h = s_p.hk * G + (s_p.r0 + r) % G;
       const float f = s.l > 0.f ? a.alpha / s.l * exp2f(s.mo - s.m) : 0.f;
       v.x *= f, v.y *= f, v.z *= f, v.w *= f;
       if (a.add) {
-        const float4 w = ld4(static_cast<const T*>(a.add) + n * a.sadd.n + h * a.sadd.h + tt * a.sadd.t + d0);
+        const float4 w = ld4(static_cast<const T*>(a.add) + s_p.n * a.sadd.n + h * a.sadd.h + tt * a.sadd.t + d0);
         v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
       }
-      st4(static_cast<T*>(a.y) + n * a.sy.n + h * a.sy.h + tt * a.sy.t + d0, v);
+      st4(static_cast<T*>(a.y) + s_p.n * a.sy.n + h * a.sy.h + tt * a.sy.t + d0, v);
     };
     auto join = [](RowStat& s, float4& v, RowStat b, float4 w) {
       const float mm = fmaxf(s.m, b.m), mo2 = fmaxf(s.mo, b.mo);
@@ -764,7 +763,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG, Solo>::kPerSm)
       s.m = mm, s.mo = mo2;
     };
     const int d0 = (tt_id % V4) * 4;
-    for (int r = tt_id / V4; r < rows; r += ROWSTEP) {
+    for (int r = tt_id / V4; r < s_p.rows; r += ROWSTEP) {
       RowStat s{-INFINITY, -INFINITY, 0.f};
       float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
@@ -772,8 +771,8 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG, Solo>::kPerSm)
         const int w = Solo ? warp : q * RG + r / 16;
         join(s, v, s_st[w][r % 16], *merge_at(w, r % 16, d0 / 4));
       }
-      if (ua == 0) {
-        const int h = hk * G + (r0 + r) % G;
+      if (s_p.ua == 0) {
+        const int h = s_p.hk * G + (s_p.r0 + r) % G;
         for (int j = 0; j < a.M; ++j) {
           const float z = s_zm[r * kMaxM + j];
           join(s, v, RowStat{z, z, 1.f}, ld4(static_cast<const T*>(a.mv) + ((size_t)h * a.M + j) * D + d0));
@@ -782,16 +781,16 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG, Solo>::kPerSm)
       if (whole_seg) {
         finish(r, s, v, d0);
       } else {
-        float* p = slot(worker, ua == 0);
+        float* p = slot(worker, s_p.ua == 0);
         *reinterpret_cast<float4*>(p + (size_t)r * D + d0) = v;
         if (d0 == 0)
           *reinterpret_cast<float4*>(p + (size_t)prow * D + 4 * r) = make_float4(s.m, s.mo, s.l, 0.f);
       }
     }
-    if (ua == 0)  // queries beyond the sequence's count
-      for (int r = rows + tt_id / V4; r < RR && r0 + r < a.T * G; r += ROWSTEP) {
-        const int tt = (r0 + r) / G, h = hk * G + (r0 + r) % G;
-        st4(static_cast<T*>(a.y) + n * a.sy.n + h * a.sy.h + tt * a.sy.t + d0, make_float4(0.f, 0.f, 0.f, 0.f));
+    if (s_p.ua == 0)  // queries beyond the sequence's count
+      for (int r = s_p.rows + tt_id / V4; r < RR && s_p.r0 + r < a.T * G; r += ROWSTEP) {
+        const int tt = (s_p.r0 + r) / G, h = s_p.hk * G + (s_p.r0 + r) % G;
+        st4(static_cast<T*>(a.y) + s_p.n * a.sy.n + h * a.sy.h + tt * a.sy.t + d0, make_float4(0.f, 0.f, 0.f, 0.f));
       }
     if (!whole_seg) {
       const int c0 = s_p.c0, c1 = s_p.c1;
@@ -812,14 +811,14 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG, Solo>::kPerSm)
         const int k = tt_id % V4;
         constexpr int RW = 4, GROUPS = ROWSTEP;
         int rp = 1;
-        while (rp < rows && rp < GROUPS) rp <<= 1;
+        while (rp < s_p.rows && rp < GROUPS) rp <<= 1;
         if (!Solo && rp < GROUPS) {
           // fewer rows than groups of lanes: GROUPS / rp groups share out a row's partials
           const int grp = tt_id / V4, r = grp % rp, sub = grp / rp, PS = GROUPS / rp, np = c1 - c0 + 1;
           RowStat s{-INFINITY, -INFINITY, 0.f};
           for (int cb = c0; cb <= c1; cb += V4) {
             float4 b = make_float4(-INFINITY, -INFINITY, 0.f, 0.f);
-            if (r < rows && cb + k <= c1)
+            if (r < s_p.rows && cb + k <= c1)
               b = __ldcg(reinterpret_cast<const float4*>(slot(cb + k, cb + k == c0) + (size_t)prow * D + 4 * r));
             float mm = b.x, mw = b.y;
 #pragma unroll
@@ -837,7 +836,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG, Solo>::kPerSm)
           const int ca = c0 + np * sub / PS, cz = c0 + np * (sub + 1) / PS;
           for (int cb = ca; __any_sync(0xffffffffu, cb < cz); cb += V4) {
             float wk = 0.f;
-            if (r < rows && cb + k < cz) {
+            if (r < s_p.rows && cb + k < cz) {
               const float mo_k = __ldcg(slot(cb + k, cb + k == c0) + (size_t)prow * D + 4 * r + 1);
               if (mo_k != -INFINITY) wk = exp2f(mo_k - s.mo);
             }
@@ -847,7 +846,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG, Solo>::kPerSm)
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
                 x[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (r < rows && i + e < cn)
+                if (r < s_p.rows && i + e < cn)
                   x[e] = __ldcg(reinterpret_cast<const float4*>(slot(cb + i + e, cb + i + e == c0) + (size_t)r * D + d0));
               }
 #pragma unroll
@@ -861,14 +860,14 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG, Solo>::kPerSm)
           float4* s_v = reinterpret_cast<float4*>(s_o);
           s_v[tt_id] = v;
           team_sync();
-          if (sub == 0 && r < rows) {
+          if (sub == 0 && r < s_p.rows) {
             for (int q = 1; q < PS; ++q) {
               const float4 w = s_v[(q * rp + r) * V4 + k];
               v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
             }
             finish(r, s, v, d0);
           }
-        } else for (int rb = tt_id / V4; rb - tt_id / V4 < rows; rb += RW * ROWSTEP) {
+        } else for (int rb = tt_id / V4; rb - tt_id / V4 < s_p.rows; rb += RW * ROWSTEP) {
           RowStat s[RW];
           float4 v[RW];
 #pragma unroll
@@ -879,7 +878,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG, Solo>::kPerSm)
 #pragma unroll
             for (int q = 0; q < RW; ++q) {
               b[q] = make_float4(-INFINITY, -INFINITY, 0.f, 0.f);
-              if (rb + q * ROWSTEP < rows && cb + k <= c1)
+              if (rb + q * ROWSTEP < s_p.rows && cb + k <= c1)
                 b[q] = __ldcg(reinterpret_cast<const float4*>(slot(cb + k, cb + k == c0) + (size_t)prow * D +
                                                               4 * (rb + q * ROWSTEP)));
             }
@@ -908,7 +907,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG, Solo>::kPerSm)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                   x[q][e] = make_float4(0.f, 0.f, 0.f, 0.f);
-                  if (rb + q * ROWSTEP < rows && i + e < cn)
+                  if (rb + q * ROWSTEP < s_p.rows && i + e < cn)
                     x[q][e] = __ldcg(reinterpret_cast<const float4*>(slot(cb + i + e, cb + i + e == c0) +
                                                                      (size_t)(rb + q * ROWSTEP) * D + d0));
                 }
@@ -924,7 +923,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG, Solo>::kPerSm)
           }
 #pragma unroll
           for (int q = 0; q < RW; ++q)
-            if (rb + q * ROWSTEP < rows) finish(rb + q * ROWSTEP, s[q], v[q], d0);
+            if (rb + q * ROWSTEP < s_p.rows) finish(rb + q * ROWSTEP, s[q], v[q], d0);
         }
         if (tt_id == 0) reinterpret_cast<unsigned*>(a.ws)[s_p.seg] = 0u;
       }
