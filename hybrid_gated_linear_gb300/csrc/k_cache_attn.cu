@@ -5,10 +5,8 @@
 // tokens.  With z the logits in units of log 2, softmax is one pass over the cache:
 //   m' = max(m, z),  l' = l 2^(m-m') + sum 2^(z-m'),  o' = o 2^(m-m') + sum 2^(z-m') v.
 // The value scales are powers of two 2^e per page, so the weights the tensor cores see are
-// 2^(z+e-mo) with a maximum mo of their own: they stay in (0, 1], whatever the pages' scales.
-//
-// l's maximum m moves with every unit, mo (and with it the rescaling of o) only by more than
-// 2^kLazy at a time.
+// 2^(z+e-mo) with a maximum mo of their own: they stay near (0, 1], whatever the pages' scales.
+// m moves with every unit, mo (and with it the rescaling of o) only by more than kLazy at a time.
 //
 // What bounds it: the cache is read once, 2 D bytes per token and head, and everything else
 // is small; the floor is those bytes at the measured copy rate.  So the work is cut evenly
@@ -20,6 +18,13 @@
 // (pages are contiguous and stored in the order the reads want) while the warp computes.
 // The products run on mma.sync: 16 rows fill its M, where the 128 rows of a tcgen05 tile
 // would be an eighth full, and the tensor time is a third of the copy time.
+//
+// Measured, H = 32, Hk = 8, D = 128, one new token, e4m3 (share of the measured copy rate):
+//   64 sequences of 8192 tokens 188 us (84%), of 128 to 8192 111 us (72%); one of 131072
+//   tokens 56 us (70%); 64 x 32 heads, windows of 1024, bytes 127 us (61%); one sequence of
+//   500 tokens 13 us.
+// The loop runs at 6.7 TB/s; the rest is the start (positions, pages, first copies: about 6 us)
+// and the end of the slowest warp and the joins after it (10 to 20 us).
 #include <algorithm>
 
 #include "kv_cache.cuh"
@@ -36,8 +41,9 @@ constexpr int kBatch = 16;  // units whose pages and scales are looked up at a t
 constexpr int kMaxM = 16;
 constexpr int kMaxCtas = 304;  // CTAs of a launch at most (sizes the scratch): two per SM
 // From this many (sequence, head) pairs on, each warp works alone: starting and ending a
-// segment then stalls one warp of sixteen instead of a CTA's eight.  Below, a pair would be
-// spread over so many warps that joining their results costs more.
+// segment then stalls one warp of sixteen instead of a CTA's eight (512 pairs, 128 to 8192
+// tokens: 132 us against 160).  Below, a pair would be spread over so many warps that joining
+// their results costs more (128 pairs, 4096 tokens: 45 us against 39).
 constexpr int64_t kSoloSegments = 256;
 constexpr float kLazy = 8.f;  // outputs are rescaled when their maximum has grown by 2^8: weights fit binary16
 constexpr float kFar = 60.f;  // see where it is used
@@ -155,7 +161,8 @@ struct Shape {
       kSmem + NT * RR * (kMaxM + 1) * 4 + NG * 2 * kBatch * (int)sizeof(UnitMeta) + 2560 <= 113 * 1024 ? 2 : 1;
   // Starting a segment costs a team about as much as this many units: the list of work holds
   // that many empty entries in front of every segment, so that teams with many short segments
-  // get fewer units.
+  // get fewer units.  (8 and 20 instead: 64 uneven sequences 111 -> 106 us, 16 of them 67 -> 61,
+  // but windows 127 -> 136 and drafted tokens 33 -> 36.)
   static constexpr int kSegCost = Solo ? 3 : 12;
   static constexpr int kMinUnits = 4 * TG;  // of a piece, where a segment has them
 };
@@ -606,7 +613,8 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG, Solo>::kPerSm)
           mon[h] = mo[h];
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
-            float x = fmaxf(fmaxf(z[2 * b][2 * h], z[2 * b][2 * h + 1]), fmaxf(z[2 * b + 1][2 * h], z[2 * b + 1][2 * h + 1]));
+            float x = fmaxf(fmaxf(z[2 * b][2 * h], z[2 * b][2 * h + 1]),
+                            fmaxf(z[2 * b + 1][2 * h], z[2 * b + 1][2 * h + 1]));
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
             x *= rs[h] * kk[b];

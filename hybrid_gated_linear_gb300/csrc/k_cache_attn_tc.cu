@@ -20,6 +20,12 @@
 // cache's bytes are few.  One CTA per SM takes an equal share of the list of all blocks of
 // all (sequence, rows, head), whatever their lengths; where a share ends inside one, its parts
 // are joined by the last CTA to finish (fixed order: results do not depend on timing).
+//
+// Measured, H = 32, Hk = 8, D = 128, e4m3: two sequences, 2048 new tokens at 14336: 1.10 ms,
+// 934 TFLOP/s (47% of the measured bf16 burst; bytes 1.28 ms, their conversion takes twice the
+// operations).  With the row warps' work left out 1.01, with the conversions left out 0.87, with
+// both 0.64 ms: the roles contend for issue slots and shared memory, which the operands alone
+// keep three quarters busy.  Staging the queries and joining parts cost about 80 us of it.
 #include <algorithm>
 
 #include "kv_cache.cuh"
@@ -493,7 +499,8 @@ __device__ __noinline__ void join_rows(const CacheAttn& args, const Piece& p, co
     float m = -INFINITY, mo = -INFINITY, l = 0.f;
 #pragma unroll 4
     for (int c = c0; c <= c1; ++c) {
-      const float4 x = __ldcg(reinterpret_cast<const float4*>(part + partial_at<D>(c, c == c0) + (size_t)kRows * D + 4 * tid));
+      const float4 x =
+          __ldcg(reinterpret_cast<const float4*>(part + partial_at<D>(c, c == c0) + (size_t)kRows * D + 4 * tid));
       const float mm = fmaxf(m, x.x);
       if (x.x != -INFINITY) l = (m == -INFINITY ? 0.f : l * exp2f(m - mm)) + x.z * exp2f(x.x - mm);
       m = mm, mo = fmaxf(mo, x.y);
@@ -594,7 +601,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   unsigned char* sm = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   __shared__ Ctl<NB> s_ctl;
   __shared__ float s_rs[kRows];
-  __shared__ __align__(16) float2 s_scale[4][8];  // of a block's 16-token parts: key scale (0: unseen), log2 of the value scale
+  // of a block's 16-token parts: key scale (0: unseen), log2 of the value scale
+  __shared__ __align__(16) float2 s_scale[4][8];
   __shared__ int64_t s_sum[kThreads / 32];
   __shared__ Piece s_p;
   __shared__ int s_last;
@@ -669,310 +677,310 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
   int it = 0;  // blocks done in earlier pieces: stages and phases go on from there
 
   while (true) {
-  if (tid == 0) {
-    Piece& p = s_p;
-    p.ub = 0;
-    if (p.f < f1) {
-      p.v = view_of(a, p.m, tiles, G);
-      p.n = p.m / tiles;
-      const int entries = p.v.units + kCost;
-      p.hk = (int)((p.f - p.seg0) / entries);
-      const int64_t next = p.seg0 + (int64_t)(p.hk + 1) * entries, head0 = next - p.v.units;
-      p.ua = (int)max((int64_t)0, p.f - head0);
-      // 0: the share ends before this head's first block
-      p.ub = (int)max((int64_t)0, min((int64_t)p.v.units, f1 - head0));
-      p.seg = p.m * Hk + p.hk;
-      p.c0 = (int)(head0 / share);
-      p.c1 = (int)((next - 1) / share);
-      p.f = next;
-      if (p.hk == Hk - 1) p.seg0 = next, ++p.m;
-    }
-  }
-  cta_sync();
-  if (s_p.ub == 0) break;
-  const View& s_v = s_p.v;
-  const int n = s_p.n, hk = s_p.hk, b0 = s_p.ua, nblk = s_p.ub - s_p.ua;
-  const int rows = s_v.rows, r0 = s_v.r0;
-
-  stage_queries<D>(a, s_p, sm + Sm::Q, s_rs, reinterpret_cast<int64_t*>(sm + Sm::R),
-                   reinterpret_cast<int*>(sm + Sm::R) + 2 * kRows, reinterpret_cast<float2*>(sm + Sm::K));
-  cta_sync();
-
-  bool done_ok = true;
-  float l = 0.f, m = -INFINITY, mo = -INFINITY;
-  if (warp == kMmaWarp) {
-    // ------------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      // descriptors differ in their address field (16-byte units) only: one addition per MMA,
-      // since this thread's instructions are what the tensor cores wait for
-      const uint32_t sb = smem_u32(sm);
-      const uint64_t dq = desc_k(sb + Sm::Q, kBlock, 0), dk = desc_k(sb + Sm::K, kBlock, 0);
-      const uint64_t dv = desc_mn(sb + Sm::V, kBlock, 0);
-      constexpr uint32_t kTile16 = Sm::kTile / 16;
-      const uint32_t id_s = idesc_f16(128, kBlock, false), id_o = idesc_f16(128, D, true);
-      bool ok = true;
-      auto scores = [&](int t, int i) {
-        const uint64_t qa = dq + t * kTile16, kb = dk + (i & 1) * kTile16;  // i counts over all pieces
-        const uint32_t ts = tmem + t * kBlock;
-#pragma unroll
-        for (int j = 0; j < D / 16; ++j) {
-          constexpr uint32_t kCol = kBlock * 128 / 16;  // next 64 channels
-          const uint32_t off = (j >> 2) * kCol + (j & 3) * 2;
-          mma_bf16(ts, qa + off, kb + off, id_s, j > 0);
-        }
-        mma_commit(&ctl->bar[SF + t]);
-        if (t == 1) mma_commit(&ctl->bar[KE + (i & 1)]);
-      };
-      const int end = it + nblk;
-      if ((ok = wait_bar(ctl, KF + (it & 1), (it >> 1) & 1))) {
-        tc_fence_after();
-        scores(0, it), scores(1, it);
+    if (tid == 0) {
+      Piece& p = s_p;
+      p.ub = 0;
+      if (p.f < f1) {
+        p.v = view_of(a, p.m, tiles, G);
+        p.n = p.m / tiles;
+        const int entries = p.v.units + kCost;
+        p.hk = (int)((p.f - p.seg0) / entries);
+        const int64_t next = p.seg0 + (int64_t)(p.hk + 1) * entries, head0 = next - p.v.units;
+        p.ua = (int)max((int64_t)0, p.f - head0);
+        // 0: the share ends before this head's first block
+        p.ub = (int)max((int64_t)0, min((int64_t)p.v.units, f1 - head0));
+        p.seg = p.m * Hk + p.hk;
+        p.c0 = (int)(head0 / share);
+        p.c1 = (int)((next - 1) / share);
+        p.f = next;
+        if (p.hk == Hk - 1) p.seg0 = next, ++p.m;
       }
-      for (int i = it; ok && i < end; ++i) {
-        const uint32_t par = (i >> 1) & 1;
-        ok = wait_bar(ctl, VF + (i & 1), par);
-        for (int t = 0; ok && t < 2; ++t) {
-          if (!(ok = wait_bar(ctl, PF + t, i & 1))) break;
-          tc_fence_after();
-          const uint64_t vb = dv + (i & 1) * kTile16;
-          const uint32_t to = tmem + 256 + t * D, ts = tmem + t * kBlock;
+    }
+    cta_sync();
+    if (s_p.ub == 0) break;
+    const View& s_v = s_p.v;
+    const int n = s_p.n, hk = s_p.hk, b0 = s_p.ua, nblk = s_p.ub - s_p.ua;
+    const int rows = s_v.rows, r0 = s_v.r0;
+
+    stage_queries<D>(a, s_p, sm + Sm::Q, s_rs, reinterpret_cast<int64_t*>(sm + Sm::R),
+                     reinterpret_cast<int*>(sm + Sm::R) + 2 * kRows, reinterpret_cast<float2*>(sm + Sm::K));
+    cta_sync();
+
+    bool done_ok = true;
+    float l = 0.f, m = -INFINITY, mo = -INFINITY;
+    if (warp == kMmaWarp) {
+      // ------------------------------------------------------------------ MMA issuer
+      if (lane == 0) {
+        // descriptors differ in their address field (16-byte units) only: one addition per MMA,
+        // since this thread's instructions are what the tensor cores wait for
+        const uint32_t sb = smem_u32(sm);
+        const uint64_t dq = desc_k(sb + Sm::Q, kBlock, 0), dk = desc_k(sb + Sm::K, kBlock, 0);
+        const uint64_t dv = desc_mn(sb + Sm::V, kBlock, 0);
+        constexpr uint32_t kTile16 = Sm::kTile / 16;
+        const uint32_t id_s = idesc_f16(128, kBlock, false), id_o = idesc_f16(128, D, true);
+        bool ok = true;
+        auto scores = [&](int t, int i) {
+          const uint64_t qa = dq + t * kTile16, kb = dk + (i & 1) * kTile16;  // i counts over all pieces
+          const uint32_t ts = tmem + t * kBlock;
 #pragma unroll
-          for (int j = 0; j < kBlock / 16; ++j) mma_f16_ts(to, ts + 8 * j, vb + j * 128, id_o, j > 0 || i > it);
-          mma_commit(&ctl->bar[OD + t]);
-          if (t == 1) mma_commit(&ctl->bar[VE + (i & 1)]);
-          if (i + 1 < end) {
-            if (t == 0 && !(ok = wait_bar(ctl, KF + ((i + 1) & 1), ((i + 1) >> 1) & 1))) break;
+          for (int j = 0; j < D / 16; ++j) {
+            constexpr uint32_t kCol = kBlock * 128 / 16;  // next 64 channels
+            const uint32_t off = (j >> 2) * kCol + (j & 3) * 2;
+            mma_bf16(ts, qa + off, kb + off, id_s, j > 0);
+          }
+          mma_commit(&ctl->bar[SF + t]);
+          if (t == 1) mma_commit(&ctl->bar[KE + (i & 1)]);
+        };
+        const int end = it + nblk;
+        if ((ok = wait_bar(ctl, KF + (it & 1), (it >> 1) & 1))) {
+          tc_fence_after();
+          scores(0, it), scores(1, it);
+        }
+        for (int i = it; ok && i < end; ++i) {
+          const uint32_t par = (i >> 1) & 1;
+          ok = wait_bar(ctl, VF + (i & 1), par);
+          for (int t = 0; ok && t < 2; ++t) {
+            if (!(ok = wait_bar(ctl, PF + t, i & 1))) break;
             tc_fence_after();
-            scores(t, i + 1);
+            const uint64_t vb = dv + (i & 1) * kTile16;
+            const uint32_t to = tmem + 256 + t * D, ts = tmem + t * kBlock;
+#pragma unroll
+            for (int j = 0; j < kBlock / 16; ++j) mma_f16_ts(to, ts + 8 * j, vb + j * 128, id_o, j > 0 || i > it);
+            mma_commit(&ctl->bar[OD + t]);
+            if (t == 1) mma_commit(&ctl->bar[VE + (i & 1)]);
+            if (i + 1 < end) {
+              if (t == 0 && !(ok = wait_bar(ctl, KF + ((i + 1) & 1), ((i + 1) >> 1) & 1))) break;
+              tc_fence_after();
+              scores(t, i + 1);
+            }
           }
         }
+        if (!ok) ctl->abort = 1;
       }
-      if (!ok) ctl->abort = 1;
-    }
-  } else if (warp >= 8) {
-    // ------------------------------------------------------------------ codes -> binary16
-    // Warp w takes the 16-token parts w, w + 3, w + 6 of a block: IT steps of 32 chunks each.
-    constexpr int IT = D / 32, NP = (8 + kCodeWarps - 1) / kCodeWarps;
-    const int w = warp - 8;
-    // Eight lanes that access together hold four chunks each of two rows.  At D = 128 the rows
-    // are r and r ^ 5: the codes they read lie in different halves of the banks (chunk c of row r
-    // is at place c ^ (r & 7)), and so do the binary16 chunks they store, 2 c ^ (r & 7).
-    const int chunk = D == 128 ? 4 * ((lane >> 3) & 1) + (lane & 3) : lane & 3;
-    const int row = D == 128 ? ((lane >> 4) & 1) ^ ((lane & 4) ? 5 : 0) : lane >> 2;
-    auto row_of = [&](int k) { return D == 128 ? 8 * (k >> 1) + (row ^ (2 * (k & 1))) : 8 * k + row; };
-    const int lo = s_v.lo, hi = s_v.hi;
-    const int64_t base = s_v.base;
-    // Four blocks are looked up at a time: lane 8 b + p has part p of block b.  The page numbers
-    // of the batch after next are on their way while the next batch's scales are.
-    int at = -1, nat = -1;  // where the part is (in parts of 16 rows; -1: unseen)
-    uint32_t full = 0, nfull = 0;  // the lanes whose part exists
-    float2 sc = make_float2(0.f, 0.f), nsc = sc;
-    int id = -1;
-    auto token = [&](int i) { return (b0 + i + (lane >> 3)) * kBlock + (lane & 7) * 16; };
-    auto look = [&](int i) {
-      id = -2;  // nothing to see
-      const int tok = token(i);
-      if (i + (lane >> 3) < nblk && tok + 15 >= lo && tok <= hi)
-        id = a.c.table[(size_t)n * a.c.max_pages + (uint32_t)((base + tok) >> a.c.log_p) % (uint32_t)a.c.max_pages];
-    };
-    auto find = [&](int i) {
-      nat = -1;
-      nsc = make_float2(0.f, 0.f);
-      if ((unsigned)id < (unsigned)a.c.pages) {
-        const size_t ph = (size_t)id * Hk + hk;
-        nat = (int)((ph * a.c.P + (int)((base + token(i)) & (a.c.P - 1))) >> 4);
-        nsc = make_float2(a.c.ks[ph], a.c.vs[ph]);
-      } else if (id != -2) {
-        raise_status(a.status, kDevCheck);
-      }
-      nfull = __ballot_sync(0xffffffffu, nat >= 0);
-    };
-    // Copies block i's codes (x = 0 keys, 1 values); past the batch in `at`, it is the next one's.
-    auto copy = [&](int x, int i) {
-      const uint32_t mask = ((i & 3) ? full : nfull) >> ((i & 3) * 8) & 0xff;
-      const int part = __shfl_sync(0xffffffffu, (i & 3) ? at : nat, (i & 3) * 8 + (lane & 7));
-      if (lane == 0) mbar_arrive_expect_tx(&ctl->bar[RF + x], __popc(mask) * 16 * D);
-      __syncwarp();
-      if (lane < 8 && part >= 0)
-        bulk_load(sm + Sm::R + x * Sm::kRaw + lane * 16 * D, (x ? a.c.v : a.c.k) + (size_t)part * (16 * D), 16 * D,
-                  &ctl->bar[RF + x]);
-    };
-    auto convert = [&](const unsigned char* raw, unsigned char* tile, int i) {
-      const int tok = (b0 + i) * kBlock;
-      const uint32_t mask = full >> ((i & 3) * 8) & 0xff;
-      // parts that end beyond what is seen hold bytes that were never written
-      const bool whole = mask == 0xff && tok >= lo && tok + kBlock - 1 <= hi;
-#pragma unroll
-      for (int q = 0; q < NP; ++q) {
-        const int p = w + q * kCodeWarps;
-        if (p >= 8) break;
-        uint4 u[IT];
-#pragma unroll
-        for (int k = 0; k < IT; ++k) {
-          const int r = row_of(k);
-          u[k] = *reinterpret_cast<const uint4*>(raw + (p * 16 + r) * D + 16 * chunk_place<D>(r, chunk));
+    } else if (warp >= 8) {
+      // ------------------------------------------------------------------ codes -> binary16
+      // Warp w takes the 16-token parts w, w + 3, w + 6 of a block: IT steps of 32 chunks each.
+      constexpr int IT = D / 32, NP = (8 + kCodeWarps - 1) / kCodeWarps;
+      const int w = warp - 8;
+      // Eight lanes that access together hold four chunks each of two rows.  At D = 128 the rows
+      // are r and r ^ 5: the codes they read lie in different halves of the banks (chunk c of row r
+      // is at place c ^ (r & 7)), and so do the binary16 chunks they store, 2 c ^ (r & 7).
+      const int chunk = D == 128 ? 4 * ((lane >> 3) & 1) + (lane & 3) : lane & 3;
+      const int row = D == 128 ? ((lane >> 4) & 1) ^ ((lane & 4) ? 5 : 0) : lane >> 2;
+      auto row_of = [&](int k) { return D == 128 ? 8 * (k >> 1) + (row ^ (2 * (k & 1))) : 8 * k + row; };
+      const int lo = s_v.lo, hi = s_v.hi;
+      const int64_t base = s_v.base;
+      // Four blocks are looked up at a time: lane 8 b + p has part p of block b.  The page numbers
+      // of the batch after next are on their way while the next batch's scales are.
+      int at = -1, nat = -1;  // where the part is (in parts of 16 rows; -1: unseen)
+      uint32_t full = 0, nfull = 0;  // the lanes whose part exists
+      float2 sc = make_float2(0.f, 0.f), nsc = sc;
+      int id = -1;
+      auto token = [&](int i) { return (b0 + i + (lane >> 3)) * kBlock + (lane & 7) * 16; };
+      auto look = [&](int i) {
+        id = -2;  // nothing to see
+        const int tok = token(i);
+        if (i + (lane >> 3) < nblk && tok + 15 >= lo && tok <= hi)
+          id = a.c.table[(size_t)n * a.c.max_pages + (uint32_t)((base + tok) >> a.c.log_p) % (uint32_t)a.c.max_pages];
+      };
+      auto find = [&](int i) {
+        nat = -1;
+        nsc = make_float2(0.f, 0.f);
+        if ((unsigned)id < (unsigned)a.c.pages) {
+          const size_t ph = (size_t)id * Hk + hk;
+          nat = (int)((ph * a.c.P + (int)((base + token(i)) & (a.c.P - 1))) >> 4);
+          nsc = make_float2(a.c.ks[ph], a.c.vs[ph]);
+        } else if (id != -2) {
+          raise_status(a.status, kDevCheck);
         }
-        if (!whole) {
+        nfull = __ballot_sync(0xffffffffu, nat >= 0);
+      };
+      // Copies block i's codes (x = 0 keys, 1 values); past the batch in `at`, it is the next one's.
+      auto copy = [&](int x, int i) {
+        const uint32_t mask = ((i & 3) ? full : nfull) >> ((i & 3) * 8) & 0xff;
+        const int part = __shfl_sync(0xffffffffu, (i & 3) ? at : nat, (i & 3) * 8 + (lane & 7));
+        if (lane == 0) mbar_arrive_expect_tx(&ctl->bar[RF + x], __popc(mask) * 16 * D);
+        __syncwarp();
+        if (lane < 8 && part >= 0)
+          bulk_load(sm + Sm::R + x * Sm::kRaw + lane * 16 * D, (x ? a.c.v : a.c.k) + (size_t)part * (16 * D), 16 * D,
+                    &ctl->bar[RF + x]);
+      };
+      auto convert = [&](const unsigned char* raw, unsigned char* tile, int i) {
+        const int tok = (b0 + i) * kBlock;
+        const uint32_t mask = full >> ((i & 3) * 8) & 0xff;
+        // parts that end beyond what is seen hold bytes that were never written
+        const bool whole = mask == 0xff && tok >= lo && tok + kBlock - 1 <= hi;
+#pragma unroll
+        for (int q = 0; q < NP; ++q) {
+          const int p = w + q * kCodeWarps;
+          if (p >= 8) break;
+          uint4 u[IT];
 #pragma unroll
           for (int k = 0; k < IT; ++k) {
-            const int tk = tok + 16 * p + row_of(k);
-            if (!(mask >> p & 1) || tk < lo || tk > hi) u[k] = make_uint4(0, 0, 0, 0);
+            const int r = row_of(k);
+            u[k] = *reinterpret_cast<const uint4*>(raw + (p * 16 + r) * D + 16 * chunk_place<D>(r, chunk));
+          }
+          if (!whole) {
+#pragma unroll
+            for (int k = 0; k < IT; ++k) {
+              const int tk = tok + 16 * p + row_of(k);
+              if (!(mask >> p & 1) || tk < lo || tk > hi) u[k] = make_uint4(0, 0, 0, 0);
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < IT; ++k) {
+            const int r = row_of(k);
+            uint32_t h[8];
+            const uint32_t x[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) codes_to_half<F>(x[e], h[2 * e], h[2 * e + 1]);
+            unsigned char* t = tile + p * 16 * 128;
+            *reinterpret_cast<uint4*>(t + sw128_offset(r, 16 * chunk, kBlock)) = make_uint4(h[0], h[1], h[2], h[3]);
+            *reinterpret_cast<uint4*>(t + sw128_offset(r, 16 * chunk + 8, kBlock)) = make_uint4(h[4], h[5], h[6], h[7]);
           }
         }
-#pragma unroll
-        for (int k = 0; k < IT; ++k) {
-          const int r = row_of(k);
-          uint32_t h[8];
-          const uint32_t x[4] = {u[k].x, u[k].y, u[k].z, u[k].w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) codes_to_half<F>(x[e], h[2 * e], h[2 * e + 1]);
-          unsigned char* t = tile + p * 16 * 128;
-          *reinterpret_cast<uint4*>(t + sw128_offset(r, 16 * chunk, kBlock)) = make_uint4(h[0], h[1], h[2], h[3]);
-          *reinterpret_cast<uint4*>(t + sw128_offset(r, 16 * chunk + 8, kBlock)) = make_uint4(h[4], h[5], h[6], h[7]);
+        fence_proxy_async_smem();
+      };
+      look(0);
+      find(0);
+      look(4);
+      if (w < 2) copy(w, 0);
+      bool ok = true;
+      for (int i = 0; i < nblk; ++i) {
+        const int gi = it + i, st = gi & 1;  // gi counts over all pieces
+        const uint32_t free_par = ((gi >> 1) & 1) ^ 1;
+        if ((i & 3) == 0) {
+          at = nat, sc = nsc, full = nfull;
+          find(i + 4);
+          look(i + 8);
         }
-      }
-      fence_proxy_async_smem();
-    };
-    look(0);
-    find(0);
-    look(4);
-    if (w < 2) copy(w, 0);
-    bool ok = true;
-    for (int i = 0; i < nblk; ++i) {
-      const int gi = it + i, st = gi & 1;  // gi counts over all pieces
-      const uint32_t free_par = ((gi >> 1) & 1) ^ 1;
-      if ((i & 3) == 0) {
-        at = nat, sc = nsc, full = nfull;
-        find(i + 4);
-        look(i + 8);
-      }
-      // Keys, then values.  Warp x copies the next block's once all three have read this one's.
+        // Keys, then values.  Warp x copies the next block's once all three have read this one's.
 #pragma unroll 1
-      for (int x = 0; x < 2; ++x) {
-        if (gi >= 2 && !(ok = wait_all((x ? VE : KE) + st, free_par))) break;
-        if (x == 0 && w == 0) {
-          // Block i - 4's scales are no longer read: the keys' stage is free, so the scores of
-          // block i - 2 are done, which were issued after every row had finished block i - 3.
-          if (lane >> 3 == (i & 3))
-            s_scale[gi & 3][lane & 7] =
-                make_float2(sc.x, at >= 0 ? (float)((int)(__float_as_uint(sc.y) >> 23 & 0xff) - 127) : 0.f);
+        for (int x = 0; x < 2; ++x) {
+          if (gi >= 2 && !(ok = wait_all((x ? VE : KE) + st, free_par))) break;
+          if (x == 0 && w == 0) {
+            // Block i - 4's scales are no longer read: the keys' stage is free, so the scores of
+            // block i - 2 are done, which were issued after every row had finished block i - 3.
+            if (lane >> 3 == (i & 3))
+              s_scale[gi & 3][lane & 7] =
+                  make_float2(sc.x, at >= 0 ? (float)((int)(__float_as_uint(sc.y) >> 23 & 0xff) - 127) : 0.f);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl->bar[SC + (gi & 3)]);
+          }
+          if (!(ok = wait_all(RF + x, gi & 1))) break;
+          convert(sm + Sm::R + x * Sm::kRaw, sm + (x ? Sm::V : Sm::K) + st * Sm::kTile, i);
           __syncwarp();
-          if (lane == 0) mbar_arrive(&ctl->bar[SC + (gi & 3)]);
-        }
-        if (!(ok = wait_all(RF + x, gi & 1))) break;
-        convert(sm + Sm::R + x * Sm::kRaw, sm + (x ? Sm::V : Sm::K) + st * Sm::kTile, i);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl->bar[(x ? VF : KF) + st]), mbar_arrive(&ctl->bar[RE + x]);
-        if (w == x && i + 1 < nblk) {
-          if (!(ok = wait_all(RE + x, gi & 1))) break;
-          copy(x, i + 1);
-        }
-      }
-      if (!ok) break;
-    }
-    if (!ok) ctl->abort = 1;
-  } else {
-    // ------------------------------------------------------------------ rows
-    const int t = warp >> 2, r = warp * 32 + lane;  // row tile, row of the CTA
-    const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t ts = tl + t * kBlock, to = tl + 256 + t * D;
-    const float rs = s_rs[r];
-    auto sees_from = [&](int64_t p) {
-      const int64_t x = max(s_v.first, a.W > 0 ? p - a.W + 1 : (int64_t)0) - s_v.base;
-      return (int)max((int64_t)0, min(x, (int64_t)0x7fffffff));
-    };
-    const int64_t p = s_v.p0 + (r0 + r) / G;
-    const int lo_r = sees_from(p), hi_r = r < rows ? (int)(p - s_v.base) : -1;
-    // tokens every live row of the tile sees (dead rows may see anything)
-    const int last = min(rows, 128 * t + 128) - 1;
-    const int all_lo = last >= 128 * t ? sees_from(s_v.p0 + (r0 + last) / G) : 0;
-    const int all_hi = last >= 128 * t ? (int)(s_v.p0 + (r0 + 128 * t) / G - s_v.base) : 0x7fffffff;
-    bool ok = true;
-    for (int i = 0; i < nblk; ++i) {
-      const int tok = (b0 + i) * kBlock;
-      const int gi = it + i;  // counts over all pieces
-      if (!(ok = wait_all(SC + (gi & 3), (gi >> 2) & 1) && wait_all(SF + t, gi & 1))) break;
-      tc_fence_after();
-      float2 sc[8];
-#pragma unroll
-      for (int b = 0; b < 8; b += 2) {
-        const float4 x = *reinterpret_cast<const float4*>(&s_scale[gi & 3][b]);
-        sc[b] = make_float2(x.x, x.y), sc[b + 1] = make_float2(x.z, x.w);
-      }
-      bool checked = tok < all_lo || tok + kBlock - 1 > all_hi;
-#pragma unroll
-      for (int b = 0; b < 8; ++b) checked |= sc[b].x == 0.f;
-      float mb[8], mn = m, mon = mo;
-      if (checked) part_maxima<true>(ts, sc, rs, tok, lo_r, hi_r, mb);
-      else part_maxima<false>(ts, sc, rs, tok, lo_r, hi_r, mb);
-#pragma unroll
-      for (int b = 0; b < 8; ++b) mn = fmaxf(mn, mb[b]), mon = fmaxf(mon, mb[b] + sc[b].y);
-      // the sum's scale follows m exactly, the output's only in steps
-      if (mn > m) l *= exp2f(m - mn), m = mn;
-      const bool jump = mon > mo + kLazy;
-      if (__any_sync(0xffffffffu, jump)) {
-        const float f = mon > mo ? exp2f(mo - mon) : 1.f;
-        mo = fmaxf(mo, mon);
-        if (i > 0) {
-          if (!(ok = wait_all(OD + t, (gi - 1) & 1))) break;
-          tc_fence_after();
-#pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
-            uint32_t u[32];
-            tmem_ld32(to + c, u);
-            tmem_ld_wait();
-#pragma unroll
-            for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * f);
-            tmem_st32(to + c, u);
+          if (lane == 0) mbar_arrive(&ctl->bar[(x ? VF : KF) + st]), mbar_arrive(&ctl->bar[RE + x]);
+          if (w == x && i + 1 < nblk) {
+            if (!(ok = wait_all(RE + x, gi & 1))) break;
+            copy(x, i + 1);
           }
-          tmem_st_wait();
         }
+        if (!ok) break;
       }
-      const float ml = m == -INFINITY ? 0.f : m, mol = mo == -INFINITY ? 0.f : mo;
-      bool far = false;
+      if (!ok) ctl->abort = 1;
+    } else {
+      // ------------------------------------------------------------------ rows
+      const int t = warp >> 2, r = warp * 32 + lane;  // row tile, row of the CTA
+      const uint32_t tl = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+      const uint32_t ts = tl + t * kBlock, to = tl + 256 + t * D;
+      const float rs = s_rs[r];
+      auto sees_from = [&](int64_t p) {
+        const int64_t x = max(s_v.first, a.W > 0 ? p - a.W + 1 : (int64_t)0) - s_v.base;
+        return (int)max((int64_t)0, min(x, (int64_t)0x7fffffff));
+      };
+      const int64_t p = s_v.p0 + (r0 + r) / G;
+      const int lo_r = sees_from(p), hi_r = r < rows ? (int)(p - s_v.base) : -1;
+      // tokens every live row of the tile sees (dead rows may see anything)
+      const int last = min(rows, 128 * t + 128) - 1;
+      const int all_lo = last >= 128 * t ? sees_from(s_v.p0 + (r0 + last) / G) : 0;
+      const int all_hi = last >= 128 * t ? (int)(s_v.p0 + (r0 + 128 * t) / G - s_v.base) : 0x7fffffff;
+      bool ok = true;
+      for (int i = 0; i < nblk; ++i) {
+        const int tok = (b0 + i) * kBlock;
+        const int gi = it + i;  // counts over all pieces
+        if (!(ok = wait_all(SC + (gi & 3), (gi >> 2) & 1) && wait_all(SF + t, gi & 1))) break;
+        tc_fence_after();
+        float2 sc[8];
 #pragma unroll
-      for (int b = 0; b < 8; ++b) far |= mol - sc[b].y - ml > kFar;
-      if (__any_sync(0xffffffffu, checked || far)) l += weights<true>(ts, sc, rs, tok, lo_r, hi_r, ml, mol);
-      else l += weights<false>(ts, sc, rs, tok, lo_r, hi_r, ml, mol);
-      tmem_st_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl->bar[PF + t]);
+        for (int b = 0; b < 8; b += 2) {
+          const float4 x = *reinterpret_cast<const float4*>(&s_scale[gi & 3][b]);
+          sc[b] = make_float2(x.x, x.y), sc[b + 1] = make_float2(x.z, x.w);
+        }
+        bool checked = tok < all_lo || tok + kBlock - 1 > all_hi;
+#pragma unroll
+        for (int b = 0; b < 8; ++b) checked |= sc[b].x == 0.f;
+        float mb[8], mn = m, mon = mo;
+        if (checked) part_maxima<true>(ts, sc, rs, tok, lo_r, hi_r, mb);
+        else part_maxima<false>(ts, sc, rs, tok, lo_r, hi_r, mb);
+#pragma unroll
+        for (int b = 0; b < 8; ++b) mn = fmaxf(mn, mb[b]), mon = fmaxf(mon, mb[b] + sc[b].y);
+        // the sum's scale follows m exactly, the output's only in steps
+        if (mn > m) l *= exp2f(m - mn), m = mn;
+        const bool jump = mon > mo + kLazy;
+        if (__any_sync(0xffffffffu, jump)) {
+          const float f = mon > mo ? exp2f(mo - mon) : 1.f;
+          mo = fmaxf(mo, mon);
+          if (i > 0) {
+            if (!(ok = wait_all(OD + t, (gi - 1) & 1))) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+              uint32_t u[32];
+              tmem_ld32(to + c, u);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(__uint_as_float(u[e]) * f);
+              tmem_st32(to + c, u);
+            }
+            tmem_st_wait();
+          }
+        }
+        const float ml = m == -INFINITY ? 0.f : m, mol = mo == -INFINITY ? 0.f : mo;
+        bool far = false;
+#pragma unroll
+        for (int b = 0; b < 8; ++b) far |= mol - sc[b].y - ml > kFar;
+        if (__any_sync(0xffffffffu, checked || far)) l += weights<true>(ts, sc, rs, tok, lo_r, hi_r, ml, mol);
+        else l += weights<false>(ts, sc, rs, tok, lo_r, hi_r, ml, mol);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->bar[PF + t]);
+      }
+      if (ok && (ok = wait_all(OD + t, (it + nblk - 1) & 1))) tc_fence_after();
+      if (!ok) ctl->abort = 1;
+      done_ok = ok;
     }
-    if (ok && (ok = wait_all(OD + t, (it + nblk - 1) & 1))) tc_fence_after();
-    if (!ok) ctl->abort = 1;
-    done_ok = ok;
-  }
 
-  // ---- output
-  const bool alone = s_p.ua == 0 && s_p.ub == s_v.units;
-  float* part = reinterpret_cast<float*>(a.ws + (((size_t)M2 * Hk * sizeof(unsigned) + 255) & ~(size_t)255));
-  auto slot = [&](int c) { return part + partial_at<D>(c, c == s_p.c0); };
-  if (warp < 8 && __all_sync(0xffffffffu, done_ok && !*(volatile int*)&ctl->abort)) {
-    const uint32_t to = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 256 + (warp >> 2) * D;
-    if (alone) write_rows<D>(a, s_p, to, m, mo, l);
-    else write_partial<D>(slot(blockIdx.x), to, m, mo, l);
-  }
-  it += nblk;
-  tc_fence_before();
-  cta_sync();
-  tc_fence_after();
-  if (*(volatile int*)&ctl->abort) break;
-  if (!alone) {
-    __threadfence();
-    __syncthreads();
-    unsigned* counter = reinterpret_cast<unsigned*>(a.ws) + s_p.seg;
-    const int c0 = s_p.c0, c1 = s_p.c1;
-    if (tid == 0) s_last = atomicAdd(counter, 1u) == (unsigned)(c1 - c0);
-    __syncthreads();
-    if (s_last) {
-      __threadfence();
-      join_rows<D>(a, s_p, part, reinterpret_cast<float2*>(sm + Sm::K), reinterpret_cast<float*>(sm + Sm::V),
-                   reinterpret_cast<float*>(sm + Sm::Q));
-      if (tid == 0) *counter = 0u;
+    // ---- output
+    const bool alone = s_p.ua == 0 && s_p.ub == s_v.units;
+    float* part = reinterpret_cast<float*>(a.ws + (((size_t)M2 * Hk * sizeof(unsigned) + 255) & ~(size_t)255));
+    auto slot = [&](int c) { return part + partial_at<D>(c, c == s_p.c0); };
+    if (warp < 8 && __all_sync(0xffffffffu, done_ok && !*(volatile int*)&ctl->abort)) {
+      const uint32_t to = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 256 + (warp >> 2) * D;
+      if (alone) write_rows<D>(a, s_p, to, m, mo, l);
+      else write_partial<D>(slot(blockIdx.x), to, m, mo, l);
     }
-  }
-  cta_sync();  // before s_p and the queries' tiles are written again
+    it += nblk;
+    tc_fence_before();
+    cta_sync();
+    tc_fence_after();
+    if (*(volatile int*)&ctl->abort) break;
+    if (!alone) {
+      __threadfence();
+      __syncthreads();
+      unsigned* counter = reinterpret_cast<unsigned*>(a.ws) + s_p.seg;
+      const int c0 = s_p.c0, c1 = s_p.c1;
+      if (tid == 0) s_last = atomicAdd(counter, 1u) == (unsigned)(c1 - c0);
+      __syncthreads();
+      if (s_last) {
+        __threadfence();
+        join_rows<D>(a, s_p, part, reinterpret_cast<float2*>(sm + Sm::K), reinterpret_cast<float*>(sm + Sm::V),
+                     reinterpret_cast<float*>(sm + Sm::Q));
+        if (tid == 0) *counter = 0u;
+      }
+    }
+    cta_sync();  // before s_p and the queries' tiles are written again
   }
   if (warp == kMmaWarp) {
     if (lane == 0) {

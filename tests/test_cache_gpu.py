@@ -414,3 +414,75 @@ def test_no_tokens_is_a_no_op():
     assert lz.lizard_last_launch_count() == 0
     lz.lizard_cache_write(dev.h, lz.lizard_cache_io(0, lz.LIZARD_F32), e, e, None, ints([0], 8), None, dev.ws)
     assert lz.lizard_last_launch_count() == 0
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "i8"])
+def test_pages_beyond_32_bits(fmt):
+    """The same tokens in pages at the start of a small pool and at the end of one whose codes
+    pass 2^32 bytes: writes, reads and both attention paths give the same bits."""
+    import torch
+    N, H, Hk, P, d, S = 2, 8, 2, 128, 128, 3
+    big = 2 ** 32 // (Hk * P * d) + N * S
+    rng = np.random.default_rng(12)
+    rows = [dev_rows(rng.standard_normal((N, Hk, 300, d)), "bf16")[0] for _ in "kv"]
+    pos = torch.tensor([0, 50], device="cuda")
+    outs = []
+    for pages in (N * S, big):
+        codes = [torch.empty(pages, Hk, P, d, dtype=torch.uint8, device="cuda") for _ in "kv"]
+        scales = [torch.empty(pages, Hk, device="cuda") for _ in "kv"]
+        table = (pages - N * S + torch.randperm(N * S, generator=torch.Generator().manual_seed(1)).to(torch.int32))
+        table = table.view(N, S).cuda()
+        cache = lz.lizard_cache(*codes, *scales, table, FMT[fmt])
+        ws = torch.zeros(lz.lizard_cache_workspace_bytes(), dtype=torch.uint8, device="cuda")
+        lz.lizard_cache_write(cache, lz.lizard_cache_io(300, lz.LIZARD_BF16), *rows, None, pos, None, ws)
+        back = [torch.empty(N, Hk, 300, d, dtype=torch.bfloat16, device="cuda") for _ in "kv"]
+        lz.lizard_cache_read(cache, lz.lizard_cache_io(300, lz.LIZARD_BF16), pos, None, *back, ws)
+        assert lz.lizard_check_device_errors(ws) == 0
+        got = back
+        for T in (1, 40):
+            q = dev_rows(np.random.default_rng(T).standard_normal((N, H, T, d)), "bf16")[0]
+            first, at = pos, pos + 300 - T
+            dims = lz.lizard_cache_attn_dims(H, T, 0, 0, lz.LIZARD_BF16, 0.0, 1.0)
+            aws = torch.zeros(lz.lizard_cache_attn_workspace_bytes(cache, dims), dtype=torch.uint8, device="cuda")
+            y = torch.empty_like(q)
+            lz.lizard_cache_attn(cache, dims, q, None, at, None, first, None, None, None, y, aws)
+            assert lz.lizard_check_device_errors(aws) == 0
+            got = got + [y]
+        outs.append(got)
+        del codes, cache
+    for a, b in zip(*outs):
+        assert torch.isfinite(a.float()).all()
+        assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("T,G", [(1, 4), (80, 1)])
+def test_attention_of_a_long_context(T, G):
+    """40000 tokens (many parts to be joined), against fp64 on the same cache values."""
+    import torch
+    Hk, P, d, L = 2, 64, 128, 40000
+    H, S = Hk * G, (L + T) // P + 1
+    g = torch.Generator(device="cuda").manual_seed(5)
+    codes = [torch.empty(S, Hk, P, d, dtype=torch.uint8, device="cuda") for _ in "kv"]
+    scales = [torch.empty(S, Hk, device="cuda") for _ in "kv"]
+    cache = lz.lizard_cache(*codes, *scales, torch.randperm(S, generator=g, device="cuda").to(torch.int32)[None], 0)
+    ws = torch.zeros(lz.lizard_cache_workspace_bytes(), dtype=torch.uint8, device="cuda")
+    rows = [torch.randn(1, Hk, L + T, d, generator=g, device="cuda") for _ in "kv"]
+    zero = torch.zeros(1, dtype=torch.int64, device="cuda")
+    io = lz.lizard_cache_io(L + T, lz.LIZARD_F32)
+    lz.lizard_cache_write(cache, io, *rows, None, zero, None, ws)
+    lz.lizard_cache_read(cache, io, zero, None, *rows, ws)
+    for dtype, dt in (("f32", torch.float32), ("bf16", torch.bfloat16)):
+        q = (1.5 * torch.randn(1, H, T, d, generator=g, device="cuda")).to(dt)
+        dims = lz.lizard_cache_attn_dims(H, T, 0, 0, DT[dtype], 0.0, 1.0)
+        aws = torch.zeros(lz.lizard_cache_attn_workspace_bytes(cache, dims), dtype=torch.uint8, device="cuda")
+        y = torch.empty_like(q)
+        lz.lizard_cache_attn(cache, dims, q, None, zero + L, None, None, None, None, None, y, aws)
+        assert lz.lizard_check_device_errors(aws) == 0
+        k, v = (x[0].double().repeat_interleave(G, 0) for x in rows)
+        z = q[0].double() @ k.transpose(1, 2) / d ** 0.5
+        hide = torch.arange(L + T, device="cuda") > L + torch.arange(T, device="cuda")[:, None]
+        p = torch.softmax(z.masked_fill(hide, -float("inf")), -1)
+        want, A = p @ v, p @ v.abs()
+        Z = (q[0].double().abs() @ k.abs().transpose(1, 2)).amax(-1, keepdim=True) / d ** 0.5
+        bound = co.attend_bound(want.cpu().numpy(), A.cpu().numpy(), Z.cpu().numpy(), dtype, d, L + T)
+        assert ((y[0].double() - want).abs().cpu().numpy() <= bound).all()
