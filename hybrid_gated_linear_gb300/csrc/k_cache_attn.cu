@@ -21,7 +21,7 @@
 //
 // Measured, H = 32, Hk = 8, D = 128, one new token, e4m3 (share of the measured copy rate):
 //   64 sequences of 8192 tokens 188 us (84%), of 128 to 8192 111 us (72%); one of 131072
-//   tokens 56 us (70%); 64 x 32 heads, windows of 1024, bytes 127 us (61%); one sequence of
+//   tokens 56 us (70%); 64 x 32 heads, windows of 1024, bytes 116 us (67%); one sequence of
 //   500 tokens 13 us.
 // The loop runs at 6.7 TB/s; the rest is the start (positions, pages, first copies: about 6 us)
 // and the end of the slowest warp and the joins after it (10 to 20 us).
@@ -180,6 +180,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG, Solo>::kPerSm)
   __shared__ RowStat s_st[8][16];
   __shared__ UnitMeta s_meta[NG][2][kBatch];  // of each group, two batches
   __shared__ int64_t s_sum[8];
+  __shared__ int s_most[8];
   __shared__ Piece s_pieces[kTeams];
   __shared__ int s_abort, s_last;
 
@@ -209,33 +210,59 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG, Solo>::kPerSm)
   }
   pdl_wait();
 
-  // How the units are shared out.  With few segments for the teams there are, every segment is
-  // cut into ceil(units / U) equal pieces, U such that the pieces are at most as many as the
-  // teams; else the list of all units (sequence-major, then head, then token, kSegCost empty
-  // entries in front of each segment) is cut into equal shares, whatever segments they cross.
-  const int M2 = a.c.N * RB;
+  // How the units are shared out.  Either every segment is cut into ceil(units / U) equal pieces,
+  // U such that the pieces are at most as many as the teams; or the list of all units
+  // (sequence-major, then head, then token, kSegCost empty entries in front of each segment) is
+  // cut into equal shares, whatever segments they cross.  A team then has one piece, or often
+  // two with a start and a join more: pieces are taken while the longest is not longer than a
+  // share by more than those two cost.  (64 x 32 heads, windows of 1024: 127 us in shares, 116 in
+  // pieces; 96 segments of drafted tokens 33 and 27.)
+  const int M2 = a.c.N * RB, segs = M2 * Hk;
   const int workers = gridDim.x * kTeams, worker = blockIdx.x * kTeams + team;
-  const bool pieces = (int64_t)M2 * Hk * 8 <= workers;
-  int64_t U = 0, share = 1, f1, total;
+  bool pieces = false;
+  int64_t U = 1, share = 1, f1, total;
   {
     const int mine = tid < M2 ? segment_of(a, tid, RB, RR, G).units : 0;
     int64_t c = mine;
-    for (int m = tid + kThreads; m < M2; m += kThreads) c += segment_of(a, m, RB, RR, G).units;
+    int most = mine;
+    for (int m = tid + kThreads; m < M2; m += kThreads) {
+      const int u = segment_of(a, m, RB, RR, G).units;
+      c += u, most = max(most, u);
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
-    if (lane == 0) s_sum[warp] = c;
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (lane == 0) s_sum[warp] = c, s_most[warp] = most;
     if (tid < kTeams) s_pieces[tid].m = -1;
     __syncthreads();
     int64_t units = 0;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) units += s_sum[w];
+    for (int w = 0; w < 8; ++w) units += s_sum[w], most = max(most, s_most[w]);
     units *= Hk;
-    if (pieces) {
-      U = max((units + workers - M2 * Hk - 1) / (workers - M2 * Hk), (int64_t)Sh::kMinUnits);
-    } else {
-      total = units + (int64_t)M2 * Hk * kSegCost;
-      share = max((total + workers - 1) / workers, (int64_t)(Sh::kMinUnits + kSegCost));
+    total = units + (int64_t)segs * kSegCost;
+    share = max((total + workers - 1) / workers, (int64_t)(Sh::kMinUnits + kSegCost));
+    if ((int64_t)segs * 8 <= workers) {  // the pieces' rounding hardly counts
+      U = max((units + workers - segs - 1) / (workers - segs), (int64_t)Sh::kMinUnits);
+      pieces = true;
+    } else if (segs <= workers) {
+      // pieces of U: at most units / U + segs of them, or segs where U is the longest segment
+      U = segs < workers ? min((units + workers - segs - 1) / (workers - segs), (int64_t)most) : most;
+      U = max(U, (int64_t)Sh::kMinUnits);
+      int longest = 0;
+      for (int m = tid; m < M2; m += kThreads) {
+        const int u = m == tid ? mine : segment_of(a, m, RB, RR, G).units;
+        const int k = (int)((u + U - 1) / U);
+        longest = max(longest, (u + k - 1) / k);
+      }
+      longest = __reduce_max_sync(0xffffffffu, longest);
+      __syncthreads();
+      if (lane == 0) s_most[warp] = longest;
+      __syncthreads();
+#pragma unroll
+      for (int w = 0; w < 8; ++w) longest = max(longest, s_most[w]);
+      pieces = longest <= share + 2 * kSegCost;
     }
+    if (pieces) share = 1;
     const int64_t cta_f = (int64_t)blockIdx.x * kTeams * share;  // where the first team starts
     int64_t before = 0;
     for (int m0 = 0; m0 < M2; m0 += kThreads) {

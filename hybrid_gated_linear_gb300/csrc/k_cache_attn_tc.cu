@@ -45,7 +45,7 @@ constexpr int kThreads = 32 * (kMmaWarp + 1);
 constexpr int kMaxM = 16;
 // Starting rows costs a CTA about as much as kCost blocks; pieces shorter than kMinBlocks are
 // not worth joining.
-constexpr int kCost = 2, kMinBlocks = 4;
+constexpr int kCost = 6, kMinBlocks = 6;
 constexpr float kLazy = 8.f;     // P <= 2^8 fits binary16 with room for its sums
 constexpr float kFar = 60.f;      // see weights()
 constexpr float kLog2e = 1.4426950408889634f;
@@ -626,28 +626,61 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     fence_mbar_init();
   }
   pdl_wait();
-  // this CTA's share [f, f1) of the list: kCost empty entries, then the blocks, of each view
-  // and head (sequence-major, then rows, then head)
-  const int M2 = a.c.N * tiles;
-  int64_t share, f1;
+  // How the blocks are shared out.  Either every view and head is cut into ceil(units / U) equal
+  // pieces, U such that the pieces are at most as many as the CTAs; or the list of all blocks
+  // (sequence-major, then rows, then head, kCost empty entries in front of each) is cut into equal
+  // shares.  A CTA then has one piece, or several with a start and a join each: pieces are taken
+  // while the longest is not longer than a share by more than those cost.
+  const int M2 = a.c.N * tiles, segs = M2 * Hk, workers = gridDim.x;
+  bool pieces = false;
+  int64_t U = 1, share, f1;
   {
-    const int mine = tid < M2 ? view_of(a, tid, tiles, G).units + kCost : 0;
+    __shared__ int s_most[kThreads / 32];
+    const int mine = tid < M2 ? view_of(a, tid, tiles, G).units : 0;
     int64_t c = mine;
-    for (int m = tid + kThreads; m < M2; m += kThreads) c += view_of(a, m, tiles, G).units + kCost;
+    int most = mine;
+    for (int m = tid + kThreads; m < M2; m += kThreads) {
+      const int u = view_of(a, m, tiles, G).units;
+      c += u, most = max(most, u);
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
-    if (lane == 0) s_sum[warp] = c;
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (lane == 0) s_sum[warp] = c, s_most[warp] = most;
     __syncthreads();
-    int64_t total = 0;
-    for (int w = 0; w < kThreads / 32; ++w) total += s_sum[w];
-    total *= Hk;
-    share = max((total + gridDim.x - 1) / gridDim.x, (int64_t)(kMinBlocks + kCost));
+    int64_t units = 0;
+    for (int w = 0; w < kThreads / 32; ++w) units += s_sum[w], most = max(most, s_most[w]);
+    units *= Hk;
+    int64_t total = units + (int64_t)segs * kCost;
+    share = max((total + workers - 1) / workers, (int64_t)(kMinBlocks + kCost));
+    if (segs <= workers) {
+      U = segs < workers ? min((units + workers - segs - 1) / (workers - segs), (int64_t)most) : most;
+      U = max(U, (int64_t)kMinBlocks);
+      int longest = 0;
+      for (int m = tid; m < M2; m += kThreads) {
+        const int u = m == tid ? mine : view_of(a, m, tiles, G).units;
+        const int k = (int)((u + U - 1) / U);
+        longest = max(longest, (u + k - 1) / k);
+      }
+      longest = __reduce_max_sync(0xffffffffu, longest);
+      __syncthreads();
+      if (lane == 0) s_most[warp] = longest;
+      __syncthreads();
+      for (int w = 0; w < kThreads / 32; ++w) longest = max(longest, s_most[w]);
+      pieces = longest <= share + 2 * kCost;
+    }
+    if (pieces) share = 1, total = workers;
     const int64_t f = blockIdx.x * share;
     f1 = min(total, f + share);
+    if (tid == 0) s_p.f = f1;  // nothing to do, unless found below
     int64_t before = 0;
     for (int m0 = 0; f < total && m0 < M2; m0 += kThreads) {
       const int m = m0 + tid;
-      const int64_t u = (int64_t)Hk * (m0 == 0 ? mine : m < M2 ? view_of(a, m, tiles, G).units + kCost : 0);
+      int64_t u = 0;
+      if (m < M2) {
+        const int n_u = m0 == 0 ? mine : view_of(a, m, tiles, G).units;
+        u = Hk * (pieces ? (n_u + U - 1) / U : (int64_t)n_u + kCost);
+      }
       c = u;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -663,7 +696,6 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       for (int w = 0; w < kThreads / 32; ++w) before += s_sum[w];
       if (f < before) break;
     }
-    if (f >= total && tid == 0) s_p.f = f1;
   }
   tc_fence_before();
   cta_sync();
@@ -683,17 +715,27 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
       if (p.f < f1) {
         p.v = view_of(a, p.m, tiles, G);
         p.n = p.m / tiles;
-        const int entries = p.v.units + kCost;
-        p.hk = (int)((p.f - p.seg0) / entries);
-        const int64_t next = p.seg0 + (int64_t)(p.hk + 1) * entries, head0 = next - p.v.units;
-        p.ua = (int)max((int64_t)0, p.f - head0);
-        // 0: the share ends before this head's first block
-        p.ub = (int)max((int64_t)0, min((int64_t)p.v.units, f1 - head0));
+        if (pieces) {
+          const int k = (int)((p.v.units + U - 1) / U), i = (int)(p.f - p.seg0);
+          p.hk = i / k;
+          p.ua = (int)((int64_t)p.v.units * (i - p.hk * k) / k);
+          p.ub = (int)((int64_t)p.v.units * (i - p.hk * k + 1) / k);
+          p.c0 = (int)p.seg0 + p.hk * k;
+          p.c1 = p.c0 + k - 1;
+          p.f = f1;
+        } else {
+          const int entries = p.v.units + kCost;
+          p.hk = (int)((p.f - p.seg0) / entries);
+          const int64_t next = p.seg0 + (int64_t)(p.hk + 1) * entries, head0 = next - p.v.units;
+          p.ua = (int)max((int64_t)0, p.f - head0);
+          // 0: the share ends before this head's first block
+          p.ub = (int)max((int64_t)0, min((int64_t)p.v.units, f1 - head0));
+          p.c0 = (int)(head0 / share);
+          p.c1 = (int)((next - 1) / share);
+          p.f = next;
+        }
         p.seg = p.m * Hk + p.hk;
-        p.c0 = (int)(head0 / share);
-        p.c1 = (int)((next - 1) / share);
-        p.f = next;
-        if (p.hk == Hk - 1) p.seg0 = next, ++p.m;
+        if (p.hk == Hk - 1) p.seg0 = p.f, ++p.m;
       }
     }
     cta_sync();
