@@ -175,6 +175,8 @@ def build(force: bool = False) -> str:
 def library():
     """The loaded ctypes library; raises if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -252,13 +254,17 @@ def _stream(stream):
     return ctypes.c_void_p(int(handle))
 
 
+_dtype_codes: dict = {}
+
+
 def _dtype_code(t) -> int:
-    import torch
-    if t.dtype == torch.float32:
-        return LIZARD_F32
-    if t.dtype == torch.bfloat16:
-        return LIZARD_BF16
-    raise TypeError(f"unsupported dtype {t.dtype}")
+    if not _dtype_codes:
+        import torch
+        _dtype_codes.update({torch.float32: LIZARD_F32, torch.bfloat16: LIZARD_BF16})
+    code = _dtype_codes.get(t.dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {t.dtype}")
+    return code
 
 
 def _check(status: int, what: str):
@@ -511,8 +517,8 @@ def _ints(t, shape, size: int):
     """Pointer of a contiguous device tensor of integers of `size` bytes (None -> NULL)."""
     if t is None:
         return None
-    if (t.shape != shape or t.element_size() != size or t.is_floating_point() or not t.is_cuda
-            or not t.is_contiguous()):
+    if (t.shape != shape or not t.is_cuda or not t.is_contiguous() or t.element_size() != size
+            or t.is_floating_point()):
         raise ValueError(f"expected a contiguous int{8 * size} device tensor of shape {shape}, got "
                          f"{tuple(t.shape)} {t.dtype} on {t.device}")
     return t.data_ptr()

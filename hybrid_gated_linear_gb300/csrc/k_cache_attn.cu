@@ -983,7 +983,8 @@ cudaError_t launch_split(const CacheAttn& a, cudaStream_t s, int* launches) {
   using Sh = Shape<T, D, F, RG, Solo>;
   const int rows = a.H / a.c.Hk * a.T, RB = (rows + Sh::RR - 1) / Sh::RR;
   auto* kernel = split_kernel<T, D, F, RG, Solo>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kSmem);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(kernel, Sh::kSmem, done);
   if (e != cudaSuccess) return e;
   trace_begin("cache_attn", s);
   e = launch_pdl(kernel, dim3(std::min(ctas_per_wave(Sh::kPerSm), kMaxCtas)), dim3(kThreads), Sh::kSmem, s, a, RB,

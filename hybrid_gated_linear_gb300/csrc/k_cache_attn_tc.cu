@@ -1054,7 +1054,8 @@ template <int D, int F>
 cudaError_t launch(const CacheAttn& a, cudaStream_t s, int* launches) {
   const int tiles = (a.H / a.c.Hk * a.T + kRows - 1) / kRows;
   constexpr int smem = Smem<D>::kBytes + 1024;
-  cudaError_t e = cudaFuncSetAttribute(prompt_kernel<D, F>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = allow_smem(prompt_kernel<D, F>, smem, done);
   if (e != cudaSuccess) return e;
   trace_begin("cache_attn_prompt", s);
   e = launch_pdl(prompt_kernel<D, F>, dim3(std::min(ctas_per_wave(1), kMaxCtas)), dim3(kThreads), smem, s, a, tiles);
