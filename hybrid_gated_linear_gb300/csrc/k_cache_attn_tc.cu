@@ -21,8 +21,8 @@
 // all (sequence, rows, head), whatever their lengths; where a share ends inside one, its parts
 // are joined by the last CTA to finish (fixed order: results do not depend on timing).
 //
-// Measured, H = 32, Hk = 8, D = 128, e4m3: two sequences, 2048 new tokens at 14336: 1.10 ms,
-// 934 TFLOP/s (47% of the measured bf16 burst; bytes 1.28 ms, their conversion takes twice the
+// Measured, H = 32, Hk = 8, D = 128, e4m3: two sequences, 2048 new tokens at 14336: 1.07 ms,
+// 960 TFLOP/s (49% of the measured bf16 burst; bytes 1.28 ms, their conversion takes twice the
 // operations).  With the row warps' work left out 1.01, with the conversions left out 0.87, with
 // both 0.64 ms: the roles contend for issue slots and shared memory, which the operands alone
 // keep three quarters busy.  Staging the queries and joining parts cost about 80 us of it.
@@ -1066,9 +1066,10 @@ cudaError_t launch(const CacheAttn& a, cudaStream_t s, int* launches) {
 
 }  // namespace
 
-// Us for H = 32, Hk = 8, d = 128 here and in k_cache_attn.cu: 64 rows 130 against 121 (eight
-// sequences of 8192 tokens), 128 rows 137 against 221 there and 151 against 268 (one of 65536),
-// but 73 against 55 at 1000 tokens, where neither fills the GPU.
+// Us for H = 32, Hk = 8, d = 128, here against k_cache_attn.cu with as many rows: 128 rows 137
+// against 272 (eight sequences of 8192 tokens), 145 against 285 (one of 65536), 53 against 58 (one
+// of 1000), 34 against 63 (eight of 200); 64 rows 134 against 130, 136 against 143, 46 against 34,
+// 33 against 29; 32 rows 130 against 72 (eight of 8192).
 bool cache_attn_tc_used(int H, int Hk, int T, lizard_dtype dt) { return dt == LIZARD_BF16 && H / Hk * T > 64; }
 
 size_t cache_attn_tc_workspace(int N, int Hk, int H, int T, int d) {

@@ -15,52 +15,38 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// VP consecutive elements (16 bytes when VP > 1).
+// VP consecutive elements, aligned to their size together, in one access of up to 16 bytes.
+template <int BYTES> struct Word;
+template <> struct Word<2> { typedef unsigned short type; };
+template <> struct Word<4> { typedef uint32_t type; };
+template <> struct Word<8> { typedef uint2 type; };
+template <> struct Word<16> { typedef uint4 type; };
+template <typename T, int VP>
+union Packed {
+  typename Word<VP * sizeof(T)>::type word;
+  T v[VP];
+  __device__ __forceinline__ Packed() {}
+};
 template <typename T, int VP>
 __device__ __forceinline__ void load_v(const T* p, float (&x)[VP]) {
-  if (VP == 1) {
-    x[0] = ld_f(p);
-  } else {
+  Packed<T, VP> u;
+  u.word = *reinterpret_cast<const decltype(u.word)*>(p);
 #pragma unroll
-    for (int i = 0; i < VP; i += 4) {
-      const float4 v = ld4(p + i);
-      x[i] = v.x, x[i + 1] = v.y, x[i + 2] = v.z, x[i + 3] = v.w;
-    }
-  }
-}
-template <>
-__device__ __forceinline__ void load_v<bf16, 8>(const bf16* p, float (&x)[8]) {
-  const uint4 u = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = __uint_as_float(w[i] << 16);
-    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
+  for (int i = 0; i < VP; ++i) x[i] = ld_f(&u.v[i]);
 }
 template <typename T, int VP>
 __device__ __forceinline__ void store_v(T* p, const float (&x)[VP]) {
-  if (VP == 1) {
-    *p = cvt_out<T>(x[0]);
-  } else {
+  Packed<T, VP> u;
 #pragma unroll
-    for (int i = 0; i < VP; i += 4) st4(p + i, make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]));
-  }
-}
-template <>
-__device__ __forceinline__ void store_v<bf16, 8>(bf16* p, const float (&x)[8]) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-    w[i] = *reinterpret_cast<const uint32_t*>(&b);
-  }
-  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  for (int i = 0; i < VP; ++i) u.v[i] = cvt_out<T>(x[i]);
+  *reinterpret_cast<decltype(u.word)*>(p) = u.word;
 }
 
-// One thread per (token, unit of 2 VP channels, group of `hpt` heads).  Units below
-// rot / (2 VP) are rotated (VP pairs); the others are copied.  VP = 16 bytes' worth of
-// elements where both halves of a unit are aligned, else 1.
+// One thread per (token, unit of 2 VP channels, group of `hpt` heads).  The first units hold VP
+// pairs each and are rotated (neighbours that are pairs may end inside a unit); the others are
+// copied.  VP = 16 bytes' worth of elements, fewer where the halves' distance rot / 2 is not a
+// multiple of that (11 x 752 tokens x 26 heads of 64, rot = 56, bf16: 31 us with single elements,
+// 12 with these; an odd number of pairs in halves is left with those).
 template <typename T, int VP>
 __global__ void __launch_bounds__(kThreads) rope_kernel(RopeCall a, int units, int hpt,
                                                         int groups) {
@@ -73,7 +59,8 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(RopeCall a, int units, i
   const int64_t nt = r % ((int64_t)a.N * a.T);
   const int g = (int)(r / ((int64_t)a.N * a.T));
   const int n = (int)(nt / a.T), t = (int)(nt % a.T);
-  const bool turned = u < a.rope.rot / (2 * VP);
+  const int pairs = a.rope.rot / 2;
+  const bool turned = u * VP < pairs;
   const bool half = a.rope.layout == LIZARD_ROPE_HALF;
   // channels of the unit's two vectors
   const int c0 = turned && half ? u * VP : u * 2 * VP;
@@ -83,7 +70,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(RopeCall a, int units, i
     const int64_t p = a.positions ? a.positions[nt] : t;
 #pragma unroll
     for (int i = 0; i < VP; ++i) {
-      rope_angle(a.rope.turns[u * VP + i], p, a.rope.factor, co[i], si[i]);
+      rope_angle(a.rope.turns[min(u * VP + i, pairs - 1)], p, a.rope.factor, co[i], si[i]);
       si[i] *= a.sign;
     }
   }
@@ -106,19 +93,15 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(RopeCall a, int units, i
         v[i] = p * co[i] - s * si[i];
         w[i] = s * co[i] + p * si[i];
       }
-    } else if (turned) {
-      // neighbours are pairs: pairs 0..VP/2-1 lie in v, the others in w
+    } else if (VP > 1 && turned) {
+      // neighbours are pairs (VP > 1 always): pairs 0..VP/2-1 lie in v, the others in w
 #pragma unroll
       for (int i = 0; i < VP; ++i) {
-        if (VP == 1) {
-          const float p = v[0], s = w[0];
-          v[0] = p * co[0] - s * si[0];
-          w[0] = s * co[0] + p * si[0];
-        } else {
-          float* e = i < VP / 2 ? &v[2 * i] : &w[2 * i - VP];
-          const float p = e[0], s = e[VP > 1 ? 1 : 0];
+        float* e = i < VP / 2 ? &v[2 * i] : &w[(2 * i - VP) & (VP - 1)];
+        const float p = e[0], s = e[VP > 1];
+        if (u * VP + i < pairs) {
           e[0] = p * co[i] - s * si[i];
-          e[VP > 1 ? 1 : 0] = s * co[i] + p * si[i];
+          e[VP > 1] = s * co[i] + p * si[i];
         }
       }
     }
@@ -148,8 +131,10 @@ cudaError_t launch(const RopeCall& a, cudaStream_t s, int* launches) {
 template <typename T>
 cudaError_t launch_typed(const RopeCall& a, cudaStream_t s, int* launches) {
   constexpr int V = 16 / sizeof(T);
-  return a.rope.rot % (2 * V) == 0 && a.d % (2 * V) == 0 ? launch<T, V>(a, s, launches)
-                                                         : launch<T, 1>(a, s, launches);
+  const int pairs = a.rope.layout == LIZARD_ROPE_HALF ? a.rope.rot / 2 : V;
+  if (pairs % V == 0 && a.d % (2 * V) == 0) return launch<T, V>(a, s, launches);
+  if (sizeof(T) == 2 && pairs % 4 == 0) return launch<T, 4>(a, s, launches);
+  return pairs % 2 == 0 ? launch<T, 2>(a, s, launches) : launch<T, 1>(a, s, launches);
 }
 
 }  // namespace
