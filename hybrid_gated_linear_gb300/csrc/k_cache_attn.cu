@@ -20,7 +20,7 @@
 // would be an eighth full, and the tensor time is a third of the copy time.
 //
 // Measured, H = 32, Hk = 8, D = 128, one new token, e4m3 (share of the measured copy rate):
-//   64 sequences of 8192 tokens 188 us (84%), of 128 to 8192 111 us (72%); one of 131072
+//   64 sequences of 8192 tokens 184 us (86%), of 128 to 8192 106 us (76%); one of 131072
 //   tokens 56 us (70%); 64 x 32 heads, windows of 1024, bytes 116 us (67%); one sequence of
 //   500 tokens 13 us.
 // The loop runs at 6.7 TB/s; the rest is the start (positions, pages, first copies: about 6 us)
@@ -161,9 +161,8 @@ struct Shape {
       kSmem + NT * RR * (kMaxM + 1) * 4 + NG * 2 * kBatch * (int)sizeof(UnitMeta) + 2560 <= 113 * 1024 ? 2 : 1;
   // Starting a segment costs a team about as much as this many units: the list of work holds
   // that many empty entries in front of every segment, so that teams with many short segments
-  // get fewer units.  (8 and 20 instead: 64 uneven sequences 111 -> 106 us, 16 of them 67 -> 61,
-  // but windows 127 -> 136 and drafted tokens 33 -> 36.)
-  static constexpr int kSegCost = Solo ? 3 : 12;
+  // get fewer units.  (3 and 12 instead: 64 uneven sequences 106 -> 110 us, 16 of them 62 -> 66.)
+  static constexpr int kSegCost = Solo ? 8 : 20;
   static constexpr int kMinUnits = 4 * TG;  // of a piece, where a segment has them
 };
 
@@ -215,7 +214,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG, Solo>::kPerSm)
   // (sequence-major, then head, then token, kSegCost empty entries in front of each segment) is
   // cut into equal shares, whatever segments they cross.  A team then has one piece, or often
   // two with a start and a join more: pieces are taken while the longest is not longer than a
-  // share by more than those two cost.  (64 x 32 heads, windows of 1024: 127 us in shares, 116 in
+  // share by more than half of that cost.  (64 x 32 heads, windows of 1024: 127 us in shares, 116 in
   // pieces; 96 segments of drafted tokens 33 and 27.)
   const int M2 = a.c.N * RB, segs = M2 * Hk;
   const int workers = gridDim.x * kTeams, worker = blockIdx.x * kTeams + team;
@@ -260,7 +259,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG, Solo>::kPerSm)
       __syncthreads();
 #pragma unroll
       for (int w = 0; w < 8; ++w) longest = max(longest, s_most[w]);
-      pieces = longest <= share + 2 * kSegCost;
+      pieces = longest <= share + kSegCost / 2;
     }
     if (pieces) share = 1;
     const int64_t cta_f = (int64_t)blockIdx.x * kTeams * share;  // where the first team starts
