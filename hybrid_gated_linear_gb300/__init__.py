@@ -528,6 +528,22 @@ def _ref(x):
     return None if x is None else ctypes.byref(x)
 
 
+def _held(x):
+    """A handle (None -> NULL) whose tensors are on a device: a host pointer would fault."""
+    if x is None:
+        return None
+    keep = x._keep
+    if not (keep[0] if isinstance(keep, tuple) else keep).is_cuda:
+        raise ValueError(f"{type(x).__name__}'s tensors must be on the device")
+    return ctypes.byref(x)
+
+
+def _workspace(ws):
+    if ws is not None and not ws.is_cuda:
+        raise ValueError("the workspace must be on the device")
+    return _ptr(ws), _ws_bytes(ws)
+
+
 def lizard_rope_table(spec: lizard_rope_spec):
     """The rotary table of ``spec`` as an int64 CPU tensor of rot/2 words (64-bit fixed-point
     turns per token); move it to the device and pass it to :class:`lizard_rope`."""
@@ -542,7 +558,7 @@ def _rope_call(name, dims, rope, a_q, a_k, positions, b_q, b_k, stream):
     sk = (dims.N, dims.Hk, dims.T, dims.d)
     aq, bq = _rows(a_q, sq, dims.dtype), _rows(b_q, sq, dims.dtype)
     ak, bk = _rows(a_k, sk, dims.dtype), _rows(b_k, sk, dims.dtype)
-    st = getattr(library(), name)(_ref(dims), _ref(rope), *aq, *ak,
+    st = getattr(library(), name)(_ref(dims), _held(rope), *aq, *ak,
                                   _ints(positions, (dims.N, dims.T), 8), *bq, *bk, _stream(stream))
     _check(st, name)
 
@@ -570,9 +586,9 @@ def lizard_cache_write(cache: lizard_cache, io: lizard_cache_io, k, v, rope, pos
     (None: T) of the cache, the keys rotated first if ``rope`` is given."""
     shape = (cache.N, cache.Hk, io.T, cache.d)
     st = library().lizard_cache_write(
-        _ref(cache), _ref(io), *_rows(k, shape, io.dtype), *_rows(v, shape, io.dtype), _ref(rope),
-        _ints(pos, (cache.N,), 8), _ints(count, (cache.N,), 4), _ptr(workspace),
-        _ws_bytes(workspace), _stream(stream))
+        _held(cache), _ref(io), *_rows(k, shape, io.dtype), *_rows(v, shape, io.dtype), _held(rope),
+        _ints(pos, (cache.N,), 8), _ints(count, (cache.N,), 4), *_workspace(workspace),
+        _stream(stream))
     _check(st, "lizard_cache_write")
 
 
@@ -581,9 +597,9 @@ def lizard_cache_read(cache: lizard_cache, io: lizard_cache_io, pos, count, k, v
     """Values of positions pos[n] + j, j < count[n] (None: T) into k, v [N,Hk,T,d]; other rows 0."""
     shape = (cache.N, cache.Hk, io.T, cache.d)
     st = library().lizard_cache_read(
-        _ref(cache), _ref(io), _ints(pos, (cache.N,), 8), _ints(count, (cache.N,), 4),
-        *_rows(k, shape, io.dtype), *_rows(v, shape, io.dtype), _ptr(workspace),
-        _ws_bytes(workspace), _stream(stream))
+        _held(cache), _ref(io), _ints(pos, (cache.N,), 8), _ints(count, (cache.N,), 4),
+        *_rows(k, shape, io.dtype), *_rows(v, shape, io.dtype),
+        *_workspace(workspace), _stream(stream))
     _check(st, "lizard_cache_read")
 
 
@@ -597,11 +613,12 @@ def lizard_cache_attn(cache: lizard_cache, dims: lizard_cache_attn_dims, q, rope
     (meta_k, meta_v [H,M,d]); q, y_add and y may be strided, y_add may be None or y."""
     shape = (cache.N, dims.H, dims.T, cache.d)
     for m in (meta_k, meta_v):
-        if m is not None and (m.shape != (dims.H, dims.M, cache.d) or _dtype_code(m) != dims.dtype):
-            raise ValueError("meta_k and meta_v must be [H, M, d] in the call's element type")
+        if m is not None and (m.shape != (dims.H, dims.M, cache.d) or not m.is_cuda
+                              or _dtype_code(m) != dims.dtype):
+            raise ValueError("meta_k and meta_v must be [H, M, d] in the call's element type, on the device")
     st = library().lizard_cache_attn(
-        _ref(cache), _ref(dims), *_rows(q, shape, dims.dtype), _ref(rope), _ints(pos, (cache.N,), 8),
+        _held(cache), _ref(dims), *_rows(q, shape, dims.dtype), _held(rope), _ints(pos, (cache.N,), 8),
         _ints(count, (cache.N,), 4), _ints(first, (cache.N,), 8), _ptr(meta_k), _ptr(meta_v),
-        *_rows(y_add, shape, dims.dtype), *_rows(y, shape, dims.dtype), _ptr(workspace),
-        _ws_bytes(workspace), _stream(stream))
+        *_rows(y_add, shape, dims.dtype), *_rows(y, shape, dims.dtype),
+        *_workspace(workspace), _stream(stream))
     _check(st, "lizard_cache_attn")

@@ -256,3 +256,25 @@ def test_oracle_rotation_is_orthogonal_and_its_adjoint_undoes_it():
         d1 = (co.rotate(a, [9], th, layout) * co.rotate(b, [4], th, layout)).sum()
         d2 = (co.rotate(a, [105], th, layout) * co.rotate(b, [100], th, layout)).sum()
         np.testing.assert_allclose(d1, d2, atol=1e-12)
+
+
+def test_binding_refuses_host_memory_everywhere():
+    """Handles, workspaces, rows and integers on the host raise before the library is called."""
+    import torch
+    z = torch.zeros
+    k, s, t = z(3, 2, 16, 64, dtype=torch.uint8), z(3, 2), z(1, 3, dtype=torch.int32)
+    cache = lz.lizard_cache(k, k.clone(), s, s.clone(), t, 0)
+    io, pos, ws = lz.lizard_cache_io(1, lz.LIZARD_F32), z(1, dtype=torch.int64), z(256, dtype=torch.uint8)
+    x = z(1, 2, 1, 64)
+    dims = lz.lizard_cache_attn_dims(2, 1, 0, 0, lz.LIZARD_F32, 0.0, 1.0)
+    for call in (lambda: lz.lizard_cache_write(cache, io, x, x, None, pos, None, ws, stream=0),
+                 lambda: lz.lizard_cache_read(cache, io, pos, None, x, x, ws, stream=0),
+                 lambda: lz.lizard_cache_attn(cache, dims, x, None, pos, None, None, None, None, None, x, ws, stream=0)):
+        with pytest.raises(ValueError, match="device"):
+            call()
+    rope = lz.lizard_rope(z(32, dtype=torch.int64), 64, 0)
+    with pytest.raises(ValueError, match="device"):
+        lz.lizard_rope_fwd(lz.lizard_rope_dims(1, 2, 0, 0, 64, lz.LIZARD_F32), rope, None, None, None, None, None, stream=0)
+    for bad in (dict(workspace=ws), dict(workspace=None)):
+        with pytest.raises(ValueError):
+            lz.lizard_cache_write(cache, io, x, x, rope, pos, None, bad["workspace"], stream=0)
