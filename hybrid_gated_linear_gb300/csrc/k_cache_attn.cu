@@ -40,6 +40,7 @@ constexpr int kUnit = 32;   // tokens per unit of work
 constexpr int kBatch = 16;  // units whose pages and scales are looked up at a time
 constexpr int kMaxM = 16;
 constexpr int kMaxCtas = 304;  // CTAs of a launch at most (sizes the scratch): two per SM
+static_assert(kMaxCtas * 8 <= kCacheCounters, "a counter per team");
 // From this many (sequence, head) pairs on, each warp works alone: starting and ending a
 // segment then stalls one warp of sixteen instead of a CTA's eight (512 pairs, 128 to 8192
 // tokens: 132 us against 160).  Below, a pair would be spread over so many warps that joining
@@ -114,7 +115,7 @@ __device__ __forceinline__ Segment segment_of(const CacheAttn& a, int m, int RB,
 struct Piece {
   Segment s;
   int64_t f, seg0;      // list indices: of the next piece, of segment m's first entry (head 0)
-  int m, n, r0, hk, ua, ub, seg, rows;
+  int m, n, r0, hk, ua, ub, rows;
   int c0, c1;           // the teams that share the segment and head
   int all_lo, all_hi;   // tokens that every row sees, relative to the segment's base
 };
@@ -343,7 +344,6 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG, Solo>::kPerSm)
           p.c1 = (int)((next - 1) / share);
           p.f = next;
         }
-        p.seg = p.m * Hk + p.hk;
         const int64_t last = p.s.p0 + (p.r0 + max(p.rows, 1) - 1) / G;
         p.all_lo = (int)min(max((int64_t)0, max(p.s.first, a.W > 0 ? last - a.W + 1 : (int64_t)0) - p.s.base),
                             (int64_t)0x7fffffff);
@@ -758,7 +758,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG, Solo>::kPerSm)
     constexpr int V4 = D / 4, ROWSTEP = kTeam / V4;
     // o[k][2 i + e] is channel (D/8) (2 t4 + e) + k of row g + 8 i
     const bool whole_seg = s_p.ua == 0 && s_p.ub == s_p.s.units;
-    float* part = reinterpret_cast<float*>(a.ws + (((size_t)M2 * Hk * sizeof(unsigned) + 255) & ~(size_t)255));
+    float* part = reinterpret_cast<float*>(a.ws + kCacheParts);
     auto slot = [&](int w, bool starts) { return part + (size_t)(2 * w + (starts ? 1 : 0)) * prow * (D + 4); };
     // Four channels f of row r of warp w: lanes g, t4 write them together, so their places in a
     // row are spread by both.
@@ -830,7 +830,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG, Solo>::kPerSm)
       const int c0 = s_p.c0, c1 = s_p.c1;
       team_sync();
       int last = 0;
-      if (tt_id == 0) last = count_up(reinterpret_cast<unsigned*>(a.ws) + s_p.seg) == (unsigned)(c1 - c0);
+      if (tt_id == 0) last = count_up(reinterpret_cast<unsigned*>(a.ws) + c0) == (unsigned)(c1 - c0);
       if (Solo) {
         last = __shfl_sync(0xffffffffu, last, 0);
         __syncwarp();
@@ -959,7 +959,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG, Solo>::kPerSm)
           for (int q = 0; q < RW; ++q)
             if (rb + q * ROWSTEP < s_p.rows) finish(rb + q * ROWSTEP, s[q], v[q], d0);
         }
-        if (tt_id == 0) reinterpret_cast<unsigned*>(a.ws)[s_p.seg] = 0u;
+        if (tt_id == 0) reinterpret_cast<unsigned*>(a.ws)[c0] = 0u;
       }
     }
     // the buffers were written with ordinary stores: order them before the next copies
@@ -1019,12 +1019,11 @@ cudaError_t by_format(const CacheAttn& a, cudaStream_t s, int* launches) {
 }  // namespace
 
 size_t cache_attn_workspace(int N, int Hk, int H, int T, int d, lizard_dtype dt) {
-  if (cache_attn_tc_used(H, Hk, T, dt)) return cache_attn_tc_workspace(N, Hk, H, T, d);
-  const int rows = H / Hk * T, RR = team_rows(rows), RB = rows > 0 ? (rows + RR - 1) / RR : 1;
+  if (cache_attn_tc_used(H, Hk, T, dt)) return cache_attn_tc_workspace(d);
+  const int rows = H / Hk * T;
   const int teams = kMaxCtas * (solo_warps(N, Hk, rows) ? 8 : 1);
-  // a counter per (sequence, rows, head), then two partial results per team
-  return align_up((size_t)N * RB * Hk * sizeof(unsigned), 256) +
-         (size_t)2 * teams * std::min(rows, RR) * (d + 4) * sizeof(float);
+  // the counters, then two partial results per team
+  return kCacheParts + (size_t)2 * teams * std::min(rows, team_rows(rows)) * (d + 4) * sizeof(float);
 }
 
 cudaError_t launch_cache_attn(const CacheAttn& a, lizard_dtype dt, cudaStream_t s, int* launches) {

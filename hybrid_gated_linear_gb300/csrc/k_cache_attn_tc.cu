@@ -247,7 +247,7 @@ __device__ __forceinline__ View view_of(const CacheAttn& a, int m, int tiles, in
 struct Piece {
   View v;
   int64_t f, seg0;  // list indices: of the next piece, of view m's first entry (head 0)
-  int m, n, hk, ua, ub, seg;
+  int m, n, hk, ua, ub;
   int c0, c1;       // the CTAs that share it
 };
 
@@ -734,7 +734,6 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
           p.c1 = (int)((next - 1) / share);
           p.f = next;
         }
-        p.seg = p.m * Hk + p.hk;
         if (p.hk == Hk - 1) p.seg0 = p.f, ++p.m;
       }
     }
@@ -996,7 +995,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
 
     // ---- output
     const bool alone = s_p.ua == 0 && s_p.ub == s_v.units;
-    float* part = reinterpret_cast<float*>(a.ws + (((size_t)M2 * Hk * sizeof(unsigned) + 255) & ~(size_t)255));
+    float* part = reinterpret_cast<float*>(a.ws + kCacheParts);
     auto slot = [&](int c) { return part + partial_at<D>(c, c == s_p.c0); };
     if (warp < 8 && __all_sync(0xffffffffu, done_ok && !*(volatile int*)&ctl->abort)) {
       const uint32_t to = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 256 + (warp >> 2) * D;
@@ -1011,8 +1010,8 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
     if (!alone) {
       __threadfence();
       __syncthreads();
-      unsigned* counter = reinterpret_cast<unsigned*>(a.ws) + s_p.seg;
       const int c0 = s_p.c0, c1 = s_p.c1;
+      unsigned* counter = reinterpret_cast<unsigned*>(a.ws) + c0;
       if (tid == 0) s_last = atomicAdd(counter, 1u) == (unsigned)(c1 - c0);
       __syncthreads();
       if (s_last) {
@@ -1072,11 +1071,9 @@ cudaError_t launch(const CacheAttn& a, cudaStream_t s, int* launches) {
 // 33 against 29; 32 rows 130 against 72 (eight of 8192).
 bool cache_attn_tc_used(int H, int Hk, int T, lizard_dtype dt) { return dt == LIZARD_BF16 && H / Hk * T > 64; }
 
-size_t cache_attn_tc_workspace(int N, int Hk, int H, int T, int d) {
-  const int tiles = (H / Hk * T + kRows - 1) / kRows;
-  // a counter per (sequence, rows, head), then two partial results per CTA
-  return align_up((size_t)tiles * N * Hk * sizeof(unsigned), 256) +
-         (size_t)2 * kMaxCtas * kRows * (d + 4) * sizeof(float);
+size_t cache_attn_tc_workspace(int d) {
+  // the counters, then two partial results per CTA
+  return kCacheParts + (size_t)2 * kMaxCtas * kRows * (d + 4) * sizeof(float);
 }
 
 cudaError_t launch_cache_attn_tc(const CacheAttn& a, cudaStream_t s, int* launches) {

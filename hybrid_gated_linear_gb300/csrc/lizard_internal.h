@@ -362,10 +362,17 @@ struct CacheAttn {
   unsigned* status;
   unsigned char* ws;  // workspace after the header
 };
+// The workspace of the attention over the cache, after the header: a counter for every team of
+// threads that a launch can have, then partial results.  A segment that several teams share has
+// one team that starts it, whose counter it uses, so the counters lie in the same place whatever
+// the call's shape and path: what one call leaves as partial results is no other call's counter.
+constexpr int kCacheCounters = 304 * 8;
+constexpr size_t kCacheParts = kCacheCounters * sizeof(unsigned);
+static_assert(kCacheParts % 256 == 0, "partial results are read 16 bytes at a time");
 size_t cache_attn_workspace(int N, int Hk, int H, int T, int d, lizard_dtype dt);
 // The tcgen05 path for many rows (query heads of a key head times new tokens).
 bool cache_attn_tc_used(int H, int Hk, int T, lizard_dtype dt);
-size_t cache_attn_tc_workspace(int N, int Hk, int H, int T, int d);
+size_t cache_attn_tc_workspace(int d);
 cudaError_t launch_cache_attn_tc(const CacheAttn& a, cudaStream_t s, int* launches);
 cudaError_t launch_cache_attn(const CacheAttn& a, lizard_dtype dt, cudaStream_t s, int* launches);
 

@@ -544,9 +544,10 @@ lizard_status lizard_cache_read(const lizard_cache* cache, const lizard_cache_io
  * LIZARD_ERR_DEVICE_CHECK.  Every sum and the softmax are in fp32; bf16 calls round the
  * query and the unnormalised probabilities to 11 bits for the tensor cores, fp32 calls
  * carry them in two such parts.  Run-to-run identical.
- * Workspace: lizard_cache_attn_workspace_bytes, zero before the first call; each call
- * leaves it zero but for the status word and scratch.  Calls that may run at the same time
- * need their own.
+ * Workspace: at least lizard_cache_attn_workspace_bytes, zero before the first call.  Calls of
+ * this function ordered one after the other may share one, whatever their shapes, if it is large
+ * enough for each; calls that may run at the same time need their own.  After
+ * LIZARD_ERR_TIMEOUT it has to be set to zero again.
  */
 typedef struct lizard_cache_attn_dims {
     int32_t H;             /* query heads, a multiple of the cache's Hk */
