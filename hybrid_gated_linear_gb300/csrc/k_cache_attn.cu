@@ -559,6 +559,10 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG, Solo>::kPerSm)
       // an unseen block's products become -inf: any positive factor will do
       const float kk[2] = {ok0 ? __uint_as_float((ex & 0xff) << 23) : 1.f,
                            ok1 ? __uint_as_float((ex >> 8 & 0xff) << 23) : 1.f};
+      // what makes a logit of row half h's product in block b.  Tiny queries over tiny keys would
+      // make it 0, and the -inf of hidden tokens NaN; the smallest normal number makes 0 of any
+      // product (below 2^31) just as well.
+      auto factor = [&](float r, int b) { return fmaxf(r * kk[b], 0x1p-126f); };
       const float ve[2] = {(float)((int)(ex >> 16 & 0xff) - 127), (float)((int)(ex >> 24) - 127)};
       float z[4][4];
 #pragma unroll
@@ -609,7 +613,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG, Solo>::kPerSm)
       refill(0);
 
       // Row half h (rows g, g + 8) and 16-token block b: z holds raw products, to be multiplied
-      // by f = rs kk.  The upper half is skipped where there are eight rows or fewer.
+      // by factor(rs, b).  The upper half is skipped where there are eight rows or fewer.
       const bool whole = ok0 && ok1 && tok >= s_p.all_lo && tok + kUnit - 1 <= s_p.all_hi;
       const float rs[2] = {s_rs[rg * 16 + g], s_rs[rg * 16 + g + 8]};
       if (!whole) {  // column 8 i + 2 t4 + e; at the ends only, so the limits are found here
@@ -643,7 +647,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG, Solo>::kPerSm)
                             fmaxf(z[2 * b + 1][2 * h], z[2 * b + 1][2 * h + 1]));
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-            x *= rs[h] * kk[b];
+            x *= factor(rs[h], b);
             mn = fmaxf(mn, x);
             mon[h] = fmaxf(mon[h], x + ve[b]);
           }
@@ -668,7 +672,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG, Solo>::kPerSm)
           const float ml = mrow[h] == -INFINITY ? 0.f : mrow[h], mol = mo[h] == -INFINITY ? 0.f : mo[h];
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
-            const float f = rs[h] * kk[b], sh = mol - ve[b];
+            const float f = factor(rs[h], b), sh = mol - ve[b];
             float sum = 0.f;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {

@@ -1,0 +1,37 @@
+"""Attention over the 8-bit cache at the edges of its inputs' range, against the definition in 64
+bits over the cache's own values (cache_oracle.attend_bound)."""
+import pytest
+
+from cache_gpu_util import Filled, check_attention, gaussian
+
+pytestmark = pytest.mark.gpu
+
+PATHS = [  # N, H, Hk, d, T, dtype: one of each kernel variant
+    (2, 4, 2, 64, 1, "bf16"), (2, 4, 2, 128, 1, "f32"),          # 16 rows
+    (2, 6, 2, 64, 7, "bf16"), (2, 3, 1, 64, 7, "f32"),           # 32 rows
+    (1, 4, 1, 64, 13, "bf16"), (1, 4, 1, 128, 13, "f32"),        # 64 rows
+    (1, 2, 1, 64, 75, "f32"),                                    # 128 rows
+    (40, 16, 8, 64, 1, "bf16"), (40, 8, 8, 128, 2, "f32"),       # a warp per sequence and head
+    (2, 4, 2, 64, 70, "bf16"), (1, 2, 1, 128, 140, "bf16"),      # tcgen05
+]
+IDS = ["-".join(map(str, p)) for p in PATHS]
+
+
+def typed(x, dtype):
+    import torch
+    return x.to(torch.float32 if dtype == "f32" else torch.bfloat16)
+
+
+@pytest.mark.parametrize("keys,queries", [(0.0, 0.0), (0.0, 2.0 ** -9), (0.0, 1.0), (2.0 ** -30, 0.0), (1.0, 0.0),
+                                          (2.0 ** -100, 2.0 ** -60)])
+@pytest.mark.parametrize("path", PATHS, ids=IDS)
+def test_zero_and_tiny_queries_and_keys(path, keys, queries):
+    """All logits (nearly) 0: the mean of the visible values, although hidden tokens share blocks
+    with visible ones and the logits' factor is below the smallest fp32 number."""
+    N, H, Hk, d, T, dtype = path
+    held = [T + 37 - n % 30 for n in range(N)]
+    k, v = gaussian((N, Hk, max(held), d), 1, keys), gaussian((N, Hk, max(held), d), 2)
+    q = typed(gaussian((N, H, T, d), 3, queries), dtype)
+    add = typed(gaussian((N, H, T, d), 4), dtype)
+    f = Filled(k, v, [0] * N, held, 16, "e4m3")
+    check_attention(f, q, [h - T for h in held], W=20, y_add=add)
