@@ -5,8 +5,10 @@
 // tokens.  With z the logits in units of log 2, softmax is one pass over the cache:
 //   m' = max(m, z),  l' = l 2^(m-m') + sum 2^(z-m'),  o' = o 2^(m-m') + sum 2^(z-m') v.
 // The value scales are powers of two 2^e per page, so the weights the tensor cores see are
-// 2^(z+e-mo) with a maximum mo of their own: they stay near (0, 1], whatever the pages' scales.
-// m moves with every unit, mo (and with it the rescaling of o) only by more than kLazy at a time.
+// 2^(z+e-mo), whatever the pages' scales, with a reference mo of their own, kLift below the
+// maximum of z + e when it is set: binary16 holds 2^-24 to 2^16, and what many light tokens next to
+// a heavy one weigh is lost at the low end.  m moves with every unit, mo (and with it the
+// rescaling of o) only when the maximum has grown by more than kLazy.
 //
 // What bounds it: the cache is read once, 2 D bytes per token and head, and everything else
 // is small; the floor is those bytes at the measured copy rate.  So the work is cut evenly
@@ -46,7 +48,6 @@ static_assert(kMaxCtas * 8 <= kCacheCounters, "a counter per team");
 // tokens: 132 us against 160).  Below, a pair would be spread over so many warps that joining
 // their results costs more (128 pairs, 4096 tokens: 45 us against 39).
 constexpr int64_t kSoloSegments = 256;
-constexpr float kLazy = 8.f;  // outputs are rescaled when their maximum has grown by 2^8: weights fit binary16
 constexpr float kFar = 60.f;  // see where it is used
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -165,6 +166,10 @@ struct Shape {
   // get fewer units.  (3 and 12 instead: 64 uneven sequences 106 -> 110 us, 16 of them 62 -> 66.)
   static constexpr int kSegCost = Solo ? 8 : 20;
   static constexpr int kMinUnits = 4 * TG;  // of a piece, where a segment has them
+  // Weights reach 2^(kLift + kLazy), a quarter of binary16's range: logits may be off by their own
+  // rounding.  Two parts of a weight resolve 2^-25 / 2^kLift of the largest; fp32 calls, whose
+  // rescaling is little beside their products, take most of the range for that.
+  static constexpr float kLift = NS == 2 ? 12.f : 6.f, kLazy = 14.f - kLift;
 };
 
 template <typename T, int D, int F, int RG, bool Solo>
@@ -649,11 +654,11 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG, Solo>::kPerSm)
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
             x *= factor(rs[h], b);
             mn = fmaxf(mn, x);
-            mon[h] = fmaxf(mon[h], x + ve[b]);
+            mon[h] = fmaxf(mon[h], x + ve[b] - Sh::kLift);
           }
           // the sum's scale follows its maximum exactly, the output's only in steps
           if (mn > mrow[h]) l[h] *= tc::ex2_approx(mrow[h] - mn), mrow[h] = mn;
-          jump |= mon[h] > mo[h] + kLazy;
+          jump |= mon[h] > mo[h] + Sh::kLazy;
         }
       if (__any_sync(0xffffffffu, jump)) {
 #pragma unroll

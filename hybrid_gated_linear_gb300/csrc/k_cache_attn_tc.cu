@@ -11,9 +11,10 @@
 //   2 x 4 warps, one thread per row: running maxima and sum, P = 2^(z + e - mo) as binary16
 //             over the columns S was read from
 // The two tiles alternate, so the tensor cores work on one while the other's exponentials
-// are taken.  z = logits in units of log 2, e = log2 of the page's value scale; mo is the
-// running maximum of z + e, so the weights stay near (0, 1] whatever the pages' scales, and
-// m that of z, for the sum.  O is rescaled only when mo has grown by more than 2^kLazy.
+// are taken.  z = logits in units of log 2, e = log2 of the page's value scale; m is the running
+// maximum of z, for the sum, and mo, for the weights, that of z + e less kLift, whatever the
+// pages' scales: binary16 holds 2^-24 to 2^16, and light tokens are lost at its low end.  O is
+// rescaled only when the maximum has grown by more than kLazy.
 //
 // What bounds it: 4 D multiply-adds per row and token on the tensor cores against one
 // exponential (32 per clock and SM) and a handful of fp32 operations per row and token; the
@@ -46,7 +47,9 @@ constexpr int kMaxM = 16;
 // Starting rows costs a CTA about as much as kCost blocks; pieces shorter than kMinBlocks are
 // not worth joining.
 constexpr int kCost = 6, kMinBlocks = 6;
-constexpr float kLazy = 8.f;     // P <= 2^8 fits binary16 with room for its sums
+// The weights' reference is set kLift below the running maximum, so P <= 2^(kLift + kLazy), a
+// quarter of binary16's range: logits may be off by their own rounding.
+constexpr float kLift = 6.f, kLazy = 8.f;
 constexpr float kFar = 60.f;      // see weights()
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -955,7 +958,7 @@ __global__ void __launch_bounds__(kThreads, 1) prompt_kernel(const __grid_consta
         if (checked) part_maxima<true>(ts, sc, rs, tok, lo_r, hi_r, mb);
         else part_maxima<false>(ts, sc, rs, tok, lo_r, hi_r, mb);
 #pragma unroll
-        for (int b = 0; b < 8; ++b) mn = fmaxf(mn, mb[b]), mon = fmaxf(mon, mb[b] + sc[b].y);
+        for (int b = 0; b < 8; ++b) mn = fmaxf(mn, mb[b]), mon = fmaxf(mon, mb[b] + sc[b].y - kLift);
         // the sum's scale follows m exactly, the output's only in steps
         if (mn > m) l *= exp2f(m - mn), m = mn;
         const bool jump = mon > mo + kLazy;

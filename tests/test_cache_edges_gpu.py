@@ -35,3 +35,23 @@ def test_zero_and_tiny_queries_and_keys(path, keys, queries):
     add = typed(gaussian((N, H, T, d), 4), dtype)
     f = Filled(k, v, [0] * N, held, 16, "e4m3")
     check_attention(f, q, [h - T for h in held], W=20, y_add=add)
+
+
+# What the weights cannot resolve, in units of a row's largest: include/lizard.h.
+FLOOR = {"bf16": 2.0 ** -31, "f32": 2.0 ** -37}
+
+
+@pytest.mark.parametrize("below", [12.3, 18.7, 21.4, 24.6])
+@pytest.mark.parametrize("path", PATHS, ids=IDS)
+def test_a_token_far_above_the_others(path, below):
+    """The first token takes nearly all of the weight and has a value of zero (an attention sink):
+    the output is what the others, each 2^-below as heavy, add up to."""
+    import math
+    N, H, Hk, d, T, dtype = path
+    L = 600 if N > 2 else 3000
+    k, v = gaussian((N, Hk, L + T, d), 1, 0.0), gaussian((N, Hk, L + T, d), 2) + 1.0
+    k[:, :, 0, 0], v[:, :, 0] = 16.0, 0.0
+    q = gaussian((N, H, T, d), 3)
+    q[..., 0] = below * math.log(2) * d ** 0.5 / 16
+    f = Filled(k, v, [0] * N, [L + T] * N, 64, "e4m3")
+    check_attention(f, typed(q, dtype), [L] * N, floor=FLOOR[dtype])
