@@ -645,7 +645,7 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG, Solo>::kPerSm)
       for (int h = 0; h < 2; ++h)
         if (h == 0 || high) {
           float mn = mrow[h];
-          mon[h] = mo[h];
+          float top = -INFINITY;
 #pragma unroll
           for (int b = 0; b < 2; ++b) {
             float x = fmaxf(fmaxf(z[2 * b][2 * h], z[2 * b][2 * h + 1]),
@@ -654,8 +654,9 @@ __global__ void __launch_bounds__(kThreads, Shape<T, D, F, RG, Solo>::kPerSm)
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
             x *= factor(rs[h], b);
             mn = fmaxf(mn, x);
-            mon[h] = fmaxf(mon[h], x + ve[b] - Sh::kLift);
+            top = fmaxf(top, x + ve[b]);
           }
+          mon[h] = fmaxf(mo[h], top - Sh::kLift);
           // the sum's scale follows its maximum exactly, the output's only in steps
           if (mn > mrow[h]) l[h] *= tc::ex2_approx(mrow[h] - mn), mrow[h] = mn;
           jump |= mon[h] > mo[h] + Sh::kLazy;
