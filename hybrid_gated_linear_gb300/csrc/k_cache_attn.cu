@@ -86,11 +86,12 @@ __device__ __forceinline__ Segment segment_of(const CacheAttn& a, int m, int RB,
   s.p0 = a.pos[n];
   s.cnt = a.count ? a.count[n] : a.T;
   s.first = a.first ? max((int64_t)0, a.first[n]) : 0;
-  const bool known = s.cnt >= 0 && s.cnt <= a.T && s.p0 >= 0;
-  if (!known) raise_status(a.status, kDevCheck);
-  s.cnt = known ? s.cnt : 0;
+  // rows of an unknown count are 0; with a bad position they see no cached token
+  const bool known = s.cnt >= 0 && s.cnt <= a.T, placed = position_ok(s.p0);
+  if (!known || !placed) raise_status(a.status, kDevCheck);
+  s.cnt = known ? s.cnt : 0, s.p0 = placed ? s.p0 : 0;
   s.base = 0, s.lo = 0, s.hi = -1, s.units = 1;
-  if (r0 < s.cnt * G) {
+  if (placed && r0 < s.cnt * G) {
     // what the whole sequence sees has to fit its table
     const int64_t all_lo = max(s.first, a.W > 0 ? s.p0 - a.W + 1 : (int64_t)0), all_hi = s.p0 + s.cnt - 1;
     if (all_lo <= all_hi) {

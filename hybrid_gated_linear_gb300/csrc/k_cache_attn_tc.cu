@@ -222,14 +222,15 @@ __device__ __forceinline__ View view_of(const CacheAttn& a, int m, int tiles, in
   v.p0 = a.pos[n];
   v.cnt = a.count ? a.count[n] : a.T;
   v.first = a.first ? max((int64_t)0, a.first[n]) : 0;
-  const bool known = v.cnt >= 0 && v.cnt <= a.T && v.p0 >= 0;
-  if (!known) raise_status(a.status, kDevCheck);
-  v.cnt = known ? v.cnt : 0;
+  // rows of an unknown count are 0; with a bad position they see no cached token
+  const bool known = v.cnt >= 0 && v.cnt <= a.T, placed = position_ok(v.p0);
+  if (!known || !placed) raise_status(a.status, kDevCheck);
+  v.cnt = known ? v.cnt : 0, v.p0 = placed ? v.p0 : 0;
   v.r0 = (m - n * tiles) * kRows;
   v.rows = max(0, min(kRows, v.cnt * G - v.r0));
   v.base = 0, v.lo = 0, v.hi = -1, v.units = 1;
   const int64_t all_lo = max(v.first, a.W > 0 ? v.p0 - a.W + 1 : (int64_t)0), all_hi = v.p0 + v.cnt - 1;
-  if (v.rows > 0 && all_lo <= all_hi) {
+  if (placed && v.rows > 0 && all_lo <= all_hi) {
     if (!span_ok(a.c, all_lo, all_hi)) {
       raise_status(a.status, kDevCheck);
     } else {

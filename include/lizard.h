@@ -540,11 +540,12 @@ lizard_status lizard_cache_read(const lizard_cache* cache, const lizard_cache_io
  *   q, y, y_add [N,H,T,d] T (y_add NULL, or y itself, or apart from it); meta_k, meta_v
  *   [H,M,d] T contiguous; pos, first [N] int64, count [N] int32.
  * A sequence that fails the checks of lizard_cache_write (for the pages its queries see)
- * sees no cached token, a page number outside the pool is skipped, and both set
- * LIZARD_ERR_DEVICE_CHECK.  Every sum and the softmax are in fp32; bf16 calls round the
- * query and the unnormalised probabilities to 11 bits for the tensor cores, fp32 calls
- * carry them in two such parts.  A probability is held to 2^-31 (bf16 calls) or 2^-37 of the
- * largest (value scale included) that its row has met.  Run-to-run identical.
+ * sees no cached token (if its count is outside 0..T, its rows are written as 0), a page
+ * number outside the pool is skipped, and both set LIZARD_ERR_DEVICE_CHECK.
+ * Every sum and the softmax are in fp32; bf16 calls round the query and the unnormalised
+ * probabilities to 11 bits for the tensor cores, fp32 calls carry them in two such parts.  A
+ * probability is held to 2^-31 (bf16 calls) or 2^-37 of the largest (value scale included)
+ * that its row has met.  Run-to-run identical.
  * Workspace: at least lizard_cache_attn_workspace_bytes, zero before the first call.  Calls of
  * this function ordered one after the other may share one, whatever their shapes, if it is large
  * enough for each; calls that may run at the same time need their own.  After

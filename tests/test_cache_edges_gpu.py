@@ -2,7 +2,8 @@
 bits over the cache's own values (cache_oracle.attend_bound)."""
 import pytest
 
-from cache_gpu_util import Filled, check_attention, gaussian
+import hybrid_gated_linear_gb300 as lz
+from cache_gpu_util import Filled, assert_within, attend, bound_of, check_attention, definition, gaussian, on_device
 
 pytestmark = pytest.mark.gpu
 
@@ -55,3 +56,46 @@ def test_a_token_far_above_the_others(path, below):
     q[..., 0] = below * math.log(2) * d ** 0.5 / 16
     f = Filled(k, v, [0] * N, [L + T] * N, 64, "e4m3")
     check_attention(f, typed(q, dtype), [L] * N, floor=FLOOR[dtype])
+
+
+@pytest.mark.parametrize("path", PATHS, ids=IDS)
+def test_bad_positions_see_no_cached_token(path):
+    """A position below zero or too far to be counted: the sequence sees the meta tokens only, is
+    merged as any other, and the status says so; a bad count leaves rows of zeros."""
+    import torch
+    N, H, Hk, d, T, dtype = path
+    N = max(N, 3)
+    k, v = gaussian((N, Hk, T + 40, d), 1), gaussian((N, Hk, T + 40, d), 2)
+    f = Filled(k, v, [0] * N, [T + 40] * N, 16, "i8")
+    q, add = typed(gaussian((N, H, T, d), 3), dtype), typed(gaussian((N, H, T, d), 4), dtype)
+    meta = [typed(gaussian((H, 3, d), 5 + i), dtype) for i in range(2)]
+    check = lz.LizardError(5, "").status
+    for bad in (-1, -2 ** 63, 2 ** 63 - 1, 2 ** 62 + 5):
+        pos = [40, bad] + [40] * (N - 2)
+        y = attend(f, q, pos, meta=meta, y_add=add, alpha=0.5, status=check)
+        # the same with nothing visible
+        kw = dict(meta=meta, y_add=add, alpha=0.5, first=[0, 2 ** 40] + [0] * (N - 2))
+        want = definition(f, q, [40] * N, **kw)
+        assert_within(y, want[0], bound_of(q, [40], *want, add))
+    count = [T] * N
+    for bad in (-1, T + 1, -2 ** 31, 2 ** 31 - 1):
+        count[1] = bad
+        y = attend(f, q, [40] * N, count=count, meta=meta, y_add=add, alpha=0.5, status=check)
+        assert (y[1] == 0).all() and torch.isfinite(y).all()
+
+
+def test_writes_and_reads_at_positions_too_far_to_be_counted_are_flagged():
+    import torch
+    k = gaussian((2, 1, 5, 64), 1)
+    f = Filled(k, k, [0, 0], [5, 5], 16, "e4m3")
+    was = [x.clone() for x in f.h._keep]
+    ws = torch.zeros(lz.lizard_cache_workspace_bytes(), dtype=torch.uint8, device="cuda")
+    io = lz.lizard_cache_io(5, lz.LIZARD_F32)
+    for bad in (2 ** 63 - 1, 2 ** 63 - 3, -2 ** 63, -1):
+        lz.lizard_cache_write(f.h, io, k, k, None, on_device([bad] * 2), None, ws)
+        assert lz.lizard_check_device_errors(ws) == lz.LizardError(5, "").status
+        assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(was, f.h._keep))
+        out = [torch.full_like(k, 3.0) for _ in "kv"]
+        lz.lizard_cache_read(f.h, io, on_device([bad, 0]), None, *out, ws)
+        assert lz.lizard_check_device_errors(ws) == lz.LizardError(5, "").status
+        assert all((o[0] == 0).all() and torch.equal(o[1], h[1]) for o, h in zip(out, f.held))
