@@ -80,9 +80,9 @@ bool any_overlap(const Span* outs, int no, const Span* ins, int ni) {
   return false;
 }
 
-// Two strided tensors share no element: their spans are apart, or both keep all heads of a
-// token together, step over tokens alike and lie side by side inside that step (slices of
-// one packed projection).
+// Two strided tensors share no element: their spans are apart, or, counted modulo the stride of
+// some axis of either, what each covers lies beside the other (slices of one packed projection:
+// of its heads, whichever axis is outermost).
 struct Tensor {
   const void* p;
   const Rows* r;
@@ -90,13 +90,24 @@ struct Tensor {
 };
 bool apart(const Tensor& a, const Tensor& b) {
   if (!overlap(Span{a.p, a.r->bytes}, Span{b.p, b.r->bytes})) return true;
-  if (a.T < 2 || a.r->s.t != b.r->s.t) return false;
-  if (a.N > 1 && (a.r->s.n != b.r->s.n || a.r->s.n % a.r->s.t)) return false;
-  const int64_t step = a.r->s.t * a.es;
-  const int64_t wa = ((a.H - 1) * a.r->s.h + a.d) * a.es, wb = ((b.H - 1) * b.r->s.h + b.d) * b.es;
   const int64_t off = static_cast<const char*>(b.p) - static_cast<const char*>(a.p);
-  const int64_t at = (off % step + step) % step;
-  return wa <= at && at + wb <= step;
+  for (const Tensor* x : {&a, &b}) {
+    const int64_t dim[3] = {x->N, x->H, x->T}, stride[3] = {x->r->s.n, x->r->s.h, x->r->s.t};
+    for (int i = 0; i < 3; ++i) {
+      if (dim[i] <= 1 || stride[i] <= 0) continue;
+      // bytes from the first element on, steps of a multiple of the stride left out
+      auto width = [&](const Tensor& t) {
+        const int64_t td[3] = {t.N, t.H, t.T}, ts[3] = {t.r->s.n, t.r->s.h, t.r->s.t};
+        int64_t w = t.d;
+        for (int k = 0; k < 3; ++k)
+          if (td[k] > 1 && ts[k] % stride[i]) w += (td[k] - 1) * ts[k];
+        return w * t.es;
+      };
+      const int64_t step = stride[i] * a.es, at = (off % step + step) % step;
+      if (width(a) <= at && at + width(b) <= step) return true;
+    }
+  }
+  return false;
 }
 
 bool same(const lz::Strides& a, const lz::Strides& b) { return a.n == b.n && a.h == b.h && a.t == b.t; }
@@ -210,9 +221,14 @@ lizard_status io_call(const lizard_cache* cache, const lizard_cache_io* io, void
                         {a.rope.turns, (size_t)a.rope.rot * 4}};
   const Span ws[] = {{workspace, workspace_bytes}};
   if (any_overlap(ws, 1, c, 5) || any_overlap(ws, 1, rows, 2) || any_overlap(ws, 1, small + 1, 3) ||
-      any_overlap(rows, write ? 0 : 2, c, 4) || any_overlap(c, 4, small, 4) || any_overlap(c, 4, rows, 2) ||
-      (!write && any_overlap(rows, 2, small, 4)))
+      any_overlap(c, 4, small, 4) || any_overlap(c, 4, rows, 2))
     return LIZARD_ERR_INVALID_ARG;
+  if (!write) {  // the rows are outputs, apart from each other and from what is read
+    const int64_t es = (int64_t)elem_size(io->dtype);
+    const Tensor tk{k, &rk, a.c.N, a.c.Hk, io->T, a.c.d, es}, tv{v, &rv, a.c.N, a.c.Hk, io->T, a.c.d, es};
+    if (any_overlap(rows, 1, small, 4) || any_overlap(rows + 1, 1, small, 4) || !apart(tk, tv))
+      return LIZARD_ERR_INVALID_ARG;
+  }
   if (none) return LIZARD_OK;
   a.T = io->T;
   a.k = k, a.v = v, a.sk = rk.s, a.sv = rv.s;
@@ -323,13 +339,15 @@ lizard_status lizard_cache_attn(const lizard_cache* cache, const lizard_cache_at
   cache_spans(a.c, c);
   const size_t meta = (size_t)d.H * d.M * a.c.d * elem_size(d.dtype);
   const Span outs[] = {{y, ry.bytes}, {workspace, workspace_bytes}};
-  const Span ins[] = {{q, rq.bytes}, {pos, (size_t)a.c.N * 8}, {count, (size_t)a.c.N * 4},
-                      {first, (size_t)a.c.N * 8}, {meta_k, meta}, {meta_v, meta},
-                      {a.rope.turns, (size_t)a.rope.rot * 4}};
-  const Span sum{y_add, ra.bytes};
+  const Span ins[] = {{pos, (size_t)a.c.N * 8}, {count, (size_t)a.c.N * 4}, {first, (size_t)a.c.N * 8},
+                      {meta_k, meta}, {meta_v, meta}, {a.rope.turns, (size_t)a.rope.rot * 4}};
+  const Span rows[] = {{q, rq.bytes}, {y_add, ra.bytes}};
+  const int64_t es = (int64_t)elem_size(d.dtype);
+  const Tensor tq{q, &rq, a.c.N, d.H, d.T, a.c.d, es}, ta{y_add, &ra, a.c.N, d.H, d.T, a.c.d, es};
+  const Tensor ty{y, &ry, a.c.N, d.H, d.T, a.c.d, es};
   const bool place = y_add == y && same(ra.s, ry.s);
-  if (any_overlap(outs, 2, ins, 7) || any_overlap(outs, 2, c, 5) || overlap(sum, outs[1]) ||
-      (!place && overlap(sum, outs[0])))
+  if (any_overlap(outs, 2, ins, 6) || any_overlap(outs, 2, c, 5) || any_overlap(outs + 1, 1, rows, 2) ||
+      !apart(ty, tq) || (!place && !apart(ty, ta)))
     return LIZARD_ERR_INVALID_ARG;
   if (none) return LIZARD_OK;
   a.H = d.H, a.T = d.T, a.M = d.M, a.W = d.W;

@@ -276,3 +276,33 @@ def test_binding_refuses_host_memory_everywhere():
     for bad in (dict(workspace=ws), dict(workspace=None)):
         with pytest.raises(ValueError):
             lz.lizard_cache_write(cache, io, x, x, rope, pos, None, bad["workspace"], stream=0)
+
+
+# ---------------------------------------------------------------------------------------
+# slices of one buffer that share an element
+# ---------------------------------------------------------------------------------------
+def test_slices_of_one_buffer_that_share_an_element_are_refused(lib):
+    """Token-major and head-major, one new token included; every call here shares a head, a part of
+    one, or steps over its neighbour differently (those that share nothing run on the GPU)."""
+    H, Hk, d, f32 = 4, 2, 128, lz.LIZARD_F32
+    for N, T in ((3, 1), (3, 5), (1, 5)):
+        for head_major in (False, True):
+            w = (H + 2 * Hk) * d
+            s = (T * w, T * d, d) if head_major else (T * w, d, w)
+            head = (T if head_major else 1) * d * 4  # bytes from one head to the next
+            for k in (_a(1) + (H - 1) * head, _a(1) + H * head - 16, _a(1) + 16):
+                assert _rope_st(lib, dims=(N, H, Hk, T, d, f32), xq=_a(1), sxq=s, yq=_a(1), syq=s, xk=k, sxk=s, yk=k,
+                                syk=s) == INVALID, (N, T, head_major)
+                kw = dict(N=N, Hk=Hk, dims=(H, T, 0, 0, f32, 0.0, 1.0))
+                assert _attn_st(lib, q=_a(1), sq=s, y=k, sy=s, **kw) == INVALID
+                assert _attn_st(lib, q=_a(2), add=_a(1), sadd=s, y=k, sy=s, **kw) == INVALID
+            # the last head reaches into the next sequence's or token's first
+            if N > 1 or not head_major:
+                assert _attn_st(lib, q=_a(1), sq=s, y=_a(1) + (2 * Hk + 1) * head, sy=s, N=N, Hk=Hk,
+                                dims=(H, T, 0, 0, f32, 0.0, 1.0)) == INVALID
+            v = _a(1) + (Hk - 1) * head
+            assert _io_st(lib, False, N=N, Hk=Hk, T=T, dtype=f32, k=_a(1), sk=s, v=v, sv=s) == INVALID
+            # beside each other in the first token (sequence), but the second tensor steps differently
+            if N > 1 and T > 1:
+                t = (s[0] + d, s[1], s[2])
+                assert _io_st(lib, False, N=N, Hk=Hk, T=T, dtype=f32, k=_a(1), sk=s, v=_a(1) + Hk * head, sv=t) == INVALID

@@ -99,3 +99,32 @@ def test_writes_and_reads_at_positions_too_far_to_be_counted_are_flagged():
         lz.lizard_cache_read(f.h, io, on_device([bad, 0]), None, *out, ws)
         assert lz.lizard_check_device_errors(ws) == lz.LizardError(5, "").status
         assert all((o[0] == 0).all() and torch.equal(o[1], h[1]) for o, h in zip(out, f.held))
+
+
+@pytest.mark.parametrize("order", ["token", "head"])
+@pytest.mark.parametrize("N,T", [(5, 1), (3, 6)])
+def test_outputs_beside_other_tensors_in_one_buffer(N, T, order):
+    """Attention into a slice of the buffer that holds its queries and the other branch's output,
+    and a read-back of keys and values into one buffer: no element is shared."""
+    import torch
+    H, Hk, d = 4, 2, 64
+    f = Filled(gaussian((N, Hk, 50, d), 1), gaussian((N, Hk, 50, d), 2), [0] * N, [50] * N, 16, "e4m3")
+    shape = (N, T, 3 * H, d) if order == "token" else (N, 3 * H, T, d)
+    w = gaussian(shape, 3)
+    x = w.permute(0, 2, 1, 3) if order == "token" else w
+    q, add, y = x[:, :H], x[:, H:2 * H], x[:, 2 * H:]
+    pos = [50 - T] * N
+    want = attend(f, q.contiguous(), pos, y_add=add.contiguous())
+    was = x[:, :2 * H].clone()
+    dims = lz.lizard_cache_attn_dims(H, T, 0, 0, lz.LIZARD_F32, 0.0, 1.0)
+    ws = torch.zeros(lz.lizard_cache_attn_workspace_bytes(f.h, dims), dtype=torch.uint8, device="cuda")
+    lz.lizard_cache_attn(f.h, dims, q, None, on_device(pos), None, None, None, None, add, y, ws)
+    assert lz.lizard_check_device_errors(ws) == 0
+    assert torch.equal(y, want) and torch.equal(x[:, :2 * H], was)
+    shape = (N, T, 2 * Hk, d) if order == "token" else (N, 2 * Hk, T, d)
+    both = gaussian(shape, 4)
+    both = both.permute(0, 2, 1, 3) if order == "token" else both
+    lz.lizard_cache_read(f.h, lz.lizard_cache_io(T, lz.LIZARD_F32), on_device(pos), None, both[:, :Hk], both[:, Hk:], ws)
+    assert lz.lizard_check_device_errors(ws) == 0
+    for i in range(2):
+        assert torch.equal(both[:, i * Hk:(i + 1) * Hk], f.held[i][:, :, 50 - T:])

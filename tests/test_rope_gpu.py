@@ -154,3 +154,24 @@ def test_rope_around_the_window_branch_of_the_operator():
     ref = oracle.bwd(*(ref_in[n] for n in NAMES), x["dy"], W=W)
     assert rel_l2(host(dq), co.rotate(ref["d_q"], pos, th, sign=-1.0)) < 2e-2
     assert rel_l2(host(dk), co.rotate(ref["d_k"], pos, th, sign=-1.0)) < 2e-2
+
+
+@pytest.mark.parametrize("order", ["token", "head"])
+@pytest.mark.parametrize("N,T", [(5, 1), (1, 1), (3, 4)])
+def test_rope_in_place_on_slices_of_a_packed_projection(N, T, order):
+    """q and k inside one [N,T,(H+2Hk),d] or [N,(H+2Hk),T,d] projection, one new token included:
+    the slices share no element, although their spans overlap."""
+    import torch
+    H, Hk, d = 4, 2, 64
+    rng = np.random.default_rng(N + T)
+    rope, th = make_rope(d)
+    shape = (N, T, H + 2 * Hk, d) if order == "token" else (N, H + 2 * Hk, T, d)
+    w = torch.from_numpy(rng.standard_normal(shape).astype(np.float32)).cuda()
+    x = w.permute(0, 2, 1, 3) if order == "token" else w
+    was = x.cpu().numpy().astype(np.float64)
+    q, k = x[:, :H], x[:, H:H + Hk]
+    lz.lizard_rope_fwd(lz.lizard_rope_dims(N, H, Hk, T, d, lz.LIZARD_F32), rope, q, k, None, q, k)
+    pos = np.arange(T)[None, None]
+    check(q, was[:, :H], pos, th, "half", 1.0, 1.0, "f32")
+    check(k, was[:, H:H + Hk], pos, th, "half", 1.0, 1.0, "f32")
+    np.testing.assert_array_equal(x[:, H + Hk:].cpu().numpy(), was[:, H + Hk:])
