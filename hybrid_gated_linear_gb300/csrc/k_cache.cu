@@ -45,7 +45,7 @@ template <typename T> struct Raw16 {
 // Cosines and sines of a row's pairs in shared memory, four floats of padding every 32: lanes
 // that read the pairs of different chunks with 16-byte accesses hit different banks.
 __device__ __forceinline__ int pair_at(int i) { return i + 4 * (i >> 5); }
-__host__ __device__ __forceinline__ int row_floats(int pairs) { return (pairs + 4 * ((pairs - 1) >> 5) + 3) & ~3; }
+__host__ __device__ constexpr int row_floats(int pairs) { return (pairs + 4 * ((pairs - 1) >> 5) + 3) & ~3; }
 
 // Half layout with pairs that do not come in whole chunks; kept out of line for its registers.
 template <typename T>
@@ -295,9 +295,11 @@ cudaError_t launch_write_as(const CacheIo& a, cudaStream_t s, int* launches) {
   const int per = (int64_t)J * a.c.Hk * a.c.N * 2 / kHeads >= ctas_per_wave(4) ? kHeads : 1;
   const dim3 grid(J, 2 * ((a.c.Hk + per - 1) / per), a.c.N);
   const size_t smem = a.rope.turns ? (size_t)min(a.T, a.c.P) * row_floats(a.rope.rot / 2) * 2 * sizeof(float) : 0;
-  cudaError_t e = cudaSuccess;
-  if (smem > 48 * 1024)
-    e = cudaFuncSetAttribute(write_kernel<T, D, F, CH, TH>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  // The most that any rotation and any count of rows need (a page of 128, all channels), once: near
+  // 48 KiB the kernel's own 64 bytes count too, and a limit set per call would be another thread's.
+  constexpr int most = 128 * row_floats(D / 2) * 2 * (int)sizeof(float);
+  static std::atomic<uint64_t> done{0};
+  cudaError_t e = smem ? allow_smem(write_kernel<T, D, F, CH, TH>, most, done) : cudaSuccess;
   if (e != cudaSuccess) return e;
   trace_begin("cache_write", s);
   e = launch_pdl(write_kernel<T, D, F, CH, TH>, grid, dim3(TH), smem, s, a, per);

@@ -4,6 +4,7 @@ import pytest
 
 import hybrid_gated_linear_gb300 as lz
 from cache_gpu_util import Filled, assert_within, attend, bound_of, check_attention, definition, gaussian, on_device
+from test_rope_gpu import make_rope
 
 pytestmark = pytest.mark.gpu
 
@@ -128,3 +129,28 @@ def test_outputs_beside_other_tensors_in_one_buffer(N, T, order):
     assert lz.lizard_check_device_errors(ws) == 0
     for i in range(2):
         assert torch.equal(both[:, i * Hk:(i + 1) * Hk], f.held[i][:, :, 50 - T:])
+
+
+@pytest.mark.parametrize("rot,T", [(82, 130), (84, 128), (88, 300), (114, 96), (120, 96), (128, 300)])
+def test_rotated_writes_of_large_pages(rot, T):
+    """Pages of 128 tokens of 128 channels with any number of rotated channels: the angles' shared
+    memory is near or above what a launch gets without asking."""
+    import numpy as np
+    import torch
+
+    import cache_oracle as co
+    N, Hk, P, d = 2, 2, 128, 128
+    k, v = gaussian((N, Hk, T, d), rot), gaussian((N, Hk, T, d), rot + 1)
+    f = Filled(k, v, [0] * N, [T] * N, P, "e4m3")
+    rope, th = make_rope(rot)
+    ws = torch.zeros(lz.lizard_cache_workspace_bytes(), dtype=torch.uint8, device="cuda")
+    io = lz.lizard_cache_io(T, lz.LIZARD_F32)
+    lz.lizard_cache_write(f.h, io, k, v, rope, on_device([0] * N), None, ws)
+    out = [torch.empty_like(k), torch.empty_like(v)]
+    lz.lizard_cache_read(f.h, io, on_device([0] * N), None, *out, ws)
+    assert lz.lizard_check_device_errors(ws) == 0
+    want = co.rotate(k.cpu().numpy(), np.arange(T), th)
+    scale = f.h._keep[2].cpu().numpy()[f.table.cpu().numpy()[:, np.arange(T) // P]].transpose(0, 2, 1)[..., None]
+    half = np.maximum(np.abs(want) * 2.0 ** -4, scale * 2.0 ** -10) * 1.001 + 2.0 ** -20 * np.abs(want).max()
+    assert (np.abs(out[0].cpu().numpy() - want) <= half).all()
+    assert torch.equal(out[1], f.held[1])
