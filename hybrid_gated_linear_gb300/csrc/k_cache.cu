@@ -10,6 +10,8 @@
 // Both are memory bound where prompts are long and bound by a chain of dependent loads
 // (position, page, row) for single tokens.  Measured, 8 heads of 128, e4m3: four prompts of 4096
 // tokens with rotation, write 60 us (100 MB), read 23 us; one token of 64 sequences, write 8 us.
+#include <algorithm>
+
 #include "kv_cache.cuh"
 
 namespace lz {
@@ -291,7 +293,8 @@ __global__ void __launch_bounds__(kThreads) read_kernel(CacheIo a) {
 
 template <typename T, int D, int F, int CH, int TH>
 cudaError_t launch_write_as(const CacheIo& a, cudaStream_t s, int* launches) {
-  const int J = (a.T + a.c.P - 2) / a.c.P + 1;
+  // pages that T tokens touch; a sequence that needs more than its table holds is refused
+  const int J = (int)std::min(((int64_t)a.T + a.c.P - 2) / a.c.P + 1, (int64_t)a.c.max_pages);
   const int per = (int64_t)J * a.c.Hk * a.c.N * 2 / kHeads >= ctas_per_wave(4) ? kHeads : 1;
   const dim3 grid(J, 2 * ((a.c.Hk + per - 1) / per), a.c.N);
   const size_t smem = a.rope.turns ? (size_t)min(a.T, a.c.P) * row_floats(a.rope.rot / 2) * 2 * sizeof(float) : 0;

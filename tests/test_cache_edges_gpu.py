@@ -154,3 +154,20 @@ def test_rotated_writes_of_large_pages(rot, T):
     half = np.maximum(np.abs(want) * 2.0 ** -4, scale * 2.0 ** -10) * 1.001 + 2.0 ** -20 * np.abs(want).max()
     assert (np.abs(out[0].cpu().numpy() - want) <= half).all()
     assert torch.equal(out[1], f.held[1])
+
+
+def test_rows_that_a_write_repeats_may_be_very_many():
+    """One row seen 2^31 - 1 times through a stride of 0, of which the counts take a few."""
+    import torch
+    row = gaussian((1, 2, 1, 64), 1)
+    f = Filled(gaussian((1, 2, 20, 64), 2), gaussian((1, 2, 20, 64), 3), [0], [20], 16, "e4m3")
+    many = row.expand(1, 2, 2 ** 31 - 1, 64)
+    ws = torch.zeros(lz.lizard_cache_workspace_bytes(), dtype=torch.uint8, device="cuda")
+    lz.lizard_cache_write(f.h, lz.lizard_cache_io(2 ** 31 - 1, lz.LIZARD_F32), many, many, None, on_device([16]),
+                          on_device([3], 32), ws)
+    assert lz.lizard_check_device_errors(ws) == 0
+    g = Filled(row.repeat(1, 1, 3, 1), row.repeat(1, 1, 3, 1), [16], [19], 16, "e4m3", slots=2)
+    out = [torch.empty(1, 2, 19, 64, device="cuda") for _ in "kv"]
+    lz.lizard_cache_read(f.h, lz.lizard_cache_io(19, lz.LIZARD_F32), on_device([0]), None, *out, ws)
+    for o, h, w in zip(out, f.held, g.held):
+        assert torch.equal(o[:, :, :16], h[:, :, :16]) and torch.equal(o[:, :, 16:], w)
