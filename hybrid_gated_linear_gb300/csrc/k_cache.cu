@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(TH, TH == 256 ? 2 : 1) write_kernel(CacheIo a,
   const int64_t p0 = a.pos[n];
   const int cnt = a.count ? a.count[n] : a.T;
   if (cnt == 0) return;
-  const bool bad = cnt < 0 || cnt > a.T || !position_ok(p0) || !span_ok(a.c, p0, p0 + cnt - 1);
+  const bool bad = cnt < 0 || cnt > a.T || p0 < 0 || !span_ok(a.c, p0, last_of(p0, cnt));
   if (bad) {
     if (tid == 0) raise_status(a.status, kDevCheck);
     return;
@@ -262,7 +262,7 @@ __global__ void __launch_bounds__(kThreads) read_kernel(CacheIo a) {
   if (j >= a.T) return;
   const int64_t p0 = a.pos[n];
   const int cnt = a.count ? a.count[n] : a.T;
-  const bool bad = cnt < 0 || cnt > a.T || (cnt > 0 && (!position_ok(p0) || !span_ok(a.c, p0, p0 + cnt - 1)));
+  const bool bad = cnt < 0 || cnt > a.T || (cnt > 0 && (p0 < 0 || !span_ok(a.c, p0, last_of(p0, cnt))));
   if (bad && e == 0) raise_status(a.status, kDevCheck);
   float x[16];
 #pragma unroll

@@ -112,6 +112,9 @@ __device__ __forceinline__ void rope_angle(uint64_t turns, int64_t p, float f, f
 // A position that counts and windows can be added to and taken from.
 __device__ __forceinline__ bool position_ok(int64_t p) { return p >= 0 && p < (1ll << 62); }
 
+// The last of cnt positions from p on; beyond the end of int64 it wraps below p.
+__device__ __forceinline__ int64_t last_of(int64_t p, int cnt) { return (int64_t)((uint64_t)p + (uint64_t)(cnt - 1)); }
+
 // The pages that tokens lo..hi (lo <= hi) of a sequence touch fit its table, positions are
 // not negative and logical pages fit 31 bits.
 __device__ __forceinline__ bool span_ok(const CacheArgs& c, int64_t lo, int64_t hi) {
