@@ -171,3 +171,25 @@ def test_rows_that_a_write_repeats_may_be_very_many():
     lz.lizard_cache_read(f.h, lz.lizard_cache_io(19, lz.LIZARD_F32), on_device([0]), None, *out, ws)
     for o, h, w in zip(out, f.held, g.held):
         assert torch.equal(o[:, :, :16], h[:, :, :16]) and torch.equal(o[:, :, 16:], w)
+
+
+@pytest.mark.parametrize("path", PATHS, ids=IDS)
+def test_logits_in_the_millions(path):
+    """Logits so large that their own rounding is a good part of 1 still give finite outputs, the
+    value of the token they pick where one stands out."""
+    import torch
+    N, H, Hk, d, T, dtype = path
+    L = 500 + T
+    k, v = gaussian((N, Hk, L, d), 1, 300.0), gaussian((N, Hk, L, d), 2)
+    f = Filled(k, v, [0] * N, [L] * N, 32, "e4m3")
+    q = typed(gaussian((N, H, T, d), 3, 3000.0), dtype)
+    y = attend(f, q, [L - T] * N).double()
+    K, V = (x.double().repeat_interleave(H // Hk, 1) for x in f.held)
+    z = q.double() @ K.transpose(2, 3) * d ** -0.5
+    z.masked_fill_(torch.arange(L, device="cuda") > L - T + torch.arange(T, device="cuda")[:, None], -float("inf"))
+    top, at = z.topk(2, -1)
+    clear = (top[..., 0] - top[..., 1] > 2.0 ** -8 * top[..., 0].abs() + 100)
+    want = V.gather(2, at[..., :1].expand(-1, -1, -1, d))
+    assert torch.isfinite(y).all() and clear.any()
+    assert ((y - want).abs() <= 2.0 ** -8 * want.abs())[clear].all()
+    assert (y.abs() <= V.abs().amax(2, keepdim=True) * (1 + 2.0 ** -7)).all()
