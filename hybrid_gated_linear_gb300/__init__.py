@@ -248,8 +248,11 @@ def _ptr(t):
 def _stream(stream):
     if stream is None:
         import torch
-        # the current stream's handle, without the Stream object around it
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        # the current stream's handle; where torch offers it, without the Stream object around it
+        try:
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        except AttributeError:
+            stream = torch.cuda.current_stream()
     handle = getattr(stream, "cuda_stream", stream)
     return ctypes.c_void_p(int(handle))
 

@@ -278,6 +278,21 @@ def test_binding_refuses_host_memory_everywhere():
             lz.lizard_cache_write(cache, io, x, x, rope, pos, None, bad["workspace"], stream=0)
 
 
+def test_current_stream_without_torchs_private_names(monkeypatch):
+    """The shortcut to the current stream's handle is torch's own affair; without it the public
+    call is used."""
+    import torch
+
+    class Stream:
+        cuda_stream = 0x1230
+    monkeypatch.setattr(torch.cuda, "current_stream", Stream)
+    for name in ("_cuda_getCurrentRawStream", "_cuda_getDevice"):
+        with monkeypatch.context() as m:
+            m.delattr(torch._C, name, raising=False)
+            assert lz._stream(None).value == 0x1230
+    assert lz._stream(Stream()).value == 0x1230 and lz._stream(0x50).value == 0x50
+
+
 # ---------------------------------------------------------------------------------------
 # slices of one buffer that share an element
 # ---------------------------------------------------------------------------------------
