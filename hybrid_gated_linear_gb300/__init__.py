@@ -114,7 +114,8 @@ class lizard_rope(ctypes.Structure):
                 ("attn_factor", ctypes.c_float)]
 
     def __init__(self, turns, rot: int, layout: int, attn_factor: float = 1.0):
-        if turns.element_size() != 8 or turns.numel() != rot // 2 or not turns.is_contiguous():
+        if (turns.element_size() != 8 or turns.is_floating_point() or turns.is_complex()
+                or turns.numel() != rot // 2 or not turns.is_contiguous()):
             raise ValueError("turns must be the rot/2 words of lizard_rope_table")
         super().__init__(turns.data_ptr(), rot, layout, attn_factor)
         self._keep = turns
@@ -521,7 +522,7 @@ def _ints(t, shape, size: int):
     if t is None:
         return None
     if (t.shape != shape or not t.is_cuda or not t.is_contiguous() or t.element_size() != size
-            or t.is_floating_point()):
+            or t.is_floating_point() or t.is_complex()):
         raise ValueError(f"expected a contiguous int{8 * size} device tensor of shape {shape}, got "
                          f"{tuple(t.shape)} {t.dtype} on {t.device}")
     return t.data_ptr()

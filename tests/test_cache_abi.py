@@ -278,6 +278,27 @@ def test_binding_refuses_host_memory_everywhere():
             lz.lizard_cache_write(cache, io, x, x, rope, pos, None, bad["workspace"], stream=0)
 
 
+def test_binding_refuses_tables_and_positions_that_are_not_integers():
+    import torch
+
+    class OnDevice:  # a device tensor's checks, without a device
+        is_cuda = True
+
+        def __init__(self, t):
+            self.t = t
+
+        def __getattr__(self, name):
+            return getattr(self.t, name)
+
+    for dtype in (torch.float64, torch.complex64, torch.int32):
+        with pytest.raises(ValueError):
+            lz.lizard_rope(torch.zeros(4, dtype=dtype), 8, 0)
+        with pytest.raises(ValueError):
+            lz._ints(OnDevice(torch.zeros(2, 3, dtype=dtype)), (2, 3), 8)
+    ok = torch.zeros(2, 3, dtype=torch.int64)
+    assert lz._ints(OnDevice(ok), (2, 3), 8) == ok.data_ptr()
+
+
 def test_current_stream_without_torchs_private_names(monkeypatch):
     """The shortcut to the current stream's handle is torch's own affair; without it the public
     call is used."""
