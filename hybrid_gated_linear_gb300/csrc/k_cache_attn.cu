@@ -22,9 +22,10 @@
 // would be an eighth full, and the tensor time is a third of the copy time.
 //
 // Measured, H = 32, Hk = 8, D = 128, one new token, e4m3 (share of the measured copy rate):
-//   64 sequences of 8192 tokens 184 us (86%), of 128 to 8192 106 us (76%); one of 131072
-//   tokens 56 us (70%); 64 x 32 heads, windows of 1024, bytes 116 us (67%); one sequence of
-//   500 tokens 13 us.
+//   64 sequences of 8192 tokens 183 us (86%), of 128 to 8192 106 us (75%), in fp32 135 us; one
+//   of 131072 tokens 56 us (70%), in fp32 65; 64 x 32 heads, windows of 1024, bytes 117 us (67%),
+//   e4m3 101; one sequence of 500 tokens 12 us.  Many rows in fp32 (T = 512, two sequences at 3000:
+//   506 us; T = 2048 at 14336: 8.0 ms, 130 TFLOP/s) are bound by their two-part products.
 // The loop runs at 6.7 TB/s; the rest is the start (positions, pages, first copies: about 6 us)
 // and the end of the slowest warp and the joins after it (10 to 20 us).
 #include <algorithm>

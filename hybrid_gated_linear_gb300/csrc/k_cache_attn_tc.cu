@@ -22,9 +22,9 @@
 // all (sequence, rows, head), whatever their lengths; where a share ends inside one, its parts
 // are joined by the last CTA to finish (fixed order: results do not depend on timing).
 //
-// Measured, H = 32, Hk = 8, D = 128, e4m3: two sequences, 2048 new tokens at 14336: 1.07 ms,
-// 960 TFLOP/s (49% of the measured bf16 burst; bytes 1.28 ms, their conversion takes twice the
-// operations).  With the row warps' work left out 1.01, with the conversions left out 0.87, with
+// Measured, H = 32, Hk = 8, D = 128, e4m3: two sequences, 2048 new tokens at 14336: 1.08 ms,
+// 957 TFLOP/s (48% of the measured bf16 burst; bytes 1.23 ms, their conversion takes twice the
+// operations; D = 64 0.95 ms, the same exponentials for half the products).  With the row warps' work left out 1.01, with the conversions left out 0.87, with
 // both 0.64 ms: the roles contend for issue slots and shared memory, which the operands alone
 // keep three quarters busy.  Staging the queries and joining parts cost about 80 us of it.
 #include <algorithm>

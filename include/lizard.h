@@ -506,6 +506,9 @@ typedef struct lizard_cache_io {
  * int64, count [N] int32.  A page whose first row is written starts afresh; a page that
  * already holds earlier tokens keeps the larger of its scale and the new tokens' one, its
  * codes rounded again when the scale grows; rows after the last written token are dead.
+ * (So the codes depend on how tokens were grouped into calls, and a page rewritten from an
+ * earlier row keeps the scale of tokens that are gone.  Where a sequence starts inside a page,
+ * set that page's scales to 0 first: nothing was written there that they could belong to.)
  * The same page must not be written for two sequences in one call.  NaN is stored as 0 and
  * an infinity as the largest code, and both set LIZARD_ERR_DEVICE_CHECK; so does a sequence
  * whose tokens span more than max_pages pages, a negative position, a count outside 0..T or
@@ -546,10 +549,10 @@ lizard_status lizard_cache_read(const lizard_cache* cache, const lizard_cache_io
  * probabilities to 11 bits for the tensor cores, fp32 calls carry them in two such parts.  A
  * probability is held to 2^-31 (bf16 calls) or 2^-37 of the largest (value scale included)
  * that its row has met.  Run-to-run identical.
- * Workspace: at least lizard_cache_attn_workspace_bytes, zero before the first call.  Calls of
- * this function ordered one after the other may share one, whatever their shapes, if it is large
- * enough for each; calls that may run at the same time need their own.  After
- * LIZARD_ERR_TIMEOUT it has to be set to zero again.
+ * Workspace: at least lizard_cache_attn_workspace_bytes, zero before the first call
+ * (lizard_workspace_init does that).  Calls of this function ordered one after the other may
+ * share one, whatever their shapes, if it is large enough for each; calls that may run at the
+ * same time need their own.  After LIZARD_ERR_TIMEOUT it has to be set to zero again.
  */
 typedef struct lizard_cache_attn_dims {
     int32_t H;             /* query heads, a multiple of the cache's Hk */
