@@ -34,6 +34,9 @@ __all__ = [
     "LIZARD_ROPE_LINEAR", "LIZARD_ROPE_PARTS", "lizard_strides", "lizard_cache", "lizard_cache_io",
     "lizard_cache_workspace_bytes", "lizard_cache_write", "lizard_cache_read",
     "lizard_cache_attn_dims", "lizard_cache_attn_workspace_bytes", "lizard_cache_attn",
+    "lizard_decay_dims", "lizard_decay_attn_workspace_bytes", "lizard_decay_attn_fwd",
+    "lizard_decay_attn_bwd", "lizard_decay_attn_step", "lizard_norm_dims",
+    "lizard_layer_norm_workspace_bytes", "lizard_layer_norm_fwd", "lizard_layer_norm_bwd",
     "LIZARD_KV_E4M3", "LIZARD_KV_I8", "LIZARD_F32", "LIZARD_BF16", "EXPORTED_SYMBOLS",
 ]
 
@@ -60,7 +63,9 @@ EXPORTED_SYMBOLS = (
     "lizard_gate_workspace_bytes", "lizard_gla_std_fwd", "lizard_gla_std_workspace_bytes",
     "lizard_rope_table", "lizard_rope_fwd", "lizard_rope_bwd", "lizard_cache_workspace_bytes",
     "lizard_cache_write", "lizard_cache_read", "lizard_cache_attn_workspace_bytes",
-    "lizard_cache_attn",
+    "lizard_cache_attn", "lizard_decay_attn_workspace_bytes", "lizard_decay_attn_fwd",
+    "lizard_decay_attn_bwd", "lizard_decay_attn_step", "lizard_layer_norm_workspace_bytes",
+    "lizard_layer_norm_fwd", "lizard_layer_norm_bwd",
 )
 
 STATUS_NAMES = {0: "LIZARD_OK", 1: "LIZARD_ERR_INVALID_ARG", 2: "LIZARD_ERR_UNSUPPORTED",
@@ -164,6 +169,18 @@ class lizard_cache_attn_dims(ctypes.Structure):
                 ("alpha", ctypes.c_float)]
 
 
+class lizard_decay_dims(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("H", ctypes.c_int32), ("Hk", ctypes.c_int32),
+                ("L", ctypes.c_int32), ("dk", ctypes.c_int32), ("dv", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class lizard_norm_dims(ctypes.Structure):
+    _fields_ = [("N", ctypes.c_int32), ("H", ctypes.c_int32), ("T", ctypes.c_int32),
+                ("d", ctypes.c_int32), ("per_head", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("eps", ctypes.c_float)]
+
+
 _lock = threading.Lock()
 _lib = None
 
@@ -226,6 +243,13 @@ def library():
                 "lizard_cache_read": (I32, [P] * 9 + [SZ, P]),
                 "lizard_cache_attn_workspace_bytes": (SZ, [P, P]),
                 "lizard_cache_attn": (I32, [P] * 15 + [SZ, P]),
+                "lizard_decay_attn_workspace_bytes": (SZ, [P, I32]),
+                "lizard_decay_attn_fwd": (I32, [P] * 15 + [SZ, P]),
+                "lizard_decay_attn_bwd": (I32, [P] * 23 + [SZ, P]),
+                "lizard_decay_attn_step": (I32, [P] * 13),
+                "lizard_layer_norm_workspace_bytes": (SZ, [P]),
+                "lizard_layer_norm_fwd": (I32, [P] * 8),
+                "lizard_layer_norm_bwd": (I32, [P] * 11 + [SZ, P]),
             }
             for name, (res, args) in sig.items():
                 fn = getattr(lib, name)
@@ -626,3 +650,112 @@ def lizard_cache_attn(cache: lizard_cache, dims: lizard_cache_attn_dims, q, rope
         *_rows(y_add, shape, dims.dtype), *_rows(y, shape, dims.dtype),
         *_workspace(workspace), _stream(stream))
     _check(st, "lizard_cache_attn")
+
+
+# ------------------------------------------------------------------------------------
+# linear attention with a decay per head, and layer norm
+# ------------------------------------------------------------------------------------
+def _floats(t, shape):
+    """Pointer of a contiguous fp32 device tensor (None -> NULL)."""
+    if t is None:
+        return None
+    if t.shape != shape or not t.is_cuda or not t.is_contiguous() or _dtype_code(t) != LIZARD_F32:
+        raise ValueError(f"expected a contiguous float32 device tensor of shape {shape}, got "
+                         f"{tuple(t.shape)} {t.dtype} on {t.device}")
+    return t.data_ptr()
+
+
+def _decays(t, shape):
+    """Pointer and strides (None when contiguous) of a [B,H,L] fp32 device tensor of any strides."""
+    if t is None:
+        return None, None
+    if t.shape != shape or not t.is_cuda or _dtype_code(t) != LIZARD_F32:
+        raise ValueError(f"expected a float32 device tensor of shape {shape}, got "
+                         f"{tuple(t.shape)} {t.dtype} on {t.device}")
+    return t.data_ptr(), None if t.is_contiguous() else ctypes.byref(lizard_strides(*t.stride()))
+
+
+def _decay_inputs(d, q, k, v, log_decay):
+    return (*_rows(q, (d.B, d.H, d.L, d.dk), d.dtype), *_rows(k, (d.B, d.Hk, d.L, d.dk), d.dtype),
+            *_rows(v, (d.B, d.Hk, d.L, d.dv), d.dtype), *_decays(log_decay, (d.B, d.H, d.L)))
+
+
+def lizard_decay_attn_workspace_bytes(dims: lizard_decay_dims, is_bwd: bool) -> int:
+    return library().lizard_decay_attn_workspace_bytes(_ref(dims), int(bool(is_bwd)))
+
+
+def lizard_decay_attn_fwd(dims: lizard_decay_dims, q, k, v, log_decay, count, h0, y, h_final, workspace,
+                          stream=None):
+    """y (and h_final [B,H,dk,dv], unless None) of the linear attention with one decay per head and
+    token: q [B,H,L,dk], k [B,Hk,L,dk], v [B,Hk,L,dv], y [B,H,L,dv] and log_decay [B,H,L] may be
+    strided; count [B] int32 (None: L tokens each), h0 (None: zeros)."""
+    d = dims
+    state = (d.B, d.H, d.dk, d.dv)
+    st = library().lizard_decay_attn_fwd(
+        _ref(d), *_decay_inputs(d, q, k, v, log_decay), _ints(count, (d.B,), 4), _floats(h0, state),
+        *_rows(y, (d.B, d.H, d.L, d.dv), d.dtype), _floats(h_final, state), *_workspace(workspace),
+        _stream(stream))
+    _check(st, "lizard_decay_attn_fwd")
+
+
+def lizard_decay_attn_bwd(dims: lizard_decay_dims, q, k, v, log_decay, count, h0, dy, d_h_final, d_q, d_k,
+                          d_v, d_log_decay, d_h0, workspace, stream=None):
+    """Gradients of lizard_decay_attn_fwd from those of y and of h_final (None: zeros); d_log_decay
+    [B,H,L] fp32 and d_h0 may be None."""
+    d = dims
+    state = (d.B, d.H, d.dk, d.dv)
+    st = library().lizard_decay_attn_bwd(
+        _ref(d), *_decay_inputs(d, q, k, v, log_decay), _ints(count, (d.B,), 4), _floats(h0, state),
+        *_rows(dy, (d.B, d.H, d.L, d.dv), d.dtype), _floats(d_h_final, state),
+        *_rows(d_q, (d.B, d.H, d.L, d.dk), d.dtype), *_rows(d_k, (d.B, d.Hk, d.L, d.dk), d.dtype),
+        *_rows(d_v, (d.B, d.Hk, d.L, d.dv), d.dtype), _floats(d_log_decay, (d.B, d.H, d.L)),
+        _floats(d_h0, state), *_workspace(workspace), _stream(stream))
+    _check(st, "lizard_decay_attn_bwd")
+
+
+def lizard_decay_attn_step(dims: lizard_decay_dims, q, k, v, log_decay, h, y, stream=None):
+    """The recurrent form: dims.L new tokens of every sequence (one as a rule) into y, the states
+    h [B,H,dk,dv] fp32 updated in place."""
+    d = dims
+    st = library().lizard_decay_attn_step(
+        _ref(d), *_decay_inputs(d, q, k, v, log_decay), _floats(h, (d.B, d.H, d.dk, d.dv)),
+        *_rows(y, (d.B, d.H, d.L, d.dv), d.dtype), _stream(stream))
+    _check(st, "lizard_decay_attn_step")
+
+
+def _norm_weight(t, d):
+    if t is None:
+        return None
+    shape = (d.H, d.d) if d.per_head else (d.d,)
+    if t.shape != shape or not t.is_cuda or not t.is_contiguous() or _dtype_code(t) != d.dtype:
+        raise ValueError(f"expected a contiguous device tensor of shape {shape} in the call's element type, "
+                         f"got {tuple(t.shape)} {t.dtype} on {t.device}")
+    return t.data_ptr()
+
+
+def lizard_layer_norm_workspace_bytes(dims: lizard_norm_dims) -> int:
+    return library().lizard_layer_norm_workspace_bytes(_ref(dims))
+
+
+def lizard_layer_norm_fwd(dims: lizard_norm_dims, x, weight, bias, y, stream=None):
+    """Layer norm of the rows of x [N,H,T,d] into y (which may be x); weight and bias [d], or [H,d]
+    with dims.per_head, or None.  x and y may be strided."""
+    d = dims
+    shape = (d.N, d.H, d.T, d.d)
+    st = library().lizard_layer_norm_fwd(
+        _ref(d), *_rows(x, shape, d.dtype), _norm_weight(weight, d), _norm_weight(bias, d),
+        *_rows(y, shape, d.dtype), _stream(stream))
+    _check(st, "lizard_layer_norm_fwd")
+
+
+def lizard_layer_norm_bwd(dims: lizard_norm_dims, x, weight, dy, d_x, d_weight, d_bias, workspace, stream=None):
+    """Gradients of lizard_layer_norm_fwd: d_x (may be x or dy) and, in fp32 and summed over all rows,
+    d_weight and d_bias; any of the three may be None."""
+    d = dims
+    shape = (d.N, d.H, d.T, d.d)
+    wshape = (d.H, d.d) if d.per_head else (d.d,)
+    st = library().lizard_layer_norm_bwd(
+        _ref(d), *_rows(x, shape, d.dtype), _norm_weight(weight, d), *_rows(dy, shape, d.dtype),
+        *_rows(d_x, shape, d.dtype), _floats(d_weight, wshape), _floats(d_bias, wshape),
+        *_workspace(workspace), _stream(stream))
+    _check(st, "lizard_layer_norm_bwd")

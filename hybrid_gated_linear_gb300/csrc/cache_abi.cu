@@ -4,113 +4,13 @@
 #include <stdint.h>
 
 #include <algorithm>
-#include <utility>
 
+#include "abi_rows.h"
 #include "lizard_internal.h"
 
 namespace {
 
-size_t elem_size(lizard_dtype t) { return t == LIZARD_F32 ? 4 : 2; }
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool ptr_ok(const void* p, bool optional) { return p ? aligned16(p) : optional; }
-bool dtype_ok(lizard_dtype t) { return t == LIZARD_F32 || t == LIZARD_BF16; }
-constexpr int64_t kMaxExtent = 1ll << 46;  // elements a strided tensor may span
-
-// A strided [N,H,T,d] tensor: its strides and the bytes from its first to past its last
-// element.
-struct Rows {
-  lz::Strides s{};
-  size_t bytes = 0;
-  bool ok = false;
-};
-
-Rows rows_of(const lizard_strides* s, int64_t N, int64_t H, int64_t T, int64_t d, lizard_dtype dt,
-             bool output) {
-  Rows r;
-  if (!s) {
-    r.s = {H * T * d, T * d, d};
-  } else {
-    r.s = {s->n, s->h, s->t};
-    const int64_t dim[3] = {N, H, T}, st[3] = {s->n, s->h, s->t};
-    const int64_t unit = 16 / (int64_t)elem_size(dt);
-    for (int i = 0; i < 3; ++i) {
-      if (dim[i] <= 1) continue;  // never stepped over
-      if (st[i] < 0 || st[i] % unit || st[i] > kMaxExtent) return r;
-      if (output && st[i] < d) return r;
-    }
-    if (output) {
-      // distinct elements: sorted by stride, each axis steps past all of the smaller ones
-      std::pair<int64_t, int64_t> axes[3];
-      int k = 0;
-      for (int i = 0; i < 3; ++i)
-        if (dim[i] > 1) axes[k++] = {st[i], dim[i]};
-      std::sort(axes, axes + k);
-      int64_t span = d;
-      for (int i = 0; i < k; ++i) {
-        if (axes[i].first < span || axes[i].second > kMaxExtent / axes[i].first) return r;
-        span += axes[i].first * (axes[i].second - 1);
-      }
-    }
-  }
-  const __int128 span = (__int128)(N > 1 ? (N - 1) * (__int128)r.s.n : 0) +
-                        (H > 1 ? (H - 1) * (__int128)r.s.h : 0) +
-                        (T > 1 ? (T - 1) * (__int128)r.s.t : 0) + d;
-  if (span > kMaxExtent) return r;
-  r.bytes = N && H && T ? (size_t)span * elem_size(dt) : 0;
-  r.ok = true;
-  return r;
-}
-
-struct Span {
-  const void* p;
-  size_t n;
-};
-bool overlap(const Span& a, const Span& b) {
-  if (!a.p || !b.p || !a.n || !b.n) return false;
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
-  return x < y + b.n && y < x + a.n;
-}
-bool any_overlap(const Span* outs, int no, const Span* ins, int ni) {
-  for (int i = 0; i < no; ++i) {
-    for (int j = 0; j < ni; ++j)
-      if (overlap(outs[i], ins[j])) return true;
-    for (int j = i + 1; j < no; ++j)
-      if (overlap(outs[i], outs[j])) return true;
-  }
-  return false;
-}
-
-// Two strided tensors share no element: their spans are apart, or, counted modulo the stride of
-// some axis of either, what each covers lies beside the other (slices of one packed projection:
-// of its heads, whichever axis is outermost).
-struct Tensor {
-  const void* p;
-  const Rows* r;
-  int64_t N, H, T, d, es;
-};
-bool apart(const Tensor& a, const Tensor& b) {
-  if (!overlap(Span{a.p, a.r->bytes}, Span{b.p, b.r->bytes})) return true;
-  const int64_t off = static_cast<const char*>(b.p) - static_cast<const char*>(a.p);
-  for (const Tensor* x : {&a, &b}) {
-    const int64_t dim[3] = {x->N, x->H, x->T}, stride[3] = {x->r->s.n, x->r->s.h, x->r->s.t};
-    for (int i = 0; i < 3; ++i) {
-      if (dim[i] <= 1 || stride[i] <= 0) continue;
-      // bytes from the first element on, steps of a multiple of the stride left out
-      auto width = [&](const Tensor& t) {
-        const int64_t td[3] = {t.N, t.H, t.T}, ts[3] = {t.r->s.n, t.r->s.h, t.r->s.t};
-        int64_t w = t.d;
-        for (int k = 0; k < 3; ++k)
-          if (td[k] > 1 && ts[k] % stride[i]) w += (td[k] - 1) * ts[k];
-        return w * t.es;
-      };
-      const int64_t step = stride[i] * a.es, at = (off % step + step) % step;
-      if (width(a) <= at && at + width(b) <= step) return true;
-    }
-  }
-  return false;
-}
-
-bool same(const lz::Strides& a, const lz::Strides& b) { return a.n == b.n && a.h == b.h && a.t == b.t; }
+using namespace lz::abi;
 
 // null `rope` means no rotation.
 bool rope_ok(const lizard_rope* rope, int d, lz::RopeArgs* out) {
@@ -147,11 +47,6 @@ void cache_spans(const lz::CacheArgs& c, Span (&s)[5]) {
   const size_t codes = (size_t)c.pages * c.Hk * c.P * c.d, scales = (size_t)c.pages * c.Hk * sizeof(float);
   s[0] = {c.k, codes}, s[1] = {c.v, codes}, s[2] = {c.ks, scales}, s[3] = {c.vs, scales};
   s[4] = {c.table, (size_t)c.N * c.max_pages * sizeof(int32_t)};
-}
-
-lizard_status finish(cudaError_t e, int launches) {
-  lz::set_last_launches(launches);
-  return e == cudaSuccess ? LIZARD_OK : LIZARD_ERR_CUDA;
 }
 
 lizard_status rope_call(const lizard_rope_dims* dims, const lizard_rope* rope, float sign, const void* x_q,

@@ -1,0 +1,354 @@
+// decay_abi.cu -- C entry points of the linear attention with a decay per head and of layer norm:
+// validation of every argument, then the passes.
+#include <math.h>
+#include <stdint.h>
+
+#include "abi_rows.h"
+#include "lizard_internal.h"
+
+namespace {
+
+using namespace lz::abi;
+
+bool decay_dims_ok(const lizard_decay_dims* d) {
+  return d && d->B >= 1 && d->B <= 65535 && d->H >= 1 && d->Hk >= 1 && d->H % d->Hk == 0 && d->L >= 0 &&
+         dtype_ok(d->dtype) && isfinite(d->scale) && (__int128)d->B * d->H < (1 << 28) &&
+         (__int128)d->B * d->H * d->L < (1ll << 31);
+}
+bool width_ok(int d) { return d == 64 || d == 128; }
+
+float scale_of(const lizard_decay_dims& d) { return d.scale > 0.f ? d.scale : 1.0f / sqrtf((float)d.dk); }
+
+// Decays are read one by one: any fp32 address will do (a slice of a longer row).
+bool decay_ptr_ok(const float* p, bool optional) {
+  return p ? (reinterpret_cast<uintptr_t>(p) & 3u) == 0 : optional;
+}
+
+// The decays' strides and the bytes they span.
+struct Decays {
+  lz::Strides s{};
+  size_t bytes = 0;
+  bool ok = false;
+};
+Decays decays_of(const lizard_strides* s, int64_t B, int64_t H, int64_t L) {
+  Decays r;
+  r.s = s ? lz::Strides{s->n, s->h, s->t} : lz::Strides{H * L, L, 1};
+  const int64_t dim[3] = {B, H, L}, st[3] = {r.s.n, r.s.h, r.s.t};
+  __int128 span = 1;
+  for (int i = 0; i < 3; ++i) {
+    if (dim[i] <= 1) continue;
+    if (st[i] < 0 || st[i] > kMaxExtent) return r;
+    span += (dim[i] - 1) * (__int128)st[i];
+  }
+  if (span > kMaxExtent) return r;
+  r.bytes = L ? (size_t)span * sizeof(float) : 0;
+  r.ok = true;
+  return r;
+}
+
+// Scratch of a backward call after the header.
+struct BwdScratch {
+  size_t dots, parts, d_h0, bytes;  // offsets, then the size
+};
+BwdScratch bwd_scratch(const lizard_decay_dims& d) {
+  BwdScratch w;
+  const size_t rows = (size_t)d.B * d.H * d.L, slices = d.dk / lz::kDecaySlice;
+  size_t at = 0;
+  w.dots = at, at += lz::align_up(4 * slices * rows * sizeof(float), 256);
+  w.parts = at, at += d.H > d.Hk ? lz::align_up(rows * (d.dk > d.dv ? d.dk : d.dv) * sizeof(float), 256) : 0;
+  w.d_h0 = at, at += (size_t)d.B * d.H * d.dk * d.dv * sizeof(float);
+  w.bytes = at;
+  return w;
+}
+
+bool norm_dims_ok(const lizard_norm_dims* d) {
+  return d && d->N >= 1 && d->H >= 1 && d->T >= 0 && (d->per_head == 0 || d->per_head == 1) && dtype_ok(d->dtype) &&
+         isfinite(d->eps) && (__int128)d->N * d->H * d->T < (1ll << 31) && (!d->per_head || d->H <= 65535);
+}
+bool norm_width_ok(int d) { return d >= 8 && d <= 16384 && d % 8 == 0; }
+
+}  // namespace
+
+extern "C" {
+
+size_t lizard_decay_attn_workspace_bytes(const lizard_decay_dims* dims, int32_t is_bwd) {
+  if (!decay_dims_ok(dims) || !width_ok(dims->dk) || !width_ok(dims->dv)) return 0;
+  return lz::kWsHeader + (is_bwd ? bwd_scratch(*dims).bytes : 0);
+}
+
+lizard_status lizard_decay_attn_fwd(const lizard_decay_dims* dims, const void* q, const lizard_strides* s_q,
+                                    const void* k, const lizard_strides* s_k, const void* v,
+                                    const lizard_strides* s_v, const float* log_decay,
+                                    const lizard_strides* s_decay, const int32_t* count, const float* h0, void* y,
+                                    const lizard_strides* s_y, float* h_final, void* workspace,
+                                    size_t workspace_bytes, void* stream) {
+  lz::set_last_launches(0);
+  if (!decay_dims_ok(dims)) return LIZARD_ERR_INVALID_ARG;
+  const lizard_decay_dims& d = *dims;
+  if (!width_ok(d.dk) || !width_ok(d.dv)) return LIZARD_ERR_UNSUPPORTED;
+  const bool none = d.L == 0;
+  if (!ptr_ok(q, none) || !ptr_ok(k, none) || !ptr_ok(v, none) || !decay_ptr_ok(log_decay, none) || !ptr_ok(y, none) ||
+      !ptr_ok(count, true) || !ptr_ok(h0, true) || !ptr_ok(h_final, true))
+    return LIZARD_ERR_INVALID_ARG;
+  const Rows rq = rows_of(s_q, d.B, d.H, d.L, d.dk, d.dtype, false);
+  const Rows rk = rows_of(s_k, d.B, d.Hk, d.L, d.dk, d.dtype, false);
+  const Rows rv = rows_of(s_v, d.B, d.Hk, d.L, d.dv, d.dtype, false);
+  const Rows ry = rows_of(s_y, d.B, d.H, d.L, d.dv, d.dtype, true);
+  const Decays rg = decays_of(s_decay, d.B, d.H, d.L);
+  if (!rq.ok || !rk.ok || !rv.ok || !ry.ok || !rg.ok) return LIZARD_ERR_INVALID_ARG;
+  if (!workspace || !aligned16(workspace) || workspace_bytes < lizard_decay_attn_workspace_bytes(dims, 0))
+    return LIZARD_ERR_WORKSPACE;
+  const int64_t es = (int64_t)elem_size(d.dtype);
+  const size_t states = (size_t)d.B * d.H * d.dk * d.dv * sizeof(float);
+  const Span outs[] = {{h_final, states}, {workspace, workspace_bytes}};
+  const Span rows[] = {{q, rq.bytes}, {k, rk.bytes}, {v, rv.bytes}, {y, ry.bytes}};
+  const Span ins[] = {{log_decay, rg.bytes}, {count, (size_t)d.B * 4}, {h0, states}};
+  const Tensor ty{y, &ry, d.B, d.H, d.L, d.dv, es}, tq{q, &rq, d.B, d.H, d.L, d.dk, es};
+  const Tensor tk{k, &rk, d.B, d.Hk, d.L, d.dk, es}, tv{v, &rv, d.B, d.Hk, d.L, d.dv, es};
+  if (any_overlap(outs, 2, rows, 4) || any_overlap(outs, 2, ins, 3) || any_overlap(rows + 3, 1, ins, 3) ||
+      !apart(ty, tq) || !apart(ty, tk) || !apart(ty, tv))
+    return LIZARD_ERR_INVALID_ARG;
+  if (none && !h_final) return LIZARD_OK;
+  const int G = d.H / d.Hk;
+  lz::DecayPass a{};
+  a.B = d.B, a.H = d.H, a.L = d.L, a.da = d.dk, a.dc = d.dv;
+  a.a = q, a.b = k, a.c = v, a.sa = rq.s, a.sb = rk.s, a.sc = rv.s, a.ga = 1, a.gb = G, a.gc = G;
+  a.lg = log_decay, a.sg = rg.s, a.count = count;
+  a.init = h0, a.fin = h_final;
+  a.out = y, a.so = ry.s;
+  a.scale_out = scale_of(d), a.scale_in = 1.f;
+  a.status = static_cast<unsigned*>(workspace);
+  int launches = 0;
+  const cudaError_t e = lz::launch_decay_simt(a, d.dtype, (cudaStream_t)stream, &launches);
+  return finish(e, launches);
+}
+
+lizard_status lizard_decay_attn_bwd(const lizard_decay_dims* dims, const void* q, const lizard_strides* s_q,
+                                    const void* k, const lizard_strides* s_k, const void* v,
+                                    const lizard_strides* s_v, const float* log_decay,
+                                    const lizard_strides* s_decay, const int32_t* count, const float* h0,
+                                    const void* dy, const lizard_strides* s_dy, const float* d_h_final, void* d_q,
+                                    const lizard_strides* s_dq, void* d_k, const lizard_strides* s_dk, void* d_v,
+                                    const lizard_strides* s_dv, float* d_log_decay, float* d_h0, void* workspace,
+                                    size_t workspace_bytes, void* stream) {
+  lz::set_last_launches(0);
+  if (!decay_dims_ok(dims)) return LIZARD_ERR_INVALID_ARG;
+  const lizard_decay_dims& d = *dims;
+  if (!width_ok(d.dk) || !width_ok(d.dv)) return LIZARD_ERR_UNSUPPORTED;
+  const bool none = d.L == 0;
+  if (!ptr_ok(q, none) || !ptr_ok(k, none) || !ptr_ok(v, none) || !decay_ptr_ok(log_decay, none) || !ptr_ok(dy, none) ||
+      !ptr_ok(d_q, none) || !ptr_ok(d_k, none) || !ptr_ok(d_v, none) || !ptr_ok(count, true) || !ptr_ok(h0, true) ||
+      !ptr_ok(d_h_final, true) || !ptr_ok(d_log_decay, true) || !ptr_ok(d_h0, true))
+    return LIZARD_ERR_INVALID_ARG;
+  const Rows rq = rows_of(s_q, d.B, d.H, d.L, d.dk, d.dtype, false);
+  const Rows rk = rows_of(s_k, d.B, d.Hk, d.L, d.dk, d.dtype, false);
+  const Rows rv = rows_of(s_v, d.B, d.Hk, d.L, d.dv, d.dtype, false);
+  const Rows ry = rows_of(s_dy, d.B, d.H, d.L, d.dv, d.dtype, false);
+  const Rows oq = rows_of(s_dq, d.B, d.H, d.L, d.dk, d.dtype, true);
+  const Rows ok = rows_of(s_dk, d.B, d.Hk, d.L, d.dk, d.dtype, true);
+  const Rows ov = rows_of(s_dv, d.B, d.Hk, d.L, d.dv, d.dtype, true);
+  const Decays rg = decays_of(s_decay, d.B, d.H, d.L);
+  if (!rq.ok || !rk.ok || !rv.ok || !ry.ok || !oq.ok || !ok.ok || !ov.ok || !rg.ok) return LIZARD_ERR_INVALID_ARG;
+  if (!workspace || !aligned16(workspace) || workspace_bytes < lizard_decay_attn_workspace_bytes(dims, 1))
+    return LIZARD_ERR_WORKSPACE;
+  const int64_t es = (int64_t)elem_size(d.dtype);
+  const size_t states = (size_t)d.B * d.H * d.dk * d.dv * sizeof(float);
+  const Span flat[] = {{d_log_decay, (size_t)d.B * d.H * d.L * 4}, {d_h0, states}, {workspace, workspace_bytes}};
+  const Span rows[] = {{q, rq.bytes},   {k, rk.bytes},   {v, rv.bytes},  {dy, ry.bytes},
+                       {d_q, oq.bytes}, {d_k, ok.bytes}, {d_v, ov.bytes}};
+  const Span ins[] = {{log_decay, rg.bytes}, {count, (size_t)d.B * 4}, {h0, states}, {d_h_final, states}};
+  const Tensor in[] = {{q, &rq, d.B, d.H, d.L, d.dk, es},
+                       {k, &rk, d.B, d.Hk, d.L, d.dk, es},
+                       {v, &rv, d.B, d.Hk, d.L, d.dv, es},
+                       {dy, &ry, d.B, d.H, d.L, d.dv, es}};
+  const Tensor out[] = {{d_q, &oq, d.B, d.H, d.L, d.dk, es},
+                        {d_k, &ok, d.B, d.Hk, d.L, d.dk, es},
+                        {d_v, &ov, d.B, d.Hk, d.L, d.dv, es}};
+  if (any_overlap(flat, 3, rows, 7) || any_overlap(flat, 3, ins, 4)) return LIZARD_ERR_INVALID_ARG;
+  for (int i = 0; i < 3; ++i) {
+    const Span s{out[i].p, out[i].r->bytes};
+    for (const Span& x : ins)
+      if (overlap(s, x)) return LIZARD_ERR_INVALID_ARG;
+    for (const Tensor& x : in)
+      if (!apart(out[i], x)) return LIZARD_ERR_INVALID_ARG;
+    for (int j = i + 1; j < 3; ++j)
+      if (!apart(out[i], out[j])) return LIZARD_ERR_INVALID_ARG;
+  }
+  if (none && !d_h0) return LIZARD_OK;
+  const int G = d.H / d.Hk;
+  const float scale = scale_of(d);
+  const BwdScratch w = bwd_scratch(d);
+  unsigned char* ws = static_cast<unsigned char*>(workspace) + lz::kWsHeader;
+  const size_t plane = (size_t)d.B * d.H * d.L * (d.dk / lz::kDecaySlice);
+  float* dots = reinterpret_cast<float*>(ws + w.dots);
+  float* part = reinterpret_cast<float*>(ws + w.parts);
+  const cudaStream_t s = (cudaStream_t)stream;
+  const bool gate = d_log_decay && !none;
+  if (!d_h0 && h0 && gate) d_h0 = reinterpret_cast<float*>(ws + w.d_h0);
+  int launches = 0;
+  lz::DecayPass a{};
+  a.B = d.B, a.H = d.H, a.L = d.L, a.lg = log_decay, a.sg = rg.s, a.count = count;
+  a.status = static_cast<unsigned*>(workspace);
+  // d_v: (k, q, dy) reversed; its state is dh, and leaves as d_h0
+  lz::DecayPass b = a;
+  b.da = d.dk, b.dc = d.dv, b.rev = true;
+  b.a = k, b.b = q, b.c = dy, b.sa = rk.s, b.sb = rq.s, b.sc = ry.s, b.ga = G, b.gb = b.gc = 1;
+  b.init = d_h_final, b.fin = d_h0;
+  b.scale_out = 1.f, b.scale_in = scale;
+  const lz::Strides heads_v{(int64_t)d.H * d.L * d.dv, (int64_t)d.L * d.dv, d.dv};
+  b.out = G > 1 ? static_cast<void*>(part) : d_v, b.so = G > 1 ? heads_v : ov.s, b.out_f32 = G > 1;
+  cudaError_t e = lz::launch_decay_simt(b, d.dtype, s, &launches);
+  if (e != cudaSuccess || none) return finish(e, launches);
+  if (G > 1) e = lz::launch_decay_heads(d.B, d.Hk, G, d.L, d.dv, part, d_v, ov.s, d.dtype, s, &launches);
+  if (e != cudaSuccess) return finish(e, launches);
+  // d_k: (v, dy, q) reversed; its state is dh transposed
+  b = a;
+  b.da = d.dv, b.dc = d.dk, b.rev = true;
+  b.a = v, b.b = dy, b.c = q, b.sa = rv.s, b.sb = ry.s, b.sc = rq.s, b.ga = G, b.gb = b.gc = 1;
+  b.init = d_h_final, b.state_t = true;
+  b.scale_out = 1.f, b.scale_in = scale;
+  const lz::Strides heads_k{(int64_t)d.H * d.L * d.dk, (int64_t)d.L * d.dk, d.dk};
+  b.out = G > 1 ? static_cast<void*>(part) : d_k, b.so = G > 1 ? heads_k : ok.s, b.out_f32 = G > 1;
+  if (gate) b.x = k, b.sx = rk.s, b.gx = G, b.dot_in = dots, b.dot_out = dots + plane;
+  e = lz::launch_decay_simt(b, d.dtype, s, &launches);
+  if (e == cudaSuccess && G > 1)
+    e = lz::launch_decay_heads(d.B, d.Hk, G, d.L, d.dk, part, d_k, ok.s, d.dtype, s, &launches);
+  if (e != cudaSuccess) return finish(e, launches);
+  // d_q: (dy, v, k) forward; its state is h transposed
+  b = a;
+  b.da = d.dv, b.dc = d.dk;
+  b.a = dy, b.b = v, b.c = k, b.sa = ry.s, b.sb = rv.s, b.sc = rk.s, b.ga = 1, b.gb = b.gc = G;
+  b.init = h0, b.state_t = true;
+  b.scale_out = scale, b.scale_in = 1.f;
+  b.out = d_q, b.so = oq.s;
+  if (gate) b.x = q, b.sx = rq.s, b.gx = 1, b.dot_in = dots + 2 * plane, b.dot_out = dots + 3 * plane;
+  e = lz::launch_decay_simt(b, d.dtype, s, &launches);
+  if (e != cudaSuccess || !gate) return finish(e, launches);
+  lz::DecayGate g{};
+  g.B = d.B, g.H = d.H, g.L = d.L, g.chunk = lz::kDecayChunk;
+  g.row_slices = g.col_slices = d.dk / lz::kDecaySlice;
+  g.col_in = dots, g.col_out = dots + plane, g.row_in = dots + 2 * plane, g.row_out = dots + 3 * plane;
+  g.h0 = h0, g.d_h0 = d_h0, g.state = d.dk * d.dv;
+  g.lg = log_decay, g.sg = rg.s, g.count = count, g.d_lg = d_log_decay;
+  e = lz::launch_decay_gate(g, s, &launches);
+  return finish(e, launches);
+}
+
+lizard_status lizard_decay_attn_step(const lizard_decay_dims* dims, const void* q, const lizard_strides* s_q,
+                                     const void* k, const lizard_strides* s_k, const void* v,
+                                     const lizard_strides* s_v, const float* log_decay,
+                                     const lizard_strides* s_decay, float* h, void* y, const lizard_strides* s_y,
+                                     void* stream) {
+  lz::set_last_launches(0);
+  if (!decay_dims_ok(dims)) return LIZARD_ERR_INVALID_ARG;
+  const lizard_decay_dims& d = *dims;
+  if (!width_ok(d.dk) || !width_ok(d.dv)) return LIZARD_ERR_UNSUPPORTED;
+  const bool none = d.L == 0;
+  if (!ptr_ok(q, none) || !ptr_ok(k, none) || !ptr_ok(v, none) || !decay_ptr_ok(log_decay, none) || !ptr_ok(y, none) ||
+      !ptr_ok(h, none))
+    return LIZARD_ERR_INVALID_ARG;
+  const Rows rq = rows_of(s_q, d.B, d.H, d.L, d.dk, d.dtype, false);
+  const Rows rk = rows_of(s_k, d.B, d.Hk, d.L, d.dk, d.dtype, false);
+  const Rows rv = rows_of(s_v, d.B, d.Hk, d.L, d.dv, d.dtype, false);
+  const Rows ry = rows_of(s_y, d.B, d.H, d.L, d.dv, d.dtype, true);
+  const Decays rg = decays_of(s_decay, d.B, d.H, d.L);
+  if (!rq.ok || !rk.ok || !rv.ok || !ry.ok || !rg.ok) return LIZARD_ERR_INVALID_ARG;
+  const int64_t es = (int64_t)elem_size(d.dtype);
+  const Span outs[] = {{h, (size_t)d.B * d.H * d.dk * d.dv * sizeof(float)}};
+  const Span rows[] = {{q, rq.bytes}, {k, rk.bytes}, {v, rv.bytes}, {y, ry.bytes}, {log_decay, rg.bytes}};
+  const Tensor ty{y, &ry, d.B, d.H, d.L, d.dv, es}, tq{q, &rq, d.B, d.H, d.L, d.dk, es};
+  const Tensor tk{k, &rk, d.B, d.Hk, d.L, d.dk, es}, tv{v, &rv, d.B, d.Hk, d.L, d.dv, es};
+  if (any_overlap(outs, 1, rows, 5) || overlap(rows[3], rows[4]) || !apart(ty, tq) || !apart(ty, tk) ||
+      !apart(ty, tv))
+    return LIZARD_ERR_INVALID_ARG;
+  if (none) return LIZARD_OK;
+  lz::DecayStep a{};
+  a.B = d.B, a.H = d.H, a.G = d.H / d.Hk, a.L = d.L, a.dk = d.dk, a.dv = d.dv;
+  a.q = q, a.k = k, a.v = v, a.sq = rq.s, a.sk = rk.s, a.sv = rv.s;
+  a.lg = log_decay, a.sg = rg.s, a.h = h, a.y = y, a.sy = ry.s, a.scale = scale_of(d);
+  int launches = 0;
+  const cudaError_t e = lz::launch_decay_step(a, d.dtype, (cudaStream_t)stream, &launches);
+  return finish(e, launches);
+}
+
+size_t lizard_layer_norm_workspace_bytes(const lizard_norm_dims* dims) {
+  if (!norm_dims_ok(dims) || !norm_width_ok(dims->d)) return 0;
+  return lz::kWsHeader +
+         lz::norm_part_floats(dims->N, dims->H, dims->T, dims->d, dims->per_head != 0) * sizeof(float);
+}
+
+lizard_status lizard_layer_norm_fwd(const lizard_norm_dims* dims, const void* x, const lizard_strides* s_x,
+                                    const void* weight, const void* bias, void* y, const lizard_strides* s_y,
+                                    void* stream) {
+  lz::set_last_launches(0);
+  if (!norm_dims_ok(dims)) return LIZARD_ERR_INVALID_ARG;
+  const lizard_norm_dims& d = *dims;
+  if (!norm_width_ok(d.d)) return LIZARD_ERR_UNSUPPORTED;
+  const bool none = d.T == 0;
+  if (!ptr_ok(x, none) || !ptr_ok(y, none) || !ptr_ok(weight, true) || !ptr_ok(bias, true))
+    return LIZARD_ERR_INVALID_ARG;
+  const Rows rx = rows_of(s_x, d.N, d.H, d.T, d.d, d.dtype, false);
+  const Rows ry = rows_of(s_y, d.N, d.H, d.T, d.d, d.dtype, true);
+  if (!rx.ok || !ry.ok) return LIZARD_ERR_INVALID_ARG;
+  const int64_t es = (int64_t)elem_size(d.dtype);
+  const size_t wb = (size_t)(d.per_head ? d.H : 1) * d.d * es;
+  const Span out[] = {{y, ry.bytes}}, ins[] = {{weight, wb}, {bias, wb}};
+  const Tensor tx{x, &rx, d.N, d.H, d.T, d.d, es}, ty{y, &ry, d.N, d.H, d.T, d.d, es};
+  const bool place = x == y && same(rx.s, ry.s);
+  if (any_overlap(out, 1, ins, 2) || (!place && !apart(ty, tx))) return LIZARD_ERR_INVALID_ARG;
+  if (none) return LIZARD_OK;
+  lz::NormCall a{};
+  a.N = d.N, a.H = d.H, a.T = d.T, a.d = d.d, a.per_head = d.per_head != 0, a.eps = d.eps > 0.f ? d.eps : 1e-5f;
+  a.x = x, a.w = weight, a.b = bias, a.y = y, a.sx = rx.s, a.sy = ry.s;
+  int launches = 0;
+  const cudaError_t e = lz::launch_norm_fwd(a, d.dtype, (cudaStream_t)stream, &launches);
+  return finish(e, launches);
+}
+
+lizard_status lizard_layer_norm_bwd(const lizard_norm_dims* dims, const void* x, const lizard_strides* s_x,
+                                    const void* weight, const void* dy, const lizard_strides* s_dy, void* d_x,
+                                    const lizard_strides* s_dx, float* d_weight, float* d_bias, void* workspace,
+                                    size_t workspace_bytes, void* stream) {
+  lz::set_last_launches(0);
+  if (!norm_dims_ok(dims)) return LIZARD_ERR_INVALID_ARG;
+  const lizard_norm_dims& d = *dims;
+  if (!norm_width_ok(d.d)) return LIZARD_ERR_UNSUPPORTED;
+  const bool none = d.T == 0;
+  if (!ptr_ok(x, none) || !ptr_ok(dy, none) || !ptr_ok(d_x, true) || !ptr_ok(weight, true) ||
+      !ptr_ok(d_weight, true) || !ptr_ok(d_bias, true))
+    return LIZARD_ERR_INVALID_ARG;
+  const Rows rx = rows_of(s_x, d.N, d.H, d.T, d.d, d.dtype, false);
+  const Rows ry = rows_of(s_dy, d.N, d.H, d.T, d.d, d.dtype, false);
+  const Rows ro = rows_of(s_dx, d.N, d.H, d.T, d.d, d.dtype, true);
+  if (!rx.ok || !ry.ok || !ro.ok) return LIZARD_ERR_INVALID_ARG;
+  if (!workspace || !aligned16(workspace) || workspace_bytes < lizard_layer_norm_workspace_bytes(dims))
+    return LIZARD_ERR_WORKSPACE;
+  const int64_t es = (int64_t)elem_size(d.dtype);
+  const size_t w = (size_t)(d.per_head ? d.H : 1) * d.d;
+  const Span flat[] = {{d_weight, w * 4}, {d_bias, w * 4}, {workspace, workspace_bytes}};
+  const Span rows[] = {{x, rx.bytes}, {dy, ry.bytes}, {d_x, ro.bytes}, {weight, w * es}};
+  const Tensor tx{x, &rx, d.N, d.H, d.T, d.d, es}, ty{dy, &ry, d.N, d.H, d.T, d.d, es};
+  const Tensor to{d_x, &ro, d.N, d.H, d.T, d.d, es};
+  const bool on_x = d_x == x && same(ro.s, rx.s), on_dy = d_x == dy && same(ro.s, ry.s);
+  if (any_overlap(flat, 3, rows, 4) || overlap(rows[2], rows[3]) || (d_x && !on_x && !apart(to, tx)) ||
+      (d_x && !on_dy && !apart(to, ty)))
+    return LIZARD_ERR_INVALID_ARG;
+  if (!d_x && !d_weight && !d_bias) return LIZARD_OK;
+  const cudaStream_t s = (cudaStream_t)stream;
+  if (none) {
+    cudaError_t e = cudaSuccess;
+    for (float* p : {d_weight, d_bias})
+      if (p && e == cudaSuccess) e = cudaMemsetAsync(p, 0, w * sizeof(float), s);
+    return finish(e, 0);
+  }
+  lz::NormCall a{};
+  a.N = d.N, a.H = d.H, a.T = d.T, a.d = d.d, a.per_head = d.per_head != 0, a.eps = d.eps > 0.f ? d.eps : 1e-5f;
+  a.x = x, a.w = weight, a.dy = dy, a.y = d_x, a.sx = rx.s, a.sdy = ry.s, a.sy = ro.s;
+  a.dw = d_weight, a.db = d_bias;
+  if (d_weight || d_bias) a.part = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + lz::kWsHeader);
+  int launches = 0;
+  const cudaError_t e = lz::launch_norm_bwd(a, d.dtype, s, &launches);
+  return finish(e, launches);
+}
+
+}  // extern "C"

@@ -1,0 +1,421 @@
+// k_decay_simt.cu -- one pass of the linear attention with a decay per head on CUDA cores, for fp32
+// (and for what the tensor-core pass does not take), the sum over the heads of a group, and the
+// gradient of log_decay from the passes' sums.
+//   out_o = sum_s D(o, s) (a_o . b_s) c_s + (decay from the chunk's edge) a_o^T H,
+// chunk after chunk of 64 tokens in the pass's direction, H the state that enters the chunk.  A CTA
+// takes 64 of c's channels of one head; H, the chunk's rows and its scores stay in shared memory,
+// every product is fp32 with 4 x 4 (or 8 x 4) results a thread.
+#include "lizard_dev.cuh"
+#include "lizard_internal.h"
+
+namespace lz {
+namespace {
+
+constexpr int kC = kDecayChunk;  // tokens of a chunk
+constexpr int kDc = kDecaySlice;  // channels of c of a CTA
+constexpr int kThreads = 256;
+constexpr int kSp = kC + 4;  // pitch of the scores
+
+template <int DA>
+struct Smem {
+  static constexpr int P = DA + 4;
+  float a[kC][P], b[kC][P], c[kC][kDc], s[kC][kSp], h[DA][kDc];
+  float hi[kC], lo[kC];    // the sum of log_decay up to each token (its finite part) in two floats
+  int doc[kC];             // documents begun up to each token
+  float in[kC], out[kC];   // decays from before the chunk to each token, from each token to the end
+  float diag[kC];
+  float all;               // decay of the whole chunk
+};
+
+// Rows t0 .. t0 + 63 of d channels (the pitch of dst is its own) as fp32; zeros from `end` on.
+template <typename T, int P>
+__device__ __forceinline__ void load_rows(float (*dst)[P], const T* src, int64_t st, int t0, int end, int d) {
+  const int quads = d / 4;
+  for (int i = threadIdx.x; i < kC * quads; i += kThreads) {
+    const int r = i / quads, q = i - r * quads;
+    const float4 v = t0 + r < end ? ld4(src + (int64_t)(t0 + r) * st + 4 * q) : make_float4(0.f, 0.f, 0.f, 0.f);
+    *reinterpret_cast<float4*>(&dst[r][4 * q]) = v;
+  }
+}
+
+// The chunk's decays, by one warp: two tokens a lane, sums in 64 bits so that differences of far
+// sums keep their digits.
+template <int DA>
+__device__ __forceinline__ void decays(Smem<DA>& m, const float* lg, int64_t st, int t0, int end) {
+  const int lane = threadIdx.x;
+  double x[2];
+  int n[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int t = t0 + 2 * lane + k;
+    const float g = t < end ? lg[t * st] : 0.f;
+    n[k] = g < kDecayNone;
+    x[k] = n[k] ? 0.0 : (double)g;
+  }
+  double sum = x[0] + x[1];
+  int docs = n[0] + n[1];
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const double u = __shfl_up_sync(0xffffffffu, sum, o);
+    const int v = __shfl_up_sync(0xffffffffu, docs, o);
+    if (lane >= o) sum += u, docs += v;
+  }
+  const double total = __shfl_sync(0xffffffffu, sum, 31);
+  const int last = __shfl_sync(0xffffffffu, docs, 31);
+  const double b[2] = {sum - x[1], sum};
+  const int dc[2] = {docs - n[1], docs};
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int i = 2 * lane + k;
+    m.hi[i] = (float)b[k];
+    m.lo[i] = (float)(b[k] - (double)m.hi[i]);
+    m.doc[i] = dc[k];
+    m.in[i] = dc[k] ? 0.f : expf((float)b[k]);
+    m.out[i] = dc[k] != last ? 0.f : expf((float)(total - b[k]));
+  }
+  if (lane == 0) m.all = last ? 0.f : expf((float)total);
+}
+
+template <typename T, int DA>
+__global__ void __launch_bounds__(kThreads) decay_simt_kernel(DecayPass a) {
+  extern __shared__ __align__(16) unsigned char raw[];
+  Smem<DA>& m = *reinterpret_cast<Smem<DA>*>(raw);
+  pdl_wait();
+  const int tid = threadIdx.x, tc = tid % 16, ti = tid / 16;
+  const int slices = a.dc / kDc, slice = blockIdx.x % slices, unit = blockIdx.x / slices;
+  const int n = unit / a.H, h = unit - n * a.H, c0 = slice * kDc;
+  int count = a.L;
+  if (a.count) {
+    count = a.count[n];
+    if (count < 0 || count > a.L) {
+      if (tid == 0) raise_status(a.status, kDevCheck);
+      count = 0;
+    }
+  }
+  const T* pa = static_cast<const T*>(a.a) + n * a.sa.n + h / a.ga * a.sa.h;
+  const T* pb = static_cast<const T*>(a.b) + n * a.sb.n + h / a.gb * a.sb.h;
+  const T* pc = static_cast<const T*>(a.c) + n * a.sc.n + h / a.gc * a.sc.h + c0;
+  const T* px = a.x ? static_cast<const T*>(a.x) + n * a.sx.n + h / a.gx * a.sx.h + c0 : nullptr;
+  const float* lg = a.lg + n * a.sg.n + h * a.sg.h;
+  const int64_t so = n * a.so.n + h * a.so.h + c0;
+  auto put = [&](int t, int col, float4 v) {
+    if (a.out_f32)
+      st4(static_cast<float*>(a.out) + so + t * a.so.t + col, v);
+    else
+      st4(static_cast<T*>(a.out) + so + t * a.so.t + col, v);
+  };
+  // element (i, j) of the state of this head
+  auto state = [&](int i, int j) {
+    return (int64_t)unit * DA * a.dc + (a.state_t ? (int64_t)(c0 + j) * DA + i : (int64_t)i * a.dc + c0 + j);
+  };
+  for (int e = tid; e < DA * kDc; e += kThreads) {
+    const int i = a.state_t ? e % DA : e / kDc, j = a.state_t ? e / DA : e % kDc;
+    m.h[i][j] = a.init ? a.init[state(i, j)] : 0.f;
+  }
+  float* dots[2] = {nullptr, nullptr};
+  if (px) {
+    const int64_t o = ((int64_t)slice * a.B * a.H + unit) * a.L;
+    dots[0] = a.dot_in + o, dots[1] = a.dot_out + o;
+  }
+  const int chunks = (count + kC - 1) / kC;
+  for (int step = 0; step < chunks; ++step) {
+    const int t0 = (a.rev ? chunks - 1 - step : step) * kC;
+    load_rows<T>(m.a, pa, a.sa.t, t0, count, DA);
+    load_rows<T>(m.b, pb, a.sb.t, t0, count, DA);
+    load_rows<T>(m.c, pc, a.sc.t, t0, count, kDc);
+    if (tid < 32) decays(m, lg, a.sg.t, t0, count);
+    __syncthreads();
+    const float* from_state = a.rev ? m.out : m.in;  // from the state that enters to each token
+    const float* to_state = a.rev ? m.in : m.out;    // from each token to the state that leaves
+    // scores with their decays; the diagonal apart
+    float acc[4][4] = {};
+#pragma unroll 4
+    for (int k = 0; k < DA; k += 4) {
+      float4 x[4], y[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        x[r] = *reinterpret_cast<const float4*>(&m.a[ti + 16 * r][k]);
+        y[r] = *reinterpret_cast<const float4*>(&m.b[tc + 16 * r][k]);
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          acc[r][c] = fmaf(x[r].x, y[c].x, acc[r][c]);
+          acc[r][c] = fmaf(x[r].y, y[c].y, acc[r][c]);
+          acc[r][c] = fmaf(x[r].z, y[c].z, acc[r][c]);
+          acc[r][c] = fmaf(x[r].w, y[c].w, acc[r][c]);
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int o = ti + 16 * r, s = tc + 16 * c;
+        const int late = a.rev ? s : o, early = a.rev ? o : s;
+        float d = 0.f;
+        if (late > early && m.doc[late] == m.doc[early])
+          d = expf((m.hi[late] - m.hi[early]) + (m.lo[late] - m.lo[early]));
+        m.s[o][s] = d > 0.f ? acc[r][c] * a.scale_in * d : 0.f;
+        if (o == s) m.diag[o] = acc[r][c] * a.scale_in;
+      }
+    __syncthreads();
+    // out = scores c + decay a^T H
+    float in[4][4] = {}, st[4][4] = {};
+#pragma unroll 4
+    for (int j = 0; j < kC; j += 4) {
+      float4 x[4], y[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        x[r] = *reinterpret_cast<const float4*>(&m.s[ti + 16 * r][j]);
+        y[r] = *reinterpret_cast<const float4*>(&m.c[j + r][4 * tc]);
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float w[4] = {x[r].x, x[r].y, x[r].z, x[r].w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          in[r][0] = fmaf(w[q], y[q].x, in[r][0]);
+          in[r][1] = fmaf(w[q], y[q].y, in[r][1]);
+          in[r][2] = fmaf(w[q], y[q].z, in[r][2]);
+          in[r][3] = fmaf(w[q], y[q].w, in[r][3]);
+        }
+      }
+    }
+#pragma unroll 4
+    for (int j = 0; j < DA; j += 4) {
+      float4 x[4], y[4];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        x[r] = *reinterpret_cast<const float4*>(&m.a[ti + 16 * r][j]);
+        y[r] = *reinterpret_cast<const float4*>(&m.h[j + r][4 * tc]);
+      }
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const float w[4] = {x[r].x, x[r].y, x[r].z, x[r].w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          st[r][0] = fmaf(w[q], y[q].x, st[r][0]);
+          st[r][1] = fmaf(w[q], y[q].y, st[r][1]);
+          st[r][2] = fmaf(w[q], y[q].z, st[r][2]);
+          st[r][3] = fmaf(w[q], y[q].w, st[r][3]);
+        }
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const int o = ti + 16 * r, t = t0 + o;
+      const float e = from_state[o];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) st[r][q] = e > 0.f ? e * st[r][q] : 0.f;
+      if (px) {
+        const float4 x = t < count ? ld4(px + t * a.sx.t + 4 * tc) : make_float4(0.f, 0.f, 0.f, 0.f);
+        float d0 = x.x * in[r][0] + x.y * in[r][1] + x.z * in[r][2] + x.w * in[r][3];
+        float d1 = x.x * st[r][0] + x.y * st[r][1] + x.z * st[r][2] + x.w * st[r][3];
+#pragma unroll
+        for (int x16 = 8; x16 > 0; x16 >>= 1) {
+          d0 += __shfl_xor_sync(0xffffffffu, d0, x16);
+          d1 += __shfl_xor_sync(0xffffffffu, d1, x16);
+        }
+        if (tc == 0 && t < count) dots[0][t] = a.scale_out * d0, dots[1][t] = a.scale_out * d1;
+      }
+      const float4 cd = *reinterpret_cast<const float4*>(&m.c[o][4 * tc]);
+      const float dg = m.diag[o];
+      if (t < count)
+        put(t, 4 * tc, make_float4(a.scale_out * (fmaf(dg, cd.x, in[r][0]) + st[r][0]),
+                                   a.scale_out * (fmaf(dg, cd.y, in[r][1]) + st[r][1]),
+                                   a.scale_out * (fmaf(dg, cd.z, in[r][2]) + st[r][2]),
+                                   a.scale_out * (fmaf(dg, cd.w, in[r][3]) + st[r][3])));
+    }
+    __syncthreads();
+    // H <- decay H + sum_s decay_s b_s c_s^T: rows ti * NR + r, columns 4 tc ..
+    constexpr int NR = DA / 16;
+    float u[NR][4];
+    const float all = m.all;
+#pragma unroll
+    for (int r = 0; r < NR; ++r) {
+      const float4 x = *reinterpret_cast<const float4*>(&m.h[ti * NR + r][4 * tc]);
+      u[r][0] = all > 0.f ? all * x.x : 0.f, u[r][1] = all > 0.f ? all * x.y : 0.f;
+      u[r][2] = all > 0.f ? all * x.z : 0.f, u[r][3] = all > 0.f ? all * x.w : 0.f;
+    }
+#pragma unroll 2
+    for (int s = 0; s < kC; ++s) {
+      const float e = to_state[s] * a.scale_in;
+      float4 y = *reinterpret_cast<const float4*>(&m.c[s][4 * tc]);
+      y = e != 0.f ? make_float4(y.x * e, y.y * e, y.z * e, y.w * e) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int r = 0; r < NR; r += 4) {
+        const float4 x = *reinterpret_cast<const float4*>(&m.b[s][ti * NR + r]);
+        const float w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          u[r + q][0] = fmaf(w[q], y.x, u[r + q][0]);
+          u[r + q][1] = fmaf(w[q], y.y, u[r + q][1]);
+          u[r + q][2] = fmaf(w[q], y.z, u[r + q][2]);
+          u[r + q][3] = fmaf(w[q], y.w, u[r + q][3]);
+        }
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < NR; ++r)
+      *reinterpret_cast<float4*>(&m.h[ti * NR + r][4 * tc]) = make_float4(u[r][0], u[r][1], u[r][2], u[r][3]);
+    __syncthreads();
+  }
+  for (int64_t i = tid; i < (int64_t)(a.L - count) * (kDc / 4); i += kThreads)
+    put(count + (int)(i / (kDc / 4)), 4 * (int)(i % (kDc / 4)), make_float4(0.f, 0.f, 0.f, 0.f));
+  if (a.fin) {
+    __syncthreads();  // without a chunk, the initial state
+    for (int e = tid; e < DA * kDc; e += kThreads) {
+      const int i = a.state_t ? e % DA : e / kDc, j = a.state_t ? e / DA : e % kDc;
+      a.fin[state(i, j)] = m.h[i][j];
+    }
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) decay_heads_kernel(int Hk, int G, int L, int d, const float* part, T* out,
+                                                               Strides so, int64_t quads) {
+  pdl_wait();
+  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  if (i >= quads) return;
+  const int per = d / 4;
+  const int64_t row = i / per;
+  const int c = 4 * (int)(i - row * per);
+  const int64_t u = row / L;
+  const int t = (int)(row - u * L), n = (int)(u / Hk), h = (int)(u - (int64_t)n * Hk);
+  const float* p = part + (u * G * L + t) * d + c;
+  float4 s = ld4(p);
+  for (int g = 1; g < G; ++g) {
+    const float4 x = ld4(p + (int64_t)g * L * d);
+    s.x += x.x, s.y += x.y, s.z += x.z, s.w += x.w;
+  }
+  st4(out + n * so.n + h * so.h + t * so.t + c, s);
+}
+
+// d log_decay_t = g_t <h_{t-1}, dh_t>: the sum of all products that pass over token t.  With, for
+// each token, what it receives from (rows) and gives to (cols) other tokens of its chunk and the
+// states at the chunk's ends,
+//   = sum_{i >= t} row_in_i - sum_{j >= t} col_in_j        within the chunk (t's own pair cancels)
+//   + sum_{i >= t} row_out_i + sum_{j < t} col_out_j       between the chunk and what lies around it
+//   + through                                              from before the chunk to after it.
+// `through` of the chunks follows from the pairs over the edge before the first one, <h0, d_h0>:
+//   edge after = through + sum col_out,  through = edge before - sum row_out  (0 where a document
+// starts in the chunk).  Sums of a chunk run in 64 bits; one warp for each head and sequence.
+__global__ void __launch_bounds__(32) decay_gate_kernel(DecayGate a) {
+  pdl_wait();
+  const int unit = blockIdx.x, lane = threadIdx.x;
+  const int n = unit / a.H, h = unit - n * a.H;
+  const int64_t plane = (int64_t)a.B * a.H * a.L, base = (int64_t)unit * a.L;
+  int count = a.count ? a.count[n] : a.L;
+  if (count < 0 || count > a.L) count = 0;
+  double edge = 0.0;
+  if (a.h0) {
+    const float *x = a.h0 + (int64_t)unit * a.state, *y = a.d_h0 + (int64_t)unit * a.state;
+    for (int i = lane; i < a.state; i += 32) edge += (double)(x[i] * y[i]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) edge += __shfl_xor_sync(0xffffffffu, edge, o);
+  }
+  const float* lg = a.lg + n * a.sg.n + h * a.sg.h;
+  for (int t0 = 0; t0 < count; t0 += a.chunk) {
+    // the chunk's groups of 32 tokens from the last to the first, with what lies behind each
+    const int end = min(t0 + a.chunk, count);
+    double rows = 0.0, cols = 0.0;
+    bool start = false;
+    for (int t = t0 + lane; t < end; t += 32) {
+      for (int s = 0; s < a.row_slices; ++s) rows += a.row_out[s * plane + base + t];
+      for (int s = 0; s < a.col_slices; ++s) cols += a.col_out[s * plane + base + t];
+      start |= lg[t * a.sg.t] < kDecayNone;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      rows += __shfl_xor_sync(0xffffffffu, rows, o);
+      cols += __shfl_xor_sync(0xffffffffu, cols, o);
+    }
+    start = __any_sync(0xffffffffu, start);
+    const double through = start ? 0.0 : edge - rows;
+    double behind = 0.0, before = cols;  // of the suffix sums; col_out of the tokens before the group's end
+    for (int g0 = t0 + (end - t0 - 1) / 32 * 32; g0 >= t0; g0 -= 32) {
+      const int t = g0 + lane;
+      double suffix = 0.0, col = 0.0;
+      float g = 0.f;
+      if (t < end) {
+        g = lg[t * a.sg.t];
+        for (int s = 0; s < a.row_slices; ++s)
+          suffix += (double)a.row_in[s * plane + base + t] + a.row_out[s * plane + base + t];
+        for (int s = 0; s < a.col_slices; ++s) {
+          suffix -= a.col_in[s * plane + base + t];
+          col += a.col_out[s * plane + base + t];
+        }
+      }
+      // a document's start cuts the sums: nothing behind it passes over the tokens before it
+      const bool cut = t < end && g < kDecayNone;
+      double sum = suffix;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const double u = __shfl_down_sync(0xffffffffu, sum, o);
+        if (lane + o < 32) sum += u;
+      }
+      double colsum = col;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const double u = __shfl_down_sync(0xffffffffu, colsum, o);
+        if (lane + o < 32) colsum += u;
+      }
+      if (t < end) a.d_lg[base + t] = cut ? 0.f : (float)(behind + sum + (before - colsum) + through);
+      behind += __shfl_sync(0xffffffffu, sum, 0);
+      before -= __shfl_sync(0xffffffffu, colsum, 0);
+    }
+    edge = through + cols;
+  }
+  for (int t = count + lane; t < a.L; t += 32) a.d_lg[base + t] = 0.f;
+}
+
+template <typename T, int DA>
+cudaError_t launch(const DecayPass& a, cudaStream_t s) {
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_smem(decay_simt_kernel<T, DA>, sizeof(Smem<DA>), done);
+  if (e != cudaSuccess) return e;
+  const int64_t blocks = (int64_t)a.B * a.H * (a.dc / kDc);
+  if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
+  return launch_pdl(decay_simt_kernel<T, DA>, dim3((unsigned)blocks), dim3(kThreads), sizeof(Smem<DA>), s, a);
+}
+
+}  // namespace
+
+cudaError_t launch_decay_simt(const DecayPass& a, lizard_dtype dt, cudaStream_t s, int* launches) {
+  trace_begin("decay_simt", s);
+  cudaError_t e;
+  if (dt == LIZARD_F32)
+    e = a.da == 64 ? launch<float, 64>(a, s) : launch<float, 128>(a, s);
+  else
+    e = a.da == 64 ? launch<bf16, 64>(a, s) : launch<bf16, 128>(a, s);
+  trace_end(s);
+  ++*launches;
+  return e;
+}
+
+cudaError_t launch_decay_heads(int B, int Hk, int G, int L, int d, const float* part, void* out, Strides so,
+                               lizard_dtype dt, cudaStream_t s, int* launches) {
+  const int64_t quads = (int64_t)B * Hk * L * (d / 4), blocks = (quads + kThreads - 1) / kThreads;
+  if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
+  trace_begin("decay_heads", s);
+  const cudaError_t e =
+      dt == LIZARD_F32
+          ? launch_pdl(decay_heads_kernel<float>, dim3((unsigned)blocks), dim3(kThreads), 0, s, Hk, G, L, d, part,
+                       static_cast<float*>(out), so, quads)
+          : launch_pdl(decay_heads_kernel<bf16>, dim3((unsigned)blocks), dim3(kThreads), 0, s, Hk, G, L, d, part,
+                       static_cast<bf16*>(out), so, quads);
+  trace_end(s);
+  ++*launches;
+  return e;
+}
+
+cudaError_t launch_decay_gate(const DecayGate& a, cudaStream_t s, int* launches) {
+  trace_begin("decay_gate", s);
+  const cudaError_t e = launch_pdl(decay_gate_kernel, dim3((unsigned)a.B * a.H), dim3(32), 0, s, a);
+  trace_end(s);
+  ++*launches;
+  return e;
+}
+
+}  // namespace lz

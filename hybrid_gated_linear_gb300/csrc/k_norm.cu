@@ -1,0 +1,377 @@
+// k_norm.cu -- layer norm of rows of d channels and its backward.
+//   n = (x - mean) r,  r = 1 / sqrt(mean((x - mean)^2) + eps),  y = n w + b
+//   a = dy w,  dx = r (a - mean(a) - n mean(a n)),  dw = sum dy n,  db = sum dy
+// Both are bound by memory (x in, y out; x and dy in, dx out).  A row lies in the registers of
+// TPR threads, 16 channels each, from its one read to its one write: the mean is summed first, the
+// variance around it second, both from registers, so that a large mean costs no digits and the
+// backward needs nothing but x.
+#include "lizard_dev.cuh"
+#include "lizard_internal.h"
+
+namespace lz {
+namespace {
+
+constexpr int kEpt = 16;  // channels of a thread
+constexpr int kBlock = 256;
+
+template <typename T>
+struct Frag {
+  static constexpr int V = 16 / (int)sizeof(T);  // channels of a 16-byte vector
+  static constexpr int NV = kEpt / V;
+  uint4 v[NV];
+};
+
+__device__ __forceinline__ void unpack(const Frag<float>& f, float (&o)[kEpt]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    o[4 * i] = __uint_as_float(f.v[i].x), o[4 * i + 1] = __uint_as_float(f.v[i].y);
+    o[4 * i + 2] = __uint_as_float(f.v[i].z), o[4 * i + 3] = __uint_as_float(f.v[i].w);
+  }
+}
+__device__ __forceinline__ void unpack(const Frag<bf16>& f, float (&o)[kEpt]) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t w[4] = {f.v[i].x, f.v[i].y, f.v[i].z, f.v[i].w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      o[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
+      o[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+    }
+  }
+}
+__device__ __forceinline__ void pack(const float (&o)[kEpt], Frag<float>& f) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    f.v[i] = make_uint4(__float_as_uint(o[4 * i]), __float_as_uint(o[4 * i + 1]), __float_as_uint(o[4 * i + 2]),
+                        __float_as_uint(o[4 * i + 3]));
+}
+__device__ __forceinline__ void pack(const float (&o)[kEpt], Frag<bf16>& f) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const __nv_bfloat162 p = __floats2bfloat162_rn(o[8 * i + 2 * j], o[8 * i + 2 * j + 1]);
+      w[j] = *reinterpret_cast<const uint32_t*>(&p);
+    }
+    f.v[i] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+// Thread `lane` of a row holds the vectors lane, lane + TPR, ...; those past the row are zeros.
+template <typename T, int TPR>
+__device__ __forceinline__ void load(const T* row, int lane, int d, Frag<T>& f) {
+#pragma unroll
+  for (int i = 0; i < Frag<T>::NV; ++i) {
+    const int c = (lane + TPR * i) * Frag<T>::V;
+    f.v[i] = row && c < d ? *reinterpret_cast<const uint4*>(row + c) : make_uint4(0, 0, 0, 0);
+  }
+}
+template <typename T, int TPR>
+__device__ __forceinline__ void store(T* row, int lane, int d, const Frag<T>& f) {
+#pragma unroll
+  for (int i = 0; i < Frag<T>::NV; ++i) {
+    const int c = (lane + TPR * i) * Frag<T>::V;
+    if (c < d) *reinterpret_cast<uint4*>(row + c) = f.v[i];
+  }
+}
+// Whether the thread's element e lies inside the row.
+template <typename T, int TPR>
+__device__ __forceinline__ bool inside(int lane, int d, int e) {
+  return (lane + TPR * (e / Frag<T>::V)) * Frag<T>::V < d;
+}
+
+// Sums over the TPR threads of a row, the same in all of them.  Rows of more than a warp use
+// `part` and a barrier: every thread of the block calls, and two calls in turn use `part` of two
+// parities, so that the second's writes do not meet the first's reads.
+template <int TPR, int N>
+__device__ __forceinline__ void row_sum(float (&s)[N], float* part, int parity) {
+#pragma unroll
+  for (int o = (TPR < 32 ? TPR : 32) / 2; o > 0; o >>= 1)
+#pragma unroll
+    for (int k = 0; k < N; ++k) s[k] += __shfl_xor_sync(0xffffffffu, s[k], o);
+  if (TPR > 32) {
+    constexpr int W = TPR > 32 ? TPR / 32 : 1;  // warps of a row
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    float* p = part + parity * 64;
+    if (lane == 0)
+#pragma unroll
+      for (int k = 0; k < N; ++k) p[warp * 2 + k] = s[k];
+    __syncthreads();
+    const int w0 = warp / W * W;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      float t = lane < W ? p[(w0 + lane) * 2 + k] : 0.f;
+#pragma unroll
+      for (int o = W / 2; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+      s[k] = W < 32 ? __shfl_sync(0xffffffffu, t, 0) : t;
+    }
+  }
+}
+
+// x becomes x - mean; returns 1 / sqrt(var + eps).
+template <typename T, int TPR>
+__device__ __forceinline__ float centre(float (&x)[kEpt], int lane, int d, float eps, float inv_d, float* part) {
+  float s[1] = {0.f};
+#pragma unroll
+  for (int e = 0; e < kEpt; ++e) s[0] += x[e];
+  row_sum<TPR>(s, part, 0);
+  const float mean = s[0] * inv_d;
+  s[0] = 0.f;
+#pragma unroll
+  for (int e = 0; e < kEpt; ++e) {
+    x[e] = inside<T, TPR>(lane, d, e) ? x[e] - mean : 0.f;
+    s[0] = fmaf(x[e], x[e], s[0]);
+  }
+  row_sum<TPR>(s, part, 1);
+  return rsqrtf(fmaf(s[0], inv_d, eps));
+}
+
+// Row r (of rows of all heads, or of one head) as n, h, t; the axis with the smaller stride of x
+// is the inner one, so that neighbouring threads' rows are neighbours in memory.
+struct Index {
+  uint32_t n, h, t;
+};
+__device__ __forceinline__ Index index_of(const NormCall& a, uint32_t r, bool heads_inner) {
+  Index i;
+  if (heads_inner) {
+    const uint32_t q = r / a.H;
+    i.h = r - q * a.H;
+    i.n = q / a.T;
+    i.t = q - i.n * a.T;
+  } else {
+    const uint32_t q = r / a.T;
+    i.t = r - q * a.T;
+    i.n = q / a.H;
+    i.h = q - i.n * a.H;
+  }
+  return i;
+}
+__device__ __forceinline__ int64_t offset(const Strides& s, const Index& i) {
+  return i.n * s.n + i.h * s.h + i.t * s.t;
+}
+
+template <typename T, int TPR>
+__global__ void __launch_bounds__(TPR > kBlock ? TPR : kBlock) norm_fwd_kernel(NormCall a, uint32_t rows, bool heads_inner) {
+  constexpr int RPB = (TPR > kBlock ? TPR : kBlock) / TPR;
+  __shared__ float part[128];
+  pdl_wait();
+  const int lane = threadIdx.x % TPR;
+  const uint32_t r = blockIdx.x * RPB + threadIdx.x / TPR;
+  const bool live = r < rows;
+  const Index i = index_of(a, live ? r : 0, heads_inner);
+  Frag<T> f, fw, fb;
+  load<T, TPR>(live ? static_cast<const T*>(a.x) + offset(a.sx, i) : nullptr, lane, a.d, f);
+  const int64_t wo = a.per_head ? (int64_t)i.h * a.d : 0;
+  load<T, TPR>(a.w ? static_cast<const T*>(a.w) + wo : nullptr, lane, a.d, fw);
+  load<T, TPR>(a.b ? static_cast<const T*>(a.b) + wo : nullptr, lane, a.d, fb);
+  float x[kEpt], w[kEpt], b[kEpt];
+  unpack(f, x);
+  const float rs = centre<T, TPR>(x, lane, a.d, a.eps, 1.f / a.d, part);
+  unpack(fw, w);
+  unpack(fb, b);
+#pragma unroll
+  for (int e = 0; e < kEpt; ++e) {
+    const float n = x[e] * rs;
+    x[e] = a.w ? fmaf(n, w[e], b[e]) : n + b[e];
+  }
+  pack(x, f);
+  if (live) store<T, TPR>(static_cast<T*>(a.y) + offset(a.sy, i), lane, a.d, f);
+}
+
+// Block (x, y): every gridDim.x-th group of rows of head y (per_head) or of all rows.  The sums of
+// dw and db stay in the threads' registers until the block's last row; then the block's rows are
+// added up in a fixed order into part[y][x][2][d].  The next row is on its way while one is
+// worked on.
+template <typename T, int TPR>
+__global__ void __launch_bounds__(TPR > kBlock ? TPR : kBlock) norm_bwd_kernel(NormCall a, uint32_t rows, bool heads_inner) {
+  constexpr int THREADS = TPR > kBlock ? TPR : kBlock, RPB = THREADS / TPR;
+  extern __shared__ float sums[];  // [warps][2][d] for rows within a warp, [RPB][2][d] for wider ones
+  __shared__ float part[128], part2[128];
+  pdl_wait();
+  const int lane = threadIdx.x % TPR;
+  const T* xs = static_cast<const T*>(a.x);
+  const T* dys = static_cast<const T*>(a.dy);
+  auto at = [&](uint32_t r) {
+    if (!a.per_head) return index_of(a, r, heads_inner);
+    const uint32_t n = r / a.T;
+    return Index{n, blockIdx.y, r - n * a.T};
+  };
+  float w[kEpt], dw[kEpt], db[kEpt];
+  Frag<T> f, g;
+  load<T, TPR>(a.w ? static_cast<const T*>(a.w) + (a.per_head ? (int64_t)blockIdx.y * a.d : 0) : nullptr, lane, a.d, f);
+  unpack(f, w);
+#pragma unroll
+  for (int e = 0; e < kEpt; ++e) {
+    if (!a.w) w[e] = 1.f;
+    dw[e] = db[e] = 0.f;
+  }
+  const float inv_d = 1.f / a.d;
+  const uint32_t step = gridDim.x * RPB;
+  uint32_t r = blockIdx.x * RPB + threadIdx.x / TPR;
+  bool live = r < rows;
+  Index i = at(live ? r : 0);
+  load<T, TPR>(live ? xs + offset(a.sx, i) : nullptr, lane, a.d, f);
+  load<T, TPR>(live ? dys + offset(a.sdy, i) : nullptr, lane, a.d, g);
+  for (uint32_t first = blockIdx.x * RPB; first < rows; first += step) {
+    float x[kEpt], dy[kEpt];
+    unpack(f, x);
+    unpack(g, dy);
+    const bool live_now = live;
+    const int64_t to = offset(a.sy, i);
+    r += step;  // rows + step fits: both are below 2^31
+    live = r < rows;
+    i = at(live ? r : 0);
+    load<T, TPR>(live ? xs + offset(a.sx, i) : nullptr, lane, a.d, f);
+    load<T, TPR>(live ? dys + offset(a.sdy, i) : nullptr, lane, a.d, g);
+    const float rs = centre<T, TPR>(x, lane, a.d, a.eps, inv_d, part);
+    float s[2] = {0.f, 0.f};
+#pragma unroll
+    for (int e = 0; e < kEpt; ++e) {
+      x[e] *= rs;
+      db[e] += dy[e];
+      dw[e] = fmaf(dy[e], x[e], dw[e]);
+      dy[e] *= w[e];
+      s[0] += dy[e];
+      s[1] = fmaf(dy[e], x[e], s[1]);
+    }
+    row_sum<TPR>(s, part2, 0);
+    const float m0 = s[0] * inv_d, m1 = s[1] * inv_d;
+#pragma unroll
+    for (int e = 0; e < kEpt; ++e) x[e] = rs * (dy[e] - m0 - x[e] * m1);
+    Frag<T> o;
+    pack(x, o);
+    if (live_now && a.y) store<T, TPR>(static_cast<T*>(a.y) + to, lane, a.d, o);
+  }
+  if (!a.part) return;
+  // rows of one warp, then the block's warps (or rows) one after the other
+  constexpr int PARTS = TPR < 32 ? THREADS / 32 : RPB;
+#pragma unroll
+  for (int o = TPR; o < 32; o <<= 1)
+#pragma unroll
+    for (int e = 0; e < kEpt; ++e) {
+      dw[e] += __shfl_xor_sync(0xffffffffu, dw[e], o);
+      db[e] += __shfl_xor_sync(0xffffffffu, db[e], o);
+    }
+  float* mine = PARTS == 1 ? a.part + ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 2 * a.d
+                           : sums + (TPR < 32 ? threadIdx.x / 32 : threadIdx.x / TPR) * 2 * a.d;
+  if (TPR >= 32 || threadIdx.x % 32 < TPR) {
+#pragma unroll
+    for (int e = 0; e < kEpt; ++e) {
+      const int c = (lane + TPR * (e / Frag<T>::V)) * Frag<T>::V + e % Frag<T>::V;
+      if (inside<T, TPR>(lane, a.d, e)) mine[c] = dw[e], mine[a.d + c] = db[e];
+    }
+  }
+  if (PARTS == 1) return;
+  __syncthreads();
+  float* out = a.part + ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 2 * a.d;
+  for (int c = threadIdx.x; c < 2 * a.d; c += THREADS) {
+    float s = 0.f;
+#pragma unroll
+    for (int p = 0; p < PARTS; ++p) s += sums[p * 2 * a.d + c];
+    out[c] = s;
+  }
+}
+
+// dw, db from the blocks' parts [sets][parts][2][d]: 32 columns and 32 strands of parts a block,
+// the strands joined in order.
+__global__ void __launch_bounds__(1024) norm_weights_kernel(const float* part, int parts, int d, float* dw, float* db) {
+  __shared__ float s[32][33];
+  pdl_wait();
+  const int c = blockIdx.x * 32 + threadIdx.x;
+  const float* p = part + (int64_t)blockIdx.y * parts * 2 * d + c;
+  float sum = 0.f;
+  if (c < 2 * d) {
+#pragma unroll 8
+    for (int k = threadIdx.y; k < parts; k += 32) sum += p[(int64_t)k * 2 * d];
+  }
+  s[threadIdx.y][threadIdx.x] = sum;
+  __syncthreads();
+  if (threadIdx.y || c >= 2 * d) return;
+  sum = 0.f;
+#pragma unroll
+  for (int k = 0; k < 32; ++k) sum += s[k][threadIdx.x];
+  float* o = c < d ? dw : db;
+  if (o) o[(int64_t)blockIdx.y * d + (c < d ? c : c - d)] = sum;
+}
+
+// Threads of a row: 16 channels each, a power of two from 4 on.
+int threads_per_row(int d) {
+  int t = 4;
+  while (t * kEpt < d) t *= 2;
+  return t;
+}
+int rows_per_block(int d) {
+  const int t = threads_per_row(d);
+  return t >= kBlock ? 1 : kBlock / t;
+}
+// Blocks that share the rows of one set of weights in the backward: about one wave of four blocks
+// an SM over all sets.  (152 SMs: written down, so that the workspace does not ask for a device.)
+int bwd_blocks(int64_t rows, int sets, int d) {
+  const int64_t most = (rows + rows_per_block(d) - 1) / rows_per_block(d);
+  const int per_sm = threads_per_row(d) > kBlock ? 2 : 4;
+  int64_t n = ((int64_t)152 * per_sm + sets - 1) / sets;
+  n = n < most ? n : most;
+  return (int)(n < 1 ? 1 : n);
+}
+bool heads_inner(const NormCall& a) { return a.H > 1 && (a.T == 1 || a.sx.h < a.sx.t); }
+
+template <typename T, int TPR>
+cudaError_t fwd(const NormCall& a, cudaStream_t s) {
+  const uint32_t rows = (uint32_t)a.N * a.H * a.T;
+  const int rpb = rows_per_block(a.d);
+  return launch_pdl(norm_fwd_kernel<T, TPR>, dim3((rows + rpb - 1) / rpb), dim3(TPR > kBlock ? TPR : kBlock), 0, s, a,
+                    rows, heads_inner(a));
+}
+template <typename T, int TPR>
+cudaError_t bwd(const NormCall& a, cudaStream_t s) {
+  const uint32_t rows = (uint32_t)a.N * a.T * (a.per_head ? 1 : a.H);
+  const int sets = a.per_head ? a.H : 1;
+  const int parts = TPR < 32 ? kBlock / 32 : TPR >= kBlock ? 0 : kBlock / TPR;  // at most 32 KB
+  return launch_pdl(norm_bwd_kernel<T, TPR>, dim3(bwd_blocks(rows, sets, a.d), sets), dim3(TPR > kBlock ? TPR : kBlock),
+                    (size_t)parts * 2 * a.d * sizeof(float), s, a, rows, heads_inner(a));
+}
+
+template <typename T>
+cudaError_t dispatch(const NormCall& a, bool back, cudaStream_t s) {
+  switch (threads_per_row(a.d)) {
+#define LZ_NORM(n) \
+  case n: return back ? bwd<T, n>(a, s) : fwd<T, n>(a, s);
+    LZ_NORM(4) LZ_NORM(8) LZ_NORM(16) LZ_NORM(32) LZ_NORM(64) LZ_NORM(128) LZ_NORM(256) LZ_NORM(512) LZ_NORM(1024)
+#undef LZ_NORM
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+size_t norm_part_floats(int N, int H, int T, int d, bool per_head) {
+  const int sets = per_head ? H : 1;
+  return (size_t)sets * bwd_blocks((int64_t)N * T * (per_head ? 1 : H), sets, d) * 2 * d;
+}
+
+cudaError_t launch_norm_fwd(const NormCall& a, lizard_dtype dt, cudaStream_t s, int* launches) {
+  trace_begin("norm_fwd", s);
+  const cudaError_t e = dt == LIZARD_F32 ? dispatch<float>(a, false, s) : dispatch<bf16>(a, false, s);
+  trace_end(s);
+  ++*launches;
+  return e;
+}
+
+cudaError_t launch_norm_bwd(const NormCall& a, lizard_dtype dt, cudaStream_t s, int* launches) {
+  trace_begin("norm_bwd", s);
+  cudaError_t e = dt == LIZARD_F32 ? dispatch<float>(a, true, s) : dispatch<bf16>(a, true, s);
+  trace_end(s);
+  ++*launches;
+  if (e != cudaSuccess || !a.part) return e;
+  const int sets = a.per_head ? a.H : 1;
+  const int parts = bwd_blocks((int64_t)a.N * a.T * (a.per_head ? 1 : a.H), sets, a.d);
+  trace_begin("norm_weights", s);
+  e = launch_pdl(norm_weights_kernel, dim3((2 * a.d + 31) / 32, sets), dim3(32, 32), 0, s,
+                 static_cast<const float*>(a.part), parts, a.d, a.dw, a.db);
+  trace_end(s);
+  ++*launches;
+  return e;
+}
+
+}  // namespace lz

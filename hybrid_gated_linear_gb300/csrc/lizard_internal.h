@@ -376,4 +376,83 @@ size_t cache_attn_tc_workspace(int d);
 cudaError_t launch_cache_attn_tc(const CacheAttn& a, cudaStream_t s, int* launches);
 cudaError_t launch_cache_attn(const CacheAttn& a, lizard_dtype dt, cudaStream_t s, int* launches);
 
+// One pass of the linear attention with a decay per head, over tokens in either direction:
+//   out_o = scale_out sum_s scale_in D(o, s) (a_o . b_s) c_s  (+ the part of the initial state)
+// with s <= o (forward) or s >= o (rev) and D the product of the decays after the earlier of the
+// two up to the later.  The forward is (a, b, c) = (q, k, v); the gradients are (dy, v, k) forward
+// for q, (v, dy, q) and (k, q, dy) reversed for k and v.  a, b have da channels, c and out dc.
+struct DecayPass {
+  int B, H, L, da, dc;
+  const void *a, *b, *c;
+  Strides sa, sb, sc;
+  int ga, gb, gc;          // head h reads head h / g
+  const float* lg;         // at n * sg.n + h * sg.h + t * sg.t
+  Strides sg;
+  const int32_t* count;    // or null
+  const float* init;       // state that enters, or null; [B,H,da,dc], transposed if `state_t`
+  float* fin;              // state that leaves, or null; the same layout
+  bool state_t;
+  void* out;
+  Strides so;
+  bool out_f32;            // out is fp32 whatever the dtype
+  // The gradient of log_decay: x rows [.,dc] whose products with out are summed per token, split in
+  // what comes from other tokens of the same chunk and what comes from the state; or null.
+  const void* x;
+  Strides sx;
+  int gx;
+  float *dot_in, *dot_out;  // [slices][B,H,L]
+  float scale_out, scale_in;
+  bool rev;
+  unsigned* status;
+};
+// A decay that is 0 in fp32 (e^-104 is below half of the smallest number): a document starts.  So
+// no sum of log decays ever holds a number that would swallow the others.
+constexpr float kDecayNone = -104.f;
+// Tokens of a chunk and channels of c that a CTA of the CUDA-core pass takes.
+constexpr int kDecayChunk = 64;
+constexpr int kDecaySlice = 64;
+cudaError_t launch_decay_simt(const DecayPass& a, lizard_dtype dt, cudaStream_t s, int* launches);
+// Sums the heads of a group: out [B,Hk,L,d] T from part [B,Hk*G,L,d] fp32.
+cudaError_t launch_decay_heads(int B, int Hk, int G, int L, int d, const float* part, void* out,
+                               Strides so, lizard_dtype dt, cudaStream_t s, int* launches);
+// d log_decay from the passes' sums (rows: of the pass for q, cols: of the pass for k).
+struct DecayGate {
+  int B, H, L, chunk;
+  int row_slices, col_slices;
+  const float *row_in, *row_out, *col_in, *col_out;  // [slices][B,H,L]
+  const float *h0, *d_h0;                            // [B,H,state], or null
+  int state;
+  const float* lg;
+  Strides sg;
+  const int32_t* count;
+  float* d_lg;
+};
+cudaError_t launch_decay_gate(const DecayGate& a, cudaStream_t s, int* launches);
+struct DecayStep {
+  int B, H, G, L, dk, dv;  // G: query heads per key head
+  const void *q, *k, *v;
+  Strides sq, sk, sv;
+  const float* lg;
+  Strides sg;
+  float* h;
+  void* y;
+  Strides sy;
+  float scale;
+};
+cudaError_t launch_decay_step(const DecayStep& a, lizard_dtype dt, cudaStream_t s, int* launches);
+
+struct NormCall {
+  int N, H, T, d;
+  bool per_head;
+  float eps;
+  const void *x, *w, *b, *dy;  // w, b may be null; dy: backward
+  void* y;                     // y or d_x (may be null in the backward)
+  Strides sx, sdy, sy;
+  float *dw, *db;              // or null
+  float* part;                 // backward: norm_part_floats
+};
+size_t norm_part_floats(int N, int H, int T, int d, bool per_head);
+cudaError_t launch_norm_fwd(const NormCall& a, lizard_dtype dt, cudaStream_t s, int* launches);
+cudaError_t launch_norm_bwd(const NormCall& a, lizard_dtype dt, cudaStream_t s, int* launches);
+
 }  // namespace lz

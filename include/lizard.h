@@ -574,6 +574,116 @@ lizard_status lizard_cache_attn(const lizard_cache* cache, const lizard_cache_at
                                 const lizard_strides* s_add, void* y, const lizard_strides* s_y,
                                 void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * Linear attention with one decay per head and token, next to the gated branch whose decay is
+ * per key channel ("Gated Linear Attention Transformers", arXiv 2312.06635, section 2.2, the
+ * scalar-decay forms; "RetNet", arXiv 2307.08621, section 2.1): a layer whose gate is a number
+ * reads 4 bytes per token and head for it instead of 4 dk.
+ *   h_t = g_t h_{t-1} + k_t v_t^T,   y_t = scale q_t^T h_t,   g_t = exp(log_decay_t),  h_{-1} = h0
+ *   q [B,H,L,dk], k [B,Hk,L,dk], v [B,Hk,L,dv], y [B,H,L,dv] T, all strided as above (query head
+ *   h reads key and value head h / (H / Hk); states, decays and outputs are per query head);
+ *   log_decay [B,H,L] fp32 at n * s.n + h * s.h + t * s.t elements (any fp32 address and strides
+ *   >= 0, 0 repeats: a constant per head has s.n = s.t = 0; NULL: contiguous);
+ *   h0, h_final [B,H,dk,dv] fp32 or NULL (zeros / not wanted);  count [B] int32 or NULL: sequence n
+ *   has its tokens in rows t < count[n] (NULL: all L).  Rows from count[n] on are neither read as
+ *   tokens nor change the state; their y and gradients are written as 0.
+ * log_decay is <= 0 as a rule.  Minus infinity starts a new document: nothing before that token
+ * is seen from it on; so does every value below -104, whose decay is 0 in fp32.  Positive values are accepted as long as the products of the decays between
+ * any two tokens are finite in fp32.  NaN is not accepted, and a token whose q, k, v or dy is not
+ * finite leaves every output of its sequence unspecified.
+ * Sums and states are fp32 throughout.  bf16 calls round, for the tensor cores, the decayed scores
+ * of a 128-token chunk and the state that a chunk starts from to bf16; a state that is returned
+ * and the gradient of log_decay are made from unrounded (three-part) operands.
+ * A count outside 0..L sets LIZARD_ERR_DEVICE_CHECK; its sequence has no tokens.
+ * Workspace: lizard_decay_attn_workspace_bytes, zero before the first call (lizard_workspace_init);
+ * calls ordered one after the other may share one, whatever their shapes, if it is large enough
+ * for each.  Run-to-run identical.
+ */
+typedef struct lizard_decay_dims {
+    int32_t B;            /* sequences, 1..65535 */
+    int32_t H, Hk;        /* query heads; key and value heads (divides H) */
+    int32_t L;            /* tokens per sequence at most, >= 0 */
+    int32_t dk, dv;       /* 64 or 128 each */
+    lizard_dtype dtype;   /* of q, k, v, y, dy, d_q, d_k, d_v */
+    float scale;          /* <= 0 selects 1/sqrt(dk) */
+} lizard_decay_dims;
+
+size_t lizard_decay_attn_workspace_bytes(const lizard_decay_dims* dims, int32_t is_bwd);
+/* L = 0 writes h_final = h0 (or zeros) only. */
+lizard_status lizard_decay_attn_fwd(const lizard_decay_dims* dims, const void* q,
+                                    const lizard_strides* s_q, const void* k,
+                                    const lizard_strides* s_k, const void* v,
+                                    const lizard_strides* s_v, const float* log_decay,
+                                    const lizard_strides* s_decay, const int32_t* count,
+                                    const float* h0, void* y, const lizard_strides* s_y,
+                                    float* h_final, void* workspace, size_t workspace_bytes,
+                                    void* stream);
+
+/*
+ * Gradients of sum(y dy) + sum(h_final d_h_final).
+ *   dy [B,H,L,dv] T; d_h_final [B,H,dk,dv] fp32 or NULL (zeros).
+ *   d_q [B,H,L,dk], d_k [B,Hk,L,dk], d_v [B,Hk,L,dv] T (shared heads summed in fp32);
+ *   d_log_decay [B,H,L] fp32 contiguous or NULL: per token and head, 0 where a document starts;
+ *   the caller of a broadcast decay sums it.  d_h0 [B,H,dk,dv] fp32 or NULL.
+ *   Per token dq = scale h dy, dk = dh v, dv = dh^T k, d log_decay = g <h_{t-1}, dh_t> with
+ *   dh_t = scale q_t dy_t^T + g_{t+1} dh_{t+1}.
+ * L = 0 writes d_h0 = d_h_final (or zeros) only.
+ */
+lizard_status lizard_decay_attn_bwd(const lizard_decay_dims* dims, const void* q,
+                                    const lizard_strides* s_q, const void* k,
+                                    const lizard_strides* s_k, const void* v,
+                                    const lizard_strides* s_v, const float* log_decay,
+                                    const lizard_strides* s_decay, const int32_t* count,
+                                    const float* h0, const void* dy, const lizard_strides* s_dy,
+                                    const float* d_h_final, void* d_q, const lizard_strides* s_dq,
+                                    void* d_k, const lizard_strides* s_dk, void* d_v,
+                                    const lizard_strides* s_dv, float* d_log_decay, float* d_h0,
+                                    void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * The recurrent form for new tokens (L of them for every sequence; one as a rule): h is updated
+ * in place, in fp32 throughout whatever the dtype.  Needs no workspace.  L = 0 is a no-op.
+ */
+lizard_status lizard_decay_attn_step(const lizard_decay_dims* dims, const void* q,
+                                     const lizard_strides* s_q, const void* k,
+                                     const lizard_strides* s_k, const void* v,
+                                     const lizard_strides* s_v, const float* log_decay,
+                                     const lizard_strides* s_decay, float* h, void* y,
+                                     const lizard_strides* s_y, void* stream);
+
+/*
+ * Layer norm of each row of d channels, as it follows a linear attention's heads (a weight per
+ * head) or a block (one weight):
+ *   n = (x - mean x) / sqrt(mean (x - mean x)^2 + eps),   y = n weight + bias
+ *   x, y [N,H,T,d] T, strided as above (rows of a plain matrix: N = H = 1); weight, bias [d] T,
+ *   [H,d] with per_head, contiguous; NULL: 1 and 0.  y may be x itself (same pointer and strides).
+ * The backward reads x again (mean and variance are taken from it, so that nothing is kept
+ * between the calls) and returns
+ *   d_x = (a - mean a - n mean(a n)) / sqrt(..),  a = dy weight;   d_x may be x or dy itself
+ *   d_weight = sum over rows of dy n,  d_bias = sum over rows of dy: fp32, weight's shape; NULL:
+ *   not wanted.  d_x NULL: not wanted.  Summed in a fixed order (run-to-run identical).
+ * Statistics and sums are fp32; the variance is taken around the mean.  T = 0 writes zeros to
+ * d_weight and d_bias only.  Workspace: the backward's, lizard_layer_norm_workspace_bytes.
+ */
+typedef struct lizard_norm_dims {
+    int32_t N, H, T;      /* sequences, heads, tokens (>= 0) */
+    int32_t d;            /* channels of a row, a multiple of 8, 8..16384 */
+    int32_t per_head;     /* weight, bias [H,d] instead of [d] */
+    lizard_dtype dtype;   /* of x, y, dy, d_x, weight, bias */
+    float eps;            /* <= 0 selects 1e-5 */
+} lizard_norm_dims;
+
+size_t lizard_layer_norm_workspace_bytes(const lizard_norm_dims* dims);
+lizard_status lizard_layer_norm_fwd(const lizard_norm_dims* dims, const void* x,
+                                    const lizard_strides* s_x, const void* weight,
+                                    const void* bias, void* y, const lizard_strides* s_y,
+                                    void* stream);
+lizard_status lizard_layer_norm_bwd(const lizard_norm_dims* dims, const void* x,
+                                    const lizard_strides* s_x, const void* weight, const void* dy,
+                                    const lizard_strides* s_dy, void* d_x,
+                                    const lizard_strides* s_dx, float* d_weight, float* d_bias,
+                                    void* workspace, size_t workspace_bytes, void* stream);
+
 /* Static description of a status code. */
 const char* lizard_status_string(lizard_status status);
 
