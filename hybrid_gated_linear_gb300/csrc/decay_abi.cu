@@ -48,17 +48,33 @@ Decays decays_of(const lizard_strides* s, int64_t B, int64_t H, int64_t L) {
 
 // Scratch of a backward call after the header.
 struct BwdScratch {
-  size_t dots, parts, d_h0, bytes;  // offsets, then the size
+  size_t dots, parts, d_h0, segs, bytes;  // offsets, then the size
 };
+size_t seg_bytes(const lizard_decay_dims& d, int da, int dc) {
+  return d.dtype == LIZARD_BF16 && d.L ? lz::align_up(lz::decay_tc_workspace(d.B, d.H, d.L, da, dc), 256) : 0;
+}
+// Planes of [B,H,L] sums for d log_decay: within chunks, and with the states (the tensor-core pass
+// leaves two for each 64 channels), of the rows and of the columns.
+size_t in_planes(const lizard_decay_dims& d) { return d.dk / lz::kDecaySlice; }
+size_t out_planes(const lizard_decay_dims& d) { return 2 * in_planes(d); }
 BwdScratch bwd_scratch(const lizard_decay_dims& d) {
   BwdScratch w;
-  const size_t rows = (size_t)d.B * d.H * d.L, slices = d.dk / lz::kDecaySlice;
+  const size_t rows = (size_t)d.B * d.H * d.L;
   size_t at = 0;
-  w.dots = at, at += lz::align_up(4 * slices * rows * sizeof(float), 256);
+  w.dots = at, at += lz::align_up(2 * (in_planes(d) + out_planes(d)) * rows * sizeof(float), 256);
   w.parts = at, at += d.H > d.Hk ? lz::align_up(rows * (d.dk > d.dv ? d.dk : d.dv) * sizeof(float), 256) : 0;
   w.d_h0 = at, at += (size_t)d.B * d.H * d.dk * d.dv * sizeof(float);
+  w.segs = at, at += std::max(seg_bytes(d, d.dk, d.dv), seg_bytes(d, d.dv, d.dk));
   w.bytes = at;
   return w;
+}
+
+// Whether the tensor cores take rows of these strides (all of a call's, or none).
+bool tc_rows(const lizard_decay_dims& d, const Tensor* t, int n) {
+  if (d.dtype != LIZARD_BF16 || d.L == 0 || !lz::tma_encode_available()) return false;
+  for (int i = 0; i < n; ++i)
+    if (!lz::decay_tc_rows_ok((int)t[i].N, (int)t[i].H, (int)t[i].T, (int)t[i].d, t[i].r->s)) return false;
+  return true;
 }
 
 bool norm_dims_ok(const lizard_norm_dims* d) {
@@ -73,7 +89,7 @@ extern "C" {
 
 size_t lizard_decay_attn_workspace_bytes(const lizard_decay_dims* dims, int32_t is_bwd) {
   if (!decay_dims_ok(dims) || !width_ok(dims->dk) || !width_ok(dims->dv)) return 0;
-  return lz::kWsHeader + (is_bwd ? bwd_scratch(*dims).bytes : 0);
+  return lz::kWsHeader + (is_bwd ? bwd_scratch(*dims).bytes : seg_bytes(*dims, dims->dk, dims->dv));
 }
 
 lizard_status lizard_decay_attn_fwd(const lizard_decay_dims* dims, const void* q, const lizard_strides* s_q,
@@ -119,7 +135,11 @@ lizard_status lizard_decay_attn_fwd(const lizard_decay_dims* dims, const void* q
   a.scale_out = scale_of(d), a.scale_in = 1.f;
   a.status = static_cast<unsigned*>(workspace);
   int launches = 0;
-  const cudaError_t e = lz::launch_decay_simt(a, d.dtype, (cudaStream_t)stream, &launches);
+  const cudaStream_t s = (cudaStream_t)stream;
+  const Tensor in[] = {tq, tk, tv};
+  float* segs = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + lz::kWsHeader);
+  const cudaError_t e = tc_rows(d, in, 3) ? lz::launch_decay_tc(a, false, segs, s, &launches)
+                                          : lz::launch_decay_simt(a, d.dtype, s, &launches);
   return finish(e, launches);
 }
 
@@ -179,13 +199,22 @@ lizard_status lizard_decay_attn_bwd(const lizard_decay_dims* dims, const void* q
   const float scale = scale_of(d);
   const BwdScratch w = bwd_scratch(d);
   unsigned char* ws = static_cast<unsigned char*>(workspace) + lz::kWsHeader;
-  const size_t plane = (size_t)d.B * d.H * d.L * (d.dk / lz::kDecaySlice);
+  const size_t plane = (size_t)d.B * d.H * d.L;
   float* dots = reinterpret_cast<float*>(ws + w.dots);
+  float *row_in = dots, *col_in = row_in + in_planes(d) * plane, *row_out = col_in + in_planes(d) * plane,
+        *col_out = row_out + out_planes(d) * plane;
+  float* segs = reinterpret_cast<float*>(ws + w.segs);
   float* part = reinterpret_cast<float*>(ws + w.parts);
   const cudaStream_t s = (cudaStream_t)stream;
   const bool gate = d_log_decay && !none;
   if (!d_h0 && h0 && gate) d_h0 = reinterpret_cast<float*>(ws + w.d_h0);
+  const bool tc = tc_rows(d, in, 4);
   int launches = 0;
+  // the gradient of log_decay takes the products with the states as results: from exact states
+  auto pass = [&](const lz::DecayPass& p) {
+    return tc ? lz::launch_decay_tc(p, p.x != nullptr, segs, s, &launches)
+              : lz::launch_decay_simt(p, d.dtype, s, &launches);
+  };
   lz::DecayPass a{};
   a.B = d.B, a.H = d.H, a.L = d.L, a.lg = log_decay, a.sg = rg.s, a.count = count;
   a.status = static_cast<unsigned*>(workspace);
@@ -197,7 +226,7 @@ lizard_status lizard_decay_attn_bwd(const lizard_decay_dims* dims, const void* q
   b.scale_out = 1.f, b.scale_in = scale;
   const lz::Strides heads_v{(int64_t)d.H * d.L * d.dv, (int64_t)d.L * d.dv, d.dv};
   b.out = G > 1 ? static_cast<void*>(part) : d_v, b.so = G > 1 ? heads_v : ov.s, b.out_f32 = G > 1;
-  cudaError_t e = lz::launch_decay_simt(b, d.dtype, s, &launches);
+  cudaError_t e = pass(b);
   if (e != cudaSuccess || none) return finish(e, launches);
   if (G > 1) e = lz::launch_decay_heads(d.B, d.Hk, G, d.L, d.dv, part, d_v, ov.s, d.dtype, s, &launches);
   if (e != cudaSuccess) return finish(e, launches);
@@ -209,8 +238,8 @@ lizard_status lizard_decay_attn_bwd(const lizard_decay_dims* dims, const void* q
   b.scale_out = 1.f, b.scale_in = scale;
   const lz::Strides heads_k{(int64_t)d.H * d.L * d.dk, (int64_t)d.L * d.dk, d.dk};
   b.out = G > 1 ? static_cast<void*>(part) : d_k, b.so = G > 1 ? heads_k : ok.s, b.out_f32 = G > 1;
-  if (gate) b.x = k, b.sx = rk.s, b.gx = G, b.dot_in = dots, b.dot_out = dots + plane;
-  e = lz::launch_decay_simt(b, d.dtype, s, &launches);
+  if (gate) b.x = k, b.sx = rk.s, b.gx = G, b.dot_in = col_in, b.dot_out = col_out;
+  e = pass(b);
   if (e == cudaSuccess && G > 1)
     e = lz::launch_decay_heads(d.B, d.Hk, G, d.L, d.dk, part, d_k, ok.s, d.dtype, s, &launches);
   if (e != cudaSuccess) return finish(e, launches);
@@ -221,13 +250,22 @@ lizard_status lizard_decay_attn_bwd(const lizard_decay_dims* dims, const void* q
   b.init = h0, b.state_t = true;
   b.scale_out = scale, b.scale_in = 1.f;
   b.out = d_q, b.so = oq.s;
-  if (gate) b.x = q, b.sx = rq.s, b.gx = 1, b.dot_in = dots + 2 * plane, b.dot_out = dots + 3 * plane;
-  e = lz::launch_decay_simt(b, d.dtype, s, &launches);
+  if (gate) b.x = q, b.sx = rq.s, b.gx = 1, b.dot_in = row_in, b.dot_out = row_out;
+  e = pass(b);
   if (e != cudaSuccess || !gate) return finish(e, launches);
+  if (tc) {
+    lz::DecayPairs pr{};
+    pr.B = d.B, pr.H = d.H, pr.G = G, pr.L = d.L, pr.dk = d.dk, pr.dv = d.dv;
+    pr.q = q, pr.k = k, pr.v = v, pr.dy = dy, pr.sq = rq.s, pr.sk = rk.s, pr.sv = rv.s, pr.sy = ry.s;
+    pr.lg = log_decay, pr.sg = rg.s, pr.count = count, pr.scale = scale;
+    pr.row = row_in, pr.col = col_in, pr.status = a.status;
+    e = lz::launch_decay_pairs(pr, s, &launches);
+    if (e != cudaSuccess) return finish(e, launches);
+  }
   lz::DecayGate g{};
-  g.B = d.B, g.H = d.H, g.L = d.L, g.chunk = lz::kDecayChunk;
-  g.row_slices = g.col_slices = d.dk / lz::kDecaySlice;
-  g.col_in = dots, g.col_out = dots + plane, g.row_in = dots + 2 * plane, g.row_out = dots + 3 * plane;
+  g.B = d.B, g.H = d.H, g.L = d.L, g.chunk = tc ? lz::kDecayTile : lz::kDecayChunk;
+  g.in_slices = tc ? 1 : (int)in_planes(d), g.out_slices = (int)(tc ? out_planes(d) : in_planes(d));
+  g.row_in = row_in, g.col_in = col_in, g.row_out = row_out, g.col_out = col_out;
   g.h0 = h0, g.d_h0 = d_h0, g.state = d.dk * d.dv;
   g.lg = log_decay, g.sg = rg.s, g.count = count, g.d_lg = d_log_decay;
   e = lz::launch_decay_gate(g, s, &launches);

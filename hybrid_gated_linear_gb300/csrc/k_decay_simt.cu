@@ -322,8 +322,8 @@ __global__ void __launch_bounds__(32) decay_gate_kernel(DecayGate a) {
     double rows = 0.0, cols = 0.0;
     bool start = false;
     for (int t = t0 + lane; t < end; t += 32) {
-      for (int s = 0; s < a.row_slices; ++s) rows += a.row_out[s * plane + base + t];
-      for (int s = 0; s < a.col_slices; ++s) cols += a.col_out[s * plane + base + t];
+      for (int s = 0; s < a.out_slices; ++s)
+        rows += a.row_out[s * plane + base + t], cols += a.col_out[s * plane + base + t];
       start |= lg[t * a.sg.t] < kDecayNone;
     }
 #pragma unroll
@@ -340,12 +340,10 @@ __global__ void __launch_bounds__(32) decay_gate_kernel(DecayGate a) {
       float g = 0.f;
       if (t < end) {
         g = lg[t * a.sg.t];
-        for (int s = 0; s < a.row_slices; ++s)
-          suffix += (double)a.row_in[s * plane + base + t] + a.row_out[s * plane + base + t];
-        for (int s = 0; s < a.col_slices; ++s) {
-          suffix -= a.col_in[s * plane + base + t];
-          col += a.col_out[s * plane + base + t];
-        }
+        for (int s = 0; s < a.in_slices; ++s)
+          suffix += (double)a.row_in[s * plane + base + t] - a.col_in[s * plane + base + t];
+        for (int s = 0; s < a.out_slices; ++s)
+          suffix += a.row_out[s * plane + base + t], col += a.col_out[s * plane + base + t];
       }
       // a document's start cuts the sums: nothing behind it passes over the tokens before it
       const bool cut = t < end && g < kDecayNone;

@@ -100,6 +100,11 @@ bool make_tma_map_bf16(CUtensorMap* m, const void* base, uint64_t dim0, uint64_t
 bool make_tma_map_f32(CUtensorMap* m, const void* base, uint64_t dim0, uint64_t dim1,
                       uint64_t dim2, uint32_t box0, uint32_t box1, CUtensorMapSwizzle sw);
 
+// 4D bf16 map over dims (innermost first, contiguous) with byte strides of the outer three, box
+// {box0, box1, 1, 1}, 128-byte swizzle.
+bool make_tma_map_4d_bf16(CUtensorMap* m, const void* base, const uint64_t (&dims)[4], const uint64_t (&strides)[3],
+                          uint32_t box0, uint32_t box1);
+
 // Launches `kernel` on `s` with programmatic stream serialisation, so that its CTAs may
 // start (and run up to pdl_wait) while the previous kernel on the stream drains.
 template <typename... KArgs, typename... Args>
@@ -412,14 +417,36 @@ constexpr float kDecayNone = -104.f;
 constexpr int kDecayChunk = 64;
 constexpr int kDecaySlice = 64;
 cudaError_t launch_decay_simt(const DecayPass& a, lizard_dtype dt, cudaStream_t s, int* launches);
+// The same on the tensor cores: bf16, L > 0, tensors that decay_tc_rows_ok accepts; exact_state: A H from
+// three bf16 parts of the state (dot_out [2 dc / 64][B,H,L]; dot_in is not written).  `ws` of
+// decay_tc_workspace bytes.
+constexpr int kDecayTile = 128;
+bool decay_tc_rows_ok(int B, int H, int L, int d, const Strides& s);
+size_t decay_tc_workspace(int B, int H, int L, int da, int dc);
+cudaError_t launch_decay_tc(const DecayPass& a, bool exact_state, float* ws, cudaStream_t s, int* launches);
+// What each token receives from (row) and gives to (col) other tokens of its chunk in the gradient of
+// log_decay, in 128-token chunks.
+struct DecayPairs {
+  int B, H, G, L, dk, dv;
+  const void *q, *k, *v, *dy;
+  Strides sq, sk, sv, sy;
+  const float* lg;
+  Strides sg;
+  const int32_t* count;
+  float scale;
+  float *row, *col;  // [B,H,L]
+  unsigned* status;
+};
+cudaError_t launch_decay_pairs(const DecayPairs& a, cudaStream_t s, int* launches);
 // Sums the heads of a group: out [B,Hk,L,d] T from part [B,Hk*G,L,d] fp32.
 cudaError_t launch_decay_heads(int B, int Hk, int G, int L, int d, const float* part, void* out,
                                Strides so, lizard_dtype dt, cudaStream_t s, int* launches);
 // d log_decay from the passes' sums (rows: of the pass for q, cols: of the pass for k).
 struct DecayGate {
   int B, H, L, chunk;
-  int row_slices, col_slices;
-  const float *row_in, *row_out, *col_in, *col_out;  // [slices][B,H,L]
+  int in_slices, out_slices;
+  const float *row_in, *col_in;    // [in_slices][B,H,L]
+  const float *row_out, *col_out;  // [out_slices][B,H,L]
   const float *h0, *d_h0;                            // [B,H,state], or null
   int state;
   const float* lg;

@@ -83,6 +83,17 @@ bool make_map(CUtensorMap* m, CUtensorMapDataType dt, uint32_t esize, const void
 }
 }  // namespace
 
+bool make_tma_map_4d_bf16(CUtensorMap* m, const void* base, const uint64_t (&dims)[4], const uint64_t (&strides)[3],
+                          uint32_t box0, uint32_t box1) {
+  EncodeTiled enc = get_encode();
+  if (!enc) return false;
+  const cuuint64_t d[4] = {dims[0], dims[1], dims[2], dims[3]}, st[3] = {strides[0], strides[1], strides[2]};
+  const cuuint32_t box[4] = {box0, box1, 1, 1}, es[4] = {1, 1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), d, st, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool make_tma_map_f32(CUtensorMap* m, const void* base, uint64_t dim0, uint64_t dim1,
                       uint64_t dim2, uint32_t box0, uint32_t box1, CUtensorMapSwizzle sw) {
   return make_map(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, base, dim0, dim1, dim2, box0, box1, sw);
