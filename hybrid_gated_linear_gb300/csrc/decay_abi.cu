@@ -48,7 +48,7 @@ Decays decays_of(const lizard_strides* s, int64_t B, int64_t H, int64_t L) {
 
 // Scratch of a backward call after the header.
 struct BwdScratch {
-  size_t dots, parts, d_h0, segs, bytes;  // offsets, then the size
+  size_t dots, parts, d_h0, segs, sums, bytes;  // offsets, then the size
 };
 size_t seg_bytes(const lizard_decay_dims& d, int da, int dc) {
   return d.dtype == LIZARD_BF16 && d.L ? lz::align_up(lz::decay_tc_workspace(d.B, d.H, d.L, da, dc), 256) : 0;
@@ -63,8 +63,9 @@ BwdScratch bwd_scratch(const lizard_decay_dims& d) {
   size_t at = 0;
   w.dots = at, at += lz::align_up(2 * (in_planes(d) + out_planes(d)) * rows * sizeof(float), 256);
   w.parts = at, at += d.H > d.Hk ? lz::align_up(rows * (d.dk > d.dv ? d.dk : d.dv) * sizeof(float), 256) : 0;
-  w.d_h0 = at, at += (size_t)d.B * d.H * d.dk * d.dv * sizeof(float);
+  w.d_h0 = at, at += (size_t)d.B * d.H * d.dk * d.dv * sizeof(float);  // a multiple of 16 KB
   w.segs = at, at += std::max(seg_bytes(d, d.dk, d.dv), seg_bytes(d, d.dv, d.dk));
+  w.sums = at, at += lz::decay_gate_workspace(d.B, d.H, d.L, lz::kDecayChunk);
   w.bytes = at;
   return w;
 }
@@ -268,6 +269,7 @@ lizard_status lizard_decay_attn_bwd(const lizard_decay_dims* dims, const void* q
   g.row_in = row_in, g.col_in = col_in, g.row_out = row_out, g.col_out = col_out;
   g.h0 = h0, g.d_h0 = d_h0, g.state = d.dk * d.dv;
   g.lg = log_decay, g.sg = rg.s, g.count = count, g.d_lg = d_log_decay;
+  g.sums = reinterpret_cast<double2*>(ws + w.sums);
   e = lz::launch_decay_gate(g, s, &launches);
   return finish(e, launches);
 }

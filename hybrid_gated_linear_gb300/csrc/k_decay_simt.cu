@@ -300,72 +300,110 @@ __global__ void __launch_bounds__(kThreads) decay_heads_kernel(int Hk, int G, in
 //   + through                                              from before the chunk to after it.
 // `through` of the chunks follows from the pairs over the edge before the first one, <h0, d_h0>:
 //   edge after = through + sum col_out,  through = edge before - sum row_out  (0 where a document
-// starts in the chunk).  Sums of a chunk run in 64 bits; one warp for each head and sequence.
-__global__ void __launch_bounds__(32) decay_gate_kernel(DecayGate a) {
+// starts in the chunk).  Sums run in 64 bits.  First a warp for each chunk takes its sums of row_out
+// and col_out and whether a document starts, and a block for each head <h0, d_h0>; then a warp for
+// each chunk adds up the edge in front of it and writes its tokens.
+__device__ __forceinline__ double warp_sum(double x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
+}
+__device__ __forceinline__ int gate_count(const DecayGate& a, int n) {
+  const int c = a.count ? a.count[n] : a.L;
+  return c < 0 || c > a.L ? 0 : c;
+}
+
+constexpr int kGateWarps = 4;
+// sums [units][chunks + 1]: of the chunks (x: rows, y: cols; a start as rows = NaN), then <h0, d_h0>
+__global__ void __launch_bounds__(32 * kGateWarps) decay_gate_sums_kernel(DecayGate a, int chunks) {
   pdl_wait();
-  const int unit = blockIdx.x, lane = threadIdx.x;
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  const int units = a.B * a.H, per = (chunks + kGateWarps - 1) / kGateWarps;
+  if (blockIdx.x < units) {
+    double s = 0.0;
+    if (a.h0) {
+      const float4* x = reinterpret_cast<const float4*>(a.h0 + (int64_t)blockIdx.x * a.state);
+      const float4* y = reinterpret_cast<const float4*>(a.d_h0 + (int64_t)blockIdx.x * a.state);
+#pragma unroll 4
+      for (int i = threadIdx.x; i < a.state / 4; i += 32 * kGateWarps) {
+        const float4 u = x[i], v = y[i];
+        s += (double)(u.x * v.x) + (double)(u.y * v.y) + (double)(u.z * v.z) + (double)(u.w * v.w);
+      }
+    }
+    __shared__ double part[kGateWarps];
+    s = warp_sum(s);
+    if (lane == 0) part[warp] = s;
+    __syncthreads();
+    s = 0.0;
+    for (int w = 0; w < kGateWarps; ++w) s += part[w];
+    if (threadIdx.x == 0) a.sums[(int64_t)blockIdx.x * (chunks + 1) + chunks] = make_double2(s, 0.0);
+    return;
+  }
+  const int unit = (blockIdx.x - units) / per, c = (blockIdx.x - units - unit * per) * kGateWarps + warp;
   const int n = unit / a.H, h = unit - n * a.H;
-  const int64_t plane = (int64_t)a.B * a.H * a.L, base = (int64_t)unit * a.L;
-  int count = a.count ? a.count[n] : a.L;
-  if (count < 0 || count > a.L) count = 0;
-  double edge = 0.0;
-  if (a.h0) {
-    const float *x = a.h0 + (int64_t)unit * a.state, *y = a.d_h0 + (int64_t)unit * a.state;
-    for (int i = lane; i < a.state; i += 32) edge += (double)(x[i] * y[i]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) edge += __shfl_xor_sync(0xffffffffu, edge, o);
-  }
+  const int t0 = c * a.chunk, end = min(t0 + a.chunk, gate_count(a, n));
+  if (t0 >= end) return;
+  const int64_t plane = (int64_t)units * a.L, base = (int64_t)unit * a.L;
   const float* lg = a.lg + n * a.sg.n + h * a.sg.h;
-  for (int t0 = 0; t0 < count; t0 += a.chunk) {
-    // the chunk's groups of 32 tokens from the last to the first, with what lies behind each
-    const int end = min(t0 + a.chunk, count);
-    double rows = 0.0, cols = 0.0;
-    bool start = false;
-    for (int t = t0 + lane; t < end; t += 32) {
-      for (int s = 0; s < a.out_slices; ++s)
-        rows += a.row_out[s * plane + base + t], cols += a.col_out[s * plane + base + t];
-      start |= lg[t * a.sg.t] < kDecayNone;
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      rows += __shfl_xor_sync(0xffffffffu, rows, o);
-      cols += __shfl_xor_sync(0xffffffffu, cols, o);
-    }
-    start = __any_sync(0xffffffffu, start);
-    const double through = start ? 0.0 : edge - rows;
-    double behind = 0.0, before = cols;  // of the suffix sums; col_out of the tokens before the group's end
-    for (int g0 = t0 + (end - t0 - 1) / 32 * 32; g0 >= t0; g0 -= 32) {
-      const int t = g0 + lane;
-      double suffix = 0.0, col = 0.0;
-      float g = 0.f;
-      if (t < end) {
-        g = lg[t * a.sg.t];
-        for (int s = 0; s < a.in_slices; ++s)
-          suffix += (double)a.row_in[s * plane + base + t] - a.col_in[s * plane + base + t];
-        for (int s = 0; s < a.out_slices; ++s)
-          suffix += a.row_out[s * plane + base + t], col += a.col_out[s * plane + base + t];
-      }
-      // a document's start cuts the sums: nothing behind it passes over the tokens before it
-      const bool cut = t < end && g < kDecayNone;
-      double sum = suffix;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const double u = __shfl_down_sync(0xffffffffu, sum, o);
-        if (lane + o < 32) sum += u;
-      }
-      double colsum = col;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const double u = __shfl_down_sync(0xffffffffu, colsum, o);
-        if (lane + o < 32) colsum += u;
-      }
-      if (t < end) a.d_lg[base + t] = cut ? 0.f : (float)(behind + sum + (before - colsum) + through);
-      behind += __shfl_sync(0xffffffffu, sum, 0);
-      before -= __shfl_sync(0xffffffffu, colsum, 0);
-    }
-    edge = through + cols;
+  double rows = 0.0, cols = 0.0;
+  bool start = false;
+  for (int t = t0 + lane; t < end; t += 32) {
+    for (int s = 0; s < a.out_slices; ++s)
+      rows += a.row_out[s * plane + base + t], cols += a.col_out[s * plane + base + t];
+    start |= lg[t * a.sg.t] < kDecayNone;
   }
-  for (int t = count + lane; t < a.L; t += 32) a.d_lg[base + t] = 0.f;
+  rows = warp_sum(rows), cols = warp_sum(cols);
+  start = __any_sync(0xffffffffu, start);
+  if (lane == 0) a.sums[(int64_t)unit * (chunks + 1) + c] = make_double2(start ? nan("") : rows, cols);
+}
+
+__global__ void __launch_bounds__(32 * kGateWarps) decay_gate_kernel(DecayGate a, int chunks) {
+  pdl_wait();
+  const int lane = threadIdx.x % 32, per = (chunks + kGateWarps - 1) / kGateWarps;
+  const int unit = blockIdx.x / per, c = (blockIdx.x - unit * per) * kGateWarps + threadIdx.x / 32;
+  if (c >= chunks) return;
+  const int n = unit / a.H, h = unit - n * a.H, count = gate_count(a, n);
+  const int t0 = c * a.chunk, end = min(t0 + a.chunk, count);
+  const int64_t plane = (int64_t)a.B * a.H * a.L, base = (int64_t)unit * a.L;
+  for (int t = max(t0, count) + lane; t < min(t0 + a.chunk, a.L); t += 32) a.d_lg[base + t] = 0.f;
+  if (t0 >= end) return;
+  // the edge in front of the chunk: 32 chunks at a time, from the last start on
+  const double2* sums = a.sums + (int64_t)unit * (chunks + 1);
+  double edge = sums[chunks].x;
+  for (int k = 0; k < c; k += 32) {
+    double2 s = make_double2(0.0, 0.0);
+    if (k + lane < c) s = sums[k + lane];
+    const unsigned starts = __ballot_sync(0xffffffffu, isnan(s.x));
+    const int last = 31 - __clz(starts);  // -1: none
+    if (starts) edge = 0.0;
+    edge += warp_sum(lane < last ? 0.0 : lane == last ? s.y : s.y - s.x);
+  }
+  const double2 own = sums[c];
+  const double through = isnan(own.x) ? 0.0 : edge - own.x;
+  const float* lg = a.lg + n * a.sg.n + h * a.sg.h;
+  // the chunk's groups of 32 tokens from the last to the first, with what lies behind each
+  double behind = 0.0, before = own.y;  // of the suffix sums; col_out of the tokens before the group's end
+  for (int g0 = t0 + (end - t0 - 1) / 32 * 32; g0 >= t0; g0 -= 32) {
+    const int t = g0 + lane;
+    double sum = 0.0, col = 0.0;
+    bool cut = false;
+    if (t < end) {
+      // a document's start: nothing passes over it
+      cut = lg[t * a.sg.t] < kDecayNone;
+      for (int s = 0; s < a.in_slices; ++s)
+        sum += (double)a.row_in[s * plane + base + t] - a.col_in[s * plane + base + t];
+      for (int s = 0; s < a.out_slices; ++s)
+        sum += a.row_out[s * plane + base + t], col += a.col_out[s * plane + base + t];
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const double u = __shfl_down_sync(0xffffffffu, sum, o), v = __shfl_down_sync(0xffffffffu, col, o);
+      if (lane + o < 32) sum += u, col += v;
+    }
+    if (t < end) a.d_lg[base + t] = cut ? 0.f : (float)(behind + sum + (before - col) + through);
+    behind += __shfl_sync(0xffffffffu, sum, 0);
+    before -= __shfl_sync(0xffffffffu, col, 0);
+  }
 }
 
 template <typename T, int DA>
@@ -409,11 +447,23 @@ cudaError_t launch_decay_heads(int B, int Hk, int G, int L, int d, const float* 
 }
 
 cudaError_t launch_decay_gate(const DecayGate& a, cudaStream_t s, int* launches) {
+  const int chunks = (a.L + a.chunk - 1) / a.chunk;
+  const int64_t units = (int64_t)a.B * a.H, blocks = units * ((chunks + kGateWarps - 1) / kGateWarps);
+  if (units + blocks > 0x7fffffffll) return cudaErrorInvalidValue;
+  trace_begin("decay_gate_sums", s);
+  cudaError_t e = launch_pdl(decay_gate_sums_kernel, dim3((unsigned)(units + blocks)), dim3(32 * kGateWarps), 0, s, a, chunks);
+  trace_end(s);
+  ++*launches;
+  if (e != cudaSuccess) return e;
   trace_begin("decay_gate", s);
-  const cudaError_t e = launch_pdl(decay_gate_kernel, dim3((unsigned)a.B * a.H), dim3(32), 0, s, a);
+  e = launch_pdl(decay_gate_kernel, dim3((unsigned)blocks), dim3(32 * kGateWarps), 0, s, a, chunks);
   trace_end(s);
   ++*launches;
   return e;
+}
+
+size_t decay_gate_workspace(int B, int H, int L, int chunk) {
+  return (size_t)B * H * ((L + chunk - 1) / chunk + 1) * sizeof(double2);
 }
 
 }  // namespace lz

@@ -352,11 +352,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (q.states_only && !(ok = wait_bar(ctl, FB + it % Sm::NBt, (it / Sm::NBt) & 1))) break;
         if (it > 0 && !(ok = wait_bar(ctl, KVF, (it - 1) & 1))) break;
         tc_fence_after();
-        for (int k = 0; k < q.parts; ++k) {
+        // (the smallest parts first, while the sum and what its additions cut off are small)
+        for (int k = q.parts - 1; k >= 0; --k) {
           const uint32_t tp = sb + Sm::CP + k * kTileC;
 #pragma unroll
           for (int j = 0; j < kC / 16; ++j)
-            mma_bf16(tmem + kColKV, desc_mn(tb, kC, j), desc_mn(tp, kC, j), id_kv, k > 0 || j > 0);
+            mma_bf16(tmem + kColKV, desc_mn(tb, kC, j), desc_mn(tp, kC, j), id_kv, k < q.parts - 1 || j > 0);
         }
         mma_commit(&ctl->bar[KVR]);
         mma_commit(&ctl->bar[EB + it % Sm::NBt]);
@@ -372,10 +373,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const uint32_t ta = sb + Sm::A + it % Sm::NA * Sm::kTile;
 #pragma unroll
-        for (int k = 0; k < NPH; ++k)
+        for (int k = NPH - 1; k >= 0; --k)
 #pragma unroll
           for (int j = 0; j < DA / 16; ++j)
-            mma_bf16(tmem + kColYs, desc_k(ta, kC, j), desc_mn(sb + Sm::H + k * Sm::kPartH, DA, j), id_h, k > 0 || j > 0);
+            mma_bf16(tmem + kColYs, desc_k(ta, kC, j), desc_mn(sb + Sm::H + k * Sm::kPartH, DA, j), id_h, k < NPH - 1 || j > 0);
         mma_commit(&ctl->bar[HF]);
         mma_commit(&ctl->bar[EA + it % Sm::NA]);
         // P C

@@ -453,7 +453,9 @@ struct DecayGate {
   Strides sg;
   const int32_t* count;
   float* d_lg;
+  double2* sums;  // decay_gate_workspace bytes
 };
+size_t decay_gate_workspace(int B, int H, int L, int chunk);
 cudaError_t launch_decay_gate(const DecayGate& a, cudaStream_t s, int* launches);
 struct DecayStep {
   int B, H, G, L, dk, dv;  // G: query heads per key head
