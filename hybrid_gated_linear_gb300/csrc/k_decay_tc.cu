@@ -40,20 +40,24 @@ constexpr int kColS = 0, kColP = 256, kColKV = 320, kColY = 384, kColYs = 448;
 enum {
   FA = 0, FB = 2, FC = 4, EA = 6, EB = 8, EC = 10,  // tiles full and empty, by stage
   SR = 12,                                          // scores ready, by buffer
-  CT = 14, KVR, KVF, HR, HF, PR, YR, YF, FACF, FACE, FIX, DONE, NB
+  FACF = 14, FACE = 16,                             // factors full and empty, by buffer
+  CT = 18, KVR, KVF, HR, HF, PR, YR, YF, FIX, DONE, NB
 };
 
+// Of a chunk: x the log2 decays; col the decays from a token to its 16-token block's end (with rev
+// from the block's start to the token); g those over the blocks between [the output's][the source's];
+// head and tail those over the blocks between the chunk's edge where the state enters (leaves) and a
+// block.
 struct alignas(16) Factors {
-  float x[kC];    // log2 of the decays
-  float row[kC], col[kC];
-  float from[kC], to[kC];
-  float g[64];    // [block of the output row][block of the source], the blocks between
+  float x[kC], col[kC];
+  float g[64];
+  float head[8], tail[8];
   float all;
 };
 
 struct Head {  // in front of the tiles
   Ctl<NB> ctl;
-  Factors f;
+  Factors f[2];
 };
 constexpr int kHead = 3072;
 static_assert(sizeof(Head) <= kHead, "barriers and factors");
@@ -90,15 +94,43 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, i
       : "memory");
 }
 
-// D(tmem) (+)= A(tmem) * B(smem)^T ; issued by one thread.
-__device__ __forceinline__ void mma_bf16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate) {
-  const uint32_t acc = accumulate ? 1u : 0u;
+// Operand descriptors of 128-byte-swizzled tiles differ in their lower words only: the address, and the
+// distance of 64-column blocks (K-major operands do not use it).  A k-step of 16 adds to the lower word.
+constexpr uint32_t kDescUpper = (1024u >> 4) | (1u << 14) | (kSw128 << 29);
+__device__ __forceinline__ uint32_t desc_lower(uint32_t saddr, uint32_t block) { return (saddr >> 4) | ((block >> 4) << 16); }
+constexpr uint32_t step_k(int j) { return (uint32_t)(j >> 2) * (kC * 128 / 16) + (uint32_t)(j & 3) * 2; }
+constexpr uint32_t step_mn(int j) { return (uint32_t)j * (16 * 128 / 16); }
+
+// D(tmem) (+)= A(smem) * B(smem)^T, and with A in TMEM.  The whole warp calls and one lane issues, so
+// that addresses and descriptors stay in uniform registers: from a branch that one lane takes, each MMA
+// cost about 90 cycles of moves.
+__device__ __forceinline__ void mma_lo(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(acc)
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 x, y;\n\telect.sync _|q, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\tmov.b64 x, {%1, %3};\n\tmov.b64 y, {%2, %3};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(kDescUpper), "r"(idesc), "r"(accumulate ? 1u : 0u)
       : "memory");
+}
+__device__ __forceinline__ void mma_lo_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 y;\n\telect.sync _|q, 0xffffffff;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\tmov.b64 y, {%2, %3};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(kDescUpper), "r"(idesc), "r"(accumulate ? 1u : 0u)
+      : "memory");
+}
+// elect.sync picks the same lane each time, whose MMAs these are.
+__device__ __forceinline__ void commit_lo(uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
+      : "memory");
+}
+// A wait by a whole warp with one answer.
+template <int N>
+__device__ __forceinline__ bool wait_warp(Ctl<N>* ctl, int i, uint32_t parity) {
+  return __all_sync(0xffffffffu, wait_bar(ctl, i, parity));
 }
 
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
@@ -114,20 +146,50 @@ __device__ __forceinline__ float f32(uint32_t u) { return __uint_as_float(u); }
 __device__ __forceinline__ float lo_f(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float hi_f(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
 
-// Two values as sums of bf16 parts: the nearest, the nearest to what is left, and again.
-__device__ __forceinline__ void split(float a, float b, uint32_t (&o)[3]) {
-  o[0] = pack_bf16x2(a, b);
-  a -= lo_f(o[0]), b -= hi_f(o[0]);
-  o[1] = pack_bf16x2(a, b);
-  a -= lo_f(o[1]), b -= hi_f(o[1]);
-  o[2] = pack_bf16x2(a, b);
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmul.rn.f32x2 z, x, y;\n\t"
+      "mov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+
+// The upper halves of two words, the first's below: two floats cut to bf16.
+__device__ __forceinline__ uint32_t upper(float a, float b) {
+  return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+}
+__device__ __forceinline__ float2 cut(float2 v) {
+  return make_float2(f32(__float_as_uint(v.x) & 0xffff0000u), f32(__float_as_uint(v.y) & 0xffff0000u));
+}
+// Two values as sums of bf16 parts.  Three parts of 8 bits are the whole 24: cut off, the rest is exact
+// each time.  Two: the second is rounded to nearest.
+__device__ __forceinline__ void split(float2 v, bool three, uint32_t (&o)[3]) {
+  const float2 minus = make_float2(-1.f, -1.f);
+  o[0] = upper(v.x, v.y);
+  v = fma2(cut(v), minus, v);
+  if (three) {
+    o[1] = upper(v.x, v.y);
+    v = fma2(cut(v), minus, v);
+    o[2] = upper(v.x, v.y);
+  } else {
+    o[1] = pack_bf16x2(v.x, v.y);
+  }
 }
 
 // One warp: the factors of a chunk from its log decays (log2, minus infinity where a document starts),
 // four tokens a lane, four lanes a block.
-__device__ __forceinline__ void make_factors(const float (&x)[4], float (&pre)[4], float (&suf)[4], float (&in)[4],
-                                             float (&out)[4], float (&g)[2], float& all) {
-  const int lane = threadIdx.x & 31;
+__device__ __forceinline__ void make_factors(const float (&x)[4], bool rev, Factors& f) {
+  const int lane = threadIdx.x & 31, own = lane >> 2;
+  float pre[4], suf[4];
   pre[0] = x[0], pre[1] = pre[0] + x[1], pre[2] = pre[1] + x[2], pre[3] = pre[2] + x[3];
   suf[3] = 0.f, suf[2] = x[3], suf[1] = suf[2] + x[2], suf[0] = suf[1] + x[1];
   float up = pre[3], down = pre[3];
@@ -140,21 +202,22 @@ __device__ __forceinline__ void make_factors(const float (&x)[4], float (&pre)[4
   float before = __shfl_up_sync(0xffffffffu, up, 1, 4), behind = __shfl_down_sync(0xffffffffu, down, 1, 4);
   if ((lane & 3) == 0) before = 0.f;
   if ((lane & 3) == 3) behind = 0.f;
-  float t[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) t[j] = __shfl_sync(0xffffffffu, up, 4 * j + 3);
-  float head = 0.f, tail = 0.f, sum = 0.f;
+  float t[8], sum = 0.f, first = 0.f, last = 0.f;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    if (j < (lane >> 2)) head += t[j];
-    if (j > (lane >> 2)) tail += t[j];
+    t[j] = __shfl_sync(0xffffffffu, up, 4 * j + 3);
+    if (j < own) first += t[j];
+    if (j > own) last += t[j];
     sum += t[j];
   }
+  float c[4];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const float p = pre[k] + before, s = suf[k] + behind;
-    pre[k] = exp2f(p), suf[k] = exp2f(s);
-    in[k] = exp2f(p + head), out[k] = exp2f(s + tail);
+  for (int k = 0; k < 4; ++k) c[k] = exp2f(rev ? pre[k] + before : suf[k] + behind);
+  *reinterpret_cast<float4*>(f.x + 4 * lane) = make_float4(x[0], x[1], x[2], x[3]);
+  *reinterpret_cast<float4*>(f.col + 4 * lane) = make_float4(c[0], c[1], c[2], c[3]);
+  if ((lane & 3) == 0) {
+    f.head[own] = exp2f(rev ? last : first);
+    f.tail[own] = exp2f(rev ? first : last);
   }
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
@@ -163,9 +226,9 @@ __device__ __forceinline__ void make_factors(const float (&x)[4], float (&pre)[4
 #pragma unroll
     for (int k = 0; k < 8; ++k)
       if (k > min(i, j) && k < max(i, j)) between += t[k];
-    g[e] = exp2f(between);
+    f.g[lane + 32 * e] = exp2f(between);
   }
-  all = exp2f(sum);
+  if (lane == 0) f.all = exp2f(sum);
 }
 
 // Four of a chunk's log decays in log2 (a lane's own); past the sequence's end 0.
@@ -179,30 +242,31 @@ __device__ __forceinline__ void load_decays(const float* lg, int64_t st, int t0,
   }
 }
 
-__device__ __forceinline__ void store_factors(Factors& f, bool rev, const float (&x)[4], const float (&pre)[4], const float (&suf)[4],
-                                              const float (&in)[4], const float (&out)[4], const float (&g)[2], float all) {
-  const int lane = threadIdx.x & 31;
-  auto put = [&](float* d, const float (&v)[4]) {
-    *reinterpret_cast<float4*>(d + 4 * lane) = make_float4(v[0], v[1], v[2], v[3]);
-  };
-  put(f.x, x);
-  put(rev ? f.col : f.row, pre);
-  put(rev ? f.row : f.col, suf);
-  put(rev ? f.to : f.from, in);
-  put(rev ? f.from : f.to, out);
-  f.g[lane] = g[0], f.g[lane + 32] = g[1];
-  if (lane == 0) f.all = all;
+// The 16 log2 decays of a block.
+__device__ __forceinline__ void block_x(const float* x, float (&v)[16]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float4 q = *reinterpret_cast<const float4*>(x + 4 * j);
+    v[4 * j] = q.x, v[4 * j + 1] = q.y, v[4 * j + 2] = q.z, v[4 * j + 3] = q.w;
+  }
+}
+
+// log2 of the decay from the edge of token o's block to it: from the block's start with it, or with
+// rev behind it to the block's end.
+__device__ __forceinline__ float row_sum(const float* x, int o, bool rev) {
+  float v[16], sum = 0.f;
+  block_x(x, v);
+#pragma unroll
+  for (int s = 0; s < 16; ++s)
+    if (rev ? s > o : s <= o) sum += v[s];
+  return sum;
 }
 
 // The decays within a 16-token block between token `o` of it and each token s, s <= o (s >= o with
 // rev) and 0 elsewhere; x: the block's log2 decays.
 __device__ __forceinline__ void block_decays(const float* x, int o, bool rev, float (&d)[16]) {
   float v[16];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float4 q = *reinterpret_cast<const float4*>(x + 4 * j);
-    v[4 * j] = q.x, v[4 * j + 1] = q.y, v[4 * j + 2] = q.z, v[4 * j + 3] = q.w;
-  }
+  block_x(x, v);
   float sum = 0.f;
   if (rev) {
 #pragma unroll
@@ -219,18 +283,31 @@ __device__ __forceinline__ void block_decays(const float* x, int o, bool rev, fl
   }
 }
 
-// 16 values to a row of out, as bf16 or fp32.
-__device__ __forceinline__ void put_row(void* out, int64_t at, bool wide, const float (&v)[16]) {
-  if (wide) {
-    float4* d = reinterpret_cast<float4*>(static_cast<float*>(out) + at);
+// The 4 x 4 pieces of 16 bytes that four neighbouring lanes hold of their rows, transposed.
+__device__ __forceinline__ void transpose4(uint4 (&c)[4]) {
+  const int lane = threadIdx.x & 31;
+  auto swap = [&](uint4& lower, uint4& upper, int bit) {
+    const bool up = lane & bit;
+    uint4 t = up ? lower : upper;
+    t.x = __shfl_xor_sync(0xffffffffu, t.x, bit), t.y = __shfl_xor_sync(0xffffffffu, t.y, bit);
+    t.z = __shfl_xor_sync(0xffffffffu, t.z, bit), t.w = __shfl_xor_sync(0xffffffffu, t.w, bit);
+    if (up) lower = t;
+    else upper = t;
+  };
+  swap(c[0], c[1], 1), swap(c[2], c[3], 1);
+  swap(c[0], c[2], 2), swap(c[1], c[3], 2);
+}
+
+// A warp's 32 rows from token t0 on, 64 bytes of each lane's row: four neighbouring lanes store a row's
+// piece together (whole sectors; each lane its own row: 16 of 32 bytes at a time, 1650 against 700
+// cycles a chunk).  Rows from L on are not there.
+__device__ __forceinline__ void put64(unsigned char* out, int64_t pitch, int t0, int L, uint4 (&c)[4]) {
+  const int lane = threadIdx.x & 31;
+  transpose4(c);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) d[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-  } else {
-    uint4* d = reinterpret_cast<uint4*>(static_cast<bf16*>(out) + at);
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-      d[j] = make_uint4(pack_bf16x2(v[8 * j], v[8 * j + 1]), pack_bf16x2(v[8 * j + 2], v[8 * j + 3]),
-                        pack_bf16x2(v[8 * j + 4], v[8 * j + 5]), pack_bf16x2(v[8 * j + 6], v[8 * j + 7]));
+  for (int k = 0; k < 4; ++k) {
+    const int t = t0 + (lane & ~3) + k;
+    if (t < L) *reinterpret_cast<uint4*>(out + t * pitch + (lane & 3) * 16) = c[k];
   }
 }
 
@@ -243,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   Head& hd = *reinterpret_cast<Head*>(smem_raw);
   Ctl<NB>* ctl = &hd.ctl;
   unsigned char* sm = smem_raw + kHead;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   // tiles of the 128-byte swizzle start on 1024 bytes: so does the dynamic part where there is no
   // static one; anything else would be caught here, not computed with
   if ((smem_u32(smem_raw) & 1023u) != 0) {
@@ -259,18 +336,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_relinquish();
   }
   if (tid == 0) {
-    for (int i = FA; i < CT; ++i) mbar_init(&ctl->bar[i], 1);
+    for (int i = FA; i < FACE; ++i) mbar_init(&ctl->bar[i], 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&ctl->bar[FACE + i], kScoreWarps + kStateWarps);
     mbar_init(&ctl->bar[CT], kScoreWarps), mbar_init(&ctl->bar[PR], kScoreWarps), mbar_init(&ctl->bar[FIX], kScoreWarps);
     mbar_init(&ctl->bar[HR], kStateWarps), mbar_init(&ctl->bar[KVF], kStateWarps), mbar_init(&ctl->bar[YF], kStateWarps);
     mbar_init(&ctl->bar[KVR], 1), mbar_init(&ctl->bar[HF], 1), mbar_init(&ctl->bar[YR], 1), mbar_init(&ctl->bar[DONE], 1);
-    mbar_init(&ctl->bar[FACF], 1), mbar_init(&ctl->bar[FACE], kScoreWarps + kStateWarps);
     ctl->abort = 0;
     fence_mbar_init();
   }
   tc_fence_before();
   cta_sync();
   tc_fence_after();
-  const uint32_t tmem = ctl->tmem;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, ctl->tmem, 0);
   pdl_wait();
 
   int count = p.L;
@@ -281,6 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       count = 0;
     }
   }
+  count = __shfl_sync(0xffffffffu, count, 0);  // (known to be the same in the warp)
   // this segment's chunks, in the pass's order from `first` on
   const int chunks = (count + kC - 1) / kC;
   const int done = min(seg * q.cps, chunks), num = min(q.cps, chunks - done);
@@ -293,16 +371,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     if (lane == 0) {
       bool ok = true;
-      uint32_t armed_a[2] = {0, 0}, armed_b[2] = {0, 0}, armed_c[2] = {0, 0};
-      const int na = q.an * n, nb = q.bn * n, nc = q.cn * n, ha = q.ah * (h / p.ga), hb = q.bh * (h / p.gb),
-                hc = q.ch * (h / p.gc);
+      uint32_t armed_a[2] = {0, 0}, armed_b[2] = {0, 0};
+      const int na = q.an * n, nb = q.bn * n, ha = q.ah * (h / p.ga), hb = q.bh * (h / p.gb);
       for (int it = 0; it < num && ok; ++it) {
-        const int t0 = token(it);
-        const int sc = it % Sm::NCt, sb = it % Sm::NBt, sa = it % Sm::NA;
-        if (it >= Sm::NCt && !(ok = wait_bar(ctl, EC + sc, (it / Sm::NCt - 1) & 1))) break;
-        mbar_arrive_expect_tx(&ctl->bar[FC + sc], kTileC);
-        tma_load_4d(sm + Sm::Ct + sc * kTileC, &maps.c, c0, t0, hc, nc, &ctl->bar[FC + sc]);
-        armed_c[0] += sc == 0, armed_c[1] += sc == 1;
+        const int t0 = token(it), sb = it % Sm::NBt, sa = it % Sm::NA;
         if (it >= Sm::NBt && !(ok = wait_bar(ctl, EB + sb, (it / Sm::NBt - 1) & 1))) break;
         mbar_arrive_expect_tx(&ctl->bar[FB + sb], Sm::kTile);
 #pragma unroll
@@ -323,96 +395,118 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int k = 0; k < 2; ++k) {
         drain_bar(ctl, FA + k, armed_a[k], t0);
         drain_bar(ctl, FB + k, armed_b[k], t0);
-        drain_bar(ctl, FC + k, armed_c[k], t0);
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
+    {
       const uint32_t sb = smem_u32(sm);
       const uint32_t id_s = idesc_bf16(kC, kC, false, false), id_kv = idesc_bf16(128, kN, true, true),
                      id_h = idesc_bf16(kC, kN, false, true);
+      constexpr uint32_t kRow = kC * 128;  // bytes of a 64-column block of a tile
+      const uint32_t da = desc_lower(sb + Sm::A, 16), db = desc_lower(sb + Sm::B, 16), dbt = desc_lower(sb + Sm::B, kRow),
+                     dc = desc_lower(sb + Sm::Ct, kRow), dp = desc_lower(sb + Sm::CP, kRow), dh = desc_lower(sb + Sm::H, kRow);
       bool ok = true;
       auto scores = [&](int it) {  // S = A B^T
-        if (!wait_bar(ctl, FA + it % Sm::NA, (it / Sm::NA) & 1) || !wait_bar(ctl, FB + it % Sm::NBt, (it / Sm::NBt) & 1))
+        if (!wait_warp(ctl, FA + it % Sm::NA, (it / Sm::NA) & 1) || !wait_warp(ctl, FB + it % Sm::NBt, (it / Sm::NBt) & 1))
           return false;
-        if (ragged(it) && !wait_bar(ctl, FIX, 0)) return false;
+        if (ragged(it) && !wait_warp(ctl, FIX, 0)) return false;
         tc_fence_after();
-        const uint32_t ta = sb + Sm::A + it % Sm::NA * Sm::kTile, tb = sb + Sm::B + it % Sm::NBt * Sm::kTile;
+        const uint32_t a = da + it % Sm::NA * (Sm::kTile / 16), b = db + it % Sm::NBt * (Sm::kTile / 16);
+        const uint32_t d = tmem + kColS + (it & 1) * 128;
 #pragma unroll
-        for (int j = 0; j < DA / 16; ++j)
-          mma_bf16(tmem + kColS + (it & 1) * 128, desc_k(ta, kC, j), desc_k(tb, kC, j), id_s, j > 0);
-        mma_commit(&ctl->bar[SR + (it & 1)]);
+        for (int j = 0; j < DA / 16; ++j) mma_lo(d, a + step_k(j), b + step_k(j), id_s, j > 0);
+        commit_lo(&ctl->bar[SR + (it & 1)]);
         return true;
       };
       if (num > 0 && !q.states_only) ok = scores(0);
       for (int it = 0; it < num && ok; ++it) {
-        const uint32_t tb = sb + Sm::B + it % Sm::NBt * Sm::kTile, tc_ = sb + Sm::Ct + it % Sm::NCt * kTileC;
         // B^T C~ (the B tile is there: its scores are, or it is waited for)
-        if (!(ok = wait_bar(ctl, CT, it & 1))) break;
-        if (q.states_only && !(ok = wait_bar(ctl, FB + it % Sm::NBt, (it / Sm::NBt) & 1))) break;
-        if (it > 0 && !(ok = wait_bar(ctl, KVF, (it - 1) & 1))) break;
+        if (!(ok = wait_warp(ctl, CT, it & 1))) break;
+        if (q.states_only && !(ok = wait_warp(ctl, FB + it % Sm::NBt, (it / Sm::NBt) & 1))) break;
+        if (it > 0 && !(ok = wait_warp(ctl, KVF, (it - 1) & 1))) break;
         tc_fence_after();
+        const uint32_t b = dbt + it % Sm::NBt * (Sm::kTile / 16);
         // (the smallest parts first, while the sum and what its additions cut off are small)
-        for (int k = q.parts - 1; k >= 0; --k) {
-          const uint32_t tp = sb + Sm::CP + k * kTileC;
+        bool more = false;
+#pragma unroll
+        for (int k = 2; k >= 0; --k) {
+          if (k >= q.parts) continue;
 #pragma unroll
           for (int j = 0; j < kC / 16; ++j)
-            mma_bf16(tmem + kColKV, desc_mn(tb, kC, j), desc_mn(tp, kC, j), id_kv, k < q.parts - 1 || j > 0);
+            mma_lo(tmem + kColKV, b + step_mn(j), dp + k * (kTileC / 16) + step_mn(j), id_kv, more || j > 0);
+          more = true;
         }
-        mma_commit(&ctl->bar[KVR]);
-        mma_commit(&ctl->bar[EB + it % Sm::NBt]);
+        commit_lo(&ctl->bar[KVR]);
+        commit_lo(&ctl->bar[EB + it % Sm::NBt]);
         if (q.states_only) {
-          mma_commit(&ctl->bar[EC + it % Sm::NCt]);
+          commit_lo(&ctl->bar[EC + it % Sm::NCt]);
           continue;
         }
         // the next chunk's scores go first where their B tile can be there already
         if (Sm::NBt > 1 && it + 1 < num && !(ok = scores(it + 1))) break;
         // A H
-        if (!(ok = wait_bar(ctl, HR, it & 1))) break;
-        if (it > 0 && !(ok = wait_bar(ctl, YF, (it - 1) & 1))) break;
+        if (!(ok = wait_warp(ctl, HR, it & 1))) break;
+        if (it > 0 && !(ok = wait_warp(ctl, YF, (it - 1) & 1))) break;
         tc_fence_after();
-        const uint32_t ta = sb + Sm::A + it % Sm::NA * Sm::kTile;
+        const uint32_t a = da + it % Sm::NA * (Sm::kTile / 16);
 #pragma unroll
         for (int k = NPH - 1; k >= 0; --k)
 #pragma unroll
           for (int j = 0; j < DA / 16; ++j)
-            mma_bf16(tmem + kColYs, desc_k(ta, kC, j), desc_mn(sb + Sm::H + k * Sm::kPartH, DA, j), id_h, k < NPH - 1 || j > 0);
-        mma_commit(&ctl->bar[HF]);
-        mma_commit(&ctl->bar[EA + it % Sm::NA]);
+            mma_lo(tmem + kColYs, a + step_k(j), dh + k * (Sm::kPartH / 16) + step_mn(j), id_h, k < NPH - 1 || j > 0);
+        commit_lo(&ctl->bar[HF]);
+        commit_lo(&ctl->bar[EA + it % Sm::NA]);
         // P C
-        if (!(ok = wait_bar(ctl, PR, it & 1))) break;
+        if (!(ok = wait_warp(ctl, PR, it & 1))) break;
         tc_fence_after();
+        const uint32_t c = dc + it % Sm::NCt * (kTileC / 16);
 #pragma unroll
-        for (int j = 0; j < kC / 16; ++j)
-          mma_bf16_ts(tmem + kColY, tmem + kColP + 8 * j, desc_mn(tc_, kC, j), id_h, j > 0);
-        mma_commit(&ctl->bar[YR]);
-        mma_commit(&ctl->bar[EC + it % Sm::NCt]);
+        for (int j = 0; j < kC / 16; ++j) mma_lo_ts(tmem + kColY, tmem + kColP + 8 * j, c + step_mn(j), id_h, j > 0);
+        commit_lo(&ctl->bar[YR]);
+        commit_lo(&ctl->bar[EC + it % Sm::NCt]);
         if (Sm::NBt == 1 && it + 1 < num) ok = scores(it + 1);
       }
       if (!ok) ctl->abort = 1;
-      mma_commit(&ctl->bar[DONE]);
+      commit_lo(&ctl->bar[DONE]);
       drain_bar(ctl, DONE, 1, globaltimer_ns());
+      __syncwarp();
     }
   } else if (warp == 2) {
     const float* lg = p.lg + n * p.sg.n + h * p.sg.h;
     float x[4], nx[4] = {};
     if (num > 0) load_decays(lg, p.sg.t, token(0), count, x);
-    for (int it = 0; it < num; ++it) {
-      float pre[4], suf[4], in[4], out[4], g[2], all;
+    bool ok = true;
+    for (int it = 0; it < num && ok; ++it) {
       if (it + 1 < num) load_decays(lg, p.sg.t, token(it + 1), count, nx);
-      make_factors(x, pre, suf, in, out, g, all);
-      if (it > 0 && !wait_bar(ctl, FACE, (it - 1) & 1)) break;
-      store_factors(hd.f, p.rev, x, pre, suf, in, out, g, all);
+      if (it > 1 && !(ok = wait_bar(ctl, FACE + (it & 1), (it / 2 - 1) & 1))) break;
+      make_factors(x, p.rev, hd.f[it & 1]);
       __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl->bar[FACF]);
+      if (lane == 0) mbar_arrive(&ctl->bar[FACF + (it & 1)]);
 #pragma unroll
       for (int k = 0; k < 4; ++k) x[k] = nx[k];
+    }
+    if (!ok) ctl->abort = 1;
+  } else if (warp == 3) {
+    if (lane == 0) {
+      bool ok = true;
+      uint32_t armed[2] = {0, 0};
+      const int nc = q.cn * n, hc = q.ch * (h / p.gc);
+      for (int it = 0; it < num && ok; ++it) {
+        const int s = it % Sm::NCt;
+        if (it >= Sm::NCt && !(ok = wait_bar(ctl, EC + s, (it / Sm::NCt - 1) & 1))) break;
+        mbar_arrive_expect_tx(&ctl->bar[FC + s], kTileC);
+        tma_load_4d(sm + Sm::Ct + s * kTileC, &maps.c, c0, token(it), hc, nc, &ctl->bar[FC + s]);
+        armed[0] += s == 0, armed[1] += s == 1;
+      }
+      if (!ok) ctl->abort = 1;
+      const uint64_t t0 = globaltimer_ns();
+      drain_bar(ctl, FC, armed[0], t0);
+      drain_bar(ctl, FC + 1, armed[1], t0);
     }
   } else if (warp >= 4 && warp < 12) {
     const int half = (warp - 4) >> 2, qw = warp & 3, wt = tid - 128;  // thread of the group
     const int o = 32 * qw + lane, I = o >> 4;
     const uint32_t tl = (uint32_t)(qw * 32) << 16;
-    const Factors& f = hd.f;
     if (!q.states_only) {  // the part of P that is always 0
       const uint32_t z[16] = {};
 #pragma unroll
@@ -440,52 +534,54 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl->bar[FIX]);
       }
-      if (!(ok = wait_bar(ctl, FACF, it & 1))) break;
+      if (!(ok = wait_bar(ctl, FACF + (it & 1), (it >> 1) & 1))) break;
+      const Factors& f = hd.f[it & 1];
       // C~ (its tiles are free once the chunk before has been multiplied)
       if (it > 0 && !(ok = wait_bar(ctl, KVR, (it - 1) & 1))) break;
 #pragma unroll
       for (int e = 0; e < kTileC / 16 / (32 * kScoreWarps); ++e) {
         const int at = (wt + 32 * kScoreWarps * e) * 16;  // byte of the tile: the swizzle stays as it is
-        const float w = f.to[at >> 7] * p.scale_in;
+        const float w = f.col[at >> 7] * f.tail[at >> 11] * p.scale_in;
+        const float2 w2 = make_float2(w, w);
         const uint4 v = *reinterpret_cast<const uint4*>(tc_ + at);
+        const bool three = q.parts > 2;
         uint32_t o0[3], o1[3], o2[3], o3[3];
-        split(w * lo_f(v.x), w * hi_f(v.x), o0);
-        split(w * lo_f(v.y), w * hi_f(v.y), o1);
-        split(w * lo_f(v.z), w * hi_f(v.z), o2);
-        split(w * lo_f(v.w), w * hi_f(v.w), o3);
+        split(mul2(w2, make_float2(lo_f(v.x), hi_f(v.x))), three, o0);
+        split(mul2(w2, make_float2(lo_f(v.y), hi_f(v.y))), three, o1);
+        split(mul2(w2, make_float2(lo_f(v.z), hi_f(v.z))), three, o2);
+        split(mul2(w2, make_float2(lo_f(v.w), hi_f(v.w))), three, o3);
         unsigned char* d = sm + Sm::CP + at;
         *reinterpret_cast<uint4*>(d) = make_uint4(o0[0], o1[0], o2[0], o3[0]);
         *reinterpret_cast<uint4*>(d + kTileC) = make_uint4(o0[1], o1[1], o2[1], o3[1]);
-        if (q.parts > 2) *reinterpret_cast<uint4*>(d + 2 * kTileC) = make_uint4(o0[2], o1[2], o2[2], o3[2]);
+        if (three) *reinterpret_cast<uint4*>(d + 2 * kTileC) = make_uint4(o0[2], o1[2], o2[2], o3[2]);
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->bar[CT]);
       if (q.states_only) {
-        if (lane == 0) mbar_arrive(&ctl->bar[FACE]);
+        if (lane == 0) mbar_arrive(&ctl->bar[FACE + (it & 1)]);
         continue;
       }
-      // P
+      // P, 32 columns at a time; those of the thread's own 32 rows with the decays within its block
+      const float rf = ex2_approx(row_sum(f.x + 16 * I, lane & 15, p.rev)) * p.scale_in;
       if (!(ok = wait_bar(ctl, SR + (it & 1), (it >> 1) & 1))) break;
-      if (it > 0 && !(ok = wait_bar(ctl, YR, (it - 1) & 1))) break;
       tc_fence_after();
-      const float rf = f.row[o] * p.scale_in;
+      bool free_p = it == 0;
 #pragma unroll 1
       for (int g = half; g < 4; g += 2) {
         if (p.rev ? g < qw : g > qw) continue;
         uint32_t s[32], w[16];
         tmem_ld32(tmem + tl + kColS + (it & 1) * 128 + 32 * g, s);
         if (g != qw) {
+          const float r0 = rf * f.g[I * 8 + 2 * g], r1 = rf * f.g[I * 8 + 2 * g + 1];
           tmem_ld_wait();
 #pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            const float r = rf * f.g[I * 8 + 2 * g + b];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float4 c = *reinterpret_cast<const float4*>(&f.col[32 * g + 16 * b + 4 * j]);
-              w[8 * b + 2 * j] = pack_bf16x2(f32(s[16 * b + 4 * j]) * (r * c.x), f32(s[16 * b + 4 * j + 1]) * (r * c.y));
-              w[8 * b + 2 * j + 1] = pack_bf16x2(f32(s[16 * b + 4 * j + 2]) * (r * c.z), f32(s[16 * b + 4 * j + 3]) * (r * c.w));
-            }
+          for (int j = 0; j < 8; ++j) {
+            const float4 c = *reinterpret_cast<const float4*>(&f.col[32 * g + 4 * j]);
+            const float2 r = j < 4 ? make_float2(r0, r0) : make_float2(r1, r1);
+            const float2 u = mul2(make_float2(f32(s[4 * j]), f32(s[4 * j + 1])), mul2(r, make_float2(c.x, c.y)));
+            const float2 v = mul2(make_float2(f32(s[4 * j + 2]), f32(s[4 * j + 3])), mul2(r, make_float2(c.z, c.w)));
+            w[2 * j] = pack_bf16x2(u.x, u.y), w[2 * j + 1] = pack_bf16x2(v.x, v.y);
           }
         } else {
           float d[16];
@@ -500,16 +596,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = 0; j < 8; ++j) {
               const float2 c = *reinterpret_cast<const float2*>(&f.col[32 * g + 16 * b + 2 * j]);
               const float d0 = own ? d[2 * j] * p.scale_in : r * c.x, d1 = own ? d[2 * j + 1] * p.scale_in : r * c.y;
-              w[8 * b + j] = pack_bf16x2(f32(s[16 * b + 2 * j]) * d0, f32(s[16 * b + 2 * j + 1]) * d1);
+              const float2 u = mul2(make_float2(f32(s[16 * b + 2 * j]), f32(s[16 * b + 2 * j + 1])), make_float2(d0, d1));
+              w[8 * b + j] = pack_bf16x2(u.x, u.y);
             }
           }
         }
+        if (!free_p) {  // the chunk before has been multiplied
+          if (!(ok = wait_bar(ctl, YR, (it - 1) & 1))) break;
+          tc_fence_after();
+          free_p = true;
+        }
         tmem_st16(tmem + tl + kColP + 16 * g, w);
       }
+      // (a warp with nothing to store waits too: no arrival is a chunk ahead of another warp's)
+      if (!ok || (!free_p && !(ok = wait_bar(ctl, YR, (it - 1) & 1)))) break;
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl->bar[PR]), mbar_arrive(&ctl->bar[FACE]);
+      if (lane == 0) mbar_arrive(&ctl->bar[PR]), mbar_arrive(&ctl->bar[FACE + (it & 1)]);
     }
     if (!ok) ctl->abort = 1;
   } else if (warp >= 12) {
@@ -517,7 +621,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int i = 32 * qw + lane;  // row of the state, row of the output
     const bool mine = i < DA;
     const uint32_t tl = tmem + ((uint32_t)(qw * 32) << 16) + 32 * half;
-    const Factors& f = hd.f;
     float x[32];
     auto at = [&](int j) {  // column j of this thread in a state of the caller's
       const int c = c0 + 32 * half + j;
@@ -546,7 +649,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (NPH == 1)
               o[k][0] = pack_bf16x2(x[8 * j + 2 * k], x[8 * j + 2 * k + 1]);
             else
-              split(x[8 * j + 2 * k], x[8 * j + 2 * k + 1], o[k]);
+              split(make_float2(x[8 * j + 2 * k], x[8 * j + 2 * k + 1]), true, o[k]);
           }
           const int c = ((4 * half + j) ^ (i & 7)) * 16;
 #pragma unroll
@@ -565,10 +668,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     float product = 1.f;
     if (num > 0 && !q.states_only) put_state();
     for (int it = 0; it < num && ok; ++it) {
-      if (!(ok = wait_bar(ctl, FACF, it & 1))) break;
-      const float from = f.from[i], all = f.all;
+      if (!(ok = wait_bar(ctl, FACF + (it & 1), (it >> 1) & 1))) break;
+      const Factors& f = hd.f[it & 1];
+      const float from = exp2f(row_sum(f.x + (i & ~15), i & 15, p.rev)) * f.head[i >> 4], all = f.all;
       __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl->bar[FACE]);
+      if (lane == 0) mbar_arrive(&ctl->bar[FACE + (it & 1)]);
       product *= all;
       // H = all H + B^T C~
       if (!(ok = wait_bar(ctl, KVR, it & 1))) break;
@@ -580,8 +684,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl->bar[KVF]);
+        const float2 all2 = make_float2(all, all);
 #pragma unroll
-        for (int j = 0; j < 32; ++j) x[j] = fmaf(all, x[j], f32(kv[j]));
+        for (int j = 0; j < 32; j += 2) {
+          const float2 u = fma2(all2, make_float2(x[j], x[j + 1]), make_float2(f32(kv[j]), f32(kv[j + 1])));
+          x[j] = u.x, x[j + 1] = u.y;
+        }
       }
       if (q.states_only) continue;
       if (it + 1 < num) {
@@ -594,6 +702,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!(ok = wait_bar(ctl, YR, it & 1))) break;
       tc_fence_after();
       float d = 0.f;
+      uint4 w[4];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         uint32_t y[16], ys[16];
@@ -605,24 +714,43 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(&ctl->bar[YF]);
         }
-        float v[16];
         if (px && live) {
           const uint4* xr = reinterpret_cast<const uint4*>(px + t * p.sx.t + 16 * e);
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
             const uint4 u = xr[k];
-            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+            const uint32_t z[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-              d = fmaf(lo_f(w[r]), f32(ys[8 * k + 2 * r]), d);
-              d = fmaf(hi_f(w[r]), f32(ys[8 * k + 2 * r + 1]), d);
+              d = fmaf(lo_f(z[r]), f32(ys[8 * k + 2 * r]), d);
+              d = fmaf(hi_f(z[r]), f32(ys[8 * k + 2 * r + 1]), d);
             }
           }
         }
+        const float2 scale = make_float2(live ? p.scale_out : 0.f, live ? p.scale_out : 0.f), from2 = make_float2(from, from);
+        float2 v[8];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) v[j] = live ? p.scale_out * fmaf(from, f32(ys[j]), f32(y[j])) : 0.f;
-        if (t < p.L) put_row(p.out, so + t * p.so.t + 16 * e, p.out_f32, v);
+        for (int j = 0; j < 8; ++j)
+          v[j] = mul2(scale, fma2(from2, make_float2(f32(ys[2 * j]), f32(ys[2 * j + 1])),
+                                  make_float2(f32(y[2 * j]), f32(y[2 * j + 1]))));
+        if (!live) {  // rows behind the sequence may have held anything
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[j] = make_float2(0.f, 0.f);
+        }
+        if (p.out_f32) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            w[j] = make_uint4(__float_as_uint(v[2 * j].x), __float_as_uint(v[2 * j].y), __float_as_uint(v[2 * j + 1].x),
+                              __float_as_uint(v[2 * j + 1].y));
+          put64(static_cast<unsigned char*>(p.out) + (so + 16 * e) * 4, p.so.t * 4, t - lane, p.L, w);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            w[2 * e + j] = make_uint4(pack_bf16x2(v[4 * j].x, v[4 * j].y), pack_bf16x2(v[4 * j + 1].x, v[4 * j + 1].y),
+                                      pack_bf16x2(v[4 * j + 2].x, v[4 * j + 2].y), pack_bf16x2(v[4 * j + 3].x, v[4 * j + 3].y));
+        }
       }
+      if (!p.out_f32) put64(static_cast<unsigned char*>(p.out) + so * 2, p.so.t * 2, t - lane, p.L, w);
       if (px && live) dot[t] = p.scale_out * from * d;
     }
     if (!ok) ctl->abort = 1;
@@ -640,14 +768,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the rows of whole chunks behind the sequence
       const int all_chunks = (p.L + kC - 1) / kC;
       const int za = max(seg * q.cps, chunks), zb = min((seg + 1) * q.cps, all_chunks);
-      const float z[16] = {};
-      for (int c = za; c < zb; ++c) {
-        const int t = c * kC + i;
-        if (t < p.L) {
-          put_row(p.out, so + t * p.so.t, p.out_f32, z);
-          put_row(p.out, so + t * p.so.t + 16, p.out_f32, z);
+      const int es = p.out_f32 ? 4 : 2;
+      for (int c = za; c < zb; ++c)
+        for (int b = 0; b < es / 2; ++b) {
+          uint4 z[4] = {};
+          put64(static_cast<unsigned char*>(p.out) + (so + 16 * b) * es, p.so.t * es, c * kC + 32 * qw, p.L, z);
         }
-      }
     }
   }
   tc_fence_before();
@@ -711,8 +837,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   using Sm = PairSmem<DK, DV>;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   Ctl<GN>* ctl = reinterpret_cast<Ctl<GN>*>(smem_raw);
-  Factors& f = *reinterpret_cast<Factors*>(smem_raw + 64);
-  static_assert(sizeof(Ctl<GN>) <= 64 && 64 + sizeof(Factors) <= kHead, "barriers and factors");
+  Factors* f = reinterpret_cast<Factors*>(smem_raw + 64);  // of the rows, of the columns
+  static_assert(sizeof(Ctl<GN>) <= 64 && 64 + 2 * sizeof(Factors) <= kHead, "barriers and factors");
   unsigned char* sm = smem_raw + kHead;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if ((smem_u32(smem_raw) & 1023u) != 0) {
@@ -782,19 +908,18 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     const bool rev = warp >= 8;  // the columns: token s receives from the later ones
     const int qw = warp & 3, o = 32 * qw + lane, I = o >> 4;
     if (warp == 4) {
-      float x[4], pre[4], suf[4], in[4], out[4], g[2], all;
+      float x[4];
       load_decays(p.lg + n * p.sg.n + h * p.sg.h, p.sg.t, t0, count, x);
-      make_factors(x, pre, suf, in, out, g, all);
-      store_factors(f, false, x, pre, suf, in, out, g, all);
+      make_factors(x, false, f[0]);
+      make_factors(x, true, f[1]);
     }
     named_sync(1, 256);
-    const float* rowf = rev ? f.col : f.row;
-    const float* colf = rev ? f.row : f.col;
+    const Factors& f_ = f[rev];
     const uint32_t tl = tmem + ((uint32_t)(qw * 32) << 16) + (rev ? 256 : 0);
     const bool ok = wait_bar(ctl, rev ? GT : GS, 0);
     if (ok) {
       tc_fence_after();
-      const float rf = rowf[o];
+      const float rf = exp2f(row_sum(f_.x + 16 * I, lane & 15, rev));
       float sum = 0.f;
 #pragma unroll 1
       for (int g = 0; g < 4; ++g) {
@@ -803,16 +928,16 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         tmem_ld32(tl + 32 * g, s);
         tmem_ld32(tl + 128 + 32 * g, y);
         float d[16];
-        if (g == qw) block_decays(f.x + 16 * I, lane & 15, rev, d);
+        if (g == qw) block_decays(f_.x + 16 * I, lane & 15, rev, d);
         tmem_ld_wait();
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
           const bool own = g == qw && (lane >> 4) == b;
-          const float r = g != qw ? rf * f.g[I * 8 + 2 * g + b] : (rev ? b == 1 : b == 0) ? rf : 0.f;
+          const float r = g != qw ? rf * f_.g[I * 8 + 2 * g + b] : (rev ? b == 1 : b == 0) ? rf : 0.f;
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
             const int e = 32 * g + 16 * b + j;
-            const float w = own ? (e == o ? 0.f : d[j]) : r * colf[e];
+            const float w = own ? (e == o ? 0.f : d[j]) : r * f_.col[e];
             // (a decay of 0 hides the token, and rows behind the sequence may hold anything)
             const float v = f32(s[16 * b + j]) * f32(y[16 * b + j]);
             sum += w != 0.f && t0 + e < count ? w * v : 0.f;
