@@ -6,10 +6,10 @@
 //   S = A B^T,  P = S o D,  out = P C + from o (A H),  H' = all H + B^T (to o C)
 // D the decays between the chunk's tokens, `from` and `to` those between a token and the chunk's edges.
 // Every decay is a product of exponentials of sums of few log decays of one sign: for tokens of
-// different 16-token blocks D = row (edge of its block to the one) G (blocks between) col, within
-// a block the exponential of the running sum.  No difference of sums is formed, so minus infinity
-// (a document's start) and very strong decays need no case of their own, and an element of P costs two
-// multiplications instead of an exponential.
+// different 16-token blocks D = row (edge of its block to the one) G (blocks between) col, so that an
+// element of P costs two multiplications instead of an exponential; within a block it is the exponential
+// of a difference of two sums of at most 16.  A document's start counts as 2^-300, which is 0 in every
+// product: no sum is infinite.
 //
 // A CTA takes 64 of C's channels of one head over the chunks of one segment; H stays in registers in
 // fp32.  Twenty warps:
@@ -44,12 +44,13 @@ enum {
   CT = 18, KVR, KVF, HR, HF, PR, YR, YF, FIX, DONE, NB
 };
 
-// Of a chunk: x the log2 decays; col the decays from a token to its 16-token block's end (with rev
-// from the block's start to the token); g those over the blocks between [the output's][the source's];
-// head and tail those over the blocks between the chunk's edge where the state enters (leaves) and a
-// block.
+// Of a chunk: row, log2 of the decay from the edge of a token's 16-token block to the token (from the
+// block's start with it; with rev from behind it to the block's end), so that between two tokens of a
+// block it is the difference; col the decays from a token to the other edge of its block; g those over
+// the blocks between [the output's][the source's]; head and tail those over the blocks between the
+// chunk's edge where the state enters (leaves) and a block.
 struct alignas(16) Factors {
-  float x[kC], col[kC];
+  float row[kC], col[kC];
   float g[64];
   float head[8], tail[8];
   float all;
@@ -98,8 +99,8 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, i
 // distance of 64-column blocks (K-major operands do not use it).  A k-step of 16 adds to the lower word.
 constexpr uint32_t kDescUpper = (1024u >> 4) | (1u << 14) | (kSw128 << 29);
 __device__ __forceinline__ uint32_t desc_lower(uint32_t saddr, uint32_t block) { return (saddr >> 4) | ((block >> 4) << 16); }
-constexpr uint32_t step_k(int j) { return (uint32_t)(j >> 2) * (kC * 128 / 16) + (uint32_t)(j & 3) * 2; }
-constexpr uint32_t step_mn(int j) { return (uint32_t)j * (16 * 128 / 16); }
+__host__ __device__ constexpr uint32_t step_k(int j) { return (uint32_t)(j >> 2) * (kC * 128 / 16) + (uint32_t)(j & 3) * 2; }
+__host__ __device__ constexpr uint32_t step_mn(int j) { return (uint32_t)j * (16 * 128 / 16); }
 
 // D(tmem) (+)= A(smem) * B(smem)^T, and with A in TMEM.  The whole warp calls and one lane issues, so
 // that addresses and descriptors stay in uniform registers: from a branch that one lane takes, each MMA
@@ -127,19 +128,26 @@ __device__ __forceinline__ void commit_lo(uint64_t* bar) {
       "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
       : "memory");
 }
+// wait_bar with its polling out of line: the roles' loops are long, and what they share should be in the
+// instruction cache once.
+template <int N>
+__device__ __noinline__ bool wait_polls(Ctl<N>* ctl, int i, uint32_t parity) {
+  return wait_bar(ctl, i, parity);
+}
+template <int N>
+__device__ __forceinline__ bool wait_for(Ctl<N>* ctl, int i, uint32_t parity) {
+  return mbar_try_wait(&ctl->bar[i], parity) || wait_polls(ctl, i, parity);
+}
 // A wait by a whole warp with one answer.
 template <int N>
 __device__ __forceinline__ bool wait_warp(Ctl<N>* ctl, int i, uint32_t parity) {
-  return __all_sync(0xffffffffu, wait_bar(ctl, i, parity));
+  return __all_sync(0xffffffffu, wait_for(ctl, i, parity));
 }
 
-__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
 }
 
 __device__ __forceinline__ float f32(uint32_t u) { return __uint_as_float(u); }
@@ -185,51 +193,54 @@ __device__ __forceinline__ void split(float2 v, bool three, uint32_t (&o)[3]) {
   }
 }
 
-// One warp: the factors of a chunk from its log decays (log2, minus infinity where a document starts),
-// four tokens a lane, four lanes a block.
-__device__ __forceinline__ void make_factors(const float (&x)[4], bool rev, Factors& f) {
-  const int lane = threadIdx.x & 31, own = lane >> 2;
-  float pre[4], suf[4];
-  pre[0] = x[0], pre[1] = pre[0] + x[1], pre[2] = pre[1] + x[2], pre[3] = pre[2] + x[3];
-  suf[3] = 0.f, suf[2] = x[3], suf[1] = suf[2] + x[2], suf[0] = suf[1] + x[1];
-  float up = pre[3], down = pre[3];
+// One warp: the factors of a chunk from its log2 decays, four tokens a lane, four lanes a block; a lane's share is made in registers, then stored.
+struct Share {
+  float x[4], row[4], col[4], g[2], head, tail, all;
+  __device__ __forceinline__ void make(bool rev) {
+    const int lane = threadIdx.x & 31, own = lane >> 2;
+    float pre[4], suf[4];
+    pre[0] = x[0], pre[1] = pre[0] + x[1], pre[2] = pre[1] + x[2], pre[3] = pre[2] + x[3];
+    suf[3] = 0.f, suf[2] = x[3], suf[1] = suf[2] + x[2], suf[0] = suf[1] + x[1];
+    float up = pre[3], down = pre[3];
 #pragma unroll
-  for (int o = 1; o < 4; o <<= 1) {
-    const float u = __shfl_up_sync(0xffffffffu, up, o, 4), d = __shfl_down_sync(0xffffffffu, down, o, 4);
-    if ((lane & 3) >= o) up += u;
-    if ((lane & 3) + o < 4) down += d;
+    for (int o = 1; o < 4; o <<= 1) {
+      const float u = __shfl_up_sync(0xffffffffu, up, o, 4), d = __shfl_down_sync(0xffffffffu, down, o, 4);
+      if ((lane & 3) >= o) up += u;
+      if ((lane & 3) + o < 4) down += d;
+    }
+    float before = __shfl_up_sync(0xffffffffu, up, 1, 4), behind = __shfl_down_sync(0xffffffffu, down, 1, 4);
+    if ((lane & 3) == 0) before = 0.f;
+    if ((lane & 3) == 3) behind = 0.f;
+    float sum = 0.f, first = 0.f, last = 0.f, between[2] = {0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float t = __shfl_sync(0xffffffffu, up, 4 * j + 3);
+      if (j < own) first += t;
+      if (j > own) last += t;
+      sum += t;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int a = (lane >> 3) + 4 * e, b = lane & 7;
+        if (j > min(a, b) && j < max(a, b)) between[e] += t;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float p = pre[k] + before, s = suf[k] + behind;
+      row[k] = rev ? s : p, col[k] = exp2f(rev ? p : s);
+    }
+    g[0] = exp2f(between[0]), g[1] = exp2f(between[1]);
+    head = exp2f(rev ? last : first), tail = exp2f(rev ? first : last), all = exp2f(sum);
   }
-  float before = __shfl_up_sync(0xffffffffu, up, 1, 4), behind = __shfl_down_sync(0xffffffffu, down, 1, 4);
-  if ((lane & 3) == 0) before = 0.f;
-  if ((lane & 3) == 3) behind = 0.f;
-  float t[8], sum = 0.f, first = 0.f, last = 0.f;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    t[j] = __shfl_sync(0xffffffffu, up, 4 * j + 3);
-    if (j < own) first += t[j];
-    if (j > own) last += t[j];
-    sum += t[j];
+  __device__ __forceinline__ void put(Factors& f) const {
+    const int lane = threadIdx.x & 31;
+    *reinterpret_cast<float4*>(f.row + 4 * lane) = make_float4(row[0], row[1], row[2], row[3]);
+    *reinterpret_cast<float4*>(f.col + 4 * lane) = make_float4(col[0], col[1], col[2], col[3]);
+    f.g[lane] = g[0], f.g[lane + 32] = g[1];
+    if ((lane & 3) == 0) f.head[lane >> 2] = head, f.tail[lane >> 2] = tail;
+    if (lane == 0) f.all = all;
   }
-  float c[4];
-#pragma unroll
-  for (int k = 0; k < 4; ++k) c[k] = exp2f(rev ? pre[k] + before : suf[k] + behind);
-  *reinterpret_cast<float4*>(f.x + 4 * lane) = make_float4(x[0], x[1], x[2], x[3]);
-  *reinterpret_cast<float4*>(f.col + 4 * lane) = make_float4(c[0], c[1], c[2], c[3]);
-  if ((lane & 3) == 0) {
-    f.head[own] = exp2f(rev ? last : first);
-    f.tail[own] = exp2f(rev ? first : last);
-  }
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const int i = (lane >> 3) + 4 * e, j = lane & 7;
-    float between = 0.f;
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (k > min(i, j) && k < max(i, j)) between += t[k];
-    f.g[lane + 32 * e] = exp2f(between);
-  }
-  if (lane == 0) f.all = exp2f(sum);
-}
+};
 
 // Four of a chunk's log decays in log2 (a lane's own); past the sequence's end 0.
 __device__ __forceinline__ void load_decays(const float* lg, int64_t st, int t0, int count, float (&x)[4]) {
@@ -238,12 +249,12 @@ __device__ __forceinline__ void load_decays(const float* lg, int64_t st, int t0,
   for (int k = 0; k < 4; ++k) {
     const int t = t0 + 4 * lane + k;
     const float g = t < count ? lg[t * st] : 0.f;
-    x[k] = g < kDecayNone ? -INFINITY : g * 1.4426950408889634f;
+    x[k] = g < kDecayNone ? -300.f : g * 1.4426950408889634f;
   }
 }
 
-// The 16 log2 decays of a block.
-__device__ __forceinline__ void block_x(const float* x, float (&v)[16]) {
+// A block's 16 numbers.
+__device__ __forceinline__ void block_of(const float* x, float (&v)[16]) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const float4 q = *reinterpret_cast<const float4*>(x + 4 * j);
@@ -251,22 +262,11 @@ __device__ __forceinline__ void block_x(const float* x, float (&v)[16]) {
   }
 }
 
-// log2 of the decay from the edge of token o's block to it: from the block's start with it, or with
-// rev behind it to the block's end.
-__device__ __forceinline__ float row_sum(const float* x, int o, bool rev) {
-  float v[16], sum = 0.f;
-  block_x(x, v);
-#pragma unroll
-  for (int s = 0; s < 16; ++s)
-    if (rev ? s > o : s <= o) sum += v[s];
-  return sum;
-}
-
 // The decays within a 16-token block between token `o` of it and each token s, s <= o (s >= o with
-// rev) and 0 elsewhere; x: the block's log2 decays.
+// rev) and 0 elsewhere, by running sums; x: the block's log2 decays.
 __device__ __forceinline__ void block_decays(const float* x, int o, bool rev, float (&d)[16]) {
   float v[16];
-  block_x(x, v);
+  block_of(x, v);
   float sum = 0.f;
   if (rev) {
 #pragma unroll
@@ -283,32 +283,18 @@ __device__ __forceinline__ void block_decays(const float* x, int o, bool rev, fl
   }
 }
 
-// The 4 x 4 pieces of 16 bytes that four neighbouring lanes hold of their rows, transposed.
-__device__ __forceinline__ void transpose4(uint4 (&c)[4]) {
+// A warp's 32 rows from token t0 on, 32 bytes of each lane's row: two neighbouring lanes store both of
+// their rows' pieces together, so that every store covers whole sectors.  Rows from L on are not there.
+__device__ __forceinline__ void put32(unsigned char* out, int64_t pitch, int t0, int L, uint4 a, uint4 b) {
   const int lane = threadIdx.x & 31;
-  auto swap = [&](uint4& lower, uint4& upper, int bit) {
-    const bool up = lane & bit;
-    uint4 t = up ? lower : upper;
-    t.x = __shfl_xor_sync(0xffffffffu, t.x, bit), t.y = __shfl_xor_sync(0xffffffffu, t.y, bit);
-    t.z = __shfl_xor_sync(0xffffffffu, t.z, bit), t.w = __shfl_xor_sync(0xffffffffu, t.w, bit);
-    if (up) lower = t;
-    else upper = t;
-  };
-  swap(c[0], c[1], 1), swap(c[2], c[3], 1);
-  swap(c[0], c[2], 2), swap(c[1], c[3], 2);
-}
-
-// A warp's 32 rows from token t0 on, 64 bytes of each lane's row: four neighbouring lanes store a row's
-// piece together (whole sectors; each lane its own row: 16 of 32 bytes at a time, 1650 against 700
-// cycles a chunk).  Rows from L on are not there.
-__device__ __forceinline__ void put64(unsigned char* out, int64_t pitch, int t0, int L, uint4 (&c)[4]) {
-  const int lane = threadIdx.x & 31;
-  transpose4(c);
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int t = t0 + (lane & ~3) + k;
-    if (t < L) *reinterpret_cast<uint4*>(out + t * pitch + (lane & 3) * 16) = c[k];
-  }
+  const bool odd = lane & 1;
+  uint4 u = odd ? a : b;
+  u.x = __shfl_xor_sync(0xffffffffu, u.x, 1), u.y = __shfl_xor_sync(0xffffffffu, u.y, 1);
+  u.z = __shfl_xor_sync(0xffffffffu, u.z, 1), u.w = __shfl_xor_sync(0xffffffffu, u.w, 1);
+  const int t = t0 + (lane & ~1);
+  unsigned char* o = out + t * pitch + (odd ? 16 : 0);
+  if (t < L) *reinterpret_cast<uint4*>(o) = odd ? u : a;
+  if (t + 1 < L) *reinterpret_cast<uint4*>(o + pitch) = odd ? b : u;
 }
 
 template <int DA, int NPH>
@@ -375,14 +361,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int na = q.an * n, nb = q.bn * n, ha = q.ah * (h / p.ga), hb = q.bh * (h / p.gb);
       for (int it = 0; it < num && ok; ++it) {
         const int t0 = token(it), sb = it % Sm::NBt, sa = it % Sm::NA;
-        if (it >= Sm::NBt && !(ok = wait_bar(ctl, EB + sb, (it / Sm::NBt - 1) & 1))) break;
+        if (it >= Sm::NBt && !(ok = wait_for(ctl, EB + sb, (it / Sm::NBt - 1) & 1))) break;
         mbar_arrive_expect_tx(&ctl->bar[FB + sb], Sm::kTile);
 #pragma unroll
         for (int k = 0; k < DA / 64; ++k)
           tma_load_4d(sm + Sm::B + sb * Sm::kTile + k * (kC * 128), &maps.b, 64 * k, t0, hb, nb, &ctl->bar[FB + sb]);
         armed_b[0] += sb == 0, armed_b[1] += sb == 1;
         if (q.states_only) continue;
-        if (it >= Sm::NA && !(ok = wait_bar(ctl, EA + sa, (it / Sm::NA - 1) & 1))) break;
+        if (it >= Sm::NA && !(ok = wait_for(ctl, EA + sa, (it / Sm::NA - 1) & 1))) break;
         mbar_arrive_expect_tx(&ctl->bar[FA + sa], Sm::kTile);
 #pragma unroll
         for (int k = 0; k < DA / 64; ++k)
@@ -413,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const uint32_t a = da + it % Sm::NA * (Sm::kTile / 16), b = db + it % Sm::NBt * (Sm::kTile / 16);
         const uint32_t d = tmem + kColS + (it & 1) * 128;
-#pragma unroll
+#pragma unroll 4
         for (int j = 0; j < DA / 16; ++j) mma_lo(d, a + step_k(j), b + step_k(j), id_s, j > 0);
         commit_lo(&ctl->bar[SR + (it & 1)]);
         return true;
@@ -428,10 +414,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t b = dbt + it % Sm::NBt * (Sm::kTile / 16);
         // (the smallest parts first, while the sum and what its additions cut off are small)
         bool more = false;
-#pragma unroll
-        for (int k = 2; k >= 0; --k) {
-          if (k >= q.parts) continue;
-#pragma unroll
+#pragma unroll 1
+        for (int k = q.parts - 1; k >= 0; --k) {
+#pragma unroll 4
           for (int j = 0; j < kC / 16; ++j)
             mma_lo(tmem + kColKV, b + step_mn(j), dp + k * (kTileC / 16) + step_mn(j), id_kv, more || j > 0);
           more = true;
@@ -449,9 +434,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (it > 0 && !(ok = wait_warp(ctl, YF, (it - 1) & 1))) break;
         tc_fence_after();
         const uint32_t a = da + it % Sm::NA * (Sm::kTile / 16);
-#pragma unroll
+#pragma unroll 1
         for (int k = NPH - 1; k >= 0; --k)
-#pragma unroll
+#pragma unroll 4
           for (int j = 0; j < DA / 16; ++j)
             mma_lo(tmem + kColYs, a + step_k(j), dh + k * (Sm::kPartH / 16) + step_mn(j), id_h, k < NPH - 1 || j > 0);
         commit_lo(&ctl->bar[HF]);
@@ -460,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!(ok = wait_warp(ctl, PR, it & 1))) break;
         tc_fence_after();
         const uint32_t c = dc + it % Sm::NCt * (kTileC / 16);
-#pragma unroll
+#pragma unroll 4
         for (int j = 0; j < kC / 16; ++j) mma_lo_ts(tmem + kColY, tmem + kColP + 8 * j, c + step_mn(j), id_h, j > 0);
         commit_lo(&ctl->bar[YR]);
         commit_lo(&ctl->bar[EC + it % Sm::NCt]);
@@ -473,17 +458,20 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 2) {
     const float* lg = p.lg + n * p.sg.n + h * p.sg.h;
-    float x[4], nx[4] = {};
-    if (num > 0) load_decays(lg, p.sg.t, token(0), count, x);
+    Share f;
+    if (num > 0) load_decays(lg, p.sg.t, token(0), count, f.x);
     bool ok = true;
+#pragma unroll 1
     for (int it = 0; it < num && ok; ++it) {
-      if (it + 1 < num) load_decays(lg, p.sg.t, token(it + 1), count, nx);
-      if (it > 1 && !(ok = wait_bar(ctl, FACE + (it & 1), (it / 2 - 1) & 1))) break;
-      make_factors(x, p.rev, hd.f[it & 1]);
+      float next[4] = {};
+      if (it + 1 < num) load_decays(lg, p.sg.t, token(it + 1), count, next);
+      f.make(p.rev);
+      if (it > 1 && !(ok = wait_for(ctl, FACE + (it & 1), (it / 2 - 1) & 1))) break;
+      f.put(hd.f[it & 1]);
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->bar[FACF + (it & 1)]);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) x[k] = nx[k];
+      for (int k = 0; k < 4; ++k) f.x[k] = next[k];
     }
     if (!ok) ctl->abort = 1;
   } else if (warp == 3) {
@@ -493,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int nc = q.cn * n, hc = q.ch * (h / p.gc);
       for (int it = 0; it < num && ok; ++it) {
         const int s = it % Sm::NCt;
-        if (it >= Sm::NCt && !(ok = wait_bar(ctl, EC + s, (it / Sm::NCt - 1) & 1))) break;
+        if (it >= Sm::NCt && !(ok = wait_for(ctl, EC + s, (it / Sm::NCt - 1) & 1))) break;
         mbar_arrive_expect_tx(&ctl->bar[FC + s], kTileC);
         tma_load_4d(sm + Sm::Ct + s * kTileC, &maps.c, c0, token(it), hc, nc, &ctl->bar[FC + s]);
         armed[0] += s == 0, armed[1] += s == 1;
@@ -507,20 +495,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int half = (warp - 4) >> 2, qw = warp & 3, wt = tid - 128;  // thread of the group
     const int o = 32 * qw + lane, I = o >> 4;
     const uint32_t tl = (uint32_t)(qw * 32) << 16;
-    if (!q.states_only) {  // the part of P that is always 0
-      const uint32_t z[16] = {};
-#pragma unroll
-      for (int g = 0; g < 4; ++g)
-        if ((g & 1) == half && (p.rev ? g < qw : g > qw)) tmem_st16(tmem + tl + kColP + 16 * g, z);
+    // Of the 16-token blocks of sources, a warp's rows see `full` ones wholly, from `j0` on every other
+    // one (its half of them), and take part in two, of which it has j1: the decays within a block for
+    // the rows that lie in it, for the others all of it or nothing.  The rest of P is always 0.
+    const int full = p.rev ? 3 - qw : qw, j0 = p.rev ? 2 * qw + 2 + half : half, j1 = 2 * qw + half;
+    const bool own = (lane >> 4) == half, sees = p.rev ? half == 1 : half == 0;
+    if (!q.states_only) {
+      const uint32_t z[8] = {};
+      for (int j = half; j < 8; j += 2)
+        if (p.rev ? j < 2 * qw : j > 2 * qw + 1) tmem_st8(tmem + tl + kColP + 8 * j, z);
       tmem_st_wait();
     }
     bool ok = true;
+#pragma unroll 1
     for (int it = 0; it < num && ok; ++it) {
       const int valid = min(kC, count - token(it));
       unsigned char* tc_ = sm + Sm::Ct + it % Sm::NCt * kTileC;
-      if (!(ok = wait_bar(ctl, FC + it % Sm::NCt, (it / Sm::NCt) & 1))) break;
+      if (!(ok = wait_for(ctl, FC + it % Sm::NCt, (it / Sm::NCt) & 1))) break;
       if (ragged(it)) {
-        if (!(ok = wait_bar(ctl, FB + it % Sm::NBt, (it / Sm::NBt) & 1))) break;
+        if (!(ok = wait_for(ctl, FB + it % Sm::NBt, (it / Sm::NBt) & 1))) break;
         unsigned char* tb = sm + Sm::B + it % Sm::NBt * Sm::kTile;
         const uint4 z = make_uint4(0, 0, 0, 0);
         // (each thread the same places of C that it reads below)
@@ -534,11 +527,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl->bar[FIX]);
       }
-      if (!(ok = wait_bar(ctl, FACF + (it & 1), (it >> 1) & 1))) break;
+      if (!(ok = wait_for(ctl, FACF + (it & 1), (it >> 1) & 1))) break;
       const Factors& f = hd.f[it & 1];
       // C~ (its tiles are free once the chunk before has been multiplied)
-      if (it > 0 && !(ok = wait_bar(ctl, KVR, (it - 1) & 1))) break;
-#pragma unroll
+      if (it > 0 && !(ok = wait_for(ctl, KVR, (it - 1) & 1))) break;
+#pragma unroll 1
       for (int e = 0; e < kTileC / 16 / (32 * kScoreWarps); ++e) {
         const int at = (wt + 32 * kScoreWarps * e) * 16;  // byte of the tile: the swizzle stays as it is
         const float w = f.col[at >> 7] * f.tail[at >> 11] * p.scale_in;
@@ -562,54 +555,52 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(&ctl->bar[FACE + (it & 1)]);
         continue;
       }
-      // P, 32 columns at a time; those of the thread's own 32 rows with the decays within its block
-      const float rf = ex2_approx(row_sum(f.x + 16 * I, lane & 15, p.rev)) * p.scale_in;
-      if (!(ok = wait_bar(ctl, SR + (it & 1), (it >> 1) & 1))) break;
-      tc_fence_after();
-      bool free_p = it == 0;
-#pragma unroll 1
-      for (int g = half; g < 4; g += 2) {
-        if (p.rev ? g < qw : g > qw) continue;
-        uint32_t s[32], w[16];
-        tmem_ld32(tmem + tl + kColS + (it & 1) * 128 + 32 * g, s);
-        if (g != qw) {
-          const float r0 = rf * f.g[I * 8 + 2 * g], r1 = rf * f.g[I * 8 + 2 * g + 1];
-          tmem_ld_wait();
+      // P, 16 columns at a time
+      const float row = f.row[o], rf = ex2_approx(row) * p.scale_in;
+      const uint32_t ts = tmem + tl + kColS + (it & 1) * 128, tp = tmem + tl + kColP;
+      float d[16];
+      block_of((own ? f.row : f.col) + 16 * j1, d);
+      const int io = lane & 15;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float4 c = *reinterpret_cast<const float4*>(&f.col[32 * g + 4 * j]);
-            const float2 r = j < 4 ? make_float2(r0, r0) : make_float2(r1, r1);
-            const float2 u = mul2(make_float2(f32(s[4 * j]), f32(s[4 * j + 1])), mul2(r, make_float2(c.x, c.y)));
-            const float2 v = mul2(make_float2(f32(s[4 * j + 2]), f32(s[4 * j + 3])), mul2(r, make_float2(c.z, c.w)));
-            w[2 * j] = pack_bf16x2(u.x, u.y), w[2 * j + 1] = pack_bf16x2(v.x, v.y);
-          }
-        } else {
-          float d[16];
-          block_decays(f.x + 16 * I, lane & 15, p.rev, d);
-          tmem_ld_wait();
-#pragma unroll
-          for (int b = 0; b < 2; ++b) {
-            const bool own = (lane >> 4) == b;
-            // the other block of the pair: seen by the later tokens (the earlier ones with rev)
-            const float r = (p.rev ? b == 1 : b == 0) ? rf : 0.f;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const float2 c = *reinterpret_cast<const float2*>(&f.col[32 * g + 16 * b + 2 * j]);
-              const float d0 = own ? d[2 * j] * p.scale_in : r * c.x, d1 = own ? d[2 * j + 1] * p.scale_in : r * c.y;
-              const float2 u = mul2(make_float2(f32(s[16 * b + 2 * j]), f32(s[16 * b + 2 * j + 1])), make_float2(d0, d1));
-              w[8 * b + j] = pack_bf16x2(u.x, u.y);
-            }
-          }
-        }
-        if (!free_p) {  // the chunk before has been multiplied
-          if (!(ok = wait_bar(ctl, YR, (it - 1) & 1))) break;
-          tc_fence_after();
-          free_p = true;
-        }
-        tmem_st16(tmem + tl + kColP + 16 * g, w);
+      for (int k = 0; k < 16; ++k) {
+        const float e = (p.rev ? k >= io : k <= io) ? ex2_approx(row - d[k]) * p.scale_in : 0.f;
+        d[k] = own ? e : sees ? rf * d[k] : 0.f;
       }
-      // (a warp with nothing to store waits too: no arrival is a chunk ahead of another warp's)
-      if (!ok || (!free_p && !(ok = wait_bar(ctl, YR, (it - 1) & 1)))) break;
+      if (!(ok = wait_warp(ctl, SR + (it & 1), (it >> 1) & 1))) break;
+      if (it > 0 && !(ok = wait_warp(ctl, YR, (it - 1) & 1))) break;  // the chunk before has been multiplied
+      tc_fence_after();
+      {
+        uint32_t s[16], w[8];
+        tmem_ld16(ts + 16 * j1, s);
+        tmem_ld_wait();
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float2 u = mul2(make_float2(f32(s[2 * k]), f32(s[2 * k + 1])), make_float2(d[2 * k], d[2 * k + 1]));
+          w[k] = pack_bf16x2(u.x, u.y);
+        }
+        tmem_st8(tp + 8 * j1, w);
+      }
+#pragma unroll 1
+      for (int k = 0; k < full; ++k) {
+        const int j = j0 + 2 * k;
+        uint32_t s[16], w[8];
+        tmem_ld16(ts + 16 * j, s);
+        const float r1 = rf * f.g[I * 8 + j];
+        const float2 r = make_float2(r1, r1);
+        float2 c[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float4 v = *reinterpret_cast<const float4*>(&f.col[16 * j + 4 * e]);
+          c[2 * e] = mul2(r, make_float2(v.x, v.y)), c[2 * e + 1] = mul2(r, make_float2(v.z, v.w));
+        }
+        tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float2 u = mul2(make_float2(f32(s[2 * e]), f32(s[2 * e + 1])), c[e]);
+          w[e] = pack_bf16x2(u.x, u.y);
+        }
+        tmem_st8(tp + 8 * j, w);
+      }
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
@@ -622,10 +613,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool mine = i < DA;
     const uint32_t tl = tmem + ((uint32_t)(qw * 32) << 16) + 32 * half;
     float x[32];
-    auto at = [&](int j) {  // column j of this thread in a state of the caller's
-      const int c = c0 + 32 * half + j;
-      return (int64_t)unit * DA * p.dc + (p.state_t ? (int64_t)c * DA + i : (int64_t)i * p.dc + c);
-    };
+    // this thread's columns in a state of the caller's
+    const int c1 = c0 + 32 * half, state_step = p.state_t ? DA : 1;
+    const int64_t state_at = (int64_t)unit * DA * p.dc + (p.state_t ? c1 * DA + i : i * p.dc + c1);
     float* seg_h = q.seg_h + ((((int64_t)seg * units + unit) * slices + slice) * DA + i) * kN + 32 * half;
 #pragma unroll
     for (int j = 0; j < 32; ++j) x[j] = 0.f;
@@ -635,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = 0; j < 32; ++j) x[j] = seg_h[j];
       } else if (p.init) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) x[j] = p.init[at(j)];
+        for (int j = 0; j < 32; ++j) x[j] = p.init[state_at + j * state_step];
       }
     }
     auto put_state = [&]() {  // the parts of H for A H: rows of 64 channels, swizzled
@@ -667,15 +657,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     float product = 1.f;
     if (num > 0 && !q.states_only) put_state();
+#pragma unroll 1
     for (int it = 0; it < num && ok; ++it) {
-      if (!(ok = wait_bar(ctl, FACF + (it & 1), (it >> 1) & 1))) break;
+      if (!(ok = wait_for(ctl, FACF + (it & 1), (it >> 1) & 1))) break;
       const Factors& f = hd.f[it & 1];
-      const float from = exp2f(row_sum(f.x + (i & ~15), i & 15, p.rev)) * f.head[i >> 4], all = f.all;
+      const float from = exp2f(f.row[i]) * f.head[i >> 4], all = f.all;
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->bar[FACE + (it & 1)]);
       product *= all;
       // H = all H + B^T C~
-      if (!(ok = wait_bar(ctl, KVR, it & 1))) break;
+      if (!(ok = wait_for(ctl, KVR, it & 1))) break;
       tc_fence_after();
       {
         uint32_t kv[32];
@@ -693,17 +684,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (q.states_only) continue;
       if (it + 1 < num) {
-        if (!(ok = wait_bar(ctl, HF, it & 1))) break;
+        if (!(ok = wait_for(ctl, HF, it & 1))) break;
         put_state();
       }
       // out = P C + from o (A H)
       const int t = token(it) + i;
       const bool live = t < count;
-      if (!(ok = wait_bar(ctl, YR, it & 1))) break;
+      if (!(ok = wait_for(ctl, YR, it & 1))) break;
       tc_fence_after();
       float d = 0.f;
-      uint4 w[4];
-#pragma unroll
+      const float2 scale = make_float2(p.scale_out, p.scale_out), from2 = make_float2(from, from);
+#pragma unroll 1
       for (int e = 0; e < 2; ++e) {
         uint32_t y[16], ys[16];
         tmem_ld16(tl + kColY + 16 * e, y);
@@ -714,7 +705,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(&ctl->bar[YF]);
         }
-        if (px && live) {
+        if (NPH == 3 && px && live) {
           const uint4* xr = reinterpret_cast<const uint4*>(px + t * p.sx.t + 16 * e);
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
@@ -727,31 +718,29 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        const float2 scale = make_float2(live ? p.scale_out : 0.f, live ? p.scale_out : 0.f), from2 = make_float2(from, from);
         float2 v[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
+        for (int j = 0; j < 8; ++j) {
           v[j] = mul2(scale, fma2(from2, make_float2(f32(ys[2 * j]), f32(ys[2 * j + 1])),
                                   make_float2(f32(y[2 * j]), f32(y[2 * j + 1]))));
-        if (!live) {  // rows behind the sequence may have held anything
-#pragma unroll
-          for (int j = 0; j < 8; ++j) v[j] = make_float2(0.f, 0.f);
+          if (!live) v[j] = make_float2(0.f, 0.f);  // rows behind the sequence may have held anything
         }
         if (p.out_f32) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            w[j] = make_uint4(__float_as_uint(v[2 * j].x), __float_as_uint(v[2 * j].y), __float_as_uint(v[2 * j + 1].x),
-                              __float_as_uint(v[2 * j + 1].y));
-          put64(static_cast<unsigned char*>(p.out) + (so + 16 * e) * 4, p.so.t * 4, t - lane, p.L, w);
+          unsigned char* o = static_cast<unsigned char*>(p.out) + (so + 16 * e) * 4;
+          auto bits = [&](int j) {
+            return make_uint4(__float_as_uint(v[j].x), __float_as_uint(v[j].y), __float_as_uint(v[j + 1].x), __float_as_uint(v[j + 1].y));
+          };
+          put32(o, p.so.t * 4, t - lane, p.L, bits(0), bits(2));
+          put32(o + 32, p.so.t * 4, t - lane, p.L, bits(4), bits(6));
         } else {
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-            w[2 * e + j] = make_uint4(pack_bf16x2(v[4 * j].x, v[4 * j].y), pack_bf16x2(v[4 * j + 1].x, v[4 * j + 1].y),
-                                      pack_bf16x2(v[4 * j + 2].x, v[4 * j + 2].y), pack_bf16x2(v[4 * j + 3].x, v[4 * j + 3].y));
+          auto bits = [&](int j) {
+            return make_uint4(pack_bf16x2(v[j].x, v[j].y), pack_bf16x2(v[j + 1].x, v[j + 1].y), pack_bf16x2(v[j + 2].x, v[j + 2].y),
+                              pack_bf16x2(v[j + 3].x, v[j + 3].y));
+          };
+          put32(static_cast<unsigned char*>(p.out) + (so + 16 * e) * 2, p.so.t * 2, t - lane, p.L, bits(0), bits(4));
         }
       }
-      if (!p.out_f32) put64(static_cast<unsigned char*>(p.out) + so * 2, p.so.t * 2, t - lane, p.L, w);
-      if (px && live) dot[t] = p.scale_out * from * d;
+      if (NPH == 3 && px && live) dot[t] = p.scale_out * from * d;
     }
     if (!ok) ctl->abort = 1;
     if (ok && q.states_only) {
@@ -763,17 +752,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (ok) {
       if (mine && p.fin && seg == q.segs - 1) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) p.fin[at(j)] = x[j];
+        for (int j = 0; j < 32; ++j) p.fin[state_at + j * state_step] = x[j];
       }
       // the rows of whole chunks behind the sequence
       const int all_chunks = (p.L + kC - 1) / kC;
       const int za = max(seg * q.cps, chunks), zb = min((seg + 1) * q.cps, all_chunks);
       const int es = p.out_f32 ? 4 : 2;
+      const uint4 z = make_uint4(0, 0, 0, 0);
       for (int c = za; c < zb; ++c)
-        for (int b = 0; b < es / 2; ++b) {
-          uint4 z[4] = {};
-          put64(static_cast<unsigned char*>(p.out) + (so + 16 * b) * es, p.so.t * es, c * kC + 32 * qw, p.L, z);
-        }
+        for (int b = 0; b < es; ++b)
+          put32(static_cast<unsigned char*>(p.out) + so * es + 32 * b, p.so.t * es, c * kC + 32 * qw, p.L, z, z);
     }
   }
   tc_fence_before();
@@ -838,6 +826,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   Ctl<GN>* ctl = reinterpret_cast<Ctl<GN>*>(smem_raw);
   Factors* f = reinterpret_cast<Factors*>(smem_raw + 64);  // of the rows, of the columns
+  __shared__ __align__(16) float x[kC];
   static_assert(sizeof(Ctl<GN>) <= 64 && 64 + 2 * sizeof(Factors) <= kHead, "barriers and factors");
   unsigned char* sm = smem_raw + kHead;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -884,7 +873,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   } else if (warp == 1) {
     if (lane == 0) {
       const uint32_t sb = smem_u32(sm), id = idesc_bf16(kC, kC, false, false);
-      bool ok = wait_bar(ctl, GF, 0);
+      bool ok = wait_for(ctl, GF, 0);
       if (ok) {
         tc_fence_after();
 #pragma unroll
@@ -908,18 +897,21 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     const bool rev = warp >= 8;  // the columns: token s receives from the later ones
     const int qw = warp & 3, o = 32 * qw + lane, I = o >> 4;
     if (warp == 4) {
-      float x[4];
-      load_decays(p.lg + n * p.sg.n + h * p.sg.h, p.sg.t, t0, count, x);
-      make_factors(x, false, f[0]);
-      make_factors(x, true, f[1]);
+      Share v;
+      load_decays(p.lg + n * p.sg.n + h * p.sg.h, p.sg.t, t0, count, v.x);
+      *reinterpret_cast<float4*>(x + 4 * lane) = make_float4(v.x[0], v.x[1], v.x[2], v.x[3]);
+      v.make(false);
+      v.put(f[0]);
+      v.make(true);
+      v.put(f[1]);
     }
     named_sync(1, 256);
     const Factors& f_ = f[rev];
     const uint32_t tl = tmem + ((uint32_t)(qw * 32) << 16) + (rev ? 256 : 0);
-    const bool ok = wait_bar(ctl, rev ? GT : GS, 0);
+    const bool ok = wait_for(ctl, rev ? GT : GS, 0);
     if (ok) {
       tc_fence_after();
-      const float rf = exp2f(row_sum(f_.x + 16 * I, lane & 15, rev));
+      const float rf = exp2f(f_.row[o]);
       float sum = 0.f;
 #pragma unroll 1
       for (int g = 0; g < 4; ++g) {
@@ -928,7 +920,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         tmem_ld32(tl + 32 * g, s);
         tmem_ld32(tl + 128 + 32 * g, y);
         float d[16];
-        if (g == qw) block_decays(f_.x + 16 * I, lane & 15, rev, d);
+        if (g == qw) block_decays(x + 16 * I, lane & 15, rev, d);
         tmem_ld_wait();
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
