@@ -20,7 +20,9 @@
 //          sequence, so its operands are not rounded), then P, rounded once to bf16, into TMEM
 //   12-19  the state: H = all H + (B^T C~); its bf16 parts for the next chunk's A H (one part, as P is
 //          rounded too, or three where the product with H itself is a result); then the rows of out
-// TMEM: S twice 2 x 128 columns, P 64, B^T C~ 64, P C 64, A H 64.
+// TMEM: S 128 columns, P 64, B^T C~ 3 x 64 (its parts side by side: one reading of B for all of them),
+// P C 64, A H 64.
+// The shared memory's bandwidth bounds it: the MMAs read their operands there.
 #include "lizard_dev.cuh"
 #include "lizard_internal.h"
 #include "tc_pipe.cuh"
@@ -35,13 +37,13 @@ constexpr int kN = 64;           // channels of c of a CTA
 constexpr int kThreads = 640;
 constexpr int kScoreWarps = 8, kStateWarps = 8;
 constexpr int kTileC = kC * kN * 2;
-constexpr int kColS = 0, kColP = 256, kColKV = 320, kColY = 384, kColYs = 448;
+constexpr int kColS = 0, kColP = 128, kColKV = 192, kColY = 384, kColYs = 448;
 
 enum {
   FA = 0, FB = 2, FC = 4, EA = 6, EB = 8, EC = 10,  // tiles full and empty, by stage
-  SR = 12,                                          // scores ready, by buffer
-  FACF = 14, FACE = 16,                             // factors full and empty, by buffer
-  CT = 18, KVR, KVF, HR, HF, PR, YR, YF, FIX, DONE, NB
+  FACF = 12, FACE = 14,                             // factors full and empty, by buffer
+  CT = 16, KVR = 18, KVF = 20,                      // C~ ready, B^T C~ ready, read; by parity
+  SR = 22, HR, HF, PR, YR, YF, FIX, DONE, NB
 };
 
 // Of a chunk: row, log2 of the decay from the edge of a token's 16-token block to the token (from the
@@ -70,7 +72,10 @@ struct Smem {
   static constexpr int A = 0, B = A + NA * kTile, Ct = B + NBt * kTile, CP = Ct + NCt * kTileC;
   static constexpr int kPartH = DA * kN * 2;
   static constexpr int H = CP + 3 * kTileC;
-  static constexpr int kBytes = kHead + H + NPH * kPartH;
+  // a second place for the parts of C~ where there is no A (the state pass)
+  static constexpr int CP2 = DA == 128 ? A : H + NPH * kPartH;
+  static constexpr int kBytes = kHead + (DA == 128 ? H + NPH * kPartH : CP2 + 3 * kTileC);
+  static_assert(DA != 128 || NA * kTile >= 3 * kTileC, "the second place lies over the tiles of A");
   static_assert(kBytes <= 232448, "shared memory of a CTA");
 };
 
@@ -128,11 +133,29 @@ __device__ __forceinline__ void commit_lo(uint64_t* bar) {
       "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
       : "memory");
 }
-// wait_bar with its polling out of line: the roles' loops are long, and what they share should be in the
-// instruction cache once.
+// wait_bar with its polling out of line (the roles' loops are long, and what they share should be in the
+// instruction cache once) and a hint of how long the hardware may suspend a try (every poll reads shared
+// memory).
 template <int N>
 __device__ __noinline__ bool wait_polls(Ctl<N>* ctl, int i, uint32_t parity) {
-  return wait_bar(ctl, i, parity);
+  const uint32_t bar = smem_u32(&ctl->bar[i]);
+  const long long t0 = clock64();
+  while (true) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(20000u)
+        : "memory");
+    if (ok) return true;
+    if (*(volatile int*)&ctl->abort) return false;
+    if (clock64() - t0 > kWaitCycles) {
+      *(volatile int*)&ctl->abort = 1;
+      return false;
+    }
+  }
 }
 template <int N>
 __device__ __forceinline__ bool wait_for(Ctl<N>* ctl, int i, uint32_t parity) {
@@ -142,6 +165,13 @@ __device__ __forceinline__ bool wait_for(Ctl<N>* ctl, int i, uint32_t parity) {
 template <int N>
 __device__ __forceinline__ bool wait_warp(Ctl<N>* ctl, int i, uint32_t parity) {
   return __all_sync(0xffffffffu, wait_for(ctl, i, parity));
+}
+
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr)
+               : "memory");
 }
 
 __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
@@ -283,18 +313,26 @@ __device__ __forceinline__ void block_decays(const float* x, int o, bool rev, fl
   }
 }
 
-// A warp's 32 rows from token t0 on, 32 bytes of each lane's row: two neighbouring lanes store both of
-// their rows' pieces together, so that every store covers whole sectors.  Rows from L on are not there.
-__device__ __forceinline__ void put32(unsigned char* out, int64_t pitch, int t0, int L, uint4 a, uint4 b) {
+// A warp's 32 rows from token t0 on, 64 bytes of each lane's row: four neighbouring lanes exchange their
+// pieces of 16 and store each row's together (whole sectors, and a quarter of the lines a store).  Rows
+// from L on are not there.
+__device__ __forceinline__ void put64(unsigned char* out, int64_t pitch, int t0, int L, uint4 (&c)[4]) {
   const int lane = threadIdx.x & 31;
-  const bool odd = lane & 1;
-  uint4 u = odd ? a : b;
-  u.x = __shfl_xor_sync(0xffffffffu, u.x, 1), u.y = __shfl_xor_sync(0xffffffffu, u.y, 1);
-  u.z = __shfl_xor_sync(0xffffffffu, u.z, 1), u.w = __shfl_xor_sync(0xffffffffu, u.w, 1);
-  const int t = t0 + (lane & ~1);
-  unsigned char* o = out + t * pitch + (odd ? 16 : 0);
-  if (t < L) *reinterpret_cast<uint4*>(o) = odd ? u : a;
-  if (t + 1 < L) *reinterpret_cast<uint4*>(o + pitch) = odd ? b : u;
+  auto swap = [&](uint4& lower, uint4& upper, int bit) {
+    const bool up = lane & bit;
+    uint4 t = up ? lower : upper;
+    t.x = __shfl_xor_sync(0xffffffffu, t.x, bit), t.y = __shfl_xor_sync(0xffffffffu, t.y, bit);
+    t.z = __shfl_xor_sync(0xffffffffu, t.z, bit), t.w = __shfl_xor_sync(0xffffffffu, t.w, bit);
+    if (up) lower = t;
+    else upper = t;
+  };
+  swap(c[0], c[1], 1), swap(c[2], c[3], 1);
+  swap(c[0], c[2], 2), swap(c[1], c[3], 2);
+  const int t = t0 + (lane & ~3);
+  unsigned char* o = out + t * pitch + (lane & 3) * 16;
+#pragma unroll
+  for (int k = 0; k < 4; ++k, o += pitch)
+    if (t + k < L) *reinterpret_cast<uint4*>(o) = c[k];
 }
 
 template <int DA, int NPH>
@@ -322,11 +360,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_relinquish();
   }
   if (tid == 0) {
-    for (int i = FA; i < FACE; ++i) mbar_init(&ctl->bar[i], 1);
-    for (int i = 0; i < 2; ++i) mbar_init(&ctl->bar[FACE + i], kScoreWarps + kStateWarps);
-    mbar_init(&ctl->bar[CT], kScoreWarps), mbar_init(&ctl->bar[PR], kScoreWarps), mbar_init(&ctl->bar[FIX], kScoreWarps);
-    mbar_init(&ctl->bar[HR], kStateWarps), mbar_init(&ctl->bar[KVF], kStateWarps), mbar_init(&ctl->bar[YF], kStateWarps);
-    mbar_init(&ctl->bar[KVR], 1), mbar_init(&ctl->bar[HF], 1), mbar_init(&ctl->bar[YR], 1), mbar_init(&ctl->bar[DONE], 1);
+    for (int i = 0; i < NB; ++i) {
+      const bool both = i == FACE || i == FACE + 1, score = i == CT || i == CT + 1 || i == PR || i == FIX,
+                 state = i == KVF || i == KVF + 1 || i == HR || i == YF;
+      mbar_init(&ctl->bar[i], both ? kScoreWarps + kStateWarps : score ? kScoreWarps : state ? kStateWarps : 1);
+    }
     ctl->abort = 0;
     fence_mbar_init();
   }
@@ -386,54 +424,46 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {
     {
       const uint32_t sb = smem_u32(sm);
-      const uint32_t id_s = idesc_bf16(kC, kC, false, false), id_kv = idesc_bf16(128, kN, true, true),
+      const uint32_t id_s = idesc_bf16(kC, kC, false, false), id_kv = idesc_bf16(128, q.parts * kN, true, true),
                      id_h = idesc_bf16(kC, kN, false, true);
       constexpr uint32_t kRow = kC * 128;  // bytes of a 64-column block of a tile
+      static_assert(kRow == kTileC, "the parts of C~ are the blocks of one operand");
       const uint32_t da = desc_lower(sb + Sm::A, 16), db = desc_lower(sb + Sm::B, 16), dbt = desc_lower(sb + Sm::B, kRow),
-                     dc = desc_lower(sb + Sm::Ct, kRow), dp = desc_lower(sb + Sm::CP, kRow), dh = desc_lower(sb + Sm::H, kRow);
+                     dc = desc_lower(sb + Sm::Ct, kRow), dp = desc_lower(sb + Sm::CP, kRow),
+                     dp2 = desc_lower(sb + Sm::CP2, kRow), dh = desc_lower(sb + Sm::H, kRow);
       bool ok = true;
-      auto scores = [&](int it) {  // S = A B^T
-        if (!wait_warp(ctl, FA + it % Sm::NA, (it / Sm::NA) & 1) || !wait_warp(ctl, FB + it % Sm::NBt, (it / Sm::NBt) & 1))
-          return false;
-        if (ragged(it) && !wait_warp(ctl, FIX, 0)) return false;
-        tc_fence_after();
-        const uint32_t a = da + it % Sm::NA * (Sm::kTile / 16), b = db + it % Sm::NBt * (Sm::kTile / 16);
-        const uint32_t d = tmem + kColS + (it & 1) * 128;
-#pragma unroll 4
-        for (int j = 0; j < DA / 16; ++j) mma_lo(d, a + step_k(j), b + step_k(j), id_s, j > 0);
-        commit_lo(&ctl->bar[SR + (it & 1)]);
-        return true;
-      };
-      if (num > 0 && !q.states_only) ok = scores(0);
-      for (int it = 0; it < num && ok; ++it) {
-        // B^T C~ (the B tile is there: its scores are, or it is waited for)
-        if (!(ok = wait_warp(ctl, CT, it & 1))) break;
-        if (q.states_only && !(ok = wait_warp(ctl, FB + it % Sm::NBt, (it / Sm::NBt) & 1))) break;
-        if (it > 0 && !(ok = wait_warp(ctl, KVF, (it - 1) & 1))) break;
-        tc_fence_after();
-        const uint32_t b = dbt + it % Sm::NBt * (Sm::kTile / 16);
-        // (the smallest parts first, while the sum and what its additions cut off are small)
-        bool more = false;
 #pragma unroll 1
-        for (int k = q.parts - 1; k >= 0; --k) {
+      for (int it = 0; it < num && ok; ++it) {
+        const uint32_t a = da + it % Sm::NA * (Sm::kTile / 16), b = it % Sm::NBt * (Sm::kTile / 16);
+        if (!(ok = wait_warp(ctl, FB + it % Sm::NBt, (it / Sm::NBt) & 1))) break;
+        if (!q.states_only) {
+          // S = A B^T (the last one has been read: P C has been issued)
+          if (!(ok = wait_warp(ctl, FA + it % Sm::NA, (it / Sm::NA) & 1))) break;
+          if (ragged(it) && !(ok = wait_warp(ctl, FIX, 0))) break;
+          tc_fence_after();
 #pragma unroll 4
-          for (int j = 0; j < kC / 16; ++j)
-            mma_lo(tmem + kColKV, b + step_mn(j), dp + k * (kTileC / 16) + step_mn(j), id_kv, more || j > 0);
-          more = true;
+          for (int j = 0; j < DA / 16; ++j) mma_lo(tmem + kColS, a + step_k(j), db + b + step_k(j), id_s, j > 0);
+          commit_lo(&ctl->bar[SR]);
         }
-        commit_lo(&ctl->bar[KVR]);
+        // B^T C~, into alternate columns where there are no scores
+        const bool other = q.states_only && (it & 1);
+        if (!(ok = wait_warp(ctl, CT + (it & 1), (it >> 1) & 1))) break;
+        const int lag = q.states_only ? 2 : 1;
+        if (it >= lag && !(ok = wait_warp(ctl, KVF + ((it - lag) & 1), ((it - lag) >> 1) & 1))) break;
+        tc_fence_after();
+#pragma unroll 4
+        for (int j = 0; j < kC / 16; ++j)
+          mma_lo(tmem + (other ? 0 : kColKV), dbt + b + step_mn(j), (other ? dp2 : dp) + step_mn(j), id_kv, j > 0);
+        commit_lo(&ctl->bar[KVR + (it & 1)]);
         commit_lo(&ctl->bar[EB + it % Sm::NBt]);
         if (q.states_only) {
           commit_lo(&ctl->bar[EC + it % Sm::NCt]);
           continue;
         }
-        // the next chunk's scores go first where their B tile can be there already
-        if (Sm::NBt > 1 && it + 1 < num && !(ok = scores(it + 1))) break;
-        // A H
+        // A H, the smallest parts first, while the sum and what its additions cut off are small
         if (!(ok = wait_warp(ctl, HR, it & 1))) break;
         if (it > 0 && !(ok = wait_warp(ctl, YF, (it - 1) & 1))) break;
         tc_fence_after();
-        const uint32_t a = da + it % Sm::NA * (Sm::kTile / 16);
 #pragma unroll 1
         for (int k = NPH - 1; k >= 0; --k)
 #pragma unroll 4
@@ -449,7 +479,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = 0; j < kC / 16; ++j) mma_lo_ts(tmem + kColY, tmem + kColP + 8 * j, c + step_mn(j), id_h, j > 0);
         commit_lo(&ctl->bar[YR]);
         commit_lo(&ctl->bar[EC + it % Sm::NCt]);
-        if (Sm::NBt == 1 && it + 1 < num) ok = scores(it + 1);
       }
       if (!ok) ctl->abort = 1;
       commit_lo(&ctl->bar[DONE]);
@@ -529,8 +558,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!(ok = wait_for(ctl, FACF + (it & 1), (it >> 1) & 1))) break;
       const Factors& f = hd.f[it & 1];
-      // C~ (its tiles are free once the chunk before has been multiplied)
-      if (it > 0 && !(ok = wait_for(ctl, KVR, (it - 1) & 1))) break;
+      // C~ (its tiles are free once the chunk before has been multiplied; with two places the one before it)
+      const int lag = q.states_only ? 2 : 1;
+      if (it >= lag && !(ok = wait_for(ctl, KVR + ((it - lag) & 1), ((it - lag) >> 1) & 1))) break;
+      unsigned char* cp = sm + (q.states_only && (it & 1) ? Sm::CP2 : Sm::CP);
 #pragma unroll 1
       for (int e = 0; e < kTileC / 16 / (32 * kScoreWarps); ++e) {
         const int at = (wt + 32 * kScoreWarps * e) * 16;  // byte of the tile: the swizzle stays as it is
@@ -543,21 +574,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         split(mul2(w2, make_float2(lo_f(v.y), hi_f(v.y))), three, o1);
         split(mul2(w2, make_float2(lo_f(v.z), hi_f(v.z))), three, o2);
         split(mul2(w2, make_float2(lo_f(v.w), hi_f(v.w))), three, o3);
-        unsigned char* d = sm + Sm::CP + at;
+        unsigned char* d = cp + at;
         *reinterpret_cast<uint4*>(d) = make_uint4(o0[0], o1[0], o2[0], o3[0]);
         *reinterpret_cast<uint4*>(d + kTileC) = make_uint4(o0[1], o1[1], o2[1], o3[1]);
         if (three) *reinterpret_cast<uint4*>(d + 2 * kTileC) = make_uint4(o0[2], o1[2], o2[2], o3[2]);
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl->bar[CT]);
+      if (lane == 0) mbar_arrive(&ctl->bar[CT + (it & 1)]);
       if (q.states_only) {
         if (lane == 0) mbar_arrive(&ctl->bar[FACE + (it & 1)]);
         continue;
       }
       // P, 16 columns at a time
       const float row = f.row[o], rf = ex2_approx(row) * p.scale_in;
-      const uint32_t ts = tmem + tl + kColS + (it & 1) * 128, tp = tmem + tl + kColP;
+      const uint32_t ts = tmem + tl + kColS, tp = tmem + tl + kColP;
       float d[16];
       block_of((own ? f.row : f.col) + 16 * j1, d);
       const int io = lane & 15;
@@ -566,7 +597,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float e = (p.rev ? k >= io : k <= io) ? ex2_approx(row - d[k]) * p.scale_in : 0.f;
         d[k] = own ? e : sees ? rf * d[k] : 0.f;
       }
-      if (!(ok = wait_warp(ctl, SR + (it & 1), (it >> 1) & 1))) break;
+      if (!(ok = wait_warp(ctl, SR, it & 1))) break;
       if (it > 0 && !(ok = wait_warp(ctl, YR, (it - 1) & 1))) break;  // the chunk before has been multiplied
       tc_fence_after();
       {
@@ -665,23 +696,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->bar[FACE + (it & 1)]);
       product *= all;
-      // H = all H + B^T C~
-      if (!(ok = wait_for(ctl, KVR, it & 1))) break;
+      // H = all H + B^T C~, whose parts are added up from the smallest
+      if (!(ok = wait_for(ctl, KVR + (it & 1), (it >> 1) & 1))) break;
       tc_fence_after();
-      {
-        uint32_t kv[32];
-        tmem_ld32(tl + kColKV, kv);
-        tmem_ld_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl->bar[KVF]);
-        const float2 all2 = make_float2(all, all);
+      const uint32_t tk = tl + (q.states_only && (it & 1) ? 0 : kColKV);
+      const float2 all2 = make_float2(all, all);
 #pragma unroll
-        for (int j = 0; j < 32; j += 2) {
-          const float2 u = fma2(all2, make_float2(x[j], x[j + 1]), make_float2(f32(kv[j]), f32(kv[j + 1])));
-          x[j] = u.x, x[j + 1] = u.y;
+      for (int e = 0; e < 4; ++e) {
+        uint32_t k0[8], k1[8], k2[8] = {};
+        tmem_ld8(tk + 8 * e, k0);
+        tmem_ld8(tk + kN + 8 * e, k1);
+        if (q.parts > 2) tmem_ld8(tk + 2 * kN + 8 * e, k2);
+        tmem_ld_wait();
+        const float2 one = make_float2(1.f, 1.f);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float* h2 = &x[8 * e + 2 * j];
+          const float2 v = fma2(one, make_float2(f32(k2[2 * j]), f32(k2[2 * j + 1])), make_float2(f32(k1[2 * j]), f32(k1[2 * j + 1])));
+          const float2 w = fma2(one, v, make_float2(f32(k0[2 * j]), f32(k0[2 * j + 1])));
+          const float2 u = fma2(all2, make_float2(h2[0], h2[1]), w);
+          h2[0] = u.x, h2[1] = u.y;
         }
       }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->bar[KVF + (it & 1)]);
       if (q.states_only) continue;
       if (it + 1 < num) {
         if (!(ok = wait_for(ctl, HF, it & 1))) break;
@@ -693,6 +732,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!(ok = wait_for(ctl, YR, it & 1))) break;
       tc_fence_after();
       float d = 0.f;
+      uint4 w[4];
       const float2 scale = make_float2(p.scale_out, p.scale_out), from2 = make_float2(from, from);
 #pragma unroll 1
       for (int e = 0; e < 2; ++e) {
@@ -730,16 +770,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           auto bits = [&](int j) {
             return make_uint4(__float_as_uint(v[j].x), __float_as_uint(v[j].y), __float_as_uint(v[j + 1].x), __float_as_uint(v[j + 1].y));
           };
-          put32(o, p.so.t * 4, t - lane, p.L, bits(0), bits(2));
-          put32(o + 32, p.so.t * 4, t - lane, p.L, bits(4), bits(6));
+          uint4 c[4] = {bits(0), bits(2), bits(4), bits(6)};
+          put64(o, p.so.t * 4, t - lane, p.L, c);
         } else {
           auto bits = [&](int j) {
             return make_uint4(pack_bf16x2(v[j].x, v[j].y), pack_bf16x2(v[j + 1].x, v[j + 1].y), pack_bf16x2(v[j + 2].x, v[j + 2].y),
                               pack_bf16x2(v[j + 3].x, v[j + 3].y));
           };
-          put32(static_cast<unsigned char*>(p.out) + (so + 16 * e) * 2, p.so.t * 2, t - lane, p.L, bits(0), bits(4));
+          if (e == 0)
+            w[0] = bits(0), w[1] = bits(4);
+          else
+            w[2] = bits(0), w[3] = bits(4);
         }
       }
+      if (!p.out_f32) put64(static_cast<unsigned char*>(p.out) + so * 2, p.so.t * 2, t - lane, p.L, w);
       if (NPH == 3 && px && live) dot[t] = p.scale_out * from * d;
     }
     if (!ok) ctl->abort = 1;
@@ -758,10 +802,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int all_chunks = (p.L + kC - 1) / kC;
       const int za = max(seg * q.cps, chunks), zb = min((seg + 1) * q.cps, all_chunks);
       const int es = p.out_f32 ? 4 : 2;
-      const uint4 z = make_uint4(0, 0, 0, 0);
       for (int c = za; c < zb; ++c)
-        for (int b = 0; b < es; ++b)
-          put32(static_cast<unsigned char*>(p.out) + so * es + 32 * b, p.so.t * es, c * kC + 32 * qw, p.L, z, z);
+        for (int b = 0; b < es / 2; ++b) {
+          uint4 z[4] = {};
+          put64(static_cast<unsigned char*>(p.out) + so * es + 64 * b, p.so.t * es, c * kC + 32 * qw, p.L, z);
+        }
     }
   }
   tc_fence_before();
