@@ -77,12 +77,13 @@ __device__ __forceinline__ void decays(Smem<DA>& m, const float* lg, int64_t st,
 }
 
 template <typename T, int DA>
-__global__ void __launch_bounds__(kThreads) decay_simt_kernel(DecayPass a) {
+__global__ void __launch_bounds__(kThreads) decay_simt_kernel(DecayPass a, DecaySegs g) {
   extern __shared__ __align__(16) unsigned char raw[];
   Smem<DA>& m = *reinterpret_cast<Smem<DA>*>(raw);
   pdl_wait();
   const int tid = threadIdx.x, tc = tid % 16, ti = tid / 16;
-  const int slices = a.dc / kDc, slice = blockIdx.x % slices, unit = blockIdx.x / slices;
+  const int slices = a.dc / kDc, units = a.B * a.H;
+  const int slice = blockIdx.x % slices, unit = blockIdx.x / slices % units, seg = blockIdx.x / slices / units;
   const int n = unit / a.H, h = unit - n * a.H, c0 = slice * kDc;
   int count = a.L;
   if (a.count) {
@@ -108,25 +109,33 @@ __global__ void __launch_bounds__(kThreads) decay_simt_kernel(DecayPass a) {
   auto state = [&](int i, int j) {
     return (int64_t)unit * DA * a.dc + (a.state_t ? (int64_t)(c0 + j) * DA + i : (int64_t)i * a.dc + c0 + j);
   };
+  float* seg_h = g.seg_h + (((int64_t)seg * units + unit) * slices + slice) * DA * kDc;
   for (int e = tid; e < DA * kDc; e += kThreads) {
     const int i = a.state_t ? e % DA : e / kDc, j = a.state_t ? e / DA : e % kDc;
-    m.h[i][j] = a.init ? a.init[state(i, j)] : 0.f;
+    if (g.segs > 1)
+      m.h[e / kDc][e % kDc] = g.states_only ? 0.f : seg_h[e];
+    else
+      m.h[i][j] = a.init ? a.init[state(i, j)] : 0.f;
   }
   float* dots[2] = {nullptr, nullptr};
   if (px) {
     const int64_t o = ((int64_t)slice * a.B * a.H + unit) * a.L;
     dots[0] = a.dot_in + o, dots[1] = a.dot_out + o;
   }
-  const int chunks = (count + kC - 1) / kC;
-  for (int step = 0; step < chunks; ++step) {
+  // this segment's chunks, in the pass's order
+  const int chunks = (count + kC - 1) / kC, done = min(seg * g.cps, chunks), num = min(g.cps, chunks - done);
+  float product = 1.f;
+  for (int step = done; step < done + num; ++step) {
     const int t0 = (a.rev ? chunks - 1 - step : step) * kC;
-    load_rows<T>(m.a, pa, a.sa.t, t0, count, DA);
+    if (!g.states_only) load_rows<T>(m.a, pa, a.sa.t, t0, count, DA);
     load_rows<T>(m.b, pb, a.sb.t, t0, count, DA);
     load_rows<T>(m.c, pc, a.sc.t, t0, count, kDc);
     if (tid < 32) decays(m, lg, a.sg.t, t0, count);
     __syncthreads();
     const float* from_state = a.rev ? m.out : m.in;  // from the state that enters to each token
     const float* to_state = a.rev ? m.in : m.out;    // from each token to the state that leaves
+    product *= m.all;
+    if (!g.states_only) {
     // scores with their decays; the diagonal apart
     float acc[4][4] = {};
 #pragma unroll 4
@@ -228,6 +237,7 @@ __global__ void __launch_bounds__(kThreads) decay_simt_kernel(DecayPass a) {
                                    a.scale_out * (fmaf(dg, cd.w, in[r][3]) + st[r][3])));
     }
     __syncthreads();
+    }
     // H <- decay H + sum_s decay_s b_s c_s^T: rows ti * NR + r, columns 4 tc ..
     constexpr int NR = DA / 16;
     float u[NR][4];
@@ -261,13 +271,48 @@ __global__ void __launch_bounds__(kThreads) decay_simt_kernel(DecayPass a) {
       *reinterpret_cast<float4*>(&m.h[ti * NR + r][4 * tc]) = make_float4(u[r][0], u[r][1], u[r][2], u[r][3]);
     __syncthreads();
   }
-  for (int64_t i = tid; i < (int64_t)(a.L - count) * (kDc / 4); i += kThreads)
-    put(count + (int)(i / (kDc / 4)), 4 * (int)(i % (kDc / 4)), make_float4(0.f, 0.f, 0.f, 0.f));
-  if (a.fin) {
+  if (g.states_only) {
+    __syncthreads();  // without a chunk, zeros
+    for (int e = tid; e < DA * kDc; e += kThreads) seg_h[e] = m.h[e / kDc][e % kDc];
+    if (tid == 0) g.seg_d[((int64_t)seg * units + unit) * slices + slice] = product;
+    return;
+  }
+  // rows behind the sequence, each segment its share of the axis
+  const int z0 = max(count, (int)min((int64_t)seg * g.cps * kC, (int64_t)a.L)),
+            z1 = (int)min((int64_t)(seg + 1) * g.cps * kC, (int64_t)a.L);
+  for (int64_t i = tid; i < (int64_t)(z1 - z0) * (kDc / 4); i += kThreads)
+    put(z0 + (int)(i / (kDc / 4)), 4 * (int)(i % (kDc / 4)), make_float4(0.f, 0.f, 0.f, 0.f));
+  if (a.fin && seg == g.segs - 1) {
     __syncthreads();  // without a chunk, the initial state
     for (int e = tid; e < DA * kDc; e += kThreads) {
       const int i = a.state_t ? e % DA : e / kDc, j = a.state_t ? e / DA : e % kDc;
       a.fin[state(i, j)] = m.h[i][j];
+    }
+  }
+}
+
+// The segments' starting states in place of their own states: cur = init; for each segment its slot
+// becomes cur, and cur = decay cur + the segment's state.  A thread has one element of a head's state;
+// eight segments' states are on their way at a time.
+__global__ void __launch_bounds__(256) decay_join_kernel(DecayPass p, DecaySegs g) {
+  pdl_wait();
+  const int slices = p.dc / kDc, per = p.da * kDc;
+  const int us = blockIdx.x / (per / 256), e = (blockIdx.x - us * (per / 256)) * 256 + threadIdx.x;
+  const int unit = us / slices, i = e / kDc, c = (us - unit * slices) * kDc + e % kDc;
+  const int64_t total = (int64_t)p.B * p.H * slices, at = (int64_t)us * per + e;
+  float cur = p.init ? p.init[(int64_t)unit * p.da * p.dc + (p.state_t ? c * p.da + i : i * p.dc + c)] : 0.f;
+  for (int s0 = 0; s0 < g.segs; s0 += 8) {
+    float own[8], d[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const bool has = s0 + k + 1 < g.segs;
+      own[k] = has ? g.seg_h[(s0 + k) * total * per + at] : 0.f;
+      d[k] = has ? g.seg_d[(s0 + k) * total + us] : 0.f;
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      if (s0 + k < g.segs) g.seg_h[(s0 + k) * total * per + at] = cur;
+      cur = fmaf(d[k], cur, own[k]);
     }
   }
 }
@@ -407,24 +452,79 @@ __global__ void __launch_bounds__(32 * kGateWarps) decay_gate_kernel(DecayGate a
 }
 
 template <typename T, int DA>
-cudaError_t launch(const DecayPass& a, cudaStream_t s) {
+cudaError_t launch(const DecayPass& a, const DecaySegs& g, int64_t blocks, cudaStream_t s) {
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = allow_smem(decay_simt_kernel<T, DA>, sizeof(Smem<DA>), done);
   if (e != cudaSuccess) return e;
-  const int64_t blocks = (int64_t)a.B * a.H * (a.dc / kDc);
   if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
-  return launch_pdl(decay_simt_kernel<T, DA>, dim3((unsigned)blocks), dim3(kThreads), sizeof(Smem<DA>), s, a);
+  return launch_pdl(decay_simt_kernel<T, DA>, dim3((unsigned)blocks), dim3(kThreads), sizeof(Smem<DA>), s, a, g);
+}
+
+cudaError_t dispatch(const DecayPass& a, lizard_dtype dt, const DecaySegs& g, int64_t blocks, cudaStream_t s) {
+  if (dt == LIZARD_F32)
+    return a.da == 64 ? launch<float, 64>(a, g, blocks, s) : launch<float, 128>(a, g, blocks, s);
+  return a.da == 64 ? launch<bf16, 64>(a, g, blocks, s) : launch<bf16, 128>(a, g, blocks, s);
+}
+
+// One CTA an SM at da = 128, two at 64, by their shared memory; a state pass is a third of the work.
+int simt_segments(int64_t ctas, int L, int da) {
+  return decay_segments(ctas, da == 64 ? 304 : 152, (L + kC - 1) / kC, 0.35, 0.4);
 }
 
 }  // namespace
 
-cudaError_t launch_decay_simt(const DecayPass& a, lizard_dtype dt, cudaStream_t s, int* launches) {
+int decay_segments(int64_t ctas, int per_wave, int chunks, double part, double extra) {
+  if (ctas >= 8 * per_wave) return 1;
+  int best = 1;
+  double least = 1e30;
+  for (int s = 1; s <= 64 && s <= chunks; ++s) {
+    const int cps = (chunks + s - 1) / s;
+    if (s > 1 && (chunks + cps - 1) / cps < s) continue;  // some would be empty
+    double t = (double)((ctas * s + per_wave - 1) / per_wave) * cps;
+    if (s > 1) t += part * (double)((ctas * (s - 1) + per_wave - 1) / per_wave) * cps + extra;
+    if (t < least) least = t, best = s;
+  }
+  return best;
+}
+
+size_t decay_seg_bytes(int segs, int64_t ctas, int da) {
+  return segs > 1 ? (size_t)segs * ctas * ((size_t)da * kDc + 1) * sizeof(float) : 0;
+}
+
+cudaError_t launch_decay_join(const DecayPass& a, const DecaySegs& g, cudaStream_t s, int* launches) {
+  const int64_t blocks = (int64_t)a.B * a.H * (a.dc / kDc) * (a.da * kDc / 256);
+  if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
+  trace_begin("decay_join", s);
+  const cudaError_t e = launch_pdl(decay_join_kernel, dim3((unsigned)blocks), dim3(256), 0, s, a, g);
+  trace_end(s);
+  ++*launches;
+  return e;
+}
+
+size_t decay_simt_workspace(int B, int H, int L, int da, int dc) {
+  const int64_t ctas = (int64_t)B * H * (dc / kDc);
+  return decay_seg_bytes(simt_segments(ctas, L, da), ctas, da);
+}
+
+cudaError_t launch_decay_simt(const DecayPass& a, lizard_dtype dt, float* ws, cudaStream_t s, int* launches) {
+  const int64_t ctas = (int64_t)a.B * a.H * (a.dc / kDc);
+  const int chunks = (a.L + kC - 1) / kC;
+  DecaySegs g{};
+  g.segs = simt_segments(ctas, a.L, a.da);
+  g.cps = chunks ? (chunks + g.segs - 1) / g.segs : 1;
+  if (g.segs > 1) {
+    g.seg_h = ws, g.seg_d = ws + (size_t)g.segs * ctas * a.da * kDc;
+    DecaySegs f = g;
+    f.states_only = true;
+    trace_begin("decay_states", s);
+    cudaError_t e = dispatch(a, dt, f, ctas * (g.segs - 1), s);
+    trace_end(s);
+    ++*launches;
+    if (e == cudaSuccess) e = launch_decay_join(a, g, s, launches);
+    if (e != cudaSuccess) return e;
+  }
   trace_begin("decay_simt", s);
-  cudaError_t e;
-  if (dt == LIZARD_F32)
-    e = a.da == 64 ? launch<float, 64>(a, s) : launch<float, 128>(a, s);
-  else
-    e = a.da == 64 ? launch<bf16, 64>(a, s) : launch<bf16, 128>(a, s);
+  const cudaError_t e = dispatch(a, dt, g, ctas * g.segs, s);
   trace_end(s);
   ++*launches;
   return e;

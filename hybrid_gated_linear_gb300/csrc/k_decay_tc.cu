@@ -86,10 +86,8 @@ struct Maps {
 struct TcParams {
   DecayPass p;
   int an, ah, bn, bh, cn, ch;  // 0 where a tensor repeats over sequences or heads, else 1
-  int segs, cps;               // segments of the axis, chunks of each
   int parts;                   // bf16 parts of C~
-  bool states_only;            // first pass: the segments' states from zero
-  float *seg_h, *seg_d;        // [segs][units][slices][da][64], [segs][units][slices]
+  DecaySegs g;
 };
 
 __device__ __forceinline__ void tma_load_4d(void* dst, const CUtensorMap* map, int x, int y, int z, int w, uint64_t* bar) {
@@ -385,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   count = __shfl_sync(0xffffffffu, count, 0);  // (known to be the same in the warp)
   // this segment's chunks, in the pass's order from `first` on
   const int chunks = (count + kC - 1) / kC;
-  const int done = min(seg * q.cps, chunks), num = min(q.cps, chunks - done);
+  const int done = min(seg * q.g.cps, chunks), num = min(q.g.cps, chunks - done);
   const int first = p.rev ? chunks - 1 - done : done, dir = p.rev ? -1 : 1;
   auto token = [&](int it) { return (first + dir * it) * kC; };
   // the one chunk whose last rows lie behind the sequence but inside the tensor: they are zeroed
@@ -405,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int k = 0; k < DA / 64; ++k)
           tma_load_4d(sm + Sm::B + sb * Sm::kTile + k * (kC * 128), &maps.b, 64 * k, t0, hb, nb, &ctl->bar[FB + sb]);
         armed_b[0] += sb == 0, armed_b[1] += sb == 1;
-        if (q.states_only) continue;
+        if (q.g.states_only) continue;
         if (it >= Sm::NA && !(ok = wait_for(ctl, EA + sa, (it / Sm::NA - 1) & 1))) break;
         mbar_arrive_expect_tx(&ctl->bar[FA + sa], Sm::kTile);
 #pragma unroll
@@ -427,6 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t id_s = idesc_bf16(kC, kC, false, false), id_kv = idesc_bf16(128, q.parts * kN, true, true),
                      id_h = idesc_bf16(kC, kN, false, true);
       constexpr uint32_t kRow = kC * 128;  // bytes of a 64-column block of a tile
+      static_assert(kN == kDecaySlice, "segments' states are kept by slices");
       static_assert(kRow == kTileC, "the parts of C~ are the blocks of one operand");
       const uint32_t da = desc_lower(sb + Sm::A, 16), db = desc_lower(sb + Sm::B, 16), dbt = desc_lower(sb + Sm::B, kRow),
                      dc = desc_lower(sb + Sm::Ct, kRow), dp = desc_lower(sb + Sm::CP, kRow),
@@ -436,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int it = 0; it < num && ok; ++it) {
         const uint32_t a = da + it % Sm::NA * (Sm::kTile / 16), b = it % Sm::NBt * (Sm::kTile / 16);
         if (!(ok = wait_warp(ctl, FB + it % Sm::NBt, (it / Sm::NBt) & 1))) break;
-        if (!q.states_only) {
+        if (!q.g.states_only) {
           // S = A B^T (the last one has been read: P C has been issued)
           if (!(ok = wait_warp(ctl, FA + it % Sm::NA, (it / Sm::NA) & 1))) break;
           if (ragged(it) && !(ok = wait_warp(ctl, FIX, 0))) break;
@@ -446,9 +445,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           commit_lo(&ctl->bar[SR]);
         }
         // B^T C~, into alternate columns where there are no scores
-        const bool other = q.states_only && (it & 1);
+        const bool other = q.g.states_only && (it & 1);
         if (!(ok = wait_warp(ctl, CT + (it & 1), (it >> 1) & 1))) break;
-        const int lag = q.states_only ? 2 : 1;
+        const int lag = q.g.states_only ? 2 : 1;
         if (it >= lag && !(ok = wait_warp(ctl, KVF + ((it - lag) & 1), ((it - lag) >> 1) & 1))) break;
         tc_fence_after();
 #pragma unroll 4
@@ -456,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mma_lo(tmem + (other ? 0 : kColKV), dbt + b + step_mn(j), (other ? dp2 : dp) + step_mn(j), id_kv, j > 0);
         commit_lo(&ctl->bar[KVR + (it & 1)]);
         commit_lo(&ctl->bar[EB + it % Sm::NBt]);
-        if (q.states_only) {
+        if (q.g.states_only) {
           commit_lo(&ctl->bar[EC + it % Sm::NCt]);
           continue;
         }
@@ -529,7 +528,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // the rows that lie in it, for the others all of it or nothing.  The rest of P is always 0.
     const int full = p.rev ? 3 - qw : qw, j0 = p.rev ? 2 * qw + 2 + half : half, j1 = 2 * qw + half;
     const bool own = (lane >> 4) == half, sees = p.rev ? half == 1 : half == 0;
-    if (!q.states_only) {
+    if (!q.g.states_only) {
       const uint32_t z[8] = {};
       for (int j = half; j < 8; j += 2)
         if (p.rev ? j < 2 * qw : j > 2 * qw + 1) tmem_st8(tmem + tl + kColP + 8 * j, z);
@@ -559,10 +558,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!(ok = wait_for(ctl, FACF + (it & 1), (it >> 1) & 1))) break;
       const Factors& f = hd.f[it & 1];
       // C~ (its tiles are free once the chunk before has been multiplied; with two places the one before it)
-      const int lag = q.states_only ? 2 : 1;
+      const int lag = q.g.states_only ? 2 : 1;
       if (it >= lag && !(ok = wait_for(ctl, KVR + ((it - lag) & 1), ((it - lag) >> 1) & 1))) break;
-      unsigned char* cp = sm + (q.states_only && (it & 1) ? Sm::CP2 : Sm::CP);
-#pragma unroll 1
+      unsigned char* cp = sm + (q.g.states_only && (it & 1) ? Sm::CP2 : Sm::CP);
+#pragma unroll
       for (int e = 0; e < kTileC / 16 / (32 * kScoreWarps); ++e) {
         const int at = (wt + 32 * kScoreWarps * e) * 16;  // byte of the tile: the swizzle stays as it is
         const float w = f.col[at >> 7] * f.tail[at >> 11] * p.scale_in;
@@ -582,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->bar[CT + (it & 1)]);
-      if (q.states_only) {
+      if (q.g.states_only) {
         if (lane == 0) mbar_arrive(&ctl->bar[FACE + (it & 1)]);
         continue;
       }
@@ -647,11 +646,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     // this thread's columns in a state of the caller's
     const int c1 = c0 + 32 * half, state_step = p.state_t ? DA : 1;
     const int64_t state_at = (int64_t)unit * DA * p.dc + (p.state_t ? c1 * DA + i : i * p.dc + c1);
-    float* seg_h = q.seg_h + ((((int64_t)seg * units + unit) * slices + slice) * DA + i) * kN + 32 * half;
+    float* seg_h = q.g.seg_h + ((((int64_t)seg * units + unit) * slices + slice) * DA + i) * kN + 32 * half;
 #pragma unroll
     for (int j = 0; j < 32; ++j) x[j] = 0.f;
-    if (mine && !q.states_only) {
-      if (q.segs > 1) {
+    if (mine && !q.g.states_only) {
+      if (q.g.segs > 1) {
 #pragma unroll
         for (int j = 0; j < 32; ++j) x[j] = seg_h[j];
       } else if (p.init) {
@@ -687,7 +686,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     float* dot = p.x ? p.dot_out + ((int64_t)(2 * slice + half) * units + unit) * p.L : nullptr;
     bool ok = true;
     float product = 1.f;
-    if (num > 0 && !q.states_only) put_state();
+    if (num > 0 && !q.g.states_only) put_state();
 #pragma unroll 1
     for (int it = 0; it < num && ok; ++it) {
       if (!(ok = wait_for(ctl, FACF + (it & 1), (it >> 1) & 1))) break;
@@ -699,7 +698,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // H = all H + B^T C~, whose parts are added up from the smallest
       if (!(ok = wait_for(ctl, KVR + (it & 1), (it >> 1) & 1))) break;
       tc_fence_after();
-      const uint32_t tk = tl + (q.states_only && (it & 1) ? 0 : kColKV);
+      const uint32_t tk = tl + (q.g.states_only && (it & 1) ? 0 : kColKV);
       const float2 all2 = make_float2(all, all);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
@@ -721,7 +720,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->bar[KVF + (it & 1)]);
-      if (q.states_only) continue;
+      if (q.g.states_only) continue;
       if (it + 1 < num) {
         if (!(ok = wait_for(ctl, HF, it & 1))) break;
         put_state();
@@ -734,7 +733,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float d = 0.f;
       uint4 w[4];
       const float2 scale = make_float2(p.scale_out, p.scale_out), from2 = make_float2(from, from);
-#pragma unroll 1
+#pragma unroll
       for (int e = 0; e < 2; ++e) {
         uint32_t y[16], ys[16];
         tmem_ld16(tl + kColY + 16 * e, y);
@@ -787,20 +786,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (NPH == 3 && px && live) dot[t] = p.scale_out * from * d;
     }
     if (!ok) ctl->abort = 1;
-    if (ok && q.states_only) {
+    if (ok && q.g.states_only) {
       if (mine) {
 #pragma unroll
         for (int j = 0; j < 32; ++j) seg_h[j] = x[j];
       }
-      if (i == 0 && half == 0) q.seg_d[((int64_t)seg * units + unit) * slices + slice] = product;
+      if (i == 0 && half == 0) q.g.seg_d[((int64_t)seg * units + unit) * slices + slice] = product;
     } else if (ok) {
-      if (mine && p.fin && seg == q.segs - 1) {
+      if (mine && p.fin && seg == q.g.segs - 1) {
 #pragma unroll
         for (int j = 0; j < 32; ++j) p.fin[state_at + j * state_step] = x[j];
       }
       // the rows of whole chunks behind the sequence
       const int all_chunks = (p.L + kC - 1) / kC;
-      const int za = max(seg * q.cps, chunks), zb = min((seg + 1) * q.cps, all_chunks);
+      const int za = max(seg * q.g.cps, chunks), zb = min((seg + 1) * q.g.cps, all_chunks);
       const int es = p.out_f32 ? 4 : 2;
       for (int c = za; c < zb; ++c)
         for (int b = 0; b < es / 2; ++b) {
@@ -816,26 +815,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_dealloc(tmem, 512);
   }
   if (tid == 0 && ctl->abort) raise_status(p.status, kDevTimeout);
-}
-
-// The segments' starting states in place of their own states: cur = init; for each segment its slot
-// becomes cur, and cur = decay cur + the segment's state.
-__global__ void __launch_bounds__(256) decay_join_kernel(DecayPass p, int segs, float* seg_h, const float* seg_d) {
-  pdl_wait();
-  const int slices = p.dc / kN, units = p.B * p.H;
-  const int64_t per = (int64_t)p.da * kN, total = (int64_t)units * slices * per;
-  const int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (e >= total) return;
-  const int64_t us = e / per;
-  const int unit = (int)(us / slices), slice = (int)(us - (int64_t)unit * slices);
-  const int r = (int)(e - us * per), i = r / kN, c = slice * kN + r % kN;
-  float cur = p.init ? p.init[(int64_t)unit * p.da * p.dc + (p.state_t ? (int64_t)c * p.da + i : (int64_t)i * p.dc + c)] : 0.f;
-  for (int s = 0; s < segs; ++s) {
-    float* slot = seg_h + s * total + e;
-    const float own = s + 1 < segs ? *slot : 0.f, d = s + 1 < segs ? seg_d[(int64_t)s * units * slices + us] : 0.f;
-    *slot = cur;
-    cur = fmaf(d, cur, own);
-  }
 }
 
 // ---------------------------------------------------------------------------------
@@ -1033,26 +1012,12 @@ cudaError_t launch_pairs(const PairMaps& m, const PairParams& p, cudaStream_t s)
 
 bool decay_tc_rows_ok(int B, int H, int L, int d, const Strides& s) { return strides_ok(B, H, L, d, s); }
 
-// Segments of the axis: CTAs run one to an SM (152), so that `ctas` of them take ceil(ctas S / 152) rounds of
-// ceil(chunks / S) chunks, and before that, for S > 1, the states of all segments but the last, at
-// about half the time a chunk, and a join.
-int decay_segments(int ctas, int chunks) {
-  int best = 1;
-  double least = 1e30;
-  for (int s = 1; s <= 32 && s <= chunks; ++s) {
-    const int cps = (chunks + s - 1) / s;
-    if (s > 1 && (chunks + cps - 1) / cps < s) continue;  // some would be empty
-    double t = (double)(((int64_t)ctas * s + 151) / 152) * (cps + 2);
-    if (s > 1) t += 0.5 * (double)(((int64_t)ctas * (s - 1) + 151) / 152) * (cps + 2) + 4;
-    if (t < least) least = t, best = s;
-  }
-  return best;
-}
+// One CTA an SM (152); a state pass takes about 0.6 of the pass's time a chunk.
+static int tc_segments(int64_t ctas, int L) { return decay_segments(ctas, 152, (L + kC - 1) / kC, 0.6, 5.0); }
 
 size_t decay_tc_workspace(int B, int H, int L, int da, int dc) {
   const int64_t ctas = (int64_t)B * H * (dc / kN);
-  const int segs = ctas > 152 * 32 ? 1 : decay_segments((int)ctas, (L + kC - 1) / kC);
-  return segs > 1 ? (size_t)segs * ctas * ((size_t)da * kN + 1) * sizeof(float) : 0;
+  return decay_seg_bytes(tc_segments(ctas, L), ctas, da);
 }
 
 cudaError_t launch_decay_tc(const DecayPass& a, bool exact_state, float* ws, cudaStream_t s, int* launches) {
@@ -1065,29 +1030,25 @@ cudaError_t launch_decay_tc(const DecayPass& a, bool exact_state, float* ws, cud
     return cudaErrorInvalidValue;
   const int64_t ctas = (int64_t)a.B * a.H * (a.dc / kN);
   const int chunks = (a.L + kC - 1) / kC;
-  q.segs = ctas > 152 * 32 ? 1 : decay_segments((int)ctas, chunks);
-  q.cps = (chunks + q.segs - 1) / q.segs;
+  DecaySegs& g = q.g;
+  g.segs = tc_segments(ctas, a.L);
+  g.cps = (chunks + g.segs - 1) / g.segs;
   q.parts = a.fin || a.x ? 3 : 2;
-  if (ctas * q.segs > 0x7fffffffll) return cudaErrorInvalidValue;
+  if (ctas * g.segs > 0x7fffffffll) return cudaErrorInvalidValue;
   cudaError_t e;
-  if (q.segs > 1) {
-    q.seg_h = ws, q.seg_d = ws + q.segs * ctas * a.da * kN;
+  if (g.segs > 1) {
+    g.seg_h = ws, g.seg_d = ws + (size_t)g.segs * ctas * a.da * kN;
     TcParams f = q;
-    f.states_only = true;
+    f.g.states_only = true;
     trace_begin("decay_states", s);
-    e = a.da == 64 ? launch<64, 1>(m, f, (int)(ctas * (q.segs - 1)), s) : launch<128, 1>(m, f, (int)(ctas * (q.segs - 1)), s);
+    e = a.da == 64 ? launch<64, 1>(m, f, (int)(ctas * (g.segs - 1)), s) : launch<128, 1>(m, f, (int)(ctas * (g.segs - 1)), s);
     trace_end(s);
     ++*launches;
-    if (e != cudaSuccess) return e;
-    trace_begin("decay_join", s);
-    e = launch_pdl(decay_join_kernel, dim3((unsigned)((ctas * a.da * kN + 255) / 256)), dim3(256), 0, s, a, q.segs, q.seg_h,
-                   static_cast<const float*>(q.seg_d));
-    trace_end(s);
-    ++*launches;
+    if (e == cudaSuccess) e = launch_decay_join(a, g, s, launches);
     if (e != cudaSuccess) return e;
   }
   trace_begin("decay_tc", s);
-  const int blocks = (int)(ctas * q.segs);
+  const int blocks = (int)(ctas * g.segs);
   if (exact_state)
     e = a.da == 64 ? launch<64, 3>(m, q, blocks, s) : launch<128, 3>(m, q, blocks, s);
   else

@@ -416,7 +416,21 @@ constexpr float kDecayNone = -104.f;
 // Tokens of a chunk and channels of c that a CTA of the CUDA-core pass takes.
 constexpr int kDecayChunk = 64;
 constexpr int kDecaySlice = 64;
-cudaError_t launch_decay_simt(const DecayPass& a, lizard_dtype dt, cudaStream_t s, int* launches);
+// A long axis is cut into segments where the heads alone leave SMs idle: first the states of all segments
+// but the last, from zero (seg_h [segs][units][dc / 64][da][64]) with their decays (seg_d
+// [segs][units][dc / 64]); a join makes seg_h the states that the segments start from; then the pass.
+struct DecaySegs {
+  int segs, cps;  // segments, chunks of each
+  bool states_only;
+  float *seg_h, *seg_d;
+};
+// The segments for `ctas` CTAs of which `per_wave` run at a time, a state pass costing `part` of the pass
+// a chunk and `extra` chunks for its start and the join; and the bytes of seg_h and seg_d.
+int decay_segments(int64_t ctas, int per_wave, int chunks, double part, double extra);
+size_t decay_seg_bytes(int segs, int64_t ctas, int da);
+cudaError_t launch_decay_join(const DecayPass& a, const DecaySegs& g, cudaStream_t s, int* launches);
+size_t decay_simt_workspace(int B, int H, int L, int da, int dc);
+cudaError_t launch_decay_simt(const DecayPass& a, lizard_dtype dt, float* ws, cudaStream_t s, int* launches);
 // The same on the tensor cores: bf16, L > 0, tensors that decay_tc_rows_ok accepts; exact_state: A H from
 // three bf16 parts of the state (dot_out [2 dc / 64][B,H,L]; dot_in is not written).  `ws` of
 // decay_tc_workspace bytes.
