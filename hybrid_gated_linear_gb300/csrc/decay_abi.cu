@@ -260,14 +260,14 @@ lizard_status lizard_decay_attn_bwd(const lizard_decay_dims* dims, const void* q
     pr.B = d.B, pr.H = d.H, pr.G = G, pr.L = d.L, pr.dk = d.dk, pr.dv = d.dv;
     pr.q = q, pr.k = k, pr.v = v, pr.dy = dy, pr.sq = rq.s, pr.sk = rk.s, pr.sv = rv.s, pr.sy = ry.s;
     pr.lg = log_decay, pr.sg = rg.s, pr.count = count, pr.scale = scale;
-    pr.row = row_in, pr.col = col_in, pr.status = a.status;
+    pr.diff = row_in, pr.status = a.status;
     e = lz::launch_decay_pairs(pr, s, &launches);
     if (e != cudaSuccess) return finish(e, launches);
   }
   lz::DecayGate g{};
   g.B = d.B, g.H = d.H, g.L = d.L, g.chunk = tc ? lz::kDecayTile : lz::kDecayChunk;
   g.in_slices = tc ? 1 : (int)in_planes(d), g.out_slices = (int)(tc ? out_planes(d) : in_planes(d));
-  g.row_in = row_in, g.col_in = col_in, g.row_out = row_out, g.col_out = col_out;
+  g.row_in = row_in, g.col_in = tc ? nullptr : col_in, g.row_out = row_out, g.col_out = col_out;
   g.h0 = h0, g.d_h0 = d_h0, g.state = d.dk * d.dv;
   g.lg = log_decay, g.sg = rg.s, g.count = count, g.d_lg = d_log_decay;
   g.sums = reinterpret_cast<double2*>(ws + w.sums);

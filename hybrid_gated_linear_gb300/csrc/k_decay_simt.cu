@@ -345,10 +345,12 @@ __global__ void __launch_bounds__(kThreads) decay_heads_kernel(int Hk, int G, in
 //   + through                                              from before the chunk to after it.
 // `through` of the chunks follows from the pairs over the edge before the first one, <h0, d_h0>:
 //   edge after = through + sum col_out,  through = edge before - sum row_out  (0 where a document
-// starts in the chunk).  Sums run in 64 bits.  First a warp for each chunk takes its sums of row_out
+// starts in the chunk).  Sums over chunks run in 64 bits, within 32 tokens in trees of fp32 (64-bit
+// additions are what this GPU has least of: with them throughout, 49 us against 13 for 64 heads x 4096
+// tokens).  First a warp for each chunk takes its sums of row_out
 // and col_out and whether a document starts, and a block for each head <h0, d_h0>; then a warp for
 // each chunk adds up the edge in front of it and writes its tokens.
-__device__ __forceinline__ double warp_sum(double x) {
+__device__ __forceinline__ double warp_sum64(double x) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
   return x;
@@ -376,7 +378,7 @@ __global__ void __launch_bounds__(32 * kGateWarps) decay_gate_sums_kernel(DecayG
       }
     }
     __shared__ double part[kGateWarps];
-    s = warp_sum(s);
+    s = warp_sum64(s);
     if (lane == 0) part[warp] = s;
     __syncthreads();
     s = 0.0;
@@ -392,12 +394,16 @@ __global__ void __launch_bounds__(32 * kGateWarps) decay_gate_sums_kernel(DecayG
   const float* lg = a.lg + n * a.sg.n + h * a.sg.h;
   double rows = 0.0, cols = 0.0;
   bool start = false;
-  for (int t = t0 + lane; t < end; t += 32) {
-    for (int s = 0; s < a.out_slices; ++s)
-      rows += a.row_out[s * plane + base + t], cols += a.col_out[s * plane + base + t];
-    start |= lg[t * a.sg.t] < kDecayNone;
+  for (int g = t0; g < end; g += 32) {
+    float r = 0.f, c = 0.f;
+    if (g + lane < end) {
+      const int64_t at = base + g + lane;
+#pragma unroll 4
+      for (int s = 0; s < a.out_slices; ++s) r += a.row_out[s * plane + at], c += a.col_out[s * plane + at];
+      start |= lg[(g + lane) * a.sg.t] < kDecayNone;
+    }
+    rows += warp_sum(r), cols += warp_sum(c);
   }
-  rows = warp_sum(rows), cols = warp_sum(cols);
   start = __any_sync(0xffffffffu, start);
   if (lane == 0) a.sums[(int64_t)unit * (chunks + 1) + c] = make_double2(start ? nan("") : rows, cols);
 }
@@ -421,7 +427,7 @@ __global__ void __launch_bounds__(32 * kGateWarps) decay_gate_kernel(DecayGate a
     const unsigned starts = __ballot_sync(0xffffffffu, isnan(s.x));
     const int last = 31 - __clz(starts);  // -1: none
     if (starts) edge = 0.0;
-    edge += warp_sum(lane < last ? 0.0 : lane == last ? s.y : s.y - s.x);
+    edge += warp_sum64(lane < last ? 0.0 : lane == last ? s.y : s.y - s.x);
   }
   const double2 own = sums[c];
   const double through = isnan(own.x) ? 0.0 : edge - own.x;
@@ -430,22 +436,23 @@ __global__ void __launch_bounds__(32 * kGateWarps) decay_gate_kernel(DecayGate a
   double behind = 0.0, before = own.y;  // of the suffix sums; col_out of the tokens before the group's end
   for (int g0 = t0 + (end - t0 - 1) / 32 * 32; g0 >= t0; g0 -= 32) {
     const int t = g0 + lane;
-    double sum = 0.0, col = 0.0;
+    float sum = 0.f, col = 0.f;
     bool cut = false;
     if (t < end) {
       // a document's start: nothing passes over it
       cut = lg[t * a.sg.t] < kDecayNone;
+#pragma unroll 2
       for (int s = 0; s < a.in_slices; ++s)
-        sum += (double)a.row_in[s * plane + base + t] - a.col_in[s * plane + base + t];
-      for (int s = 0; s < a.out_slices; ++s)
-        sum += a.row_out[s * plane + base + t], col += a.col_out[s * plane + base + t];
+        sum += a.row_in[s * plane + base + t] - (a.col_in ? a.col_in[s * plane + base + t] : 0.f);
+#pragma unroll 4
+      for (int s = 0; s < a.out_slices; ++s) sum += a.row_out[s * plane + base + t], col += a.col_out[s * plane + base + t];
     }
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const double u = __shfl_down_sync(0xffffffffu, sum, o), v = __shfl_down_sync(0xffffffffu, col, o);
+      const float u = __shfl_down_sync(0xffffffffu, sum, o), v = __shfl_down_sync(0xffffffffu, col, o);
       if (lane + o < 32) sum += u, col += v;
     }
-    if (t < end) a.d_lg[base + t] = cut ? 0.f : (float)(behind + sum + (before - col) + through);
+    if (t < end) a.d_lg[base + t] = cut ? 0.f : (float)(behind + before + through + (double)(sum - col));
     behind += __shfl_sync(0xffffffffu, sum, 0);
     before -= __shfl_sync(0xffffffffu, col, 0);
   }

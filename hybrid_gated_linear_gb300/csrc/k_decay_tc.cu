@@ -15,7 +15,7 @@
 // fp32.  Twenty warps:
 //   0      copies the tiles of A, B [128][da] and C [128][64] in by TMA, two stages ahead
 //   1      issues the MMAs: S, B^T C~, A H, P C
-//   2      the decays of the next chunk
+//   2-3    the decays, one warp those of the even chunks, one of the odd
 //   4-11   C~ = to o C in two or three bf16 parts (16 or 24 bits: the state is a sum over the whole
 //          sequence, so its operands are not rounded), then P, rounded once to bf16, into TMEM
 //   12-19  the state: H = all H + (B^T C~); its bf16 parts for the next chunk's A H (one part, as P is
@@ -393,23 +393,31 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 0) {
     if (lane == 0) {
       bool ok = true;
-      uint32_t armed_a[2] = {0, 0}, armed_b[2] = {0, 0};
-      const int na = q.an * n, nb = q.bn * n, ha = q.ah * (h / p.ga), hb = q.bh * (h / p.gb);
+      uint32_t armed_a[2] = {0, 0}, armed_b[2] = {0, 0}, armed_c[2] = {0, 0};
+      const int na = q.an * n, nb = q.bn * n, nc = q.cn * n, ha = q.ah * (h / p.ga), hb = q.bh * (h / p.gb),
+                hc = q.ch * (h / p.gc);
       for (int it = 0; it < num && ok; ++it) {
         const int t0 = token(it), sb = it % Sm::NBt, sa = it % Sm::NA;
+        const int sc = it % Sm::NCt;
+        // in the order in which the stages come free
         if (it >= Sm::NBt && !(ok = wait_for(ctl, EB + sb, (it / Sm::NBt - 1) & 1))) break;
         mbar_arrive_expect_tx(&ctl->bar[FB + sb], Sm::kTile);
 #pragma unroll
         for (int k = 0; k < DA / 64; ++k)
           tma_load_4d(sm + Sm::B + sb * Sm::kTile + k * (kC * 128), &maps.b, 64 * k, t0, hb, nb, &ctl->bar[FB + sb]);
         armed_b[0] += sb == 0, armed_b[1] += sb == 1;
-        if (q.g.states_only) continue;
-        if (it >= Sm::NA && !(ok = wait_for(ctl, EA + sa, (it / Sm::NA - 1) & 1))) break;
-        mbar_arrive_expect_tx(&ctl->bar[FA + sa], Sm::kTile);
+        if (!q.g.states_only) {
+          if (it >= Sm::NA && !(ok = wait_for(ctl, EA + sa, (it / Sm::NA - 1) & 1))) break;
+          mbar_arrive_expect_tx(&ctl->bar[FA + sa], Sm::kTile);
 #pragma unroll
-        for (int k = 0; k < DA / 64; ++k)
-          tma_load_4d(sm + Sm::A + sa * Sm::kTile + k * (kC * 128), &maps.a, 64 * k, t0, ha, na, &ctl->bar[FA + sa]);
-        armed_a[0] += sa == 0, armed_a[1] += sa == 1;
+          for (int k = 0; k < DA / 64; ++k)
+            tma_load_4d(sm + Sm::A + sa * Sm::kTile + k * (kC * 128), &maps.a, 64 * k, t0, ha, na, &ctl->bar[FA + sa]);
+          armed_a[0] += sa == 0, armed_a[1] += sa == 1;
+        }
+        if (it >= Sm::NCt && !(ok = wait_for(ctl, EC + sc, (it / Sm::NCt - 1) & 1))) break;
+        mbar_arrive_expect_tx(&ctl->bar[FC + sc], kTileC);
+        tma_load_4d(sm + Sm::Ct + sc * kTileC, &maps.c, c0, t0, hc, nc, &ctl->bar[FC + sc]);
+        armed_c[0] += sc == 0, armed_c[1] += sc == 1;
       }
       if (!ok) ctl->abort = 1;
       const uint64_t t0 = globaltimer_ns();
@@ -417,6 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int k = 0; k < 2; ++k) {
         drain_bar(ctl, FA + k, armed_a[k], t0);
         drain_bar(ctl, FB + k, armed_b[k], t0);
+        drain_bar(ctl, FC + k, armed_c[k], t0);
       }
     }
   } else if (warp == 1) {
@@ -484,15 +493,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       drain_bar(ctl, DONE, 1, globaltimer_ns());
       __syncwarp();
     }
-  } else if (warp == 2) {
+  } else if (warp == 2 || warp == 3) {
     const float* lg = p.lg + n * p.sg.n + h * p.sg.h;
     Share f;
-    if (num > 0) load_decays(lg, p.sg.t, token(0), count, f.x);
+    if (warp - 2 < num) load_decays(lg, p.sg.t, token(warp - 2), count, f.x);
     bool ok = true;
 #pragma unroll 1
-    for (int it = 0; it < num && ok; ++it) {
+    for (int it = warp - 2; it < num && ok; it += 2) {  // one warp the even chunks, one the odd
       float next[4] = {};
-      if (it + 1 < num) load_decays(lg, p.sg.t, token(it + 1), count, next);
+      if (it + 2 < num) load_decays(lg, p.sg.t, token(it + 2), count, next);
       f.make(p.rev);
       if (it > 1 && !(ok = wait_for(ctl, FACE + (it & 1), (it / 2 - 1) & 1))) break;
       f.put(hd.f[it & 1]);
@@ -502,23 +511,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int k = 0; k < 4; ++k) f.x[k] = next[k];
     }
     if (!ok) ctl->abort = 1;
-  } else if (warp == 3) {
-    if (lane == 0) {
-      bool ok = true;
-      uint32_t armed[2] = {0, 0};
-      const int nc = q.cn * n, hc = q.ch * (h / p.gc);
-      for (int it = 0; it < num && ok; ++it) {
-        const int s = it % Sm::NCt;
-        if (it >= Sm::NCt && !(ok = wait_for(ctl, EC + s, (it / Sm::NCt - 1) & 1))) break;
-        mbar_arrive_expect_tx(&ctl->bar[FC + s], kTileC);
-        tma_load_4d(sm + Sm::Ct + s * kTileC, &maps.c, c0, token(it), hc, nc, &ctl->bar[FC + s]);
-        armed[0] += s == 0, armed[1] += s == 1;
-      }
-      if (!ok) ctl->abort = 1;
-      const uint64_t t0 = globaltimer_ns();
-      drain_bar(ctl, FC, armed[0], t0);
-      drain_bar(ctl, FC + 1, armed[1], t0);
-    }
   } else if (warp >= 4 && warp < 12) {
     const int half = (warp - 4) >> 2, qw = warp & 3, wt = tid - 128;  // thread of the group
     const int o = 32 * qw + lane, I = o >> 4;
@@ -818,12 +810,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ---------------------------------------------------------------------------------
-// Within a chunk: row_i = sum_{s < i} W_is, col_s = sum_{i > s} W_is with W_is = scale (q_i . k_s) D (dy_i . v_s),
-// from exact products of the bf16 rows in fp32 sums.  One CTA a chunk: both scores and their transposes by
-// four MMAs; four warps sum the rows, four the columns, each thread its own.
+// Within a chunk: diff_i = sum_{s < i} W_is - sum_{s > i} W_si with W_is = scale (q_i . k_s) D (dy_i . v_s), from
+// exact products of the bf16 rows in fp32 sums.  One CTA a chunk, two an SM: the two scores by MMAs (dy
+// takes q's place in shared memory once the first is done), then eight warps of which each has every other
+// 32 columns of its 32 rows: a thread sums its row, and the 32 columns are summed over the warp by halving
+// exchanges.
 // ---------------------------------------------------------------------------------
 constexpr int kPairThreads = 384;
-enum { GF = 0, GS, GT, GN };
+enum { GQ = 0, GY, GS, GP, GN };
 struct PairMaps {
   CUtensorMap q, k, v, y;
 };
@@ -834,25 +828,44 @@ struct PairParams {
   Strides sg;
   const int32_t* count;
   float scale;
-  float *row, *col;  // [B,H,L]
+  float* diff;  // [B,H,L]
   unsigned* status;
+};
+struct alignas(16) PairHead {
+  Ctl<GN> ctl;
+  Factors f;
+  float x[kC];
+  float rows[2][kC], cols[4][kC];  // by half of the columns, by quarter of the rows
 };
 template <int DK, int DV>
 struct PairSmem {
-  static constexpr int kQ = kC * DK * 2, kV = kC * DV * 2;
-  static constexpr int Q = 0, K = kQ, V = 2 * kQ, Y = V + kV, kBytes = kHead + Y + kV;
+  static constexpr int kHead = 5120;
+  static_assert(sizeof(PairHead) <= kHead, "barriers, factors and sums");
+  static constexpr int kQ = kC * DK * 2, kV = kC * DV * 2, kFirst = kQ > kV ? kQ : kV;
+  static constexpr int Q = 0, K = kFirst, V = K + kQ, kBytes = kHead + V + kV;
 };
 
+// 32 values a lane, of 32 columns: lane j gets the sum over the lanes of column j, in a fixed order.
+__device__ __forceinline__ float column_sums(float (&w)[32]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+      if (j < o) w[j] = (up ? w[j + o] : w[j]) + __shfl_xor_sync(0xffffffffu, up ? w[j] : w[j + o], o);
+  }
+  return w[0];
+}
+
 template <int DK, int DV>
-__global__ void __launch_bounds__(kPairThreads, 1)
+__global__ void __launch_bounds__(kPairThreads, 2)
     decay_pairs_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ PairParams p, int chunks) {
   using Sm = PairSmem<DK, DV>;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
-  Ctl<GN>* ctl = reinterpret_cast<Ctl<GN>*>(smem_raw);
-  Factors* f = reinterpret_cast<Factors*>(smem_raw + 64);  // of the rows, of the columns
-  __shared__ __align__(16) float x[kC];
-  static_assert(sizeof(Ctl<GN>) <= 64 && 64 + 2 * sizeof(Factors) <= kHead, "barriers and factors");
-  unsigned char* sm = smem_raw + kHead;
+  PairHead& hd = *reinterpret_cast<PairHead*>(smem_raw);
+  Ctl<GN>* ctl = &hd.ctl;
+  unsigned char* sm = smem_raw + Sm::kHead;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if ((smem_u32(smem_raw) & 1023u) != 0) {
     if (tid == 0) raise_status(p.status, kDevCheck);
@@ -865,7 +878,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   if (count < 0 || count > p.L) count = 0;  // flagged by the passes
   if (t0 >= count) return;
   if (warp == 1) {
-    tmem_alloc(&ctl->tmem, 512);
+    tmem_alloc(&ctl->tmem, 256);
     tmem_relinquish();
   }
   if (tid == 0) {
@@ -879,98 +892,118 @@ __global__ void __launch_bounds__(kPairThreads, 1)
   const uint32_t tmem = ctl->tmem;
   if (warp == 0) {
     if (lane == 0) {
-      uint64_t* bar = &ctl->bar[GF];
-      mbar_arrive_expect_tx(bar, 2 * (Sm::kQ + Sm::kV));
       const int hk = h / p.G;
+      mbar_arrive_expect_tx(&ctl->bar[GQ], 2 * Sm::kQ);
 #pragma unroll
       for (int k = 0; k < DK / 64; ++k) {
-        tma_load_4d(sm + Sm::Q + k * kC * 128, &maps.q, 64 * k, t0, p.qh * h, p.qn * n, bar);
-        tma_load_4d(sm + Sm::K + k * kC * 128, &maps.k, 64 * k, t0, p.kh * hk, p.kn * n, bar);
+        tma_load_4d(sm + Sm::Q + k * kC * 128, &maps.q, 64 * k, t0, p.qh * h, p.qn * n, &ctl->bar[GQ]);
+        tma_load_4d(sm + Sm::K + k * kC * 128, &maps.k, 64 * k, t0, p.kh * hk, p.kn * n, &ctl->bar[GQ]);
       }
+      mbar_arrive_expect_tx(&ctl->bar[GY], 2 * Sm::kV);
 #pragma unroll
-      for (int k = 0; k < DV / 64; ++k) {
-        tma_load_4d(sm + Sm::V + k * kC * 128, &maps.v, 64 * k, t0, p.vh * hk, p.vn * n, bar);
-        tma_load_4d(sm + Sm::Y + k * kC * 128, &maps.y, 64 * k, t0, p.yh * h, p.yn * n, bar);
-      }
-      drain_bar(ctl, GF, 1, globaltimer_ns());
-    }
-  } else if (warp == 1) {
-    if (lane == 0) {
-      const uint32_t sb = smem_u32(sm), id = idesc_bf16(kC, kC, false, false);
-      bool ok = wait_for(ctl, GF, 0);
+      for (int k = 0; k < DV / 64; ++k)
+        tma_load_4d(sm + Sm::V + k * kC * 128, &maps.v, 64 * k, t0, p.vh * hk, p.vn * n, &ctl->bar[GY]);
+      const bool ok = wait_for(ctl, GS, 0);
       if (ok) {
-        tc_fence_after();
 #pragma unroll
-        for (int j = 0; j < DK / 16; ++j) mma_bf16(tmem, desc_k(sb + Sm::Q, kC, j), desc_k(sb + Sm::K, kC, j), id, j > 0);
-#pragma unroll
-        for (int j = 0; j < DV / 16; ++j) mma_bf16(tmem + 128, desc_k(sb + Sm::Y, kC, j), desc_k(sb + Sm::V, kC, j), id, j > 0);
-        mma_commit(&ctl->bar[GS]);
-#pragma unroll
-        for (int j = 0; j < DK / 16; ++j)
-          mma_bf16(tmem + 256, desc_k(sb + Sm::K, kC, j), desc_k(sb + Sm::Q, kC, j), id, j > 0);
-#pragma unroll
-        for (int j = 0; j < DV / 16; ++j)
-          mma_bf16(tmem + 384, desc_k(sb + Sm::V, kC, j), desc_k(sb + Sm::Y, kC, j), id, j > 0);
+        for (int k = 0; k < DV / 64; ++k)
+          tma_load_4d(sm + Sm::Q + k * kC * 128, &maps.y, 64 * k, t0, p.yh * h, p.yn * n, &ctl->bar[GY]);
       } else {
         ctl->abort = 1;
       }
-      mma_commit(&ctl->bar[GT]);
-      drain_bar(ctl, GT, 1, globaltimer_ns());
+      const uint64_t began = globaltimer_ns();
+      drain_bar(ctl, GQ, 1, began);
+      drain_bar(ctl, GY, 1, began);
     }
+  } else if (warp == 1) {
+    const uint32_t sb = smem_u32(sm), id = idesc_bf16(kC, kC, false, false);
+    const uint32_t dq = desc_lower(sb + Sm::Q, 16), dk = desc_lower(sb + Sm::K, 16), dv = desc_lower(sb + Sm::V, 16);
+    bool ok = wait_warp(ctl, GQ, 0);
+    if (ok) {
+      tc_fence_after();
+#pragma unroll 4
+      for (int j = 0; j < DK / 16; ++j) mma_lo(tmem, dq + step_k(j), dk + step_k(j), id, j > 0);
+    }
+    commit_lo(&ctl->bar[GS]);
+    ok = ok && wait_warp(ctl, GY, 0);
+    if (ok) {
+      tc_fence_after();
+#pragma unroll 4
+      for (int j = 0; j < DV / 16; ++j) mma_lo(tmem + 128, dq + step_k(j), dv + step_k(j), id, j > 0);
+    } else {
+      ctl->abort = 1;
+    }
+    commit_lo(&ctl->bar[GP]);
+    drain_bar(ctl, GP, 1, globaltimer_ns());
+    __syncwarp();
   } else if (warp >= 4) {
-    const bool rev = warp >= 8;  // the columns: token s receives from the later ones
-    const int qw = warp & 3, o = 32 * qw + lane, I = o >> 4;
+    const int half = (warp - 4) >> 2, qw = warp & 3, o = 32 * qw + lane, I = o >> 4;
     if (warp == 4) {
       Share v;
       load_decays(p.lg + n * p.sg.n + h * p.sg.h, p.sg.t, t0, count, v.x);
-      *reinterpret_cast<float4*>(x + 4 * lane) = make_float4(v.x[0], v.x[1], v.x[2], v.x[3]);
+      *reinterpret_cast<float4*>(hd.x + 4 * lane) = make_float4(v.x[0], v.x[1], v.x[2], v.x[3]);
       v.make(false);
-      v.put(f[0]);
-      v.make(true);
-      v.put(f[1]);
+      v.put(hd.f);
     }
     named_sync(1, 256);
-    const Factors& f_ = f[rev];
-    const uint32_t tl = tmem + ((uint32_t)(qw * 32) << 16) + (rev ? 256 : 0);
-    const bool ok = wait_for(ctl, rev ? GT : GS, 0);
+    const Factors& f = hd.f;
+    const uint32_t tl = tmem + ((uint32_t)(qw * 32) << 16);
+    const bool ok = wait_for(ctl, GP, 0);
+    float sum = 0.f;
     if (ok) {
       tc_fence_after();
-      const float rf = exp2f(f_.row[o]);
-      float sum = 0.f;
+      const float rf = exp2f(f.row[o]);
+      const bool there = t0 + o < count;
 #pragma unroll 1
-      for (int g = 0; g < 4; ++g) {
-        if (rev ? g < qw : g > qw) continue;
-        uint32_t s[32], y[32];
-        tmem_ld32(tl + 32 * g, s);
-        tmem_ld32(tl + 128 + 32 * g, y);
-        float d[16];
-        if (g == qw) block_decays(x + 16 * I, lane & 15, rev, d);
-        tmem_ld_wait();
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          const bool own = g == qw && (lane >> 4) == b;
-          const float r = g != qw ? rf * f_.g[I * 8 + 2 * g + b] : (rev ? b == 1 : b == 0) ? rf : 0.f;
+      for (int g = half; g <= qw; g += 2) {
+        uint32_t s[32];
+        float w[32];
+        if (g == qw) {
+          // the thread's own block of 16 by running sums, the one before it wholly, what is behind nothing
+          float d[16];
+          block_decays(hd.x + 16 * I, lane & 15, false, d);
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
-            const int e = 32 * g + 16 * b + j;
-            const float w = own ? (e == o ? 0.f : d[j]) : r * f_.col[e];
-            // (a decay of 0 hides the token, and rows behind the sequence may hold anything)
-            const float v = f32(s[16 * b + j]) * f32(y[16 * b + j]);
-            sum += w != 0.f && t0 + e < count ? w * v : 0.f;
+            const float in = j == (lane & 15) ? 0.f : d[j];
+            w[j] = lane < 16 ? in : rf * f.col[32 * g + j];
+            w[16 + j] = lane < 16 ? 0.f : in;
           }
+        } else {
+          const float r0 = rf * f.g[I * 8 + 2 * g], r1 = rf * f.g[I * 8 + 2 * g + 1];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) w[j] = (j < 16 ? r0 : r1) * f.col[32 * g + j];
         }
+        tmem_ld32(tl + 32 * g, s);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 32; ++j) w[j] = w[j] != 0.f && there ? w[j] * f32(s[j]) : 0.f;
+        tmem_ld32(tl + 128 + 32 * g, s);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          // (rows behind the sequence may hold anything, and a decay of 0 hides a token)
+          w[j] = w[j] != 0.f ? w[j] * f32(s[j]) : 0.f;
+          sum += w[j];
+        }
+        hd.cols[qw][32 * g + lane] = column_sums(w);
       }
-      const int t = t0 + o;
-      if (t < count) (rev ? p.col : p.row)[(int64_t)unit * p.L + t] = p.scale * sum;
+      hd.rows[half][o] = sum;
     } else {
       ctl->abort = 1;
+    }
+    named_sync(1, 256);
+    const int t = tid - 128;
+    if (t < kC && t0 + t < count && !*(volatile int*)&ctl->abort) {
+      float d = hd.rows[0][t] + hd.rows[1][t], c = 0.f;
+      for (int r = t >> 5; r < 4; ++r) c += hd.cols[r][t];
+      p.diff[(int64_t)unit * p.L + t0 + t] = p.scale * (d - c);
     }
   }
   tc_fence_before();
   cta_sync();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc(tmem, 256);
   }
   if (tid == 0 && ctl->abort) raise_status(p.status, kDevTimeout);
 }
@@ -1068,7 +1101,7 @@ cudaError_t launch_decay_pairs(const DecayPairs& a, cudaStream_t s, int* launche
       !rows_map(&m.y, a.dy, a.B, a.H, a.L, a.dv, a.sy, &p.yn, &p.yh))
     return cudaErrorInvalidValue;
   p.B = a.B, p.H = a.H, p.L = a.L, p.G = a.G, p.lg = a.lg, p.sg = a.sg, p.count = a.count, p.scale = a.scale;
-  p.row = a.row, p.col = a.col, p.status = a.status;
+  p.diff = a.diff, p.status = a.status;
   trace_begin("decay_pairs", s);
   cudaError_t e;
   if (a.dk == 64)

@@ -179,14 +179,30 @@ __global__ void __launch_bounds__(TPR > kBlock ? TPR : kBlock) norm_fwd_kernel(N
   if (live) store<T, TPR>(static_cast<T*>(a.y) + offset(a.sy, i), lane, a.d, f);
 }
 
+// Rows on their way to a thread of the backward: a ring of its own vectors of x and dy in shared memory,
+// filled by asynchronous copies.  Memory's latency times its rate is about 40 KB for each SM; a row ahead
+// in registers is 32 (8191 rows of 4096: 70 us).
+template <typename T, int THREADS>
+struct Ring {
+  static constexpr int NV = Frag<T>::NV, kStage = 2 * NV * THREADS * 16;
+  static constexpr int D = kStage <= 16384 ? 4 : kStage <= 65536 ? 3 : 1;
+  static constexpr int kBytes = D * kStage;
+};
+__device__ __forceinline__ void copy16(uint4* dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+               "l"(src), "r"(there ? 16 : 0)
+               : "memory");
+}
+
 // Block (x, y): every gridDim.x-th group of rows of head y (per_head) or of all rows.  The sums of
 // dw and db stay in the threads' registers until the block's last row; then the block's rows are
-// added up in a fixed order into part[y][x][2][d].  The next row is on its way while one is
-// worked on.
+// added up in a fixed order into part[y][x][2][d].
 template <typename T, int TPR>
 __global__ void __launch_bounds__(TPR > kBlock ? TPR : kBlock) norm_bwd_kernel(NormCall a, uint32_t rows, bool heads_inner) {
   constexpr int THREADS = TPR > kBlock ? TPR : kBlock, RPB = THREADS / TPR;
-  extern __shared__ float sums[];  // [warps][2][d] for rows within a warp, [RPB][2][d] for wider ones
+  using R = Ring<T, THREADS>;
+  // the ring; then [warps][2][d] sums for rows within a warp, [RPB][2][d] for wider ones
+  extern __shared__ __align__(16) uint4 ring[];
   __shared__ float part[128], part2[128];
   pdl_wait();
   const int lane = threadIdx.x % TPR;
@@ -198,32 +214,52 @@ __global__ void __launch_bounds__(TPR > kBlock ? TPR : kBlock) norm_bwd_kernel(N
     return Index{n, blockIdx.y, r - n * a.T};
   };
   float w[kEpt], dw[kEpt], db[kEpt];
-  Frag<T> f, g;
-  load<T, TPR>(a.w ? static_cast<const T*>(a.w) + (a.per_head ? (int64_t)blockIdx.y * a.d : 0) : nullptr, lane, a.d, f);
-  unpack(f, w);
+  {
+    Frag<T> f;
+    load<T, TPR>(a.w ? static_cast<const T*>(a.w) + (a.per_head ? (int64_t)blockIdx.y * a.d : 0) : nullptr, lane, a.d, f);
+    unpack(f, w);
+  }
 #pragma unroll
   for (int e = 0; e < kEpt; ++e) {
     if (!a.w) w[e] = 1.f;
     dw[e] = db[e] = 0.f;
   }
   const float inv_d = 1.f / a.d;
-  const uint32_t step = gridDim.x * RPB;
-  uint32_t r = blockIdx.x * RPB + threadIdx.x / TPR;
-  bool live = r < rows;
-  Index i = at(live ? r : 0);
-  load<T, TPR>(live ? xs + offset(a.sx, i) : nullptr, lane, a.d, f);
-  load<T, TPR>(live ? dys + offset(a.sdy, i) : nullptr, lane, a.d, g);
-  for (uint32_t first = blockIdx.x * RPB; first < rows; first += step) {
+  const uint32_t step = gridDim.x * RPB, first = blockIdx.x * RPB, own = first + threadIdx.x / TPR;
+  auto fetch = [&](uint32_t r, int stage) {  // (one group a row, there or not)
+    if (r < rows) {
+      const Index i = at(r);
+      const T *px = xs + offset(a.sx, i), *py = dys + offset(a.sdy, i);
+      uint4* d = ring + stage * (2 * R::NV * THREADS) + threadIdx.x;
+#pragma unroll
+      for (int k = 0; k < R::NV; ++k) {
+        const int c = (lane + TPR * k) * Frag<T>::V;
+        const bool there = c < a.d;
+        copy16(d + k * THREADS, px + (there ? c : 0), there);
+        copy16(d + (R::NV + k) * THREADS, py + (there ? c : 0), there);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+#pragma unroll
+  for (int k = 0; k < R::D; ++k) fetch(own + k * step, k);
+  int stage = 0;
+  for (uint32_t base = first; base < rows; base += step) {
+    const uint32_t r = own + (base - first);
     float x[kEpt], dy[kEpt];
+    Frag<T> f, g;
+    asm volatile("cp.async.wait_group %0;" ::"n"(R::D - 1) : "memory");
+    const uint4* d = ring + stage * (2 * R::NV * THREADS) + threadIdx.x;
+    const bool live = r < rows;
+#pragma unroll
+    for (int k = 0; k < R::NV; ++k) {
+      f.v[k] = live ? d[k * THREADS] : make_uint4(0, 0, 0, 0);
+      g.v[k] = live ? d[(R::NV + k) * THREADS] : make_uint4(0, 0, 0, 0);
+    }
     unpack(f, x);
     unpack(g, dy);
-    const bool live_now = live;
-    const int64_t to = offset(a.sy, i);
-    r += step;  // rows + step fits: both are below 2^31
-    live = r < rows;
-    i = at(live ? r : 0);
-    load<T, TPR>(live ? xs + offset(a.sx, i) : nullptr, lane, a.d, f);
-    load<T, TPR>(live ? dys + offset(a.sdy, i) : nullptr, lane, a.d, g);
+    fetch(r + R::D * step, stage);  // (below 2^32: rows are below 2^31, a step below 2^16)
+    stage = stage + 1 == R::D ? 0 : stage + 1;
     const float rs = centre<T, TPR>(x, lane, a.d, a.eps, inv_d, part);
     float s[2] = {0.f, 0.f};
 #pragma unroll
@@ -241,9 +277,10 @@ __global__ void __launch_bounds__(TPR > kBlock ? TPR : kBlock) norm_bwd_kernel(N
     for (int e = 0; e < kEpt; ++e) x[e] = rs * (dy[e] - m0 - x[e] * m1);
     Frag<T> o;
     pack(x, o);
-    if (live_now && a.y) store<T, TPR>(static_cast<T*>(a.y) + to, lane, a.d, o);
+    if (live && a.y) store<T, TPR>(static_cast<T*>(a.y) + offset(a.sy, at(r)), lane, a.d, o);
   }
   if (!a.part) return;
+  float* sums = reinterpret_cast<float*>(ring + R::kBytes / 16);
   // rows of one warp, then the block's warps (or rows) one after the other
   constexpr int PARTS = TPR < 32 ? THREADS / 32 : RPB;
 #pragma unroll
@@ -327,9 +364,13 @@ template <typename T, int TPR>
 cudaError_t bwd(const NormCall& a, cudaStream_t s) {
   const uint32_t rows = (uint32_t)a.N * a.T * (a.per_head ? 1 : a.H);
   const int sets = a.per_head ? a.H : 1;
-  const int parts = TPR < 32 ? kBlock / 32 : TPR >= kBlock ? 0 : kBlock / TPR;  // at most 32 KB
-  return launch_pdl(norm_bwd_kernel<T, TPR>, dim3(bwd_blocks(rows, sets, a.d), sets), dim3(TPR > kBlock ? TPR : kBlock),
-                    (size_t)parts * 2 * a.d * sizeof(float), s, a, rows, heads_inner(a));
+  const int parts = TPR < 32 ? kBlock / 32 : TPR >= kBlock ? 0 : kBlock / TPR;  // at most 32 KB of sums
+  constexpr int threads = TPR > kBlock ? TPR : kBlock;
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_smem(norm_bwd_kernel<T, TPR>, Ring<T, threads>::kBytes + (TPR >= kBlock ? 0 : 32768), done);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(norm_bwd_kernel<T, TPR>, dim3(bwd_blocks(rows, sets, a.d), sets), dim3(threads),
+                    Ring<T, threads>::kBytes + (size_t)parts * 2 * a.d * sizeof(float), s, a, rows, heads_inner(a));
 }
 
 template <typename T>

@@ -438,7 +438,7 @@ constexpr int kDecayTile = 128;
 bool decay_tc_rows_ok(int B, int H, int L, int d, const Strides& s);
 size_t decay_tc_workspace(int B, int H, int L, int da, int dc);
 cudaError_t launch_decay_tc(const DecayPass& a, bool exact_state, float* ws, cudaStream_t s, int* launches);
-// What each token receives from (row) and gives to (col) other tokens of its chunk in the gradient of
+// What each token receives from other tokens of its chunk less what it gives to them in the gradient of
 // log_decay, in 128-token chunks.
 struct DecayPairs {
   int B, H, G, L, dk, dv;
@@ -448,7 +448,7 @@ struct DecayPairs {
   Strides sg;
   const int32_t* count;
   float scale;
-  float *row, *col;  // [B,H,L]
+  float* diff;  // [B,H,L]
   unsigned* status;
 };
 cudaError_t launch_decay_pairs(const DecayPairs& a, cudaStream_t s, int* launches);
@@ -459,7 +459,7 @@ cudaError_t launch_decay_heads(int B, int Hk, int G, int L, int d, const float* 
 struct DecayGate {
   int B, H, L, chunk;
   int in_slices, out_slices;
-  const float *row_in, *col_in;    // [in_slices][B,H,L]
+  const float *row_in, *col_in;    // [in_slices][B,H,L]; col_in may be null (the difference in row_in)
   const float *row_out, *col_out;  // [out_slices][B,H,L]
   const float *h0, *d_h0;                            // [B,H,state], or null
   int state;
