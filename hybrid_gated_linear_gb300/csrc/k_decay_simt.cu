@@ -392,18 +392,15 @@ __global__ void __launch_bounds__(32 * kGateWarps) decay_gate_sums_kernel(DecayG
   if (t0 >= end) return;
   const int64_t plane = (int64_t)units * a.L, base = (int64_t)unit * a.L;
   const float* lg = a.lg + n * a.sg.n + h * a.sg.h;
-  double rows = 0.0, cols = 0.0;
+  float r = 0.f, c1 = 0.f;
   bool start = false;
-  for (int g = t0; g < end; g += 32) {
-    float r = 0.f, c = 0.f;
-    if (g + lane < end) {
-      const int64_t at = base + g + lane;
 #pragma unroll 4
-      for (int s = 0; s < a.out_slices; ++s) r += a.row_out[s * plane + at], c += a.col_out[s * plane + at];
-      start |= lg[(g + lane) * a.sg.t] < kDecayNone;
-    }
-    rows += warp_sum(r), cols += warp_sum(c);
+  for (int t = t0 + lane; t < end; t += 32) {
+#pragma unroll 4
+    for (int s = 0; s < a.out_slices; ++s) r += a.row_out[s * plane + base + t], c1 += a.col_out[s * plane + base + t];
+    start |= lg[t * a.sg.t] < kDecayNone;
   }
+  const double rows = warp_sum(r), cols = warp_sum(c1);
   start = __any_sync(0xffffffffu, start);
   if (lane == 0) a.sums[(int64_t)unit * (chunks + 1) + c] = make_double2(start ? nan("") : rows, cols);
 }
@@ -432,29 +429,38 @@ __global__ void __launch_bounds__(32 * kGateWarps) decay_gate_kernel(DecayGate a
   const double2 own = sums[c];
   const double through = isnan(own.x) ? 0.0 : edge - own.x;
   const float* lg = a.lg + n * a.sg.n + h * a.sg.h;
-  // the chunk's groups of 32 tokens from the last to the first, with what lies behind each
-  double behind = 0.0, before = own.y;  // of the suffix sums; col_out of the tokens before the group's end
-  for (int g0 = t0 + (end - t0 - 1) / 32 * 32; g0 >= t0; g0 -= 32) {
-    const int t = g0 + lane;
-    float sum = 0.f, col = 0.f;
-    bool cut = false;
+  // the chunk's groups of 32 tokens: all of their numbers first, then from the last group to the first
+  // with what lies behind each
+  constexpr int kG = kDecayTile / 32;
+  static_assert(kDecayTile >= kDecayChunk && kDecayTile % 32 == 0, "groups of a chunk");
+  float sum[kG], col[kG];
+  unsigned cut = 0;  // a document's start: nothing passes over it
+#pragma unroll
+  for (int g = 0; g < kG; ++g) {
+    const int t = t0 + 32 * g + lane;
+    sum[g] = col[g] = 0.f;
     if (t < end) {
-      // a document's start: nothing passes over it
-      cut = lg[t * a.sg.t] < kDecayNone;
+      if (lg[t * a.sg.t] < kDecayNone) cut |= 1u << g;
 #pragma unroll 2
       for (int s = 0; s < a.in_slices; ++s)
-        sum += a.row_in[s * plane + base + t] - (a.col_in ? a.col_in[s * plane + base + t] : 0.f);
+        sum[g] += a.row_in[s * plane + base + t] - (a.col_in ? a.col_in[s * plane + base + t] : 0.f);
 #pragma unroll 4
-      for (int s = 0; s < a.out_slices; ++s) sum += a.row_out[s * plane + base + t], col += a.col_out[s * plane + base + t];
+      for (int s = 0; s < a.out_slices; ++s)
+        sum[g] += a.row_out[s * plane + base + t], col[g] += a.col_out[s * plane + base + t];
     }
+  }
+  double behind = through, before = own.y;  // the suffix sums behind a group; col_out of the tokens before its end
+#pragma unroll
+  for (int g = kG - 1; g >= 0; --g) {
+    const int t = t0 + 32 * g + lane;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const float u = __shfl_down_sync(0xffffffffu, sum, o), v = __shfl_down_sync(0xffffffffu, col, o);
-      if (lane + o < 32) sum += u, col += v;
+      const float u = __shfl_down_sync(0xffffffffu, sum[g], o), v = __shfl_down_sync(0xffffffffu, col[g], o);
+      if (lane + o < 32) sum[g] += u, col[g] += v;
     }
-    if (t < end) a.d_lg[base + t] = cut ? 0.f : (float)(behind + before + through + (double)(sum - col));
-    behind += __shfl_sync(0xffffffffu, sum, 0);
-    before -= __shfl_sync(0xffffffffu, col, 0);
+    if (t < end) a.d_lg[base + t] = cut >> g & 1 ? 0.f : (float)(behind + before + (double)(sum[g] - col[g]));
+    behind += __shfl_sync(0xffffffffu, sum[g], 0);
+    before -= __shfl_sync(0xffffffffu, col[g], 0);
   }
 }
 

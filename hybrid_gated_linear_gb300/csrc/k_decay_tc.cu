@@ -182,23 +182,6 @@ __device__ __forceinline__ float f32(uint32_t u) { return __uint_as_float(u); }
 __device__ __forceinline__ float lo_f(uint32_t u) { return __uint_as_float(u << 16); }
 __device__ __forceinline__ float hi_f(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
 
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  float2 d;
-  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmul.rn.f32x2 z, x, y;\n\t"
-      "mov.b64 {%0, %1}, z;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
-      "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-  return d;
-}
-
 // The upper halves of two words, the first's below: two floats cut to bf16.
 __device__ __forceinline__ uint32_t upper(float a, float b) {
   return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
@@ -211,10 +194,10 @@ __device__ __forceinline__ float2 cut(float2 v) {
 __device__ __forceinline__ void split(float2 v, bool three, uint32_t (&o)[3]) {
   const float2 minus = make_float2(-1.f, -1.f);
   o[0] = upper(v.x, v.y);
-  v = fma2(cut(v), minus, v);
+  v = f2_fma(cut(v), minus, v);
   if (three) {
     o[1] = upper(v.x, v.y);
-    v = fma2(cut(v), minus, v);
+    v = f2_fma(cut(v), minus, v);
     o[2] = upper(v.x, v.y);
   } else {
     o[1] = pack_bf16x2(v.x, v.y);
@@ -561,10 +544,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint4 v = *reinterpret_cast<const uint4*>(tc_ + at);
         const bool three = q.parts > 2;
         uint32_t o0[3], o1[3], o2[3], o3[3];
-        split(mul2(w2, make_float2(lo_f(v.x), hi_f(v.x))), three, o0);
-        split(mul2(w2, make_float2(lo_f(v.y), hi_f(v.y))), three, o1);
-        split(mul2(w2, make_float2(lo_f(v.z), hi_f(v.z))), three, o2);
-        split(mul2(w2, make_float2(lo_f(v.w), hi_f(v.w))), three, o3);
+        split(f2_mul(w2, make_float2(lo_f(v.x), hi_f(v.x))), three, o0);
+        split(f2_mul(w2, make_float2(lo_f(v.y), hi_f(v.y))), three, o1);
+        split(f2_mul(w2, make_float2(lo_f(v.z), hi_f(v.z))), three, o2);
+        split(f2_mul(w2, make_float2(lo_f(v.w), hi_f(v.w))), three, o3);
         unsigned char* d = cp + at;
         *reinterpret_cast<uint4*>(d) = make_uint4(o0[0], o1[0], o2[0], o3[0]);
         *reinterpret_cast<uint4*>(d + kTileC) = make_uint4(o0[1], o1[1], o2[1], o3[1]);
@@ -597,7 +580,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld_wait();
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          const float2 u = mul2(make_float2(f32(s[2 * k]), f32(s[2 * k + 1])), make_float2(d[2 * k], d[2 * k + 1]));
+          const float2 u = f2_mul(make_float2(f32(s[2 * k]), f32(s[2 * k + 1])), make_float2(d[2 * k], d[2 * k + 1]));
           w[k] = pack_bf16x2(u.x, u.y);
         }
         tmem_st8(tp + 8 * j1, w);
@@ -613,12 +596,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float4 v = *reinterpret_cast<const float4*>(&f.col[16 * j + 4 * e]);
-          c[2 * e] = mul2(r, make_float2(v.x, v.y)), c[2 * e + 1] = mul2(r, make_float2(v.z, v.w));
+          c[2 * e] = f2_mul(r, make_float2(v.x, v.y)), c[2 * e + 1] = f2_mul(r, make_float2(v.z, v.w));
         }
         tmem_ld_wait();
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const float2 u = mul2(make_float2(f32(s[2 * e]), f32(s[2 * e + 1])), c[e]);
+          const float2 u = f2_mul(make_float2(f32(s[2 * e]), f32(s[2 * e + 1])), c[e]);
           w[e] = pack_bf16x2(u.x, u.y);
         }
         tmem_st8(tp + 8 * j, w);
@@ -699,13 +682,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld8(tk + kN + 8 * e, k1);
         if (q.parts > 2) tmem_ld8(tk + 2 * kN + 8 * e, k2);
         tmem_ld_wait();
-        const float2 one = make_float2(1.f, 1.f);
-#pragma unroll
+        #pragma unroll
         for (int j = 0; j < 4; ++j) {
           float* h2 = &x[8 * e + 2 * j];
-          const float2 v = fma2(one, make_float2(f32(k2[2 * j]), f32(k2[2 * j + 1])), make_float2(f32(k1[2 * j]), f32(k1[2 * j + 1])));
-          const float2 w = fma2(one, v, make_float2(f32(k0[2 * j]), f32(k0[2 * j + 1])));
-          const float2 u = fma2(all2, make_float2(h2[0], h2[1]), w);
+          const float2 v = f2_add(make_float2(f32(k2[2 * j]), f32(k2[2 * j + 1])), make_float2(f32(k1[2 * j]), f32(k1[2 * j + 1])));
+          const float2 w = f2_add(v, make_float2(f32(k0[2 * j]), f32(k0[2 * j + 1])));
+          const float2 u = f2_fma(all2, make_float2(h2[0], h2[1]), w);
           h2[0] = u.x, h2[1] = u.y;
         }
       }
@@ -752,7 +734,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float2 v[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          v[j] = mul2(scale, fma2(from2, make_float2(f32(ys[2 * j]), f32(ys[2 * j + 1])),
+          v[j] = f2_mul(scale, f2_fma(from2, make_float2(f32(ys[2 * j]), f32(ys[2 * j + 1])),
                                   make_float2(f32(y[2 * j]), f32(y[2 * j + 1]))));
           if (!live) v[j] = make_float2(0.f, 0.f);  // rows behind the sequence may have held anything
         }

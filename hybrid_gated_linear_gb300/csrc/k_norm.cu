@@ -21,37 +21,36 @@ struct Frag {
   uint4 v[NV];
 };
 
-__device__ __forceinline__ void unpack(const Frag<float>& f, float (&o)[kEpt]) {
+// A thread's channels in pairs, for the instructions that take two.
+constexpr int kP = kEpt / 2;
+__device__ __forceinline__ void unpack(const Frag<float>& f, float2 (&o)[kP]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    o[4 * i] = __uint_as_float(f.v[i].x), o[4 * i + 1] = __uint_as_float(f.v[i].y);
-    o[4 * i + 2] = __uint_as_float(f.v[i].z), o[4 * i + 3] = __uint_as_float(f.v[i].w);
+    o[2 * i] = make_float2(__uint_as_float(f.v[i].x), __uint_as_float(f.v[i].y));
+    o[2 * i + 1] = make_float2(__uint_as_float(f.v[i].z), __uint_as_float(f.v[i].w));
   }
 }
-__device__ __forceinline__ void unpack(const Frag<bf16>& f, float (&o)[kEpt]) {
+__device__ __forceinline__ void unpack(const Frag<bf16>& f, float2 (&o)[kP]) {
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const uint32_t w[4] = {f.v[i].x, f.v[i].y, f.v[i].z, f.v[i].w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      o[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
-      o[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-    }
+    for (int j = 0; j < 4; ++j) o[4 * i + j] = make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xffff0000u));
   }
 }
-__device__ __forceinline__ void pack(const float (&o)[kEpt], Frag<float>& f) {
+__device__ __forceinline__ void pack(const float2 (&o)[kP], Frag<float>& f) {
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    f.v[i] = make_uint4(__float_as_uint(o[4 * i]), __float_as_uint(o[4 * i + 1]), __float_as_uint(o[4 * i + 2]),
-                        __float_as_uint(o[4 * i + 3]));
+    f.v[i] = make_uint4(__float_as_uint(o[2 * i].x), __float_as_uint(o[2 * i].y), __float_as_uint(o[2 * i + 1].x),
+                        __float_as_uint(o[2 * i + 1].y));
 }
-__device__ __forceinline__ void pack(const float (&o)[kEpt], Frag<bf16>& f) {
+__device__ __forceinline__ void pack(const float2 (&o)[kP], Frag<bf16>& f) {
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     uint32_t w[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const __nv_bfloat162 p = __floats2bfloat162_rn(o[8 * i + 2 * j], o[8 * i + 2 * j + 1]);
+      const __nv_bfloat162 p = __floats2bfloat162_rn(o[4 * i + j].x, o[4 * i + j].y);
       w[j] = *reinterpret_cast<const uint32_t*>(&p);
     }
     f.v[i] = make_uint4(w[0], w[1], w[2], w[3]);
@@ -109,20 +108,24 @@ __device__ __forceinline__ void row_sum(float (&s)[N], float* part, int parity) 
   }
 }
 
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
 // x becomes x - mean; returns 1 / sqrt(var + eps).
 template <typename T, int TPR>
-__device__ __forceinline__ float centre(float (&x)[kEpt], int lane, int d, float eps, float inv_d, float* part) {
-  float s[1] = {0.f};
+__device__ __forceinline__ float centre(float2 (&x)[kP], int lane, int d, float eps, float inv_d, float* part) {
+  float2 t = x[0];
 #pragma unroll
-  for (int e = 0; e < kEpt; ++e) s[0] += x[e];
+  for (int e = 1; e < kP; ++e) t = f2_add(t, x[e]);
+  float s[1] = {t.x + t.y};
   row_sum<TPR>(s, part, 0);
-  const float mean = s[0] * inv_d;
-  s[0] = 0.f;
+  const float2 minus = both(-s[0] * inv_d);
+  t = both(0.f);
 #pragma unroll
-  for (int e = 0; e < kEpt; ++e) {
-    x[e] = inside<T, TPR>(lane, d, e) ? x[e] - mean : 0.f;
-    s[0] = fmaf(x[e], x[e], s[0]);
+  for (int e = 0; e < kP; ++e) {
+    x[e] = inside<T, TPR>(lane, d, 2 * e) ? f2_add(x[e], minus) : both(0.f);
+    t = f2_fma(x[e], x[e], t);
   }
+  s[0] = t.x + t.y;
   row_sum<TPR>(s, part, 1);
   return rsqrtf(fmaf(s[0], inv_d, eps));
 }
@@ -147,6 +150,19 @@ __device__ __forceinline__ Index index_of(const NormCall& a, uint32_t r, bool he
   }
   return i;
 }
+// The index `step` rows on, by its parts (a division costs what a third of a row's arithmetic does).
+struct Walk {
+  uint32_t in, mid, out;  // the inner axis, the next, and n
+  __device__ __forceinline__ void start(uint32_t r, uint32_t n_in, uint32_t n_mid) {
+    const uint32_t q = r / n_in;
+    in = r - q * n_in, out = q / n_mid, mid = q - out * n_mid;
+  }
+  __device__ __forceinline__ void advance(const Walk& step, uint32_t n_in, uint32_t n_mid) {
+    in += step.in, mid += step.mid, out += step.out;
+    if (in >= n_in) in -= n_in, ++mid;
+    if (mid >= n_mid) mid -= n_mid, ++out;
+  }
+};
 __device__ __forceinline__ int64_t offset(const Strides& s, const Index& i) {
   return i.n * s.n + i.h * s.h + i.t * s.t;
 }
@@ -165,16 +181,13 @@ __global__ void __launch_bounds__(TPR > kBlock ? TPR : kBlock) norm_fwd_kernel(N
   const int64_t wo = a.per_head ? (int64_t)i.h * a.d : 0;
   load<T, TPR>(a.w ? static_cast<const T*>(a.w) + wo : nullptr, lane, a.d, fw);
   load<T, TPR>(a.b ? static_cast<const T*>(a.b) + wo : nullptr, lane, a.d, fb);
-  float x[kEpt], w[kEpt], b[kEpt];
+  float2 x[kP], w[kP], b[kP];
   unpack(f, x);
-  const float rs = centre<T, TPR>(x, lane, a.d, a.eps, 1.f / a.d, part);
+  const float2 rs = both(centre<T, TPR>(x, lane, a.d, a.eps, 1.f / a.d, part));
   unpack(fw, w);
   unpack(fb, b);
 #pragma unroll
-  for (int e = 0; e < kEpt; ++e) {
-    const float n = x[e] * rs;
-    x[e] = a.w ? fmaf(n, w[e], b[e]) : n + b[e];
-  }
+  for (int e = 0; e < kP; ++e) x[e] = f2_fma(f2_mul(x[e], rs), a.w ? w[e] : both(1.f), b[e]);
   pack(x, f);
   if (live) store<T, TPR>(static_cast<T*>(a.y) + offset(a.sy, i), lane, a.d, f);
 }
@@ -208,27 +221,32 @@ __global__ void __launch_bounds__(TPR > kBlock ? TPR : kBlock) norm_bwd_kernel(N
   const int lane = threadIdx.x % TPR;
   const T* xs = static_cast<const T*>(a.x);
   const T* dys = static_cast<const T*>(a.dy);
-  auto at = [&](uint32_t r) {
-    if (!a.per_head) return index_of(a, r, heads_inner);
-    const uint32_t n = r / a.T;
-    return Index{n, blockIdx.y, r - n * a.T};
+  // rows of one head: tokens of sequences; of all heads: in the order of index_of
+  const uint32_t n_in = a.per_head || !heads_inner ? a.T : a.H, n_mid = a.per_head ? 1 : heads_inner ? a.T : a.H;
+  auto at = [&](const Walk& p) {
+    if (a.per_head) return Index{p.out, blockIdx.y, p.in};
+    return heads_inner ? Index{p.out, p.in, p.mid} : Index{p.out, p.mid, p.in};
   };
-  float w[kEpt], dw[kEpt], db[kEpt];
+  float2 w[kP], dw[kP], db[kP];
   {
     Frag<T> f;
     load<T, TPR>(a.w ? static_cast<const T*>(a.w) + (a.per_head ? (int64_t)blockIdx.y * a.d : 0) : nullptr, lane, a.d, f);
     unpack(f, w);
   }
 #pragma unroll
-  for (int e = 0; e < kEpt; ++e) {
-    if (!a.w) w[e] = 1.f;
-    dw[e] = db[e] = 0.f;
+  for (int e = 0; e < kP; ++e) {
+    if (!a.w) w[e] = both(1.f);
+    dw[e] = db[e] = both(0.f);
   }
   const float inv_d = 1.f / a.d;
   const uint32_t step = gridDim.x * RPB, first = blockIdx.x * RPB, own = first + threadIdx.x / TPR;
+  Walk next, here, by;  // of the row to fetch, of the row at work, of a step
+  next.start(own, n_in, n_mid);
+  here = next;
+  by.start(step, n_in, n_mid);
   auto fetch = [&](uint32_t r, int stage) {  // (one group a row, there or not)
     if (r < rows) {
-      const Index i = at(r);
+      const Index i = at(next);
       const T *px = xs + offset(a.sx, i), *py = dys + offset(a.sdy, i);
       uint4* d = ring + stage * (2 * R::NV * THREADS) + threadIdx.x;
 #pragma unroll
@@ -239,6 +257,7 @@ __global__ void __launch_bounds__(TPR > kBlock ? TPR : kBlock) norm_bwd_kernel(N
         copy16(d + (R::NV + k) * THREADS, py + (there ? c : 0), there);
       }
     }
+    next.advance(by, n_in, n_mid);
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
 #pragma unroll
@@ -246,7 +265,7 @@ __global__ void __launch_bounds__(TPR > kBlock ? TPR : kBlock) norm_bwd_kernel(N
   int stage = 0;
   for (uint32_t base = first; base < rows; base += step) {
     const uint32_t r = own + (base - first);
-    float x[kEpt], dy[kEpt];
+    float2 x[kP], dy[kP];
     Frag<T> f, g;
     asm volatile("cp.async.wait_group %0;" ::"n"(R::D - 1) : "memory");
     const uint4* d = ring + stage * (2 * R::NV * THREADS) + threadIdx.x;
@@ -260,24 +279,26 @@ __global__ void __launch_bounds__(TPR > kBlock ? TPR : kBlock) norm_bwd_kernel(N
     unpack(g, dy);
     fetch(r + R::D * step, stage);  // (below 2^32: rows are below 2^31, a step below 2^16)
     stage = stage + 1 == R::D ? 0 : stage + 1;
-    const float rs = centre<T, TPR>(x, lane, a.d, a.eps, inv_d, part);
-    float s[2] = {0.f, 0.f};
+    const float2 rs = both(centre<T, TPR>(x, lane, a.d, a.eps, inv_d, part));
+    float2 s0 = both(0.f), s1 = both(0.f);
 #pragma unroll
-    for (int e = 0; e < kEpt; ++e) {
-      x[e] *= rs;
-      db[e] += dy[e];
-      dw[e] = fmaf(dy[e], x[e], dw[e]);
-      dy[e] *= w[e];
-      s[0] += dy[e];
-      s[1] = fmaf(dy[e], x[e], s[1]);
+    for (int e = 0; e < kP; ++e) {
+      x[e] = f2_mul(x[e], rs);
+      db[e] = f2_add(db[e], dy[e]);
+      dw[e] = f2_fma(dy[e], x[e], dw[e]);
+      dy[e] = f2_mul(dy[e], w[e]);
+      s0 = f2_add(s0, dy[e]);
+      s1 = f2_fma(dy[e], x[e], s1);
     }
+    float s[2] = {s0.x + s0.y, s1.x + s1.y};
     row_sum<TPR>(s, part2, 0);
-    const float m0 = s[0] * inv_d, m1 = s[1] * inv_d;
+    const float2 m0 = both(-s[0] * inv_d), m1 = both(-s[1] * inv_d);
 #pragma unroll
-    for (int e = 0; e < kEpt; ++e) x[e] = rs * (dy[e] - m0 - x[e] * m1);
+    for (int e = 0; e < kP; ++e) x[e] = f2_mul(rs, f2_fma(x[e], m1, f2_add(dy[e], m0)));
     Frag<T> o;
     pack(x, o);
-    if (live && a.y) store<T, TPR>(static_cast<T*>(a.y) + offset(a.sy, at(r)), lane, a.d, o);
+    if (live && a.y) store<T, TPR>(static_cast<T*>(a.y) + offset(a.sy, at(here)), lane, a.d, o);
+    here.advance(by, n_in, n_mid);
   }
   if (!a.part) return;
   float* sums = reinterpret_cast<float*>(ring + R::kBytes / 16);
@@ -286,17 +307,20 @@ __global__ void __launch_bounds__(TPR > kBlock ? TPR : kBlock) norm_bwd_kernel(N
 #pragma unroll
   for (int o = TPR; o < 32; o <<= 1)
 #pragma unroll
-    for (int e = 0; e < kEpt; ++e) {
-      dw[e] += __shfl_xor_sync(0xffffffffu, dw[e], o);
-      db[e] += __shfl_xor_sync(0xffffffffu, db[e], o);
+    for (int e = 0; e < kP; ++e) {
+      dw[e].x += __shfl_xor_sync(0xffffffffu, dw[e].x, o), dw[e].y += __shfl_xor_sync(0xffffffffu, dw[e].y, o);
+      db[e].x += __shfl_xor_sync(0xffffffffu, db[e].x, o), db[e].y += __shfl_xor_sync(0xffffffffu, db[e].y, o);
     }
   float* mine = PARTS == 1 ? a.part + ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 2 * a.d
                            : sums + (TPR < 32 ? threadIdx.x / 32 : threadIdx.x / TPR) * 2 * a.d;
   if (TPR >= 32 || threadIdx.x % 32 < TPR) {
 #pragma unroll
-    for (int e = 0; e < kEpt; ++e) {
-      const int c = (lane + TPR * (e / Frag<T>::V)) * Frag<T>::V + e % Frag<T>::V;
-      if (inside<T, TPR>(lane, a.d, e)) mine[c] = dw[e], mine[a.d + c] = db[e];
+    for (int e = 0; e < kP; ++e) {
+      const int c = (lane + TPR * (2 * e / Frag<T>::V)) * Frag<T>::V + 2 * e % Frag<T>::V;
+      if (inside<T, TPR>(lane, a.d, 2 * e)) {
+        *reinterpret_cast<float2*>(mine + c) = dw[e];
+        *reinterpret_cast<float2*>(mine + a.d + c) = db[e];
+      }
     }
   }
   if (PARTS == 1) return;
