@@ -51,7 +51,7 @@ struct BwdScratch {
   size_t dots, parts, d_h0, segs, sums, bytes;  // offsets, then the size
 };
 size_t seg_bytes(const lizard_decay_dims& d, int da, int dc) {
-  const size_t n = lz::decay_simt_workspace(d.B, d.H, d.L, da, dc);
+  const size_t n = lz::decay_f32_workspace(d.B, d.H, d.L, da, dc);
   return lz::align_up(d.dtype == LIZARD_BF16 ? std::max(n, lz::decay_tc_workspace(d.B, d.H, d.L, da, dc)) : n, 256);
 }
 // Planes of [B,H,L] sums for d log_decay: within chunks, and with the states (the tensor-core pass
@@ -141,7 +141,7 @@ lizard_status lizard_decay_attn_fwd(const lizard_decay_dims* dims, const void* q
   const Tensor in[] = {tq, tk, tv};
   float* segs = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + lz::kWsHeader);
   const cudaError_t e = tc_rows(d, in, 3) ? lz::launch_decay_tc(a, false, segs, s, &launches)
-                                          : lz::launch_decay_simt(a, d.dtype, segs, s, &launches);
+                                          : lz::launch_decay_f32(a, d.dtype, segs, s, &launches);
   return finish(e, launches);
 }
 
@@ -215,7 +215,7 @@ lizard_status lizard_decay_attn_bwd(const lizard_decay_dims* dims, const void* q
   // the gradient of log_decay takes the products with the states as results: from exact states
   auto pass = [&](const lz::DecayPass& p) {
     return tc ? lz::launch_decay_tc(p, p.x != nullptr, segs, s, &launches)
-              : lz::launch_decay_simt(p, d.dtype, segs, s, &launches);
+              : lz::launch_decay_f32(p, d.dtype, segs, s, &launches);
   };
   lz::DecayPass a{};
   a.B = d.B, a.H = d.H, a.L = d.L, a.lg = log_decay, a.sg = rg.s, a.count = count;

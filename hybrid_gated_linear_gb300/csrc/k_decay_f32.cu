@@ -1,12 +1,16 @@
-// k_decay_simt.cu -- one pass of the linear attention with a decay per head on CUDA cores, for fp32
-// (and for what the tensor-core pass does not take), the sum over the heads of a group, and the
+// k_decay_f32.cu -- one pass of the linear attention with a decay per head in fp32 (and for the bf16 rows that
+// the tensor-memory pass does not take), the join of segments, the sum over the heads of a group, and the
 // gradient of log_decay from the passes' sums.
 //   out_o = sum_s D(o, s) (a_o . b_s) c_s + (decay from the chunk's edge) a_o^T H,
-// chunk after chunk of 64 tokens in the pass's direction, H the state that enters the chunk.  A CTA
-// takes 64 of c's channels of one head; H, the chunk's rows and its scores stay in shared memory,
-// every product is fp32 with 4 x 4 (or 8 x 4) results a thread.
+// chunk after chunk of 64 tokens in the pass's direction, H the state that enters the chunk.  A CTA takes
+// 64 of c's channels of one head; the chunk's rows, its scores and H lie in shared memory in fp32.
+// Every product is made of three tf32 products of the warp-level tensor instructions, x = hi + lo with hi the
+// upper 11 bits: hi hi + hi lo + lo hi, which leaves 2^-22 of a product (8 more bits in each operand than
+// tcgen05's bf16 parts, whose three tiles an operand would not fit beside each other).  Against 4 x 4 results a
+// thread by fp32 multiply-adds: 5 sequences of 1999 tokens, 12 heads of 64 x 128, 248 -> 101 us.
 #include "lizard_dev.cuh"
 #include "lizard_internal.h"
+#include "tc_sm100.cuh"
 
 namespace lz {
 namespace {
@@ -14,29 +18,43 @@ namespace {
 constexpr int kC = kDecayChunk;  // tokens of a chunk
 constexpr int kDc = kDecaySlice;  // channels of c of a CTA
 constexpr int kThreads = 256;
-constexpr int kSp = kC + 4;  // pitch of the scores
+// Pitches: 4 more than a multiple of 32 words where a fragment's eight rows lie along the pitch, 8 more where
+// its four do.
+constexpr int kSp = kC + 4, kCp = kDc + 8;
 
 template <int DA>
 struct Smem {
   static constexpr int P = DA + 4;
-  float a[kC][P], b[kC][P], c[kC][kDc], s[kC][kSp], h[DA][kDc];
-  float hi[kC], lo[kC];    // the sum of log_decay up to each token (its finite part) in two floats
+  float a[kC][P], b[kC][P], c[kC][kCp], s[kC][kSp], h[DA][kCp];
+  float hi[kC], lo[kC];    // log2 of the decays up to each token (their finite part) in two floats
   int doc[kC];             // documents begun up to each token
   float in[kC], out[kC];   // decays from before the chunk to each token, from each token to the end
-  float diag[kC];
+  float diag[kC];          // the scores of the tokens themselves
+  float dots[2][2][kC];    // of a row: [within the chunk, with the state][half of the channels]
   float all;               // decay of the whole chunk
 };
 
-// Rows t0 .. t0 + 63 of d channels (the pitch of dst is its own) as fp32; zeros from `end` on.
+// Rows t0 .. t0 + 63 of d channels (the pitch of dst is its own) as fp32; zeros from `end` on.  fp32 rows by
+// asynchronous copies, all of a chunk's on their way together (rows_wait).
 template <typename T, int P>
 __device__ __forceinline__ void load_rows(float (*dst)[P], const T* src, int64_t st, int t0, int end, int d) {
   const int quads = d / 4;
+#pragma unroll 4
   for (int i = threadIdx.x; i < kC * quads; i += kThreads) {
     const int r = i / quads, q = i - r * quads;
+    if (sizeof(T) == 4) {
+      const bool there = t0 + r < end;
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(tc::smem_u32(&dst[r][4 * q])),
+                   "l"(src + (there ? (int64_t)(t0 + r) * st + 4 * q : 0)), "r"(there ? 16 : 0)
+                   : "memory");
+      continue;
+    }
     const float4 v = t0 + r < end ? ld4(src + (int64_t)(t0 + r) * st + 4 * q) : make_float4(0.f, 0.f, 0.f, 0.f);
     *reinterpret_cast<float4*>(&dst[r][4 * q]) = v;
   }
 }
+
+__device__ __forceinline__ void rows_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // The chunk's decays, by one warp: two tokens a lane, sums in 64 bits so that differences of far
 // sums keep their digits.
@@ -50,7 +68,7 @@ __device__ __forceinline__ void decays(Smem<DA>& m, const float* lg, int64_t st,
     const int t = t0 + 2 * lane + k;
     const float g = t < end ? lg[t * st] : 0.f;
     n[k] = g < kDecayNone;
-    x[k] = n[k] ? 0.0 : (double)g;
+    x[k] = n[k] ? 0.0 : (double)g * 1.4426950408889634;
   }
   double sum = x[0] + x[1];
   int docs = n[0] + n[1];
@@ -70,18 +88,63 @@ __device__ __forceinline__ void decays(Smem<DA>& m, const float* lg, int64_t st,
     m.hi[i] = (float)b[k];
     m.lo[i] = (float)(b[k] - (double)m.hi[i]);
     m.doc[i] = dc[k];
-    m.in[i] = dc[k] ? 0.f : expf((float)b[k]);
-    m.out[i] = dc[k] != last ? 0.f : expf((float)(total - b[k]));
+    m.in[i] = dc[k] ? 0.f : exp2f((float)b[k]);
+    m.out[i] = dc[k] != last ? 0.f : exp2f((float)(total - b[k]));
   }
-  if (lane == 0) m.all = last ? 0.f : expf((float)total);
+  if (lane == 0) m.all = last ? 0.f : exp2f((float)total);
 }
 
+// A word as two tf32 operands, both rounded to nearest: 11 bits, and 11 of what is left.  (The instruction
+// does not read a word's lower 13 bits; cut off instead of rounded, results were 1.4e-6 off, this way 3e-7.)
+struct Two {
+  uint32_t hi, lo;
+};
+__device__ __forceinline__ Two two(float x) {
+  const uint32_t hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
+  return {hi, __float_as_uint(x - __uint_as_float(hi)) + 0x1000u};
+}
+// d (16 x 8) += a (16 x 8) b (8 x 8)
+__device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// One k-step of 8 of a warp's 16 x (8 NT) results: a(row, k) and b(col, k, k / 4) give the operands' elements
+// at the lane's places.  The instruction cuts its sums off at 24 bits: the small products have sums of their
+// own, so that the large ones are cut once a step and not three times.
+template <int NT, typename A, typename B>
+__device__ __forceinline__ void step8(float (&d)[NT][4], float (&small)[NT][4], A a, B b) {
+  const int g = (threadIdx.x & 31) >> 2, c = threadIdx.x & 3;
+  uint32_t ah[4], al[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const Two t = two(a(g + 8 * (e & 1), c + 4 * (e >> 1)));
+    ah[e] = t.hi, al[e] = t.lo;
+  }
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const Two b0 = two(b(8 * n + g, c, 0)), b1 = two(b(8 * n + g, c + 4, 1));
+    mma_tf32(small[n], al, b0.hi, b1.hi);
+    mma_tf32(small[n], ah, b0.lo, b1.lo);
+    mma_tf32(d[n], ah, b0.hi, b1.hi);
+  }
+}
+template <int NT>
+__device__ __forceinline__ void join_small(float (&d)[NT][4], float (&small)[NT][4]) {
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) d[n][e] += small[n][e], small[n][e] = 0.f;
+}
+
+// Warp w of eight: rows 16 (w mod 4) .. of the chunk's 64, columns 32 (w / 4) .. of 64; of the state the rows
+// DA / 4 (w mod 4) ...  A lane's results of tile n: rows g, g + 8, columns 8 n + 2 c, + 1.
 template <typename T, int DA>
-__global__ void __launch_bounds__(kThreads) decay_simt_kernel(DecayPass a, DecaySegs g) {
+__global__ void __launch_bounds__(kThreads) decay_f32_kernel(DecayPass a, DecaySegs g) {
   extern __shared__ __align__(16) unsigned char raw[];
   Smem<DA>& m = *reinterpret_cast<Smem<DA>*>(raw);
   pdl_wait();
-  const int tid = threadIdx.x, tc = tid % 16, ti = tid / 16;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int slices = a.dc / kDc, units = a.B * a.H;
   const int slice = blockIdx.x % slices, unit = blockIdx.x / slices % units, seg = blockIdx.x / slices / units;
   const int n = unit / a.H, h = unit - n * a.H, c0 = slice * kDc;
@@ -117,11 +180,10 @@ __global__ void __launch_bounds__(kThreads) decay_simt_kernel(DecayPass a, Decay
     else
       m.h[i][j] = a.init ? a.init[state(i, j)] : 0.f;
   }
-  float* dots[2] = {nullptr, nullptr};
-  if (px) {
-    const int64_t o = ((int64_t)slice * a.B * a.H + unit) * a.L;
-    dots[0] = a.dot_in + o, dots[1] = a.dot_out + o;
-  }
+  const int64_t dot0 = ((int64_t)slice * units + unit) * a.L;
+  const int r0 = 16 * (warp & 3), n0 = 32 * (warp >> 2), gr = lane >> 2, cq = 2 * (lane & 3);
+  constexpr int MT = DA / 64;  // 16-row tiles of the state of a warp
+  const int h0 = 16 * MT * (warp & 3);
   // this segment's chunks, in the pass's order
   const int chunks = (count + kC - 1) / kC, done = min(seg * g.cps, chunks), num = min(g.cps, chunks - done);
   float product = 1.f;
@@ -131,145 +193,128 @@ __global__ void __launch_bounds__(kThreads) decay_simt_kernel(DecayPass a, Decay
     load_rows<T>(m.b, pb, a.sb.t, t0, count, DA);
     load_rows<T>(m.c, pc, a.sc.t, t0, count, kDc);
     if (tid < 32) decays(m, lg, a.sg.t, t0, count);
+    rows_wait();
     __syncthreads();
     const float* from_state = a.rev ? m.out : m.in;  // from the state that enters to each token
     const float* to_state = a.rev ? m.in : m.out;    // from each token to the state that leaves
     product *= m.all;
     if (!g.states_only) {
-    // scores with their decays; the diagonal apart
-    float acc[4][4] = {};
-#pragma unroll 4
-    for (int k = 0; k < DA; k += 4) {
-      float4 x[4], y[4];
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        x[r] = *reinterpret_cast<const float4*>(&m.a[ti + 16 * r][k]);
-        y[r] = *reinterpret_cast<const float4*>(&m.b[tc + 16 * r][k]);
-      }
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          acc[r][c] = fmaf(x[r].x, y[c].x, acc[r][c]);
-          acc[r][c] = fmaf(x[r].y, y[c].y, acc[r][c]);
-          acc[r][c] = fmaf(x[r].z, y[c].z, acc[r][c]);
-          acc[r][c] = fmaf(x[r].w, y[c].w, acc[r][c]);
-        }
-    }
-#pragma unroll
-    for (int r = 0; r < 4; ++r)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int o = ti + 16 * r, s = tc + 16 * c;
-        const int late = a.rev ? s : o, early = a.rev ? o : s;
-        float d = 0.f;
-        if (late > early && m.doc[late] == m.doc[early])
-          d = expf((m.hi[late] - m.hi[early]) + (m.lo[late] - m.lo[early]));
-        m.s[o][s] = d > 0.f ? acc[r][c] * a.scale_in * d : 0.f;
-        if (o == s) m.diag[o] = acc[r][c] * a.scale_in;
-      }
-    __syncthreads();
-    // out = scores c + decay a^T H
-    float in[4][4] = {}, st[4][4] = {};
-#pragma unroll 4
-    for (int j = 0; j < kC; j += 4) {
-      float4 x[4], y[4];
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        x[r] = *reinterpret_cast<const float4*>(&m.s[ti + 16 * r][j]);
-        y[r] = *reinterpret_cast<const float4*>(&m.c[j + r][4 * tc]);
-      }
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const float w[4] = {x[r].x, x[r].y, x[r].z, x[r].w};
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          in[r][0] = fmaf(w[q], y[q].x, in[r][0]);
-          in[r][1] = fmaf(w[q], y[q].y, in[r][1]);
-          in[r][2] = fmaf(w[q], y[q].z, in[r][2]);
-          in[r][3] = fmaf(w[q], y[q].w, in[r][3]);
-        }
-      }
-    }
-#pragma unroll 4
-    for (int j = 0; j < DA; j += 4) {
-      float4 x[4], y[4];
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        x[r] = *reinterpret_cast<const float4*>(&m.a[ti + 16 * r][j]);
-        y[r] = *reinterpret_cast<const float4*>(&m.h[j + r][4 * tc]);
-      }
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const float w[4] = {x[r].x, x[r].y, x[r].z, x[r].w};
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          st[r][0] = fmaf(w[q], y[q].x, st[r][0]);
-          st[r][1] = fmaf(w[q], y[q].y, st[r][1]);
-          st[r][2] = fmaf(w[q], y[q].z, st[r][2]);
-          st[r][3] = fmaf(w[q], y[q].w, st[r][3]);
-        }
-      }
-    }
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const int o = ti + 16 * r, t = t0 + o;
-      const float e = from_state[o];
-#pragma unroll
-      for (int q = 0; q < 4; ++q) st[r][q] = e > 0.f ? e * st[r][q] : 0.f;
-      if (px) {
-        const float4 x = t < count ? ld4(px + t * a.sx.t + 4 * tc) : make_float4(0.f, 0.f, 0.f, 0.f);
-        float d0 = x.x * in[r][0] + x.y * in[r][1] + x.z * in[r][2] + x.w * in[r][3];
-        float d1 = x.x * st[r][0] + x.y * st[r][1] + x.z * st[r][2] + x.w * st[r][3];
-#pragma unroll
-        for (int x16 = 8; x16 > 0; x16 >>= 1) {
-          d0 += __shfl_xor_sync(0xffffffffu, d0, x16);
-          d1 += __shfl_xor_sync(0xffffffffu, d1, x16);
-        }
-        if (tc == 0 && t < count) dots[0][t] = a.scale_out * d0, dots[1][t] = a.scale_out * d1;
-      }
-      const float4 cd = *reinterpret_cast<const float4*>(&m.c[o][4 * tc]);
-      const float dg = m.diag[o];
-      if (t < count)
-        put(t, 4 * tc, make_float4(a.scale_out * (fmaf(dg, cd.x, in[r][0]) + st[r][0]),
-                                   a.scale_out * (fmaf(dg, cd.y, in[r][1]) + st[r][1]),
-                                   a.scale_out * (fmaf(dg, cd.z, in[r][2]) + st[r][2]),
-                                   a.scale_out * (fmaf(dg, cd.w, in[r][3]) + st[r][3])));
-    }
-    __syncthreads();
-    }
-    // H <- decay H + sum_s decay_s b_s c_s^T: rows ti * NR + r, columns 4 tc ..
-    constexpr int NR = DA / 16;
-    float u[NR][4];
-    const float all = m.all;
-#pragma unroll
-    for (int r = 0; r < NR; ++r) {
-      const float4 x = *reinterpret_cast<const float4*>(&m.h[ti * NR + r][4 * tc]);
-      u[r][0] = all > 0.f ? all * x.x : 0.f, u[r][1] = all > 0.f ? all * x.y : 0.f;
-      u[r][2] = all > 0.f ? all * x.z : 0.f, u[r][3] = all > 0.f ? all * x.w : 0.f;
-    }
+      // scores with their decays: the chunk's half on the pass's side of the diagonal, and that apart (the
+      // token's own pair passes over no decay)
+      if (a.rev ? n0 + 31 >= r0 : n0 <= r0 + 15) {
+        float acc[4][4] = {}, small[4][4] = {};
 #pragma unroll 2
-    for (int s = 0; s < kC; ++s) {
-      const float e = to_state[s] * a.scale_in;
-      float4 y = *reinterpret_cast<const float4*>(&m.c[s][4 * tc]);
-      y = e != 0.f ? make_float4(y.x * e, y.y * e, y.z * e, y.w * e) : make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int k = 0; k < DA; k += 8)
+          step8(acc, small, [&](int r, int c) { return m.a[r0 + r][k + c]; }, [&](int r, int c, int) { return m.b[n0 + r][k + c]; });
+        join_small(acc, small);
 #pragma unroll
-      for (int r = 0; r < NR; r += 4) {
-        const float4 x = *reinterpret_cast<const float4*>(&m.b[s][ti * NR + r]);
-        const float w[4] = {x.x, x.y, x.z, x.w};
+        for (int e = 0; e < 4; ++e)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          u[r + q][0] = fmaf(w[q], y.x, u[r + q][0]);
-          u[r + q][1] = fmaf(w[q], y.y, u[r + q][1]);
-          u[r + q][2] = fmaf(w[q], y.z, u[r + q][2]);
-          u[r + q][3] = fmaf(w[q], y.w, u[r + q][3]);
+          for (int q = 0; q < 4; ++q) {
+            const int o = r0 + gr + 8 * (q >> 1), s = n0 + 8 * e + cq + (q & 1);
+            const int late = a.rev ? s : o, early = a.rev ? o : s;
+            float d = 0.f;
+            if (late > early && m.doc[late] == m.doc[early])
+              d = tc::ex2_approx((m.hi[late] - m.hi[early]) + (m.lo[late] - m.lo[early]));
+            m.s[o][s] = d > 0.f ? acc[e][q] * a.scale_in * d : 0.f;
+            if (o == s) m.diag[o] = acc[e][q] * a.scale_in;
+          }
+      }
+      __syncthreads();
+      // out = scores c + decay a^T H
+      float in[4][4] = {}, st[4][4] = {};
+      {
+        float small[4][4] = {};
+        const int ka = a.rev ? r0 : 0, kb = a.rev ? kC : r0 + 16;  // the other scores of these rows are 0
+#pragma unroll 2
+        for (int k = ka; k < kb; k += 8)
+          step8(in, small, [&](int r, int c) { return m.s[r0 + r][k + c]; }, [&](int r, int c, int) { return m.c[k + c][n0 + r]; });
+        join_small(in, small);
+#pragma unroll 2
+        for (int k = 0; k < DA; k += 8)
+          step8(st, small, [&](int r, int c) { return m.a[r0 + r][k + c]; }, [&](int r, int c, int) { return m.h[k + c][n0 + r]; });
+        join_small(st, small);
+      }
+      float dot[2][2] = {};  // [row][within, with the state]
+      float2 y[4][2];
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int o = r0 + gr + 8 * q, t = t0 + o;
+        const float e = from_state[o], dg = m.diag[o];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 u = make_float2(in[k][2 * q], in[k][2 * q + 1]);
+          float2 w = make_float2(e * st[k][2 * q], e * st[k][2 * q + 1]);
+          if (!(e > 0.f)) w = make_float2(0.f, 0.f);
+          const int col = n0 + 8 * k + cq;
+          const float2 cd = *reinterpret_cast<const float2*>(&m.c[o][col]);
+          y[k][q] = make_float2(a.scale_out * (fmaf(dg, cd.x, u.x) + w.x), a.scale_out * (fmaf(dg, cd.y, u.y) + w.y));
+          if (px && t < count) {
+            float x0, x1;
+            if (sizeof(T) == 4) {
+              const float2 v = *reinterpret_cast<const float2*>(px + t * a.sx.t + col);
+              x0 = v.x, x1 = v.y;
+            } else {
+              const uint32_t v = *reinterpret_cast<const uint32_t*>(px + t * a.sx.t + col);
+              x0 = __uint_as_float(v << 16), x1 = __uint_as_float(v & 0xffff0000u);
+            }
+            dot[q][0] += x0 * u.x + x1 * u.y;
+            dot[q][1] += x0 * w.x + x1 * w.y;
+          }
         }
       }
-    }
+      if (px) {
 #pragma unroll
-    for (int r = 0; r < NR; ++r)
-      *reinterpret_cast<float4*>(&m.h[ti * NR + r][4 * tc]) = make_float4(u[r][0], u[r][1], u[r][2], u[r][3]);
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            dot[q][k] += __shfl_xor_sync(0xffffffffu, dot[q][k], 1);
+            dot[q][k] += __shfl_xor_sync(0xffffffffu, dot[q][k], 2);
+            if ((lane & 3) == 0) m.dots[k][warp >> 2][r0 + gr + 8 * q] = dot[q][k];
+          }
+      }
+      __syncthreads();  // the scores and H have been read
+      if (px && tid < 2 * kC) {
+        const int k = tid / kC, o = tid - k * kC;
+        if (t0 + o < count) (k ? a.dot_out : a.dot_in)[dot0 + t0 + o] = a.scale_out * (m.dots[k][0][o] + m.dots[k][1][o]);
+      }
+      // the rows of out through the scores' place
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) *reinterpret_cast<float2*>(&m.s[r0 + gr + 8 * q][n0 + 8 * k + cq]) = y[k][q];
+    }
+    // H <- decay H + sum_s decay_s b_s c_s^T
+    const float all = m.all;
+#pragma unroll 1
+    for (int r = 0; r < MT; ++r) {
+      float u[4][4] = {}, small[4][4] = {};
+#pragma unroll 2
+      for (int k = 0; k < kC; k += 8) {
+        float w[2];  // of the lane's two tokens
+#pragma unroll
+        for (int e = 0; e < 2; ++e) w[e] = to_state[k + (lane & 3) + 4 * e] * a.scale_in;
+        step8(u, small, [&](int i, int c) { return m.b[k + c][h0 + 16 * r + i]; },
+              [&](int j, int c, int e) { return w[e] * m.c[k + c][n0 + j]; });
+      }
+      join_small(u, small);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          float2* at = reinterpret_cast<float2*>(&m.h[h0 + 16 * r + gr + 8 * q][n0 + 8 * k + cq]);
+          const float2 x = all > 0.f ? *at : make_float2(0.f, 0.f);
+          *at = make_float2(fmaf(all, x.x, u[k][2 * q]), fmaf(all, x.y, u[k][2 * q + 1]));
+        }
+    }
     __syncthreads();
+    if (!g.states_only) {
+      for (int i = tid; i < kC * (kDc / 4); i += kThreads) {
+        const int o = i / (kDc / 4), c = 4 * (i % (kDc / 4));
+        if (t0 + o < count) put(t0 + o, c, *reinterpret_cast<const float4*>(&m.s[o][c]));
+      }
+      // (the next chunk's scores are written behind its first barrier)
+    }
   }
   if (g.states_only) {
     __syncthreads();  // without a chunk, zeros
@@ -467,10 +512,10 @@ __global__ void __launch_bounds__(32 * kGateWarps) decay_gate_kernel(DecayGate a
 template <typename T, int DA>
 cudaError_t launch(const DecayPass& a, const DecaySegs& g, int64_t blocks, cudaStream_t s) {
   static std::atomic<uint64_t> done{0};
-  const cudaError_t e = allow_smem(decay_simt_kernel<T, DA>, sizeof(Smem<DA>), done);
+  const cudaError_t e = allow_smem(decay_f32_kernel<T, DA>, sizeof(Smem<DA>), done);
   if (e != cudaSuccess) return e;
   if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
-  return launch_pdl(decay_simt_kernel<T, DA>, dim3((unsigned)blocks), dim3(kThreads), sizeof(Smem<DA>), s, a, g);
+  return launch_pdl(decay_f32_kernel<T, DA>, dim3((unsigned)blocks), dim3(kThreads), sizeof(Smem<DA>), s, a, g);
 }
 
 cudaError_t dispatch(const DecayPass& a, lizard_dtype dt, const DecaySegs& g, int64_t blocks, cudaStream_t s) {
@@ -479,22 +524,23 @@ cudaError_t dispatch(const DecayPass& a, lizard_dtype dt, const DecaySegs& g, in
   return a.da == 64 ? launch<bf16, 64>(a, g, blocks, s) : launch<bf16, 128>(a, g, blocks, s);
 }
 
-// One CTA an SM at da = 128, two at 64, by their shared memory; a state pass is a third of the work.
-int simt_segments(int64_t ctas, int L, int da) {
-  return decay_segments(ctas, da == 64 ? 304 : 152, (L + kC - 1) / kC, 0.35, 0.4);
+// One CTA an SM at da = 128, two at 64, by their shared memory; a state pass is a third of the work, a CTA's
+// start and its state's way in and out two thirds of a chunk.
+int f32_segments(int64_t ctas, int L, int da) {
+  return decay_segments(ctas, da == 64 ? 304 : 152, (L + kC - 1) / kC, 0.35, 0.7, 0.4);
 }
 
 }  // namespace
 
-int decay_segments(int64_t ctas, int per_wave, int chunks, double part, double extra) {
+int decay_segments(int64_t ctas, int per_wave, int chunks, double part, double start, double extra) {
   if (ctas >= 8 * per_wave) return 1;
   int best = 1;
   double least = 1e30;
   for (int s = 1; s <= 64 && s <= chunks; ++s) {
     const int cps = (chunks + s - 1) / s;
     if (s > 1 && (chunks + cps - 1) / cps < s) continue;  // some would be empty
-    double t = (double)((ctas * s + per_wave - 1) / per_wave) * cps;
-    if (s > 1) t += part * (double)((ctas * (s - 1) + per_wave - 1) / per_wave) * cps + extra;
+    double t = (double)((ctas * s + per_wave - 1) / per_wave) * (cps + start);
+    if (s > 1) t += part * (double)((ctas * (s - 1) + per_wave - 1) / per_wave) * (cps + start) + extra;
     if (t < least) least = t, best = s;
   }
   return best;
@@ -514,16 +560,16 @@ cudaError_t launch_decay_join(const DecayPass& a, const DecaySegs& g, cudaStream
   return e;
 }
 
-size_t decay_simt_workspace(int B, int H, int L, int da, int dc) {
+size_t decay_f32_workspace(int B, int H, int L, int da, int dc) {
   const int64_t ctas = (int64_t)B * H * (dc / kDc);
-  return decay_seg_bytes(simt_segments(ctas, L, da), ctas, da);
+  return decay_seg_bytes(f32_segments(ctas, L, da), ctas, da);
 }
 
-cudaError_t launch_decay_simt(const DecayPass& a, lizard_dtype dt, float* ws, cudaStream_t s, int* launches) {
+cudaError_t launch_decay_f32(const DecayPass& a, lizard_dtype dt, float* ws, cudaStream_t s, int* launches) {
   const int64_t ctas = (int64_t)a.B * a.H * (a.dc / kDc);
   const int chunks = (a.L + kC - 1) / kC;
   DecaySegs g{};
-  g.segs = simt_segments(ctas, a.L, a.da);
+  g.segs = f32_segments(ctas, a.L, a.da);
   g.cps = chunks ? (chunks + g.segs - 1) / g.segs : 1;
   if (g.segs > 1) {
     g.seg_h = ws, g.seg_d = ws + (size_t)g.segs * ctas * a.da * kDc;
@@ -536,7 +582,7 @@ cudaError_t launch_decay_simt(const DecayPass& a, lizard_dtype dt, float* ws, cu
     if (e == cudaSuccess) e = launch_decay_join(a, g, s, launches);
     if (e != cudaSuccess) return e;
   }
-  trace_begin("decay_simt", s);
+  trace_begin("decay_f32", s);
   const cudaError_t e = dispatch(a, dt, g, ctas * g.segs, s);
   trace_end(s);
   ++*launches;

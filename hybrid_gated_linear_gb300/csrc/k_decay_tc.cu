@@ -1028,7 +1028,7 @@ cudaError_t launch_pairs(const PairMaps& m, const PairParams& p, cudaStream_t s)
 bool decay_tc_rows_ok(int B, int H, int L, int d, const Strides& s) { return strides_ok(B, H, L, d, s); }
 
 // One CTA an SM (152); a state pass takes about 0.6 of the pass's time a chunk.
-static int tc_segments(int64_t ctas, int L) { return decay_segments(ctas, 152, (L + kC - 1) / kC, 0.6, 5.0); }
+static int tc_segments(int64_t ctas, int L) { return decay_segments(ctas, 152, (L + kC - 1) / kC, 0.6, 2.0, 4.0); }
 
 size_t decay_tc_workspace(int B, int H, int L, int da, int dc) {
   const int64_t ctas = (int64_t)B * H * (dc / kN);

@@ -424,13 +424,14 @@ struct DecaySegs {
   bool states_only;
   float *seg_h, *seg_d;
 };
-// The segments for `ctas` CTAs of which `per_wave` run at a time, a state pass costing `part` of the pass
-// a chunk and `extra` chunks for its start and the join; and the bytes of seg_h and seg_d.
-int decay_segments(int64_t ctas, int per_wave, int chunks, double part, double extra);
+// The segments for `ctas` CTAs of which `per_wave` run at a time, in units of a chunk's time: a CTA costs
+// `start` more than its chunks, the state pass `part` of the pass, the join `extra`; and the bytes of seg_h
+// and seg_d.
+int decay_segments(int64_t ctas, int per_wave, int chunks, double part, double start, double extra);
 size_t decay_seg_bytes(int segs, int64_t ctas, int da);
 cudaError_t launch_decay_join(const DecayPass& a, const DecaySegs& g, cudaStream_t s, int* launches);
-size_t decay_simt_workspace(int B, int H, int L, int da, int dc);
-cudaError_t launch_decay_simt(const DecayPass& a, lizard_dtype dt, float* ws, cudaStream_t s, int* launches);
+size_t decay_f32_workspace(int B, int H, int L, int da, int dc);
+cudaError_t launch_decay_f32(const DecayPass& a, lizard_dtype dt, float* ws, cudaStream_t s, int* launches);
 // The same on the tensor cores: bf16, L > 0, tensors that decay_tc_rows_ok accepts; exact_state: A H from
 // three bf16 parts of the state (dot_out [2 dc / 64][B,H,L]; dot_in is not written).  `ws` of
 // decay_tc_workspace bytes.
