@@ -12,10 +12,11 @@
 // product: no sum is infinite.
 //
 // A CTA takes 64 of C's channels of one head over the chunks of one segment; H stays in registers in
-// fp32.  Twenty warps:
+// fp32.  Twenty warps (five on each quarter of the SM, at 96 registers):
 //   0      copies the tiles of A, B [128][da] and C [128][64] in by TMA, two stages ahead
-//   1      issues the MMAs: S, B^T C~, A H, P C
-//   2-3    the decays, one warp those of the even chunks, one of the odd
+//   1, 3   issue the MMAs: S and P C, and B^T C~ and A H (one warp for all spent a third of its time waiting
+//          in turn for what the two sides make: 4430 against 3700 cycles a chunk)
+//   2      the decays of the next chunks
 //   4-11   C~ = to o C in two or three bf16 parts (16 or 24 bits: the state is a sum over the whole
 //          sequence, so its operands are not rounded), then P, rounded once to bf16, into TMEM
 //   12-19  the state: H = all H + (B^T C~); its bf16 parts for the next chunk's A H (one part, as P is
@@ -23,6 +24,8 @@
 // TMEM: S 128 columns, P 64, B^T C~ 3 x 64 (its parts side by side: one reading of B for all of them),
 // P C 64, A H 64.
 // The shared memory's bandwidth bounds it: the MMAs read their operands there.
+#include <math.h>
+
 #include "lizard_dev.cuh"
 #include "lizard_internal.h"
 #include "tc_pipe.cuh"
@@ -43,7 +46,7 @@ enum {
   FA = 0, FB = 2, FC = 4, EA = 6, EB = 8, EC = 10,  // tiles full and empty, by stage
   FACF = 12, FACE = 14,                             // factors full and empty, by buffer
   CT = 16, KVR = 18, KVF = 20,                      // C~ ready, B^T C~ ready, read; by parity
-  SR = 22, HR, HF, PR, YR, YF, FIX, DONE, NB
+  SR = 22, HR, HF, PR, YR, YF, FIX, DONE, DONE2, NB
 };
 
 // Of a chunk: row, log2 of the decay from the edge of a token's 16-token block to the token (from the
@@ -87,6 +90,7 @@ struct TcParams {
   DecayPass p;
   int an, ah, bn, bh, cn, ch;  // 0 where a tensor repeats over sequences or heads, else 1
   int parts;                   // bf16 parts of C~
+  float log_scale;             // log2 of what P is scaled by
   DecaySegs g;
 };
 
@@ -344,7 +348,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < NB; ++i) {
       const bool both = i == FACE || i == FACE + 1, score = i == CT || i == CT + 1 || i == PR || i == FIX,
                  state = i == KVF || i == KVF + 1 || i == HR || i == YF;
-      mbar_init(&ctl->bar[i], both ? kScoreWarps + kStateWarps : score ? kScoreWarps : state ? kStateWarps : 1);
+      // the tiles of A and B are read by both MMA warps
+      const bool shared = (i >= EA && i < EC) && !q.g.states_only;
+      mbar_init(&ctl->bar[i], both ? kScoreWarps + kStateWarps : score ? kScoreWarps : state ? kStateWarps : shared ? 2 : 1);
     }
     ctl->abort = 0;
     fence_mbar_init();
@@ -412,62 +418,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp == 1) {
-    {
+    if (!q.g.states_only) {
       const uint32_t sb = smem_u32(sm);
-      const uint32_t id_s = idesc_bf16(kC, kC, false, false), id_kv = idesc_bf16(128, q.parts * kN, true, true),
-                     id_h = idesc_bf16(kC, kN, false, true);
-      constexpr uint32_t kRow = kC * 128;  // bytes of a 64-column block of a tile
-      static_assert(kN == kDecaySlice, "segments' states are kept by slices");
-      static_assert(kRow == kTileC, "the parts of C~ are the blocks of one operand");
-      const uint32_t da = desc_lower(sb + Sm::A, 16), db = desc_lower(sb + Sm::B, 16), dbt = desc_lower(sb + Sm::B, kRow),
-                     dc = desc_lower(sb + Sm::Ct, kRow), dp = desc_lower(sb + Sm::CP, kRow),
-                     dp2 = desc_lower(sb + Sm::CP2, kRow), dh = desc_lower(sb + Sm::H, kRow);
+      const uint32_t id_s = idesc_bf16(kC, kC, false, false), id_c = idesc_bf16(kC, kN, false, true);
+      const uint32_t da = desc_lower(sb + Sm::A, 16), db = desc_lower(sb + Sm::B, 16), dc = desc_lower(sb + Sm::Ct, kC * 128);
       bool ok = true;
 #pragma unroll 1
       for (int it = 0; it < num && ok; ++it) {
-        const uint32_t a = da + it % Sm::NA * (Sm::kTile / 16), b = it % Sm::NBt * (Sm::kTile / 16);
+        // S = A B^T (the last one has been read: P C has been issued)
         if (!(ok = wait_warp(ctl, FB + it % Sm::NBt, (it / Sm::NBt) & 1))) break;
-        if (!q.g.states_only) {
-          // S = A B^T (the last one has been read: P C has been issued)
-          if (!(ok = wait_warp(ctl, FA + it % Sm::NA, (it / Sm::NA) & 1))) break;
-          if (ragged(it) && !(ok = wait_warp(ctl, FIX, 0))) break;
-          tc_fence_after();
-#pragma unroll 4
-          for (int j = 0; j < DA / 16; ++j) mma_lo(tmem + kColS, a + step_k(j), db + b + step_k(j), id_s, j > 0);
-          commit_lo(&ctl->bar[SR]);
-        }
-        // B^T C~, into alternate columns where there are no scores
-        const bool other = q.g.states_only && (it & 1);
-        if (!(ok = wait_warp(ctl, CT + (it & 1), (it >> 1) & 1))) break;
-        const int lag = q.g.states_only ? 2 : 1;
-        if (it >= lag && !(ok = wait_warp(ctl, KVF + ((it - lag) & 1), ((it - lag) >> 1) & 1))) break;
+        if (!(ok = wait_warp(ctl, FA + it % Sm::NA, (it / Sm::NA) & 1))) break;
+        if (ragged(it) && !(ok = wait_warp(ctl, FIX, 0))) break;
         tc_fence_after();
+        const uint32_t a = da + it % Sm::NA * (Sm::kTile / 16), b = db + it % Sm::NBt * (Sm::kTile / 16);
 #pragma unroll 4
-        for (int j = 0; j < kC / 16; ++j)
-          mma_lo(tmem + (other ? 0 : kColKV), dbt + b + step_mn(j), (other ? dp2 : dp) + step_mn(j), id_kv, j > 0);
-        commit_lo(&ctl->bar[KVR + (it & 1)]);
-        commit_lo(&ctl->bar[EB + it % Sm::NBt]);
-        if (q.g.states_only) {
-          commit_lo(&ctl->bar[EC + it % Sm::NCt]);
-          continue;
-        }
-        // A H, the smallest parts first, while the sum and what its additions cut off are small
-        if (!(ok = wait_warp(ctl, HR, it & 1))) break;
-        if (it > 0 && !(ok = wait_warp(ctl, YF, (it - 1) & 1))) break;
-        tc_fence_after();
-#pragma unroll 1
-        for (int k = NPH - 1; k >= 0; --k)
-#pragma unroll 4
-          for (int j = 0; j < DA / 16; ++j)
-            mma_lo(tmem + kColYs, a + step_k(j), dh + k * (Sm::kPartH / 16) + step_mn(j), id_h, k < NPH - 1 || j > 0);
-        commit_lo(&ctl->bar[HF]);
+        for (int j = 0; j < DA / 16; ++j) mma_lo(tmem + kColS, a + step_k(j), b + step_k(j), id_s, j > 0);
+        commit_lo(&ctl->bar[SR]);
         commit_lo(&ctl->bar[EA + it % Sm::NA]);
+        commit_lo(&ctl->bar[EB + it % Sm::NBt]);
         // P C
         if (!(ok = wait_warp(ctl, PR, it & 1))) break;
+        if (it > 0 && !(ok = wait_warp(ctl, YF, (it - 1) & 1))) break;
         tc_fence_after();
         const uint32_t c = dc + it % Sm::NCt * (kTileC / 16);
 #pragma unroll 4
-        for (int j = 0; j < kC / 16; ++j) mma_lo_ts(tmem + kColY, tmem + kColP + 8 * j, c + step_mn(j), id_h, j > 0);
+        for (int j = 0; j < kC / 16; ++j) mma_lo_ts(tmem + kColY, tmem + kColP + 8 * j, c + step_mn(j), id_c, j > 0);
         commit_lo(&ctl->bar[YR]);
         commit_lo(&ctl->bar[EC + it % Sm::NCt]);
       }
@@ -476,15 +451,61 @@ __global__ void __launch_bounds__(kThreads, 1)
       drain_bar(ctl, DONE, 1, globaltimer_ns());
       __syncwarp();
     }
-  } else if (warp == 2 || warp == 3) {
-    const float* lg = p.lg + n * p.sg.n + h * p.sg.h;
-    Share f;
-    if (warp - 2 < num) load_decays(lg, p.sg.t, token(warp - 2), count, f.x);
+  } else if (warp == 3) {
+    const uint32_t sb = smem_u32(sm);
+    constexpr uint32_t kRow = kC * 128;  // bytes of a 64-column block of a tile
+    static_assert(kN == kDecaySlice, "segments' states are kept by slices");
+    static_assert(kRow == kTileC, "the parts of C~ are the blocks of one operand");
+    const uint32_t id_kv = idesc_bf16(128, q.parts * kN, true, true), id_h = idesc_bf16(kC, kN, false, true);
+    const uint32_t da = desc_lower(sb + Sm::A, 16), db = desc_lower(sb + Sm::B, kRow), dp = desc_lower(sb + Sm::CP, kRow),
+                   dp2 = desc_lower(sb + Sm::CP2, kRow), dh = desc_lower(sb + Sm::H, kRow);
     bool ok = true;
 #pragma unroll 1
-    for (int it = warp - 2; it < num && ok; it += 2) {  // one warp the even chunks, one the odd
+    for (int it = 0; it < num && ok; ++it) {
+      // B^T C~, into alternate columns where there are no scores
+      const bool other = q.g.states_only && (it & 1);
+      const int lag = q.g.states_only ? 2 : 1;
+      if (!(ok = wait_warp(ctl, FB + it % Sm::NBt, (it / Sm::NBt) & 1))) break;
+      if (!(ok = wait_warp(ctl, CT + (it & 1), (it >> 1) & 1))) break;
+      if (it >= lag && !(ok = wait_warp(ctl, KVF + ((it - lag) & 1), ((it - lag) >> 1) & 1))) break;
+      tc_fence_after();
+      const uint32_t b = db + it % Sm::NBt * (Sm::kTile / 16);
+#pragma unroll 4
+      for (int j = 0; j < kC / 16; ++j)
+        mma_lo(tmem + (other ? 0 : kColKV), b + step_mn(j), (other ? dp2 : dp) + step_mn(j), id_kv, j > 0);
+      commit_lo(&ctl->bar[KVR + (it & 1)]);
+      commit_lo(&ctl->bar[EB + it % Sm::NBt]);
+      if (q.g.states_only) {
+        commit_lo(&ctl->bar[EC + it % Sm::NCt]);
+        continue;
+      }
+      // A H, the smallest parts first, while the sum and what its additions cut off are small
+      if (!(ok = wait_warp(ctl, HR, it & 1))) break;
+      if (!(ok = wait_warp(ctl, FA + it % Sm::NA, (it / Sm::NA) & 1))) break;
+      if (it > 0 && !(ok = wait_warp(ctl, YF, (it - 1) & 1))) break;
+      tc_fence_after();
+      const uint32_t a = da + it % Sm::NA * (Sm::kTile / 16);
+#pragma unroll 1
+      for (int k = NPH - 1; k >= 0; --k)
+#pragma unroll 4
+        for (int j = 0; j < DA / 16; ++j)
+          mma_lo(tmem + kColYs, a + step_k(j), dh + k * (Sm::kPartH / 16) + step_mn(j), id_h, k < NPH - 1 || j > 0);
+      commit_lo(&ctl->bar[HF]);
+      commit_lo(&ctl->bar[EA + it % Sm::NA]);
+    }
+    if (!ok) ctl->abort = 1;
+    commit_lo(&ctl->bar[DONE2]);
+    drain_bar(ctl, DONE2, 1, globaltimer_ns());
+    __syncwarp();
+  } else if (warp == 2) {
+    const float* lg = p.lg + n * p.sg.n + h * p.sg.h;
+    Share f;
+    if (num > 0) load_decays(lg, p.sg.t, token(0), count, f.x);
+    bool ok = true;
+#pragma unroll 1
+    for (int it = 0; it < num && ok; ++it) {
       float next[4] = {};
-      if (it + 2 < num) load_decays(lg, p.sg.t, token(it + 2), count, next);
+      if (it + 1 < num) load_decays(lg, p.sg.t, token(it + 1), count, next);
       f.make(p.rev);
       if (it > 1 && !(ok = wait_for(ctl, FACE + (it & 1), (it / 2 - 1) & 1))) break;
       f.put(hd.f[it & 1]);
@@ -561,14 +582,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         continue;
       }
       // P, 16 columns at a time
-      const float row = f.row[o], rf = ex2_approx(row) * p.scale_in;
+      const float row = f.row[o] + q.log_scale, rf = ex2_approx(row);
       const uint32_t ts = tmem + tl + kColS, tp = tmem + tl + kColP;
       float d[16];
       block_of((own ? f.row : f.col) + 16 * j1, d);
       const int io = lane & 15;
 #pragma unroll
       for (int k = 0; k < 16; ++k) {
-        const float e = (p.rev ? k >= io : k <= io) ? ex2_approx(row - d[k]) * p.scale_in : 0.f;
+        const float e = (p.rev ? k >= io : k <= io) ? ex2_approx(row - d[k]) : 0.f;
         d[k] = own ? e : sees ? rf * d[k] : 0.f;
       }
       if (!(ok = wait_warp(ctl, SR, it & 1))) break;
@@ -612,7 +633,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(&ctl->bar[PR]), mbar_arrive(&ctl->bar[FACE + (it & 1)]);
     }
     if (!ok) ctl->abort = 1;
-  } else if (warp >= 12) {
+  } else if (warp >= 12 && warp < 20) {
     const int half = (warp - 12) >> 2, qw = warp & 3;
     const int i = 32 * qw + lane;  // row of the state, row of the output
     const bool mine = i < DA;
@@ -666,7 +687,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int it = 0; it < num && ok; ++it) {
       if (!(ok = wait_for(ctl, FACF + (it & 1), (it >> 1) & 1))) break;
       const Factors& f = hd.f[it & 1];
-      const float from = exp2f(f.row[i]) * f.head[i >> 4], all = f.all;
+      const float from = exp2f(f.row[i]) * f.head[i >> 4] * p.scale_out, all = f.all;
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->bar[FACE + (it & 1)]);
       product *= all;
@@ -695,10 +716,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->bar[KVF + (it & 1)]);
       if (q.g.states_only) continue;
-      if (it + 1 < num) {
-        if (!(ok = wait_for(ctl, HF, it & 1))) break;
-        put_state();
-      }
+      if (!(ok = wait_for(ctl, HF, it & 1))) break;
+      if (it + 1 < num) put_state();
       // out = P C + from o (A H)
       const int t = token(it) + i;
       const bool live = t < count;
@@ -706,7 +725,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       float d = 0.f;
       uint4 w[4];
-      const float2 scale = make_float2(p.scale_out, p.scale_out), from2 = make_float2(from, from);
+      const float2 from2 = make_float2(from, from);
+      const bool tail = ragged(it);
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         uint32_t y[16], ys[16];
@@ -734,9 +754,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         float2 v[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          v[j] = f2_mul(scale, f2_fma(from2, make_float2(f32(ys[2 * j]), f32(ys[2 * j + 1])),
-                                  make_float2(f32(y[2 * j]), f32(y[2 * j + 1]))));
-          if (!live) v[j] = make_float2(0.f, 0.f);  // rows behind the sequence may have held anything
+          v[j] = f2_fma(from2, make_float2(f32(ys[2 * j]), f32(ys[2 * j + 1])), make_float2(f32(y[2 * j]), f32(y[2 * j + 1])));
+          if (tail && !live) v[j] = make_float2(0.f, 0.f);  // rows behind the sequence may have held anything
         }
         if (p.out_f32) {
           unsigned char* o = static_cast<unsigned char*>(p.out) + (so + 16 * e) * 4;
@@ -757,7 +776,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (!p.out_f32) put64(static_cast<unsigned char*>(p.out) + so * 2, p.so.t * 2, t - lane, p.L, w);
-      if (NPH == 3 && px && live) dot[t] = p.scale_out * from * d;
+      if (NPH == 3 && px && live) dot[t] = from * d;
     }
     if (!ok) ctl->abort = 1;
     if (ok && q.g.states_only) {
@@ -1049,6 +1068,7 @@ cudaError_t launch_decay_tc(const DecayPass& a, bool exact_state, float* ws, cud
   g.segs = tc_segments(ctas, a.L);
   g.cps = (chunks + g.segs - 1) / g.segs;
   q.parts = a.fin || a.x ? 3 : 2;
+  q.log_scale = log2f(a.scale_in * a.scale_out);
   if (ctas * g.segs > 0x7fffffffll) return cudaErrorInvalidValue;
   cudaError_t e;
   if (g.segs > 1) {
