@@ -135,29 +135,11 @@ __device__ __forceinline__ void commit_lo(uint64_t* bar) {
       "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar))
       : "memory");
 }
-// wait_bar with its polling out of line (the roles' loops are long, and what they share should be in the
-// instruction cache once) and a hint of how long the hardware may suspend a try (every poll reads shared
-// memory).
+// wait_bar with its polling out of line: the roles' loops are long, and what they share should be in the
+// instruction cache once.
 template <int N>
 __device__ __noinline__ bool wait_polls(Ctl<N>* ctl, int i, uint32_t parity) {
-  const uint32_t bar = smem_u32(&ctl->bar[i]);
-  const long long t0 = clock64();
-  while (true) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cta.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity), "r"(20000u)
-        : "memory");
-    if (ok) return true;
-    if (*(volatile int*)&ctl->abort) return false;
-    if (clock64() - t0 > kWaitCycles) {
-      *(volatile int*)&ctl->abort = 1;
-      return false;
-    }
-  }
+  return wait_bar(ctl, i, parity);
 }
 template <int N>
 __device__ __forceinline__ bool wait_for(Ctl<N>* ctl, int i, uint32_t parity) {
@@ -422,13 +404,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t sb = smem_u32(sm);
       const uint32_t id_s = idesc_bf16(kC, kC, false, false), id_c = idesc_bf16(kC, kN, false, true);
       const uint32_t da = desc_lower(sb + Sm::A, 16), db = desc_lower(sb + Sm::B, 16), dc = desc_lower(sb + Sm::Ct, kC * 128);
-      bool ok = true;
-#pragma unroll 1
-      for (int it = 0; it < num && ok; ++it) {
-        // S = A B^T (the last one has been read: P C has been issued)
-        if (!(ok = wait_warp(ctl, FB + it % Sm::NBt, (it / Sm::NBt) & 1))) break;
-        if (!(ok = wait_warp(ctl, FA + it % Sm::NA, (it / Sm::NA) & 1))) break;
-        if (ragged(it) && !(ok = wait_warp(ctl, FIX, 0))) break;
+      auto scores = [&](int it) {  // S = A B^T
+        if (!wait_warp(ctl, FB + it % Sm::NBt, (it / Sm::NBt) & 1) || !wait_warp(ctl, FA + it % Sm::NA, (it / Sm::NA) & 1))
+          return false;
+        if (ragged(it) && !wait_warp(ctl, FIX, 0)) return false;
         tc_fence_after();
         const uint32_t a = da + it % Sm::NA * (Sm::kTile / 16), b = db + it % Sm::NBt * (Sm::kTile / 16);
 #pragma unroll 4
@@ -436,8 +415,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         commit_lo(&ctl->bar[SR]);
         commit_lo(&ctl->bar[EA + it % Sm::NA]);
         commit_lo(&ctl->bar[EB + it % Sm::NBt]);
-        // P C
+        return true;
+      };
+      bool ok = num == 0 || scores(0);
+#pragma unroll 1
+      for (int it = 0; it < num && ok; ++it) {
+        // P is there, so S has been read: the next scores first, which are waited for sooner than P C
         if (!(ok = wait_warp(ctl, PR, it & 1))) break;
+        if (it + 1 < num && !(ok = scores(it + 1))) break;
         if (it > 0 && !(ok = wait_warp(ctl, YF, (it - 1) & 1))) break;
         tc_fence_after();
         const uint32_t c = dc + it % Sm::NCt * (kTileC / 16);
