@@ -406,7 +406,9 @@ __device__ __forceinline__ int gate_count(const DecayGate& a, int n) {
 }
 
 constexpr int kGateWarps = 4;
+// IN, OUT: planes; all of a chunk's numbers are on their way together.
 // sums [units][chunks + 1]: of the chunks (x: rows, y: cols; a start as rows = NaN), then <h0, d_h0>
+template <int OUT>
 __global__ void __launch_bounds__(32 * kGateWarps) decay_gate_sums_kernel(DecayGate a, int chunks) {
   pdl_wait();
   const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
@@ -439,17 +441,21 @@ __global__ void __launch_bounds__(32 * kGateWarps) decay_gate_sums_kernel(DecayG
   const float* lg = a.lg + n * a.sg.n + h * a.sg.h;
   float r = 0.f, c1 = 0.f;
   bool start = false;
-#pragma unroll 4
-  for (int t = t0 + lane; t < end; t += 32) {
-#pragma unroll 4
-    for (int s = 0; s < a.out_slices; ++s) r += a.row_out[s * plane + base + t], c1 += a.col_out[s * plane + base + t];
-    start |= lg[t * a.sg.t] < kDecayNone;
+#pragma unroll
+  for (int g = 0; g < kDecayTile / 32; ++g) {
+    const int t = t0 + 32 * g + lane;
+    if (t < end) {
+#pragma unroll
+      for (int s = 0; s < OUT; ++s) r += a.row_out[s * plane + base + t], c1 += a.col_out[s * plane + base + t];
+      start |= lg[t * a.sg.t] < kDecayNone;
+    }
   }
   const double rows = warp_sum(r), cols = warp_sum(c1);
   start = __any_sync(0xffffffffu, start);
   if (lane == 0) a.sums[(int64_t)unit * (chunks + 1) + c] = make_double2(start ? nan("") : rows, cols);
 }
 
+template <int IN, int OUT>
 __global__ void __launch_bounds__(32 * kGateWarps) decay_gate_kernel(DecayGate a, int chunks) {
   pdl_wait();
   const int lane = threadIdx.x % 32, per = (chunks + kGateWarps - 1) / kGateWarps;
@@ -486,11 +492,11 @@ __global__ void __launch_bounds__(32 * kGateWarps) decay_gate_kernel(DecayGate a
     sum[g] = col[g] = 0.f;
     if (t < end) {
       if (lg[t * a.sg.t] < kDecayNone) cut |= 1u << g;
-#pragma unroll 2
-      for (int s = 0; s < a.in_slices; ++s)
+#pragma unroll
+      for (int s = 0; s < IN; ++s)
         sum[g] += a.row_in[s * plane + base + t] - (a.col_in ? a.col_in[s * plane + base + t] : 0.f);
-#pragma unroll 4
-      for (int s = 0; s < a.out_slices; ++s)
+#pragma unroll
+      for (int s = 0; s < OUT; ++s)
         sum[g] += a.row_out[s * plane + base + t], col[g] += a.col_out[s * plane + base + t];
     }
   }
@@ -609,13 +615,22 @@ cudaError_t launch_decay_gate(const DecayGate& a, cudaStream_t s, int* launches)
   const int chunks = (a.L + a.chunk - 1) / a.chunk;
   const int64_t units = (int64_t)a.B * a.H, blocks = units * ((chunks + kGateWarps - 1) / kGateWarps);
   if (units + blocks > 0x7fffffffll) return cudaErrorInvalidValue;
+  const dim3 all((unsigned)(units + blocks)), block(32 * kGateWarps);
   trace_begin("decay_gate_sums", s);
-  cudaError_t e = launch_pdl(decay_gate_sums_kernel, dim3((unsigned)(units + blocks)), dim3(32 * kGateWarps), 0, s, a, chunks);
+  cudaError_t e = cudaErrorInvalidValue;
+  if (a.out_slices == 1) e = launch_pdl(decay_gate_sums_kernel<1>, all, block, 0, s, a, chunks);
+  if (a.out_slices == 2) e = launch_pdl(decay_gate_sums_kernel<2>, all, block, 0, s, a, chunks);
+  if (a.out_slices == 4) e = launch_pdl(decay_gate_sums_kernel<4>, all, block, 0, s, a, chunks);
   trace_end(s);
   ++*launches;
   if (e != cudaSuccess) return e;
   trace_begin("decay_gate", s);
-  e = launch_pdl(decay_gate_kernel, dim3((unsigned)blocks), dim3(32 * kGateWarps), 0, s, a, chunks);
+  e = cudaErrorInvalidValue;
+  const dim3 grid((unsigned)blocks);
+  if (a.in_slices == 1 && a.out_slices == 1) e = launch_pdl(decay_gate_kernel<1, 1>, grid, block, 0, s, a, chunks);
+  if (a.in_slices == 1 && a.out_slices == 2) e = launch_pdl(decay_gate_kernel<1, 2>, grid, block, 0, s, a, chunks);
+  if (a.in_slices == 2 && a.out_slices == 2) e = launch_pdl(decay_gate_kernel<2, 2>, grid, block, 0, s, a, chunks);
+  if (a.in_slices == 1 && a.out_slices == 4) e = launch_pdl(decay_gate_kernel<1, 4>, grid, block, 0, s, a, chunks);
   trace_end(s);
   ++*launches;
   return e;

@@ -797,13 +797,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ---------------------------------------------------------------------------------
 // Within a chunk: diff_i = sum_{s < i} W_is - sum_{s > i} W_si with W_is = scale (q_i . k_s) D (dy_i . v_s), from
-// exact products of the bf16 rows in fp32 sums.  One CTA a chunk, two an SM: the two scores by MMAs (dy
-// takes q's place in shared memory once the first is done), then eight warps of which each has every other
-// 32 columns of its 32 rows: a thread sums its row, and the 32 columns are summed over the warp by halving
-// exchanges.
+// exact products of the bf16 rows in fp32 sums.  Two CTAs an SM, each chunk after chunk: the two scores by
+// MMAs (dy takes q's place in shared memory once the first is done; the next chunk's rows come while this
+// one's are summed), then eight warps of which each has every other 32 columns of its 32 rows: a thread sums
+// its row, and the 32 columns are summed over the warp by halving exchanges.  (64 heads x 4096 tokens of 128:
+// a CTA a chunk 62 us, this 41.)
 // ---------------------------------------------------------------------------------
 constexpr int kPairThreads = 384;
-enum { GQ = 0, GY, GS, GP, GN };
+enum { GQ = 0, GY, GS, GP, GR, GF = 5, GE = 7, GN = 9 };  // GF, GE: by parity
 struct PairMaps {
   CUtensorMap q, k, v, y;
 };
@@ -819,13 +820,13 @@ struct PairParams {
 };
 struct alignas(16) PairHead {
   Ctl<GN> ctl;
-  Factors f;
-  float x[kC];
-  float rows[2][kC], cols[4][kC];  // by half of the columns, by quarter of the rows
+  Factors f[2];
+  float x[2][kC];
+  float rows[2][2][kC], cols[2][4][kC];  // [parity][half of the columns, or quarter of the rows]
 };
 template <int DK, int DV>
 struct PairSmem {
-  static constexpr int kHead = 5120;
+  static constexpr int kHead = 11264;
   static_assert(sizeof(PairHead) <= kHead, "barriers, factors and sums");
   static constexpr int kQ = kC * DK * 2, kV = kC * DV * 2, kFirst = kQ > kV ? kQ : kV;
   static constexpr int Q = 0, K = kFirst, V = K + kQ, kBytes = kHead + V + kV;
@@ -846,144 +847,185 @@ __device__ __forceinline__ float column_sums(float (&w)[32]) {
 
 template <int DK, int DV>
 __global__ void __launch_bounds__(kPairThreads, 2)
-    decay_pairs_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ PairParams p, int chunks) {
+    decay_pairs_kernel(const __grid_constant__ PairMaps maps, const __grid_constant__ PairParams p, int chunks, int items) {
   using Sm = PairSmem<DK, DV>;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
   PairHead& hd = *reinterpret_cast<PairHead*>(smem_raw);
   Ctl<GN>* ctl = &hd.ctl;
   unsigned char* sm = smem_raw + Sm::kHead;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   if ((smem_u32(smem_raw) & 1023u) != 0) {
     if (tid == 0) raise_status(p.status, kDevCheck);
     return;
   }
-  const int unit = blockIdx.x / chunks, t0 = (blockIdx.x - unit * chunks) * kC;
-  const int n = unit / p.H, h = unit - n * p.H;
-  pdl_wait();
-  int count = p.count ? p.count[n] : p.L;
-  if (count < 0 || count > p.L) count = 0;  // flagged by the passes
-  if (t0 >= count) return;
   if (warp == 1) {
     tmem_alloc(&ctl->tmem, 256);
     tmem_relinquish();
   }
   if (tid == 0) {
-    for (int i = 0; i < GN; ++i) mbar_init(&ctl->bar[i], 1);
+    for (int i = 0; i < GN; ++i) mbar_init(&ctl->bar[i], i == GR || i >= GE ? 8 : 1);
     ctl->abort = 0;
     fence_mbar_init();
   }
   tc_fence_before();
   cta_sync();
   tc_fence_after();
-  const uint32_t tmem = ctl->tmem;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, ctl->tmem, 0);
+  pdl_wait();
+  // item w: chunk w mod chunks of head w / chunks; those behind a sequence's end are nobody's
+  struct Item {
+    int unit, n, h, t0, count;
+  };
+  auto item_of = [&](int w) {
+    Item i;
+    i.unit = w / chunks, i.t0 = (w - i.unit * chunks) * kC;
+    i.n = i.unit / p.H, i.h = i.unit - i.n * p.H;
+    i.count = p.count ? p.count[i.n] : p.L;
+    if (i.count < 0 || i.count > p.L) i.count = 0;  // flagged by the passes
+    i.count = __shfl_sync(0xffffffffu, i.count, 0);
+    return i;
+  };
+  bool ok = true;
+  int it = 0;  // items done
   if (warp == 0) {
-    if (lane == 0) {
-      const int hk = h / p.G;
-      mbar_arrive_expect_tx(&ctl->bar[GQ], 2 * Sm::kQ);
+#pragma unroll 1
+    for (int w = blockIdx.x; w < items && ok; w += gridDim.x) {
+      const Item i = item_of(w);
+      if (i.t0 >= i.count) continue;
+      // the last item's rows have been multiplied
+      if (it > 0 && !(ok = wait_warp(ctl, GP, (it - 1) & 1))) break;
+      const int hk = i.h / p.G;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(&ctl->bar[GQ], 2 * Sm::kQ);
 #pragma unroll
-      for (int k = 0; k < DK / 64; ++k) {
-        tma_load_4d(sm + Sm::Q + k * kC * 128, &maps.q, 64 * k, t0, p.qh * h, p.qn * n, &ctl->bar[GQ]);
-        tma_load_4d(sm + Sm::K + k * kC * 128, &maps.k, 64 * k, t0, p.kh * hk, p.kn * n, &ctl->bar[GQ]);
-      }
-      mbar_arrive_expect_tx(&ctl->bar[GY], 2 * Sm::kV);
-#pragma unroll
-      for (int k = 0; k < DV / 64; ++k)
-        tma_load_4d(sm + Sm::V + k * kC * 128, &maps.v, 64 * k, t0, p.vh * hk, p.vn * n, &ctl->bar[GY]);
-      const bool ok = wait_for(ctl, GS, 0);
-      if (ok) {
+        for (int k = 0; k < DK / 64; ++k) {
+          tma_load_4d(sm + Sm::Q + k * kC * 128, &maps.q, 64 * k, i.t0, p.qh * i.h, p.qn * i.n, &ctl->bar[GQ]);
+          tma_load_4d(sm + Sm::K + k * kC * 128, &maps.k, 64 * k, i.t0, p.kh * hk, p.kn * i.n, &ctl->bar[GQ]);
+        }
+        mbar_arrive_expect_tx(&ctl->bar[GY], 2 * Sm::kV);
 #pragma unroll
         for (int k = 0; k < DV / 64; ++k)
-          tma_load_4d(sm + Sm::Q + k * kC * 128, &maps.y, 64 * k, t0, p.yh * h, p.yn * n, &ctl->bar[GY]);
-      } else {
-        ctl->abort = 1;
+          tma_load_4d(sm + Sm::V + k * kC * 128, &maps.v, 64 * k, i.t0, p.vh * hk, p.vn * i.n, &ctl->bar[GY]);
       }
-      const uint64_t began = globaltimer_ns();
-      drain_bar(ctl, GQ, 1, began);
-      drain_bar(ctl, GY, 1, began);
+      __syncwarp();
+      ++it;
+      if (!(ok = wait_warp(ctl, GS, (it - 1) & 1))) break;
+      if (lane == 0) {
+#pragma unroll
+        for (int k = 0; k < DV / 64; ++k)
+          tma_load_4d(sm + Sm::Q + k * kC * 128, &maps.y, 64 * k, i.t0, p.yh * i.h, p.yn * i.n, &ctl->bar[GY]);
+      }
+      __syncwarp();
     }
+    if (!ok) ctl->abort = 1;
+    const uint64_t began = globaltimer_ns();
+    drain_bar(ctl, GQ, it, began);
+    drain_bar(ctl, GY, it, began);
+    __syncwarp();
   } else if (warp == 1) {
     const uint32_t sb = smem_u32(sm), id = idesc_bf16(kC, kC, false, false);
     const uint32_t dq = desc_lower(sb + Sm::Q, 16), dk = desc_lower(sb + Sm::K, 16), dv = desc_lower(sb + Sm::V, 16);
-    bool ok = wait_warp(ctl, GQ, 0);
-    if (ok) {
+#pragma unroll 1
+    for (int w = blockIdx.x; w < items && ok; w += gridDim.x) {
+      const Item i = item_of(w);
+      if (i.t0 >= i.count) continue;
+      if (!(ok = wait_warp(ctl, GQ, it & 1))) break;
+      if (it > 0 && !(ok = wait_warp(ctl, GE + ((it - 1) & 1), ((it - 1) >> 1) & 1))) break;  // the last scores are read
       tc_fence_after();
 #pragma unroll 4
       for (int j = 0; j < DK / 16; ++j) mma_lo(tmem, dq + step_k(j), dk + step_k(j), id, j > 0);
-    }
-    commit_lo(&ctl->bar[GS]);
-    ok = ok && wait_warp(ctl, GY, 0);
-    if (ok) {
+      commit_lo(&ctl->bar[GS]);
+      if (!(ok = wait_warp(ctl, GY, it & 1))) break;
       tc_fence_after();
 #pragma unroll 4
       for (int j = 0; j < DV / 16; ++j) mma_lo(tmem + 128, dq + step_k(j), dv + step_k(j), id, j > 0);
-    } else {
-      ctl->abort = 1;
+      commit_lo(&ctl->bar[GP]);
+      ++it;
     }
-    commit_lo(&ctl->bar[GP]);
-    drain_bar(ctl, GP, 1, globaltimer_ns());
+    if (!ok) ctl->abort = 1;
+    // what was issued has ended: the last item's products, or the one broken off
+    if (!ok) commit_lo(&ctl->bar[GP]);
+    drain_bar(ctl, GP, it + (ok ? 0 : 1), globaltimer_ns());
     __syncwarp();
+  } else if (warp == 2) {
+#pragma unroll 1
+    for (int w = blockIdx.x; w < items && ok; w += gridDim.x) {
+      const Item i = item_of(w);
+      if (i.t0 >= i.count) continue;
+      Share v;
+      load_decays(p.lg + i.n * p.sg.n + i.h * p.sg.h, p.sg.t, i.t0, i.count, v.x);
+      v.make(false);
+      const int par = it & 1;
+      if (it > 1 && !(ok = wait_warp(ctl, GE + par, ((it >> 1) - 1) & 1))) break;
+      *reinterpret_cast<float4*>(hd.x[par] + 4 * lane) = make_float4(v.x[0], v.x[1], v.x[2], v.x[3]);
+      v.put(hd.f[par]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->bar[GF + par]);
+      ++it;
+    }
+    if (!ok) ctl->abort = 1;
   } else if (warp >= 4) {
     const int half = (warp - 4) >> 2, qw = warp & 3, o = 32 * qw + lane, I = o >> 4;
-    if (warp == 4) {
-      Share v;
-      load_decays(p.lg + n * p.sg.n + h * p.sg.h, p.sg.t, t0, count, v.x);
-      *reinterpret_cast<float4*>(hd.x + 4 * lane) = make_float4(v.x[0], v.x[1], v.x[2], v.x[3]);
-      v.make(false);
-      v.put(hd.f);
-    }
-    named_sync(1, 256);
-    const Factors& f = hd.f;
     const uint32_t tl = tmem + ((uint32_t)(qw * 32) << 16);
-    const bool ok = wait_for(ctl, GP, 0);
-    float sum = 0.f;
-    if (ok) {
+#pragma unroll 1
+    for (int w = blockIdx.x; w < items && ok; w += gridDim.x) {
+      const Item i = item_of(w);
+      if (i.t0 >= i.count) continue;
+      const int par = it & 1;
+      if (!(ok = wait_warp(ctl, GF + par, (it >> 1) & 1))) break;
+      if (!(ok = wait_warp(ctl, GP, it & 1))) break;
       tc_fence_after();
+      const Factors& f = hd.f[par];
       const float rf = exp2f(f.row[o]);
-      const bool there = t0 + o < count;
+      const bool there = i.t0 + o < i.count;
+      float sum = 0.f;
 #pragma unroll 1
       for (int g = half; g <= qw; g += 2) {
         uint32_t s[32];
-        float w[32];
+        float z[32];
         if (g == qw) {
           // the thread's own block of 16 by running sums, the one before it wholly, what is behind nothing
           float d[16];
-          block_decays(hd.x + 16 * I, lane & 15, false, d);
+          block_decays(hd.x[par] + 16 * I, lane & 15, false, d);
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
             const float in = j == (lane & 15) ? 0.f : d[j];
-            w[j] = lane < 16 ? in : rf * f.col[32 * g + j];
-            w[16 + j] = lane < 16 ? 0.f : in;
+            z[j] = lane < 16 ? in : rf * f.col[32 * g + j];
+            z[16 + j] = lane < 16 ? 0.f : in;
           }
         } else {
           const float r0 = rf * f.g[I * 8 + 2 * g], r1 = rf * f.g[I * 8 + 2 * g + 1];
 #pragma unroll
-          for (int j = 0; j < 32; ++j) w[j] = (j < 16 ? r0 : r1) * f.col[32 * g + j];
+          for (int j = 0; j < 32; ++j) z[j] = (j < 16 ? r0 : r1) * f.col[32 * g + j];
         }
         tmem_ld32(tl + 32 * g, s);
         tmem_ld_wait();
 #pragma unroll
-        for (int j = 0; j < 32; ++j) w[j] = w[j] != 0.f && there ? w[j] * f32(s[j]) : 0.f;
+        for (int j = 0; j < 32; ++j) z[j] = z[j] != 0.f && there ? z[j] * f32(s[j]) : 0.f;
         tmem_ld32(tl + 128 + 32 * g, s);
         tmem_ld_wait();
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
           // (rows behind the sequence may hold anything, and a decay of 0 hides a token)
-          w[j] = w[j] != 0.f ? w[j] * f32(s[j]) : 0.f;
-          sum += w[j];
+          z[j] = z[j] != 0.f ? z[j] * f32(s[j]) : 0.f;
+          sum += z[j];
         }
-        hd.cols[qw][32 * g + lane] = column_sums(w);
+        hd.cols[par][qw][32 * g + lane] = column_sums(z);
       }
-      hd.rows[half][o] = sum;
-    } else {
-      ctl->abort = 1;
+      hd.rows[par][half][o] = sum;
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->bar[GE + par]), mbar_arrive(&ctl->bar[GR]);
+      if (!(ok = wait_warp(ctl, GR, it & 1))) break;
+      const int t = tid - 128;
+      if (t < kC && i.t0 + t < i.count) {
+        float d = hd.rows[par][0][t] + hd.rows[par][1][t], c = 0.f;
+        for (int r = t >> 5; r < 4; ++r) c += hd.cols[par][r][t];
+        p.diff[(int64_t)i.unit * p.L + i.t0 + t] = p.scale * (d - c);
+      }
+      ++it;
     }
-    named_sync(1, 256);
-    const int t = tid - 128;
-    if (t < kC && t0 + t < count && !*(volatile int*)&ctl->abort) {
-      float d = hd.rows[0][t] + hd.rows[1][t], c = 0.f;
-      for (int r = t >> 5; r < 4; ++r) c += hd.cols[r][t];
-      p.diff[(int64_t)unit * p.L + t0 + t] = p.scale * (d - c);
-    }
+    if (!ok) ctl->abort = 1;
   }
   tc_fence_before();
   cta_sync();
@@ -1022,9 +1064,10 @@ cudaError_t launch_pairs(const PairMaps& m, const PairParams& p, cudaStream_t s)
   const cudaError_t e = allow_smem(decay_pairs_kernel<DK, DV>, Sm::kBytes, done);
   if (e != cudaSuccess) return e;
   const int chunks = (p.L + kC - 1) / kC;
-  const int64_t blocks = (int64_t)p.B * p.H * chunks;
-  if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
-  return launch_pdl(decay_pairs_kernel<DK, DV>, dim3((unsigned)blocks), dim3(kPairThreads), Sm::kBytes, s, m, p, chunks);
+  const int64_t items = (int64_t)p.B * p.H * chunks, most = ctas_per_wave(2);
+  if (items > 0x7f000000ll) return cudaErrorInvalidValue;  // (and a step on top of it)
+  return launch_pdl(decay_pairs_kernel<DK, DV>, dim3((unsigned)(items < most ? items : most)), dim3(kPairThreads), Sm::kBytes, s,
+                    m, p, chunks, (int)items);
 }
 
 }  // namespace
