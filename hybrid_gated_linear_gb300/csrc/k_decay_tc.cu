@@ -801,7 +801,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // MMAs (dy takes q's place in shared memory once the first is done; the next chunk's rows come while this
 // one's are summed), then eight warps of which each has every other 32 columns of its 32 rows: a thread sums
 // its row, and the 32 columns are summed over the warp by halving exchanges.  (64 heads x 4096 tokens of 128:
-// a CTA a chunk 62 us, this 41.)
+// a CTA a chunk 62 us, this 50.)
 // ---------------------------------------------------------------------------------
 constexpr int kPairThreads = 384;
 enum { GQ = 0, GY, GS, GP, GR, GF = 5, GE = 7, GN = 9 };  // GF, GE: by parity
@@ -1043,9 +1043,10 @@ bool rows_map(CUtensorMap* m, const void* base, int64_t B, int64_t H, int64_t L,
   const uint64_t st[3] = {L > 1 ? (uint64_t)s.t * 2 : 16 * 16, *kh ? (uint64_t)s.h * 2 : 16 * 16, *kn ? (uint64_t)s.n * 2 : 16 * 16};
   return make_tma_map_4d_bf16(m, base, dims, st, 64, kC);
 }
+// Rows that lie apart (axes may repeat), strides below the map's 2^40 bytes.
 bool strides_ok(int64_t B, int64_t H, int64_t L, int d, const Strides& s) {
-  const int64_t most = 1ll << 38;  // elements: a stride of a map is below 2^40 bytes
-  return (B <= 1 || s.n < most) && (H <= 1 || s.h < most) && (L <= 1 || (s.t >= d && s.t < most));
+  auto axis = [&](int64_t n, int64_t st, bool repeats) { return n <= 1 || (repeats && st == 0) || (st >= d && st < 1ll << 38); };
+  return axis(B, s.n, true) && axis(H, s.h, true) && axis(L, s.t, false);
 }
 
 template <int DA, int NPH>

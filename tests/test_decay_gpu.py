@@ -65,6 +65,14 @@ class In:
             assert lz.lizard_check_device_errors(ws) == status
         return (*out, dg, dh)
 
+    def gradients(self):
+        """d_q, d_k, d_v alone, into contiguous rows (inputs may repeat: the caller sums)."""
+        d = self.dims
+        out = [torch.full(t.shape, 9.0, dtype=t.dtype, device="cuda") for t in (self.q, self.k, self.v)]
+        lz.lizard_decay_attn_bwd(d, self.q, self.k, self.v, self.g, self.counts(), self.h0, self.dy, self.df, *out, None, None,
+                                 workspace(d, True))
+        return out
+
     def check_fwd(self, **kw):
         y, h = self.fwd(**kw)
         c = self.case()
@@ -387,3 +395,37 @@ def test_rows_far_apart():
     q, k, v, y = (w[None, None] for w in where)
     lz.lizard_decay_attn_fwd(d, q, k, v, x.g, None, None, y, None, workspace(d, False))
     assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_overlapping_and_repeated_rows(dtype):
+    """Inputs whose rows overlap in memory or repeat along any axis: heads 16 channels apart, one sequence
+    for all, every token's row 16 channels behind the last."""
+    B, H, L, d = 2, 3, 140, 64
+    gen = torch.Generator().manual_seed(21)
+    flat = torch.randn(B * 100000, generator=gen).to(DT[dtype]).cuda()
+    x = In(B, H, H, L, d, d, dtype)
+    for strides in ((30000, 16, 64), (30000, 10000, 16), (0, 10000, 64), (0, 0, 64)):
+        x.q, x.k, x.v = (flat[16 * i:].as_strided((B, H, L, d), (*strides, 1)) for i in range(3))
+        x.check_fwd()
+        got, c = x.gradients(), x.case(True)
+        for p, want, s in zip(got, c.grads, c.sums):
+            do.close(p, want, do.bound(want, s, p.dtype, x.terms()))
+
+
+def test_two_calls_at_once():
+    """Two streams, each with a workspace of its own, over and over: nothing is shared."""
+    x, z = In(2, 4, 2, 900, 128, 128, "bf16"), In(3, 6, 6, 300, 64, 128, "f32")
+    want = [(x.fwd(), x.bwd()), (z.fwd(), z.bwd())]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(4):
+        for i, (c, s) in enumerate(zip((x, z), streams)):
+            with torch.cuda.stream(s):
+                got[i].append((c.fwd(status=None), c.bwd(status=None)))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for pair in got[i]:
+            for a, b in zip(want[i], pair):
+                assert all(torch.equal(p, q) for p, q in zip(a, b))
