@@ -7,7 +7,8 @@
 // Every product is made of three tf32 products of the warp-level tensor instructions, x = hi + lo with hi the
 // upper 11 bits: hi hi + hi lo + lo hi, which leaves 2^-22 of a product (8 more bits in each operand than
 // tcgen05's bf16 parts, whose three tiles an operand would not fit beside each other).  Against 4 x 4 results a
-// thread by fp32 multiply-adds: 5 sequences of 1999 tokens, 12 heads of 64 x 128, 248 -> 101 us.
+// thread by fp32 multiply-adds: 5 sequences of 1999 tokens, 12 heads of 64 x 128, 248 -> 142 us.  Bound by the
+// chain of a chunk (rows in, scores, out, state; two CTAs an SM): tensor cycles 31%, DRAM 5%.
 #include "lizard_dev.cuh"
 #include "lizard_internal.h"
 #include "tc_sm100.cuh"
@@ -95,7 +96,8 @@ __device__ __forceinline__ void decays(Smem<DA>& m, const float* lg, int64_t st,
 }
 
 // A word as two tf32 operands, both rounded to nearest: 11 bits, and 11 of what is left.  (The instruction
-// does not read a word's lower 13 bits; cut off instead of rounded, results were 1.4e-6 off, this way 3e-7.)
+// does not read a word's lower 13 bits; cut off instead of rounded, results were 1.4e-6 off, this way 7e-7, and
+// with the small products' sums apart 3.5e-7.)
 struct Two {
   uint32_t hi, lo;
 };
@@ -391,7 +393,7 @@ __global__ void __launch_bounds__(kThreads) decay_heads_kernel(int Hk, int G, in
 // `through` of the chunks follows from the pairs over the edge before the first one, <h0, d_h0>:
 //   edge after = through + sum col_out,  through = edge before - sum row_out  (0 where a document
 // starts in the chunk).  Sums over chunks run in 64 bits, within 32 tokens in trees of fp32 (64-bit
-// additions are what this GPU has least of: with them throughout, 49 us against 13 for 64 heads x 4096
+// additions are what this GPU has least of: with them throughout, 49 us against 25 for 64 heads x 4096
 // tokens).  First a warp for each chunk takes its sums of row_out
 // and col_out and whether a document starts, and a block for each head <h0, d_h0>; then a warp for
 // each chunk adds up the edge in front of it and writes its tokens.

@@ -14,8 +14,7 @@
 // A CTA takes 64 of C's channels of one head over the chunks of one segment; H stays in registers in
 // fp32.  Twenty warps (five on each quarter of the SM, at 96 registers):
 //   0      copies the tiles of A, B [128][da] and C [128][64] in by TMA, two stages ahead
-//   1, 3   issue the MMAs: S and P C, and B^T C~ and A H (one warp for all spent a third of its time waiting
-//          in turn for what the two sides make: 4430 against 3700 cycles a chunk)
+//   1, 3   issue the MMAs: S and P C, and B^T C~ and A H
 //   2      the decays of the next chunks
 //   4-11   C~ = to o C in two or three bf16 parts (16 or 24 bits: the state is a sum over the whole
 //          sequence, so its operands are not rounded), then P, rounded once to bf16, into TMEM
@@ -23,7 +22,15 @@
 //          rounded too, or three where the product with H itself is a result); then the rows of out
 // TMEM: S 128 columns, P 64, B^T C~ 3 x 64 (its parts side by side: one reading of B for all of them),
 // P C 64, A H 64.
-// The shared memory's bandwidth bounds it: the MMAs read their operands there.
+//
+// What bounds it is none of the peaks: 2 x 4096 tokens at 32 heads of 128 take 82 us, 3.0 TB/s and 38% of
+// the tensor cycles, the shared memory about 80% busy with operands, copies and C~, the schedulers 56%.
+// A chunk takes about 4400 cycles, of which each group of warps spends 900 instructions at four to five
+// cycles; leaving out any one of the loads, of the MMAs, of P's or of out's arithmetic changes it by 5% at
+// most, C~ by 15%.  What brought it there from 128 us: MMAs issued by a whole warp in uniform registers
+// (a lane's branch: 90 cycles an MMA), loops kept short (instruction fetch was the first stall), out stored
+// by whole sectors, scores of the next chunk ahead of P C.  Not kept: clusters of a head's two slices with
+// multicast tiles (90 us), out through shared memory (148 us).
 #include <math.h>
 
 #include "lizard_dev.cuh"
@@ -542,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int lag = q.g.states_only ? 2 : 1;
       if (it >= lag && !(ok = wait_for(ctl, KVR + ((it - lag) & 1), ((it - lag) >> 1) & 1))) break;
       unsigned char* cp = sm + (q.g.states_only && (it & 1) ? Sm::CP2 : Sm::CP);
-#pragma unroll
+#pragma unroll 2
       for (int e = 0; e < kTileC / 16 / (32 * kScoreWarps); ++e) {
         const int at = (wt + 32 * kScoreWarps * e) * 16;  // byte of the tile: the swizzle stays as it is
         const float w = f.col[at >> 7] * f.tail[at >> 11] * p.scale_in;
