@@ -140,6 +140,14 @@ lizard_status lizard_decay_attn_fwd(const lizard_decay_dims* dims, const void* q
   const cudaStream_t s = (cudaStream_t)stream;
   const Tensor in[] = {tq, tk, tv};
   float* segs = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + lz::kWsHeader);
+  if (!none && d.L <= (d.dtype == LIZARD_F32 ? lz::kDecayFewF32 : lz::kDecayFew)) {
+    lz::DecayStep t{};
+    t.B = d.B, t.H = d.H, t.G = G, t.L = d.L, t.dk = d.dk, t.dv = d.dv;
+    t.q = q, t.k = k, t.v = v, t.sq = rq.s, t.sk = rk.s, t.sv = rv.s;
+    t.lg = log_decay, t.sg = rg.s, t.count = count, t.h_in = h0, t.h_out = h_final;
+    t.y = y, t.sy = ry.s, t.scale = a.scale_out, t.status = a.status;
+    return finish(lz::launch_decay_step(t, d.dtype, s, &launches), launches);
+  }
   const cudaError_t e = tc_rows(d, in, 3) ? lz::launch_decay_tc(a, false, segs, s, &launches)
                                           : lz::launch_decay_f32(a, d.dtype, segs, s, &launches);
   return finish(e, launches);
@@ -306,7 +314,7 @@ lizard_status lizard_decay_attn_step(const lizard_decay_dims* dims, const void* 
   lz::DecayStep a{};
   a.B = d.B, a.H = d.H, a.G = d.H / d.Hk, a.L = d.L, a.dk = d.dk, a.dv = d.dv;
   a.q = q, a.k = k, a.v = v, a.sq = rq.s, a.sk = rk.s, a.sv = rv.s;
-  a.lg = log_decay, a.sg = rg.s, a.h = h, a.y = y, a.sy = ry.s, a.scale = scale_of(d);
+  a.lg = log_decay, a.sg = rg.s, a.h_in = a.h_out = h, a.y = y, a.sy = ry.s, a.scale = scale_of(d);
   int launches = 0;
   const cudaError_t e = lz::launch_decay_step(a, d.dtype, (cudaStream_t)stream, &launches);
   return finish(e, launches);

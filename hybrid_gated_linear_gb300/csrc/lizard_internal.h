@@ -478,11 +478,19 @@ struct DecayStep {
   Strides sq, sk, sv;
   const float* lg;
   Strides sg;
-  float* h;
+  const int32_t* count;  // or null
+  const float* h_in;     // or null: zeros
+  float* h_out;          // or null; may be h_in
   void* y;
   Strides sy;
   float scale;
+  unsigned* status;      // of a bad count
 };
+// Up to so many tokens a forward goes this way, fp32 throughout.  128 x 128, a call's time against the
+// chunks': bf16, 4 heads, 16 tokens 9.0 / 15.8 us; 16 x 32 heads, 16 tokens 37 / 108, without states 32 / 40,
+// but 62 / 40 at 32 tokens.  fp32, whose chunks are slower: 16 x 32 heads, 24 tokens 60 / 144,
+// without states 49 / 113; 4 heads of 64 x 64 without states, 24 tokens 11.0 / 11.7, 32 tokens 14.2 / 11.7.
+constexpr int kDecayFew = 16, kDecayFewF32 = 24;
 cudaError_t launch_decay_step(const DecayStep& a, lizard_dtype dt, cudaStream_t s, int* launches);
 
 struct NormCall {

@@ -589,9 +589,11 @@ lizard_status lizard_cache_attn(const lizard_cache* cache, const lizard_cache_at
  *   tokens nor change the state; their y and gradients are written as 0.
  * log_decay is <= 0 as a rule.  Minus infinity starts a new document: nothing before that token
  * is seen from it on; so does every value below -104, whose decay is 0 in fp32.  Positive values
- * are accepted as long as the products of the decays between any two tokens are finite in fp32.  NaN is not accepted, and a token or a state that is not finite
- * leaves every output of its sequence unspecified.
- * Sums and states are fp32 throughout.  bf16 calls round, for the tensor cores, the decayed scores
+ * are accepted as long as the products of the decays between any two tokens are finite in fp32.
+ * NaN is not accepted, and a token or a state that is not finite leaves every output of its
+ * sequence unspecified.
+ * Sums and states are fp32 throughout; a forward of at most 16 tokens (fp32: 24) is the recurrence,
+ * token by token, and differs from a longer one's in the last bits.  Longer bf16 calls round, for the tensor cores, the decayed scores
  * of a 128-token chunk and the state that a chunk starts from to bf16; a state that is returned
  * and the gradient of log_decay are made from unrounded (three-part) operands, so that asking for
  * them may change the last bit of the others.  fp32 calls multiply in three tf32 parts (22 bits).

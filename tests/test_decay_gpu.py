@@ -429,3 +429,32 @@ def test_two_calls_at_once():
         for pair in got[i]:
             for a, b in zip(want[i], pair):
                 assert all(torch.equal(p, q) for p, q in zip(a, b))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("L", [1, 7, 15, 16, 17, 24, 25])
+def test_a_few_tokens(dtype, L):
+    """Short forwards take the single tokens' kernel: counts, documents, states, and the step's own result."""
+    x = In(4, 6, 2, L, 128, 64, dtype, order="blhd", seed=11)
+    x.g[1, 2, L // 2] = -INF
+    x.g[2, 0, 0] = -INF
+    whole = x.check_fwd()
+    if L <= (16 if dtype == "bf16" else 24):  # token for token the same sums
+        h, y = x.h0.clone(), torch.full_like(whole[0], 9.0)
+        lz.lizard_decay_attn_step(x.dims, x.q, x.k, x.v, x.g, h, y)
+        assert torch.equal(y, whole[0]) and torch.equal(h, whole[1])
+    x.check_fwd(final=False)
+    x.count = [L, 0, (L + 1) // 2, L - 1]
+    clean = x.fwd()
+    for b, c in enumerate(x.count):
+        for t in (x.q, x.k, x.v):
+            t[b, :, c:] = float("nan")
+        x.g[b, :, c:] = float("nan")
+    assert all(torch.equal(p, q) for p, q in zip(clean, x.check_fwd()))
+    assert all((clean[0][b, :, c:] == 0).all() for b, c in enumerate(x.count)) and torch.equal(clean[1][1], x.h0[1])
+    for bad in (-1, L + 1):
+        x.count[0] = bad
+        y, h = x.fwd(status=5)
+        assert (y[0] == 0).all() and torch.equal(h[0], x.h0[0])
+        assert torch.equal(y[1:], clean[0][1:]) and torch.equal(h[1:], clean[1][1:])
+    In(2, 4, 4, L, 64, 128, dtype, state=False, seed=12).check_fwd()
