@@ -72,7 +72,7 @@ struct Head {  // in front of the tiles
   Ctl<NB> ctl;
   Factors f[2];
 };
-constexpr int kHead = 3072;
+constexpr int kHead = 3 * 1024;
 static_assert(sizeof(Head) <= kHead, "barriers and factors");
 
 template <int DA, int NPH>
