@@ -5,8 +5,9 @@
 // TPR threads, 16 channels each, from its one read to its one write: the mean is summed first, the
 // variance around it second, both from registers, so that a large mean costs no digits and the
 // backward needs nothing but x.  Forward, 2 x 32 x 4096 rows of 128 in bf16: 27 us, 5.0 TB/s, 75% of the copy
-// rate (the arithmetic of a row and its start); backward 37 us, 80%; 8191 rows of 4096 backward 55 us, 54%
-// (three sums over eight warps a row).  Arithmetic on pairs and row indices by addition: 72 -> 55 us there.
+// rate (the arithmetic of a row and its start); backward 33 us, 89%; 8191 rows of 4096 backward 47 us, 63%
+// (two turns of sums over eight warps a row).  There arithmetic on pairs and row indices by addition made it
+// 72 -> 55 us, two turns of sums instead of three 54.6, one round of blocks 47.
 #include "lizard_dev.cuh"
 #include "lizard_internal.h"
 
@@ -218,7 +219,7 @@ __global__ void __launch_bounds__(TPR > kBlock ? TPR : kBlock) norm_bwd_kernel(N
   using R = Ring<T, THREADS>;
   // the ring; then [warps][2][d] sums for rows within a warp, [RPB][2][d] for wider ones
   extern __shared__ __align__(16) uint4 ring[];
-  __shared__ float part[128], part2[128];
+  __shared__ float part[128];
   pdl_wait();
   const int lane = threadIdx.x % TPR;
   const T* xs = static_cast<const T*>(a.x);
@@ -281,22 +282,34 @@ __global__ void __launch_bounds__(TPR > kBlock ? TPR : kBlock) norm_bwd_kernel(N
     unpack(g, dy);
     fetch(r + R::D * step, stage);  // (below 2^32: rows are below 2^31, a step below 2^16)
     stage = stage + 1 == R::D ? 0 : stage + 1;
-    const float2 rs = both(centre<T, TPR>(x, lane, a.d, a.eps, inv_d, part));
+    // two sums in one turn: of x and a, then, around the mean, of x^2 and a x
     float2 s0 = both(0.f), s1 = both(0.f);
+#pragma unroll
+    for (int e = 0; e < kP; ++e) {
+      s0 = f2_add(s0, x[e]);
+      s1 = f2_fma(dy[e], w[e], s1);
+    }
+    float s[2] = {s0.x + s0.y, s1.x + s1.y};
+    row_sum<TPR>(s, part, 0);
+    const float2 minus = both(-s[0] * inv_d), m0 = both(-s[1] * inv_d);
+    s0 = s1 = both(0.f);
+#pragma unroll
+    for (int e = 0; e < kP; ++e) {
+      x[e] = inside<T, TPR>(lane, a.d, 2 * e) ? f2_add(x[e], minus) : both(0.f);
+      s0 = f2_fma(x[e], x[e], s0);
+      s1 = f2_fma(f2_mul(dy[e], w[e]), x[e], s1);
+    }
+    s[0] = s0.x + s0.y, s[1] = s1.x + s1.y;
+    row_sum<TPR>(s, part, 1);
+    const float r1 = rsqrtf(fmaf(s[0], inv_d, a.eps));
+    const float2 rs = both(r1), m1 = both(-s[1] * r1 * inv_d);
 #pragma unroll
     for (int e = 0; e < kP; ++e) {
       x[e] = f2_mul(x[e], rs);
       db[e] = f2_add(db[e], dy[e]);
       dw[e] = f2_fma(dy[e], x[e], dw[e]);
-      dy[e] = f2_mul(dy[e], w[e]);
-      s0 = f2_add(s0, dy[e]);
-      s1 = f2_fma(dy[e], x[e], s1);
+      x[e] = f2_mul(rs, f2_fma(x[e], m1, f2_fma(dy[e], w[e], m0)));
     }
-    float s[2] = {s0.x + s0.y, s1.x + s1.y};
-    row_sum<TPR>(s, part2, 0);
-    const float2 m0 = both(-s[0] * inv_d), m1 = both(-s[1] * inv_d);
-#pragma unroll
-    for (int e = 0; e < kP; ++e) x[e] = f2_mul(rs, f2_fma(x[e], m1, f2_add(dy[e], m0)));
     Frag<T> o;
     pack(x, o);
     if (live && a.y) store<T, TPR>(static_cast<T*>(a.y) + offset(a.sy, at(here)), lane, a.d, o);
@@ -368,12 +381,13 @@ int rows_per_block(int d) {
   const int t = threads_per_row(d);
   return t >= kBlock ? 1 : kBlock / t;
 }
-// Blocks that share the rows of one set of weights in the backward: about one wave of four blocks
-// an SM over all sets.  (152 SMs: written down, so that the workspace does not ask for a device.)
+// Blocks that share the rows of one set of weights in the backward: one round of the blocks that SMs
+// hold, over all sets; a second round costs more than it fills (two rounds, then one: 32 heads' rows of 128
+// 36.1 / 33.3 us, 8191 rows of 4096 55.0 / 47.3, 4096 rows of 8192 62 / 54).  (152 SMs: written down, so that the workspace does not ask for a device.)
 int bwd_blocks(int64_t rows, int sets, int d) {
   const int64_t most = (rows + rows_per_block(d) - 1) / rows_per_block(d);
-  const int per_sm = threads_per_row(d) > kBlock ? 2 : 4;
-  int64_t n = ((int64_t)152 * per_sm + sets - 1) / sets;
+  const int per_sm = threads_per_row(d) > kBlock ? 1 : 2;  // what an SM holds at 128 registers
+  int64_t n = (int64_t)152 * per_sm / sets;
   n = n < most ? n : most;
   return (int)(n < 1 ? 1 : n);
 }
