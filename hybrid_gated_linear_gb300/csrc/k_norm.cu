@@ -5,7 +5,7 @@
 // TPR threads, 16 channels each, from its one read to its one write: the mean is summed first, the
 // variance around it second, both from registers, so that a large mean costs no digits and the
 // backward needs nothing but x.  Forward, 2 x 32 x 4096 rows of 128 in bf16: 27 us, 5.0 TB/s, 75% of the copy
-// rate (the arithmetic of a row and its start); backward 33 us, 89%; 8191 rows of 4096 backward 47 us, 63%
+// rate (the arithmetic of a row and its start); backward 35 us, 85%; 8191 rows of 4096 backward 47 us, 63%
 // (two turns of sums over eight warps a row).  There arithmetic on pairs and row indices by addition made it
 // 72 -> 55 us, two turns of sums instead of three 54.6, one round of blocks 47.
 #include "lizard_dev.cuh"
