@@ -48,25 +48,28 @@ Decays decays_of(const lizard_strides* s, int64_t B, int64_t H, int64_t L) {
 
 // Scratch of a backward call after the header.
 struct BwdScratch {
-  size_t dots, parts, d_h0, segs, sums, bytes;  // offsets, then the size
+  size_t dots, parts, edge, through, segs, bytes;  // offsets, then the size
 };
 size_t seg_bytes(const lizard_decay_dims& d, int da, int dc) {
   const size_t n = lz::decay_f32_workspace(d.B, d.H, d.L, da, dc);
   return lz::align_up(d.dtype == LIZARD_BF16 ? std::max(n, lz::decay_tc_workspace(d.B, d.H, d.L, da, dc)) : n, 256);
 }
 // Planes of [B,H,L] sums for d log_decay: within chunks, and with the states (the tensor-core pass
-// leaves two for each 64 channels), of the rows and of the columns.
+// leaves two for each 64 channels), of the rows and of the columns.  States that enter chunks: of 64 tokens,
+// as the pass takes them that any strides can go to.
 size_t in_planes(const lizard_decay_dims& d) { return d.dk / lz::kDecaySlice; }
 size_t out_planes(const lizard_decay_dims& d) { return 2 * in_planes(d); }
+size_t edge_parts(const lizard_decay_dims& d) { return lz::kDecayEdgeWarps * in_planes(d); }
 BwdScratch bwd_scratch(const lizard_decay_dims& d) {
   BwdScratch w;
   const size_t rows = (size_t)d.B * d.H * d.L;
+  const size_t chunks = (size_t)d.B * d.H * ((d.L + lz::kDecayChunk - 1) / lz::kDecayChunk);
   size_t at = 0;
-  w.dots = at, at += lz::align_up(2 * (in_planes(d) + out_planes(d)) * rows * sizeof(float), 256);
+  w.dots = at, at += lz::align_up((in_planes(d) + 2 * out_planes(d)) * rows * sizeof(float), 256);
   w.parts = at, at += d.H > d.Hk ? lz::align_up(rows * (d.dk > d.dv ? d.dk : d.dv) * sizeof(float), 256) : 0;
-  w.d_h0 = at, at += (size_t)d.B * d.H * d.dk * d.dv * sizeof(float);  // a multiple of 16 KB
+  w.edge = at, at += chunks * d.dk * d.dv * sizeof(float);  // a multiple of 16 KB
+  w.through = at, at += lz::align_up(chunks * edge_parts(d) * sizeof(float), 256);
   w.segs = at, at += std::max(seg_bytes(d, d.dk, d.dv), seg_bytes(d, d.dv, d.dk));
-  w.sums = at, at += lz::decay_gate_workspace(d.B, d.H, d.L, lz::kDecayChunk);
   w.bytes = at;
   return w;
 }
@@ -211,13 +214,12 @@ lizard_status lizard_decay_attn_bwd(const lizard_decay_dims* dims, const void* q
   unsigned char* ws = static_cast<unsigned char*>(workspace) + lz::kWsHeader;
   const size_t plane = (size_t)d.B * d.H * d.L;
   float* dots = reinterpret_cast<float*>(ws + w.dots);
-  float *row_in = dots, *col_in = row_in + in_planes(d) * plane, *row_out = col_in + in_planes(d) * plane,
-        *col_out = row_out + out_planes(d) * plane;
+  float *inside = dots, *row_out = inside + in_planes(d) * plane, *col_out = row_out + out_planes(d) * plane;
+  float *edge = reinterpret_cast<float*>(ws + w.edge), *through = reinterpret_cast<float*>(ws + w.through);
   float* segs = reinterpret_cast<float*>(ws + w.segs);
   float* part = reinterpret_cast<float*>(ws + w.parts);
   const cudaStream_t s = (cudaStream_t)stream;
   const bool gate = d_log_decay && !none;
-  if (!d_h0 && h0 && gate) d_h0 = reinterpret_cast<float*>(ws + w.d_h0);
   const bool tc = tc_rows(d, in, 4);
   int launches = 0;
   // the gradient of log_decay takes the products with the states as results: from exact states
@@ -248,7 +250,7 @@ lizard_status lizard_decay_attn_bwd(const lizard_decay_dims* dims, const void* q
   b.scale_out = 1.f, b.scale_in = scale;
   const lz::Strides heads_k{(int64_t)d.H * d.L * d.dk, (int64_t)d.L * d.dk, d.dk};
   b.out = G > 1 ? static_cast<void*>(part) : d_k, b.so = G > 1 ? heads_k : ok.s, b.out_f32 = G > 1;
-  if (gate) b.x = k, b.sx = rk.s, b.gx = G, b.dot_in = col_in, b.dot_out = col_out;
+  if (gate) b.x = k, b.sx = rk.s, b.gx = G, b.dot_out = col_out, b.edge = edge;
   e = pass(b);
   if (e == cudaSuccess && G > 1)
     e = lz::launch_decay_heads(d.B, d.Hk, G, d.L, d.dk, part, d_k, ok.s, d.dtype, s, &launches);
@@ -260,7 +262,7 @@ lizard_status lizard_decay_attn_bwd(const lizard_decay_dims* dims, const void* q
   b.init = h0, b.state_t = true;
   b.scale_out = scale, b.scale_in = 1.f;
   b.out = d_q, b.so = oq.s;
-  if (gate) b.x = q, b.sx = rq.s, b.gx = 1, b.dot_in = row_in, b.dot_out = row_out;
+  if (gate) b.x = q, b.sx = rq.s, b.gx = 1, b.dot_in = inside, b.dot_out = row_out, b.edge = edge, b.through = through;
   e = pass(b);
   if (e != cudaSuccess || !gate) return finish(e, launches);
   if (tc) {
@@ -268,17 +270,16 @@ lizard_status lizard_decay_attn_bwd(const lizard_decay_dims* dims, const void* q
     pr.B = d.B, pr.H = d.H, pr.G = G, pr.L = d.L, pr.dk = d.dk, pr.dv = d.dv;
     pr.q = q, pr.k = k, pr.v = v, pr.dy = dy, pr.sq = rq.s, pr.sk = rk.s, pr.sv = rv.s, pr.sy = ry.s;
     pr.lg = log_decay, pr.sg = rg.s, pr.count = count, pr.scale = scale;
-    pr.diff = row_in, pr.status = a.status;
+    pr.inside = inside, pr.status = a.status;
     e = lz::launch_decay_pairs(pr, s, &launches);
     if (e != cudaSuccess) return finish(e, launches);
   }
   lz::DecayGate g{};
   g.B = d.B, g.H = d.H, g.L = d.L, g.chunk = tc ? lz::kDecayTile : lz::kDecayChunk;
   g.in_slices = tc ? 1 : (int)in_planes(d), g.out_slices = (int)(tc ? out_planes(d) : in_planes(d));
-  g.row_in = row_in, g.col_in = tc ? nullptr : col_in, g.row_out = row_out, g.col_out = col_out;
-  g.h0 = h0, g.d_h0 = d_h0, g.state = d.dk * d.dv;
-  g.lg = log_decay, g.sg = rg.s, g.count = count, g.d_lg = d_log_decay;
-  g.sums = reinterpret_cast<double2*>(ws + w.sums);
+  g.parts = (int)edge_parts(d);
+  g.inside = inside, g.row_out = row_out, g.col_out = col_out, g.through = through;
+  g.count = count, g.d_lg = d_log_decay;
   e = lz::launch_decay_gate(g, s, &launches);
   return finish(e, launches);
 }

@@ -31,7 +31,8 @@ struct Smem {
   int doc[kC];             // documents begun up to each token
   float in[kC], out[kC];   // decays from before the chunk to each token, from each token to the end
   float diag[kC];          // the scores of the tokens themselves
-  float dots[2][2][kC];    // of a row: [within the chunk, with the state][half of the channels]
+  float dots[2][kC];       // of a row with the state: [half of the channels]
+  float cols[4][kC], rows[kC];  // the products that pass over a token: see pass_over
   float all;               // decay of the whole chunk
 };
 
@@ -139,9 +140,66 @@ __device__ __forceinline__ void join_small(float (&d)[NT][4], float (&small)[NT]
     for (int e = 0; e < 4; ++e) d[n][e] += small[n][e], small[n][e] = 0.f;
 }
 
+// The products W_is of a chunk's rows i and columns s < i that pass over each token t, s < t <= i, summed from
+// W in the scores' layout: E_it = sum_{s < t} W_is by running sums along the 32 columns of a warp, of which the
+// rows from t on are added up into cols[rows / 16][t]; rows[i] keeps the sum over the first 32 columns, which
+// all of the others have before them.  No product on one side of t enters, not even to be taken off again.
+template <int DA>
+__device__ __forceinline__ void pass_over(Smem<DA>& m, float (&w)[4][4], int r0, int n0) {
+  const int lane = threadIdx.x & 31, gr = lane >> 2, cq = 2 * (lane & 3);
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const int o = r0 + gr + 8 * q;
+    float run = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float w0 = w[e][2 * q], pair = w0 + w[e][2 * q + 1];
+      float to = pair;  // with the lanes before
+#pragma unroll
+      for (int k = 1; k < 4; k <<= 1) {
+        const float u = __shfl_up_sync(0xffffffffu, to, k, 4);
+        if ((lane & 3) >= k) to += u;
+      }
+      float before = __shfl_up_sync(0xffffffffu, to, 1, 4);
+      if ((lane & 3) == 0) before = 0.f;
+      before += run;
+      const int t = n0 + 8 * e + cq;
+      w[e][2 * q] = o >= t ? before : 0.f;
+      w[e][2 * q + 1] = o > t ? before + w0 : 0.f;
+      run += __shfl_sync(0xffffffffu, to, 3, 4);
+    }
+    if (n0 == 0 && (lane & 3) == 0) m.rows[o] = run;
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      float c = w[e][b] + w[e][2 + b];
+#pragma unroll
+      for (int k = 4; k < 32; k <<= 1) c += __shfl_xor_sync(0xffffffffu, c, k);
+      if (gr == 0) m.cols[r0 >> 4][n0 + 8 * e + cq + b] = c;
+    }
+}
+// Two warps, behind a barrier: the sum of token t.
+template <int DA>
+__device__ __forceinline__ float passed(const Smem<DA>& m, int t) {
+  float d = 0.f;
+  if (t >= 32) {  // the first 32 columns of the rows from t on
+    d = m.rows[t];
+#pragma unroll
+    for (int k = 1; k < 32; k <<= 1) {
+      const float u = __shfl_down_sync(0xffffffffu, d, k);
+      if ((t & 31) + k < 32) d += u;
+    }
+  }
+  for (int r = t >> 4; r < 4; ++r) d += m.cols[r][t];
+  return d;
+}
+
 // Warp w of eight: rows 16 (w mod 4) .. of the chunk's 64, columns 32 (w / 4) .. of 64; of the state the rows
 // DA / 4 (w mod 4) ...  A lane's results of tile n: rows g, g + 8, columns 8 n + 2 c, + 1.
-template <typename T, int DA>
+// GATE: the passes that the gradient of log_decay is made from (a.x is there).
+template <typename T, int DA, bool GATE>
 __global__ void __launch_bounds__(kThreads) decay_f32_kernel(DecayPass a, DecaySegs g) {
   extern __shared__ __align__(16) unsigned char raw[];
   Smem<DA>& m = *reinterpret_cast<Smem<DA>*>(raw);
@@ -161,7 +219,8 @@ __global__ void __launch_bounds__(kThreads) decay_f32_kernel(DecayPass a, DecayS
   const T* pa = static_cast<const T*>(a.a) + n * a.sa.n + h / a.ga * a.sa.h;
   const T* pb = static_cast<const T*>(a.b) + n * a.sb.n + h / a.gb * a.sb.h;
   const T* pc = static_cast<const T*>(a.c) + n * a.sc.n + h / a.gc * a.sc.h + c0;
-  const T* px = a.x ? static_cast<const T*>(a.x) + n * a.sx.n + h / a.gx * a.sx.h + c0 : nullptr;
+  const T* px = GATE ? static_cast<const T*>(a.x) + n * a.sx.n + h / a.gx * a.sx.h + c0 : nullptr;
+  const int edges = (a.L + kC - 1) / kC;  // chunks of the axis, each with a state that enters it
   const float* lg = a.lg + n * a.sg.n + h * a.sg.h;
   const int64_t so = n * a.so.n + h * a.so.h + c0;
   auto put = [&](int t, int col, float4 v) {
@@ -220,7 +279,23 @@ __global__ void __launch_bounds__(kThreads) decay_f32_kernel(DecayPass a, DecayS
               d = tc::ex2_approx((m.hi[late] - m.hi[early]) + (m.lo[late] - m.lo[early]));
             m.s[o][s] = d > 0.f ? acc[e][q] * a.scale_in * d : 0.f;
             if (o == s) m.diag[o] = acc[e][q] * a.scale_in;
+            acc[e][q] = d > 0.f ? acc[e][q] * a.scale_in * d : 0.f;
           }
+        if (GATE && a.dot_in) {
+          // times this CTA's channels of x_o . c_s
+          float xc[4][4] = {};
+#pragma unroll 2
+          for (int k = 0; k < kDc; k += 8)
+            step8(xc, small,
+                  [&](int r, int c) { return t0 + r0 + r < count ? ld_f(px + (int64_t)(t0 + r0 + r) * a.sx.t + k + c) : 0.f; },
+                  [&](int r, int c, int) { return m.c[n0 + r][k + c]; });
+          join_small(xc, small);
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) acc[e][q] *= xc[e][q];
+          pass_over(m, acc, r0, n0);
+        }
       }
       __syncthreads();
       // out = scores c + decay a^T H
@@ -237,7 +312,7 @@ __global__ void __launch_bounds__(kThreads) decay_f32_kernel(DecayPass a, DecayS
           step8(st, small, [&](int r, int c) { return m.a[r0 + r][k + c]; }, [&](int r, int c, int) { return m.h[k + c][n0 + r]; });
         join_small(st, small);
       }
-      float dot[2][2] = {};  // [row][within, with the state]
+      float dot[2] = {};  // of a row, with the state
       float2 y[4][2];
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
@@ -251,7 +326,7 @@ __global__ void __launch_bounds__(kThreads) decay_f32_kernel(DecayPass a, DecayS
           const int col = n0 + 8 * k + cq;
           const float2 cd = *reinterpret_cast<const float2*>(&m.c[o][col]);
           y[k][q] = make_float2(a.scale_out * (fmaf(dg, cd.x, u.x) + w.x), a.scale_out * (fmaf(dg, cd.y, u.y) + w.y));
-          if (px && t < count) {
+          if (GATE && t < count) {
             float x0, x1;
             if (sizeof(T) == 4) {
               const float2 v = *reinterpret_cast<const float2*>(px + t * a.sx.t + col);
@@ -260,25 +335,25 @@ __global__ void __launch_bounds__(kThreads) decay_f32_kernel(DecayPass a, DecayS
               const uint32_t v = *reinterpret_cast<const uint32_t*>(px + t * a.sx.t + col);
               x0 = __uint_as_float(v << 16), x1 = __uint_as_float(v & 0xffff0000u);
             }
-            dot[q][0] += x0 * u.x + x1 * u.y;
-            dot[q][1] += x0 * w.x + x1 * w.y;
+            dot[q] += x0 * w.x + x1 * w.y;
           }
         }
       }
-      if (px) {
+      if (GATE) {
 #pragma unroll
-        for (int q = 0; q < 2; ++q)
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            dot[q][k] += __shfl_xor_sync(0xffffffffu, dot[q][k], 1);
-            dot[q][k] += __shfl_xor_sync(0xffffffffu, dot[q][k], 2);
-            if ((lane & 3) == 0) m.dots[k][warp >> 2][r0 + gr + 8 * q] = dot[q][k];
-          }
+        for (int q = 0; q < 2; ++q) {
+          dot[q] += __shfl_xor_sync(0xffffffffu, dot[q], 1);
+          dot[q] += __shfl_xor_sync(0xffffffffu, dot[q], 2);
+          if ((lane & 3) == 0) m.dots[warp >> 2][r0 + gr + 8 * q] = dot[q];
+        }
       }
       __syncthreads();  // the scores and H have been read
-      if (px && tid < 2 * kC) {
-        const int k = tid / kC, o = tid - k * kC;
-        if (t0 + o < count) (k ? a.dot_out : a.dot_in)[dot0 + t0 + o] = a.scale_out * (m.dots[k][0][o] + m.dots[k][1][o]);
+      if (GATE && tid < kC) {
+        if (t0 + tid < count) a.dot_out[dot0 + t0 + tid] = a.scale_out * (m.dots[0][tid] + m.dots[1][tid]);
+      } else if (GATE && tid < 2 * kC && a.dot_in) {
+        const int o = tid - kC;
+        const float d = passed(m, o);
+        if (t0 + o < count) a.dot_in[dot0 + t0 + o] = a.scale_out * d;
       }
       // the rows of out through the scores' place
 #pragma unroll
@@ -288,6 +363,10 @@ __global__ void __launch_bounds__(kThreads) decay_f32_kernel(DecayPass a, DecayS
     }
     // H <- decay H + sum_s decay_s b_s c_s^T
     const float all = m.all;
+    float over = 0.f;  // <H, the state that enters from the other side>, where that was kept
+    float2* edge = GATE ? reinterpret_cast<float2*>(a.edge) +
+                              (((int64_t)unit * edges + t0 / kC) * slices + slice) * (DA * kDc / 2) + tid
+                        : nullptr;
 #pragma unroll 1
     for (int r = 0; r < MT; ++r) {
       float u[4][4] = {}, small[4][4] = {};
@@ -305,9 +384,23 @@ __global__ void __launch_bounds__(kThreads) decay_f32_kernel(DecayPass a, DecayS
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
           float2* at = reinterpret_cast<float2*>(&m.h[h0 + 16 * r + gr + 8 * q][n0 + 8 * k + cq]);
+          if (GATE) {
+            float2* kept = edge + ((r * 4 + k) * 2 + q) * kThreads;
+            if (a.through) {
+              const float2 v = *kept;
+              over = fmaf(at->x, v.x, fmaf(at->y, v.y, over));
+            } else {
+              *kept = *at;
+            }
+          }
           const float2 x = all > 0.f ? *at : make_float2(0.f, 0.f);
           *at = make_float2(fmaf(all, x.x, u[k][2 * q]), fmaf(all, x.y, u[k][2 * q + 1]));
         }
+    }
+    if (GATE && a.through) {
+      over = warp_sum(over);
+      if (lane == 0)
+        a.through[(((int64_t)unit * edges + t0 / kC) * slices + slice) * kDecayEdgeWarps + warp] = all > 0.f ? all * over : 0.f;
     }
     __syncthreads();
     if (!g.states_only) {
@@ -384,24 +477,15 @@ __global__ void __launch_bounds__(kThreads) decay_heads_kernel(int Hk, int G, in
   st4(out + n * so.n + h * so.h + t * so.t + c, s);
 }
 
-// d log_decay_t = g_t <h_{t-1}, dh_t>: the sum of all products that pass over token t.  With, for
-// each token, what it receives from (rows) and gives to (cols) other tokens of its chunk and the
-// states at the chunk's ends,
-//   = sum_{i >= t} row_in_i - sum_{j >= t} col_in_j        within the chunk (t's own pair cancels)
-//   + sum_{i >= t} row_out_i + sum_{j < t} col_out_j       between the chunk and what lies around it
-//   + through                                              from before the chunk to after it.
-// `through` of the chunks follows from the pairs over the edge before the first one, <h0, d_h0>:
-//   edge after = through + sum col_out,  through = edge before - sum row_out  (0 where a document
-// starts in the chunk).  Sums over chunks run in 64 bits, within 32 tokens in trees of fp32 (64-bit
-// additions are what this GPU has least of: with them throughout, 49 us against 25 for 64 heads x 4096
-// tokens).  First a warp for each chunk takes its sums of row_out
-// and col_out and whether a document starts, and a block for each head <h0, d_h0>; then a warp for
-// each chunk adds up the edge in front of it and writes its tokens.
-__device__ __forceinline__ double warp_sum64(double x) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  return x;
-}
+// d log_decay_t = g_t <h_{t-1}, dh_t>: the sum of all products that pass over token t,
+//   inside_t                         between two tokens of its chunk
+//   + sum_{i >= t} row_out_i         from the state before the chunk to its tokens
+//   + sum_{j < t} col_out_j          from its tokens to the state behind it
+//   + through                        from before the chunk to behind it.
+// Each sum holds what passes over t and nothing else, and `through` comes from the states themselves, so the
+// rounding of products that do not reach t stays out, however large they are (a running sum of all rows less
+// all columns would carry it on behind them, where they have decayed to nothing).  A start of a document makes
+// every product over it exactly 0.  A warp for each chunk: its sums over 32 tokens in trees of fp32.
 __device__ __forceinline__ int gate_count(const DecayGate& a, int n) {
   const int c = a.count ? a.count[n] : a.L;
   return c < 0 || c > a.L ? 0 : c;
@@ -409,121 +493,71 @@ __device__ __forceinline__ int gate_count(const DecayGate& a, int n) {
 
 constexpr int kGateWarps = 4;
 // IN, OUT: planes; all of a chunk's numbers are on their way together.
-// sums [units][chunks + 1]: of the chunks (x: rows, y: cols; a start as rows = NaN), then <h0, d_h0>
-template <int OUT>
-__global__ void __launch_bounds__(32 * kGateWarps) decay_gate_sums_kernel(DecayGate a, int chunks) {
-  pdl_wait();
-  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
-  const int units = a.B * a.H, per = (chunks + kGateWarps - 1) / kGateWarps;
-  if (blockIdx.x < units) {
-    double s = 0.0;
-    if (a.h0) {
-      const float4* x = reinterpret_cast<const float4*>(a.h0 + (int64_t)blockIdx.x * a.state);
-      const float4* y = reinterpret_cast<const float4*>(a.d_h0 + (int64_t)blockIdx.x * a.state);
-#pragma unroll 4
-      for (int i = threadIdx.x; i < a.state / 4; i += 32 * kGateWarps) {
-        const float4 u = x[i], v = y[i];
-        s += (double)(u.x * v.x) + (double)(u.y * v.y) + (double)(u.z * v.z) + (double)(u.w * v.w);
-      }
-    }
-    __shared__ double part[kGateWarps];
-    s = warp_sum64(s);
-    if (lane == 0) part[warp] = s;
-    __syncthreads();
-    s = 0.0;
-    for (int w = 0; w < kGateWarps; ++w) s += part[w];
-    if (threadIdx.x == 0) a.sums[(int64_t)blockIdx.x * (chunks + 1) + chunks] = make_double2(s, 0.0);
-    return;
-  }
-  const int unit = (blockIdx.x - units) / per, c = (blockIdx.x - units - unit * per) * kGateWarps + warp;
-  const int n = unit / a.H, h = unit - n * a.H;
-  const int t0 = c * a.chunk, end = min(t0 + a.chunk, gate_count(a, n));
-  if (t0 >= end) return;
-  const int64_t plane = (int64_t)units * a.L, base = (int64_t)unit * a.L;
-  const float* lg = a.lg + n * a.sg.n + h * a.sg.h;
-  float r = 0.f, c1 = 0.f;
-  bool start = false;
-#pragma unroll
-  for (int g = 0; g < kDecayTile / 32; ++g) {
-    const int t = t0 + 32 * g + lane;
-    if (t < end) {
-#pragma unroll
-      for (int s = 0; s < OUT; ++s) r += a.row_out[s * plane + base + t], c1 += a.col_out[s * plane + base + t];
-      start |= lg[t * a.sg.t] < kDecayNone;
-    }
-  }
-  const double rows = warp_sum(r), cols = warp_sum(c1);
-  start = __any_sync(0xffffffffu, start);
-  if (lane == 0) a.sums[(int64_t)unit * (chunks + 1) + c] = make_double2(start ? nan("") : rows, cols);
-}
-
 template <int IN, int OUT>
 __global__ void __launch_bounds__(32 * kGateWarps) decay_gate_kernel(DecayGate a, int chunks) {
   pdl_wait();
   const int lane = threadIdx.x % 32, per = (chunks + kGateWarps - 1) / kGateWarps;
   const int unit = blockIdx.x / per, c = (blockIdx.x - unit * per) * kGateWarps + threadIdx.x / 32;
   if (c >= chunks) return;
-  const int n = unit / a.H, h = unit - n * a.H, count = gate_count(a, n);
+  const int n = unit / a.H, count = gate_count(a, n);
   const int t0 = c * a.chunk, end = min(t0 + a.chunk, count);
   const int64_t plane = (int64_t)a.B * a.H * a.L, base = (int64_t)unit * a.L;
   for (int t = max(t0, count) + lane; t < min(t0 + a.chunk, a.L); t += 32) a.d_lg[base + t] = 0.f;
   if (t0 >= end) return;
-  // the edge in front of the chunk: 32 chunks at a time, from the last start on
-  const double2* sums = a.sums + (int64_t)unit * (chunks + 1);
-  double edge = sums[chunks].x;
-  for (int k = 0; k < c; k += 32) {
-    double2 s = make_double2(0.0, 0.0);
-    if (k + lane < c) s = sums[k + lane];
-    const unsigned starts = __ballot_sync(0xffffffffu, isnan(s.x));
-    const int last = 31 - __clz(starts);  // -1: none
-    if (starts) edge = 0.0;
-    edge += warp_sum64(lane < last ? 0.0 : lane == last ? s.y : s.y - s.x);
-  }
-  const double2 own = sums[c];
-  const double through = isnan(own.x) ? 0.0 : edge - own.x;
-  const float* lg = a.lg + n * a.sg.n + h * a.sg.h;
-  // the chunk's groups of 32 tokens: all of their numbers first, then from the last group to the first
-  // with what lies behind each
   constexpr int kG = kDecayTile / 32;
   static_assert(kDecayTile >= kDecayChunk && kDecayTile % 32 == 0, "groups of a chunk");
-  float sum[kG], col[kG];
-  unsigned cut = 0;  // a document's start: nothing passes over it
+  float in[kG], row[kG], col[kG];
 #pragma unroll
   for (int g = 0; g < kG; ++g) {
     const int t = t0 + 32 * g + lane;
-    sum[g] = col[g] = 0.f;
+    in[g] = row[g] = col[g] = 0.f;
     if (t < end) {
-      if (lg[t * a.sg.t] < kDecayNone) cut |= 1u << g;
 #pragma unroll
-      for (int s = 0; s < IN; ++s)
-        sum[g] += a.row_in[s * plane + base + t] - (a.col_in ? a.col_in[s * plane + base + t] : 0.f);
+      for (int s = 0; s < IN; ++s) in[g] += a.inside[s * plane + base + t];
 #pragma unroll
-      for (int s = 0; s < OUT; ++s)
-        sum[g] += a.row_out[s * plane + base + t], col[g] += a.col_out[s * plane + base + t];
+      for (int s = 0; s < OUT; ++s) row[g] += a.row_out[s * plane + base + t], col[g] += a.col_out[s * plane + base + t];
     }
   }
-  double behind = through, before = own.y;  // the suffix sums behind a group; col_out of the tokens before its end
+  const float part = lane < a.parts ? a.through[((int64_t)unit * chunks + c) * a.parts + lane] : 0.f;
+  const float through = warp_sum(part);
+  // rows from each token to its group's end, columns from the group's start to it
+  float before[kG];
 #pragma unroll
-  for (int g = kG - 1; g >= 0; --g) {
-    const int t = t0 + 32 * g + lane;
+  for (int g = 0; g < kG; ++g) {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const float u = __shfl_down_sync(0xffffffffu, sum[g], o), v = __shfl_down_sync(0xffffffffu, col[g], o);
-      if (lane + o < 32) sum[g] += u, col[g] += v;
+      const float u = __shfl_down_sync(0xffffffffu, row[g], o), v = __shfl_up_sync(0xffffffffu, col[g], o);
+      if (lane + o < 32) row[g] += u;
+      if (lane >= o) col[g] += v;
     }
-    if (t < end) a.d_lg[base + t] = cut >> g & 1 ? 0.f : (float)(behind + before + (double)(sum[g] - col[g]));
-    behind += __shfl_sync(0xffffffffu, sum[g], 0);
-    before -= __shfl_sync(0xffffffffu, col[g], 0);
+    before[g] = __shfl_up_sync(0xffffffffu, col[g], 1);
+    if (lane == 0) before[g] = 0.f;
   }
+#pragma unroll
+  for (int g = 0; g < kG; ++g) {
+    float d = in[g] + row[g] + before[g] + through;
+#pragma unroll
+    for (int e = 0; e < kG; ++e) {
+      if (e > g) d += __shfl_sync(0xffffffffu, row[e], 0);
+      if (e < g) d += __shfl_sync(0xffffffffu, col[e], 31);
+    }
+    const int t = t0 + 32 * g + lane;
+    if (t < end) a.d_lg[base + t] = d;
+  }
+}
+
+template <typename T, int DA, bool GATE>
+cudaError_t launch_pass(const DecayPass& a, const DecaySegs& g, int64_t blocks, cudaStream_t s) {
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_smem(decay_f32_kernel<T, DA, GATE>, sizeof(Smem<DA>), done);
+  if (e != cudaSuccess) return e;
+  if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
+  return launch_pdl(decay_f32_kernel<T, DA, GATE>, dim3((unsigned)blocks), dim3(kThreads), sizeof(Smem<DA>), s, a, g);
 }
 
 template <typename T, int DA>
 cudaError_t launch(const DecayPass& a, const DecaySegs& g, int64_t blocks, cudaStream_t s) {
-  static std::atomic<uint64_t> done{0};
-  const cudaError_t e = allow_smem(decay_f32_kernel<T, DA>, sizeof(Smem<DA>), done);
-  if (e != cudaSuccess) return e;
-  if (blocks > 0x7fffffffll) return cudaErrorInvalidValue;
-  return launch_pdl(decay_f32_kernel<T, DA>, dim3((unsigned)blocks), dim3(kThreads), sizeof(Smem<DA>), s, a, g);
+  return a.x && !g.states_only ? launch_pass<T, DA, true>(a, g, blocks, s) : launch_pass<T, DA, false>(a, g, blocks, s);
 }
 
 cudaError_t dispatch(const DecayPass& a, lizard_dtype dt, const DecaySegs& g, int64_t blocks, cudaStream_t s) {
@@ -615,20 +649,11 @@ cudaError_t launch_decay_heads(int B, int Hk, int G, int L, int d, const float* 
 
 cudaError_t launch_decay_gate(const DecayGate& a, cudaStream_t s, int* launches) {
   const int chunks = (a.L + a.chunk - 1) / a.chunk;
-  const int64_t units = (int64_t)a.B * a.H, blocks = units * ((chunks + kGateWarps - 1) / kGateWarps);
-  if (units + blocks > 0x7fffffffll) return cudaErrorInvalidValue;
-  const dim3 all((unsigned)(units + blocks)), block(32 * kGateWarps);
-  trace_begin("decay_gate_sums", s);
-  cudaError_t e = cudaErrorInvalidValue;
-  if (a.out_slices == 1) e = launch_pdl(decay_gate_sums_kernel<1>, all, block, 0, s, a, chunks);
-  if (a.out_slices == 2) e = launch_pdl(decay_gate_sums_kernel<2>, all, block, 0, s, a, chunks);
-  if (a.out_slices == 4) e = launch_pdl(decay_gate_sums_kernel<4>, all, block, 0, s, a, chunks);
-  trace_end(s);
-  ++*launches;
-  if (e != cudaSuccess) return e;
+  const int64_t blocks = (int64_t)a.B * a.H * ((chunks + kGateWarps - 1) / kGateWarps);
+  if (blocks > 0x7fffffffll || a.parts > 32) return cudaErrorInvalidValue;
+  const dim3 grid((unsigned)blocks), block(32 * kGateWarps);
   trace_begin("decay_gate", s);
-  e = cudaErrorInvalidValue;
-  const dim3 grid((unsigned)blocks);
+  cudaError_t e = cudaErrorInvalidValue;
   if (a.in_slices == 1 && a.out_slices == 1) e = launch_pdl(decay_gate_kernel<1, 1>, grid, block, 0, s, a, chunks);
   if (a.in_slices == 1 && a.out_slices == 2) e = launch_pdl(decay_gate_kernel<1, 2>, grid, block, 0, s, a, chunks);
   if (a.in_slices == 2 && a.out_slices == 2) e = launch_pdl(decay_gate_kernel<2, 2>, grid, block, 0, s, a, chunks);
@@ -636,10 +661,6 @@ cudaError_t launch_decay_gate(const DecayGate& a, cudaStream_t s, int* launches)
   trace_end(s);
   ++*launches;
   return e;
-}
-
-size_t decay_gate_workspace(int B, int H, int L, int chunk) {
-  return (size_t)B * H * ((L + chunk - 1) / chunk + 1) * sizeof(double2);
 }
 
 }  // namespace lz

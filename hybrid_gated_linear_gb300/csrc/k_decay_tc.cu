@@ -683,6 +683,32 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->bar[FACE + (it & 1)]);
       product *= all;
+      if (NPH == 3 && p.edge) {
+        // the states at the chunks' edges, for the gradient of log_decay: this thread's 8 x 4 of each, a warp's
+        // side by side (2 x 4096 tokens, 32 heads of 128: 134 MB, a pass 121 -> 137 us)
+        const int64_t at = ((int64_t)unit * ((p.L + kC - 1) / kC) + first + dir * it) * slices + slice;
+        float4* e = reinterpret_cast<float4*>(p.edge) + at * (DA * kN / 4) + 8 * half * DA + i;
+        if (p.through) {
+          // what passes over the whole chunk: decayed, <H, the state that enters from the other side>
+          float2 s2 = make_float2(0.f, 0.f);
+          if (mine) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const float4 v = e[j * DA];
+              s2 = f2_fma(make_float2(x[4 * j], x[4 * j + 1]), make_float2(v.x, v.y), s2);
+              s2 = f2_fma(make_float2(x[4 * j + 2], x[4 * j + 3]), make_float2(v.z, v.w), s2);
+            }
+          }
+          const float s = warp_sum(s2.x + s2.y);
+          if (lane == 0) p.through[at * kDecayEdgeWarps + 4 * half + qw] = all * s;
+          // the next chunk's into L2, a line a thread (the passes 366 -> 359 us)
+          if (it + 1 < num && 128 * half + i < DA * kN / 32)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<float4*>(p.edge) + (at + slices) * (DA * kN / 4) + 8 * (128 * half + i)));
+        } else if (mine) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) e[j * DA] = make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
+        }
+      }
       // H = all H + B^T C~, whose parts are added up from the smallest
       if (!(ok = wait_for(ctl, KVR + (it & 1), (it >> 1) & 1))) break;
       tc_fence_after();
@@ -803,12 +829,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ---------------------------------------------------------------------------------
-// Within a chunk: diff_i = sum_{s < i} W_is - sum_{s > i} W_si with W_is = scale (q_i . k_s) D (dy_i . v_s), from
-// exact products of the bf16 rows in fp32 sums.  Two CTAs an SM, each chunk after chunk: the two scores by
+// Within a chunk: inside_t = sum_{s < t <= i} W_is, W_is = scale (q_i . k_s) D (dy_i . v_s), from exact products
+// of the bf16 rows in fp32 sums: of those products alone that pass over t, since a difference of whole rows
+// and columns would leave the rounding of all others.  Two CTAs an SM, each chunk after chunk: the two scores by
 // MMAs (dy takes q's place in shared memory once the first is done; the next chunk's rows come while this
-// one's are summed), then eight warps of which each has every other 32 columns of its 32 rows: a thread sums
-// its row, and the 32 columns are summed over the warp by halving exchanges.  (64 heads x 4096 tokens of 128:
-// a CTA a chunk 62 us, this 50.)
+// one's are summed), then eight warps of which each has every other 32 columns of its 32 rows: a thread makes
+// the running sums of its row, E_it = sum_{s < t} W_is from the 32 columns' first on, and those of the rows
+// from t on are summed over the warp by halving exchanges.  The last step adds, for the columns of a group, the
+// whole groups before it: of the rows of later groups as one number each (all), of its own rows those from t on
+// (rows).  (64 heads x 4096 tokens of 128: 55 us; with whole rows and columns 52, and a CTA a chunk 62.)
 // ---------------------------------------------------------------------------------
 constexpr int kPairThreads = 384;
 enum { GQ = 0, GY, GS, GP, GR, GF = 5, GE = 7, GN = 9 };  // GF, GE: by parity
@@ -822,14 +851,16 @@ struct PairParams {
   Strides sg;
   const int32_t* count;
   float scale;
-  float* diff;  // [B,H,L]
+  float* inside;  // [B,H,L]
   unsigned* status;
 };
 struct alignas(16) PairHead {
   Ctl<GN> ctl;
   Factors f[2];
   float x[2][kC];
-  float rows[2][2][kC], cols[2][4][kC];  // [parity][half of the columns, or quarter of the rows]
+  // [parity][half of the columns, or quarter of the rows]
+  float rows[2][2][kC], cols[2][4][kC];
+  float all[2][4][4];  // [parity][quarter of the rows][of the columns, before the rows' own]
 };
 template <int DK, int DV>
 struct PairSmem {
@@ -1009,26 +1040,40 @@ __global__ void __launch_bounds__(kPairThreads, 2)
         tmem_ld_wait();
 #pragma unroll
         for (int j = 0; j < 32; ++j) z[j] = z[j] != 0.f && there ? z[j] * f32(s[j]) : 0.f;
+        float run = 0.f;
         tmem_ld32(tl + 128 + 32 * g, s);
         tmem_ld_wait();
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
           // (rows behind the sequence may hold anything, and a decay of 0 hides a token)
-          z[j] = z[j] != 0.f ? z[j] * f32(s[j]) : 0.f;
-          sum += z[j];
+          const float w1 = z[j] != 0.f ? z[j] * f32(s[j]) : 0.f;
+          z[j] = g < qw || j <= lane ? run : 0.f;
+          run += w1;
         }
         hd.cols[par][qw][32 * g + lane] = column_sums(z);
+        if (g < qw) {
+          sum += run;
+          run = warp_sum(run);
+          if (lane == 0) hd.all[par][qw][g] = run;
+        }
       }
       hd.rows[par][half][o] = sum;
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->bar[GE + par]), mbar_arrive(&ctl->bar[GR]);
       if (!(ok = wait_warp(ctl, GR, it & 1))) break;
-      const int t = tid - 128;
-      if (t < kC && i.t0 + t < i.count) {
-        float d = hd.rows[par][0][t] + hd.rows[par][1][t], c = 0.f;
-        for (int r = t >> 5; r < 4; ++r) c += hd.cols[par][r][t];
-        p.diff[(int64_t)i.unit * p.L + i.t0 + t] = p.scale * (d - c);
+      if (half == 0) {  // thread o is token o
+        float d = hd.rows[par][0][o] + hd.rows[par][1][o];
+#pragma unroll
+        for (int k = 1; k < 32; k <<= 1) {
+          const float u = __shfl_down_sync(0xffffffffu, d, k);
+          if (lane + k < 32) d += u;
+        }
+        for (int r = qw; r < 4; ++r) {
+          d += hd.cols[par][r][o];
+          for (int g = 0; g < qw && r > qw; ++g) d += hd.all[par][r][g];
+        }
+        if (there) p.inside[(int64_t)i.unit * p.L + i.t0 + o] = p.scale * d;
       }
       ++it;
     }
@@ -1139,7 +1184,7 @@ cudaError_t launch_decay_pairs(const DecayPairs& a, cudaStream_t s, int* launche
       !rows_map(&m.y, a.dy, a.B, a.H, a.L, a.dv, a.sy, &p.yn, &p.yh))
     return cudaErrorInvalidValue;
   p.B = a.B, p.H = a.H, p.L = a.L, p.G = a.G, p.lg = a.lg, p.sg = a.sg, p.count = a.count, p.scale = a.scale;
-  p.diff = a.diff, p.status = a.status;
+  p.inside = a.inside, p.status = a.status;
   trace_begin("decay_pairs", s);
   cudaError_t e;
   if (a.dk == 64)

@@ -400,12 +400,15 @@ struct DecayPass {
   void* out;
   Strides so;
   bool out_f32;            // out is fp32 whatever the dtype
-  // The gradient of log_decay: x rows [.,dc] whose products with out are summed per token, split in
-  // what comes from other tokens of the same chunk and what comes from the state; or null.
+  // The gradient of log_decay: x rows [.,dc], or null.  Their products with what out has from the state that
+  // enters the chunk are summed per token (dot_out).  The reversed pass keeps the states that enter its chunks
+  // (edge), the forward pass multiplies them with its own (through), each thread what the same thread of the
+  // other pass left, and sums the products (x_i . c_s) of the scores that pass over each token (dot_in).
   const void* x;
   Strides sx;
   int gx;
-  float *dot_in, *dot_out;  // [slices][B,H,L]
+  float *dot_in, *dot_out;  // [planes][B,H,L]; dot_in: of the fp32 forward pass, else null
+  float *edge, *through;    // [B,H,chunks][da,dc], [B,H,chunks][8 dc / 64]; through: of the forward pass, else null
   float scale_out, scale_in;
   bool rev;
   unsigned* status;
@@ -436,11 +439,12 @@ cudaError_t launch_decay_f32(const DecayPass& a, lizard_dtype dt, float* ws, cud
 // three bf16 parts of the state (dot_out [2 dc / 64][B,H,L]; dot_in is not written).  `ws` of
 // decay_tc_workspace bytes.
 constexpr int kDecayTile = 128;
+constexpr int kDecayEdgeWarps = 8;  // that make parts of a chunk's `through`, for each 64 channels
 bool decay_tc_rows_ok(int B, int H, int L, int d, const Strides& s);
 size_t decay_tc_workspace(int B, int H, int L, int da, int dc);
 cudaError_t launch_decay_tc(const DecayPass& a, bool exact_state, float* ws, cudaStream_t s, int* launches);
-// What each token receives from other tokens of its chunk less what it gives to them in the gradient of
-// log_decay, in 128-token chunks.
+// What passes over each token between others of its 128-token chunk (and itself as the later one): its part
+// of the gradient of log_decay.
 struct DecayPairs {
   int B, H, G, L, dk, dv;
   const void *q, *k, *v, *dy;
@@ -449,7 +453,7 @@ struct DecayPairs {
   Strides sg;
   const int32_t* count;
   float scale;
-  float* diff;  // [B,H,L]
+  float* inside;  // [B,H,L]
   unsigned* status;
 };
 cudaError_t launch_decay_pairs(const DecayPairs& a, cudaStream_t s, int* launches);
@@ -459,18 +463,13 @@ cudaError_t launch_decay_heads(int B, int Hk, int G, int L, int d, const float* 
 // d log_decay from the passes' sums (rows: of the pass for q, cols: of the pass for k).
 struct DecayGate {
   int B, H, L, chunk;
-  int in_slices, out_slices;
-  const float *row_in, *col_in;    // [in_slices][B,H,L]; col_in may be null (the difference in row_in)
+  int in_slices, out_slices, parts;
+  const float* inside;             // [in_slices][B,H,L]
   const float *row_out, *col_out;  // [out_slices][B,H,L]
-  const float *h0, *d_h0;                            // [B,H,state], or null
-  int state;
-  const float* lg;
-  Strides sg;
+  const float* through;            // [B,H,chunks][parts]
   const int32_t* count;
   float* d_lg;
-  double2* sums;  // decay_gate_workspace bytes
 };
-size_t decay_gate_workspace(int B, int H, int L, int chunk);
 cudaError_t launch_decay_gate(const DecayGate& a, cudaStream_t s, int* launches);
 struct DecayStep {
   int B, H, G, L, dk, dv;  // G: query heads per key head

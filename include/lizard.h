@@ -628,9 +628,12 @@ lizard_status lizard_decay_attn_fwd(const lizard_decay_dims* dims, const void* q
  *   d_q [B,H,L,dk], d_k [B,Hk,L,dk], d_v [B,Hk,L,dv] T (shared heads summed in fp32);
  *   d_log_decay [B,H,L] fp32 contiguous or NULL: per token and head, 0 where a document starts;
  *   the caller of a broadcast decay sums it.  d_h0 [B,H,dk,dv] fp32 or NULL.
+ *   d_log_decay_t is summed from the products that pass over t alone, so its rounding goes by their
+ *   size and not by that of tokens whose products end before it or begin behind it.
  *   Per token dq = scale h dy, dk = dh v, dv = dh^T k, d log_decay = g <h_{t-1}, dh_t> with
  *   dh_t = scale q_t dy_t^T + g_{t+1} dh_{t+1}.
- * L = 0 writes d_h0 = d_h_final (or zeros) only.
+ * L = 0 writes d_h0 = d_h_final (or zeros) only.  The workspace holds the states at the edges of
+ * 64-token chunks: 4 dk dv bytes for every 64 tokens of a head, and some numbers a token.
  */
 lizard_status lizard_decay_attn_bwd(const lizard_decay_dims* dims, const void* q,
                                     const lizard_strides* s_q, const void* k,
