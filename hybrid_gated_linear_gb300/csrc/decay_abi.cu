@@ -10,10 +10,11 @@ namespace {
 
 using namespace lz::abi;
 
+// (The last chunk's end, past L, is an int32 in the kernels.)
 bool decay_dims_ok(const lizard_decay_dims* d) {
   return d && d->B >= 1 && d->B <= 65535 && d->H >= 1 && d->Hk >= 1 && d->H % d->Hk == 0 && d->L >= 0 &&
          dtype_ok(d->dtype) && isfinite(d->scale) && (__int128)d->B * d->H < (1 << 28) &&
-         (__int128)d->B * d->H * d->L < (1ll << 31);
+         (__int128)d->B * d->H * d->L < (1ll << 31) && d->L < INT32_MAX - lz::kDecayTile;
 }
 bool width_ok(int d) { return d == 64 || d == 128; }
 

@@ -605,7 +605,7 @@ lizard_status lizard_cache_attn(const lizard_cache* cache, const lizard_cache_at
 typedef struct lizard_decay_dims {
     int32_t B;            /* sequences, 1..65535 */
     int32_t H, Hk;        /* query heads; key and value heads (divides H) */
-    int32_t L;            /* tokens per sequence at most, >= 0 */
+    int32_t L;            /* tokens per sequence at most, >= 0; B H L < 2^31, L < 2^31 - 129 */
     int32_t dk, dv;       /* 64 or 128 each */
     lizard_dtype dtype;   /* of q, k, v, y, dy, d_q, d_k, d_v */
     float scale;          /* <= 0 selects 1/sqrt(dk) */

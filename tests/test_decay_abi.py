@@ -62,6 +62,15 @@ def test_decay_dims_refused(lib, bad):
     assert lib.lizard_decay_attn_workspace_bytes(ctypes.byref(_dims(**{"L": 5, **bad})), 1) == 0
 
 
+@pytest.mark.parametrize("L", [2 ** 31 - 1, 2 ** 31 - 64, 2 ** 31 - 128])
+def test_decay_axes_whose_last_chunk_ends_past_31_bits_refused(lib, L):
+    d = _dims(B=1, H=1, Hk=1, L=L, dk=64, dv=64)
+    for fn, base, _ in _three(lib):
+        assert _call(fn, d, base, **({"bytes": 1 << 62} if "bytes" in base else {})) == INVALID
+    for bwd in (0, 1):
+        assert lib.lizard_decay_attn_workspace_bytes(ctypes.byref(d), bwd) == 0
+
+
 def test_decay_widths_and_missing_arguments_refused(lib):
     for fn, base, _ in _three(lib):
         for bad in (dict(dk=32), dict(dv=96), dict(dk=256), dict(dv=0)):
