@@ -325,7 +325,7 @@ lizard_status lizard_decay_attn_step(const lizard_decay_dims* dims, const void* 
 size_t lizard_layer_norm_workspace_bytes(const lizard_norm_dims* dims) {
   if (!norm_dims_ok(dims) || !norm_width_ok(dims->d)) return 0;
   return lz::kWsHeader +
-         lz::norm_part_floats(dims->N, dims->H, dims->T, dims->d, dims->per_head != 0) * sizeof(float);
+         lz::norm_part_floats(dims->N, dims->H, dims->T, dims->d, dims->per_head != 0, dims->dtype) * sizeof(float);
 }
 
 lizard_status lizard_layer_norm_fwd(const lizard_norm_dims* dims, const void* x, const lizard_strides* s_x,

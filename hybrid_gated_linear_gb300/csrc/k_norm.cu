@@ -217,7 +217,7 @@ template <typename T, int TPR>
 __global__ void __launch_bounds__(TPR > kBlock ? TPR : kBlock) norm_bwd_kernel(NormCall a, uint32_t rows, bool heads_inner) {
   constexpr int THREADS = TPR > kBlock ? TPR : kBlock, RPB = THREADS / TPR;
   using R = Ring<T, THREADS>;
-  // the ring; then [warps][2][d] sums for rows within a warp, [RPB][2][d] for wider ones
+  // the ring; after the last row in its place [warps][2][d] sums for rows within a warp, [RPB][2][d] for wider ones
   extern __shared__ __align__(16) uint4 ring[];
   __shared__ float part[128];
   pdl_wait();
@@ -316,7 +316,9 @@ __global__ void __launch_bounds__(TPR > kBlock ? TPR : kBlock) norm_bwd_kernel(N
     here.advance(by, n_in, n_mid);
   }
   if (!a.part) return;
-  float* sums = reinterpret_cast<float*>(ring + R::kBytes / 16);
+  // every copy that was started has been waited for by its row, but not by the other threads of the block
+  float* sums = reinterpret_cast<float*>(ring);
+  __syncthreads();
   // rows of one warp, then the block's warps (or rows) one after the other
   constexpr int PARTS = TPR < 32 ? THREADS / 32 : RPB;
 #pragma unroll
@@ -382,11 +384,18 @@ int rows_per_block(int d) {
   return t >= kBlock ? 1 : kBlock / t;
 }
 // Blocks that share the rows of one set of weights in the backward: one round of the blocks that SMs
-// hold, over all sets; a second round costs more than it fills (two rounds, then one: 32 heads' rows of 128
-// 36.1 / 33.3 us, 8191 rows of 4096 55.0 / 47.3, 4096 rows of 8192 62 / 54).  (152 SMs: written down, so that the workspace does not ask for a device.)
-int bwd_blocks(int64_t rows, int sets, int d) {
+// hold, over all sets; a second round costs more than it fills (bf16, two rounds, then one: 32 heads' rows of
+// 128 36.1 / 33.3 us, 8191 rows of 4096 55.0 / 47.3, 4096 rows of 8192 62 / 54).  An SM holds two blocks of 256
+// threads, by their registers and by their rings (the sums of the block's rows lie in the ring's place; behind
+// it, in fp32, a block had the SM to itself and half of the blocks came second: 61680 rows of 544 93 us, 75
+// this way).  But one fp32 ring of 96 KB is what keeps memory busy, and a second one in its way where rows
+// fill it: 134 MB of rows of 1024, 2048, 4096 two blocks 72, 73, 75 us, one 66, 64, 66; of 1792 75 / 66, of
+// 1536 70 / 73, of 1280 67 / 83; to 512 channels the same within 3.  (152 SMs: written down, so that the
+// workspace does not ask for a device.)
+int bwd_blocks(int64_t rows, int sets, int d, bool f32) {
   const int64_t most = (rows + rows_per_block(d) - 1) / rows_per_block(d);
-  const int per_sm = threads_per_row(d) > kBlock ? 1 : 2;  // what an SM holds at 128 registers
+  const int t = threads_per_row(d);
+  const int per_sm = t > kBlock || (f32 && sets == 1 && t > 32 && 4 * d > 3 * t * kEpt) ? 1 : 2;
   int64_t n = (int64_t)152 * per_sm / sets;
   n = n < most ? n : most;
   return (int)(n < 1 ? 1 : n);
@@ -404,13 +413,13 @@ template <typename T, int TPR>
 cudaError_t bwd(const NormCall& a, cudaStream_t s) {
   const uint32_t rows = (uint32_t)a.N * a.T * (a.per_head ? 1 : a.H);
   const int sets = a.per_head ? a.H : 1;
-  const int parts = TPR < 32 ? kBlock / 32 : TPR >= kBlock ? 0 : kBlock / TPR;  // at most 32 KB of sums
   constexpr int threads = TPR > kBlock ? TPR : kBlock;
   static std::atomic<uint64_t> done{0};
-  const cudaError_t e = allow_smem(norm_bwd_kernel<T, TPR>, Ring<T, threads>::kBytes + (TPR >= kBlock ? 0 : 32768), done);
+  static_assert(Ring<T, threads>::kBytes >= 32768, "the sums of a block's rows lie in the ring's place");
+  const cudaError_t e = allow_smem(norm_bwd_kernel<T, TPR>, Ring<T, threads>::kBytes, done);
   if (e != cudaSuccess) return e;
-  return launch_pdl(norm_bwd_kernel<T, TPR>, dim3(bwd_blocks(rows, sets, a.d), sets), dim3(threads),
-                    Ring<T, threads>::kBytes + (size_t)parts * 2 * a.d * sizeof(float), s, a, rows, heads_inner(a));
+  return launch_pdl(norm_bwd_kernel<T, TPR>, dim3(bwd_blocks(rows, sets, a.d, sizeof(T) == 4), sets), dim3(threads),
+                    Ring<T, threads>::kBytes, s, a, rows, heads_inner(a));
 }
 
 template <typename T>
@@ -426,9 +435,9 @@ cudaError_t dispatch(const NormCall& a, bool back, cudaStream_t s) {
 
 }  // namespace
 
-size_t norm_part_floats(int N, int H, int T, int d, bool per_head) {
+size_t norm_part_floats(int N, int H, int T, int d, bool per_head, lizard_dtype dt) {
   const int sets = per_head ? H : 1;
-  return (size_t)sets * bwd_blocks((int64_t)N * T * (per_head ? 1 : H), sets, d) * 2 * d;
+  return (size_t)sets * bwd_blocks((int64_t)N * T * (per_head ? 1 : H), sets, d, dt == LIZARD_F32) * 2 * d;
 }
 
 cudaError_t launch_norm_fwd(const NormCall& a, lizard_dtype dt, cudaStream_t s, int* launches) {
@@ -446,7 +455,7 @@ cudaError_t launch_norm_bwd(const NormCall& a, lizard_dtype dt, cudaStream_t s, 
   ++*launches;
   if (e != cudaSuccess || !a.part) return e;
   const int sets = a.per_head ? a.H : 1;
-  const int parts = bwd_blocks((int64_t)a.N * a.T * (a.per_head ? 1 : a.H), sets, a.d);
+  const int parts = bwd_blocks((int64_t)a.N * a.T * (a.per_head ? 1 : a.H), sets, a.d, dt == LIZARD_F32);
   trace_begin("norm_weights", s);
   e = launch_pdl(norm_weights_kernel, dim3((2 * a.d + 31) / 32, sets), dim3(32, 32), 0, s,
                  static_cast<const float*>(a.part), parts, a.d, a.dw, a.db);

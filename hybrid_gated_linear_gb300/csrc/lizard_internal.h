@@ -502,7 +502,7 @@ struct NormCall {
   float *dw, *db;              // or null
   float* part;                 // backward: norm_part_floats
 };
-size_t norm_part_floats(int N, int H, int T, int d, bool per_head);
+size_t norm_part_floats(int N, int H, int T, int d, bool per_head, lizard_dtype dt);
 cudaError_t launch_norm_fwd(const NormCall& a, lizard_dtype dt, cudaStream_t s, int* launches);
 cudaError_t launch_norm_bwd(const NormCall& a, lizard_dtype dt, cudaStream_t s, int* launches);
 
