@@ -99,24 +99,6 @@ __device__ __forceinline__ uint32_t half2_bits(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Two fp32 multiply-adds or additions in one instruction.
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
-      "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-  return d;
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  float2 d;
-  asm("{\n\t.reg .b64 x, y, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
-      "add.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
-
 // Waits for the row's TMEM loads; the registers are named so that no use moves in front.
 __device__ __forceinline__ void tmem_ld_wait32(uint32_t (&r)[32]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
@@ -192,10 +174,10 @@ __device__ __forceinline__ float weights(uint32_t ts, const float2 (&sc)[8], flo
           if (far) own += ex2_approx(z0 - m) + ex2_approx(z1 - m);
           w = make_float2(ex2_approx(z0 + sh), ex2_approx(z1 + sh));
         } else {
-          const float2 z = fma2(x, make_float2(k, k), make_float2(sh, sh));
+          const float2 z = f2_fma(x, make_float2(k, k), make_float2(sh, sh));
           w = make_float2(ex2_approx(z.x), ex2_approx(z.y));
         }
-        sum = add2(sum, w);
+        sum = f2_add(sum, w);
         pk[b * 8 + e / 2] = half2_bits(w.x, w.y);
       }
       l += far ? own : (sum.x + sum.y) * ex2_approx(mo - f.y - m);

@@ -266,24 +266,16 @@ __device__ __forceinline__ void block_of(const float* x, float (&v)[16]) {
   }
 }
 
-// The decays within a 16-token block between token `o` of it and each token s, s <= o (s >= o with
-// rev) and 0 elsewhere, by running sums; x: the block's log2 decays.
-__device__ __forceinline__ void block_decays(const float* x, int o, bool rev, float (&d)[16]) {
+// The decays within a 16-token block between token `o` of it and each token s <= o and 0 elsewhere, by running
+// sums; x: the block's log2 decays.
+__device__ __forceinline__ void block_decays(const float* x, int o, float (&d)[16]) {
   float v[16];
   block_of(x, v);
   float sum = 0.f;
-  if (rev) {
 #pragma unroll
-    for (int s = 0; s < 16; ++s) {
-      sum = s <= o ? 0.f : sum + v[s];
-      d[s] = s < o ? 0.f : ex2_approx(sum);
-    }
-  } else {
-#pragma unroll
-    for (int s = 15; s >= 0; --s) {
-      sum = s >= o ? 0.f : sum + v[s < 15 ? s + 1 : 15];
-      d[s] = s > o ? 0.f : ex2_approx(sum);
-    }
+  for (int s = 15; s >= 0; --s) {
+    sum = s >= o ? 0.f : sum + v[s < 15 ? s + 1 : 15];
+    d[s] = s > o ? 0.f : ex2_approx(sum);
   }
 }
 
@@ -1024,7 +1016,7 @@ __global__ void __launch_bounds__(kPairThreads, 2)
         if (g == qw) {
           // the thread's own block of 16 by running sums, the one before it wholly, what is behind nothing
           float d[16];
-          block_decays(hd.x[par] + 16 * I, lane & 15, false, d);
+          block_decays(hd.x[par] + 16 * I, lane & 15, d);
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
             const float in = j == (lane & 15) ? 0.f : d[j];
