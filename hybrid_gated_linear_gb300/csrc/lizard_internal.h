@@ -485,10 +485,17 @@ struct DecayStep {
   float scale;
   unsigned* status;      // of a bad count
 };
-// Up to so many tokens a forward goes this way, fp32 throughout.  128 x 128, a call's time against the
-// chunks': bf16, 4 heads, 16 tokens 9.0 / 15.8 us; 16 x 32 heads, 16 tokens 37 / 108, without states 32 / 40,
-// but 62 / 40 at 32 tokens.  fp32, whose chunks are slower: 16 x 32 heads, 24 tokens 60 / 144,
-// without states 49 / 113; 4 heads of 64 x 64 without states, 24 tokens 11.0 / 11.7, 32 tokens 14.2 / 11.7.
+// Up to so many tokens a forward goes this way, fp32 throughout.  On the GPU, this / the chunks, us, at 4, 512
+// and 2048 heads (replayed from a graph):
+//   bf16, 16 tokens, with states:  64 x 64 8.5 / 9.0, 17 / 34, 57 / 115;  128 x 128 8.6 / 16, 38 / 108, 158 / 429
+//   without:                       64 x 64 8.5 / 5.8, 16 / 23, 50 / 74;   128 x 128 8.4 / 5.8, 32 / 40, 109 / 141
+//   (20 tokens, with: 64 x 64 10.3 / 9.0; without: 512 heads of 128 x 64 26 / 23)
+//   fp32, 24 tokens, with states:  64 x 64 12 / 15, 23 / 38, 98 / 151;  128 x 128 12 / 19, 61 / 140, 223 / 580
+//   without:                       64 x 64 11.5 / 11.9, 22 / 32, 70 / 108;  128 x 128 11 / 17, 49 / 112, 197 / 437
+//   (32 tokens, 4 to 64 heads of 64 x 64: 15 / 12 without, 15 / 15 with)
+// The two mixed widths lie between.  Few heads without states are the one loss, of 3 us at 16 bf16 tokens (from
+// 9 on; 64 heads of 128 x 128 10.2 / 6.4): one limit for a type, so that which sums a call takes, and so its last
+// bits, does not hang on its heads or on what it returns.
 constexpr int kDecayFew = 16, kDecayFewF32 = 24;
 cudaError_t launch_decay_step(const DecayStep& a, lizard_dtype dt, cudaStream_t s, int* launches);
 
