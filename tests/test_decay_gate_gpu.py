@@ -145,3 +145,44 @@ def test_rows_that_overlap(dtype):
     ws = torch.zeros(lz.lizard_decay_attn_workspace_bytes(x.dims, True), dtype=torch.uint8, device="cuda")
     lz.lizard_decay_attn_bwd(x.dims, x.q, x.k, x.v, x.g, None, x.h0, x.dy, x.df, *out, dg, None, ws)
     do.close(dg, c.grads[3], limit(c.grads[3], c.sums[3], x.dims))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("decay", [0.0, -1e-7, -0.05, -3.0, -60.0, -1e5, 0.02])
+def test_constant_decays(dtype, decay):
+    """One number per head, none, weak, strong, and a growing state; repeated by strides of 0."""
+    x = In(1, 2, 2, 333, 64, 64, dtype)
+    x.g = (torch.tensor([decay, decay / 2], device="cuda"))[None, :, None].expand(1, 2, 333)
+    check(x)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("order", ["bhld", "blhd"])
+def test_uneven_lengths_over_segments(dtype, order):
+    """Few heads and a long axis, so that it is cut, with sequences that end in its first part, at a chunk's
+    edge, or have no token, documents, and a workspace that holds anything behind its header."""
+    x = In(5, 2, 1, 1200, 128, 64, dtype, order=order)
+    x.count = [1200, 0, 256, 131, 1025]
+    x.g[0, 1, 640] = x.g[4, 0, 1024] = x.g[2, :, 255] = -INF
+    scaled(x, slice(120, 136), 64.0)
+    for b, c in enumerate(x.count):
+        for t in (x.q, x.k, x.v, x.dy):
+            t[b, :, c:] = float("nan")
+        x.g[b, :, c:] = float("nan")
+    want = check(x)
+    ws = torch.zeros(lz.lizard_decay_attn_workspace_bytes(x.dims, True), dtype=torch.uint8, device="cuda")
+    ws[256:] = 255
+    assert torch.equal(x.bwd(ws=ws)[3], want)
+    for b, c in enumerate(x.count):
+        assert (want[b, :, c:] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_without_the_other_gradients_of_the_ends(dtype):
+    """The same bits whether the initial state's gradient is asked for or not; no states at the ends."""
+    x = In(2, 4, 2, 500, 64, 128, dtype)
+    assert torch.equal(x.bwd()[3], x.bwd(d_h0=False)[3])
+    x.h0 = None
+    check(x)
+    x.df = None
+    check(x)
