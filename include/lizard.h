@@ -592,11 +592,14 @@ lizard_status lizard_cache_attn(const lizard_cache* cache, const lizard_cache_at
  * are accepted as long as the products of the decays between any two tokens are finite in fp32.
  * NaN is not accepted, and a token or a state that is not finite leaves every output of its
  * sequence unspecified.
- * Sums and states are fp32 throughout; a forward of at most 16 tokens (fp32: 24) is the recurrence,
- * token by token, and differs from a longer one's in the last bits.  Longer bf16 calls round, for the tensor cores, the decayed scores
- * of a 128-token chunk and the state that a chunk starts from to bf16; a state that is returned
- * and the gradient of log_decay are made from unrounded (three-part) operands, so that asking for
- * them may change the last bit of the others.  fp32 calls multiply in three tf32 parts (22 bits).
+ * Sums are fp32, and so is the state that is carried on from token to token.  A forward of at most
+ * 16 tokens (fp32: 24) is the recurrence, token by token, fp32 throughout, and differs from a longer
+ * one's in the last bits.  Longer bf16 calls hand the tensor cores rounded copies: of the decayed
+ * scores of a 128-token chunk, and of the state that it starts from where only y or a gradient in
+ * bf16 is made of it, one rounding to bf16 each; of what the chunk adds to the state, 16 bits.  A
+ * state that is returned and the gradient of log_decay are made from three parts of every operand
+ * (24 bits), so that asking for them may change the last bit of the others.  fp32 calls multiply in
+ * three tf32 products (22 bits).
  * A count outside 0..L sets LIZARD_ERR_DEVICE_CHECK; its sequence has no tokens.
  * Workspace: lizard_decay_attn_workspace_bytes, zero before the first call (lizard_workspace_init);
  * calls ordered one after the other may share one, whatever their shapes, if it is large enough
